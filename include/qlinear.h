@@ -363,6 +363,110 @@ qlinear_status qlinear_kv_load_fp8(const uint8_t* cache_codes, const float* cach
                                    int32_t heads, int32_t head_dim, uint16_t* out,
                                    int32_t* status_word, void* stream);
 
+/* ---------------------------------------------------------- NVFP4 KV cache */
+
+/* A paged KV cache in 4 bits (host struct holding a device pointer).  Each (token, head) row
+ * of keys or values is held as E2M1 codes, one E4M3 scale for 16 elements and one power-of-two
+ * scale 2^e for the row; an element is E2M1(code) * E4M3(scale) * 2^e, which is exact in bf16.
+ *   e     the smallest integer with amax_row <= 2688 * 2^e, clamped to [-100, 117]
+ *         (-100 for a zero row);
+ *   scale E4M3(fl32(amax_block * 2^-e / 6));
+ *   code  sign | E2M1(|x| * 2^-e / E4M3value(scale))  (magnitude 0 where the scale is 0).
+ * data u8 [pages][heads][page_size / 16][18 * head_dim + 32]: groups of 16 tokens t of one head,
+ *   K codes  [16 t][D/2]                     byte p of a row: element 2p low, 2p + 1 high nibble
+ *   K scales [16 t][D/16]
+ *   K exps   [16 t]                          e + 127
+ *   V codes  [4 t/4][16 p%16][D/32 p/16][4 t%4]   byte p of the rows of four tokens
+ *   V scales [4 t/4][2 b%2][D/32 b/2][4 t%4]      block b
+ *   V exps   [16 t]
+ * Slot s is token s % page_size of page s / page_size.  Memory of slots never stored may hold
+ * anything.  page_size is a power of two in [16, 1024]; head_dim is 64, 128 or 256; data is
+ * 16-byte aligned, owned by the caller.
+ * The mexc.co NeMo RL FP8 page ("Praktische prestatiewinsten") takes the KV cache and
+ * attention to FP8 beside the linear layers; this is the same step in the 4-bit format that
+ * the QeRL pages put on the weights. */
+typedef struct {
+  uint8_t* data;
+  int64_t pages;
+  int32_t page_size;
+  int32_t heads;
+  int32_t head_dim;
+  int32_t reserved;
+} qlinear_kv_nvfp4;
+
+/* Bytes of a cache's data (0 for invalid sizes). */
+size_t qlinear_kv_nvfp4_bytes(int64_t pages, int32_t page_size, int32_t heads, int32_t head_dim);
+
+/* Store: k, v bf16 [tokens][heads][head_dim], token t at k + t * k_stride (v + t * v_stride),
+ * strides in elements, multiples of 8 -- the k and v parts of a fused projection are taken
+ * where they are -- into slots[t] (int64, device, distinct).  A token with an Inf or NaN in its
+ * key or value row of a head becomes a NaN token of that head: every scale byte 0xFF, loads
+ * give NaN, and attention gives NaN to the query rows that see it; QLINEAR_STATUS_NONFINITE is
+ * set in *status_word (if not NULL).  A slot outside the cache is skipped and sets
+ * QLINEAR_STATUS_BAD_ITEM.
+ * Load: slots[t] -> k_out, v_out bf16 (same strides rule); either may be NULL.  A slot outside
+ * the cache gives zeros and sets QLINEAR_STATUS_BAD_ITEM.  Values are exact, Inf where a held
+ * value passes bf16 (rows with amax >= 2^127 * 1.96 may).
+ * tokens == 0 launches nothing.  Errors: QL_ERR_NULL (cache, data, slots, k, v; both outputs),
+ * QL_ERR_SHAPE (pages, page_size, heads, head_dim, tokens < 0, a stride < heads * head_dim or
+ * not a multiple of 8, sizes beyond QLINEAR_MAX_ELEMS), QL_ERR_ALIGN. */
+qlinear_status qlinear_kv_store_nvfp4(const qlinear_kv_nvfp4* cache, const uint16_t* k, int64_t k_stride,
+                                      const uint16_t* v, int64_t v_stride, int64_t tokens,
+                                      const int64_t* slots, int32_t* status_word, void* stream);
+qlinear_status qlinear_kv_load_nvfp4(const qlinear_kv_nvfp4* cache, const int64_t* slots, int64_t tokens,
+                                     uint16_t* k_out, int64_t k_stride, uint16_t* v_out, int64_t v_stride,
+                                     int32_t* status_word, void* stream);
+
+/* The sequences of an attention call (host struct holding device pointers).
+ * q_starts int32 [batch + 1]: sequence b has the query tokens [q_starts[b], q_starts[b + 1]) of
+ * q, at most max_q_len of them; or NULL: max_q_len query tokens in every sequence and
+ * total_q == batch * max_q_len.
+ * kv_lens int32 [batch]: its cached tokens, those of its own query tokens included.
+ * page_table int32 [batch][table_stride]: the pages that hold them, in order. */
+typedef struct {
+  int32_t batch;
+  int32_t max_q_len;
+  int64_t total_q;
+  const int32_t* q_starts;
+  const int32_t* kv_lens;
+  const int32_t* page_table;
+  int64_t table_stride;
+} qlinear_attn_batch;
+
+/* Attention of bf16 queries over the NVFP4 cache, decoding (one or a few query tokens a
+ * sequence), prompt pieces and both in one call:
+ *   out[i][hq] = sum_t softmax_t(softmax_scale * q[i][hq] . k_t) v_t     t over the tokens seen,
+ * with query head hq reading KV head hq / (q_heads / heads).  q bf16 [total_q][q_heads][head_dim],
+ * token i at q + i * q_stride; out likewise with out_stride (elements, multiples of 8).
+ * causal: query token i of a sequence with n_q query and n cached tokens is at position
+ * n - n_q + i and sees the tokens up to it; otherwise every token.  window > 0 (needs causal):
+ * only the last `window` of those, its own included; 0: no window.  lse f32 [total_q][q_heads]
+ * (NULL: not wanted) gets log(sum_t exp(softmax_scale * q . k_t)).  A query row that sees no
+ * token gets zeros and lse -inf.  Query tokens of no sequence keep their out and lse.
+ * Products are f16 x f16 with float32 sums: q is scaled by a power of two a row (exact but for
+ * magnitudes below about 2^-29 of the row's largest), the cache's values are exact, and the
+ * softmax weights are rounded to f16 (2^-11) before they meet the values.
+ * Results are bitwise reproducible for the same arguments.
+ * Workspace: qlinear_attention_nvfp4_workspace(...) bytes with qlinear_forward's layout and
+ * reuse rules (zero-filled before its first use; calls that share it must not overlap, which
+ * includes replays of graphs captured on it).
+ * From the device, in the workspace's status word as QLINEAR_STATUS_BAD_ITEM: a page number
+ * outside the cache (its tokens are left out), kv_lens beyond the table or negative (cut), and
+ * q_starts that do not fit total_q or max_q_len (the sequence is left out).
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE (cache sizes; batch <= 0 or > QLINEAR_MAX_ATTN_BATCH;
+ * max_q_len, total_q <= 0 or beyond QLINEAR_MAX_M; q_heads not a multiple of heads; total_q
+ * other than batch * max_q_len without q_starts; table_stride <= 0 or 2^30 tokens and more a
+ * sequence; strides), QL_ERR_ARG (window < 0, window without causal, softmax_scale not finite),
+ * QL_ERR_ALIGN, QL_ERR_WORKSPACE. */
+#define QLINEAR_MAX_ATTN_BATCH 65535
+qlinear_status qlinear_attention_nvfp4(const qlinear_kv_nvfp4* cache, const qlinear_attn_batch* seqs,
+                                       const uint16_t* q, int64_t q_stride, int32_t q_heads,
+                                       float softmax_scale, int32_t causal, int32_t window,
+                                       uint16_t* out, int64_t out_stride, float* lse,
+                                       void* ws, size_t ws_bytes, void* stream);
+size_t qlinear_attention_nvfp4_workspace(int32_t batch, int64_t total_q, int32_t q_heads, int32_t heads,
+                                         int32_t head_dim, int32_t max_q_len);
+
 #ifdef __cplusplus
 }
 #endif

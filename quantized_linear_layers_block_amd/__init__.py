@@ -19,7 +19,8 @@ from .binding import (QL_FP8_BLOCK128, QL_FP8_POW2, QL_NVFP4, QL_OUT_BF16, QL_OU
 
 __all__ = ["NVFP4Weight", "FP8Weight", "quantize_nvfp4", "quantize_fp8_block", "quantize_act_fp8",
            "forward", "forward_fp8_prequant", "RequantTable", "QlinearError", "binding", "workspace_status",
-           "quantize_fp8_pow2", "kv_store_fp8", "kv_load_fp8"]
+           "quantize_fp8_pow2", "kv_store_fp8", "kv_load_fp8", "KVCacheNVFP4", "kv_store_nvfp4", "kv_load_nvfp4",
+           "attention_nvfp4"]
 
 
 def _dev(t):
@@ -230,4 +231,138 @@ def kv_load_fp8(cache_codes, cache_scales, slots, heads=None, status_word=None):
     out = torch.empty((t, cache_codes.shape[1], cache_codes.shape[2]), dtype=torch.bfloat16,
                       device=cache_codes.device)
     binding.qlinear_kv_load_fp8(cache_codes, cache_scales, slots, out, status_word)
+    return out
+
+
+@dataclass
+class KVCacheNVFP4:
+    """A paged KV cache in 4 bits: data uint8 [pages, heads, page_size / 16, 18 D + 32] (the
+    layout is in include/qlinear.h).  Slot s is token s % page_size of page s // page_size."""
+    data: torch.Tensor
+    pages: int
+    heads: int
+    head_dim: int
+    page_size: int
+
+    def __post_init__(self):
+        d = self.data
+        need = binding.qlinear_kv_nvfp4_bytes(self.pages, self.page_size, self.heads, self.head_dim)
+        if need == 0:
+            raise ValueError("page_size is a power of two in [16, 1024], head_dim 64, 128 or 256")
+        if d.dtype != torch.uint8 or not d.is_contiguous() or d.numel() != need:
+            raise ValueError(f"data must be {need} contiguous bytes")
+        self.handle = binding.make_kv_nvfp4(d, self.pages, self.page_size, self.heads, self.head_dim)
+
+    @staticmethod
+    def empty(pages, heads, head_dim, page_size=64, device="cuda"):
+        """A cache of pages * page_size slots; what was never stored may hold anything."""
+        data = torch.empty((pages, heads, page_size // 16, 18 * head_dim + 32), dtype=torch.uint8, device=device)
+        return KVCacheNVFP4(data, pages, heads, head_dim, page_size)
+
+
+def _check_on(device, dtype, name, t, shape=None):
+    if t.device != device:
+        raise ValueError(f"{name} must live on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have the shape {shape}")
+
+
+def _check_rows(device, name, t, heads, head_dim):
+    # the rows of a token are dense; tokens may be apart (part of a fused projection)
+    _check_on(device, torch.bfloat16, name, t)
+    if t.dim() != 3 or t.shape[1:] != (heads, head_dim):
+        raise ValueError(f"{name} must be [tokens, {heads}, {head_dim}]")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim)):
+        raise ValueError(f"{name} must have dense [heads, head_dim] rows")
+
+
+def _check_dense(device, dtype, name, t, shape):
+    _check_on(device, dtype, name, t, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_status(device, status_word):
+    if status_word is not None:
+        _check_dense(device, torch.int32, "status_word", status_word, (1,))
+
+
+def kv_store_nvfp4(k, v, slots, cache, status_word=None):
+    """Store bf16 keys and values [T, H, D] in slots[t] (int64, distinct) of an NVFP4 cache."""
+    dev = _dev(cache.data).device
+    _check_rows(dev, "k", k, cache.heads, cache.head_dim)
+    _check_rows(dev, "v", v, cache.heads, cache.head_dim)
+    t = k.shape[0]
+    if v.shape[0] != t:
+        raise ValueError("k and v must have the same tokens")
+    _check_dense(dev, torch.int64, "slots", slots, (t,))
+    _check_status(dev, status_word)
+    if t == 0:
+        return
+    with torch.cuda.device(dev):
+        binding.qlinear_kv_store_nvfp4(cache.handle, k, v, slots, status_word)
+
+
+def kv_load_nvfp4(cache, slots, k_out=None, v_out=None, status_word=None):
+    """(k, v) bf16 [T, H, D] of the cache's slots[t]."""
+    dev = _dev(cache.data).device
+    _check_dense(dev, torch.int64, "slots", slots, (slots.numel(),))
+    _check_status(dev, status_word)
+    outs = []
+    for name, o in (("k_out", k_out), ("v_out", v_out)):
+        if o is None:
+            o = torch.empty((slots.shape[0], cache.heads, cache.head_dim), dtype=torch.bfloat16, device=dev)
+        _check_rows(dev, name, o, cache.heads, cache.head_dim)
+        if o.shape[0] != slots.shape[0]:
+            raise ValueError(f"{name} must have one row a slot")
+        outs.append(o)
+    if slots.shape[0]:
+        with torch.cuda.device(dev):
+            binding.qlinear_kv_load_nvfp4(cache.handle, slots, outs[0], outs[1], status_word)
+    return outs[0], outs[1]
+
+
+def attention_nvfp4(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None, softmax_scale=None, causal=True,
+                    window=0, out=None, lse=None, ws=None):
+    """Attention of bf16 queries [Tq, Hq, D] over an NVFP4 cache: out bf16 [Tq, Hq, D].
+
+    page_table int32 [B, P] and kv_lens int32 [B] name each sequence's cached tokens, those of
+    its own queries included.  Without q_starts every sequence has Tq / B query tokens; with it
+    (int32 [B + 1]) sequence b has tokens [q_starts[b], q_starts[b + 1]), at most max_q_len.
+    softmax_scale defaults to 1 / sqrt(D).  causal aligns the last query with the last cached
+    token; window > 0 keeps the last `window` tokens.  lse (float32 [Tq, Hq]) is filled if
+    given.  ws: a zero-filled workspace kept from call to call, as forward's."""
+    dev = _dev(cache.data).device
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    tq, hq, d = q.shape
+    _check_rows(dev, "q", q, hq, cache.head_dim)
+    batch = kv_lens.shape[0]
+    _check_dense(dev, torch.int32, "kv_lens", kv_lens, (batch,))
+    _check_on(dev, torch.int32, "page_table", page_table)
+    if page_table.dim() != 2 or page_table.shape[0] != batch or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be [batch, pages] with dense rows")
+    if q_starts is not None:
+        _check_dense(dev, torch.int32, "q_starts", q_starts, (batch + 1,))
+        if max_q_len is None:
+            raise ValueError("q_starts needs max_q_len")
+    elif max_q_len is None:
+        max_q_len = tq // max(batch, 1)
+    if out is None:
+        out = torch.empty((tq, hq, d), dtype=torch.bfloat16, device=dev)
+    _check_rows(dev, "out", out, hq, d)
+    if out.shape[0] != tq:
+        raise ValueError("out must have q's tokens")
+    if lse is not None:
+        _check_dense(dev, torch.float32, "lse", lse, (tq, hq))
+    with torch.cuda.device(dev):
+        if ws is None:
+            ws = _ws(binding.qlinear_attention_nvfp4_workspace(batch, tq, hq, cache.heads, d, max_q_len), dev)
+        else:
+            _check_on(dev, torch.uint8, "ws", ws)
+        binding.qlinear_attention_nvfp4(cache.handle, q, page_table, kv_lens, out, ws, q_starts, max_q_len,
+                                        d ** -0.5 if softmax_scale is None else softmax_scale, causal, window, lse)
     return out

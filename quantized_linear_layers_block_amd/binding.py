@@ -43,11 +43,17 @@ EXPORTS = [
     "qlinear_backward_workspace",
     "qlinear_forward_group",
     "qlinear_forward_group_workspace",
+    "qlinear_kv_nvfp4_bytes",
+    "qlinear_kv_store_nvfp4",
+    "qlinear_kv_load_nvfp4",
+    "qlinear_attention_nvfp4",
+    "qlinear_attention_nvfp4_workspace",
 ]
 
 QLINEAR_STATUS_NONFINITE, QLINEAR_STATUS_TIMEOUT, QLINEAR_STATUS_BAD_ITEM = 1, 2, 4
 QLINEAR_WS_RESERVED_BYTES = 131072
 QLINEAR_NOALLOC_MAX_BYTES = 32 << 20
+QLINEAR_MAX_ATTN_BATCH = 65535
 
 
 class QlinearError(RuntimeError):
@@ -69,6 +75,17 @@ class RequantItem(ctypes.Structure):
 
 class GroupLayer(ctypes.Structure):
     _fields_ = [("w", QWeight), ("lora_a", ctypes.c_void_p), ("lora_b", ctypes.c_void_p), ("y", ctypes.c_void_p)]
+
+
+class KvNvfp4(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AttnBatch(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_q_len", ctypes.c_int32), ("total_q", ctypes.c_int64),
+                ("q_starts", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64)]
 
 
 def _load():
@@ -112,6 +129,12 @@ def _load():
         "qlinear_backward_workspace": ([i32, i64, i64, i64, i32], sz),
         "qlinear_forward_group": ([vp, i32, vp, i64, i32, f32, i32, vp, sz, vp], i32),
         "qlinear_forward_group_workspace": ([i64, i64, vp, i32, i32], sz),
+        "qlinear_kv_nvfp4_bytes": ([i64, i32, i32, i32], sz),
+        "qlinear_kv_store_nvfp4": ([ctypes.POINTER(KvNvfp4), vp, i64, vp, i64, i64, vp, vp, vp], i32),
+        "qlinear_kv_load_nvfp4": ([ctypes.POINTER(KvNvfp4), vp, i64, vp, i64, vp, i64, vp, vp], i32),
+        "qlinear_attention_nvfp4": ([ctypes.POINTER(KvNvfp4), ctypes.POINTER(AttnBatch), vp, i64, i32, f32, i32, i32,
+                                     vp, i64, vp, vp, sz, vp], i32),
+        "qlinear_attention_nvfp4_workspace": ([i32, i64, i32, i32, i32, i32], sz),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -134,6 +157,16 @@ def _check(status, where):
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _row_stride(t):
+    # PyTorch leaves the stride of a dimension of one entry open
+    if t.shape[0] > 1:
+        return t.stride(0)
+    width = 1
+    for n in t.shape[1:]:
+        width *= n
+    return width
 
 
 def _stream(stream):
@@ -302,6 +335,43 @@ def qlinear_kv_load_fp8(cache_codes, cache_scales, slots, out, status_word=None,
     _check(LIB.qlinear_kv_load_fp8(_ptr(cache_codes), _ptr(cache_scales), cache_codes.shape[0], _ptr(slots), t,
                                    h, d, _ptr(out), _ptr(status_word), _stream(stream)),
            "qlinear_kv_load_fp8")
+
+
+def make_kv_nvfp4(data, pages, page_size, heads, head_dim):
+    return KvNvfp4(_ptr(data), pages, page_size, heads, head_dim, 0)
+
+
+def qlinear_kv_nvfp4_bytes(pages, page_size, heads, head_dim):
+    return LIB.qlinear_kv_nvfp4_bytes(pages, page_size, heads, head_dim)
+
+
+def qlinear_kv_store_nvfp4(cache, k, v, slots, status_word=None, stream=None):
+    """k, v bf16 [T, H, D] (rows [H, D] dense, any token stride) -> slots[t] of the cache (KvNvfp4)."""
+    _check(LIB.qlinear_kv_store_nvfp4(ctypes.byref(cache), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), k.shape[0],
+                                      _ptr(slots), _ptr(status_word), _stream(stream)), "qlinear_kv_store_nvfp4")
+
+
+def qlinear_kv_load_nvfp4(cache, slots, k_out=None, v_out=None, status_word=None, stream=None):
+    """slots[t] of the cache -> k_out, v_out bf16 [T, H, D] (either may be None)."""
+    _check(LIB.qlinear_kv_load_nvfp4(ctypes.byref(cache), _ptr(slots), slots.shape[0], _ptr(k_out),
+                                     0 if k_out is None else _row_stride(k_out), _ptr(v_out),
+                                     0 if v_out is None else _row_stride(v_out), _ptr(status_word), _stream(stream)),
+           "qlinear_kv_load_nvfp4")
+
+
+def qlinear_attention_nvfp4_workspace(batch, total_q, q_heads, heads, head_dim, max_q_len):
+    return LIB.qlinear_attention_nvfp4_workspace(batch, total_q, q_heads, heads, head_dim, max_q_len)
+
+
+def qlinear_attention_nvfp4(cache, q, page_table, kv_lens, out, ws, q_starts=None, max_q_len=1, softmax_scale=1.0,
+                            causal=True, window=0, lse=None, stream=None):
+    """out [Tq, Hq, D] = attention of q over the cache (KvNvfp4); lse f32 [Tq, Hq] or None."""
+    seqs = AttnBatch(kv_lens.shape[0], max_q_len, q.shape[0], _ptr(q_starts), _ptr(kv_lens), _ptr(page_table),
+                     _row_stride(page_table))
+    _check(LIB.qlinear_attention_nvfp4(ctypes.byref(cache), ctypes.byref(seqs), _ptr(q), _row_stride(q), q.shape[1],
+                                       softmax_scale, 1 if causal else 0, window, _ptr(out), _row_stride(out), _ptr(lse),
+                                       _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "qlinear_attention_nvfp4")
 
 
 def qlinear_status_word(ws):

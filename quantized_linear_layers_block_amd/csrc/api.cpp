@@ -471,4 +471,134 @@ qlinear_status qlinear_kv_load_fp8(const uint8_t* cache_codes, const float* cach
                                        status_word, (hipStream_t)stream));
 }
 
+// ------------------------------------------------------------ NVFP4 KV cache
+
+static bool kv4_sizes_ok(int64_t pages, int32_t page_size, int32_t heads, int32_t head_dim) {
+  if (pages <= 0 || heads <= 0 || heads > 65535) return false;
+  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1))) return false;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return false;
+  return elems_ok(pages, (int64_t)page_size * heads * head_dim);
+}
+
+size_t qlinear_kv_nvfp4_bytes(int64_t pages, int32_t page_size, int32_t heads, int32_t head_dim) {
+  if (!kv4_sizes_ok(pages, page_size, heads, head_dim)) return 0;
+  return (size_t)pages * heads * (page_size / 16) * (18 * (size_t)head_dim + 32);
+}
+
+static qlinear_status check_kv4(const qlinear_kv_nvfp4* c, ql::Kv4Cache* out) {
+  if (!c || !c->data) return QL_ERR_NULL;
+  if (!kv4_sizes_ok(c->pages, c->page_size, c->heads, c->head_dim)) return QL_ERR_SHAPE;
+  if (!aligned16(c->data)) return QL_ERR_ALIGN;
+  *out = {c->data, c->pages, __builtin_ctz((unsigned)c->page_size), c->heads, c->head_dim};
+  return QL_OK;
+}
+
+// Rows of `width` elements, one every `stride`.
+static bool rows_ok(int64_t rows, int64_t stride, int64_t width) {
+  return stride >= width && stride % 8 == 0 && elems_ok(rows, stride);
+}
+
+qlinear_status qlinear_kv_store_nvfp4(const qlinear_kv_nvfp4* cache, const uint16_t* k, int64_t k_stride,
+                                      const uint16_t* v, int64_t v_stride, int64_t tokens, const int64_t* slots,
+                                      int32_t* status_word, void* stream) {
+  ql::Kv4Cache c;
+  const qlinear_status st = check_kv4(cache, &c);
+  if (st != QL_OK) return st;
+  if (!k || !v || !slots) return QL_ERR_NULL;
+  if (tokens < 0) return QL_ERR_SHAPE;
+  const int64_t width = (int64_t)c.heads * c.head_dim;
+  if (!rows_ok(tokens > 0 ? tokens : 1, k_stride, width) || !rows_ok(tokens > 0 ? tokens : 1, v_stride, width))
+    return QL_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v) || ((uintptr_t)slots & 7) || (status_word && ((uintptr_t)status_word & 3)))
+    return QL_ERR_ALIGN;
+  if (tokens == 0) return QL_OK;
+  ql::clear_hip_error();
+  return hip_status(ql::launch_kv4_store(c, k, k_stride, v, v_stride, tokens, slots, status_word,
+                                         (hipStream_t)stream));
+}
+
+qlinear_status qlinear_kv_load_nvfp4(const qlinear_kv_nvfp4* cache, const int64_t* slots, int64_t tokens,
+                                     uint16_t* k_out, int64_t k_stride, uint16_t* v_out, int64_t v_stride,
+                                     int32_t* status_word, void* stream) {
+  ql::Kv4Cache c;
+  const qlinear_status st = check_kv4(cache, &c);
+  if (st != QL_OK) return st;
+  if (!slots || (!k_out && !v_out)) return QL_ERR_NULL;
+  if (tokens < 0) return QL_ERR_SHAPE;
+  const int64_t width = (int64_t)c.heads * c.head_dim;
+  if (k_out && !rows_ok(tokens > 0 ? tokens : 1, k_stride, width)) return QL_ERR_SHAPE;
+  if (v_out && !rows_ok(tokens > 0 ? tokens : 1, v_stride, width)) return QL_ERR_SHAPE;
+  if ((k_out && !aligned16(k_out)) || (v_out && !aligned16(v_out)) || ((uintptr_t)slots & 7) ||
+      (status_word && ((uintptr_t)status_word & 3)))
+    return QL_ERR_ALIGN;
+  if (tokens == 0) return QL_OK;
+  ql::clear_hip_error();
+  return hip_status(ql::launch_kv4_load(c, slots, tokens, k_out, k_stride, v_out, v_stride, status_word,
+                                        (hipStream_t)stream));
+}
+
+static bool attn_sizes_ok(int64_t batch, int64_t total_q, int64_t q_heads, int64_t heads, int32_t head_dim,
+                          int64_t max_q) {
+  if (batch <= 0 || batch > QLINEAR_MAX_ATTN_BATCH || total_q <= 0 || total_q > QLINEAR_MAX_M) return false;
+  if (max_q <= 0 || max_q > QLINEAR_MAX_M || heads <= 0 || heads > 65535) return false;
+  if (q_heads <= 0 || q_heads % heads || q_heads > 65536) return false;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return false;
+  // query rows of one KV head are counted in 32 bits
+  return max_q * (q_heads / heads) < (int64_t(1) << 30) && total_q * (q_heads / heads) < (int64_t(1) << 30);
+}
+
+size_t qlinear_attention_nvfp4_workspace(int32_t batch, int64_t total_q, int32_t q_heads, int32_t heads,
+                                         int32_t head_dim, int32_t max_q_len) {
+  if (!attn_sizes_ok(batch, total_q, q_heads, heads, head_dim, max_q_len)) return 0;
+  return ql::kWsReserved + up(ql::attn4_scratch_bytes(batch, total_q, q_heads, heads, head_dim, max_q_len));
+}
+
+qlinear_status qlinear_attention_nvfp4(const qlinear_kv_nvfp4* cache, const qlinear_attn_batch* seqs,
+                                       const uint16_t* q, int64_t q_stride, int32_t q_heads, float softmax_scale,
+                                       int32_t causal, int32_t window, uint16_t* out, int64_t out_stride, float* lse,
+                                       void* ws, size_t ws_bytes, void* stream) {
+  ql::Kv4Cache c;
+  const qlinear_status st = check_kv4(cache, &c);
+  if (st != QL_OK) return st;
+  if (!seqs || !q || !out || !seqs->kv_lens || !seqs->page_table) return QL_ERR_NULL;
+  if (!attn_sizes_ok(seqs->batch, seqs->total_q, q_heads, c.heads, c.head_dim, seqs->max_q_len)) return QL_ERR_SHAPE;
+  if (!seqs->q_starts && seqs->total_q != (int64_t)seqs->batch * seqs->max_q_len) return QL_ERR_SHAPE;
+  if (seqs->table_stride <= 0 || seqs->table_stride >= (int64_t(1) << 30) / cache->page_size) return QL_ERR_SHAPE;
+  const int64_t width = (int64_t)q_heads * c.head_dim;
+  if (!rows_ok(seqs->total_q, q_stride, width) || !rows_ok(seqs->total_q, out_stride, width)) return QL_ERR_SHAPE;
+  if (window < 0 || (window > 0 && !causal) || !__builtin_isfinite(softmax_scale)) return QL_ERR_ARG;
+  if (!aligned16(q) || !aligned16(out) || (lse && ((uintptr_t)lse & 3)) || ((uintptr_t)seqs->kv_lens & 3) ||
+      ((uintptr_t)seqs->page_table & 3) || ((uintptr_t)seqs->q_starts & 3))
+    return QL_ERR_ALIGN;
+  if (!ws || ws_bytes < qlinear_attention_nvfp4_workspace(seqs->batch, seqs->total_q, q_heads, c.heads, c.head_dim,
+                                                          seqs->max_q_len))
+    return QL_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QL_ERR_ALIGN;
+  ql::Attn4 a;
+  a.data = c.data;
+  a.pages = c.pages;
+  a.page_shift = c.page_shift;
+  a.heads = c.heads;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.q_heads = q_heads;
+  a.group = q_heads / c.heads;
+  a.batch = seqs->batch;
+  a.max_q = seqs->max_q_len;
+  a.total_q = seqs->total_q;
+  a.q_starts = seqs->q_starts;
+  a.kv_lens = seqs->kv_lens;
+  a.table = seqs->page_table;
+  a.table_stride = seqs->table_stride;
+  a.scale_log2e = softmax_scale * 1.4426950408889634f;
+  a.causal = causal != 0;
+  a.window = window;
+  a.out = out;
+  a.out_stride = out_stride;
+  a.lse = lse;
+  a.status = ql::ws_status(ws);
+  ql::clear_hip_error();
+  return hip_status(ql::launch_attn4(a, c.head_dim, ql::ws_scratch(ws), (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -1,0 +1,214 @@
+// NVFP4 KV-cache codec for gfx950: keys and values written as E2M1 codes with an E4M3 scale
+// for 16 elements and one power-of-two scale for the row, and read back to bf16.
+//
+// A row (token, head) has x = E2M1 * E4M3 * 2^e.  e is the smallest integer with
+// amax <= 2688 * 2^e (2688 = 6 * 448, the largest product), so the E4M3 block scales
+// amax_b 2^-e / 6 use their whole range, and the product (at most 2 + 4 significant bits) is
+// exact in bf16: what is loaded is what attention reads, with no further rounding.  A power of
+// two costs one byte a row and no precision, since E4M3 is a floating format.
+//
+// One lane holds 8 elements of a key row and of the value row beside it; the D / 8 lanes of a
+// row form an aligned group inside a wave.  Both kernels are streaming copies.
+#include "../../include/qlinear.h"
+#include "kv4_common.hpp"
+#include "launch.hpp"
+
+namespace ql {
+
+constexpr int kKv4Threads = 256;
+
+struct Kv4Row {
+  int64_t token;
+  int head;
+};
+
+__device__ __forceinline__ Kv4Row kv4_row(int64_t v, int heads, bool narrow) {
+  if (narrow) {  // every row index fits in 32 bits
+    const uint32_t q = (uint32_t)v / (uint32_t)heads;
+    return {q, (int)((uint32_t)v - q * (uint32_t)heads)};
+  }
+  const int64_t t = v / heads;
+  return {t, (int)(v - t * heads)};
+}
+
+__device__ __forceinline__ uint8_t* kv4_group(uint8_t* data, int64_t slot, int head, int heads, int page_shift, int gb) {
+  const int64_t page = slot >> page_shift;
+  const int64_t grp = (slot & ((1 << page_shift) - 1)) >> 4;
+  return data + (((page * heads + head) << (page_shift - 4)) + grp) * gb;
+}
+
+__device__ __forceinline__ uint32_t kv4_amax8(uint4 x) {
+  u16x2 m = abs_bits2(x.x);
+  m = max_u16x2(m, abs_bits2(x.y));
+  m = max_u16x2(m, abs_bits2(x.z));
+  m = max_u16x2(m, abs_bits2(x.w));
+  return hmax_u16x2(m);
+}
+
+// e of a row whose largest magnitude has the bf16 bits `amax` (1.3125 = 2688 / 2^11 = mantissa 40).
+__device__ __forceinline__ int kv4_exponent(uint32_t amax) {
+  const int e = (int)(amax >> 7) - 138 + ((amax & 127u) > 40u);
+  return e < kKv4MinExp ? kKv4MinExp : (e > kKv4MaxExp ? kKv4MaxExp : e);
+}
+
+// Eight elements of a block whose largest magnitude is amax_b: the codes and the block's scale.
+__device__ __forceinline__ uint32_t kv4_encode8(uint4 x, uint32_t amax_b, int e, uint32_t& scale) {
+  const float want = __builtin_ldexpf(__uint_as_float(amax_b << 16), -e) / 6.0f;
+  scale = e4m3_encode(want);
+  const float s = e4m3_value(scale);
+  const float r = s > 0.0f ? 1.0f / s : 0.0f;
+  float q[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
+                bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // y / s for an 8-bit y and a 4-bit s: a quotient that is no rounding border of E2M1 is at
+    // least 2^-12 away from one, and the remainder step makes the ones that are exact
+    const float y = __builtin_ldexpf(q[i], -e);
+    const float a = y * r;
+    q[i] = __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-a, s, y), r, a), y);  // -0 keeps its sign
+  }
+  return e2m1_pack8(q);
+}
+
+template <int D>
+__global__ __launch_bounds__(kKv4Threads) void kv4_store_kernel(
+    const uint16_t* __restrict__ k, int64_t k_stride, const uint16_t* __restrict__ v, int64_t v_stride, int64_t rows,
+    int heads, const int64_t* __restrict__ slots, uint8_t* __restrict__ data, int64_t cache_slots, int page_shift,
+    int32_t* status, bool narrow) {
+  constexpr int kLanes = D / 8, kPer = kKv4Threads / kLanes;
+  const int part = (int)(threadIdx.x & (kLanes - 1));
+  for (int64_t r0 = (int64_t)blockIdx.x * kPer; r0 < rows; r0 += (int64_t)gridDim.x * kPer) {
+    const int64_t row = r0 + threadIdx.x / kLanes;
+    const bool in = row < rows;
+    const Kv4Row p = kv4_row(in ? row : rows - 1, heads, narrow);
+    const int64_t slot = slots[p.token];
+    const uint4 xk = *(const uint4*)(k + p.token * k_stride + p.head * D + part * 8);
+    const uint4 xv = *(const uint4*)(v + p.token * v_stride + p.head * D + part * 8);
+    const uint32_t bk = max_pair(kv4_amax8(xk)), bv = max_pair(kv4_amax8(xv));
+    uint32_t ak = bk, av = bv;
+#pragma unroll
+    for (int o = kLanes / 2; o >= 2; o >>= 1) {
+      ak = umax(ak, (uint32_t)__shfl_xor((int)ak, o));
+      av = umax(av, (uint32_t)__shfl_xor((int)av, o));
+    }
+    if (!in) continue;
+    if (slot < 0 || slot >= cache_slots) {
+      if (part == 0 && status) atomicOr(status, (int32_t)kStatusBadItem);
+      continue;
+    }
+    int ek = kv4_exponent(ak), ev = kv4_exponent(av);
+    uint32_t sk, sv;
+    uint32_t ck = kv4_encode8(xk, bk, ek, sk), cv = kv4_encode8(xv, bv, ev, sv);
+    if (umax(ak, av) >= kBf16InfBits) {  // a token with Inf or NaN is a NaN token
+      ck = cv = 0;
+      sk = sv = 0xFF;
+      ek = ev = 0;
+      if (part == 0 && status) atomicOr(status, (int32_t)kStatusNonFinite);
+    }
+    uint8_t* g = kv4_group(data, slot, p.head, heads, page_shift, kv4_group_bytes(D));
+    const int t = (int)(slot & 15);
+    *(uint32_t*)(g + t * (D / 2) + part * 4) = ck;
+    uint8_t* gv = g + kv4_v_codes(D) + (t >> 2) * (2 * D) + (part & 3) * 4 * (D / 8) + (part >> 2) * 4 + (t & 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) gv[i * (D / 8)] = (uint8_t)(cv >> (8 * i));
+    if ((part & 1) == 0) {
+      const int b = part >> 1;
+      g[kv4_k_scales(D) + t * (D / 16) + b] = (uint8_t)sk;
+      g[kv4_v_scales(D) + (t >> 2) * (D / 4) + (b & 1) * (D / 8) + (b >> 1) * 4 + (t & 3)] = (uint8_t)sv;
+    }
+    if (part == 0) {
+      g[kv4_k_exps(D) + t] = (uint8_t)(ek + 127);
+      g[kv4_v_exps(D) + t] = (uint8_t)(ev + 127);
+    }
+  }
+}
+
+// Eight codes times their scale as bf16 (exact; Inf where 2112 * 2^117 passes the format).
+__device__ __forceinline__ uint4 kv4_decode8(uint32_t codes, uint32_t scale, uint32_t exp) {
+  const float s = __builtin_ldexpf(e4m3_value(scale), (int)exp - 127);
+  const f32x2 a = e2m1_unpack2<0>(codes), b = e2m1_unpack2<1>(codes), c = e2m1_unpack2<2>(codes),
+              d = e2m1_unpack2<3>(codes);
+  return make_uint4(pack_bf16x2_rne(a[0] * s, a[1] * s), pack_bf16x2_rne(b[0] * s, b[1] * s),
+                    pack_bf16x2_rne(c[0] * s, c[1] * s), pack_bf16x2_rne(d[0] * s, d[1] * s));
+}
+
+template <int D>
+__global__ __launch_bounds__(kKv4Threads) void kv4_load_kernel(
+    const uint8_t* __restrict__ data, int64_t cache_slots, int page_shift, const int64_t* __restrict__ slots,
+    int64_t rows, int heads, uint16_t* __restrict__ k, int64_t k_stride, uint16_t* __restrict__ v, int64_t v_stride,
+    int32_t* status, bool narrow) {
+  constexpr int kLanes = D / 8, kPer = kKv4Threads / kLanes;
+  const int part = (int)(threadIdx.x & (kLanes - 1));
+  for (int64_t r0 = (int64_t)blockIdx.x * kPer; r0 < rows; r0 += (int64_t)gridDim.x * kPer) {
+    const int64_t row = r0 + threadIdx.x / kLanes;
+    if (row >= rows) continue;
+    const Kv4Row p = kv4_row(row, heads, narrow);
+    const int64_t slot = slots[p.token];
+    const bool ok = slot >= 0 && slot < cache_slots;
+    // a slot outside the cache is read from slot 0 and dropped
+    const uint8_t* g = kv4_group((uint8_t*)data, ok ? slot : 0, p.head, heads, page_shift, kv4_group_bytes(D));
+    const int t = ok ? (int)(slot & 15) : 0;
+    const int b = part >> 1;
+    uint4 ok4 = make_uint4(0, 0, 0, 0), ov4 = ok4;
+    if (k) {
+      ok4 = kv4_decode8(*(const uint32_t*)(g + t * (D / 2) + part * 4), g[kv4_k_scales(D) + t * (D / 16) + b],
+                        g[kv4_k_exps(D) + t]);
+    }
+    if (v) {
+      const uint8_t* gv = g + kv4_v_codes(D) + (t >> 2) * (2 * D) + (part & 3) * 4 * (D / 8) + (part >> 2) * 4 + (t & 3);
+      uint32_t c = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c |= (uint32_t)gv[i * (D / 8)] << (8 * i);
+      ov4 = kv4_decode8(c, g[kv4_v_scales(D) + (t >> 2) * (D / 4) + (b & 1) * (D / 8) + (b >> 1) * 4 + (t & 3)],
+                        g[kv4_v_exps(D) + t]);
+    }
+    if (!ok) {
+      ok4 = ov4 = make_uint4(0, 0, 0, 0);
+      if (part == 0 && status) atomicOr(status, (int32_t)kStatusBadItem);
+    }
+    if (k) *(uint4*)(k + p.token * k_stride + p.head * D + part * 8) = ok4;
+    if (v) *(uint4*)(v + p.token * v_stride + p.head * D + part * 8) = ov4;
+  }
+}
+
+static unsigned kv4_grid(int64_t rows, int d) {
+  const int64_t per = kKv4Threads / (d / 8);
+  const int64_t blocks = (rows + per - 1) / per;
+  return (unsigned)(blocks < 8192 ? blocks : 8192);
+}
+
+template <int D>
+static hipError_t store_d(const Kv4Cache& c, const uint16_t* k, int64_t ks, const uint16_t* v, int64_t vs,
+                          int64_t tokens, const int64_t* slots, int32_t* status, hipStream_t s) {
+  const int64_t rows = tokens * c.heads;
+  kv4_store_kernel<D><<<kv4_grid(rows, D), kKv4Threads, 0, s>>>(k, ks, v, vs, rows, c.heads, slots, c.data,
+                                                               c.pages << c.page_shift, c.page_shift, status,
+                                                               rows <= (int64_t)UINT32_MAX);
+  return hipGetLastError();
+}
+
+template <int D>
+static hipError_t load_d(const Kv4Cache& c, const int64_t* slots, int64_t tokens, uint16_t* k, int64_t ks, uint16_t* v,
+                         int64_t vs, int32_t* status, hipStream_t s) {
+  const int64_t rows = tokens * c.heads;
+  kv4_load_kernel<D><<<kv4_grid(rows, D), kKv4Threads, 0, s>>>(c.data, c.pages << c.page_shift, c.page_shift, slots,
+                                                              rows, c.heads, k, ks, v, vs, status,
+                                                              rows <= (int64_t)UINT32_MAX);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv4_store(const Kv4Cache& c, const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                            int64_t tokens, const int64_t* slots, int32_t* status, hipStream_t s) {
+  if (c.head_dim == 64) return store_d<64>(c, k, k_stride, v, v_stride, tokens, slots, status, s);
+  if (c.head_dim == 128) return store_d<128>(c, k, k_stride, v, v_stride, tokens, slots, status, s);
+  return store_d<256>(c, k, k_stride, v, v_stride, tokens, slots, status, s);
+}
+
+hipError_t launch_kv4_load(const Kv4Cache& c, const int64_t* slots, int64_t tokens, uint16_t* k, int64_t k_stride,
+                           uint16_t* v, int64_t v_stride, int32_t* status, hipStream_t s) {
+  if (c.head_dim == 64) return load_d<64>(c, slots, tokens, k, k_stride, v, v_stride, status, s);
+  if (c.head_dim == 128) return load_d<128>(c, slots, tokens, k, k_stride, v, v_stride, status, s);
+  return load_d<256>(c, slots, tokens, k, k_stride, v, v_stride, status, s);
+}
+
+}  // namespace ql

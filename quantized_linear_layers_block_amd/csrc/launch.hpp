@@ -61,6 +61,42 @@ hipError_t launch_kv_store(const uint16_t* kv, int64_t tokens, int heads, int he
 hipError_t launch_kv_load(const uint8_t* codes, const float* scales, int64_t cache_slots, const int64_t* slots,
                           int64_t tokens, int heads, int head_dim, uint16_t* out, int32_t* status, hipStream_t s);
 
+// ---- NVFP4 KV cache: codec (kv4.hip) and attention (attn4.hip); head_dim 64, 128 or 256
+struct Kv4Cache {
+  uint8_t* data;
+  int64_t pages;
+  int page_shift;  // log2 of the page size (16 tokens or more)
+  int heads;
+  int head_dim;
+};
+hipError_t launch_kv4_store(const Kv4Cache& c, const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                            int64_t tokens, const int64_t* slots, int32_t* status, hipStream_t s);
+hipError_t launch_kv4_load(const Kv4Cache& c, const int64_t* slots, int64_t tokens, uint16_t* k, int64_t k_stride,
+                           uint16_t* v, int64_t v_stride, int32_t* status, hipStream_t s);
+struct Attn4 {
+  const uint8_t* data;
+  int64_t pages;
+  int page_shift, heads;
+  const uint16_t* q;
+  int64_t q_stride;
+  int q_heads, group;       // group = q_heads / heads query heads share a KV head
+  int batch, max_q;
+  int64_t total_q;
+  const int32_t* q_starts;  // null: max_q query tokens in every sequence
+  const int32_t* kv_lens;
+  const int32_t* table;
+  int64_t table_stride;
+  float scale_log2e;
+  int causal, window;
+  uint16_t* out;
+  int64_t out_stride;
+  float* lse;               // may be null
+  int32_t* status;
+};
+size_t attn4_scratch_bytes(int64_t batch, int64_t total_q, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                           int32_t max_q);
+hipError_t launch_attn4(const Attn4& a, int head_dim, void* scratch, hipStream_t s);
+
 // ---- backward of the NVFP4 + LoRA layer (backward.hip); n % 64 == 0, k % 128 == 0
 size_t backward_scratch_bytes(int64_t m, int64_t n, int64_t k, int32_t rank);
 hipError_t launch_backward_nvfp4(const uint16_t* x, const uint16_t* dy, int64_t m, int64_t n, int64_t k,
