@@ -543,14 +543,15 @@ static bool attn_sizes_ok(int64_t batch, int64_t total_q, int64_t q_heads, int64
   if (max_q <= 0 || max_q > QLINEAR_MAX_M || heads <= 0 || heads > 65535) return false;
   if (q_heads <= 0 || q_heads % heads || q_heads > 65536) return false;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return false;
-  // query rows of one KV head are counted in 32 bits
-  return max_q * (q_heads / heads) < (int64_t(1) << 30) && total_q * (q_heads / heads) < (int64_t(1) << 30);
+  // query rows and work items are counted in 32 bits
+  return max_q * (q_heads / heads) < (int64_t(1) << 30) && total_q * q_heads < (int64_t(1) << 30) &&
+         batch * heads < (int64_t(1) << 30);
 }
 
 size_t qlinear_attention_nvfp4_workspace(int32_t batch, int64_t total_q, int32_t q_heads, int32_t heads,
                                          int32_t head_dim, int32_t max_q_len) {
   if (!attn_sizes_ok(batch, total_q, q_heads, heads, head_dim, max_q_len)) return 0;
-  return ql::kWsReserved + up(ql::attn4_scratch_bytes(batch, total_q, q_heads, heads, head_dim, max_q_len));
+  return ql::kWsReserved + up(ql::attn4_scratch_bytes(head_dim));
 }
 
 qlinear_status qlinear_attention_nvfp4(const qlinear_kv_nvfp4* cache, const qlinear_attn_batch* seqs,
@@ -597,8 +598,10 @@ qlinear_status qlinear_attention_nvfp4(const qlinear_kv_nvfp4* cache, const qlin
   a.out_stride = out_stride;
   a.lse = lse;
   a.status = ql::ws_status(ws);
+  a.counters = ql::ws_counters(ws);
+  a.parts = (uint8_t*)ql::ws_scratch(ws);
   ql::clear_hip_error();
-  return hip_status(ql::launch_attn4(a, c.head_dim, ql::ws_scratch(ws), (hipStream_t)stream));
+  return hip_status(ql::launch_attn4(a, c.head_dim, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -18,6 +18,7 @@
 // that a lane holds one query row's logits for four consecutive tokens -- the four a lane
 // takes of V^T -- and P goes from one product to the next in registers.
 #include "../../include/qlinear.h"
+#include "gemv_common.hpp"
 #include "kv4_common.hpp"
 #include "launch.hpp"
 
@@ -61,10 +62,13 @@ __device__ __forceinline__ AttnRange attn_range(const Attn4& a, int b) {
 
 // Registers of 16 tokens of one head as one lane takes them.
 template <int D>
-struct Frag4 {
+struct Keys4 {
   uint32_t k[D / 32];   // token lane % 16, elements (lane / 16) D / 4 on
   uint32_t ks;          // their D / 64 scales
   uint32_t ke, ve;      // exponent bytes of tokens 4 (lane / 16) + 0..3
+};
+template <int D>
+struct Values4 {
   uint32_t v[D / 32];   // pair 16 j + lane % 16 of those tokens
   uint32_t vs[D / 32];  // their scales in block 2 j + (lane % 16) / 8
 };
@@ -88,7 +92,7 @@ __device__ __forceinline__ void load_words(uint32_t* dst, const uint8_t* p) {
 }
 
 template <int D>
-__device__ __forceinline__ void load_frag(Frag4<D>& f, const uint8_t* grp, int lane) {
+__device__ __forceinline__ void load_keys(Keys4<D>& f, const uint8_t* grp, int lane) {
   const int m = lane & 15, g = lane >> 4;
   load_words<D / 32>(f.k, grp + m * (D / 2) + g * (D / 8));
   const uint8_t* ks = grp + kv4_k_scales(D) + m * (D / 16) + g * (D / 64);
@@ -96,9 +100,13 @@ __device__ __forceinline__ void load_frag(Frag4<D>& f, const uint8_t* grp, int l
   if constexpr (D == 128) f.ks = *(const uint16_t*)ks;
   if constexpr (D == 256) f.ks = *(const uint32_t*)ks;
   f.ke = *(const uint32_t*)(grp + kv4_k_exps(D) + 4 * g);
+  f.ve = *(const uint32_t*)(grp + kv4_v_exps(D) + 4 * g);
+}
+template <int D>
+__device__ __forceinline__ void load_values(Values4<D>& f, const uint8_t* grp, int lane) {
+  const int m = lane & 15, g = lane >> 4;
   load_words<D / 32>(f.v, grp + kv4_v_codes(D) + lane * (D / 8));
   load_words<D / 32>(f.vs, grp + kv4_v_scales(D) + g * (D / 4) + (m >> 3) * (D / 8));
-  f.ve = *(const uint32_t*)(grp + kv4_v_exps(D) + 4 * g);
 }
 
 // Eight key elements times their scale (0xFF, a NaN token, gives NaN).
@@ -137,42 +145,144 @@ __device__ __forceinline__ f16x8 join8(const f16x2* a, const f16x2* b) {
   return f16x8{a[0][0], a[0][1], a[1][0], a[1][1], b[0][0], b[0][1], b[1][0], b[1][1]};
 }
 
-// One workgroup: 16 query rows (token, head of the group) of one sequence and KV head; the
-// waves take alternate 32-token steps and their sums are joined through shared memory.
+// The call's work, cut on the device from the lengths that are there when it runs (so that a
+// captured call follows them): an item is 16 query rows of one sequence and KV head against
+// `span` of its tokens, `span` the same for every sequence and such that there are about
+// kAttnItems of them; a sequence of at most `span` tokens is one item.  Items go (sequence,
+// row tile, head, split).  Every wave works the cut out for itself, 64 sequences at a time.
+constexpr int kAttnItems = 1024;  // four workgroups a CU
+constexpr int kAttnStep = 32;     // tokens of one wave's step
+struct AttnItem {
+  int nq, n;
+  int64_t q0;
+  int b, tile, head, split, splits;
+  int lo, span;  // first token of the sequence's range, tokens of a split
+  int part;      // first of the splits' partial results, when there are more than one
+};
+
+__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
+  for (int o = 32; o >= 1; o >>= 1) {
+    const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)v, o), hi = (uint32_t)__shfl_xor((int)(v >> 32), o);
+    v += ((uint64_t)hi << 32) | lo;
+  }
+  return v;
+}
+
+__device__ __forceinline__ int attn_lo(const Attn4& a, const AttnRange& r) {
+  return a.window ? max(r.n - r.nq + 1 - a.window, 0) & ~(kAttnStep - 1) : 0;
+}
+
+__device__ __forceinline__ bool attn_item(const Attn4& a, int id, AttnItem& it) {
+  const int lane = threadIdx.x & 63;
+  const auto cost = [&](const AttnRange& r, int& tiles, int& tok) {
+    tiles = (r.nq * a.group + 15) >> 4;
+    tok = max(r.n - attn_lo(a, r), 0);
+  };
+  AttnRange first{0, 0, 0, false};
+  uint64_t sum = 0;
+  bool bad = false;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    if (b0 + lane >= a.batch) continue;
+    const AttnRange r = attn_range(a, b0 + lane);
+    if (b0 == 0) first = r;
+    int tiles, tok;
+    cost(r, tiles, tok);
+    sum += (uint64_t)tiles * (uint64_t)tok;
+    bad |= r.bad;
+  }
+  if (blockIdx.x == 0 && threadIdx.x < 64 && __any(bad) && lane == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
+  sum = wave_sum_u64(sum) * (uint64_t)a.heads;
+  constexpr int kWgStep = kAttnWaves * kAttnStep;
+  const uint64_t want = (sum + kAttnItems - 1) / kAttnItems;
+  const int span = want <= kWgStep ? kWgStep : (int)min((want + kWgStep - 1) / kWgStep * kWgStep, (uint64_t)1 << 30);
+  int items = 0, parts = 0;  // of the sequences before b0
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    AttnRange r{0, 0, 0, false};
+    int tiles = 0, tok = 0;
+    if (b0 + lane < a.batch) {
+      r = b0 == 0 ? first : attn_range(a, b0 + lane);
+      cost(r, tiles, tok);
+    }
+    const int splits = tok > span ? (int)((uint32_t)(tok + span - 1) / (uint32_t)span) : 1;
+    const int mine = tiles * a.heads * splits, pmine = splits > 1 ? mine : 0;
+    int upto = mine, pupto = pmine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int x = __shfl_up(upto, o), y = __shfl_up(pupto, o);
+      if (lane >= o) {
+        upto += x;
+        pupto += y;
+      }
+    }
+    const uint64_t past = __ballot(items + upto > id);
+    if (past) {
+      const int j = __builtin_ctzll(past);
+      const int local = id - items - __builtin_amdgcn_readlane(upto - mine, j);
+      it.splits = __builtin_amdgcn_readlane(splits, j);
+      it.split = local % it.splits;
+      const int th = local / it.splits;
+      it.tile = th / a.heads;
+      it.head = th - it.tile * a.heads;
+      it.part = parts + __builtin_amdgcn_readlane(pupto - pmine, j) + th * it.splits;
+      it.b = b0 + j;
+      it.nq = __builtin_amdgcn_readlane(r.nq, j);
+      it.n = __builtin_amdgcn_readlane(r.n, j);
+      it.q0 = ((int64_t)__builtin_amdgcn_readlane((int)(r.q0 >> 32), j) << 32) |
+              (uint32_t)__builtin_amdgcn_readlane((int)r.q0, j);
+      it.span = span;
+      it.lo = a.window ? max(it.n - it.nq + 1 - a.window, 0) & ~(kAttnStep - 1) : 0;
+      return true;
+    }
+    items += __builtin_amdgcn_readlane(upto, 63);
+    parts += __builtin_amdgcn_readlane(pupto, 63);
+  }
+  return false;
+}
+
+// Partial results of a split: rows of D float32 sums, then m and l of the 16 rows.
 template <int D>
-__global__ __launch_bounds__(kAttnWaves * 64) void attn4_kernel(Attn4 a) {
+__host__ __device__ constexpr uint32_t attn_part_bytes() {
+  return 16 * (D + 2) * 4;
+}
+
+// One workgroup an item; the waves take alternate 32-token steps and their sums are joined
+// through shared memory.  Of a split sequence, the workgroup that arrives last joins the
+// splits' results, in their order.
+template <int D>
+__global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) void attn4_kernel(Attn4 a) {
   constexpr int KW = D / 32, kRow = D + 4;
   __shared__ float so[kAttnWaves][16][kRow];
   __shared__ float sm[kAttnWaves][16], sl[kAttnWaves][16];
+  __shared__ int last;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n16 = lane & 15, g = lane >> 4;
-  const int b = blockIdx.z, h = blockIdx.y;
-  const AttnRange rg = attn_range(a, b);
-  if (rg.bad && threadIdx.x == 0 && h == 0 && blockIdx.x == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
-  const int rows = rg.nq * a.group;
-  const int r0 = blockIdx.x * 16;
-  if (r0 >= rows) return;
+  AttnItem it;
+  if (!attn_item(a, blockIdx.x, it)) return;
+  const int h = it.head;
+  const int rows = it.nq * a.group;
+  const int r0 = it.tile * 16;
 
   // this lane's query row, and the tokens [from, to) that it sees
   const int row = r0 + n16;
   const bool live = row < rows;
   const int qi = (live ? row : rows - 1) / a.group;
   const int head = h * a.group + (live ? row : rows - 1) - qi * a.group;
-  const int to = a.causal ? rg.n - rg.nq + qi + 1 : rg.n;
+  const int to = a.causal ? it.n - it.nq + qi + 1 : it.n;
   const int from = a.window ? to - a.window : 0;
   // the tile's first and last row bound what the workgroup reads
   const int qa = r0 / a.group, qb = (r0 + 16 < rows ? r0 + 15 : rows - 1) / a.group;
-  const int hi = a.causal ? rg.n - rg.nq + qb + 1 : rg.n;          // some row sees [lo, hi)
-  const int lo = a.window ? max(rg.n - rg.nq + qa + 1 - a.window, 0) & ~31 : 0;
-  const int all_to = a.causal ? rg.n - rg.nq + qa + 1 : rg.n;      // every row sees [all_from, all_to)
-  const int all_from = a.window ? hi - a.window : 0;
+  const int end = a.causal ? it.n - it.nq + qb + 1 : it.n;         // some row sees [lo, hi)
+  const int lo = it.lo + it.split * it.span;
+  const int hi = it.split + 1 < it.splits ? min(end, lo + it.span) : end;
+  const int all_to = a.causal ? it.n - it.nq + qa + 1 : it.n;      // every row sees [all_from, all_to)
+  const int all_from = a.window ? end - a.window : 0;
 
   // the query row as f16 with its largest magnitude in [2^14, 2^15)
   f16x8 q[KW];
   float kc;
   {
     uint4 x[KW];
-    const uint16_t* qp = a.q + (rg.q0 + qi) * a.q_stride + (int64_t)head * D + g * (D / 4);
+    const uint16_t* qp = a.q + (it.q0 + qi) * a.q_stride + (int64_t)head * D + g * (D / 4);
     uint32_t amax = 0;
 #pragma unroll
     for (int s = 0; s < KW; ++s) {
@@ -201,23 +311,49 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn4_kernel(Attn4 a) {
 #pragma unroll
   for (int j = 0; j < 2 * KW; ++j) o[j] = f32x4{0, 0, 0, 0};
   float m = kNoMax, l = 0.0f;
-  const int32_t* table = a.table + (int64_t)b * a.table_stride;
+  const int32_t* table = a.table + (int64_t)it.b * a.table_stride;
   const int per = 1 << (a.page_shift - 4);
   bool bad_page = false;
 
-  for (int t0 = lo + wave * 32; t0 < hi; t0 += kAttnWaves * 32) {
-    Frag4<D> f[2];
-    bool ok[2];
+  // The wave's groups of 16 tokens are numbered x = 0, 1, ..: group x is at lo + 32 wave +
+  // 128 (x / 2) + 16 (x % 2).  Lane x % 64 looks up the page of group x for all; a page
+  // outside the cache becomes -1, and so does a group past the end.
+  int pages = 0;
+  const auto look_up = [&](int x0) {
+    const int x = x0 + lane;
+    const int t = lo + wave * 32 + (x >> 1) * (kAttnWaves * 32) + (x & 1) * 16;
+    pages = -1;
+    if (t < hi) {
+      pages = table[t >> a.page_shift];
+      if (pages < 0 || pages >= a.pages) {
+        pages = -1;
+        bad_page = true;
+      }
+    }
+  };
+  const auto group_at = [&](int x, int t) {
+    const int pg = max(__builtin_amdgcn_readlane(pages, x & 63), 0);
+    const int64_t gi = (((int64_t)pg * a.heads + h) << (a.page_shift - 4)) + ((t >> 4) & (per - 1));
+    return a.data + gi * kv4_group_bytes(D);
+  };
+
+  Keys4<D> f[2];
+  Values4<D> fv[2];
+  const uint8_t* grp[2];
+  bool ok[2] = {false, false};
+  int x = 0;
+  if (lo + wave * 32 < hi) {
+    look_up(0);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int t = t0 + 16 * u < hi ? t0 + 16 * u : t0;   // a second group past the end: the first again, masked
-      const int64_t pg = table[t >> a.page_shift];
-      ok[u] = pg >= 0 && pg < a.pages;
-      bad_page |= !ok[u];
-      ok[u] = ok[u] && t0 + 16 * u < hi;
-      const int64_t gi = (((pg >= 0 && pg < a.pages ? pg : 0) * a.heads + h) << (a.page_shift - 4)) + ((t >> 4) & (per - 1));
-      load_frag<D>(f[u], a.data + gi * kv4_group_bytes(D), lane);
+      ok[u] = __builtin_amdgcn_readlane(pages, u) >= 0;
+      grp[u] = group_at(u, lo + wave * 32 + 16 * u);
+      load_keys<D>(f[u], grp[u], lane);
     }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) load_values<D>(fv[u], grp[u], lane);
+  }
+  for (int t0 = lo + wave * 32; t0 < hi; t0 += kAttnWaves * 32) {
     f32x4 c[2];
     float kf[2][4], ve[2][4], lf[2][4];
 #pragma unroll
@@ -246,6 +382,18 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn4_kernel(Attn4 a) {
             lf[u][i] = 0.0f;
           }
         }
+      }
+    }
+    // the next step's keys are on their way from here, its values from when this step's are used
+    const bool more = t0 + kAttnWaves * 32 < hi;
+    if (more) {
+      x += 2;
+      if ((x & 63) == 0) look_up(x);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        ok[u] = __builtin_amdgcn_readlane(pages, (x + u) & 63) >= 0;
+        grp[u] = group_at(x + u, t0 + kAttnWaves * 32 + 16 * u);
+        load_keys<D>(f[u], grp[u], lane);
       }
     }
     float p[2][4], top = -__builtin_inff();
@@ -283,18 +431,22 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn4_kernel(Attn4 a) {
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float x = __builtin_amdgcn_exp2f(p[u][i]);
-        l = __builtin_fmaf(x, lf[u][i], l);
-        pf[4 * u + i] = (_Float16)x;
+        const float e = __builtin_amdgcn_exp2f(p[u][i]);
+        l = __builtin_fmaf(e, lf[u][i], l);
+        pf[4 * u + i] = (_Float16)e;
       }
 #pragma unroll
     for (int j = 0; j < KW; ++j) {
-      const ValuePair v0 = value4(f[0].v[j], f[0].vs[j]), v1 = value4(f[1].v[j], f[1].vs[j]);
+      const ValuePair v0 = value4(fv[0].v[j], fv[0].vs[j]), v1 = value4(fv[1].v[j], fv[1].vs[j]);
       o[2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(join8(v0.even, v1.even), pf, o[2 * j], 0, 0, 0);
       o[2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(join8(v0.odd, v1.odd), pf, o[2 * j + 1], 0, 0, 0);
     }
+    if (more) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) load_values<D>(fv[u], grp[u], lane);
+    }
   }
-  if (bad_page && lane == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
+  if (__any(bad_page) && lane == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
 
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
@@ -313,43 +465,93 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn4_kernel(Attn4 a) {
   // 16 threads a row, D / 16 elements each
   constexpr int E = D / 16;
   const int orow = threadIdx.x >> 4, part = threadIdx.x & 15;
-  if (r0 + orow >= rows) return;
+  const bool mine = r0 + orow < rows;
   float top = sm[0][orow];
 #pragma unroll
   for (int w = 1; w < kAttnWaves; ++w) top = __builtin_fmaxf(top, sm[w][orow]);
   float acc[E], lsum = 0.0f;
 #pragma unroll
-  for (int x = 0; x < E; ++x) acc[x] = 0.0f;
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
 #pragma unroll
   for (int w = 0; w < kAttnWaves; ++w) {
     const float s = __builtin_exp2f(sm[w][orow] - top);
     lsum += s * sl[w][orow];
 #pragma unroll
-    for (int x = 0; x < E; ++x) acc[x] += s * so[w][orow][part * E + x];
+    for (int e = 0; e < E; ++e) acc[e] += s * so[w][orow][part * E + e];
   }
+  if (it.splits > 1) {
+    const __amdgpu_buffer_rsrc_t rs = dev_rsrc(a.parts);
+    const uint32_t at = (uint32_t)(it.part + it.split) * attn_part_bytes<D>();
+    const uint32_t mine_at = (uint32_t)(orow * D + part * E) * 4;
+    if (mine) {
+#pragma unroll
+      for (int e = 0; e < E; e += 4)
+        st_dev4v(rs, at + mine_at + 4 * e, f32x4{acc[e], acc[e + 1], acc[e + 2], acc[e + 3]});
+      if (part == 0) {
+        st_dev_u32((uint32_t*)(a.parts + at + 16 * D * 4) + orow, __float_as_uint(top));
+        st_dev_u32((uint32_t*)(a.parts + at + 16 * D * 4) + 16 + orow, __float_as_uint(lsum));
+      }
+    }
+    wait_stores();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      uint32_t* c = a.counters + it.part;
+      const uint32_t old = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      last = old == (uint32_t)it.splits - 1;
+      if (last) st_dev_u32(c, 0u);
+    }
+    __syncthreads();
+    if (!last || !mine) return;
+    const uint32_t first = (uint32_t)it.part * attn_part_bytes<D>();
+    const uint32_t* ml = (const uint32_t*)(a.parts + first + 16 * D * 4) + orow;
+    constexpr uint32_t kStep = attn_part_bytes<D>() / 4;
+    top = kNoMax;
+    for (int s = 0; s < it.splits; ++s) top = __builtin_fmaxf(top, __uint_as_float(ld_dev_u32(ml + s * kStep)));
+    lsum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < it.splits; ++s) {
+      const float w = __builtin_exp2f(__uint_as_float(ld_dev_u32(ml + s * kStep)) - top);
+      lsum += w * __uint_as_float(ld_dev_u32(ml + s * kStep + 16));
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const f32x4 v = ld_dev4v(rs, first + (uint32_t)s * attn_part_bytes<D>() + mine_at + 4 * e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[e + i] += w * v[i];
+      }
+    }
+  }
+  if (!mine) return;
   const int oq = (r0 + orow) / a.group, oh = h * a.group + (r0 + orow) - oq * a.group;
   const float inv = lsum == 0.0f ? 0.0f : 0.001953125f / lsum;  // a row that sees nothing: zeros
-  uint16_t* op = a.out + (rg.q0 + oq) * a.out_stride + (int64_t)oh * D + part * E;
+  uint16_t* op = a.out + (it.q0 + oq) * a.out_stride + (int64_t)oh * D + part * E;
 #pragma unroll
-  for (int x = 0; x < E; x += 2) *(uint32_t*)(op + x) = pack_bf16x2_rne(acc[x] * inv, acc[x + 1] * inv);
+  for (int e = 0; e < E; e += 2) *(uint32_t*)(op + e) = pack_bf16x2_rne(acc[e] * inv, acc[e + 1] * inv);
   if (a.lse && part == 0)
-    a.lse[(rg.q0 + oq) * a.q_heads + oh] =
+    a.lse[(it.q0 + oq) * a.q_heads + oh] =
         lsum == 0.0f ? -__builtin_inff() : (__builtin_log2f(lsum) + top) * 0.6931471805599453f;
 }
 
-size_t attn4_scratch_bytes(int64_t batch, int64_t total_q, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
-                           int32_t max_q) {
-  (void)batch, (void)total_q, (void)q_heads, (void)kv_heads, (void)head_dim, (void)max_q;
-  return 0;
+// Items of split sequences: each has fewer than 2 tokens / span of them, so at most 2 kAttnItems.
+static_assert(2 * kAttnItems * 4 + kWsCounterOff <= kWsReserved, "one counter a split item");
+
+size_t attn4_scratch_bytes(int32_t head_dim) { return (size_t)2 * kAttnItems * 16 * (head_dim + 2) * 4; }
+
+template <int D>
+static hipError_t launch_d(const Attn4& a, hipStream_t s) {
+  // every 16 rows of every KV head, at most one tile a sequence more, and the splits
+  const int64_t tiles = (a.total_q * a.group >> 4) + a.batch;
+  const int64_t items = tiles * a.heads + kAttnItems;
+  if (items > (int64_t)INT32_MAX) return hipErrorInvalidValue;
+  attn4_kernel<D><<<(unsigned)items, kAttnWaves * 64, 0, s>>>(a);
+  return hipGetLastError();
 }
 
-hipError_t launch_attn4(const Attn4& a, int head_dim, void* scratch, hipStream_t s) {
-  (void)scratch;
-  const dim3 grid((unsigned)(((int64_t)a.max_q * a.group + 15) / 16), (unsigned)a.heads, (unsigned)a.batch);
-  if (head_dim == 64) attn4_kernel<64><<<grid, kAttnWaves * 64, 0, s>>>(a);
-  if (head_dim == 128) attn4_kernel<128><<<grid, kAttnWaves * 64, 0, s>>>(a);
-  if (head_dim == 256) attn4_kernel<256><<<grid, kAttnWaves * 64, 0, s>>>(a);
-  return hipGetLastError();
+hipError_t launch_attn4(const Attn4& a, int head_dim, hipStream_t s) {
+  if (head_dim == 64) return launch_d<64>(a, s);
+  if (head_dim == 128) return launch_d<128>(a, s);
+  return launch_d<256>(a, s);
 }
 
 }  // namespace ql

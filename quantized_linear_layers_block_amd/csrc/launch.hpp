@@ -92,10 +92,11 @@ struct Attn4 {
   int64_t out_stride;
   float* lse;               // may be null
   int32_t* status;
+  uint32_t* counters;       // zero before and after a call
+  uint8_t* parts;           // attn4_scratch_bytes
 };
-size_t attn4_scratch_bytes(int64_t batch, int64_t total_q, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
-                           int32_t max_q);
-hipError_t launch_attn4(const Attn4& a, int head_dim, void* scratch, hipStream_t s);
+size_t attn4_scratch_bytes(int32_t head_dim);
+hipError_t launch_attn4(const Attn4& a, int head_dim, hipStream_t s);
 
 // ---- backward of the NVFP4 + LoRA layer (backward.hip); n % 64 == 0, k % 128 == 0
 size_t backward_scratch_bytes(int64_t m, int64_t n, int64_t k, int32_t rank);
