@@ -384,15 +384,18 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
         }
       }
     }
-    // the next step's keys are on their way from here, its values from when this step's are used
-    const bool more = t0 + kAttnWaves * 32 < hi;
-    if (more) {
-      x += 2;
-      if ((x & 63) == 0) look_up(x);
+    // The next step's keys are on their way from here, its values from when this step's are
+    // used.  After the last step the same groups are fetched again: with a branch around the
+    // loads the compiler would wait for all that are in flight.
+    {
+      const bool more = t0 + kAttnWaves * 32 < hi;
+      x += more ? 2 : 0;
+      const int tn = t0 + (more ? kAttnWaves * 32 : 0);
+      if (more && (x & 63) == 0) look_up(x);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         ok[u] = __builtin_amdgcn_readlane(pages, (x + u) & 63) >= 0;
-        grp[u] = group_at(x + u, t0 + kAttnWaves * 32 + 16 * u);
+        grp[u] = group_at(x + u, tn + 16 * u);
         load_keys<D>(f[u], grp[u], lane);
       }
     }
@@ -441,10 +444,8 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
       o[2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(join8(v0.even, v1.even), pf, o[2 * j], 0, 0, 0);
       o[2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(join8(v0.odd, v1.odd), pf, o[2 * j + 1], 0, 0, 0);
     }
-    if (more) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) load_values<D>(fv[u], grp[u], lane);
-    }
+    for (int u = 0; u < 2; ++u) load_values<D>(fv[u], grp[u], lane);
   }
   if (__any(bad_page) && lane == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
 
