@@ -400,8 +400,8 @@ size_t qlinear_kv_nvfp4_bytes(int64_t pages, int32_t page_size, int32_t heads, i
 /* Store: k, v bf16 [tokens][heads][head_dim], token t at k + t * k_stride (v + t * v_stride),
  * strides in elements, multiples of 8 -- the k and v parts of a fused projection are taken
  * where they are -- into slots[t] (int64, device, distinct).  A token with an Inf or NaN in its
- * key or value row of a head becomes a NaN token of that head: every scale byte 0xFF, loads
- * give NaN, and attention gives NaN to the query rows that see it; QLINEAR_STATUS_NONFINITE is
+ * key or value row of a head becomes a NaN token of that head (key scales 0xFF, the rest of
+ * both rows zero with e = 0): loads give NaN for both rows, and attention gives NaN to the query rows that see it; QLINEAR_STATUS_NONFINITE is
  * set in *status_word (if not NULL).  A slot outside the cache is skipped and sets
  * QLINEAR_STATUS_BAD_ITEM.
  * Load: slots[t] -> k_out, v_out bf16 (same strides rule); either may be NULL.  A slot outside

@@ -10,8 +10,8 @@ to FP8; this is the 4-bit format of the QeRL pages at the same place.  Readings:
 * block scale  E4M3_RNE(fl32(amax_block * 2^-e / 6));
 * code         sign | E2M1_RNE(|x| * 2^-e / scale), magnitude 0 where the scale is 0;
 * value        E2M1 * E4M3 * 2^e, exact;
-* a token with Inf or NaN in its key or value row of a head: scale bytes 0xFF, codes 0, e = 0
-  in both rows, and NaN values;
+* a token with Inf or NaN in its key or value row of a head: key scale bytes 0xFF, codes and
+  value scales 0, e = 0, and NaN values in both rows;
 * attention    softmax over the tokens a query row sees, zeros and lse -inf for a row that
   sees none.
 
@@ -89,7 +89,7 @@ def store(data, k_bits, v_bits, slots):
             for side in range(2):
                 code, scale, e = (a[i * h + j] for a in enc[side])
                 if bad[i, j]:
-                    code, scale, e = np.zeros(d, np.uint8), np.full(d // 16, 0xFF, np.uint8), 0
+                    code, scale, e = np.zeros(d, np.uint8), np.full(d // 16, 0 if side else 0xFF, np.uint8), 0
                 flat[at[3 * side]] = code[0::2] | (code[1::2] << 4)
                 flat[at[3 * side + 1]] = scale
                 flat[at[3 * side + 2]] = e + 127
@@ -111,6 +111,8 @@ def load(data, slots, d):
                 code[0::2], code[1::2] = byte & 15, byte >> 4
                 scale = np.repeat(e4m3_decode(flat[at[3 * side + 1]]), 16)
                 out[side, i, j] = e2m1_decode(code) * scale * 2.0 ** (int(flat[at[3 * side + 2]]) - 127)
+                if flat[at[1][0]] == 0xFF:
+                    out[side, i, j] = np.nan
     return out[0], out[1]
 
 

@@ -65,11 +65,11 @@ template <int D>
 struct Keys4 {
   uint32_t k[D / 32];   // token lane % 16, elements (lane / 16) D / 4 on
   uint32_t ks;          // their D / 64 scales
-  uint32_t ke, ve;      // exponent bytes of tokens 4 (lane / 16) + 0..3
+  uint32_t e;           // an exponent byte: lanes 0..15 the key row's, the others the value row's of token lane % 16
 };
 template <int D>
 struct Values4 {
-  uint32_t v[D / 32];   // pair 16 j + lane % 16 of those tokens
+  uint32_t v[D / 32];   // pair 16 j + lane % 16 of tokens 4 (lane / 16) + 0..3
   uint32_t vs[D / 32];  // their scales in block 2 j + (lane % 16) / 8
 };
 
@@ -99,8 +99,7 @@ __device__ __forceinline__ void load_keys(Keys4<D>& f, const uint8_t* grp, int l
   if constexpr (D == 64) f.ks = *ks;
   if constexpr (D == 128) f.ks = *(const uint16_t*)ks;
   if constexpr (D == 256) f.ks = *(const uint32_t*)ks;
-  f.ke = *(const uint32_t*)(grp + kv4_k_exps(D) + 4 * g);
-  f.ve = *(const uint32_t*)(grp + kv4_v_exps(D) + 4 * g);
+  f.e = grp[(g ? kv4_v_exps(D) : kv4_k_exps(D)) + m];
 }
 template <int D>
 __device__ __forceinline__ void load_values(Values4<D>& f, const uint8_t* grp, int lane) {
@@ -109,44 +108,24 @@ __device__ __forceinline__ void load_values(Values4<D>& f, const uint8_t* grp, i
   load_words<D / 32>(f.vs, grp + kv4_v_scales(D) + g * (D / 4) + (m >> 3) * (D / 8));
 }
 
-// Eight key elements times their scale (0xFF, a NaN token, gives NaN).
-__device__ __forceinline__ f16x8 key8(uint32_t codes, uint32_t scale_byte) {
-  const uint32_t s = (scale_byte << 7) & 0x7F80u;
-  const f16x2 sp = __builtin_bit_cast(f16x2, s | (s << 16));
-  const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 256.0f, 0) * sp;
-  const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 256.0f, 1) * sp;
-  const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 256.0f, 2) * sp;
-  const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 256.0f, 3) * sp;
+// Two E4M3 scales (bytes 0 and 1 of w, or 2 and 3) as f16, exactly; 0x7F and 0xFF are NaN.
+template <bool HI>
+__device__ __forceinline__ f16x2 scales2(uint32_t w) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, HI);
+}
+
+// Eight elements of one dword of codes times a scale; the products are exact.
+__device__ __forceinline__ f16x8 scaled8(uint32_t codes, f16x2 s0, f16x2 s1, f16x2 s2, f16x2 s3) {
+  const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 0) * s0;
+  const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 1) * s1;
+  const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 2) * s2;
+  const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 3) * s3;
   return f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
-
-struct ValuePair {  // four tokens of the even and of the odd element
-  f16x2 even[2], odd[2];
-};
-
-// One dword of V (a pair of elements of four tokens) times the four tokens' scales.  A scale
-// byte of unwritten memory may be anything: bit 7 is dropped, which leaves finite numbers.
-__device__ __forceinline__ ValuePair value4(uint32_t w, uint32_t scales) {
-  const uint32_t s = scales & 0x7F7F7F7Fu;
-  const f16x2 s01 = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0u, s, 0x010C000Cu) >> 1);
-  const f16x2 s23 = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0u, s, 0x030C020Cu) >> 1);
-  // nibbles of the even (low) and odd (high) elements of tokens (0, 1) to byte 0, (2, 3) to byte 2
-  const uint32_t m = 0x000F000Fu, w4 = w >> 4, w8 = w >> 8;
-  const uint32_t ev = (w & m) | (w4 & ~m), od = (w4 & m) | (w8 & ~m);
-  ValuePair r;
-  r.even[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(ev, 256.0f, 0) * s01;
-  r.even[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(ev, 256.0f, 2) * s23;
-  r.odd[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(od, 256.0f, 0) * s01;
-  r.odd[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(od, 256.0f, 2) * s23;
-  return r;
-}
-
-__device__ __forceinline__ f16x8 join8(const f16x2* a, const f16x2* b) {
-  return f16x8{a[0][0], a[0][1], a[1][0], a[1][1], b[0][0], b[0][1], b[1][0], b[1][1]};
-}
+__device__ __forceinline__ f16x2 both(_Float16 s) { return f16x2{s, s}; }
 
 // The call's work, cut on the device from the lengths that are there when it runs (so that a
-// captured call follows them): an item is 16 query rows of one sequence and KV head against
+// captured call follows them): an item is R query rows of one sequence and KV head against
 // `span` of its tokens, `span` the same for every sequence and such that there are about
 // kAttnItems of them; a sequence of at most `span` tokens is one item.  Items go (sequence,
 // row tile, head, split).  Every wave works the cut out for itself, 64 sequences at a time.
@@ -172,10 +151,11 @@ __device__ __forceinline__ int attn_lo(const Attn4& a, const AttnRange& r) {
   return a.window ? max(r.n - r.nq + 1 - a.window, 0) & ~(kAttnStep - 1) : 0;
 }
 
+template <int R>
 __device__ __forceinline__ bool attn_item(const Attn4& a, int id, AttnItem& it) {
   const int lane = threadIdx.x & 63;
   const auto cost = [&](const AttnRange& r, int& tiles, int& tok) {
-    tiles = (r.nq * a.group + 15) >> 4;
+    tiles = (r.nq * a.group + R - 1) / R;
     tok = max(r.n - attn_lo(a, r), 0);
   };
   AttnRange first{0, 0, 0, false};
@@ -239,50 +219,66 @@ __device__ __forceinline__ bool attn_item(const Attn4& a, int id, AttnItem& it) 
   return false;
 }
 
-// Partial results of a split: rows of D float32 sums, then m and l of the 16 rows.
-template <int D>
+// Partial results of a split: R rows of D float32 sums, then m and l of the rows.
+template <int D, int R>
 __host__ __device__ constexpr uint32_t attn_part_bytes() {
-  return 16 * (D + 2) * 4;
+  return R * (D + 2) * 4;
+}
+
+// x / d for 0 <= x < d + 16.
+__device__ __forceinline__ int small_div(int x, int d) {
+  return d >= 16 ? x >= d : (int)(((float)x + 0.5f) * __builtin_amdgcn_rcpf((float)d));
 }
 
 // One workgroup an item; the waves take alternate 32-token steps and their sums are joined
 // through shared memory.  Of a split sequence, the workgroup that arrives last joins the
 // splits' results, in their order.
-template <int D>
+//
+// A lane's dword of V holds an even and an odd element of four tokens, and the conversion
+// gives them as pairs.  The pairs stay together as neighbours along the product's depth,
+// with P beside zeros: [p 0] takes the even elements and [0 p] the odd ones.  That doubles the
+// matrix instructions of the second product, which have room, and saves the vector
+// instructions that would part the pairs, which have none.  With R = 8 rows the two are the
+// two halves of the 16 columns of one product, with R = 16 two products.
+template <int D, int R>
 __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) void attn4_kernel(Attn4 a) {
-  constexpr int KW = D / 32, kRow = D + 4;
-  __shared__ float so[kAttnWaves][16][kRow];
-  __shared__ float sm[kAttnWaves][16], sl[kAttnWaves][16];
+  constexpr int KW = D / 32, kRow = D + 4, P = R / 8;
+  __shared__ float so[kAttnWaves][R][kRow];
+  __shared__ float sm[kAttnWaves][R], sl[kAttnWaves][R];
+  __shared__ __attribute__((aligned(16))) float sx[kAttnWaves][2][64];
   __shared__ int last;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n16 = lane & 15, g = lane >> 4;
+  const int rn = R == 16 ? n16 : n16 & 7;                 // this lane's query row of the tile
+  const int odd_shift = R == 16 ? 16 : (n16 >> 3) << 4;   // where p goes beside its zero
   AttnItem it;
-  if (!attn_item(a, blockIdx.x, it)) return;
+  if (!attn_item<R>(a, blockIdx.x, it)) return;
   const int h = it.head;
   const int rows = it.nq * a.group;
-  const int r0 = it.tile * 16;
+  const int r0 = it.tile * R;
+  const int live = min(rows - r0, R);   // rows of the tile; lanes past them repeat the last
 
-  // this lane's query row, and the tokens [from, to) that it sees
-  const int row = r0 + n16;
-  const bool live = row < rows;
-  const int qi = (live ? row : rows - 1) / a.group;
-  const int head = h * a.group + (live ? row : rows - 1) - qi * a.group;
-  const int to = a.causal ? it.n - it.nq + qi + 1 : it.n;
+  // the query tokens of the tile, this lane's, and the tokens [from, to) that it sees
+  const int qa = r0 / a.group, ra = r0 - qa * a.group;
+  const int qb = qa + small_div(ra + live - 1, a.group);
+  const int mine_r = min(rn, live - 1);
+  const int dq = small_div(ra + mine_r, a.group);
+  const int head = h * a.group + ra + mine_r - dq * a.group;
+  const int to = a.causal ? it.n - it.nq + qa + dq + 1 : it.n;
   const int from = a.window ? to - a.window : 0;
-  // the tile's first and last row bound what the workgroup reads
-  const int qa = r0 / a.group, qb = (r0 + 16 < rows ? r0 + 15 : rows - 1) / a.group;
-  const int end = a.causal ? it.n - it.nq + qb + 1 : it.n;         // some row sees [lo, hi)
+  const int end = a.causal ? it.n - it.nq + qb + 1 : it.n;         // some row sees [begin, end)
+  const int all_to = a.causal ? it.n - it.nq + qa + 1 : it.n;      // every row sees [all_from, all_to)
+  const int begin = a.window ? max(all_to - a.window, 0) : 0;
+  const int all_from = a.window ? end - a.window : 0;
   const int lo = it.lo + it.split * it.span;
   const int hi = it.split + 1 < it.splits ? min(end, lo + it.span) : end;
-  const int all_to = a.causal ? it.n - it.nq + qa + 1 : it.n;      // every row sees [all_from, all_to)
-  const int all_from = a.window ? end - a.window : 0;
 
   // the query row as f16 with its largest magnitude in [2^14, 2^15)
   f16x8 q[KW];
   float kc;
   {
     uint4 x[KW];
-    const uint16_t* qp = a.q + (it.q0 + qi) * a.q_stride + (int64_t)head * D + g * (D / 4);
+    const uint16_t* qp = a.q + (it.q0 + qa + dq) * a.q_stride + (int64_t)head * D + g * (D / 4);
     uint32_t amax = 0;
 #pragma unroll
     for (int s = 0; s < KW; ++s) {
@@ -307,23 +303,25 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
     }
   }
 
-  f32x4 o[2 * KW];
+  f32x4 o[P][KW];
 #pragma unroll
-  for (int j = 0; j < 2 * KW; ++j) o[j] = f32x4{0, 0, 0, 0};
+  for (int y = 0; y < P; ++y)
+#pragma unroll
+    for (int j = 0; j < KW; ++j) o[y][j] = f32x4{0, 0, 0, 0};
   float m = kNoMax, l = 0.0f;
   const int32_t* table = a.table + (int64_t)it.b * a.table_stride;
   const int per = 1 << (a.page_shift - 4);
   bool bad_page = false;
 
   // The wave's groups of 16 tokens are numbered x = 0, 1, ..: group x is at lo + 32 wave +
-  // 128 (x / 2) + 16 (x % 2).  Lane x % 64 looks up the page of group x for all; a page
-  // outside the cache becomes -1, and so does a group past the end.
+  // 128 (x / 2) + 16 (x % 2).  Lane x % 64 looks up the page of group x for all: -1 where it is
+  // outside the cache, and where no row of the tile sees the group.
   int pages = 0;
   const auto look_up = [&](int x0) {
     const int x = x0 + lane;
     const int t = lo + wave * 32 + (x >> 1) * (kAttnWaves * 32) + (x & 1) * 16;
     pages = -1;
-    if (t < hi) {
+    if (t < hi && t + 16 > begin) {
       pages = table[t >> a.page_shift];
       if (pages < 0 || pages >= a.pages) {
         pages = -1;
@@ -354,22 +352,34 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
     for (int u = 0; u < 2; ++u) load_values<D>(fv[u], grp[u], lane);
   }
   for (int t0 = lo + wave * 32; t0 < hi; t0 += kAttnWaves * 32) {
-    f32x4 c[2];
-    float kf[2][4], ve[2][4], lf[2][4];
+    // what depends on the token alone is worked out by one lane a token and shared: 2^ek, ev + 127
+    // and 2^(-9 - ev) at 0, 16 and 32 of sx
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+      const uint32_t b23 = f[u].e << 23;
+      const float ve = (float)f[u].e;
+      const float w = g == 0 ? __uint_as_float(b23) : g == 1 ? ve : __uint_as_float((245u << 23) - b23);
+      sx[wave][u][lane] = w;
+    }
+    __builtin_amdgcn_wave_barrier();
+    f32x4 c[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const f16x2 s01 = scales2<false>(f[u].ks), s23 = scales2<true>(f[u].ks);
       c[u] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int s = 0; s < KW; ++s)
-        c[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key8(f[u].k[s], (f[u].ks >> (8 * (s >> 1))) & 0xFFu), q[s], c[u],
-                                                      0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t eb = (f[u].ke >> (8 * i)) & 0xFFu, vb = (f[u].ve >> (8 * i)) & 0xFFu;
-        kf[u][i] = __uint_as_float(eb << 23) * kc;
-        ve[u][i] = (float)vb;
-        lf[u][i] = __uint_as_float((245u - vb) << 23);
+      for (int s = 0; s < KW; ++s) {
+        const f16x2 sp = both((s >> 1) < 2 ? s01[(s >> 1) & 1] : s23[(s >> 1) & 1]);
+        c[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(scaled8(f[u].k[s], sp, sp, sp, sp), q[s], c[u], 0, 0, 0);
       }
+    }
+    f32x4 kf[2], ve[2], lf[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      kf[u] = *(const f32x4*)&sx[wave][u][4 * g];
+      ve[u] = *(const f32x4*)&sx[wave][u][16 + 4 * g];
+      lf[u] = *(const f32x4*)&sx[wave][u][32 + 4 * g];
+      kf[u] *= kc;
       const int t = t0 + 16 * u;
       if (!ok[u] || t < all_from || t + 16 > all_to) {
 #pragma unroll
@@ -382,6 +392,12 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
             lf[u][i] = 0.0f;
           }
         }
+        // tokens that no row sees may be memory that was never written: no NaN from their scales
+        const int t4 = t + 4 * g;
+        const int skip = min(max(begin - t4, 0), 4), keep = ok[u] ? min(max(it.n - t4, 0), 4) : 0;
+        const uint32_t mask = (uint32_t)(((uint64_t)1 << (8 * keep)) - 1) & ~(uint32_t)(((uint64_t)1 << (8 * skip)) - 1);
+#pragma unroll
+        for (int j = 0; j < KW; ++j) fv[u].vs[j] &= mask;
       }
     }
     // The next step's keys are on their way from here, its values from when this step's are
@@ -423,26 +439,34 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
       m = mn;
       l *= shrink;
 #pragma unroll
-      for (int j = 0; j < 2 * KW; ++j) o[j] *= shrink;
+      for (int y = 0; y < P; ++y)
+#pragma unroll
+        for (int j = 0; j < KW; ++j) o[y][j] *= shrink;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[u][i] = p[u][i] - m + 9.0f;
     }
-    f16x8 pf;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) {
+      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+      u32x4 pe, po;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float e = __builtin_amdgcn_exp2f(p[u][i]);
         l = __builtin_fmaf(e, lf[u][i], l);
-        pf[4 * u + i] = (_Float16)e;
+        const uint32_t hbits = __builtin_bit_cast(uint16_t, (_Float16)e);
+        pe[i] = hbits;
+        po[i] = hbits << odd_shift;
       }
 #pragma unroll
-    for (int j = 0; j < KW; ++j) {
-      const ValuePair v0 = value4(fv[0].v[j], fv[0].vs[j]), v1 = value4(fv[1].v[j], fv[1].vs[j]);
-      o[2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(join8(v0.even, v1.even), pf, o[2 * j], 0, 0, 0);
-      o[2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(join8(v0.odd, v1.odd), pf, o[2 * j + 1], 0, 0, 0);
+      for (int j = 0; j < KW; ++j) {
+        const f16x2 s01 = scales2<false>(fv[u].vs[j]), s23 = scales2<true>(fv[u].vs[j]);
+        const f16x8 v = scaled8(fv[u].v[j], both(s01[0]), both(s01[1]), both(s23[0]), both(s23[1]));
+        o[0][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, __builtin_bit_cast(f16x8, R == 16 ? pe : po), o[0][j], 0, 0, 0);
+        if constexpr (R == 16)
+          o[P - 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, __builtin_bit_cast(f16x8, po), o[P - 1][j], 0, 0, 0);
+      }
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) load_values<D>(fv[u], grp[u], lane);
@@ -452,45 +476,47 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
 #pragma unroll
-  for (int j = 0; j < KW; ++j)  // elements 32 j + 8 g + 2 i (even) and + 1 (odd)
+  for (int y = 0; y < P; ++y)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      so[wave][n16][32 * j + 8 * g + 2 * i] = o[2 * j][i];
-      so[wave][n16][32 * j + 8 * g + 2 * i + 1] = o[2 * j + 1][i];
-    }
-  if (g == 0) {
-    sm[wave][n16] = m;
-    sl[wave][n16] = l;
+    for (int j = 0; j < KW; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        so[wave][rn][32 * j + 8 * g + 2 * i + (R == 16 ? y : n16 >> 3)] = o[y][j][i];
+  if (g == 0 && n16 < R) {
+    sm[wave][rn] = m;
+    sl[wave][rn] = l;
   }
   __syncthreads();
-  // 16 threads a row, D / 16 elements each
-  constexpr int E = D / 16;
-  const int orow = threadIdx.x >> 4, part = threadIdx.x & 15;
-  const bool mine = r0 + orow < rows;
-  float top = sm[0][orow];
+  // E elements of a row a thread
+  constexpr int E = R * D / (kAttnWaves * 64) < 4 ? 4 : R * D / (kAttnWaves * 64), kPer = D / E;
+  const int orow = threadIdx.x / kPer, part = threadIdx.x % kPer;
+  const bool mine = orow < live;
+  const int src = mine ? orow : 0;
+  float top = sm[0][src];
 #pragma unroll
-  for (int w = 1; w < kAttnWaves; ++w) top = __builtin_fmaxf(top, sm[w][orow]);
+  for (int w = 1; w < kAttnWaves; ++w) top = __builtin_fmaxf(top, sm[w][src]);
   float acc[E], lsum = 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
 #pragma unroll
   for (int w = 0; w < kAttnWaves; ++w) {
-    const float s = __builtin_exp2f(sm[w][orow] - top);
-    lsum += s * sl[w][orow];
+    const float s = __builtin_exp2f(sm[w][src] - top);
+    lsum += s * sl[w][src];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += s * so[w][orow][part * E + e];
+    for (int e = 0; e < E; ++e) acc[e] += s * so[w][src][part * E + e];
   }
   if (it.splits > 1) {
+    constexpr uint32_t kBytes = attn_part_bytes<D, R>();
     const __amdgpu_buffer_rsrc_t rs = dev_rsrc(a.parts);
-    const uint32_t at = (uint32_t)(it.part + it.split) * attn_part_bytes<D>();
-    const uint32_t mine_at = (uint32_t)(orow * D + part * E) * 4;
+    const uint32_t at = (uint32_t)(it.part + it.split) * kBytes;
+    const uint32_t mine_at = (uint32_t)(src * D + part * E) * 4;
     if (mine) {
 #pragma unroll
       for (int e = 0; e < E; e += 4)
         st_dev4v(rs, at + mine_at + 4 * e, f32x4{acc[e], acc[e + 1], acc[e + 2], acc[e + 3]});
       if (part == 0) {
-        st_dev_u32((uint32_t*)(a.parts + at + 16 * D * 4) + orow, __float_as_uint(top));
-        st_dev_u32((uint32_t*)(a.parts + at + 16 * D * 4) + 16 + orow, __float_as_uint(lsum));
+        st_dev_u32((uint32_t*)(a.parts + at + R * D * 4) + src, __float_as_uint(top));
+        st_dev_u32((uint32_t*)(a.parts + at + R * D * 4) + R + src, __float_as_uint(lsum));
       }
     }
     wait_stores();
@@ -503,32 +529,33 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
     }
     __syncthreads();
     if (!last || !mine) return;
-    const uint32_t first = (uint32_t)it.part * attn_part_bytes<D>();
-    const uint32_t* ml = (const uint32_t*)(a.parts + first + 16 * D * 4) + orow;
-    constexpr uint32_t kStep = attn_part_bytes<D>() / 4;
+    const uint32_t first = (uint32_t)it.part * kBytes;
+    const uint32_t* ml = (const uint32_t*)(a.parts + first + R * D * 4) + src;
     top = kNoMax;
-    for (int s = 0; s < it.splits; ++s) top = __builtin_fmaxf(top, __uint_as_float(ld_dev_u32(ml + s * kStep)));
+    for (int s = 0; s < it.splits; ++s) top = __builtin_fmaxf(top, __uint_as_float(ld_dev_u32(ml + s * (kBytes / 4))));
     lsum = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
 #pragma unroll 4
     for (int s = 0; s < it.splits; ++s) {
-      const float w = __builtin_exp2f(__uint_as_float(ld_dev_u32(ml + s * kStep)) - top);
-      lsum += w * __uint_as_float(ld_dev_u32(ml + s * kStep + 16));
+      const float w = __builtin_exp2f(__uint_as_float(ld_dev_u32(ml + s * (kBytes / 4))) - top);
+      lsum += w * __uint_as_float(ld_dev_u32(ml + s * (kBytes / 4) + R));
 #pragma unroll
       for (int e = 0; e < E; e += 4) {
-        const f32x4 v = ld_dev4v(rs, first + (uint32_t)s * attn_part_bytes<D>() + mine_at + 4 * e);
+        const f32x4 v = ld_dev4v(rs, first + (uint32_t)s * kBytes + mine_at + 4 * e);
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[e + i] += w * v[i];
       }
     }
   }
   if (!mine) return;
-  const int oq = (r0 + orow) / a.group, oh = h * a.group + (r0 + orow) - oq * a.group;
+  const int oq = qa + small_div(ra + src, a.group), oh = h * a.group + (r0 + src) - oq * a.group;
   const float inv = lsum == 0.0f ? 0.0f : 0.001953125f / lsum;  // a row that sees nothing: zeros
   uint16_t* op = a.out + (it.q0 + oq) * a.out_stride + (int64_t)oh * D + part * E;
 #pragma unroll
-  for (int e = 0; e < E; e += 2) *(uint32_t*)(op + e) = pack_bf16x2_rne(acc[e] * inv, acc[e + 1] * inv);
+  for (int e = 0; e < E; e += 4)
+    *(uint2*)(op + e) = make_uint2(pack_bf16x2_rne(acc[e] * inv, acc[e + 1] * inv),
+                                   pack_bf16x2_rne(acc[e + 2] * inv, acc[e + 3] * inv));
   if (a.lse && part == 0)
     a.lse[(it.q0 + oq) * a.q_heads + oh] =
         lsum == 0.0f ? -__builtin_inff() : (__builtin_log2f(lsum) + top) * 0.6931471805599453f;
@@ -539,14 +566,19 @@ static_assert(2 * kAttnItems * 4 + kWsCounterOff <= kWsReserved, "one counter a 
 
 size_t attn4_scratch_bytes(int32_t head_dim) { return (size_t)2 * kAttnItems * 16 * (head_dim + 2) * 4; }
 
-template <int D>
-static hipError_t launch_d(const Attn4& a, hipStream_t s) {
-  // every 16 rows of every KV head, at most one tile a sequence more, and the splits
-  const int64_t tiles = (a.total_q * a.group >> 4) + a.batch;
+template <int D, int R>
+static hipError_t launch_r(const Attn4& a, hipStream_t s) {
+  // every R rows of every KV head, at most one tile a sequence more, and the splits
+  const int64_t tiles = a.total_q * a.group / R + a.batch;
   const int64_t items = tiles * a.heads + kAttnItems;
   if (items > (int64_t)INT32_MAX) return hipErrorInvalidValue;
-  attn4_kernel<D><<<(unsigned)items, kAttnWaves * 64, 0, s>>>(a);
+  attn4_kernel<D, R><<<(unsigned)items, kAttnWaves * 64, 0, s>>>(a);
   return hipGetLastError();
+}
+
+template <int D>
+static hipError_t launch_d(const Attn4& a, hipStream_t s) {
+  return (int64_t)a.max_q * a.group <= 8 ? launch_r<D, 8>(a, s) : launch_r<D, 16>(a, s);
 }
 
 hipError_t launch_attn4(const Attn4& a, int head_dim, hipStream_t s) {

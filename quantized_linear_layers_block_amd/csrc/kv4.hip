@@ -99,9 +99,10 @@ __global__ __launch_bounds__(kKv4Threads) void kv4_store_kernel(
     int ek = kv4_exponent(ak), ev = kv4_exponent(av);
     uint32_t sk, sv;
     uint32_t ck = kv4_encode8(xk, bk, ek, sk), cv = kv4_encode8(xv, bv, ev, sv);
-    if (umax(ak, av) >= kBf16InfBits) {  // a token with Inf or NaN is a NaN token
+    if (umax(ak, av) >= kBf16InfBits) {  // a token with Inf or NaN is a NaN token, marked in its key scales
       ck = cv = 0;
-      sk = sv = 0xFF;
+      sk = 0xFF;
+      sv = 0;
       ek = ev = 0;
       if (part == 0 && status) atomicOr(status, (int32_t)kStatusNonFinite);
     }
@@ -159,8 +160,8 @@ __global__ __launch_bounds__(kKv4Threads) void kv4_load_kernel(
       uint32_t c = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) c |= (uint32_t)gv[i * (D / 8)] << (8 * i);
-      ov4 = kv4_decode8(c, g[kv4_v_scales(D) + (t >> 2) * (D / 4) + (b & 1) * (D / 8) + (b >> 1) * 4 + (t & 3)],
-                        g[kv4_v_exps(D) + t]);
+      const uint32_t sc = g[kv4_v_scales(D) + (t >> 2) * (D / 4) + (b & 1) * (D / 8) + (b >> 1) * 4 + (t & 3)];
+      ov4 = kv4_decode8(c, g[kv4_k_scales(D) + t * (D / 16)] == 0xFF ? 0xFFu : sc, g[kv4_v_exps(D) + t]);
     }
     if (!ok) {
       ok4 = ov4 = make_uint4(0, 0, 0, 0);
