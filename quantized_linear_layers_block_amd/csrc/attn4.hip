@@ -60,12 +60,26 @@ __device__ __forceinline__ AttnRange attn_range(const Attn4& a, int b) {
   return r;
 }
 
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+  return ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+}
+// The same for a sequence that the whole wave asks for, in scalar registers.
+__device__ __forceinline__ AttnRange attn_range_uniform(const Attn4& a, int b) {
+  AttnRange r = attn_range(a, b);
+  r.nq = __builtin_amdgcn_readfirstlane(r.nq);
+  r.n = __builtin_amdgcn_readfirstlane(r.n);
+  r.q0 = (int64_t)uniform((uint64_t)r.q0);
+  return r;
+}
+
 // Registers of 16 tokens of one head as one lane takes them.
 template <int D>
 struct Keys4 {
   uint32_t k[D / 32];   // token lane % 16, elements (lane / 16) D / 4 on
-  uint32_t ks;          // their D / 64 scales
-  uint32_t e;           // an exponent byte: lanes 0..15 the key row's, the others the value row's of token lane % 16
+  uint32_t ks;          // their D / 64 scales, at bit 8 (lane / 16) D / 64 % 32
+  uint32_t e;           // at byte lane % 4 the exponent byte of token lane % 16: the key row's in
+                        // lanes 0..15, the value row's in the others
 };
 template <int D>
 struct Values4 {
@@ -95,11 +109,9 @@ template <int D>
 __device__ __forceinline__ void load_keys(Keys4<D>& f, const uint8_t* grp, int lane) {
   const int m = lane & 15, g = lane >> 4;
   load_words<D / 32>(f.k, grp + m * (D / 2) + g * (D / 8));
-  const uint8_t* ks = grp + kv4_k_scales(D) + m * (D / 16) + g * (D / 64);
-  if constexpr (D == 64) f.ks = *ks;
-  if constexpr (D == 128) f.ks = *(const uint16_t*)ks;
-  if constexpr (D == 256) f.ks = *(const uint32_t*)ks;
-  f.e = grp[(g ? kv4_v_exps(D) : kv4_k_exps(D)) + m];
+  // whole dwords: the compiler's widening copies of shorter loads would wait for them at once
+  f.ks = *(const uint32_t*)(grp + kv4_k_scales(D) + ((m * (D / 16) + g * (D / 64)) & ~3));
+  f.e = *(const uint32_t*)(grp + (g ? kv4_v_exps(D) : kv4_k_exps(D)) + (m & ~3));
 }
 template <int D>
 __device__ __forceinline__ void load_values(Values4<D>& f, const uint8_t* grp, int lane) {
@@ -124,20 +136,17 @@ __device__ __forceinline__ f16x8 scaled8(uint32_t codes, f16x2 s0, f16x2 s1, f16
 }
 __device__ __forceinline__ f16x2 both(_Float16 s) { return f16x2{s, s}; }
 
-// The call's work, cut on the device from the lengths that are there when it runs (so that a
-// captured call follows them): an item is R query rows of one sequence and KV head against
-// `span` of its tokens, `span` the same for every sequence and such that there are about
-// kAttnItems of them; a sequence of at most `span` tokens is one item.  Items go (sequence,
-// row tile, head, split).  Every wave works the cut out for itself, 64 sequences at a time.
-constexpr int kAttnItems = 1024;  // four workgroups a CU
-constexpr int kAttnStep = 32;     // tokens of one wave's step
-struct AttnItem {
-  int nq, n;
-  int64_t q0;
-  int b, tile, head, split, splits;
-  int lo, span;  // first token of the sequence's range, tokens of a split
-  int part;      // first of the splits' partial results, when there are more than one
-};
+// The call's work is cut on the device from the lengths that are there when it runs (so that a
+// captured call follows them).  A unit is R query rows of one sequence and KV head, as many
+// chunks of 128 tokens long as the sequence needs (one at least); the units in the order
+// (sequence, row tile, head) make one line of chunks, of which each workgroup takes the same
+// length.  One round of workgroups fills the chip and all end together, whatever the lengths;
+// a unit that lies in more than one workgroup's part is joined from partial results.
+constexpr int kAttnStep = 32;                        // tokens of one wave's step
+constexpr int kAttnChunk = kAttnWaves * kAttnStep;   // of the workgroup's
+// Workgroups that fit the chip: 256 CUs and the waves a SIMD holds by the kernel's registers.
+constexpr int attn_wgs_per_cu(int d) { return d == 256 ? 2 : 3; }
+constexpr int attn_wgs(int d) { return 256 * attn_wgs_per_cu(d); }
 
 __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
   for (int o = 32; o >= 1; o >>= 1) {
@@ -147,74 +156,68 @@ __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
   return v;
 }
 
-__device__ __forceinline__ int attn_lo(const Attn4& a, const AttnRange& r) {
-  return a.window ? max(r.n - r.nq + 1 - a.window, 0) & ~(kAttnStep - 1) : 0;
+// The first token that some row of the sequence sees, down to a step.
+__device__ __forceinline__ int attn_lo(const Attn4& a, int nq, int n) {
+  return a.window ? max(n - nq + 1 - a.window, 0) & ~(kAttnStep - 1) : 0;
 }
 
-template <int R>
-__device__ __forceinline__ bool attn_item(const Attn4& a, int id, AttnItem& it) {
+// A workgroup's place on the line.
+struct AttnPlace {
+  uint64_t pos, stop;   // chunks of the line
+  uint64_t each;        // chunks a workgroup
+  int b, tile, head, k; // unit and its first chunk here
+};
+
+// Every wave works this out for itself, 64 sequences at a time.
+template <int R, int WGS>
+__device__ __forceinline__ bool attn_place(const Attn4& a, AttnPlace& pl) {
   const int lane = threadIdx.x & 63;
-  const auto cost = [&](const AttnRange& r, int& tiles, int& tok) {
-    tiles = (r.nq * a.group + R - 1) / R;
-    tok = max(r.n - attn_lo(a, r), 0);
-  };
-  AttnRange first{0, 0, 0, false};
-  uint64_t sum = 0;
-  bool bad = false;
-  for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    if (b0 + lane >= a.batch) continue;
-    const AttnRange r = attn_range(a, b0 + lane);
-    if (b0 == 0) first = r;
-    int tiles, tok;
-    cost(r, tiles, tok);
-    sum += (uint64_t)tiles * (uint64_t)tok;
+  const auto line = [&](int b, bool& bad) -> uint64_t {  // chunks of a sequence's units (all heads)
+    if (b >= a.batch) return 0;
+    const AttnRange r = attn_range(a, b);
     bad |= r.bad;
-  }
+    const uint32_t tiles = (uint32_t)(r.nq * a.group + R - 1) / R;
+    const uint32_t chunks = max((max(r.n - attn_lo(a, r.nq, r.n), 0) + kAttnChunk - 1) / kAttnChunk, 1);
+    return (uint64_t)tiles * (uint64_t)chunks * (uint32_t)a.heads;
+  };
+  bool bad = false;
+  const uint64_t first = line(lane, bad);
+  uint64_t sum = first;
+  for (int b0 = 64; b0 < a.batch; b0 += 64) sum += line(b0 + lane, bad);
   if (blockIdx.x == 0 && threadIdx.x < 64 && __any(bad) && lane == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
-  sum = wave_sum_u64(sum) * (uint64_t)a.heads;
-  constexpr int kWgStep = kAttnWaves * kAttnStep;
-  const uint64_t want = (sum + kAttnItems - 1) / kAttnItems;
-  const int span = want <= kWgStep ? kWgStep : (int)min((want + kWgStep - 1) / kWgStep * kWgStep, (uint64_t)1 << 30);
-  int items = 0, parts = 0;  // of the sequences before b0
+  sum = uniform(wave_sum_u64(sum));
+  pl.each = (sum + WGS - 1) / WGS;
+  pl.pos = (uint64_t)blockIdx.x * pl.each;
+  if (pl.pos >= sum) return false;
+  pl.stop = min(pl.pos + pl.each, sum);
+  uint64_t before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    AttnRange r{0, 0, 0, false};
-    int tiles = 0, tok = 0;
-    if (b0 + lane < a.batch) {
-      r = b0 == 0 ? first : attn_range(a, b0 + lane);
-      cost(r, tiles, tok);
-    }
-    const int splits = tok > span ? (int)((uint32_t)(tok + span - 1) / (uint32_t)span) : 1;
-    const int mine = tiles * a.heads * splits, pmine = splits > 1 ? mine : 0;
-    int upto = mine, pupto = pmine;
+    const uint64_t mine = b0 == 0 ? first : line(b0 + lane, bad);
+    uint64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int x = __shfl_up(upto, o), y = __shfl_up(pupto, o);
-      if (lane >= o) {
-        upto += x;
-        pupto += y;
-      }
+      const uint32_t lo = (uint32_t)__shfl_up((int)(uint32_t)upto, o), hi = (uint32_t)__shfl_up((int)(upto >> 32), o);
+      if (lane >= o) upto += ((uint64_t)hi << 32) | lo;
     }
-    const uint64_t past = __ballot(items + upto > id);
+    const uint64_t past = __ballot(before + upto > pl.pos);
+    const auto of_lane = [&](uint64_t v, int j) {
+      return ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), j) << 32) |
+             (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, j);
+    };
     if (past) {
       const int j = __builtin_ctzll(past);
-      const int local = id - items - __builtin_amdgcn_readlane(upto - mine, j);
-      it.splits = __builtin_amdgcn_readlane(splits, j);
-      it.split = local % it.splits;
-      const int th = local / it.splits;
-      it.tile = th / a.heads;
-      it.head = th - it.tile * a.heads;
-      it.part = parts + __builtin_amdgcn_readlane(pupto - pmine, j) + th * it.splits;
-      it.b = b0 + j;
-      it.nq = __builtin_amdgcn_readlane(r.nq, j);
-      it.n = __builtin_amdgcn_readlane(r.n, j);
-      it.q0 = ((int64_t)__builtin_amdgcn_readlane((int)(r.q0 >> 32), j) << 32) |
-              (uint32_t)__builtin_amdgcn_readlane((int)r.q0, j);
-      it.span = span;
-      it.lo = a.window ? max(it.n - it.nq + 1 - a.window, 0) & ~(kAttnStep - 1) : 0;
+      pl.b = b0 + j;
+      // place within the sequence; its units and their length from its own extents
+      const uint64_t at = pl.pos - before - of_lane(upto - mine, j);
+      const AttnRange r = attn_range_uniform(a, pl.b);
+      const uint32_t chunks = max((max(r.n - attn_lo(a, r.nq, r.n), 0) + kAttnChunk - 1) / kAttnChunk, 1);
+      const uint32_t unit = (uint32_t)(at / chunks);
+      pl.k = (int)(at - (uint64_t)unit * chunks);
+      pl.tile = (int)(unit / (uint32_t)a.heads);
+      pl.head = (int)(unit - (uint32_t)pl.tile * (uint32_t)a.heads);
       return true;
     }
-    items += __builtin_amdgcn_readlane(upto, 63);
-    parts += __builtin_amdgcn_readlane(pupto, 63);
+    before += of_lane(upto, 63);
   }
   return false;
 }
@@ -230,9 +233,17 @@ __device__ __forceinline__ int small_div(int x, int d) {
   return d >= 16 ? x >= d : (int)(((float)x + 0.5f) * __builtin_amdgcn_rcpf((float)d));
 }
 
-// One workgroup an item; the waves take alternate 32-token steps and their sums are joined
-// through shared memory.  Of a split sequence, the workgroup that arrives last joins the
-// splits' results, in their order.
+template <int D, int R>
+struct AttnShared {
+  float o[kAttnWaves][R][D + 4];
+  float m[kAttnWaves][R], l[kAttnWaves][R];
+  __attribute__((aligned(16))) float x[kAttnWaves][2][64];
+  int last;
+};
+
+// The waves take alternate 32-token steps of a unit and their sums are joined through shared
+// memory.  Of a unit in several workgroups' parts, the one that arrives last joins the results,
+// in their order.
 //
 // A lane's dword of V holds an even and an odd element of four tokens, and the conversion
 // gives them as pairs.  The pairs stay together as neighbours along the product's depth,
@@ -241,21 +252,16 @@ __device__ __forceinline__ int small_div(int x, int d) {
 // instructions that would part the pairs, which have none.  With R = 8 rows the two are the
 // two halves of the 16 columns of one product, with R = 16 two products.
 template <int D, int R>
-__global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) void attn4_kernel(Attn4 a) {
-  constexpr int KW = D / 32, kRow = D + 4, P = R / 8;
-  __shared__ float so[kAttnWaves][R][kRow];
-  __shared__ float sm[kAttnWaves][R], sl[kAttnWaves][R];
-  __shared__ __attribute__((aligned(16))) float sx[kAttnWaves][2][64];
-  __shared__ int last;
+__device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, const AttnRange& rg, int lo, int stop,
+                                           int chunks, AttnShared<D, R>& sh) {
+  constexpr int KW = D / 32, P = R / 8;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n16 = lane & 15, g = lane >> 4;
   const int rn = R == 16 ? n16 : n16 & 7;                 // this lane's query row of the tile
   const int odd_shift = R == 16 ? 16 : (n16 >> 3) << 4;   // where p goes beside its zero
-  AttnItem it;
-  if (!attn_item<R>(a, blockIdx.x, it)) return;
-  const int h = it.head;
-  const int rows = it.nq * a.group;
-  const int r0 = it.tile * R;
+  const int h = pl.head;
+  const int rows = rg.nq * a.group;
+  const int r0 = pl.tile * R;
   const int live = min(rows - r0, R);   // rows of the tile; lanes past them repeat the last
 
   // the query tokens of the tile, this lane's, and the tokens [from, to) that it sees
@@ -264,21 +270,20 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
   const int mine_r = min(rn, live - 1);
   const int dq = small_div(ra + mine_r, a.group);
   const int head = h * a.group + ra + mine_r - dq * a.group;
-  const int to = a.causal ? it.n - it.nq + qa + dq + 1 : it.n;
+  const int to = a.causal ? rg.n - rg.nq + qa + dq + 1 : rg.n;
   const int from = a.window ? to - a.window : 0;
-  const int end = a.causal ? it.n - it.nq + qb + 1 : it.n;         // some row sees [begin, end)
-  const int all_to = a.causal ? it.n - it.nq + qa + 1 : it.n;      // every row sees [all_from, all_to)
+  const int end = a.causal ? rg.n - rg.nq + qb + 1 : rg.n;         // some row sees [begin, end)
+  const int all_to = a.causal ? rg.n - rg.nq + qa + 1 : rg.n;      // every row sees [all_from, all_to)
   const int begin = a.window ? max(all_to - a.window, 0) : 0;
   const int all_from = a.window ? end - a.window : 0;
-  const int lo = it.lo + it.split * it.span;
-  const int hi = it.split + 1 < it.splits ? min(end, lo + it.span) : end;
+  const int hi = min(end, stop);
 
   // the query row as f16 with its largest magnitude in [2^14, 2^15)
   f16x8 q[KW];
   float kc;
   {
     uint4 x[KW];
-    const uint16_t* qp = a.q + (it.q0 + qa + dq) * a.q_stride + (int64_t)head * D + g * (D / 4);
+    const uint16_t* qp = a.q + (rg.q0 + qa + dq) * a.q_stride + (int64_t)head * D + g * (D / 4);
     uint32_t amax = 0;
 #pragma unroll
     for (int s = 0; s < KW; ++s) {
@@ -309,7 +314,7 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
 #pragma unroll
     for (int j = 0; j < KW; ++j) o[y][j] = f32x4{0, 0, 0, 0};
   float m = kNoMax, l = 0.0f;
-  const int32_t* table = a.table + (int64_t)it.b * a.table_stride;
+  const int32_t* table = a.table + (int64_t)pl.b * a.table_stride;
   const int per = 1 << (a.page_shift - 4);
   bool bad_page = false;
 
@@ -353,19 +358,20 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
   }
   for (int t0 = lo + wave * 32; t0 < hi; t0 += kAttnWaves * 32) {
     // what depends on the token alone is worked out by one lane a token and shared: 2^ek, ev + 127
-    // and 2^(-9 - ev) at 0, 16 and 32 of sx
+    // and 2^(-9 - ev) at 0, 16 and 32 of x
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint32_t b23 = f[u].e << 23;
-      const float ve = (float)f[u].e;
+      const uint32_t eb = (f[u].e >> (8 * (lane & 3))) & 0xFFu, b23 = eb << 23;
+      const float ve = (float)eb;
       const float w = g == 0 ? __uint_as_float(b23) : g == 1 ? ve : __uint_as_float((245u << 23) - b23);
-      sx[wave][u][lane] = w;
+      sh.x[wave][u][lane] = w;
     }
     __builtin_amdgcn_wave_barrier();
     f32x4 c[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const f16x2 s01 = scales2<false>(f[u].ks), s23 = scales2<true>(f[u].ks);
+      const uint32_t ks = f[u].ks >> ((8 * (D / 64) * g) & 31);
+      const f16x2 s01 = scales2<false>(ks), s23 = scales2<true>(ks);
       c[u] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < KW; ++s) {
@@ -376,9 +382,9 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
     f32x4 kf[2], ve[2], lf[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      kf[u] = *(const f32x4*)&sx[wave][u][4 * g];
-      ve[u] = *(const f32x4*)&sx[wave][u][16 + 4 * g];
-      lf[u] = *(const f32x4*)&sx[wave][u][32 + 4 * g];
+      kf[u] = *(const f32x4*)&sh.x[wave][u][4 * g];
+      ve[u] = *(const f32x4*)&sh.x[wave][u][16 + 4 * g];
+      lf[u] = *(const f32x4*)&sh.x[wave][u][32 + 4 * g];
       kf[u] *= kc;
       const int t = t0 + 16 * u;
       if (!ok[u] || t < all_from || t + 16 > all_to) {
@@ -394,7 +400,7 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
         }
         // tokens that no row sees may be memory that was never written: no NaN from their scales
         const int t4 = t + 4 * g;
-        const int skip = min(max(begin - t4, 0), 4), keep = ok[u] ? min(max(it.n - t4, 0), 4) : 0;
+        const int skip = min(max(begin - t4, 0), 4), keep = ok[u] ? min(max(rg.n - t4, 0), 4) : 0;
         const uint32_t mask = (uint32_t)(((uint64_t)1 << (8 * keep)) - 1) & ~(uint32_t)(((uint64_t)1 << (8 * skip)) - 1);
 #pragma unroll
         for (int j = 0; j < KW; ++j) fv[u].vs[j] &= mask;
@@ -481,34 +487,40 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
     for (int j = 0; j < KW; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        so[wave][rn][32 * j + 8 * g + 2 * i + (R == 16 ? y : n16 >> 3)] = o[y][j][i];
+        sh.o[wave][rn][32 * j + 8 * g + 2 * i + (R == 16 ? y : n16 >> 3)] = o[y][j][i];
   if (g == 0 && n16 < R) {
-    sm[wave][rn] = m;
-    sl[wave][rn] = l;
+    sh.m[wave][rn] = m;
+    sh.l[wave][rn] = l;
   }
   __syncthreads();
   // E elements of a row a thread
   constexpr int E = R * D / (kAttnWaves * 64) < 4 ? 4 : R * D / (kAttnWaves * 64), kPer = D / E;
+  constexpr int kJoin = 64 / E;  // splits joined at a time
   const int orow = threadIdx.x / kPer, part = threadIdx.x % kPer;
   const bool mine = orow < live;
   const int src = mine ? orow : 0;
-  float top = sm[0][src];
+  float top = sh.m[0][src];
 #pragma unroll
-  for (int w = 1; w < kAttnWaves; ++w) top = __builtin_fmaxf(top, sm[w][src]);
+  for (int w = 1; w < kAttnWaves; ++w) top = __builtin_fmaxf(top, sh.m[w][src]);
   float acc[E], lsum = 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
 #pragma unroll
   for (int w = 0; w < kAttnWaves; ++w) {
-    const float s = __builtin_exp2f(sm[w][src] - top);
-    lsum += s * sl[w][src];
+    const float s = __builtin_exp2f(sh.m[w][src] - top);
+    lsum += s * sh.l[w][src];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += s * so[w][src][part * E + e];
+    for (int e = 0; e < E; ++e) acc[e] += s * sh.o[w][src][part * E + e];
   }
-  if (it.splits > 1) {
+  const uint64_t u0 = pl.pos - (uint64_t)pl.k;   // the unit on the line, and the workgroups it lies in
+  const int w0 = (int)(u0 / pl.each), splits = (int)((u0 + chunks - 1) / pl.each) - w0 + 1;
+  if (splits > 1) {
+    // a workgroup has two places for partial results: for the unit that goes on in the next
+    // workgroup (1) and for the one that came from the one before (0)
     constexpr uint32_t kBytes = attn_part_bytes<D, R>();
     const __amdgpu_buffer_rsrc_t rs = dev_rsrc(a.parts);
-    const uint32_t at = (uint32_t)(it.part + it.split) * kBytes;
+    const int split = (int)blockIdx.x - w0;
+    const uint32_t at = (uint32_t)(2 * blockIdx.x + (split == 0)) * kBytes;
     const uint32_t mine_at = (uint32_t)(src * D + part * E) * 4;
     if (mine) {
 #pragma unroll
@@ -522,57 +534,96 @@ __global__ __launch_bounds__(kAttnWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) vo
     wait_stores();
     __syncthreads();
     if (threadIdx.x == 0) {
-      uint32_t* c = a.counters + it.part;
+      uint32_t* c = a.counters + w0;   // no two units go on from the same workgroup
       const uint32_t old = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      last = old == (uint32_t)it.splits - 1;
-      if (last) st_dev_u32(c, 0u);
+      sh.last = old == (uint32_t)splits - 1;
+      if (sh.last) st_dev_u32(c, 0u);
     }
     __syncthreads();
-    if (!last || !mine) return;
-    const uint32_t first = (uint32_t)it.part * kBytes;
-    const uint32_t* ml = (const uint32_t*)(a.parts + first + R * D * 4) + src;
+    if (!sh.last || !mine) return;
+    const uint32_t first = (uint32_t)(2 * w0 + 1) * kBytes;   // split s at w0 + s: (2 w0 + 1) or 2 (w0 + s)
+    const auto place = [&](int s) { return s == 0 ? first : first + (uint32_t)(2 * s - 1) * kBytes; };
+    const uint32_t ml = R * D * 4 + (uint32_t)src * 4;
+    const auto ld = [&](uint32_t off) { return __uint_as_float(ld_dev_u32((const uint32_t*)(a.parts + off))); };
+    // the running maximum is moved once for kJoin splits, so that their loads
+    // are in flight together (a load from another XCD takes over a microsecond)
     top = kNoMax;
-    for (int s = 0; s < it.splits; ++s) top = __builtin_fmaxf(top, __uint_as_float(ld_dev_u32(ml + s * (kBytes / 4))));
     lsum = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-    for (int s = 0; s < it.splits; ++s) {
-      const float w = __builtin_exp2f(__uint_as_float(ld_dev_u32(ml + s * (kBytes / 4))) - top);
-      lsum += w * __uint_as_float(ld_dev_u32(ml + s * (kBytes / 4) + R));
+#pragma unroll 1
+    for (int s0 = 0; s0 < splits; s0 += kJoin) {
+      float mx[kJoin], lx[kJoin];
+      f32x4 v[kJoin][E / 4];
 #pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        const f32x4 v = ld_dev4v(rs, first + (uint32_t)s * kBytes + mine_at + 4 * e);
+      for (int i = 0; i < kJoin; ++i) {
+        const uint32_t from_s = place(min(s0 + i, splits - 1));
+        mx[i] = ld(from_s + ml);
+        lx[i] = ld(from_s + ml + R * 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[e + i] += w * v[i];
+        for (int e = 0; e < E / 4; ++e) v[i][e] = ld_dev4v(rs, from_s + mine_at + 16 * e);
+      }
+      float mn = top;
+#pragma unroll
+      for (int i = 0; i < kJoin; ++i) mn = __builtin_fmaxf(mn, mx[i]);
+      const float shrink = __builtin_exp2f(top - mn);
+      top = mn;
+      lsum *= shrink;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= shrink;
+#pragma unroll
+      for (int i = 0; i < kJoin; ++i) {
+        const float w = s0 + i < splits ? __builtin_exp2f(mx[i] - top) : 0.0f;
+        lsum = __builtin_fmaf(w, lx[i], lsum);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(w, v[i][e / 4][e & 3], acc[e]);
       }
     }
   }
   if (!mine) return;
   const int oq = qa + small_div(ra + src, a.group), oh = h * a.group + (r0 + src) - oq * a.group;
   const float inv = lsum == 0.0f ? 0.0f : 0.001953125f / lsum;  // a row that sees nothing: zeros
-  uint16_t* op = a.out + (it.q0 + oq) * a.out_stride + (int64_t)oh * D + part * E;
+  uint16_t* op = a.out + (rg.q0 + oq) * a.out_stride + (int64_t)oh * D + part * E;
 #pragma unroll
   for (int e = 0; e < E; e += 4)
     *(uint2*)(op + e) = make_uint2(pack_bf16x2_rne(acc[e] * inv, acc[e + 1] * inv),
                                    pack_bf16x2_rne(acc[e + 2] * inv, acc[e + 3] * inv));
   if (a.lse && part == 0)
-    a.lse[(it.q0 + oq) * a.q_heads + oh] =
+    a.lse[(rg.q0 + oq) * a.q_heads + oh] =
         lsum == 0.0f ? -__builtin_inff() : (__builtin_log2f(lsum) + top) * 0.6931471805599453f;
 }
 
-// Items of split sequences: each has fewer than 2 tokens / span of them, so at most 2 kAttnItems.
-static_assert(2 * kAttnItems * 4 + kWsCounterOff <= kWsReserved, "one counter a split item");
+template <int D, int R>
+__global__ __launch_bounds__(kAttnWaves * 64, attn_wgs_per_cu(D)) void attn4_kernel(Attn4 a) {
+  __shared__ AttnShared<D, R> sh;
+  AttnPlace pl;
+  if (!attn_place<R, attn_wgs(D)>(a, pl)) return;
+  AttnRange rg = attn_range_uniform(a, pl.b);
+  for (;;) {
+    const int lo_b = attn_lo(a, rg.nq, rg.n);
+    const int chunks = max((max(rg.n - lo_b, 0) + kAttnChunk - 1) / kAttnChunk, 1);
+    const int k1 = (int)min((uint64_t)chunks, pl.k + (pl.stop - pl.pos));
+    attn4_unit<D, R>(a, pl, rg, lo_b + pl.k * kAttnChunk, k1 == chunks ? rg.n : lo_b + k1 * kAttnChunk, chunks, sh);
+    pl.pos += k1 - pl.k;
+    if (pl.pos >= pl.stop) break;
+    pl.k = 0;
+    if (++pl.head == a.heads) {
+      pl.head = 0;
+      if (++pl.tile * R >= rg.nq * a.group) {
+        pl.tile = 0;
+        do rg = attn_range_uniform(a, ++pl.b); while (rg.nq == 0);   // pos < stop: another unit is there
+      }
+    }
+    __syncthreads();   // the shared memory of the unit before is read
+  }
+}
+static_assert(attn_wgs(64) * 4 + kWsCounterOff <= kWsReserved, "one counter a workgroup");
 
-size_t attn4_scratch_bytes(int32_t head_dim) { return (size_t)2 * kAttnItems * 16 * (head_dim + 2) * 4; }
+size_t attn4_scratch_bytes(int32_t head_dim) { return (size_t)2 * attn_wgs(head_dim) * 16 * (head_dim + 2) * 4; }
 
 template <int D, int R>
 static hipError_t launch_r(const Attn4& a, hipStream_t s) {
-  // every R rows of every KV head, at most one tile a sequence more, and the splits
-  const int64_t tiles = a.total_q * a.group / R + a.batch;
-  const int64_t items = tiles * a.heads + kAttnItems;
-  if (items > (int64_t)INT32_MAX) return hipErrorInvalidValue;
-  attn4_kernel<D, R><<<(unsigned)items, kAttnWaves * 64, 0, s>>>(a);
+  attn4_kernel<D, R><<<attn_wgs(D), kAttnWaves * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 
