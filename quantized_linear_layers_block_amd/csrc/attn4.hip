@@ -87,37 +87,56 @@ struct Values4 {
   uint32_t vs[D / 32];  // their scales in block 2 j + (lane % 16) / 8
 };
 
+// N dwords of a group at a lane's offset.  The group is a buffer of its own (its address in
+// scalar registers, its size the bound), so that a load takes one vector register of address.
+template <int D>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t group_rsrc(const uint8_t* grp) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(grp), (short)0, kv4_group_bytes(D), 0x00020000);
+}
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t* dst, const uint8_t* p) {
+__device__ __forceinline__ void load_words(uint32_t* dst, __amdgpu_buffer_rsrc_t grp, uint32_t off) {
   if constexpr (N >= 4) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const uint4 x = *(const uint4*)(p + 16 * i);
-      dst[4 * i] = x.x;
-      dst[4 * i + 1] = x.y;
-      dst[4 * i + 2] = x.z;
-      dst[4 * i + 3] = x.w;
+      const i32x4 x = __builtin_amdgcn_raw_buffer_load_b128(grp, (int)(off + 16 * i), 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dst[4 * i + j] = (uint32_t)x[j];
     }
+  } else if constexpr (N == 2) {
+    const auto x = __builtin_amdgcn_raw_buffer_load_b64(grp, (int)off, 0, 0);
+    dst[0] = (uint32_t)x[0];
+    dst[1] = (uint32_t)x[1];
   } else {
-    const uint2 x = *(const uint2*)p;
-    dst[0] = x.x;
-    dst[1] = x.y;
+    dst[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(grp, (int)off, 0, 0);
   }
 }
 
+// Offsets of a lane's loads within a group (the group's own address is the wave's).
 template <int D>
-__device__ __forceinline__ void load_keys(Keys4<D>& f, const uint8_t* grp, int lane) {
-  const int m = lane & 15, g = lane >> 4;
-  load_words<D / 32>(f.k, grp + m * (D / 2) + g * (D / 8));
-  // whole dwords: the compiler's widening copies of shorter loads would wait for them at once
-  f.ks = *(const uint32_t*)(grp + kv4_k_scales(D) + ((m * (D / 16) + g * (D / 64)) & ~3));
-  f.e = *(const uint32_t*)(grp + (g ? kv4_v_exps(D) : kv4_k_exps(D)) + (m & ~3));
+struct Lane4 {
+  uint32_t k, ks, e, v, vs;
+  __device__ __forceinline__ explicit Lane4(int lane) {
+    const uint32_t m = lane & 15, g = lane >> 4;
+    k = m * (D / 2) + g * (D / 8);
+    // whole dwords: the compiler's widening copies of shorter loads would wait for them at once
+    ks = kv4_k_scales(D) + ((m * (D / 16) + g * (D / 64)) & ~3u);
+    e = (g ? kv4_v_exps(D) : kv4_k_exps(D)) + (m & ~3u);
+    v = kv4_v_codes(D) + lane * (D / 8);
+    vs = kv4_v_scales(D) + g * (D / 4) + (m >> 3) * (D / 8);
+  }
+};
+template <int D>
+__device__ __forceinline__ void load_keys(Keys4<D>& f, const uint8_t* grp, const Lane4<D>& at) {
+  const __amdgpu_buffer_rsrc_t rs = group_rsrc<D>(grp);
+  load_words<D / 32>(f.k, rs, at.k);
+  load_words<1>(&f.ks, rs, at.ks);
+  load_words<1>(&f.e, rs, at.e);
 }
 template <int D>
-__device__ __forceinline__ void load_values(Values4<D>& f, const uint8_t* grp, int lane) {
-  const int m = lane & 15, g = lane >> 4;
-  load_words<D / 32>(f.v, grp + kv4_v_codes(D) + lane * (D / 8));
-  load_words<D / 32>(f.vs, grp + kv4_v_scales(D) + g * (D / 4) + (m >> 3) * (D / 8));
+__device__ __forceinline__ void load_values(Values4<D>& f, const uint8_t* grp, const Lane4<D>& at) {
+  const __amdgpu_buffer_rsrc_t rs = group_rsrc<D>(grp);
+  load_words<D / 32>(f.v, rs, at.v);
+  load_words<D / 32>(f.vs, rs, at.vs);
 }
 
 // Two E4M3 scales (bytes 0 and 1 of w, or 2 and 3) as f16, exactly; 0x7F and 0xFF are NaN.
@@ -212,9 +231,9 @@ __device__ __forceinline__ bool attn_place(const Attn4& a, AttnPlace& pl) {
       const AttnRange r = attn_range_uniform(a, pl.b);
       const uint32_t chunks = max((max(r.n - attn_lo(a, r.nq, r.n), 0) + kAttnChunk - 1) / kAttnChunk, 1);
       const uint32_t unit = (uint32_t)(at / chunks);
-      pl.k = (int)(at - (uint64_t)unit * chunks);
-      pl.tile = (int)(unit / (uint32_t)a.heads);
-      pl.head = (int)(unit - (uint32_t)pl.tile * (uint32_t)a.heads);
+      pl.k = __builtin_amdgcn_readfirstlane((int)(at - (uint64_t)unit * chunks));
+      pl.tile = __builtin_amdgcn_readfirstlane((int)(unit / (uint32_t)a.heads));
+      pl.head = __builtin_amdgcn_readfirstlane((int)(unit - (uint32_t)pl.tile * (uint32_t)a.heads));
       return true;
     }
     before += of_lane(upto, 63);
@@ -337,9 +356,11 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
   const auto group_at = [&](int x, int t) {
     const int pg = max(__builtin_amdgcn_readlane(pages, x & 63), 0);
     const int64_t gi = (((int64_t)pg * a.heads + h) << (a.page_shift - 4)) + ((t >> 4) & (per - 1));
-    return a.data + gi * kv4_group_bytes(D);
+    return a.data + uniform((uint64_t)gi * kv4_group_bytes(D));
   };
 
+  const Lane4<D> lane_at(lane);
+  const uint32_t sel_k = g == 0 ? ~0u : 0u, sel_v = g == 1 ? ~0u : 0u;
   Keys4<D> f[2];
   Values4<D> fv[2];
   const uint8_t* grp[2];
@@ -351,10 +372,10 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
     for (int u = 0; u < 2; ++u) {
       ok[u] = __builtin_amdgcn_readlane(pages, u) >= 0;
       grp[u] = group_at(u, lo + wave * 32 + 16 * u);
-      load_keys<D>(f[u], grp[u], lane);
+      load_keys<D>(f[u], grp[u], lane_at);
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) load_values<D>(fv[u], grp[u], lane);
+    for (int u = 0; u < 2; ++u) load_values<D>(fv[u], grp[u], lane_at);
   }
   for (int t0 = lo + wave * 32; t0 < hi; t0 += kAttnWaves * 32) {
     // what depends on the token alone is worked out by one lane a token and shared: 2^ek, ev + 127
@@ -362,9 +383,9 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const uint32_t eb = (f[u].e >> (8 * (lane & 3))) & 0xFFu, b23 = eb << 23;
-      const float ve = (float)eb;
-      const float w = g == 0 ? __uint_as_float(b23) : g == 1 ? ve : __uint_as_float((245u << 23) - b23);
-      sh.x[wave][u][lane] = w;
+      // (selected by masks: written as a choice, the compiler branches)
+      const uint32_t ve = __float_as_uint((float)eb), lf = (245u - min(eb, 244u)) << 23;
+      sh.x[wave][u][lane] = __uint_as_float((b23 & sel_k) | (ve & sel_v) | (lf & ~(sel_k | sel_v)));
     }
     __builtin_amdgcn_wave_barrier();
     f32x4 c[2];
@@ -379,33 +400,24 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
         c[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(scaled8(f[u].k[s], sp, sp, sp, sp), q[s], c[u], 0, 0, 0);
       }
     }
-    f32x4 kf[2], ve[2], lf[2];
+    // which of its 8 tokens this lane's row sees
+    uint32_t seen = 0xFFu;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      kf[u] = *(const f32x4*)&sh.x[wave][u][4 * g];
-      ve[u] = *(const f32x4*)&sh.x[wave][u][16 + 4 * g];
-      lf[u] = *(const f32x4*)&sh.x[wave][u][32 + 4 * g];
-      kf[u] *= kc;
       const int t = t0 + 16 * u;
       if (!ok[u] || t < all_from || t + 16 > all_to) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tok = t + 4 * g + i;
-          if (!(ok[u] && tok >= from && tok < to)) {
-            c[u][i] = 0.0f;
-            kf[u][i] = 0.0f;
-            ve[u][i] = -__builtin_inff();
-            lf[u][i] = 0.0f;
-          }
-        }
-        // tokens that no row sees may be memory that was never written: no NaN from their scales
         const int t4 = t + 4 * g;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!(ok[u] && t4 + i >= from && t4 + i < to)) seen &= ~(1u << (4 * u + i));
+        // tokens that no row sees may be memory that was never written: no NaN from their scales
         const int skip = min(max(begin - t4, 0), 4), keep = ok[u] ? min(max(rg.n - t4, 0), 4) : 0;
         const uint32_t mask = (uint32_t)(((uint64_t)1 << (8 * keep)) - 1) & ~(uint32_t)(((uint64_t)1 << (8 * skip)) - 1);
 #pragma unroll
         for (int j = 0; j < KW; ++j) fv[u].vs[j] &= mask;
       }
     }
+    const bool edge = !ok[0] || !ok[1] || t0 < all_from || t0 + 32 > all_to;
     // The next step's keys are on their way from here, its values from when this step's are
     // used.  After the last step the same groups are fetched again: with a branch around the
     // loads the compiler would wait for all that are in flight.
@@ -418,27 +430,36 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
       for (int u = 0; u < 2; ++u) {
         ok[u] = __builtin_amdgcn_readlane(pages, (x + u) & 63) >= 0;
         grp[u] = group_at(x + u, tn + 16 * u);
-        load_keys<D>(f[u], grp[u], lane);
+        load_keys<D>(f[u], grp[u], lane_at);
       }
     }
-    float p[2][4], top = -__builtin_inff();
-    const float base = 9.0f - 127.0f - m;   // ve holds ev + 127
+    // w - add of the step's tokens, -inf where the row does not see them
+    float p[2][4];
+    const auto weigh = [&](float add) {
+      float top = -__builtin_inff();
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u) {
+        const f32x4 kf = *(const f32x4*)&sh.x[wave][u][4 * g] * kc;
+        const f32x4 ve = *(const f32x4*)&sh.x[wave][u][16 + 4 * g];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[u][i] = __builtin_fmaf(c[u][i], kf[u][i], ve[u][i] + base);
-        top = __builtin_fmaxf(top, p[u][i]);
+        for (int i = 0; i < 4; ++i) p[u][i] = __builtin_fmaf(c[u][i], kf[i], ve[i] + add);
       }
-    if (__any(top > 15.0f)) {  // the maximum moves: w again in full, the sums to the new one
-      float w = -__builtin_inff();
+      if (edge) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(seen >> (4 * u + i) & 1)) p[u][i] = -__builtin_inff();
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[u][i] = __builtin_fmaf(c[u][i], kf[u][i], ve[u][i] - 127.0f);
-          w = __builtin_fmaxf(w, p[u][i]);
-        }
+        for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, p[u][i]);
+      return top;
+    };
+    if (__any(weigh(9.0f - 127.0f - m) > 15.0f)) {   // x holds ev + 127
+      // the maximum moves: w again in full, the sums to the new one
+      float w = weigh(-127.0f);
       w = __builtin_fmaxf(w, __shfl_xor(w, 16));
       w = __builtin_fmaxf(w, __shfl_xor(w, 32));
       const float mn = __builtin_fmaxf(m, w), shrink = __builtin_exp2f(m - mn);
@@ -457,10 +478,11 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
     for (int u = 0; u < 2; ++u) {
       typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
       u32x4 pe, po;
+      const f32x4 lf = *(const f32x4*)&sh.x[wave][u][32 + 4 * g];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float e = __builtin_amdgcn_exp2f(p[u][i]);
-        l = __builtin_fmaf(e, lf[u][i], l);
+        l = __builtin_fmaf(e, lf[i], l);
         const uint32_t hbits = __builtin_bit_cast(uint16_t, (_Float16)e);
         pe[i] = hbits;
         po[i] = hbits << odd_shift;
@@ -475,7 +497,7 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
       }
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) load_values<D>(fv[u], grp[u], lane);
+    for (int u = 0; u < 2; ++u) load_values<D>(fv[u], grp[u], lane_at);
   }
   if (__any(bad_page) && lane == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
 
@@ -495,7 +517,7 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
   __syncthreads();
   // E elements of a row a thread
   constexpr int E = R * D / (kAttnWaves * 64) < 4 ? 4 : R * D / (kAttnWaves * 64), kPer = D / E;
-  constexpr int kJoin = 64 / E;  // splits joined at a time
+  constexpr int kJoin = 32 / E < 4 ? 4 : 32 / E;  // splits joined at a time
   const int orow = threadIdx.x / kPer, part = threadIdx.x % kPer;
   const bool mine = orow < live;
   const int src = mine ? orow : 0;
