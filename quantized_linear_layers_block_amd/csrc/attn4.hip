@@ -78,8 +78,8 @@ template <int D>
 struct Keys4 {
   uint32_t k[D / 32];   // token lane % 16, elements (lane / 16) D / 4 on
   uint32_t ks;          // their D / 64 scales, at bit 8 (lane / 16) D / 64 % 32
-  uint32_t e;           // at byte lane % 4 the exponent byte of token lane % 16: the key row's in
-                        // lanes 0..15, the value row's in the others
+  uint32_t e;           // at byte lane % 4 the exponent byte of token lane % 16: the key row's, or (few-row
+                        // kernel) in lanes past 15 the value row's
 };
 template <int D>
 struct Values4 {
@@ -195,7 +195,7 @@ __device__ __forceinline__ bool attn_place(const Attn4& a, AttnPlace& pl) {
     if (b >= a.batch) return 0;
     const AttnRange r = attn_range(a, b);
     bad |= r.bad;
-    const uint32_t tiles = (uint32_t)(r.nq * a.group + R - 1) / R;
+    const uint32_t tiles = r.nq * a.group > a.few ? 0u : (uint32_t)(r.nq * a.group + R - 1) / R;
     const uint32_t chunks = max((max(r.n - attn_lo(a, r.nq, r.n), 0) + kAttnChunk - 1) / kAttnChunk, 1);
     return (uint64_t)tiles * (uint64_t)chunks * (uint32_t)a.heads;
   };
@@ -633,12 +633,362 @@ __global__ __launch_bounds__(kAttnWaves * 64, attn_wgs_per_cu(D)) void attn4_ker
       pl.head = 0;
       if (++pl.tile * R >= rg.nq * a.group) {
         pl.tile = 0;
-        do rg = attn_range_uniform(a, ++pl.b); while (rg.nq == 0);   // pos < stop: another unit is there
+        do rg = attn_range_uniform(a, ++pl.b); while (rg.nq == 0 || rg.nq * a.group > a.few);   // pos < stop: another unit is there
       }
     }
     __syncthreads();   // the shared memory of the unit before is read
   }
 }
+// ------------------------------------------------------------------ many query rows
+//
+// Prompts and prompt pieces: waves of 32 query rows share the keys and values of 64 tokens at
+// a time, which they bring to f16 in shared memory in the order in which the 32x32x16 MFMA takes
+// them (one 16-byte slot a lane), two tiles in turn, so that one barrier a tile is enough.  The
+// codes of the tile after are on their way in registers meanwhile.
+//
+// The rows' exponents go into the f16 values here, relative to the largest of each 16 tokens,
+// E for keys and F for values: khat 2^(ek - E + 4), vhat 2^(ev - F + 4), at most 43008.  They are exact
+// for rows down to 2^-18 of the largest and off by 2^-40 of it below.  A logit then takes one
+// fused multiply-add with factors of its group, w = (acc kc 2^(E - 4)) + F, where a factor a
+// token would cost two more of some nine vector instructions a logit, and the vector
+// instructions (the exponential takes four of them) weigh as much as the matrix products.
+constexpr int kPrTok = 64, kPrGroups = kPrTok / 16;
+// Waves of a workgroup: two a SIMD, or one where the sums of 32 rows take 128 registers.
+constexpr int prompt_waves(int d) { return d == 256 ? 4 : 8; }
+
+template <int D>
+struct PromptShared {
+  uint4 k[2][kPrTok / 32][D / 16][64];   // [tile][32 tokens][16 elements][lane]
+  uint4 v[2][kPrGroups][D / 32][64];     // [tile][16 tokens][32 elements][lane]
+  float ke[2][kPrGroups];                // 2^(E - 4), 0 for a group that is left out
+  float2 vf[2][kPrGroups];               // F and 2^(-9 - F)
+};
+
+// Maximum over lanes l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ uint32_t max_rows4(uint32_t v) {
+  v = umax(v, (uint32_t)__shfl_xor((int)v, 16));
+  return umax(v, (uint32_t)__shfl_xor((int)v, 32));
+}
+// 2^e as f16 for e <= 15 (0 below the format).
+__device__ __forceinline__ _Float16 pow2_f16(int e) {
+  return (_Float16)__uint_as_float((uint32_t)max(e + 127, 0) << 23);
+}
+
+// Keys of a group to f16 slots; the group's factor.  A token outside [0, valid) counts for nothing.
+template <int D>
+__device__ __forceinline__ void prompt_keys(PromptShared<D>& sh, int buf, int grp, const Keys4<D>& f, int lane,
+                                            uint32_t valid) {
+  constexpr int KW = D / 32;
+  const int n16 = lane & 15, g = lane >> 4;
+  const uint32_t e = (f.e >> (8 * (n16 & 3))) & 0xFFu;
+  const uint32_t top = max_row16((valid >> n16 & 1) ? min(e, 244u) : 0u);
+  const f16x2 by = both(pow2_f16((int)e - (int)top + 4));
+  const uint32_t ks = f.ks >> ((8 * (D / 64) * g) & 31);
+  const f16x2 s01 = scales2<false>(ks) * by, s23 = scales2<true>(ks) * by;
+#pragma unroll
+  for (int i = 0; i < KW; ++i) {
+    const f16x2 sp = both((i >> 1) < 2 ? s01[(i >> 1) & 1] : s23[(i >> 1) & 1]);
+    const int w = g * KW + i;   // elements 8 w ..
+    sh.k[buf][grp >> 1][w >> 1][(w & 1) * 32 + (grp & 1) * 16 + n16] =
+        __builtin_bit_cast(uint4, scaled8(f.k[i], sp, sp, sp, sp));
+  }
+  if (lane == 0) sh.ke[buf][grp] = valid ? __uint_as_float((uint32_t)max((int)top - 4, 0) << 23) : 0.0f;
+}
+
+template <int D>
+__device__ __forceinline__ void prompt_values(PromptShared<D>& sh, int buf, int grp, const Values4<D>& f, uint32_t e4,
+                                              int lane, uint32_t valid) {
+  constexpr int KW = D / 32;
+  const int m = lane & 15, g = lane >> 4;
+  const uint32_t mine = valid >> (4 * g) & 15u;
+  uint32_t mask = (mine & 1 ? 0xFFu : 0) | (mine & 2 ? 0xFF00u : 0) | (mine & 4 ? 0xFF0000u : 0) |
+                  (mine & 8 ? 0xFF000000u : 0);
+  const uint32_t e = e4 & mask;
+  uint32_t ev[4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    ev[i] = min((e >> (8 * i)) & 0xFFu, 244u);
+    top = umax(top, ev[i]);
+  }
+  top = max_rows4(top);
+  f16x2 by01{pow2_f16((int)ev[0] - (int)top + 4), pow2_f16((int)ev[1] - (int)top + 4)};
+  f16x2 by23{pow2_f16((int)ev[2] - (int)top + 4), pow2_f16((int)ev[3] - (int)top + 4)};
+#pragma unroll
+  for (int j = 0; j < KW; ++j) {
+    const uint32_t sc = f.vs[j] & mask;   // unwritten memory: no NaN from its scales
+    const f16x2 s01 = scales2<false>(sc) * by01, s23 = scales2<true>(sc) * by23;
+    // nibbles of the even (low) and odd (high) elements of tokens (0, 1) to byte 0, (2, 3) to byte 2
+    const uint32_t low = 0x000F000Fu, w = f.v[j], w4 = w >> 4, w8 = w >> 8;
+    const uint32_t even = (w & low) | (w4 & ~low), odd = (w4 & low) | (w8 & ~low);
+    const f16x2 e0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(even, 1.0f, 0) * s01;
+    const f16x2 e1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(even, 1.0f, 2) * s23;
+    const f16x2 o0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(odd, 1.0f, 0) * s01;
+    const f16x2 o1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(odd, 1.0f, 2) * s23;
+    uint2* at = (uint2*)&sh.v[buf][grp][j][(g & 1) * 32 + m] + (g >> 1);
+    at[0] = make_uint2(__builtin_bit_cast(uint32_t, e0), __builtin_bit_cast(uint32_t, e1));
+    at[32] = make_uint2(__builtin_bit_cast(uint32_t, o0), __builtin_bit_cast(uint32_t, o1));
+  }
+  if (lane == 0) sh.vf[buf][grp] = make_float2((float)(int)top - 127.0f, __uint_as_float((245u - top) << 23));
+}
+
+template <int D>
+__global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) / 4) void attn4_prompt_kernel(Attn4 a) {
+  constexpr int KS = D / 16, DT = D / 32, W = prompt_waves(D), kPrRows = 32 * W;
+  extern __shared__ __attribute__((aligned(16))) uint8_t raw[];
+  PromptShared<D>& sh = *(PromptShared<D>*)raw;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n32 = lane & 31, half = lane >> 5;
+
+  // the unit: (sequence, row tile, head), a sequence's last tiles first (they see the most)
+  int b = -1, tile = 0, h = 0;
+  {
+    int before = 0;
+    bool bad = false;
+    for (int b0 = 0; b0 < a.batch && b < 0; b0 += 64) {
+      AttnRange r{0, 0, 0, false};
+      if (b0 + lane < a.batch) r = attn_range(a, b0 + lane);
+      bad |= r.bad;
+      const int rows = r.nq * a.group;
+      const int tiles = rows > a.few ? (rows + kPrRows - 1) / kPrRows : 0;
+      int upto = tiles * a.heads;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int x = __shfl_up(upto, o);
+        if (lane >= o) upto += x;
+      }
+      const uint64_t past = __ballot(before + upto > (int)blockIdx.x);
+      if (past) {
+        const int j = __builtin_ctzll(past);
+        const int nt = __builtin_amdgcn_readlane(tiles, j);
+        const int at = (int)blockIdx.x - before - (__builtin_amdgcn_readlane(upto, j) - nt * a.heads);
+        b = b0 + j;
+        tile = nt - 1 - at / a.heads;
+        h = at % a.heads;
+      }
+      before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    if (blockIdx.x == 0 && a.few == 0 && __any(bad) && threadIdx.x == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
+  }
+  if (b < 0) return;
+  tile = __builtin_amdgcn_readfirstlane(tile);
+  h = __builtin_amdgcn_readfirstlane(h);
+  const AttnRange rg = attn_range_uniform(a, b);
+  const int rows = rg.nq * a.group;
+  const int r0 = tile * kPrRows;
+  const int tile_live = min(rows - r0, kPrRows);
+  const int qa = r0 / a.group, ra = r0 - qa * a.group;
+  const int qz = (r0 + tile_live - 1) / a.group;
+  // tokens that some row of the workgroup sees
+  const int stop = a.causal ? rg.n - rg.nq + qz + 1 : rg.n;
+  const int begin = a.window ? max(rg.n - rg.nq + qa + 1 - a.window, 0) : 0;
+  const int first = begin & ~(kPrTok - 1);
+  const int tiles = stop > first ? (stop - first + kPrTok - 1) / kPrTok : 0;
+
+  // this wave's rows and this lane's
+  const int wr = wave * 32;
+  const bool busy = wr < tile_live;
+  const int row = min(ra + wr + n32, ra + tile_live - 1);
+  const int dq = (int)((uint32_t)row / (uint32_t)a.group);
+  const int head = h * a.group + row - dq * a.group;
+  const int qrow = qa + dq;
+  const int to = a.causal ? rg.n - rg.nq + qrow + 1 : rg.n;
+  const int from = a.window ? to - a.window : 0;
+  const int wq0 = qa + (ra + min(wr, tile_live - 1)) / a.group, wq1 = qa + (ra + min(wr + 31, tile_live - 1)) / a.group;
+  const int end_w = a.causal ? rg.n - rg.nq + wq1 + 1 : rg.n;      // some row of the wave sees [begin_w, end_w)
+  const int all_to = a.causal ? rg.n - rg.nq + wq0 + 1 : rg.n;     // every row sees [all_from, all_to)
+  const int begin_w = a.window ? max(all_to - a.window, 0) : 0;
+  const int all_from = a.window ? end_w - a.window : 0;
+
+  // the tiles' codes: of 8 waves 2 x and 2 x + 1 take the keys and the values of group x, of 4 each both
+  const int grp = W == 8 ? wave >> 1 : wave;
+  const bool takes_keys = W == 4 || (wave & 1) == 0, takes_values = W == 4 || (wave & 1) != 0;
+  const int32_t* table = a.table + (int64_t)b * a.table_stride;
+  int pages = 0;   // lane x % 64: the page of this wave's group in tile x, -1 if there is none to read
+  bool bad_page = false;
+  const auto look_up = [&](int x0) {
+    const int t = first + (x0 + lane) * kPrTok + grp * 16;
+    pages = -1;
+    if (t < stop && t + 16 > begin) {
+      pages = table[t >> a.page_shift];
+      if (pages < 0 || pages >= a.pages) {
+        pages = -1;
+        bad_page = true;
+      }
+    }
+  };
+  Lane4<D> lane_at(lane);
+  lane_at.e = kv4_k_exps(D) + (lane & 12);   // the key rows' exponents in every lane
+  Keys4<D> fk;
+  Values4<D> fv;
+  uint32_t fe = 0, valid = 0;
+  const auto fetch = [&](int x) {
+    const int t = first + x * kPrTok + grp * 16;
+    const int pg = __builtin_amdgcn_readlane(pages, x & 63);
+    const int64_t gi = (((int64_t)max(pg, 0) * a.heads + h) << (a.page_shift - 4)) +
+                       ((t >> 4) & ((1 << (a.page_shift - 4)) - 1));
+    const uint8_t* at = a.data + uniform((uint64_t)gi * kv4_group_bytes(D));
+    // tokens of the group that may be read
+    const int hi = pg < 0 ? 0 : min(max(stop - t, 0), 16), lo = min(max(begin - t, 0), 16);
+    valid = ((1u << hi) - 1) & ~((1u << lo) - 1);
+    if (takes_keys) load_keys<D>(fk, at, lane_at);
+    if (takes_values) {
+      load_values<D>(fv, at, lane_at);
+      load_words<1>(&fe, group_rsrc<D>(at), kv4_v_exps(D) + 4 * (lane >> 4));
+    }
+  };
+  const auto put = [&](int buf) {
+    if (takes_keys) prompt_keys<D>(sh, buf, grp, fk, lane, valid);
+    if (takes_values) prompt_values<D>(sh, buf, grp, fv, fe, lane, valid);
+  };
+
+  // the query rows as f16 with their largest magnitude in [2^14, 2^15) and the scale's sign, so that
+  // kc > 0 and a logit of -inf stays -inf; a row with Inf or NaN is NaN throughout
+  f16x8 q[KS];
+  float kc;
+  {
+    const uint16_t* qp = a.q + (rg.q0 + qrow) * a.q_stride + (int64_t)head * D + half * 8;
+    uint32_t amax = 0;
+    uint4 x[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      x[s] = *(const uint4*)(qp + 16 * s);
+      amax = umax(amax, hmax_u16x2(max_u16x2(max_u16x2(abs_bits2(x[s].x), abs_bits2(x[s].y)),
+                                             max_u16x2(abs_bits2(x[s].z), abs_bits2(x[s].w)))));
+    }
+    amax = umax(amax, (uint32_t)__shfl_xor((int)amax, 32));
+    const int e = amax ? (int)(amax >> 7) - 127 - 14 : 0;
+    kc = a.scale_log2e == 0.0f ? 1.0f : __builtin_ldexpf(__builtin_fabsf(a.scale_log2e), e);
+    const float sign = amax >= kBf16InfBits ? __builtin_nanf("") : a.scale_log2e > 0.0f ? 1.0f : a.scale_log2e < 0.0f ? -1.0f : 0.0f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const uint32_t w[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        q[s][2 * i] = (_Float16)(__builtin_ldexpf(bf16_lo(w[i]), -e) * sign);
+        q[s][2 * i + 1] = (_Float16)(__builtin_ldexpf(bf16_hi(w[i]), -e) * sign);
+      }
+    }
+  }
+
+  f32x16 o[DT];
+#pragma unroll
+  for (int j = 0; j < DT; ++j)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
+  float m = 0.0f, l = 0.0f;
+  float limit = kNoMax;   // m moves when w - m + 9 passes it: 15 once the row has seen a token
+
+  if (tiles > 0) {
+    look_up(0);
+    fetch(0);
+    put(0);
+    if (tiles > 1) fetch(1);
+  }
+  __syncthreads();
+  for (int x = 0; x < tiles; ++x) {
+    const int buf = x & 1, t0 = first + x * kPrTok;
+    if (x + 1 < tiles) {
+      put(buf ^ 1);
+      if (x + 2 < tiles) {
+        if (((x + 2) & 63) == 0) look_up(x + 2);
+        fetch(x + 2);
+      }
+    }
+    if (busy && t0 < end_w && t0 + kPrTok > begin_w) {
+      f32x16 c[2];
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) c[tt][i] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          c[tt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, sh.k[buf][tt][s][lane]), q[s], c[tt],
+                                                         0, 0, 0);
+      }
+      float kf[kPrGroups], vf[kPrGroups], lf[kPrGroups];
+      bool whole = true;
+#pragma unroll
+      for (int gr = 0; gr < kPrGroups; ++gr) {
+        const float ke = sh.ke[buf][gr];
+        whole &= ke != 0.0f;
+        kf[gr] = __builtin_fmaxf(ke * kc, 1e-37f);   // (below it a logit is 0)
+        const float2 vv = sh.vf[buf][gr];
+        vf[gr] = vv.x + (9.0f - m);
+        lf[gr] = vv.y;
+      }
+      if (!whole || t0 < all_from || t0 + kPrTok > all_to) {   // a logit that the row does not see becomes -inf
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int t = t0 + 32 * tt + 8 * (i >> 2) + 4 * half + (i & 3);
+            if (!(t >= from && t < to && sh.ke[buf][2 * tt + (i >> 3)] != 0.0f)) c[tt][i] = -__builtin_inff();
+          }
+      }
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int gr = 2 * tt + (i >> 3);
+          c[tt][i] = __builtin_fmaf(c[tt][i], kf[gr], vf[gr]);
+          top = __builtin_fmaxf(top, c[tt][i]);
+        }
+      if (__any(top > limit)) {   // the maximum moves
+        top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+        const bool fresh = limit != 15.0f, any = top > kNoMax;
+        const float up = any ? fresh ? top - 9.0f : __builtin_fmaxf(top - 9.0f, 0.0f) : 0.0f;
+        const float shrink = fresh ? 0.0f : __builtin_exp2f(-up);
+        m += up;
+        limit = any ? 15.0f : limit;
+        l *= shrink;
+#pragma unroll
+        for (int j = 0; j < DT; ++j) o[j] *= shrink;
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) c[tt][i] -= up;
+      }
+#pragma unroll
+      for (int gr = 0; gr < kPrGroups; ++gr) {
+        f16x8 p;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float e = __builtin_amdgcn_exp2f(c[gr >> 1][8 * (gr & 1) + i]);
+          sum += e;
+          p[i] = (_Float16)e;
+        }
+        l = __builtin_fmaf(sum, lf[gr], l);
+#pragma unroll
+        for (int j = 0; j < DT; ++j)
+          o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, sh.v[buf][gr][j][lane]), p, o[j], 0,
+                                                        0, 0);
+      }
+    }
+    __syncthreads();
+  }
+  if (__any(bad_page) && lane == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
+
+  l += __shfl_xor(l, 32);
+  if (wr + n32 >= tile_live) return;
+  const float inv = l == 0.0f ? 0.0f : 1.220703125e-4f / l;   // 2^-13; a row that sees nothing: zeros
+  uint16_t* op = a.out + (rg.q0 + qrow) * a.out_stride + (int64_t)head * D + 8 * half;
+#pragma unroll
+  for (int j = 0; j < DT; ++j)
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {  // elements 32 j + 16 y + 8 half ..
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2_rne(o[j][4 * y + i] * inv, o[j][8 + 4 * y + i] * inv);
+      *(uint4*)(op + 32 * j + 16 * y) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  if (a.lse && half == 0)
+    a.lse[(rg.q0 + qrow) * a.q_heads + head] =
+        l == 0.0f ? -__builtin_inff() : (__builtin_log2f(l) + m) * 0.6931471805599453f;
+}
+
 static_assert(attn_wgs(64) * 4 + kWsCounterOff <= kWsReserved, "one counter a workgroup");
 
 size_t attn4_scratch_bytes(int32_t head_dim) { return (size_t)2 * attn_wgs(head_dim) * 16 * (head_dim + 2) * 4; }
@@ -650,8 +1000,34 @@ static hipError_t launch_r(const Attn4& a, hipStream_t s) {
 }
 
 template <int D>
-static hipError_t launch_d(const Attn4& a, hipStream_t s) {
-  return (int64_t)a.max_q * a.group <= 8 ? launch_r<D, 8>(a, s) : launch_r<D, 16>(a, s);
+static hipError_t launch_prompt(const Attn4& a, hipStream_t s) {
+  // every tile's rows of every KV head, at most one tile a sequence more
+  const int64_t units = (a.total_q * a.group / (32 * prompt_waves(D)) + a.batch) * a.heads;
+  if (units > (int64_t)INT32_MAX) return hipErrorInvalidValue;
+  const size_t lds = sizeof(PromptShared<D>);
+  const hipError_t e = hipFuncSetAttribute((const void*)attn4_prompt_kernel<D>,
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  attn4_prompt_kernel<D><<<(unsigned)units, prompt_waves(D) * 64, lds, s>>>(a);
+  return hipGetLastError();
+}
+
+// Sequences of more query rows a KV head than kFewRows take the prompt kernel, the others the
+// one above; where the lengths are on the device both are launched, and each leaves the other's
+// sequences out.
+constexpr int kFewRows = 64;
+
+template <int D>
+static hipError_t launch_d(const Attn4& call, hipStream_t s) {
+  Attn4 a = call;
+  const int64_t most = (int64_t)a.max_q * a.group;
+  a.few = INT32_MAX;
+  if (most <= 8) return launch_r<D, 8>(a, s);
+  if (most <= kFewRows) return launch_r<D, 16>(a, s);
+  a.few = a.q_starts ? kFewRows : 0;
+  const hipError_t e = launch_prompt<D>(a, s);
+  if (e != hipSuccess || !a.q_starts) return e;
+  return a.group <= 8 ? launch_r<D, 8>(a, s) : launch_r<D, 16>(a, s);
 }
 
 hipError_t launch_attn4(const Attn4& a, int head_dim, hipStream_t s) {
