@@ -662,13 +662,9 @@ struct PromptShared {
   uint4 v[2][kPrGroups][D / 32][64];     // [tile][16 tokens][32 elements][lane]
   float ke[2][kPrGroups];                // 2^(E - 4), 0 for a group that is left out
   float2 vf[2][kPrGroups];               // F and 2^(-9 - F)
+  __attribute__((aligned(8))) _Float16 by[8][16];   // a wave's 2^(ev - F + 4) of 16 tokens
 };
 
-// Maximum over lanes l, l ^ 16, l ^ 32, l ^ 48.
-__device__ __forceinline__ uint32_t max_rows4(uint32_t v) {
-  v = umax(v, (uint32_t)__shfl_xor((int)v, 16));
-  return umax(v, (uint32_t)__shfl_xor((int)v, 32));
-}
 // 2^e as f16 for e <= 15 (0 below the format).
 __device__ __forceinline__ _Float16 pow2_f16(int e) {
   return (_Float16)__uint_as_float((uint32_t)max(e + 127, 0) << 23);
@@ -696,28 +692,26 @@ __device__ __forceinline__ void prompt_keys(PromptShared<D>& sh, int buf, int gr
 }
 
 template <int D>
-__device__ __forceinline__ void prompt_values(PromptShared<D>& sh, int buf, int grp, const Values4<D>& f, uint32_t e4,
+__device__ __forceinline__ void prompt_values(PromptShared<D>& sh, int buf, int grp, Values4<D>& f, uint32_t e4, int wave,
                                               int lane, uint32_t valid) {
   constexpr int KW = D / 32;
   const int m = lane & 15, g = lane >> 4;
-  const uint32_t mine = valid >> (4 * g) & 15u;
-  uint32_t mask = (mine & 1 ? 0xFFu : 0) | (mine & 2 ? 0xFF00u : 0) | (mine & 4 ? 0xFF0000u : 0) |
-                  (mine & 8 ? 0xFF000000u : 0);
-  const uint32_t e = e4 & mask;
-  uint32_t ev[4];
-  uint32_t top = 0;
+  // lane % 16 works out its token's factor; a lane takes those of its four tokens
+  const uint32_t e = (valid >> m & 1) ? min((e4 >> (8 * (m & 3))) & 0xFFu, 244u) : 0u;
+  const uint32_t top = max_row16(e);
+  sh.by[wave][m] = pow2_f16((int)e - (int)top + 4);
+  __builtin_amdgcn_wave_barrier();
+  if (valid != 0xFFFFu) {   // memory that was never written: no NaN from its scales
+    const uint32_t mine = valid >> (4 * g) & 15u;
+    const uint32_t mask = (mine & 1 ? 0xFFu : 0) | (mine & 2 ? 0xFF00u : 0) | (mine & 4 ? 0xFF0000u : 0) |
+                          (mine & 8 ? 0xFF000000u : 0);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    ev[i] = min((e >> (8 * i)) & 0xFFu, 244u);
-    top = umax(top, ev[i]);
+    for (int j = 0; j < KW; ++j) f.vs[j] &= mask;
   }
-  top = max_rows4(top);
-  f16x2 by01{pow2_f16((int)ev[0] - (int)top + 4), pow2_f16((int)ev[1] - (int)top + 4)};
-  f16x2 by23{pow2_f16((int)ev[2] - (int)top + 4), pow2_f16((int)ev[3] - (int)top + 4)};
+  const f16x2 by01 = *(const f16x2*)&sh.by[wave][4 * g], by23 = *(const f16x2*)&sh.by[wave][4 * g + 2];
 #pragma unroll
   for (int j = 0; j < KW; ++j) {
-    const uint32_t sc = f.vs[j] & mask;   // unwritten memory: no NaN from its scales
-    const f16x2 s01 = scales2<false>(sc) * by01, s23 = scales2<true>(sc) * by23;
+    const f16x2 s01 = scales2<false>(f.vs[j]) * by01, s23 = scales2<true>(f.vs[j]) * by23;
     // nibbles of the even (low) and odd (high) elements of tokens (0, 1) to byte 0, (2, 3) to byte 2
     const uint32_t low = 0x000F000Fu, w = f.v[j], w4 = w >> 4, w8 = w >> 8;
     const uint32_t even = (w & low) | (w4 & ~low), odd = (w4 & low) | (w8 & ~low);
@@ -734,7 +728,7 @@ __device__ __forceinline__ void prompt_values(PromptShared<D>& sh, int buf, int 
 
 template <int D>
 __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) / 4) void attn4_prompt_kernel(Attn4 a) {
-  constexpr int KS = D / 16, DT = D / 32, W = prompt_waves(D), kPrRows = 32 * W;
+  constexpr int KS = D / 16, DT = D / 32, W = prompt_waves(D), kPrRows = 32 * W, kAhead = 4;
   extern __shared__ __attribute__((aligned(16))) uint8_t raw[];
   PromptShared<D>& sh = *(PromptShared<D>*)raw;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -834,12 +828,12 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) / 4) void att
     if (takes_keys) load_keys<D>(fk, at, lane_at);
     if (takes_values) {
       load_values<D>(fv, at, lane_at);
-      load_words<1>(&fe, group_rsrc<D>(at), kv4_v_exps(D) + 4 * (lane >> 4));
+      load_words<1>(&fe, group_rsrc<D>(at), kv4_v_exps(D) + (lane & 12));
     }
   };
   const auto put = [&](int buf) {
     if (takes_keys) prompt_keys<D>(sh, buf, grp, fk, lane, valid);
-    if (takes_values) prompt_values<D>(sh, buf, grp, fv, fe, lane, valid);
+    if (takes_values) prompt_values<D>(sh, buf, grp, fv, fe, wave, lane, valid);
   };
 
   // the query rows as f16 with their largest magnitude in [2^14, 2^15) and the scale's sign, so that
@@ -898,14 +892,24 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) / 4) void att
     if (busy && t0 < end_w && t0 + kPrTok > begin_w) {
       f32x16 c[2];
 #pragma unroll
-      for (int tt = 0; tt < 2; ++tt) {
+      for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) c[tt][i] = 0.0f;
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
           c[tt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, sh.k[buf][tt][s][lane]), q[s], c[tt],
                                                          0, 0, 0);
+      // the reads of the key fragments kAhead products ahead (the compiler puts each right before its use)
+      __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+      for (int i = 0; i < 2 * KS - kAhead; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       }
+      __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+      __builtin_amdgcn_sched_barrier(0);
       float kf[kPrGroups], vf[kPrGroups], lf[kPrGroups];
       bool whole = true;
 #pragma unroll
@@ -965,6 +969,19 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) / 4) void att
         for (int j = 0; j < DT; ++j)
           o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, sh.v[buf][gr][j][lane]), p, o[j], 0,
                                                         0, 0);
+      }
+      // the value fragments kAhead products ahead, and the next group's exponentials beside the products
+      __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 1);
+      __builtin_amdgcn_sched_group_barrier(0x400, 8, 1);
+      __builtin_amdgcn_sched_group_barrier(0x002, 13, 1);
+#pragma unroll
+      for (int i = 0; i < kPrGroups * DT; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
+        if (i < kPrGroups * DT - kAhead) __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+        if (i < 3 * DT) {
+          __builtin_amdgcn_sched_group_barrier(0x400, 8 / DT, 1);
+          __builtin_amdgcn_sched_group_barrier(0x002, 13 / DT, 1);
+        }
       }
     }
     __syncthreads();
