@@ -260,33 +260,38 @@ class KVCacheNVFP4:
         return KVCacheNVFP4(data, pages, heads, head_dim, page_size)
 
 
-def _check_on(device, dtype, name, t, shape=None):
+# Checks of the cache's calls.  A decode step makes several of them a layer, so they are few
+# attribute reads each; the messages are put together only when one fails.
+def _refuse(device, dtype, name, t, what):
     if t.device != device:
         raise ValueError(f"{name} must live on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have the shape {shape}")
+    raise ValueError(f"{name} must be {what}")
 
 
 def _check_rows(device, name, t, heads, head_dim):
     # the rows of a token are dense; tokens may be apart (part of a fused projection)
-    _check_on(device, torch.bfloat16, name, t)
-    if t.dim() != 3 or t.shape[1:] != (heads, head_dim):
-        raise ValueError(f"{name} must be [tokens, {heads}, {head_dim}]")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim)):
-        raise ValueError(f"{name} must have dense [heads, head_dim] rows")
+    shape = t.shape
+    if t.device != device or t.dtype != torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
+        _refuse(device, torch.bfloat16, name, t, f"[tokens, {heads}, {head_dim}]")
+    if not t.is_contiguous() and shape[0]:
+        st = t.stride()
+        if st[2] != 1 or (heads > 1 and st[1] != head_dim):
+            raise ValueError(f"{name} must have dense [heads, head_dim] rows")
 
 
 def _check_dense(device, dtype, name, t, shape):
-    _check_on(device, dtype, name, t, shape)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.device != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(device, dtype, name, t, f"a contiguous tensor of the shape {tuple(shape)}")
 
 
-def _check_status(device, status_word):
-    if status_word is not None:
-        _check_dense(device, torch.int32, "status_word", status_word, (1,))
+def _call_on(device, fn, *args):
+    """fn(*args) with `device` current, on its current stream."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
 
 
 def kv_store_nvfp4(k, v, slots, cache, status_word=None):
@@ -294,34 +299,36 @@ def kv_store_nvfp4(k, v, slots, cache, status_word=None):
     dev = _dev(cache.data).device
     _check_rows(dev, "k", k, cache.heads, cache.head_dim)
     _check_rows(dev, "v", v, cache.heads, cache.head_dim)
-    t = k.shape[0]
-    if v.shape[0] != t:
+    t = k.shape[:1]
+    if v.shape[:1] != t:
         raise ValueError("k and v must have the same tokens")
-    _check_dense(dev, torch.int64, "slots", slots, (t,))
-    _check_status(dev, status_word)
-    if t == 0:
-        return
-    with torch.cuda.device(dev):
-        binding.qlinear_kv_store_nvfp4(cache.handle, k, v, slots, status_word)
+    _check_dense(dev, torch.int64, "slots", slots, t)
+    if status_word is not None:
+        _check_dense(dev, torch.int32, "status_word", status_word, (1,))
+    if t[0]:
+        _call_on(dev, binding.qlinear_kv_store_nvfp4, cache.handle, k, v, slots, status_word)
 
 
 def kv_load_nvfp4(cache, slots, k_out=None, v_out=None, status_word=None):
     """(k, v) bf16 [T, H, D] of the cache's slots[t]."""
     dev = _dev(cache.data).device
-    _check_dense(dev, torch.int64, "slots", slots, (slots.numel(),))
-    _check_status(dev, status_word)
-    outs = []
-    for name, o in (("k_out", k_out), ("v_out", v_out)):
-        if o is None:
-            o = torch.empty((slots.shape[0], cache.heads, cache.head_dim), dtype=torch.bfloat16, device=dev)
-        _check_rows(dev, name, o, cache.heads, cache.head_dim)
-        if o.shape[0] != slots.shape[0]:
-            raise ValueError(f"{name} must have one row a slot")
-        outs.append(o)
-    if slots.shape[0]:
-        with torch.cuda.device(dev):
-            binding.qlinear_kv_load_nvfp4(cache.handle, slots, outs[0], outs[1], status_word)
-    return outs[0], outs[1]
+    n = slots.numel()
+    _check_dense(dev, torch.int64, "slots", slots, (n,))
+    if status_word is not None:
+        _check_dense(dev, torch.int32, "status_word", status_word, (1,))
+    if k_out is None:
+        k_out = torch.empty((n, cache.heads, cache.head_dim), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_rows(dev, "k_out", k_out, cache.heads, cache.head_dim)
+    if v_out is None:
+        v_out = torch.empty((n, cache.heads, cache.head_dim), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_rows(dev, "v_out", v_out, cache.heads, cache.head_dim)
+    if k_out.shape[0] != n or v_out.shape[0] != n:
+        raise ValueError("k_out and v_out must have one row a slot")
+    if n:
+        _call_on(dev, binding.qlinear_kv_load_nvfp4, cache.handle, slots, k_out, v_out, status_word)
+    return k_out, v_out
 
 
 def attention_nvfp4(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None, softmax_scale=None, causal=True,
@@ -341,10 +348,9 @@ def attention_nvfp4(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None
     _check_rows(dev, "q", q, hq, cache.head_dim)
     batch = kv_lens.shape[0]
     _check_dense(dev, torch.int32, "kv_lens", kv_lens, (batch,))
-    _check_on(dev, torch.int32, "page_table", page_table)
-    if page_table.dim() != 2 or page_table.shape[0] != batch or \
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be [batch, pages] with dense rows")
+    if page_table.device != dev or page_table.dtype != torch.int32 or page_table.dim() != 2 or \
+            page_table.shape[0] != batch or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        _refuse(dev, torch.int32, "page_table", page_table, "[batch, pages] with dense rows")
     if q_starts is not None:
         _check_dense(dev, torch.int32, "q_starts", q_starts, (batch + 1,))
         if max_q_len is None:
@@ -353,16 +359,16 @@ def attention_nvfp4(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None
         max_q_len = tq // max(batch, 1)
     if out is None:
         out = torch.empty((tq, hq, d), dtype=torch.bfloat16, device=dev)
-    _check_rows(dev, "out", out, hq, d)
-    if out.shape[0] != tq:
-        raise ValueError("out must have q's tokens")
+    else:
+        _check_rows(dev, "out", out, hq, d)
+        if out.shape[0] != tq:
+            raise ValueError("out must have q's tokens")
     if lse is not None:
         _check_dense(dev, torch.float32, "lse", lse, (tq, hq))
-    with torch.cuda.device(dev):
-        if ws is None:
-            ws = _ws(binding.qlinear_attention_nvfp4_workspace(batch, tq, hq, cache.heads, d, max_q_len), dev)
-        else:
-            _check_on(dev, torch.uint8, "ws", ws)
-        binding.qlinear_attention_nvfp4(cache.handle, q, page_table, kv_lens, out, ws, q_starts, max_q_len,
-                                        d ** -0.5 if softmax_scale is None else softmax_scale, causal, window, lse)
+    if ws is None:
+        ws = _ws(binding.qlinear_attention_nvfp4_workspace(batch, tq, hq, cache.heads, d, max_q_len), dev)
+    else:
+        _check_dense(dev, torch.uint8, "ws", ws, (ws.numel(),))
+    _call_on(dev, binding.qlinear_attention_nvfp4, cache.handle, q, page_table, kv_lens, out, ws, q_starts, max_q_len,
+             d ** -0.5 if softmax_scale is None else softmax_scale, causal, window, lse)
     return out

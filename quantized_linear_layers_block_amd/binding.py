@@ -176,6 +176,12 @@ def _stream(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _stream_here():
+    # the raw handle of the current device's current stream, without a Stream object
+    import torch
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
 # ------------------------------------------------------------------ quantizers
 
 def qlinear_quantize_workspace(fmt, n, k):
@@ -348,14 +354,14 @@ def qlinear_kv_nvfp4_bytes(pages, page_size, heads, head_dim):
 def qlinear_kv_store_nvfp4(cache, k, v, slots, status_word=None, stream=None):
     """k, v bf16 [T, H, D] (rows [H, D] dense, any token stride) -> slots[t] of the cache (KvNvfp4)."""
     _check(LIB.qlinear_kv_store_nvfp4(ctypes.byref(cache), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), k.shape[0],
-                                      _ptr(slots), _ptr(status_word), _stream(stream)), "qlinear_kv_store_nvfp4")
+                                      _ptr(slots), _ptr(status_word), _stream_here() if stream is None else stream), "qlinear_kv_store_nvfp4")
 
 
 def qlinear_kv_load_nvfp4(cache, slots, k_out=None, v_out=None, status_word=None, stream=None):
     """slots[t] of the cache -> k_out, v_out bf16 [T, H, D] (either may be None)."""
     _check(LIB.qlinear_kv_load_nvfp4(ctypes.byref(cache), _ptr(slots), slots.shape[0], _ptr(k_out),
                                      0 if k_out is None else _row_stride(k_out), _ptr(v_out),
-                                     0 if v_out is None else _row_stride(v_out), _ptr(status_word), _stream(stream)),
+                                     0 if v_out is None else _row_stride(v_out), _ptr(status_word), _stream_here() if stream is None else stream),
            "qlinear_kv_load_nvfp4")
 
 
@@ -370,7 +376,7 @@ def qlinear_attention_nvfp4(cache, q, page_table, kv_lens, out, ws, q_starts=Non
                      _row_stride(page_table))
     _check(LIB.qlinear_attention_nvfp4(ctypes.byref(cache), ctypes.byref(seqs), _ptr(q), _row_stride(q), q.shape[1],
                                        softmax_scale, 1 if causal else 0, window, _ptr(out), _row_stride(out), _ptr(lse),
-                                       _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+                                       _ptr(ws), ws.numel() * ws.element_size(), _stream_here() if stream is None else stream),
            "qlinear_attention_nvfp4")
 
 
