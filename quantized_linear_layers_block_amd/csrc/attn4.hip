@@ -164,7 +164,7 @@ __device__ __forceinline__ f16x2 both(_Float16 s) { return f16x2{s, s}; }
 constexpr int kAttnStep = 32;                        // tokens of one wave's step
 constexpr int kAttnChunk = kAttnWaves * kAttnStep;   // of the workgroup's
 // Workgroups that fit the chip: 256 CUs and the waves a SIMD holds by the kernel's registers.
-constexpr int attn_wgs_per_cu(int d) { return d == 256 ? 2 : 3; }
+constexpr int attn_wgs_per_cu(int d) { return d == 256 ? 2 : d == 64 ? 4 : 3; }
 constexpr int attn_wgs(int d) { return 256 * attn_wgs_per_cu(d); }
 
 __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
@@ -187,22 +187,30 @@ struct AttnPlace {
   int b, tile, head, k; // unit and its first chunk here
 };
 
+// A sequence's chunks, and its stretch of the line (all tiles and heads).
+__device__ __forceinline__ uint32_t attn_chunks(const Attn4& a, const AttnRange& r) {
+  return max((max(r.n - attn_lo(a, r.nq, r.n), 0) + kAttnChunk - 1) / kAttnChunk, 1);
+}
+template <int R>
+__device__ __forceinline__ uint64_t attn_stretch(const Attn4& a, const AttnRange& r) {
+  const uint32_t tiles = r.nq * a.group > a.few ? 0u : (uint32_t)(r.nq * a.group + R - 1) / R;
+  return (uint64_t)tiles * (uint64_t)attn_chunks(a, r) * (uint32_t)a.heads;
+}
+
 // Every wave works this out for itself, 64 sequences at a time.
 template <int R, int WGS>
-__device__ __forceinline__ bool attn_place(const Attn4& a, AttnPlace& pl) {
+__device__ __forceinline__ bool attn_place(const Attn4& a, AttnPlace& pl, AttnRange& rg) {
   const int lane = threadIdx.x & 63;
-  const auto line = [&](int b, bool& bad) -> uint64_t {  // chunks of a sequence's units (all heads)
-    if (b >= a.batch) return 0;
-    const AttnRange r = attn_range(a, b);
-    bad |= r.bad;
-    const uint32_t tiles = r.nq * a.group > a.few ? 0u : (uint32_t)(r.nq * a.group + R - 1) / R;
-    const uint32_t chunks = max((max(r.n - attn_lo(a, r.nq, r.n), 0) + kAttnChunk - 1) / kAttnChunk, 1);
-    return (uint64_t)tiles * (uint64_t)chunks * (uint32_t)a.heads;
-  };
-  bool bad = false;
-  const uint64_t first = line(lane, bad);
+  const auto range = [&](int b) { return b < a.batch ? attn_range(a, b) : AttnRange{0, 0, 0, false}; };
+  AttnRange r = range(lane);
+  bool bad = r.bad;
+  const uint64_t first = attn_stretch<R>(a, r);
   uint64_t sum = first;
-  for (int b0 = 64; b0 < a.batch; b0 += 64) sum += line(b0 + lane, bad);
+  for (int b0 = 64; b0 < a.batch; b0 += 64) {
+    const AttnRange x = range(b0 + lane);
+    bad |= x.bad;
+    sum += attn_stretch<R>(a, x);
+  }
   if (blockIdx.x == 0 && threadIdx.x < 64 && __any(bad) && lane == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
   sum = uniform(wave_sum_u64(sum));
   pl.each = (sum + WGS - 1) / WGS;
@@ -211,7 +219,8 @@ __device__ __forceinline__ bool attn_place(const Attn4& a, AttnPlace& pl) {
   pl.stop = min(pl.pos + pl.each, sum);
   uint64_t before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    const uint64_t mine = b0 == 0 ? first : line(b0 + lane, bad);
+    if (b0 > 0) r = range(b0 + lane);
+    const uint64_t mine = b0 == 0 ? first : attn_stretch<R>(a, r);
     uint64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -226,11 +235,12 @@ __device__ __forceinline__ bool attn_place(const Attn4& a, AttnPlace& pl) {
     if (past) {
       const int j = __builtin_ctzll(past);
       pl.b = b0 + j;
-      // place within the sequence; its units and their length from its own extents
+      rg.nq = __builtin_amdgcn_readlane(r.nq, j);
+      rg.n = __builtin_amdgcn_readlane(r.n, j);
+      rg.q0 = (int64_t)of_lane((uint64_t)r.q0, j);
+      // place within the sequence: its units and their length
       const uint64_t at = pl.pos - before - of_lane(upto - mine, j);
-      const AttnRange r = attn_range_uniform(a, pl.b);
-      const uint32_t chunks = max((max(r.n - attn_lo(a, r.nq, r.n), 0) + kAttnChunk - 1) / kAttnChunk, 1);
-      const uint32_t unit = (uint32_t)(at / chunks);
+      const uint32_t chunks = attn_chunks(a, rg), unit = (uint32_t)(at / chunks);
       pl.k = __builtin_amdgcn_readfirstlane((int)(at - (uint64_t)unit * chunks));
       pl.tile = __builtin_amdgcn_readfirstlane((int)(unit / (uint32_t)a.heads));
       pl.head = __builtin_amdgcn_readfirstlane((int)(unit - (uint32_t)pl.tile * (uint32_t)a.heads));
@@ -553,6 +563,7 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
         st_dev_u32((uint32_t*)(a.parts + at + R * D * 4) + R + src, __float_as_uint(lsum));
       }
     }
+    if (a.join) return;   // by the kernel that follows
     wait_stores();
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -619,11 +630,11 @@ template <int D, int R>
 __global__ __launch_bounds__(kAttnWaves * 64, attn_wgs_per_cu(D)) void attn4_kernel(Attn4 a) {
   __shared__ AttnShared<D, R> sh;
   AttnPlace pl;
-  if (!attn_place<R, attn_wgs(D)>(a, pl)) return;
-  AttnRange rg = attn_range_uniform(a, pl.b);
+  AttnRange rg;
+  if (!attn_place<R, attn_wgs(D)>(a, pl, rg)) return;
   for (;;) {
     const int lo_b = attn_lo(a, rg.nq, rg.n);
-    const int chunks = max((max(rg.n - lo_b, 0) + kAttnChunk - 1) / kAttnChunk, 1);
+    const int chunks = (int)attn_chunks(a, rg);
     const int k1 = (int)min((uint64_t)chunks, pl.k + (pl.stop - pl.pos));
     attn4_unit<D, R>(a, pl, rg, lo_b + pl.k * kAttnChunk, k1 == chunks ? rg.n : lo_b + k1 * kAttnChunk, chunks, sh);
     pl.pos += k1 - pl.k;
@@ -639,6 +650,87 @@ __global__ __launch_bounds__(kAttnWaves * 64, attn_wgs_per_cu(D)) void attn4_ker
     __syncthreads();   // the shared memory of the unit before is read
   }
 }
+// Where few units are cut into many parts, the one workgroup that joins a unit would take longer
+// (230 KB for 64 parts of 7 rows at D = 128, 13 us) than a launch: this kernel joins each row of
+// each unit by a workgroup.
+template <int D, int R>
+__global__ __launch_bounds__(256) void attn4_join_kernel(Attn4 a, int tiles) {
+  constexpr int WGS = attn_wgs(D), kPer = D / 4, kSide = 256 / kPer;   // threads a part, parts side by side
+  constexpr uint32_t kBytes = attn_part_bytes<D, R>();
+  __shared__ float sm[WGS], sl[WGS], red[kSide][D], smax[4], ssum[kSide];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int row = blockIdx.x % R, unit = blockIdx.x / R;
+  const int head = unit % a.heads, tile = unit / a.heads % tiles, b = unit / a.heads / tiles;
+  const AttnRange rg = attn_range_uniform(a, b);
+  if (tile * R + row >= rg.nq * a.group || rg.nq * a.group > a.few) return;
+  uint64_t sum = 0, before = 0;
+  for (int x = lane; x < a.batch; x += 64) {
+    const uint64_t v = attn_stretch<R>(a, attn_range(a, x));
+    sum += v;
+    before += x < b ? v : 0;
+  }
+  sum = uniform(wave_sum_u64(sum));
+  const uint32_t chunks = attn_chunks(a, rg);
+  const uint64_t u0 = uniform(wave_sum_u64(before)) + (uint64_t)(tile * a.heads + head) * chunks;
+  const uint64_t each = (sum + WGS - 1) / WGS;
+  const int w0 = (int)(u0 / each), splits = (int)((u0 + chunks - 1) / each) - w0 + 1;
+  if (splits < 2) return;
+  const uint32_t first = (uint32_t)(2 * w0 + 1) * kBytes;   // as the parts are placed by attn4_unit
+  const auto place = [&](int s) { return s == 0 ? first : first + (uint32_t)(2 * s - 1) * kBytes; };
+  const int part = threadIdx.x % kPer, side = threadIdx.x / kPer;
+  constexpr int kFly = 8;
+  f32x4 v[kFly];
+  const auto fetch = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < kFly; ++i)
+      v[i] = *(const f32x4*)(a.parts + place(min(s0 + i * kSide + side, splits - 1)) + (uint32_t)(row * D + part * 4) * 4);
+  };
+  fetch(0);
+  float top = kNoMax;
+  for (int s = threadIdx.x; s < splits; s += 256) {
+    const float* ml = (const float*)(a.parts + place(s) + R * D * 4) + row;
+    sm[s] = ml[0];
+    sl[s] = ml[R];
+    top = __builtin_fmaxf(top, ml[0]);
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o));
+  if (lane == 0) smax[wave] = top;
+  __syncthreads();
+  top = __builtin_fmaxf(__builtin_fmaxf(smax[0], smax[1]), __builtin_fmaxf(smax[2], smax[3]));
+  f32x4 acc{0, 0, 0, 0};
+  float l = 0.0f;
+  for (int s0 = 0; s0 < splits; s0 += kFly * kSide) {
+    if (s0 > 0) fetch(s0);
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      const int s = s0 + i * kSide + side;
+      const float w = s < splits ? __builtin_exp2f(sm[min(s, splits - 1)] - top) : 0.0f;
+      l = __builtin_fmaf(w, sl[min(s, splits - 1)], l);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(w, v[i][e], acc[e]);
+    }
+  }
+  *(f32x4*)&red[side][part * 4] = acc;
+  if (part == 0) ssum[side] = l;
+  __syncthreads();
+  if (side > 0) return;
+  l = 0.0f;
+  acc = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int y = 0; y < kSide; ++y) {
+    l += ssum[y];
+    acc += *(const f32x4*)&red[y][part * 4];
+  }
+  const int r = tile * R + row, oq = r / a.group, oh = head * a.group + r - oq * a.group;
+  const float inv = l == 0.0f ? 0.0f : 0.001953125f / l;
+  *(uint2*)(a.out + (rg.q0 + oq) * a.out_stride + (int64_t)oh * D + part * 4) =
+      make_uint2(pack_bf16x2_rne(acc[0] * inv, acc[1] * inv), pack_bf16x2_rne(acc[2] * inv, acc[3] * inv));
+  if (a.lse && part == 0)
+    a.lse[(rg.q0 + oq) * a.q_heads + oh] =
+        l == 0.0f ? -__builtin_inff() : (__builtin_log2f(l) + top) * 0.6931471805599453f;
+}
+
 // ------------------------------------------------------------------ many query rows
 //
 // Prompts and prompt pieces: waves of 32 query rows share the keys and values of 64 tokens at
@@ -1010,9 +1102,18 @@ static_assert(attn_wgs(64) * 4 + kWsCounterOff <= kWsReserved, "one counter a wo
 
 size_t attn4_scratch_bytes(int32_t head_dim) { return (size_t)2 * attn_wgs(head_dim) * 16 * (head_dim + 2) * 4; }
 
+// A second launch pays where units are cut into many parts: few units, and sequences that may be
+// long enough.  28/4 heads: 1 x 8192 tokens (64 parts) 12.7 us against 15.9, 1 x 131072 (192) 29 against
+// 47; 8 x 4096 (24) 15.6 against 14.0; 2 x 8192 of 64/8 heads (48) 15.7 against 16.0.
+constexpr int kJoinParts = 48;
+
 template <int D, int R>
-static hipError_t launch_r(const Attn4& a, hipStream_t s) {
+static hipError_t launch_r(const Attn4& call, hipStream_t s) {
+  Attn4 a = call;
+  const int64_t tiles = ((int64_t)a.max_q * a.group + R - 1) / R, units = tiles * a.heads * a.batch;
+  a.join = units * kJoinParts <= attn_wgs(D) && (a.table_stride << a.page_shift) >= kJoinParts * kAttnChunk;
   attn4_kernel<D, R><<<attn_wgs(D), kAttnWaves * 64, 0, s>>>(a);
+  if (a.join) attn4_join_kernel<D, R><<<(unsigned)(units * R), 256, 0, s>>>(a, (int)tiles);
   return hipGetLastError();
 }
 

@@ -94,7 +94,9 @@ struct Attn4 {
   int32_t* status;
   uint32_t* counters;       // zero before and after a call
   uint8_t* parts;           // attn4_scratch_bytes
-  int few;                  // set by the launcher: most query rows of a sequence for the few-row kernel
+  // set by the launcher
+  int few;                  // most query rows of a sequence for the few-row kernel
+  int join;                 // a second kernel joins the parts of its units
 };
 size_t attn4_scratch_bytes(int32_t head_dim);
 hipError_t launch_attn4(const Attn4& a, int head_dim, hipStream_t s);
