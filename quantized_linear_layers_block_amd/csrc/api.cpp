@@ -551,7 +551,7 @@ static bool attn_sizes_ok(int64_t batch, int64_t total_q, int64_t q_heads, int64
 size_t qlinear_attention_nvfp4_workspace(int32_t batch, int64_t total_q, int32_t q_heads, int32_t heads,
                                          int32_t head_dim, int32_t max_q_len) {
   if (!attn_sizes_ok(batch, total_q, q_heads, heads, head_dim, max_q_len)) return 0;
-  return ql::kWsReserved + up(ql::attn4_scratch_bytes(head_dim));
+  return ql::kWsReserved + up(ql::attn4_scratch_bytes(batch, total_q, q_heads / heads, heads, head_dim, max_q_len));
 }
 
 qlinear_status qlinear_attention_nvfp4(const qlinear_kv_nvfp4* cache, const qlinear_attn_batch* seqs,

@@ -745,8 +745,23 @@ __global__ __launch_bounds__(256) void attn4_join_kernel(Attn4 a, int tiles) {
 // token would cost two more of some nine vector instructions a logit, and the vector
 // instructions (the exponential takes four of them) weigh as much as the matrix products.
 constexpr int kPrTok = 64, kPrGroups = kPrTok / 16;
-// Waves of a workgroup: two a SIMD, or one where the sums of 32 rows take 128 registers.
-constexpr int prompt_waves(int d) { return d == 256 ? 4 : 8; }
+// Waves of a workgroup, and workgroups of a CU: at D = 128 eight waves, two a SIMD; at D = 64 three
+// workgroups of four (40 sequences of up to 333 tokens in a window of 1024: 71 us against 88 with
+// eight); at D = 256, where the sums of 32 rows take 128 registers, four with a SIMD each.
+constexpr int prompt_waves(int d) { return d == 128 ? 8 : 4; }
+constexpr int prompt_wgs_per_cu(int d) { return d == 64 ? 3 : 1; }
+constexpr int prompt_rows(int d) { return 32 * prompt_waves(d); }
+// Where the units leave CUs idle they are cut along the tokens, each into the same number of parts at
+// most (two rounds of workgroups), of kPrPartTiles tiles at least; a kernel of its own joins them.
+constexpr int kPrPartTiles = 16;
+int64_t prompt_units(int64_t total_q, int64_t batch, int64_t group, int64_t heads, int d) {
+  return (total_q * group / prompt_rows(d) + batch) * heads;   // at most one tile a sequence more
+}
+int prompt_parts(int64_t units, int d) {
+  const int64_t room = 2 * 256 * prompt_wgs_per_cu(d) / units;
+  return room < 1 ? 1 : room > 64 ? 64 : (int)room;
+}
+__host__ __device__ constexpr size_t prompt_part_bytes(int d) { return (size_t)prompt_rows(d) * (d + 2) * 4; }
 
 template <int D>
 struct PromptShared {
@@ -818,58 +833,78 @@ __device__ __forceinline__ void prompt_values(PromptShared<D>& sh, int buf, int 
   if (lane == 0) sh.vf[buf][grp] = make_float2((float)(int)top - 127.0f, __uint_as_float((245u - top) << 23));
 }
 
+// Unit `id`: (sequence, row tile, head), a sequence's last tiles first (they see the most).
 template <int D>
-__global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) / 4) void attn4_prompt_kernel(Attn4 a) {
-  constexpr int KS = D / 16, DT = D / 32, W = prompt_waves(D), kPrRows = 32 * W, kAhead = 4;
+__device__ __forceinline__ bool prompt_unit(const Attn4& a, int id, int& b, int& tile, int& h) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  bool found = false;
+  for (int b0 = 0; b0 < a.batch && !found; b0 += 64) {
+    AttnRange r{0, 0, 0, false};
+    if (b0 + lane < a.batch) r = attn_range(a, b0 + lane);
+    const int rows = r.nq * a.group;
+    const int tiles = rows > a.few ? (rows + prompt_rows(D) - 1) / prompt_rows(D) : 0;
+    int upto = tiles * a.heads;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int x = __shfl_up(upto, o);
+      if (lane >= o) upto += x;
+    }
+    const uint64_t past = __ballot(before + upto > id);
+    if (past) {
+      const int j = __builtin_ctzll(past);
+      const int nt = __builtin_amdgcn_readlane(tiles, j);
+      const int at = id - before - (__builtin_amdgcn_readlane(upto, j) - nt * a.heads);
+      b = b0 + j;
+      tile = __builtin_amdgcn_readfirstlane(nt - 1 - at / a.heads);
+      h = __builtin_amdgcn_readfirstlane(at % a.heads);
+      found = true;
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return found;
+}
+
+// Tiles of 64 tokens that some row of the unit sees, from `first` on, and the parts they are cut into.
+struct PromptTiles {
+  int begin, stop, first, tiles, parts;
+};
+template <int D>
+__device__ __forceinline__ PromptTiles prompt_tiles(const Attn4& a, const AttnRange& rg, int tile) {
+  const int r0 = tile * prompt_rows(D), live = min(rg.nq * a.group - r0, prompt_rows(D));
+  const int qa = r0 / a.group, qz = (r0 + live - 1) / a.group;
+  PromptTiles t;
+  t.stop = a.causal ? rg.n - rg.nq + qz + 1 : rg.n;
+  t.begin = a.window ? max(rg.n - rg.nq + qa + 1 - a.window, 0) : 0;
+  t.first = t.begin & ~(kPrTok - 1);
+  t.tiles = t.stop > t.first ? (t.stop - t.first + kPrTok - 1) / kPrTok : 0;
+  t.parts = min(max(t.tiles / kPrPartTiles, 1), a.parts_each);
+  return t;
+}
+
+template <int D>
+__global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_per_cu(D) / 4) void attn4_prompt_kernel(Attn4 a) {
+  constexpr int KS = D / 16, DT = D / 32, W = prompt_waves(D), kPrRows = prompt_rows(D), kAhead = 4;
   extern __shared__ __attribute__((aligned(16))) uint8_t raw[];
   PromptShared<D>& sh = *(PromptShared<D>*)raw;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n32 = lane & 31, half = lane >> 5;
 
-  // the unit: (sequence, row tile, head), a sequence's last tiles first (they see the most)
-  int b = -1, tile = 0, h = 0;
-  {
-    int before = 0;
-    bool bad = false;
-    for (int b0 = 0; b0 < a.batch && b < 0; b0 += 64) {
-      AttnRange r{0, 0, 0, false};
-      if (b0 + lane < a.batch) r = attn_range(a, b0 + lane);
-      bad |= r.bad;
-      const int rows = r.nq * a.group;
-      const int tiles = rows > a.few ? (rows + kPrRows - 1) / kPrRows : 0;
-      int upto = tiles * a.heads;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int x = __shfl_up(upto, o);
-        if (lane >= o) upto += x;
-      }
-      const uint64_t past = __ballot(before + upto > (int)blockIdx.x);
-      if (past) {
-        const int j = __builtin_ctzll(past);
-        const int nt = __builtin_amdgcn_readlane(tiles, j);
-        const int at = (int)blockIdx.x - before - (__builtin_amdgcn_readlane(upto, j) - nt * a.heads);
-        b = b0 + j;
-        tile = nt - 1 - at / a.heads;
-        h = at % a.heads;
-      }
-      before += __builtin_amdgcn_readlane(upto, 63);
-    }
-    if (blockIdx.x == 0 && a.few == 0 && __any(bad) && threadIdx.x == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
-  }
-  if (b < 0) return;
-  tile = __builtin_amdgcn_readfirstlane(tile);
-  h = __builtin_amdgcn_readfirstlane(h);
+  int b, tile, h;
+  if (!prompt_unit<D>(a, (int)blockIdx.x / a.parts_each, b, tile, h)) return;
   const AttnRange rg = attn_range_uniform(a, b);
+  if (rg.bad && h == 0 && threadIdx.x == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
   const int rows = rg.nq * a.group;
   const int r0 = tile * kPrRows;
   const int tile_live = min(rows - r0, kPrRows);
   const int qa = r0 / a.group, ra = r0 - qa * a.group;
-  const int qz = (r0 + tile_live - 1) / a.group;
-  // tokens that some row of the workgroup sees
-  const int stop = a.causal ? rg.n - rg.nq + qz + 1 : rg.n;
-  const int begin = a.window ? max(rg.n - rg.nq + qa + 1 - a.window, 0) : 0;
-  const int first = begin & ~(kPrTok - 1);
-  const int tiles = stop > first ? (stop - first + kPrTok - 1) / kPrTok : 0;
+  // this part's tiles and the tokens in them that some row of the workgroup sees
+  const PromptTiles pt = prompt_tiles<D>(a, rg, tile);
+  const int part = (int)blockIdx.x % a.parts_each;
+  if (part >= pt.parts) return;
+  const int x0 = (int)((int64_t)pt.tiles * part / pt.parts), tiles = (int)((int64_t)pt.tiles * (part + 1) / pt.parts) - x0;
+  const int first = pt.first + x0 * kPrTok;
+  const int begin = max(pt.begin, first), stop = min(pt.stop, first + tiles * kPrTok);
 
   // this wave's rows and this lane's
   const int wr = wave * 32;
@@ -1082,6 +1117,23 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) / 4) void att
 
   l += __shfl_xor(l, 32);
   if (wr + n32 >= tile_live) return;
+  if (pt.parts > 1) {   // this part's sums and their maximum, for the joining kernel
+    float* to_part = (float*)(a.parts + (size_t)blockIdx.x * prompt_part_bytes(D));
+    const int r = wr + n32;
+#pragma unroll
+    for (int j = 0; j < DT; ++j)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float* at = to_part + r * D + 32 * j + 16 * y + 8 * half;
+        *(f32x4*)at = f32x4{o[j][4 * y], o[j][8 + 4 * y], o[j][4 * y + 1], o[j][8 + 4 * y + 1]};
+        *(f32x4*)(at + 4) = f32x4{o[j][4 * y + 2], o[j][8 + 4 * y + 2], o[j][4 * y + 3], o[j][8 + 4 * y + 3]};
+      }
+    if (half == 0) {
+      to_part[kPrRows * D + r] = limit == 15.0f ? m : kNoMax;
+      to_part[kPrRows * D + kPrRows + r] = l;
+    }
+    return;
+  }
   const float inv = l == 0.0f ? 0.0f : 1.220703125e-4f / l;   // 2^-13; a row that sees nothing: zeros
   uint16_t* op = a.out + (rg.q0 + qrow) * a.out_stride + (int64_t)head * D + 8 * half;
 #pragma unroll
@@ -1098,9 +1150,56 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) / 4) void att
         l == 0.0f ? -__builtin_inff() : (__builtin_log2f(l) + m) * 0.6931471805599453f;
 }
 
+// Joins the parts of the prompt kernel's units: D / 4 threads a row.
+template <int D>
+__global__ __launch_bounds__(256) void attn4_prompt_join_kernel(Attn4 a) {
+  constexpr int kPer = D / 4, kRowsWg = 256 / kPer, kWgs = prompt_rows(D) / kRowsWg, ROWS = prompt_rows(D);
+  int b, tile, h;
+  const int unit = (int)blockIdx.x / kWgs;
+  if (!prompt_unit<D>(a, unit, b, tile, h)) return;
+  const AttnRange rg = attn_range_uniform(a, b);
+  const PromptTiles pt = prompt_tiles<D>(a, rg, tile);
+  const int r = (int)blockIdx.x % kWgs * kRowsWg + (int)threadIdx.x / kPer, part = (int)threadIdx.x % kPer;
+  const int row = tile * ROWS + r;
+  if (pt.parts < 2 || row >= rg.nq * a.group) return;
+  const float* from = (const float*)(a.parts + (size_t)unit * a.parts_each * prompt_part_bytes(D));
+  constexpr size_t kStep = prompt_part_bytes(D) / 4;
+  float top = kNoMax;
+  for (int s = 0; s < pt.parts; ++s) top = __builtin_fmaxf(top, from[s * kStep + ROWS * D + r]);
+  f32x4 acc{0, 0, 0, 0};
+  float l = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < pt.parts; ++s) {
+    const float w = __builtin_exp2f(from[s * kStep + ROWS * D + r] - top);
+    l = __builtin_fmaf(w, from[s * kStep + ROWS * D + ROWS + r], l);
+    const f32x4 v = *(const f32x4*)(from + s * kStep + r * D + part * 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(w, v[e], acc[e]);
+  }
+  const int oq = row / a.group, oh = h * a.group + row - oq * a.group;
+  const float inv = l == 0.0f ? 0.0f : 1.220703125e-4f / l;
+  *(uint2*)(a.out + (rg.q0 + oq) * a.out_stride + (int64_t)oh * D + part * 4) =
+      make_uint2(pack_bf16x2_rne(acc[0] * inv, acc[1] * inv), pack_bf16x2_rne(acc[2] * inv, acc[3] * inv));
+  if (a.lse && part == 0)
+    a.lse[(rg.q0 + oq) * a.q_heads + oh] =
+        l == 0.0f ? -__builtin_inff() : (__builtin_log2f(l) + top) * 0.6931471805599453f;
+}
+
 static_assert(attn_wgs(64) * 4 + kWsCounterOff <= kWsReserved, "one counter a workgroup");
 
-size_t attn4_scratch_bytes(int32_t head_dim) { return (size_t)2 * attn_wgs(head_dim) * 16 * (head_dim + 2) * 4; }
+// Sequences of more query rows a KV head than kFewRows take the prompt kernel, the others the
+// few-row one; where the lengths are on the device both are launched, and each leaves the other's
+// sequences out.
+constexpr int kFewRows = 64;
+
+size_t attn4_scratch_bytes(int64_t batch, int64_t total_q, int64_t group, int64_t heads, int head_dim, int64_t max_q) {
+  const size_t few = (size_t)2 * attn_wgs(head_dim) * 16 * (head_dim + 2) * 4;
+  if (max_q * group <= kFewRows) return few;
+  const int64_t units = prompt_units(total_q, batch, group, heads, head_dim);
+  const int parts = prompt_parts(units, head_dim);
+  const size_t many = parts > 1 ? (size_t)units * parts * prompt_part_bytes(head_dim) : 0;
+  return many > few ? many : few;
+}
 
 // A second launch pays where units are cut into many parts: few units, and sequences that may be
 // long enough.  28/4 heads: 1 x 8192 tokens (64 parts) 12.7 us against 15.9, 1 x 131072 (192) 29 against
@@ -1118,22 +1217,22 @@ static hipError_t launch_r(const Attn4& call, hipStream_t s) {
 }
 
 template <int D>
-static hipError_t launch_prompt(const Attn4& a, hipStream_t s) {
-  // every tile's rows of every KV head, at most one tile a sequence more
-  const int64_t units = (a.total_q * a.group / (32 * prompt_waves(D)) + a.batch) * a.heads;
-  if (units > (int64_t)INT32_MAX) return hipErrorInvalidValue;
+static hipError_t launch_prompt(const Attn4& call, hipStream_t s) {
+  Attn4 a = call;
+  const int64_t units = prompt_units(a.total_q, a.batch, a.group, a.heads, D);
+  // (no more than the longest sequence that the table holds can have)
+  const int64_t most = (a.table_stride << a.page_shift) / (kPrTok * kPrPartTiles);
+  a.parts_each = (int)max((int64_t)1, min((int64_t)prompt_parts(units, D), most));
+  if (units * a.parts_each > (int64_t)INT32_MAX || units * prompt_rows(D) > (int64_t)INT32_MAX) return hipErrorInvalidValue;
   const size_t lds = sizeof(PromptShared<D>);
   const hipError_t e = hipFuncSetAttribute((const void*)attn4_prompt_kernel<D>,
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  attn4_prompt_kernel<D><<<(unsigned)units, prompt_waves(D) * 64, lds, s>>>(a);
+  attn4_prompt_kernel<D><<<(unsigned)(units * a.parts_each), prompt_waves(D) * 64, lds, s>>>(a);
+  if (a.parts_each > 1)
+    attn4_prompt_join_kernel<D><<<(unsigned)(units * (prompt_rows(D) * (D / 4) / 256)), 256, 0, s>>>(a);
   return hipGetLastError();
 }
-
-// Sequences of more query rows a KV head than kFewRows take the prompt kernel, the others the
-// one above; where the lengths are on the device both are launched, and each leaves the other's
-// sequences out.
-constexpr int kFewRows = 64;
 
 template <int D>
 static hipError_t launch_d(const Attn4& call, hipStream_t s) {

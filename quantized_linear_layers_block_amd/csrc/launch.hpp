@@ -97,8 +97,9 @@ struct Attn4 {
   // set by the launcher
   int few;                  // most query rows of a sequence for the few-row kernel
   int join;                 // a second kernel joins the parts of its units
+  int parts_each;           // most parts of a unit of the prompt kernel
 };
-size_t attn4_scratch_bytes(int32_t head_dim);
+size_t attn4_scratch_bytes(int64_t batch, int64_t total_q, int64_t group, int64_t heads, int head_dim, int64_t max_q);
 hipError_t launch_attn4(const Attn4& a, int head_dim, hipStream_t s);
 
 // ---- backward of the NVFP4 + LoRA layer (backward.hip); n % 64 == 0, k % 128 == 0

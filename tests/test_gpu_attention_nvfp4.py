@@ -71,8 +71,8 @@ class Seqs:
         torch.cuda.synchronize()
         return out, lse
 
-    def check(self, out, lse, causal=True, window=0, scale=None, rows=24, seed=0, held=None):
-        """Against the oracle, on at most `rows` query tokens a sequence."""
+    def check(self, out, lse, causal=True, window=0, scale=None, rows=24, seed=0, held=None, only=None):
+        """Against the oracle, on at most `rows` query tokens a sequence (or on those of `only`)."""
         g = np.random.default_rng(seed)
         qf = bf16_bits_to_f32(self.q_bits).astype(np.float64)
         o, z = bf16_bits_to_f32(bf16_bits_of(out)).astype(np.float64), lse.cpu().numpy().astype(np.float64)
@@ -82,6 +82,7 @@ class Seqs:
                 continue
             pick = np.arange(nq) if nq <= rows else np.unique(np.concatenate(
                 [[0, 1, nq - 2, nq - 1], g.choice(nq, rows, replace=False)]))
+            pick = pick if only is None else only
             k, v = (okv.load(self.data, okv.sequence_slots(self.table[b], n, self.page), self.d) if n
                     else (np.zeros((0, self.h, self.d)),) * 2)
             for i in pick:
@@ -124,6 +125,58 @@ def test_a_few_query_tokens(nq, hq, h, d):
 def test_prompts(lens, hq, h, d, page, causal, window):
     s = Seqs(lens, hq, h, d, page, d + len(lens))
     s.check(*s.run(causal=causal, window=window), causal=causal, window=window)
+
+
+@pytest.mark.parametrize("lens,hq,h,d,page", [
+    ([(130, 3000)], 4, 2, 128, 64), ([(70, 2500), (200, 4000), (90, 90)], 3, 1, 128, 16), ([(300, 5000)], 2, 2, 64, 32),
+    ([(66, 2100), (66, 40)], 2, 1, 256, 16)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1500)])
+def test_prompt_pieces_far_into_long_contexts(lens, hq, h, d, page, causal, window):
+    """Few units of many tokens, which are cut along the tokens and joined (a sequence with more
+    queries than keys beside them: rows that see nothing in any part)."""
+    s = Seqs(lens, hq, h, d, page, d + len(lens))
+    s.check(*s.run(causal=causal, window=window), causal=causal, window=window, rows=10)
+
+
+def test_one_row_tile_and_decode_rows_agree():
+    """The same queries as 64 rows and as 65 (the few-row kernel and the prompt kernel)."""
+    for d in (64, 128, 256):
+        s = Seqs([(65, 700)], 1, 1, d, 16, 40 + d)
+        a, la = s.run()
+        s.check(a, la)
+        t = Seqs([(65, 700)], 1, 1, d, 16, 40 + d)
+        t.starts = np.array([0, 64], np.int32)
+        t.kv_lens -= 1
+        t.max_q = 64
+        b, lb = t.run(ragged=True)
+        assert float((a[:64].float() - b[:64].float()).abs().max()) <= 2.0 ** -6 * float(a.float().abs().max())
+        assert float((la[:64] - lb[:64]).abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("scale", [-0.05, 0.0, 3.0])
+def test_prompt_scales_and_extreme_rows(scale):
+    """Negative, zero and large scales; a zero, a tiny and an infinite query row; a NaN token."""
+    s = Seqs([(100, 160)], 2, 1, 64, 16, 31)
+    s.q_bits[3] = 0
+    s.q_bits[5] = 0x0001                       # the smallest bf16
+    s.q = to_dev(s.q_bits)
+    out, lse = s.run(softmax_scale=scale)
+    s.check(out, lse, scale=scale)
+    s.q_bits[7, 1, 2] = 0x7F80
+    s.q = to_dev(s.q_bits)
+    k = f32_to_bf16_bits_rne(np.ones((1, 1, 64), np.float32))
+    bad = k.copy()
+    bad[0, 0, 9] = 0x7FC0
+    slot = torch.from_numpy(okv.sequence_slots(s.table[0], 160, 16)[140:141]).to(DEV)
+    ql.kv_store_nvfp4(to_dev(bad), to_dev(k), slot, s.cache)
+    out2, lse2 = s.run(softmax_scale=scale)
+    o, z = out2.float().cpu().numpy(), lse2.cpu().numpy()
+    assert np.isnan(o[80:]).all() and np.isnan(z[80:]).all()            # query 80 is at position 140
+    assert np.isnan(o[7, 1]).all() and np.isfinite(np.delete(o[:80], 7, axis=0)).all()
+    # the token that changed is beside the others in its 16, which share factors: those rows against
+    # the oracle again
+    s.data = s.cache.data.cpu().numpy()
+    s.check(out2, lse2, scale=scale, only=[0, 3, 5, 8, 20, 60, 70, 78, 79])
 
 
 def test_mixed_batch_with_empty_sequences():
