@@ -252,6 +252,7 @@ class KVCacheNVFP4:
         if d.dtype != torch.uint8 or not d.is_contiguous() or d.numel() != need:
             raise ValueError(f"data must be {need} contiguous bytes")
         self.handle = binding.make_kv_nvfp4(d, self.pages, self.page_size, self.heads, self.head_dim)
+        self.device = d.device
 
     @staticmethod
     def empty(pages, heads, head_dim, page_size=64, device="cuda"):
@@ -262,6 +263,10 @@ class KVCacheNVFP4:
 
 # Checks of the cache's calls.  A decode step makes several of them a layer, so they are few
 # attribute reads each; the messages are put together only when one fails.
+_BF16, _I32 = torch.bfloat16, torch.int32
+_device_now = torch.cuda.current_device
+
+
 def _refuse(device, dtype, name, t, what):
     if t.device != device:
         raise ValueError(f"{name} must live on {device}")
@@ -270,25 +275,31 @@ def _refuse(device, dtype, name, t, what):
     raise ValueError(f"{name} must be {what}")
 
 
-def _check_rows(device, name, t, heads, head_dim):
+def _cache_device(cache):
+    dev = cache.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
+    return dev
+
+
+def _check_rows(device, name, t, shape):
     # the rows of a token are dense; tokens may be apart (part of a fused projection)
-    shape = t.shape
-    if t.device != device or t.dtype != torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
-        _refuse(device, torch.bfloat16, name, t, f"[tokens, {heads}, {head_dim}]")
+    if t.shape != shape or t.dtype is not _BF16 or t.device != device:
+        _refuse(device, _BF16, name, t, f"of the shape {tuple(shape)}")
     if not t.is_contiguous() and shape[0]:
         st = t.stride()
-        if st[2] != 1 or (heads > 1 and st[1] != head_dim):
+        if st[2] != 1 or (shape[1] > 1 and st[1] != shape[2]):
             raise ValueError(f"{name} must have dense [heads, head_dim] rows")
 
 
 def _check_dense(device, dtype, name, t, shape):
-    if t.device != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         _refuse(device, dtype, name, t, f"a contiguous tensor of the shape {tuple(shape)}")
 
 
 def _call_on(device, fn, *args):
     """fn(*args) with `device` current, on its current stream."""
-    if torch.cuda.current_device() == device.index:
+    if _device_now() == device.index:
         return fn(*args)
     with torch.cuda.device(device):
         return fn(*args)
@@ -296,37 +307,35 @@ def _call_on(device, fn, *args):
 
 def kv_store_nvfp4(k, v, slots, cache, status_word=None):
     """Store bf16 keys and values [T, H, D] in slots[t] (int64, distinct) of an NVFP4 cache."""
-    dev = _dev(cache.data).device
-    _check_rows(dev, "k", k, cache.heads, cache.head_dim)
-    _check_rows(dev, "v", v, cache.heads, cache.head_dim)
-    t = k.shape[:1]
-    if v.shape[:1] != t:
-        raise ValueError("k and v must have the same tokens")
-    _check_dense(dev, torch.int64, "slots", slots, t)
+    dev = _cache_device(cache)
+    t = slots.numel()
+    shape = (t, cache.heads, cache.head_dim)
+    _check_rows(dev, "k", k, shape)
+    _check_rows(dev, "v", v, shape)
+    _check_dense(dev, torch.int64, "slots", slots, (t,))
     if status_word is not None:
-        _check_dense(dev, torch.int32, "status_word", status_word, (1,))
-    if t[0]:
+        _check_dense(dev, _I32, "status_word", status_word, (1,))
+    if t:
         _call_on(dev, binding.qlinear_kv_store_nvfp4, cache.handle, k, v, slots, status_word)
 
 
 def kv_load_nvfp4(cache, slots, k_out=None, v_out=None, status_word=None):
     """(k, v) bf16 [T, H, D] of the cache's slots[t]."""
-    dev = _dev(cache.data).device
-    n = slots.numel()
-    _check_dense(dev, torch.int64, "slots", slots, (n,))
+    dev = _cache_device(cache)
+    t = slots.numel()
+    shape = (t, cache.heads, cache.head_dim)
+    _check_dense(dev, torch.int64, "slots", slots, (t,))
     if status_word is not None:
-        _check_dense(dev, torch.int32, "status_word", status_word, (1,))
+        _check_dense(dev, _I32, "status_word", status_word, (1,))
     if k_out is None:
-        k_out = torch.empty((n, cache.heads, cache.head_dim), dtype=torch.bfloat16, device=dev)
+        k_out = torch.empty(shape, dtype=_BF16, device=dev)
     else:
-        _check_rows(dev, "k_out", k_out, cache.heads, cache.head_dim)
+        _check_rows(dev, "k_out", k_out, shape)
     if v_out is None:
-        v_out = torch.empty((n, cache.heads, cache.head_dim), dtype=torch.bfloat16, device=dev)
+        v_out = torch.empty(shape, dtype=_BF16, device=dev)
     else:
-        _check_rows(dev, "v_out", v_out, cache.heads, cache.head_dim)
-    if k_out.shape[0] != n or v_out.shape[0] != n:
-        raise ValueError("k_out and v_out must have one row a slot")
-    if n:
+        _check_rows(dev, "v_out", v_out, shape)
+    if t:
         _call_on(dev, binding.qlinear_kv_load_nvfp4, cache.handle, slots, k_out, v_out, status_word)
     return k_out, v_out
 
@@ -341,34 +350,33 @@ def attention_nvfp4(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None
     softmax_scale defaults to 1 / sqrt(D).  causal aligns the last query with the last cached
     token; window > 0 keeps the last `window` tokens.  lse (float32 [Tq, Hq]) is filled if
     given.  ws: a zero-filled workspace kept from call to call, as forward's."""
-    dev = _dev(cache.data).device
-    if q.dim() != 3:
-        raise ValueError("q must be [tokens, heads, head_dim]")
-    tq, hq, d = q.shape
-    _check_rows(dev, "q", q, hq, cache.head_dim)
+    dev = _cache_device(cache)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [tokens, heads, {cache.head_dim}]")
+    shape = q.shape
+    tq, hq, d = shape
+    _check_rows(dev, "q", q, shape)
     batch = kv_lens.shape[0]
-    _check_dense(dev, torch.int32, "kv_lens", kv_lens, (batch,))
-    if page_table.device != dev or page_table.dtype != torch.int32 or page_table.dim() != 2 or \
-            page_table.shape[0] != batch or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        _refuse(dev, torch.int32, "page_table", page_table, "[batch, pages] with dense rows")
+    _check_dense(dev, _I32, "kv_lens", kv_lens, (batch,))
+    if page_table.dtype is not _I32 or page_table.dim() != 2 or page_table.shape[0] != batch or \
+            page_table.device != dev or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        _refuse(dev, _I32, "page_table", page_table, "[batch, pages] with dense rows")
     if q_starts is not None:
-        _check_dense(dev, torch.int32, "q_starts", q_starts, (batch + 1,))
+        _check_dense(dev, _I32, "q_starts", q_starts, (batch + 1,))
         if max_q_len is None:
             raise ValueError("q_starts needs max_q_len")
     elif max_q_len is None:
         max_q_len = tq // max(batch, 1)
     if out is None:
-        out = torch.empty((tq, hq, d), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=_BF16, device=dev)
     else:
-        _check_rows(dev, "out", out, hq, d)
-        if out.shape[0] != tq:
-            raise ValueError("out must have q's tokens")
+        _check_rows(dev, "out", out, shape)
     if lse is not None:
         _check_dense(dev, torch.float32, "lse", lse, (tq, hq))
     if ws is None:
         ws = _ws(binding.qlinear_attention_nvfp4_workspace(batch, tq, hq, cache.heads, d, max_q_len), dev)
-    else:
-        _check_dense(dev, torch.uint8, "ws", ws, (ws.numel(),))
+    elif ws.device != dev or not ws.is_contiguous():
+        _refuse(dev, ws.dtype, "ws", ws, "contiguous")
     _call_on(dev, binding.qlinear_attention_nvfp4, cache.handle, q, page_table, kv_lens, out, ws, q_starts, max_q_len,
              d ** -0.5 if softmax_scale is None else softmax_scale, causal, window, lse)
     return out

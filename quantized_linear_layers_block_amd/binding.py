@@ -159,16 +159,6 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _row_stride(t):
-    # PyTorch leaves the stride of a dimension of one entry open
-    if t.shape[0] > 1:
-        return t.stride(0)
-    width = 1
-    for n in t.shape[1:]:
-        width *= n
-    return width
-
-
 def _stream(stream):
     if stream is not None:
         return stream
@@ -176,10 +166,16 @@ def _stream(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
+_raw_stream = None
+
+
 def _stream_here():
     # the raw handle of the current device's current stream, without a Stream object
-    import torch
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = (torch._C._cuda_getCurrentRawStream, torch.cuda.current_device)
+    return _raw_stream[0](_raw_stream[1]())
 
 
 # ------------------------------------------------------------------ quantizers
@@ -351,18 +347,30 @@ def qlinear_kv_nvfp4_bytes(pages, page_size, heads, head_dim):
     return LIB.qlinear_kv_nvfp4_bytes(pages, page_size, heads, head_dim)
 
 
+# A decode step makes these calls in every layer, so they pass on what they are given with few
+# steps.  PyTorch leaves the stride of a dimension of one entry open: then it is the row's width.
+
 def qlinear_kv_store_nvfp4(cache, k, v, slots, status_word=None, stream=None):
     """k, v bf16 [T, H, D] (rows [H, D] dense, any token stride) -> slots[t] of the cache (KvNvfp4)."""
-    _check(LIB.qlinear_kv_store_nvfp4(ctypes.byref(cache), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), k.shape[0],
-                                      _ptr(slots), _ptr(status_word), _stream_here() if stream is None else stream), "qlinear_kv_store_nvfp4")
+    t, h, d = k.shape
+    ks, vs = (k.stride(0), v.stride(0)) if t > 1 else (h * d, h * d)
+    st = LIB.qlinear_kv_store_nvfp4(ctypes.byref(cache), k.data_ptr(), ks, v.data_ptr(), vs, t, slots.data_ptr(),
+                                    None if status_word is None else status_word.data_ptr(),
+                                    _stream_here() if stream is None else stream)
+    if st:
+        raise QlinearError(st, "qlinear_kv_store_nvfp4")
 
 
 def qlinear_kv_load_nvfp4(cache, slots, k_out=None, v_out=None, status_word=None, stream=None):
     """slots[t] of the cache -> k_out, v_out bf16 [T, H, D] (either may be None)."""
-    _check(LIB.qlinear_kv_load_nvfp4(ctypes.byref(cache), _ptr(slots), slots.shape[0], _ptr(k_out),
-                                     0 if k_out is None else _row_stride(k_out), _ptr(v_out),
-                                     0 if v_out is None else _row_stride(v_out), _ptr(status_word), _stream_here() if stream is None else stream),
-           "qlinear_kv_load_nvfp4")
+    t, width = slots.shape[0], cache.heads * cache.head_dim
+    kp, ks = (None, 0) if k_out is None else (k_out.data_ptr(), k_out.stride(0) if t > 1 else width)
+    vp, vs = (None, 0) if v_out is None else (v_out.data_ptr(), v_out.stride(0) if t > 1 else width)
+    st = LIB.qlinear_kv_load_nvfp4(ctypes.byref(cache), slots.data_ptr(), t, kp, ks, vp, vs,
+                                   None if status_word is None else status_word.data_ptr(),
+                                   _stream_here() if stream is None else stream)
+    if st:
+        raise QlinearError(st, "qlinear_kv_load_nvfp4")
 
 
 def qlinear_attention_nvfp4_workspace(batch, total_q, q_heads, heads, head_dim, max_q_len):
@@ -372,12 +380,17 @@ def qlinear_attention_nvfp4_workspace(batch, total_q, q_heads, heads, head_dim, 
 def qlinear_attention_nvfp4(cache, q, page_table, kv_lens, out, ws, q_starts=None, max_q_len=1, softmax_scale=1.0,
                             causal=True, window=0, lse=None, stream=None):
     """out [Tq, Hq, D] = attention of q over the cache (KvNvfp4); lse f32 [Tq, Hq] or None."""
-    seqs = AttnBatch(kv_lens.shape[0], max_q_len, q.shape[0], _ptr(q_starts), _ptr(kv_lens), _ptr(page_table),
-                     _row_stride(page_table))
-    _check(LIB.qlinear_attention_nvfp4(ctypes.byref(cache), ctypes.byref(seqs), _ptr(q), _row_stride(q), q.shape[1],
-                                       softmax_scale, 1 if causal else 0, window, _ptr(out), _row_stride(out), _ptr(lse),
-                                       _ptr(ws), ws.numel() * ws.element_size(), _stream_here() if stream is None else stream),
-           "qlinear_attention_nvfp4")
+    t, h, d = q.shape
+    nb, width = page_table.shape
+    seqs = AttnBatch(nb, max_q_len, t, None if q_starts is None else q_starts.data_ptr(), kv_lens.data_ptr(),
+                     page_table.data_ptr(), page_table.stride(0) if nb > 1 else width)
+    qs, os = (q.stride(0), out.stride(0)) if t > 1 else (h * d, h * d)
+    st = LIB.qlinear_attention_nvfp4(ctypes.byref(cache), ctypes.byref(seqs), q.data_ptr(), qs, h, softmax_scale,
+                                     1 if causal else 0, window, out.data_ptr(), os,
+                                     None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                     _stream_here() if stream is None else stream)
+    if st:
+        raise QlinearError(st, "qlinear_attention_nvfp4")
 
 
 def qlinear_status_word(ws):
