@@ -332,7 +332,7 @@ def kv_load_nvfp4(cache, slots, k_out=None, v_out=None, status_word=None):
     else:
         _check_rows(dev, "k_out", k_out, shape)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=_BF16, device=dev)
+        v_out = torch.empty_like(k_out) if k_out.is_contiguous() else torch.empty(shape, dtype=_BF16, device=dev)
     else:
         _check_rows(dev, "v_out", v_out, shape)
     if t:
@@ -368,7 +368,7 @@ def attention_nvfp4(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None
     elif max_q_len is None:
         max_q_len = tq // max(batch, 1)
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=dev)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=_BF16, device=dev)
     else:
         _check_rows(dev, "out", out, shape)
     if lse is not None:

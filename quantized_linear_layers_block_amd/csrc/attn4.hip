@@ -167,12 +167,32 @@ constexpr int kAttnChunk = kAttnWaves * kAttnStep;   // of the workgroup's
 constexpr int attn_wgs_per_cu(int d) { return d == 256 ? 2 : d == 64 ? 4 : 3; }
 constexpr int attn_wgs(int d) { return 256 * attn_wgs_per_cu(d); }
 
-__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
-  for (int o = 32; o >= 1; o >>= 1) {
-    const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)v, o), hi = (uint32_t)__shfl_xor((int)(v >> 32), o);
-    v += ((uint64_t)hi << 32) | lo;
+// Positions on the line fit 32 bits unless a call could be enormous (a.wide, set from its bounds on
+// the host); the narrow form has the wave's scan in DPP steps and short divisions.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_add(uint32_t v) {
+  return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {  // inclusive
+  v = dpp_add<0x111, 0xF>(v);  // row_shr:1, 2, 4, 8
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);  // the last of rows 0 and 2 to rows 1 and 3
+  return dpp_add<0x143, 0xC>(v);  // the last of row 1 to rows 2 and 3
+}
+__device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t lo = (uint32_t)__shfl_up((int)(uint32_t)v, o), hi = (uint32_t)__shfl_up((int)(v >> 32), o);
+    if (lane >= o) v += ((uint64_t)hi << 32) | lo;
   }
   return v;
+}
+__device__ __forceinline__ uint32_t of_lane(uint32_t v, int j) { return (uint32_t)__builtin_amdgcn_readlane((int)v, j); }
+__device__ __forceinline__ uint64_t of_lane(uint64_t v, int j) {
+  return ((uint64_t)of_lane((uint32_t)(v >> 32), j) << 32) | of_lane((uint32_t)v, j);
 }
 
 // The first token that some row of the sequence sees, down to a step.
@@ -191,47 +211,38 @@ struct AttnPlace {
 __device__ __forceinline__ uint32_t attn_chunks(const Attn4& a, const AttnRange& r) {
   return max((max(r.n - attn_lo(a, r.nq, r.n), 0) + kAttnChunk - 1) / kAttnChunk, 1);
 }
-template <int R>
-__device__ __forceinline__ uint64_t attn_stretch(const Attn4& a, const AttnRange& r) {
+template <int R, typename T>
+__device__ __forceinline__ T attn_stretch(const Attn4& a, const AttnRange& r) {
   const uint32_t tiles = r.nq * a.group > a.few ? 0u : (uint32_t)(r.nq * a.group + R - 1) / R;
-  return (uint64_t)tiles * (uint64_t)attn_chunks(a, r) * (uint32_t)a.heads;
+  return (T)tiles * (T)attn_chunks(a, r) * (uint32_t)a.heads;
 }
 
 // Every wave works this out for itself, 64 sequences at a time.
-template <int R, int WGS>
+template <int R, int WGS, typename T>
 __device__ __forceinline__ bool attn_place(const Attn4& a, AttnPlace& pl, AttnRange& rg) {
   const int lane = threadIdx.x & 63;
   const auto range = [&](int b) { return b < a.batch ? attn_range(a, b) : AttnRange{0, 0, 0, false}; };
   AttnRange r = range(lane);
   bool bad = r.bad;
-  const uint64_t first = attn_stretch<R>(a, r);
-  uint64_t sum = first;
-  for (int b0 = 64; b0 < a.batch; b0 += 64) {
-    const AttnRange x = range(b0 + lane);
-    bad |= x.bad;
-    sum += attn_stretch<R>(a, x);
+  T mine = attn_stretch<R, T>(a, r), upto = wave_scan(mine), sum = of_lane(upto, 63);
+  if (a.batch > 64) {
+    T rest = 0;
+    for (int b0 = 64; b0 < a.batch; b0 += 64) {
+      const AttnRange x = range(b0 + lane);
+      bad |= x.bad;
+      rest += attn_stretch<R, T>(a, x);
+    }
+    sum += of_lane(wave_scan(rest), 63);
   }
   if (blockIdx.x == 0 && threadIdx.x < 64 && __any(bad) && lane == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
-  sum = uniform(wave_sum_u64(sum));
-  pl.each = (sum + WGS - 1) / WGS;
-  pl.pos = (uint64_t)blockIdx.x * pl.each;
-  if (pl.pos >= sum) return false;
-  pl.stop = min(pl.pos + pl.each, sum);
-  uint64_t before = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    if (b0 > 0) r = range(b0 + lane);
-    const uint64_t mine = b0 == 0 ? first : attn_stretch<R>(a, r);
-    uint64_t upto = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t lo = (uint32_t)__shfl_up((int)(uint32_t)upto, o), hi = (uint32_t)__shfl_up((int)(upto >> 32), o);
-      if (lane >= o) upto += ((uint64_t)hi << 32) | lo;
-    }
-    const uint64_t past = __ballot(before + upto > pl.pos);
-    const auto of_lane = [&](uint64_t v, int j) {
-      return ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), j) << 32) |
-             (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, j);
-    };
+  const T each = (sum + WGS - 1) / WGS, pos = (T)blockIdx.x * each;
+  if (pos >= sum) return false;
+  pl.each = each;
+  pl.pos = pos;
+  pl.stop = min(pos + each, sum);
+  T before = 0;
+  for (int b0 = 0;;) {
+    const uint64_t past = __ballot(before + upto > pos);
     if (past) {
       const int j = __builtin_ctzll(past);
       pl.b = b0 + j;
@@ -239,16 +250,31 @@ __device__ __forceinline__ bool attn_place(const Attn4& a, AttnPlace& pl, AttnRa
       rg.n = __builtin_amdgcn_readlane(r.n, j);
       rg.q0 = (int64_t)of_lane((uint64_t)r.q0, j);
       // place within the sequence: its units and their length
-      const uint64_t at = pl.pos - before - of_lane(upto - mine, j);
+      const T at = pos - before - of_lane((T)(upto - mine), j);
       const uint32_t chunks = attn_chunks(a, rg), unit = (uint32_t)(at / chunks);
-      pl.k = __builtin_amdgcn_readfirstlane((int)(at - (uint64_t)unit * chunks));
+      pl.k = __builtin_amdgcn_readfirstlane((int)(at - (T)unit * chunks));
       pl.tile = __builtin_amdgcn_readfirstlane((int)(unit / (uint32_t)a.heads));
       pl.head = __builtin_amdgcn_readfirstlane((int)(unit - (uint32_t)pl.tile * (uint32_t)a.heads));
       return true;
     }
     before += of_lane(upto, 63);
+    b0 += 64;
+    if (b0 >= a.batch) return false;
+    r = range(b0 + lane);
+    mine = attn_stretch<R, T>(a, r);
+    upto = wave_scan(mine);
   }
-  return false;
+}
+
+// The workgroups that a unit of `chunks` from u0 on the line lies in: the first, and how many.
+__device__ __forceinline__ int attn_parts(const Attn4& a, uint64_t u0, uint32_t chunks, uint64_t each, int& w0) {
+  if (a.wide) {
+    w0 = (int)(u0 / each);
+    return (int)((u0 + chunks - 1) / each) - w0 + 1;
+  }
+  const uint32_t e = (uint32_t)each;
+  w0 = (int)((uint32_t)u0 / e);
+  return (int)(((uint32_t)u0 + chunks - 1) / e) - w0 + 1;
 }
 
 // Partial results of a split: R rows of D float32 sums, then m and l of the rows.
@@ -307,36 +333,6 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
   const int all_from = a.window ? end - a.window : 0;
   const int hi = min(end, stop);
 
-  // the query row as f16 with its largest magnitude in [2^14, 2^15)
-  f16x8 q[KW];
-  float kc;
-  {
-    uint4 x[KW];
-    const uint16_t* qp = a.q + (rg.q0 + qa + dq) * a.q_stride + (int64_t)head * D + g * (D / 4);
-    uint32_t amax = 0;
-#pragma unroll
-    for (int s = 0; s < KW; ++s) {
-      x[s] = *(const uint4*)(qp + 8 * s);
-      u16x2 t = max_u16x2(max_u16x2(abs_bits2(x[s].x), abs_bits2(x[s].y)),
-                          max_u16x2(abs_bits2(x[s].z), abs_bits2(x[s].w)));
-      amax = umax(amax, hmax_u16x2(t));
-    }
-    amax = umax(amax, (uint32_t)__shfl_xor((int)amax, 16));
-    amax = umax(amax, (uint32_t)__shfl_xor((int)amax, 32));
-    const int e = amax ? (int)(amax >> 7) - 127 - 14 : 0;   // subnormal rows: -141, still exact
-    kc = __builtin_ldexpf(a.scale_log2e, e);
-    if (amax >= kBf16InfBits) kc = __builtin_nanf("");
-#pragma unroll
-    for (int s = 0; s < KW; ++s) {
-      const uint32_t w[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        q[s][2 * i] = (_Float16)__builtin_ldexpf(bf16_lo(w[i]), -e);
-        q[s][2 * i + 1] = (_Float16)__builtin_ldexpf(bf16_hi(w[i]), -e);
-      }
-    }
-  }
-
   f32x4 o[P][KW];
 #pragma unroll
   for (int y = 0; y < P; ++y)
@@ -376,8 +372,16 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
   const uint8_t* grp[2];
   bool ok[2] = {false, false};
   int x = 0;
-  if (lo + wave * 32 < hi) {
-    look_up(0);
+  const bool any = lo + wave * 32 < hi;
+  // the first loads in the order in which they are waited for: pages, the query row, codes
+  look_up(0);
+  uint4 qx[KW];
+  {
+    const uint16_t* qp = a.q + (rg.q0 + qa + dq) * a.q_stride + (int64_t)head * D + g * (D / 4);
+#pragma unroll
+    for (int s = 0; s < KW; ++s) qx[s] = *(const uint4*)(qp + 8 * s);
+  }
+  if (any) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       ok[u] = __builtin_amdgcn_readlane(pages, u) >= 0;
@@ -387,6 +391,34 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
 #pragma unroll
     for (int u = 0; u < 2; ++u) load_values<D>(fv[u], grp[u], lane_at);
   }
+
+  // the query row as f16 with its largest magnitude in [2^14, 2^15)
+  f16x8 q[KW];
+  float kc;
+  {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int s = 0; s < KW; ++s) {
+      u16x2 t = max_u16x2(max_u16x2(abs_bits2(qx[s].x), abs_bits2(qx[s].y)),
+                          max_u16x2(abs_bits2(qx[s].z), abs_bits2(qx[s].w)));
+      amax = umax(amax, hmax_u16x2(t));
+    }
+    amax = umax(amax, (uint32_t)__shfl_xor((int)amax, 16));
+    amax = umax(amax, (uint32_t)__shfl_xor((int)amax, 32));
+    const int e = amax ? (int)(amax >> 7) - 127 - 14 : 0;   // subnormal rows: -141, still exact
+    kc = __builtin_ldexpf(a.scale_log2e, e);
+    if (amax >= kBf16InfBits) kc = __builtin_nanf("");
+#pragma unroll
+    for (int s = 0; s < KW; ++s) {
+      const uint32_t w[4] = {qx[s].x, qx[s].y, qx[s].z, qx[s].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        q[s][2 * i] = (_Float16)__builtin_ldexpf(bf16_lo(w[i]), -e);
+        q[s][2 * i + 1] = (_Float16)__builtin_ldexpf(bf16_hi(w[i]), -e);
+      }
+    }
+  }
+
   for (int t0 = lo + wave * 32; t0 < hi; t0 += kAttnWaves * 32) {
     // what depends on the token alone is worked out by one lane a token and shared: 2^ek, ev + 127
     // and 2^(-9 - ev) at 0, 16 and 32 of x
@@ -545,7 +577,8 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
     for (int e = 0; e < E; ++e) acc[e] += s * sh.o[w][src][part * E + e];
   }
   const uint64_t u0 = pl.pos - (uint64_t)pl.k;   // the unit on the line, and the workgroups it lies in
-  const int w0 = (int)(u0 / pl.each), splits = (int)((u0 + chunks - 1) / pl.each) - w0 + 1;
+  int w0;
+  const int splits = attn_parts(a, u0, (uint32_t)chunks, pl.each, w0);
   if (splits > 1) {
     // a workgroup has two places for partial results: for the unit that goes on in the next
     // workgroup (1) and for the one that came from the one before (0)
@@ -631,7 +664,7 @@ __global__ __launch_bounds__(kAttnWaves * 64, attn_wgs_per_cu(D)) void attn4_ker
   __shared__ AttnShared<D, R> sh;
   AttnPlace pl;
   AttnRange rg;
-  if (!attn_place<R, attn_wgs(D)>(a, pl, rg)) return;
+  if (!(a.wide ? attn_place<R, attn_wgs(D), uint64_t>(a, pl, rg) : attn_place<R, attn_wgs(D), uint32_t>(a, pl, rg))) return;
   for (;;) {
     const int lo_b = attn_lo(a, rg.nq, rg.n);
     const int chunks = (int)attn_chunks(a, rg);
@@ -665,15 +698,16 @@ __global__ __launch_bounds__(256) void attn4_join_kernel(Attn4 a, int tiles) {
   if (tile * R + row >= rg.nq * a.group || rg.nq * a.group > a.few) return;
   uint64_t sum = 0, before = 0;
   for (int x = lane; x < a.batch; x += 64) {
-    const uint64_t v = attn_stretch<R>(a, attn_range(a, x));
+    const uint64_t v = attn_stretch<R, uint64_t>(a, attn_range(a, x));
     sum += v;
     before += x < b ? v : 0;
   }
-  sum = uniform(wave_sum_u64(sum));
+  sum = of_lane(wave_scan(sum), 63);
   const uint32_t chunks = attn_chunks(a, rg);
-  const uint64_t u0 = uniform(wave_sum_u64(before)) + (uint64_t)(tile * a.heads + head) * chunks;
+  const uint64_t u0 = of_lane(wave_scan(before), 63) + (uint64_t)(tile * a.heads + head) * chunks;
   const uint64_t each = (sum + WGS - 1) / WGS;
-  const int w0 = (int)(u0 / each), splits = (int)((u0 + chunks - 1) / each) - w0 + 1;
+  int w0;
+  const int splits = attn_parts(a, u0, chunks, each, w0);
   if (splits < 2) return;
   const uint32_t first = (uint32_t)(2 * w0 + 1) * kBytes;   // as the parts are placed by attn4_unit
   const auto place = [&](int s) { return s == 0 ? first : first + (uint32_t)(2 * s - 1) * kBytes; };
@@ -1211,6 +1245,8 @@ static hipError_t launch_r(const Attn4& call, hipStream_t s) {
   Attn4 a = call;
   const int64_t tiles = ((int64_t)a.max_q * a.group + R - 1) / R, units = tiles * a.heads * a.batch;
   a.join = units * kJoinParts <= attn_wgs(D) && (a.table_stride << a.page_shift) >= kJoinParts * kAttnChunk;
+  const int64_t chunks = (a.table_stride << a.page_shift) / kAttnChunk + 1;   // < 2^24
+  a.wide = units > (int64_t)INT32_MAX / chunks;
   attn4_kernel<D, R><<<attn_wgs(D), kAttnWaves * 64, 0, s>>>(a);
   if (a.join) attn4_join_kernel<D, R><<<(unsigned)(units * R), 256, 0, s>>>(a, (int)tiles);
   return hipGetLastError();
