@@ -200,21 +200,72 @@ __device__ __forceinline__ int attn_lo(const Attn4& a, int nq, int n) {
   return a.window ? max(n - nq + 1 - a.window, 0) & ~(kAttnStep - 1) : 0;
 }
 
+// How the line is cut.  A unit's start in a workgroup (its query rows, the first loads, the joins at
+// its end) takes as long as two or three chunks.  So, where that makes the shares hardly longer,
+// each unit gets whole workgroups: its stretch is filled up to a multiple of the share.  Else, where
+// the shares are long, a unit's stretch begins with `cost` places without a chunk.
+struct AttnCut {
+  uint64_t each;   // chunks a workgroup
+  uint32_t cost;
+  bool whole;
+  template <typename T>
+  __device__ __forceinline__ T stretch(uint32_t chunks) const {
+    if (!whole || each <= 1) return (T)chunks + cost;
+    return (T)((chunks + (uint32_t)each - 1) / (uint32_t)each) * (T)each;
+  }
+};
+constexpr uint32_t kUnitCost = 2, kCostShare = 3, kWholeMore = 2;
+
 // A workgroup's place on the line.
 struct AttnPlace {
   uint64_t pos, stop;   // chunks of the line
-  uint64_t each;        // chunks a workgroup
   int b, tile, head, k; // unit and its first chunk here
+  AttnCut cut;
+  int done, turn;       // chunks behind it; when the waves' priority is lowered next
 };
+
+// Of the workgroups that share a CU the oldest is served first at every turn: they ended at 100, 114
+// and 146 us of a call whose work was cut equally.  So a wave that is ahead in its share gives way.
+__device__ __forceinline__ void attn_give_way(AttnPlace& pl, int each) {
+  if (pl.turn < each / 2 + each / 4) {
+    __builtin_amdgcn_s_setprio(2);
+    pl.turn = each / 2 + each / 4;
+  } else if (pl.turn < each - each / 8) {
+    __builtin_amdgcn_s_setprio(1);
+    pl.turn = each - each / 8;
+  } else {
+    __builtin_amdgcn_s_setprio(0);
+    pl.turn = INT32_MAX;
+  }
+}
 
 // A sequence's chunks, and its stretch of the line (all tiles and heads).
 __device__ __forceinline__ uint32_t attn_chunks(const Attn4& a, const AttnRange& r) {
   return max((max(r.n - attn_lo(a, r.nq, r.n), 0) + kAttnChunk - 1) / kAttnChunk, 1);
 }
-template <int R, typename T>
-__device__ __forceinline__ T attn_stretch(const Attn4& a, const AttnRange& r) {
-  const uint32_t tiles = r.nq * a.group > a.few ? 0u : (uint32_t)(r.nq * a.group + R - 1) / R;
-  return (T)tiles * (T)attn_chunks(a, r) * (uint32_t)a.heads;
+template <int R>
+__device__ __forceinline__ uint32_t attn_units(const Attn4& a, const AttnRange& r) {
+  return (r.nq * a.group > a.few ? 0u : (uint32_t)(r.nq * a.group + R - 1) / R) * (uint32_t)a.heads;
+}
+
+// units, chunks: a lane's sequence (of all, if there are no more than 64); sum, sum_u: the chunks
+// and units of all
+template <int WGS, typename T>
+__device__ __forceinline__ AttnCut attn_cut(const Attn4& a, uint32_t units, uint32_t chunks, T sum, T sum_u) {
+  AttnCut c{(uint64_t)((sum + WGS - 1) / WGS), 0, sum <= WGS};
+  if (c.whole) return c;
+  if (a.batch <= 64 && sum_u <= WGS) {
+    const uint32_t each = (uint32_t)c.each;   // < 2^24: a unit's chunks are
+    for (uint32_t e = each; e <= each + kWholeMore; ++e)
+      if (of_lane(wave_scan(units * ((chunks + e - 1) / e)), 63) <= WGS) {
+        c.each = e;
+        c.whole = true;
+        return c;
+      }
+  }
+  c.cost = (uint32_t)min((T)kUnitCost, sum / (WGS * kCostShare));
+  c.each = (uint64_t)((sum + sum_u * c.cost + WGS - 1) / WGS);
+  return c;
 }
 
 // Every wave works this out for itself, 64 sequences at a time.
@@ -224,22 +275,24 @@ __device__ __forceinline__ bool attn_place(const Attn4& a, AttnPlace& pl, AttnRa
   const auto range = [&](int b) { return b < a.batch ? attn_range(a, b) : AttnRange{0, 0, 0, false}; };
   AttnRange r = range(lane);
   bool bad = r.bad;
-  T mine = attn_stretch<R, T>(a, r), upto = wave_scan(mine), sum = of_lane(upto, 63);
-  if (a.batch > 64) {
-    T rest = 0;
-    for (int b0 = 64; b0 < a.batch; b0 += 64) {
-      const AttnRange x = range(b0 + lane);
-      bad |= x.bad;
-      rest += attn_stretch<R, T>(a, x);
-    }
-    sum += of_lane(wave_scan(rest), 63);
+  const uint32_t units = attn_units<R>(a, r), chunks = attn_chunks(a, r);
+  T sum_u = units, sum = (T)units * chunks;
+  for (int b0 = 64; b0 < a.batch; b0 += 64) {
+    const AttnRange x = range(b0 + lane);
+    bad |= x.bad;
+    const uint32_t u = attn_units<R>(a, x);
+    sum_u += u;
+    sum += (T)u * attn_chunks(a, x);
   }
   if (blockIdx.x == 0 && threadIdx.x < 64 && __any(bad) && lane == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
-  const T each = (sum + WGS - 1) / WGS, pos = (T)blockIdx.x * each;
-  if (pos >= sum) return false;
-  pl.each = each;
-  pl.pos = pos;
-  pl.stop = min(pos + each, sum);
+  sum_u = of_lane(wave_scan(sum_u), 63);
+  sum = of_lane(wave_scan(sum), 63);
+  const AttnCut cut = attn_cut<WGS, T>(a, units, chunks, sum, sum_u);
+  T mine = (T)units * cut.stretch<T>(chunks), upto = wave_scan(mine);
+  const T each = (T)cut.each, pos = (T)blockIdx.x * each, end = cut.whole && each > 1 ? of_lane(upto, 63) : sum + sum_u * cut.cost;
+  if (pos >= end) return false;
+  pl.cut = cut;
+  pl.stop = min(pos + each, end);
   T before = 0;
   for (int b0 = 0;;) {
     const uint64_t past = __ballot(before + upto > pos);
@@ -251,17 +304,20 @@ __device__ __forceinline__ bool attn_place(const Attn4& a, AttnPlace& pl, AttnRa
       rg.q0 = (int64_t)of_lane((uint64_t)r.q0, j);
       // place within the sequence: its units and their length
       const T at = pos - before - of_lane((T)(upto - mine), j);
-      const uint32_t chunks = attn_chunks(a, rg), unit = (uint32_t)(at / chunks);
-      pl.k = __builtin_amdgcn_readfirstlane((int)(at - (T)unit * chunks));
+      const T len = cut.stretch<T>(attn_chunks(a, rg));
+      const uint32_t unit = (uint32_t)(at / len);
+      const int k = __builtin_amdgcn_readfirstlane((int)(at - (T)unit * len)) - (int)cut.cost;
+      pl.k = max(k, 0);
+      pl.pos = pos + (uint32_t)(pl.k - k);
       pl.tile = __builtin_amdgcn_readfirstlane((int)(unit / (uint32_t)a.heads));
       pl.head = __builtin_amdgcn_readfirstlane((int)(unit - (uint32_t)pl.tile * (uint32_t)a.heads));
-      return true;
+      return pl.pos < pl.stop;
     }
     before += of_lane(upto, 63);
     b0 += 64;
     if (b0 >= a.batch) return false;
     r = range(b0 + lane);
-    mine = attn_stretch<R, T>(a, r);
+    mine = (T)attn_units<R>(a, r) * cut.stretch<T>(attn_chunks(a, r));
     upto = wave_scan(mine);
   }
 }
@@ -307,7 +363,7 @@ struct AttnShared {
 // instructions that would part the pairs, which have none.  With R = 8 rows the two are the
 // two halves of the 16 columns of one product, with R = 16 two products.
 template <int D, int R>
-__device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, const AttnRange& rg, int lo, int stop,
+__device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const AttnRange& rg, int lo, int stop,
                                            int chunks, AttnShared<D, R>& sh) {
   constexpr int KW = D / 32, P = R / 8;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -419,7 +475,10 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
     }
   }
 
+  const int each = (int)min(pl.cut.each, (uint64_t)(1 << 30));
+  int done = pl.done;
   for (int t0 = lo + wave * 32; t0 < hi; t0 += kAttnWaves * 32) {
+    if (++done > pl.turn) attn_give_way(pl, each);
     // what depends on the token alone is worked out by one lane a token and shared: 2^ek, ev + 127
     // and 2^(-9 - ev) at 0, 16 and 32 of x
 #pragma unroll
@@ -578,7 +637,7 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, const AttnPlace& pl, 
   }
   const uint64_t u0 = pl.pos - (uint64_t)pl.k;   // the unit on the line, and the workgroups it lies in
   int w0;
-  const int splits = attn_parts(a, u0, (uint32_t)chunks, pl.each, w0);
+  const int splits = attn_parts(a, u0, (uint32_t)chunks, pl.cut.each, w0);
   if (splits > 1) {
     // a workgroup has two places for partial results: for the unit that goes on in the next
     // workgroup (1) and for the one that came from the one before (0)
@@ -665,13 +724,18 @@ __global__ __launch_bounds__(kAttnWaves * 64, attn_wgs_per_cu(D)) void attn4_ker
   AttnPlace pl;
   AttnRange rg;
   if (!(a.wide ? attn_place<R, attn_wgs(D), uint64_t>(a, pl, rg) : attn_place<R, attn_wgs(D), uint32_t>(a, pl, rg))) return;
+  pl.done = 0;
+  pl.turn = (int)min(pl.cut.each, (uint64_t)(1 << 30)) / 2;
+  __builtin_amdgcn_s_setprio(3);
   for (;;) {
     const int lo_b = attn_lo(a, rg.nq, rg.n);
     const int chunks = (int)attn_chunks(a, rg);
     const int k1 = (int)min((uint64_t)chunks, pl.k + (pl.stop - pl.pos));
     attn4_unit<D, R>(a, pl, rg, lo_b + pl.k * kAttnChunk, k1 == chunks ? rg.n : lo_b + k1 * kAttnChunk, chunks, sh);
     pl.pos += k1 - pl.k;
-    if (pl.pos >= pl.stop) break;
+    pl.done += k1 - pl.k;
+    if (k1 == chunks) pl.pos += pl.cut.cost;
+    if (pl.cut.whole || pl.pos >= pl.stop) break;
     pl.k = 0;
     if (++pl.head == a.heads) {
       pl.head = 0;
@@ -696,18 +760,16 @@ __global__ __launch_bounds__(256) void attn4_join_kernel(Attn4 a, int tiles) {
   const int head = unit % a.heads, tile = unit / a.heads % tiles, b = unit / a.heads / tiles;
   const AttnRange rg = attn_range_uniform(a, b);
   if (tile * R + row >= rg.nq * a.group || rg.nq * a.group > a.few) return;
-  uint64_t sum = 0, before = 0;
-  for (int x = lane; x < a.batch; x += 64) {
-    const uint64_t v = attn_stretch<R, uint64_t>(a, attn_range(a, x));
-    sum += v;
-    before += x < b ? v : 0;
-  }
-  sum = of_lane(wave_scan(sum), 63);
-  const uint32_t chunks = attn_chunks(a, rg);
-  const uint64_t u0 = of_lane(wave_scan(before), 63) + (uint64_t)(tile * a.heads + head) * chunks;
-  const uint64_t each = (sum + WGS - 1) / WGS;
+  // (no more than 64 sequences: launch_r)
+  const AttnRange at = lane < a.batch ? attn_range(a, lane) : AttnRange{0, 0, 0, false};
+  const uint32_t chunks = attn_chunks(a, rg), units = attn_units<R>(a, at), of_lanes = attn_chunks(a, at);
+  const AttnCut cut = attn_cut<WGS, uint64_t>(a, units, of_lanes, of_lane(wave_scan((uint64_t)units * of_lanes), 63),
+                                              of_lane(wave_scan((uint64_t)units), 63));
+  const uint64_t before = lane < b ? units * cut.stretch<uint64_t>(of_lanes) : 0;
+  const uint64_t u0 = of_lane(wave_scan(before), 63) +
+                      (uint64_t)(tile * a.heads + head) * cut.stretch<uint64_t>(chunks) + cut.cost;
   int w0;
-  const int splits = attn_parts(a, u0, chunks, each, w0);
+  const int splits = attn_parts(a, u0, chunks, cut.each, w0);
   if (splits < 2) return;
   const uint32_t first = (uint32_t)(2 * w0 + 1) * kBytes;   // as the parts are placed by attn4_unit
   const auto place = [&](int s) { return s == 0 ? first : first + (uint32_t)(2 * s - 1) * kBytes; };
@@ -1245,7 +1307,7 @@ static hipError_t launch_r(const Attn4& call, hipStream_t s) {
   Attn4 a = call;
   const int64_t tiles = ((int64_t)a.max_q * a.group + R - 1) / R, units = tiles * a.heads * a.batch;
   a.join = units * kJoinParts <= attn_wgs(D) && (a.table_stride << a.page_shift) >= kJoinParts * kAttnChunk;
-  const int64_t chunks = (a.table_stride << a.page_shift) / kAttnChunk + 1;   // < 2^24
+  const int64_t chunks = (a.table_stride << a.page_shift) / kAttnChunk + 1 + kUnitCost;   // < 2^25
   a.wide = units > (int64_t)INT32_MAX / chunks;
   attn4_kernel<D, R><<<attn_wgs(D), kAttnWaves * 64, 0, s>>>(a);
   if (a.join) attn4_join_kernel<D, R><<<(unsigned)(units * R), 256, 0, s>>>(a, (int)tiles);
