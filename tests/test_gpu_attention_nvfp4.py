@@ -138,6 +138,32 @@ def test_prompt_pieces_far_into_long_contexts(lens, hq, h, d, page, causal, wind
     s.check(*s.run(causal=causal, window=window), causal=causal, window=window, rows=10)
 
 
+@pytest.mark.parametrize("batch,n,hq,h,d", [
+    (20, 2000, 16, 8, 128),    # fewer units than workgroups: whole workgroups a unit
+    (70, 1000, 16, 16, 64),    # more, over 64 sequences: shares that begin and end within units
+    (70, 200, 16, 16, 64),     # the same with short shares
+    (33, 700, 4, 4, 256)])
+def test_cuts_of_the_work(batch, n, hq, h, d):
+    g = np.random.default_rng(batch + n)
+    s = Seqs([(1, int(x)) for x in g.integers(n // 2, n + 1, batch)], hq, h, d, 64, n)
+    s.check(*s.run())
+    s.check(*s.run(window=n // 3), window=n // 3)
+
+
+def test_bounds_that_pass_32_bits():
+    """A table of 2^24 tokens a sequence and a large max_q_len: the work could pass 2^31 chunks, and
+    the positions in it are kept in 64 bits.  The same answers as from the narrow call."""
+    s = Seqs([(1, 900), (2, 77), (0, 5), (1, 3000)], 16, 8, 128, 256, 1)
+    starts, out, lse = torch.from_numpy(s.starts).to(DEV), [], []
+    wide = torch.full((len(s.lens), 1 << 16), -1, dtype=torch.int32, device=DEV)
+    wide[:, :s.pt.shape[1]] = s.pt
+    for table, max_q in ((s.pt, 4), (wide, 16384)):
+        out.append(torch.full_like(s.q, 7.0))
+        lse.append(torch.full((s.tq, s.hq), 7.0, dtype=torch.float32, device=DEV))
+        ql.attention_nvfp4(s.q, s.cache, table, s.kv_lens, q_starts=starts, max_q_len=max_q, out=out[-1], lse=lse[-1])
+        s.check(out[-1], lse[-1])
+
+
 def test_one_row_tile_and_decode_rows_agree():
     """The same queries as 64 rows and as 65 (the few-row kernel and the prompt kernel)."""
     for d in (64, 128, 256):
