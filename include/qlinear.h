@@ -422,7 +422,8 @@ qlinear_status qlinear_kv_load_nvfp4(const qlinear_kv_nvfp4* cache, const int64_
  * q, at most max_q_len of them; or NULL: max_q_len query tokens in every sequence and
  * total_q == batch * max_q_len.
  * kv_lens int32 [batch]: its cached tokens, those of its own query tokens included.
- * page_table int32 [batch][table_stride]: the pages that hold them, in order. */
+ * page_table int32, a row of table_pages entries for each sequence, one every table_stride: the
+ * pages that hold its tokens, in order. */
 typedef struct {
   int32_t batch;
   int32_t max_q_len;
@@ -431,6 +432,7 @@ typedef struct {
   const int32_t* kv_lens;
   const int32_t* page_table;
   int64_t table_stride;
+  int64_t table_pages;
 } qlinear_attn_batch;
 
 /* Attention of bf16 queries over the NVFP4 cache, decoding (one or a few query tokens a
@@ -455,8 +457,10 @@ typedef struct {
  * q_starts that do not fit total_q or max_q_len (the sequence is left out).
  * Errors: QL_ERR_NULL, QL_ERR_SHAPE (cache sizes; batch <= 0 or > QLINEAR_MAX_ATTN_BATCH;
  * max_q_len, total_q <= 0 or beyond QLINEAR_MAX_M; q_heads not a multiple of heads; total_q
- * other than batch * max_q_len without q_starts; table_stride <= 0 or 2^30 tokens and more a
- * sequence; strides), QL_ERR_ARG (window < 0, window without causal, softmax_scale not finite),
+ * other than batch * max_q_len without q_starts; table_pages <= 0 or 2^30 tokens and more a
+ * sequence; strides; more work than a launch can count: max_q_len * q_heads / heads, total_q *
+ * q_heads or batch * heads from 2^30 on, 2^22 tiles of prompt rows), QL_ERR_ARG (window < 0,
+ * window without causal, softmax_scale * log2(e) not finite in float32),
  * QL_ERR_ALIGN, QL_ERR_WORKSPACE. */
 #define QLINEAR_MAX_ATTN_BATCH 65535
 qlinear_status qlinear_attention_nvfp4(const qlinear_kv_nvfp4* cache, const qlinear_attn_batch* seqs,

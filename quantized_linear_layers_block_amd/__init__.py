@@ -234,7 +234,7 @@ def kv_load_fp8(cache_codes, cache_scales, slots, heads=None, status_word=None):
     return out
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class KVCacheNVFP4:
     """A paged KV cache in 4 bits: data uint8 [pages, heads, page_size / 16, 18 D + 32] (the
     layout is in include/qlinear.h).  Slot s is token s % page_size of page s // page_size."""
@@ -251,8 +251,9 @@ class KVCacheNVFP4:
             raise ValueError("page_size is a power of two in [16, 1024], head_dim 64, 128 or 256")
         if d.dtype != torch.uint8 or not d.is_contiguous() or d.numel() != need:
             raise ValueError(f"data must be {need} contiguous bytes")
-        self.handle = binding.make_kv_nvfp4(d, self.pages, self.page_size, self.heads, self.head_dim)
-        self.device = d.device
+        # (frozen: the handle holds the address of data)
+        object.__setattr__(self, "handle", binding.make_kv_nvfp4(d, self.pages, self.page_size, self.heads, self.head_dim))
+        object.__setattr__(self, "device", d.device)
 
     @staticmethod
     def empty(pages, heads, head_dim, page_size=64, device="cuda"):
@@ -367,6 +368,8 @@ def attention_nvfp4(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None
             raise ValueError("q_starts needs max_q_len")
     elif max_q_len is None:
         max_q_len = tq // max(batch, 1)
+    if max_q_len > 0x7FFFFFFF or window > 0x7FFFFFFF:
+        raise ValueError("max_q_len and window are 32-bit numbers")
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=_BF16, device=dev)
     else:

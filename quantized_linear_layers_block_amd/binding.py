@@ -85,7 +85,7 @@ class KvNvfp4(ctypes.Structure):
 class AttnBatch(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("max_q_len", ctypes.c_int32), ("total_q", ctypes.c_int64),
                 ("q_starts", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
-                ("table_stride", ctypes.c_int64)]
+                ("table_stride", ctypes.c_int64), ("table_pages", ctypes.c_int64)]
 
 
 def _load():
@@ -383,7 +383,7 @@ def qlinear_attention_nvfp4(cache, q, page_table, kv_lens, out, ws, q_starts=Non
     t, h, d = q.shape
     nb, width = page_table.shape
     seqs = AttnBatch(nb, max_q_len, t, None if q_starts is None else q_starts.data_ptr(), kv_lens.data_ptr(),
-                     page_table.data_ptr(), page_table.stride(0) if nb > 1 else width)
+                     page_table.data_ptr(), page_table.stride(0) if nb > 1 else width, width)
     qs, os = (q.stride(0), out.stride(0)) if t > 1 else (h * d, h * d)
     st = LIB.qlinear_attention_nvfp4(ctypes.byref(cache), ctypes.byref(seqs), q.data_ptr(), qs, h, softmax_scale,
                                      1 if causal else 0, window, out.data_ptr(), os,

@@ -545,8 +545,10 @@ static bool attn_sizes_ok(int64_t batch, int64_t total_q, int64_t q_heads, int64
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return false;
   // query rows and work items are counted in 32 bits
   return max_q * (q_heads / heads) < (int64_t(1) << 30) && total_q * q_heads < (int64_t(1) << 30) &&
-         batch * heads < (int64_t(1) << 30);
+         batch * heads < (int64_t(1) << 30) &&
+         ql::attn4_launchable(batch, total_q, q_heads / heads, heads, head_dim, max_q);
 }
+static constexpr float kLog2e = 1.4426950408889634f;
 
 size_t qlinear_attention_nvfp4_workspace(int32_t batch, int64_t total_q, int32_t q_heads, int32_t heads,
                                          int32_t head_dim, int32_t max_q_len) {
@@ -564,10 +566,12 @@ qlinear_status qlinear_attention_nvfp4(const qlinear_kv_nvfp4* cache, const qlin
   if (!seqs || !q || !out || !seqs->kv_lens || !seqs->page_table) return QL_ERR_NULL;
   if (!attn_sizes_ok(seqs->batch, seqs->total_q, q_heads, c.heads, c.head_dim, seqs->max_q_len)) return QL_ERR_SHAPE;
   if (!seqs->q_starts && seqs->total_q != (int64_t)seqs->batch * seqs->max_q_len) return QL_ERR_SHAPE;
-  if (seqs->table_stride <= 0 || seqs->table_stride >= (int64_t(1) << 30) / cache->page_size) return QL_ERR_SHAPE;
+  if (seqs->table_pages <= 0 || seqs->table_pages >= (int64_t(1) << 30) / cache->page_size ||
+      seqs->table_stride < seqs->table_pages || !elems_ok(seqs->batch, seqs->table_stride))
+    return QL_ERR_SHAPE;
   const int64_t width = (int64_t)q_heads * c.head_dim;
   if (!rows_ok(seqs->total_q, q_stride, width) || !rows_ok(seqs->total_q, out_stride, width)) return QL_ERR_SHAPE;
-  if (window < 0 || (window > 0 && !causal) || !__builtin_isfinite(softmax_scale)) return QL_ERR_ARG;
+  if (window < 0 || (window > 0 && !causal) || !__builtin_isfinite(softmax_scale * kLog2e)) return QL_ERR_ARG;
   if (!aligned16(q) || !aligned16(out) || (lse && ((uintptr_t)lse & 3)) || ((uintptr_t)seqs->kv_lens & 3) ||
       ((uintptr_t)seqs->page_table & 3) || ((uintptr_t)seqs->q_starts & 3))
     return QL_ERR_ALIGN;
@@ -591,9 +595,10 @@ qlinear_status qlinear_attention_nvfp4(const qlinear_kv_nvfp4* cache, const qlin
   a.kv_lens = seqs->kv_lens;
   a.table = seqs->page_table;
   a.table_stride = seqs->table_stride;
-  a.scale_log2e = softmax_scale * 1.4426950408889634f;
+  a.table_pages = seqs->table_pages;
+  a.scale_log2e = softmax_scale * kLog2e;
   a.causal = causal != 0;
-  a.window = window;
+  a.window = window < (1 << 30) ? window : 1 << 30;   // no position passes 2^30: positions less a window stay in 32 bits
   a.out = out;
   a.out_stride = out_stride;
   a.lse = lse;

@@ -38,7 +38,7 @@ __device__ __forceinline__ AttnRange attn_range(const Attn4& a, int b) {
   AttnRange r;
   r.bad = false;
   int64_t n = a.kv_lens[b];
-  const int64_t room = a.table_stride << a.page_shift;
+  const int64_t room = a.table_pages << a.page_shift;
   if (n < 0 || n > room) {
     r.bad = true;
     n = n < 0 ? 0 : room;
@@ -931,32 +931,27 @@ __device__ __forceinline__ void prompt_values(PromptShared<D>& sh, int buf, int 
 
 // Unit `id`: (sequence, row tile, head), a sequence's last tiles first (they see the most).
 template <int D>
-__device__ __forceinline__ bool prompt_unit(const Attn4& a, int id, int& b, int& tile, int& h) {
+__device__ __forceinline__ bool prompt_unit(const Attn4& a, uint32_t id, int& b, int& tile, int& h) {
   const int lane = threadIdx.x & 63;
-  int before = 0;
+  uint32_t before = 0;   // (of q_starts that do not rise the sum may pass 32 bits: see below)
   bool found = false;
   for (int b0 = 0; b0 < a.batch && !found; b0 += 64) {
     AttnRange r{0, 0, 0, false};
     if (b0 + lane < a.batch) r = attn_range(a, b0 + lane);
     const int rows = r.nq * a.group;
     const int tiles = rows > a.few ? (rows + prompt_rows(D) - 1) / prompt_rows(D) : 0;
-    int upto = tiles * a.heads;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int x = __shfl_up(upto, o);
-      if (lane >= o) upto += x;
-    }
+    const uint32_t mine = (uint32_t)tiles * (uint32_t)a.heads, upto = wave_scan(mine);
     const uint64_t past = __ballot(before + upto > id);
     if (past) {
       const int j = __builtin_ctzll(past);
-      const int nt = __builtin_amdgcn_readlane(tiles, j);
-      const int at = id - before - (__builtin_amdgcn_readlane(upto, j) - nt * a.heads);
+      const uint32_t all = of_lane(mine, j), at = id - before - (of_lane(upto, j) - all);
+      if (at >= all) return false;
       b = b0 + j;
-      tile = __builtin_amdgcn_readfirstlane(nt - 1 - at / a.heads);
-      h = __builtin_amdgcn_readfirstlane(at % a.heads);
+      tile = (int)((all - 1 - at) / (uint32_t)a.heads);
+      h = (int)(at % (uint32_t)a.heads);
       found = true;
     }
-    before += __builtin_amdgcn_readlane(upto, 63);
+    before += of_lane(upto, 63);
   }
   return found;
 }
@@ -987,7 +982,7 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
   const int n32 = lane & 31, half = lane >> 5;
 
   int b, tile, h;
-  if (!prompt_unit<D>(a, (int)blockIdx.x / a.parts_each, b, tile, h)) return;
+  if (!prompt_unit<D>(a, blockIdx.x / a.parts_each, b, tile, h)) return;
   const AttnRange rg = attn_range_uniform(a, b);
   if (rg.bad && h == 0 && threadIdx.x == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
   const int rows = rg.nq * a.group;
@@ -1288,6 +1283,11 @@ static_assert(attn_wgs(64) * 4 + kWsCounterOff <= kWsReserved, "one counter a wo
 // sequences out.
 constexpr int kFewRows = 64;
 
+// The prompt kernel's grid: 2^22 units of up to 512 threads.
+bool attn4_launchable(int64_t batch, int64_t total_q, int64_t group, int64_t heads, int head_dim, int64_t max_q) {
+  return max_q * group <= kFewRows || prompt_units(total_q, batch, group, heads, head_dim) <= (int64_t)1 << 22;
+}
+
 size_t attn4_scratch_bytes(int64_t batch, int64_t total_q, int64_t group, int64_t heads, int head_dim, int64_t max_q) {
   const size_t few = (size_t)2 * attn_wgs(head_dim) * 16 * (head_dim + 2) * 4;
   if (max_q * group <= kFewRows) return few;
@@ -1305,9 +1305,10 @@ constexpr int kJoinParts = 48;
 template <int D, int R>
 static hipError_t launch_r(const Attn4& call, hipStream_t s) {
   Attn4 a = call;
-  const int64_t tiles = ((int64_t)a.max_q * a.group + R - 1) / R, units = tiles * a.heads * a.batch;
-  a.join = units * kJoinParts <= attn_wgs(D) && (a.table_stride << a.page_shift) >= kJoinParts * kAttnChunk;
-  const int64_t chunks = (a.table_stride << a.page_shift) / kAttnChunk + 1 + kUnitCost;   // < 2^25
+  const int64_t rows = min((int64_t)a.max_q * a.group, (int64_t)kFewRows);   // of a sequence here
+  const int64_t tiles = (rows + R - 1) / R, units = tiles * a.heads * a.batch;
+  a.join = units * kJoinParts <= attn_wgs(D) && (a.table_pages << a.page_shift) >= kJoinParts * kAttnChunk;
+  const int64_t chunks = (a.table_pages << a.page_shift) / kAttnChunk + 1 + kUnitCost;   // < 2^25
   a.wide = units > (int64_t)INT32_MAX / chunks;
   attn4_kernel<D, R><<<attn_wgs(D), kAttnWaves * 64, 0, s>>>(a);
   if (a.join) attn4_join_kernel<D, R><<<(unsigned)(units * R), 256, 0, s>>>(a, (int)tiles);
@@ -1319,9 +1320,8 @@ static hipError_t launch_prompt(const Attn4& call, hipStream_t s) {
   Attn4 a = call;
   const int64_t units = prompt_units(a.total_q, a.batch, a.group, a.heads, D);
   // (no more than the longest sequence that the table holds can have)
-  const int64_t most = (a.table_stride << a.page_shift) / (kPrTok * kPrPartTiles);
+  const int64_t most = (a.table_pages << a.page_shift) / (kPrTok * kPrPartTiles);
   a.parts_each = (int)max((int64_t)1, min((int64_t)prompt_parts(units, D), most));
-  if (units * a.parts_each > (int64_t)INT32_MAX || units * prompt_rows(D) > (int64_t)INT32_MAX) return hipErrorInvalidValue;
   const size_t lds = sizeof(PromptShared<D>);
   const hipError_t e = hipFuncSetAttribute((const void*)attn4_prompt_kernel<D>,
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);

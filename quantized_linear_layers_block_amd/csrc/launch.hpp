@@ -85,7 +85,7 @@ struct Attn4 {
   const int32_t* q_starts;  // null: max_q query tokens in every sequence
   const int32_t* kv_lens;
   const int32_t* table;
-  int64_t table_stride;
+  int64_t table_stride, table_pages;
   float scale_log2e;
   int causal, window;
   uint16_t* out;
@@ -100,6 +100,7 @@ struct Attn4 {
   int wide;                 // positions in the call's work may pass 32 bits
   int parts_each;           // most parts of a unit of the prompt kernel
 };
+bool attn4_launchable(int64_t batch, int64_t total_q, int64_t group, int64_t heads, int head_dim, int64_t max_q);
 size_t attn4_scratch_bytes(int64_t batch, int64_t total_q, int64_t group, int64_t heads, int head_dim, int64_t max_q);
 hipError_t launch_attn4(const Attn4& a, int head_dim, hipStream_t s);
 

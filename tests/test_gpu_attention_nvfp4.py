@@ -150,18 +150,22 @@ def test_cuts_of_the_work(batch, n, hq, h, d):
     s.check(*s.run(window=n // 3), window=n // 3)
 
 
+@pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 1])
+def test_largest_windows_with_more_queries_than_keys(window):
+    for lens in ([(5, 3), (5, 40)], [(100, 60), (70, 0), (90, 200)]):
+        s = Seqs(lens, 4, 2, 128, 16, 9)
+        s.check(*s.run(window=window), window=window)
+
+
 def test_bounds_that_pass_32_bits():
-    """A table of 2^24 tokens a sequence and a large max_q_len: the work could pass 2^31 chunks, and
-    the positions in it are kept in 64 bits.  The same answers as from the narrow call."""
-    s = Seqs([(1, 900), (2, 77), (0, 5), (1, 3000)], 16, 8, 128, 256, 1)
-    starts, out, lse = torch.from_numpy(s.starts).to(DEV), [], []
+    """A table of 2^24 tokens a sequence for 300 sequences of 8 heads: the work could pass 2^31
+    chunks, and the positions in it are kept in 64 bits."""
+    lens = [(1, 900), (2, 77), (0, 5), (1, 3000)]
+    s = Seqs(lens + [(0, 0)] * 295 + [(3, 300)], 16, 8, 128, 256, 1)
     wide = torch.full((len(s.lens), 1 << 16), -1, dtype=torch.int32, device=DEV)
     wide[:, :s.pt.shape[1]] = s.pt
-    for table, max_q in ((s.pt, 4), (wide, 16384)):
-        out.append(torch.full_like(s.q, 7.0))
-        lse.append(torch.full((s.tq, s.hq), 7.0, dtype=torch.float32, device=DEV))
-        ql.attention_nvfp4(s.q, s.cache, table, s.kv_lens, q_starts=starts, max_q_len=max_q, out=out[-1], lse=lse[-1])
-        s.check(out[-1], lse[-1])
+    for s.pt, s.max_q in ((s.pt, 4), (wide, 4), (wide, 16384)):
+        s.check(*s.run())
 
 
 def test_one_row_tile_and_decode_rows_agree():

@@ -49,9 +49,9 @@ def test_attention_errors():
     need = b.qlinear_attention_nvfp4_workspace(2, 2, 32, 8, 128, 1)
     assert need >= b.QLINEAR_WS_RESERVED_BYTES
 
-    def at(cache=_cache(), batch=2, mq=1, tq=2, starts=None, lens=FAKE, table=FAKE, ts=5, q=FAKE, qs=4096, hq=32,
+    def at(cache=_cache(), batch=2, mq=1, tq=2, starts=None, lens=FAKE, table=FAKE, ts=5, tp=5, q=FAKE, qs=4096, hq=32,
            scale=0.1, causal=1, window=0, out=FAKE, os=4096, lse=None, ws=FAKE, wsb=1 << 40):
-        seqs = b.AttnBatch(batch, mq, tq, starts, lens, table, ts)
+        seqs = b.AttnBatch(batch, mq, tq, starts, lens, table, ts, tp)
         return L.qlinear_attention_nvfp4(ctypes.byref(cache), ctypes.byref(seqs), q, qs, hq, scale, causal, window, out,
                                          os, lse, ws, wsb, None)
 
@@ -63,10 +63,14 @@ def test_attention_errors():
     assert at(mq=0, tq=0) == b.QL_ERR_SHAPE and at(tq=3) == b.QL_ERR_SHAPE
     assert at(hq=30) == b.QL_ERR_SHAPE and at(hq=0) == b.QL_ERR_SHAPE
     assert at(mq=1 << 25, starts=FAKE) == b.QL_ERR_SHAPE
-    assert at(ts=0) == b.QL_ERR_SHAPE and at(ts=1 << 24) == b.QL_ERR_SHAPE
+    assert at(tp=0) == b.QL_ERR_SHAPE and at(ts=1 << 24, tp=1 << 24) == b.QL_ERR_SHAPE
+    assert at(ts=4) == b.QL_ERR_SHAPE and at(ts=0) == b.QL_ERR_SHAPE   # rows that overlap
+    assert at(ts=1 << 60) == b.QL_ERR_SHAPE
+    assert at(_cache(heads=512), batch=16384, mq=65, tq=16384 * 65, hq=512, qs=65536, os=65536) == b.QL_ERR_SHAPE   # launch
     assert at(qs=4088) == b.QL_ERR_SHAPE and at(os=4100) == b.QL_ERR_SHAPE
     assert at(window=-1) == b.QL_ERR_ARG and at(window=5, causal=0) == b.QL_ERR_ARG
     assert at(scale=float("inf")) == b.QL_ERR_ARG and at(scale=float("nan")) == b.QL_ERR_ARG
+    assert at(scale=3e38) == b.QL_ERR_ARG   # finite, but not times log2(e)
     assert at(q=FAKE + 8) == b.QL_ERR_ALIGN and at(out=FAKE + 2) == b.QL_ERR_ALIGN and at(lse=FAKE + 2) == b.QL_ERR_ALIGN
     assert at(starts=FAKE + 2) == b.QL_ERR_ALIGN and at(table=FAKE + 1) == b.QL_ERR_ALIGN
     assert at(ws=None) == b.QL_ERR_WORKSPACE and at(wsb=need - 1) == b.QL_ERR_WORKSPACE
