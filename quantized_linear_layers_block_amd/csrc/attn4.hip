@@ -190,6 +190,18 @@ __device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
   }
   return v;
 }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {  // of all in the last lane
+  v = dpp_max<0x111, 0xF>(v);
+  v = dpp_max<0x112, 0xF>(v);
+  v = dpp_max<0x114, 0xF>(v);
+  v = dpp_max<0x118, 0xF>(v);
+  v = dpp_max<0x142, 0xA>(v);
+  return dpp_max<0x143, 0xC>(v);
+}
 __device__ __forceinline__ uint32_t of_lane(uint32_t v, int j) { return (uint32_t)__builtin_amdgcn_readlane((int)v, j); }
 __device__ __forceinline__ uint64_t of_lane(uint64_t v, int j) {
   return ((uint64_t)of_lane((uint32_t)(v >> 32), j) << 32) | of_lane((uint32_t)v, j);
@@ -847,9 +859,11 @@ constexpr int kPrTok = 64, kPrGroups = kPrTok / 16;
 constexpr int prompt_waves(int d) { return d == 128 ? 8 : 4; }
 constexpr int prompt_wgs_per_cu(int d) { return d == 64 ? 3 : 1; }
 constexpr int prompt_rows(int d) { return 32 * prompt_waves(d); }
-// Where the units leave CUs idle they are cut along the tokens, each into the same number of parts at
-// most (two rounds of workgroups), of kPrPartTiles tiles at least; a kernel of its own joins them.
-constexpr int kPrPartTiles = 16;
+// Where the units leave CUs idle they are cut along the tokens (PromptCut), into as many parts as two
+// rounds of workgroups hold at most; a kernel of its own joins them.  28/4 heads at D = 128, 512
+// queries behind 2048 tokens: 44 us, 74 uncut; behind 4096: 61.  Not worth its launch where no
+// sequence can have kPrCutFrom tokens.
+constexpr int kPrPartTiles = 4, kPrCutFrom = 1024;
 int64_t prompt_units(int64_t total_q, int64_t batch, int64_t group, int64_t heads, int d) {
   return (total_q * group / prompt_rows(d) + batch) * heads;   // at most one tile a sequence more
 }
@@ -929,36 +943,56 @@ __device__ __forceinline__ void prompt_values(PromptShared<D>& sh, int buf, int 
   if (lane == 0) sh.vf[buf][grp] = make_float2((float)(int)top - 127.0f, __uint_as_float((245u - top) << 23));
 }
 
-// Unit `id`: (sequence, row tile, head), a sequence's last tiles first (they see the most).
+// Unit `id`: (sequence, row tile, head), those that see the most tokens first, so that the last
+// to start are the shortest (4 x 1024 causal, 32/8 heads: 55 us, 77 in the order of the sequences).  A
+// tile's key is its sequence's context in row tiles less the tiles behind it: each wave finds the
+// key T with fewer than `id` units above it by bisection, 64 sequences at a time.
 template <int D>
 __device__ __forceinline__ bool prompt_unit(const Attn4& a, uint32_t id, int& b, int& tile, int& h) {
   const int lane = threadIdx.x & 63;
-  uint32_t before = 0;   // (of q_starts that do not rise the sum may pass 32 bits: see below)
-  bool found = false;
-  for (int b0 = 0; b0 < a.batch && !found; b0 += 64) {
+  const uint32_t heads = (uint32_t)a.heads;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
     AttnRange r{0, 0, 0, false};
     if (b0 + lane < a.batch) r = attn_range(a, b0 + lane);
     const int rows = r.nq * a.group;
     const int tiles = rows > a.few ? (rows + prompt_rows(D) - 1) / prompt_rows(D) : 0;
-    const uint32_t mine = (uint32_t)tiles * (uint32_t)a.heads, upto = wave_scan(mine);
-    const uint64_t past = __ballot(before + upto > id);
-    if (past) {
-      const int j = __builtin_ctzll(past);
-      const uint32_t all = of_lane(mine, j), at = id - before - (of_lane(upto, j) - all);
-      if (at >= all) return false;
-      b = b0 + j;
-      tile = (int)((all - 1 - at) / (uint32_t)a.heads);
-      h = (int)(at % (uint32_t)a.heads);
-      found = true;
+    // (of q_starts that do not rise the sums may pass 32 bits: what is found then is checked below)
+    const uint32_t all = of_lane(wave_scan((uint32_t)tiles * heads), 63);
+    if (id >= all) {
+      id -= all;
+      continue;
     }
-    before += of_lane(upto, 63);
+    const int key = max((int)min((int64_t)r.n * a.group / prompt_rows(D), (int64_t)1 << 30), tiles);   // of the last tile; >= 1 of the first
+    const uint64_t with = __ballot(tiles > 0);
+    if ((with & (with - 1)) == 0) {   // one sequence
+      const int j = __builtin_ctzll(with);
+      b = b0 + j;
+      tile = __builtin_amdgcn_readlane(tiles, j) - 1 - (int)(id / heads);
+      h = (int)(id % heads);
+      return true;
+    }
+    const auto above = [&](int t) { return of_lane(wave_scan((uint32_t)min(max(key - t, 0), tiles) * heads), 63); };
+    int lo = 0, hi = (int)of_lane(wave_max((uint32_t)(tiles ? key : 0)), 63);   // above(hi) = 0 <= id < above(lo)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      (above(mid) > id ? lo : hi) = mid;
+    }
+    id -= above(hi);
+    uint64_t at = __ballot(key - hi >= 0 && key - hi < tiles);   // sequences with a tile of the key hi
+    for (uint32_t skip = id / heads; skip && at; --skip) at &= at - 1;
+    if (!at) return false;
+    const int j = __builtin_ctzll(at);
+    b = b0 + j;
+    tile = __builtin_amdgcn_readlane(tiles, j) - 1 - (__builtin_amdgcn_readlane(key, j) - hi);
+    h = (int)(id % heads);
+    return true;
   }
-  return found;
+  return false;
 }
 
-// Tiles of 64 tokens that some row of the unit sees, from `first` on, and the parts they are cut into.
+// Tiles of 64 tokens that some row of the unit sees, from `first` on.
 struct PromptTiles {
-  int begin, stop, first, tiles, parts;
+  int begin, stop, first, tiles;
 };
 template <int D>
 __device__ __forceinline__ PromptTiles prompt_tiles(const Attn4& a, const AttnRange& rg, int tile) {
@@ -969,8 +1003,44 @@ __device__ __forceinline__ PromptTiles prompt_tiles(const Attn4& a, const AttnRa
   t.begin = a.window ? max(rg.n - rg.nq + qa + 1 - a.window, 0) : 0;
   t.first = t.begin & ~(kPrTok - 1);
   t.tiles = t.stop > t.first ? (t.stop - t.first + kPrTok - 1) / kPrTok : 0;
-  t.parts = min(max(t.tiles / kPrPartTiles, 1), a.parts_each);
   return t;
+}
+
+// How the units are cut: their number, and the tiles of a part.  Parts of `each` tiles are no more
+// than sum / each + units together; `each` is taken so that they fit one round of workgroups or
+// two, whichever ends sooner, where a workgroup's start takes the time of two or three tiles.
+// (a.parts_each > 1 only for few units: the sums stay in 32 bits.)
+struct PromptCut {
+  uint32_t units, each;
+  __device__ __forceinline__ int parts(const Attn4& a, int tiles) const {
+    return min(max((int)(((uint32_t)tiles + each - 1) / each), 1), a.parts_each);
+  }
+};
+template <int D>
+__device__ __forceinline__ PromptCut prompt_cut(const Attn4& a) {
+  const int lane = threadIdx.x & 63;
+  uint32_t sum = 0, units = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    if (b0 + lane >= a.batch) continue;
+    const AttnRange r = attn_range(a, b0 + lane);
+    const int rows = r.nq * a.group;
+    if (rows <= a.few || rows == 0) continue;
+    const int n = (rows + prompt_rows(D) - 1) / prompt_rows(D);
+    const int ends = prompt_tiles<D>(a, r, 0).tiles + prompt_tiles<D>(a, r, n - 1).tiles;
+    units += (uint32_t)n * (uint32_t)a.heads;
+    sum += (uint32_t)min(ends, 1 << 21) * (uint32_t)n * (uint32_t)a.heads;   // twice the tiles, about
+  }
+  constexpr uint32_t kSlots = 256 * prompt_wgs_per_cu(D);
+  sum = of_lane(wave_scan(sum), 63) / 2;
+  PromptCut c;
+  c.units = max(of_lane(wave_scan(units), 63), 1u);
+  c.each = sum / max(2 * kSlots - min(c.units, 2 * kSlots), 1u) + 1;
+  if (c.units < kSlots) {
+    const uint32_t one = sum / (kSlots - c.units) + 1;
+    if (one <= 2 * c.each + 2) c.each = one;
+  }
+  c.each = (uint32_t)__builtin_amdgcn_readfirstlane((int)max(c.each, (uint32_t)kPrPartTiles));
+  return c;
 }
 
 template <int D>
@@ -982,7 +1052,17 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
   const int n32 = lane & 31, half = lane >> 5;
 
   int b, tile, h;
-  if (!prompt_unit<D>(a, blockIdx.x / a.parts_each, b, tile, h)) return;
+  // the units' first parts, their second ones, ..: workgroups without work come last (between the
+  // others, some CUs got two of those while some got none)
+  PromptCut cut{1, 1};
+  uint32_t unit = blockIdx.x, part = 0;
+  if (a.parts_each > 1) {
+    cut = prompt_cut<D>(a);
+    part = (uint32_t)__builtin_amdgcn_readfirstlane((int)(unit / cut.units));
+    unit -= part * cut.units;
+    if (part >= (uint32_t)a.parts_each) return;
+  }
+  if (!prompt_unit<D>(a, unit, b, tile, h)) return;
   const AttnRange rg = attn_range_uniform(a, b);
   if (rg.bad && h == 0 && threadIdx.x == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
   const int rows = rg.nq * a.group;
@@ -991,9 +1071,10 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
   const int qa = r0 / a.group, ra = r0 - qa * a.group;
   // this part's tiles and the tokens in them that some row of the workgroup sees
   const PromptTiles pt = prompt_tiles<D>(a, rg, tile);
-  const int part = (int)blockIdx.x % a.parts_each;
-  if (part >= pt.parts) return;
-  const int x0 = (int)((int64_t)pt.tiles * part / pt.parts), tiles = (int)((int64_t)pt.tiles * (part + 1) / pt.parts) - x0;
+  const int parts = __builtin_amdgcn_readfirstlane(cut.parts(a, pt.tiles));
+  if ((int)part >= parts) return;
+  const int x0 = __builtin_amdgcn_readfirstlane((int)((int64_t)pt.tiles * part / parts));
+  const int tiles = __builtin_amdgcn_readfirstlane((int)((int64_t)pt.tiles * (part + 1) / parts)) - x0;
   const int first = pt.first + x0 * kPrTok;
   const int begin = max(pt.begin, first), stop = min(pt.stop, first + tiles * kPrTok);
 
@@ -1208,8 +1289,8 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
 
   l += __shfl_xor(l, 32);
   if (wr + n32 >= tile_live) return;
-  if (pt.parts > 1) {   // this part's sums and their maximum, for the joining kernel
-    float* to_part = (float*)(a.parts + (size_t)blockIdx.x * prompt_part_bytes(D));
+  if (parts > 1) {   // this part's sums and their maximum, for the joining kernel
+    float* to_part = (float*)(a.parts + ((size_t)unit * a.parts_each + part) * prompt_part_bytes(D));
     const int r = wr + n32;
 #pragma unroll
     for (int j = 0; j < DT; ++j)
@@ -1252,15 +1333,16 @@ __global__ __launch_bounds__(256) void attn4_prompt_join_kernel(Attn4 a) {
   const PromptTiles pt = prompt_tiles<D>(a, rg, tile);
   const int r = (int)blockIdx.x % kWgs * kRowsWg + (int)threadIdx.x / kPer, part = (int)threadIdx.x % kPer;
   const int row = tile * ROWS + r;
-  if (pt.parts < 2 || row >= rg.nq * a.group) return;
+  const int parts = prompt_cut<D>(a).parts(a, pt.tiles);
+  if (parts < 2 || row >= rg.nq * a.group) return;
   const float* from = (const float*)(a.parts + (size_t)unit * a.parts_each * prompt_part_bytes(D));
   constexpr size_t kStep = prompt_part_bytes(D) / 4;
   float top = kNoMax;
-  for (int s = 0; s < pt.parts; ++s) top = __builtin_fmaxf(top, from[s * kStep + ROWS * D + r]);
+  for (int s = 0; s < parts; ++s) top = __builtin_fmaxf(top, from[s * kStep + ROWS * D + r]);
   f32x4 acc{0, 0, 0, 0};
   float l = 0.0f;
 #pragma unroll 4
-  for (int s = 0; s < pt.parts; ++s) {
+  for (int s = 0; s < parts; ++s) {
     const float w = __builtin_exp2f(from[s * kStep + ROWS * D + r] - top);
     l = __builtin_fmaf(w, from[s * kStep + ROWS * D + ROWS + r], l);
     const f32x4 v = *(const f32x4*)(from + s * kStep + r * D + part * 4);
@@ -1320,8 +1402,8 @@ static hipError_t launch_prompt(const Attn4& call, hipStream_t s) {
   Attn4 a = call;
   const int64_t units = prompt_units(a.total_q, a.batch, a.group, a.heads, D);
   // (no more than the longest sequence that the table holds can have)
-  const int64_t most = (a.table_pages << a.page_shift) / (kPrTok * kPrPartTiles);
-  a.parts_each = (int)max((int64_t)1, min((int64_t)prompt_parts(units, D), most));
+  const int64_t room = a.table_pages << a.page_shift;
+  a.parts_each = room < kPrCutFrom ? 1 : (int)min((int64_t)prompt_parts(units, D), room / (kPrTok * kPrPartTiles));
   const size_t lds = sizeof(PromptShared<D>);
   const hipError_t e = hipFuncSetAttribute((const void*)attn4_prompt_kernel<D>,
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);

@@ -168,6 +168,16 @@ def test_bounds_that_pass_32_bits():
         s.check(*s.run())
 
 
+@pytest.mark.parametrize("hq,h,d", [(1, 1, 64), (2, 2, 128)])
+def test_prompts_of_many_sequences(hq, h, d):
+    """Over 64 sequences, of all lengths: the units' order and the cuts along the tokens."""
+    g = np.random.default_rng(d)
+    lens = [(int(q), int(q + c)) for q, c in zip(g.integers(60, 300, 70), g.integers(0, 1500, 70))]
+    s = Seqs(lens, hq, h, d, 64, d)
+    s.check(*s.run(), rows=4)
+    s.check(*s.run(window=400), window=400, rows=2)
+
+
 def test_one_row_tile_and_decode_rows_agree():
     """The same queries as 64 rows and as 65 (the few-row kernel and the prompt kernel)."""
     for d in (64, 128, 256):
