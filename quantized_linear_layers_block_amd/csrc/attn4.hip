@@ -863,7 +863,7 @@ constexpr int prompt_rows(int d) { return 32 * prompt_waves(d); }
 // rounds of workgroups hold at most; a kernel of its own joins them.  28/4 heads at D = 128, 512
 // queries behind 2048 tokens: 44 us, 74 uncut; behind 4096: 61.  Not worth its launch where no
 // sequence can have kPrCutFrom tokens.
-constexpr int kPrPartTiles = 4, kPrCutFrom = 1024;
+constexpr int kPrPartTiles = 4, kPrCutFrom = 768, kPrJoinRows = 4;
 int64_t prompt_units(int64_t total_q, int64_t batch, int64_t group, int64_t heads, int d) {
   return (total_q * group / prompt_rows(d) + batch) * heads;   // at most one tile a sequence more
 }
@@ -1006,10 +1006,11 @@ __device__ __forceinline__ PromptTiles prompt_tiles(const Attn4& a, const AttnRa
   return t;
 }
 
-// How the units are cut: their number, and the tiles of a part.  Parts of `each` tiles are no more
-// than sum / each + units together; `each` is taken so that they fit one round of workgroups or
-// two, whichever ends sooner, where a workgroup's start takes the time of two or three tiles.
-// (a.parts_each > 1 only for few units: the sums stay in 32 bits.)
+// How the units are cut: their number, and the tiles of a part.  Parts of `each` tiles are to fit one
+// round of workgroups or two: of units all alike as many each as fit, of others no more than
+// sum / each + units together.  The cut is taken that ends first, where a workgroup's start takes
+// the time of two or three tiles and the joining that of two; or none.
+// (a.parts_each > 1 only for few units, which fit one round uncut: the sums stay in 32 bits.)
 struct PromptCut {
   uint32_t units, each;
   __device__ __forceinline__ int parts(const Attn4& a, int tiles) const {
@@ -1019,27 +1020,40 @@ struct PromptCut {
 template <int D>
 __device__ __forceinline__ PromptCut prompt_cut(const Attn4& a) {
   const int lane = threadIdx.x & 63;
-  uint32_t sum = 0, units = 0;
+  uint32_t sum = 0, units = 0, most = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
     if (b0 + lane >= a.batch) continue;
     const AttnRange r = attn_range(a, b0 + lane);
     const int rows = r.nq * a.group;
     if (rows <= a.few || rows == 0) continue;
     const int n = (rows + prompt_rows(D) - 1) / prompt_rows(D);
-    const int ends = prompt_tiles<D>(a, r, 0).tiles + prompt_tiles<D>(a, r, n - 1).tiles;
+    const uint32_t t0 = min(prompt_tiles<D>(a, r, 0).tiles, 1 << 20), t1 = min(prompt_tiles<D>(a, r, n - 1).tiles, 1 << 20);
+    most = umax(most, umax(t0, t1));
     units += (uint32_t)n * (uint32_t)a.heads;
-    sum += (uint32_t)min(ends, 1 << 21) * (uint32_t)n * (uint32_t)a.heads;   // twice the tiles, about
+    sum += (t0 + t1) * (uint32_t)n * (uint32_t)a.heads;   // twice the tiles, about
   }
   constexpr uint32_t kSlots = 256 * prompt_wgs_per_cu(D);
   sum = of_lane(wave_scan(sum), 63) / 2;
+  most = of_lane(wave_max(most), 63);
   PromptCut c;
   c.units = max(of_lane(wave_scan(units), 63), 1u);
-  c.each = sum / max(2 * kSlots - min(c.units, 2 * kSlots), 1u) + 1;
-  if (c.units < kSlots) {
-    const uint32_t one = sum / (kSlots - c.units) + 1;
-    if (one <= 2 * c.each + 2) c.each = one;
+  c.each = max(most, 1u);
+  uint32_t best = c.each;   // the time in tiles beyond one start
+#pragma unroll
+  for (uint32_t k = 1; k <= 2; ++k) {
+    const uint32_t slots = k * kSlots;
+    if (c.units > slots) continue;
+    const uint32_t alike = slots / c.units;
+    uint32_t each = (most + alike - 1) / alike;
+    if (c.units < slots) each = min(each, sum / (slots - c.units) + 1);
+    each = max(each, (uint32_t)kPrPartTiles);
+    const uint32_t time = k * each + (5 * k - 5) / 2 + 2;
+    if (time < best) {
+      best = time;
+      c.each = each;
+    }
   }
-  c.each = (uint32_t)__builtin_amdgcn_readfirstlane((int)max(c.each, (uint32_t)kPrPartTiles));
+  c.each = (uint32_t)__builtin_amdgcn_readfirstlane((int)c.each);
   return c;
 }
 
@@ -1322,48 +1336,69 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
         l == 0.0f ? -__builtin_inff() : (__builtin_log2f(l) + m) * 0.6931471805599453f;
 }
 
-// Joins the parts of the prompt kernel's units: D / 4 threads a row.
+// Joins the parts of the prompt kernel's units: D / 4 threads a row, four rows each (finding the
+// unit takes as long as a row: 16 x 96 rows in two parts, 8 heads: 37 us, 46 with a row each).
 template <int D>
 __global__ __launch_bounds__(256) void attn4_prompt_join_kernel(Attn4 a) {
-  constexpr int kPer = D / 4, kRowsWg = 256 / kPer, kWgs = prompt_rows(D) / kRowsWg, ROWS = prompt_rows(D);
+  constexpr int kPer = D / 4, kSide = 256 / kPer, ROWS = prompt_rows(D), kWgs = ROWS / (kPrJoinRows * kSide);
   int b, tile, h;
   const int unit = (int)blockIdx.x / kWgs;
   if (!prompt_unit<D>(a, unit, b, tile, h)) return;
   const AttnRange rg = attn_range_uniform(a, b);
-  const PromptTiles pt = prompt_tiles<D>(a, rg, tile);
-  const int r = (int)blockIdx.x % kWgs * kRowsWg + (int)threadIdx.x / kPer, part = (int)threadIdx.x % kPer;
-  const int row = tile * ROWS + r;
-  const int parts = prompt_cut<D>(a).parts(a, pt.tiles);
-  if (parts < 2 || row >= rg.nq * a.group) return;
+  const int parts = prompt_cut<D>(a).parts(a, prompt_tiles<D>(a, rg, tile).tiles);
+  const int live = rg.nq * a.group - tile * ROWS;
+  const int r0 = (int)blockIdx.x % kWgs * (kPrJoinRows * kSide) + (int)threadIdx.x / kPer, part = (int)threadIdx.x % kPer;
+  if (parts < 2 || r0 >= live) return;
   const float* from = (const float*)(a.parts + (size_t)unit * a.parts_each * prompt_part_bytes(D));
   constexpr size_t kStep = prompt_part_bytes(D) / 4;
-  float top = kNoMax;
-  for (int s = 0; s < parts; ++s) top = __builtin_fmaxf(top, from[s * kStep + ROWS * D + r]);
-  f32x4 acc{0, 0, 0, 0};
-  float l = 0.0f;
-#pragma unroll 4
-  for (int s = 0; s < parts; ++s) {
-    const float w = __builtin_exp2f(from[s * kStep + ROWS * D + r] - top);
-    l = __builtin_fmaf(w, from[s * kStep + ROWS * D + ROWS + r], l);
-    const f32x4 v = *(const f32x4*)(from + s * kStep + r * D + part * 4);
+  float top[kPrJoinRows], l[kPrJoinRows];
+  f32x4 acc[kPrJoinRows];
+  int r[kPrJoinRows];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(w, v[e], acc[e]);
+  for (int i = 0; i < kPrJoinRows; ++i) {
+    r[i] = r0 + i * kSide < live ? r0 + i * kSide : r0;
+    top[i] = kNoMax;
+    l[i] = 0.0f;
+    acc[i] = f32x4{0, 0, 0, 0};
   }
-  const int oq = row / a.group, oh = h * a.group + row - oq * a.group;
-  const float inv = l == 0.0f ? 0.0f : 1.220703125e-4f / l;
-  *(uint2*)(a.out + (rg.q0 + oq) * a.out_stride + (int64_t)oh * D + part * 4) =
-      make_uint2(pack_bf16x2_rne(acc[0] * inv, acc[1] * inv), pack_bf16x2_rne(acc[2] * inv, acc[3] * inv));
-  if (a.lse && part == 0)
-    a.lse[(rg.q0 + oq) * a.q_heads + oh] =
-        l == 0.0f ? -__builtin_inff() : (__builtin_log2f(l) + top) * 0.6931471805599453f;
+#pragma unroll 2
+  for (int s = 0; s < parts; ++s)
+#pragma unroll
+    for (int i = 0; i < kPrJoinRows; ++i) top[i] = __builtin_fmaxf(top[i], from[s * kStep + ROWS * D + r[i]]);
+#pragma unroll 2
+  for (int s = 0; s < parts; ++s)
+#pragma unroll
+    for (int i = 0; i < kPrJoinRows; ++i) {
+      const float w = __builtin_exp2f(from[s * kStep + ROWS * D + r[i]] - top[i]);
+      l[i] = __builtin_fmaf(w, from[s * kStep + ROWS * D + ROWS + r[i]], l[i]);
+      const f32x4 v = *(const f32x4*)(from + s * kStep + r[i] * D + part * 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(w, v[e], acc[i][e]);
+    }
+#pragma unroll
+  for (int i = 0; i < kPrJoinRows; ++i) {
+    if (r0 + i * kSide >= live) return;
+    const int row = tile * ROWS + r[i], oq = row / a.group, oh = h * a.group + row - oq * a.group;
+    const float inv = l[i] == 0.0f ? 0.0f : 1.220703125e-4f / l[i];
+    *(uint2*)(a.out + (rg.q0 + oq) * a.out_stride + (int64_t)oh * D + part * 4) =
+        make_uint2(pack_bf16x2_rne(acc[i][0] * inv, acc[i][1] * inv), pack_bf16x2_rne(acc[i][2] * inv, acc[i][3] * inv));
+    if (a.lse && part == 0)
+      a.lse[(rg.q0 + oq) * a.q_heads + oh] =
+          l[i] == 0.0f ? -__builtin_inff() : (__builtin_log2f(l[i]) + top[i]) * 0.6931471805599453f;
+  }
 }
 
 static_assert(attn_wgs(64) * 4 + kWsCounterOff <= kWsReserved, "one counter a workgroup");
 
 // Sequences of more query rows a KV head than kFewRows take the prompt kernel, the others the
 // few-row one; where the lengths are on the device both are launched, and each leaves the other's
-// sequences out.
+// sequences out.  (32 sequences of 3000 tokens, 64/8 heads: 64 rows 50 us against 65 in the prompt kernel
+// at D = 64, 82 against 79 at D = 128, 127 against 210 at D = 256; 128 rows 92 against 67, 148 against 84,
+// 253 against 225.)  Up to twice the rows take the few-row kernel if the units are few enough: two
+// sequences of 1000 tokens and 128 rows, 16 us against 27 at D = 64, 17 against 31 at D = 128, 28 against
+// 73 at D = 256; eight of 8000 67 against 54, 101 against 105, 151 against 174.
 constexpr int kFewRows = 64;
+constexpr int few_units(int d) { return d == 256 ? 1024 : 384; }
 
 // The prompt kernel's grid: 2^22 units of up to 512 threads.
 bool attn4_launchable(int64_t batch, int64_t total_q, int64_t group, int64_t heads, int head_dim, int64_t max_q) {
@@ -1387,7 +1422,7 @@ constexpr int kJoinParts = 48;
 template <int D, int R>
 static hipError_t launch_r(const Attn4& call, hipStream_t s) {
   Attn4 a = call;
-  const int64_t rows = min((int64_t)a.max_q * a.group, (int64_t)kFewRows);   // of a sequence here
+  const int64_t rows = min((int64_t)a.max_q * a.group, (int64_t)a.few);   // of a sequence here
   const int64_t tiles = (rows + R - 1) / R, units = tiles * a.heads * a.batch;
   a.join = units * kJoinParts <= attn_wgs(D) && (a.table_pages << a.page_shift) >= kJoinParts * kAttnChunk;
   const int64_t chunks = (a.table_pages << a.page_shift) / kAttnChunk + 1 + kUnitCost;   // < 2^25
@@ -1410,7 +1445,7 @@ static hipError_t launch_prompt(const Attn4& call, hipStream_t s) {
   if (e != hipSuccess) return e;
   attn4_prompt_kernel<D><<<(unsigned)(units * a.parts_each), prompt_waves(D) * 64, lds, s>>>(a);
   if (a.parts_each > 1)
-    attn4_prompt_join_kernel<D><<<(unsigned)(units * (prompt_rows(D) * (D / 4) / 256)), 256, 0, s>>>(a);
+    attn4_prompt_join_kernel<D><<<(unsigned)(units * (prompt_rows(D) * (D / 4) / (256 * kPrJoinRows))), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -1420,7 +1455,8 @@ static hipError_t launch_d(const Attn4& call, hipStream_t s) {
   const int64_t most = (int64_t)a.max_q * a.group;
   a.few = INT32_MAX;
   if (most <= 8) return launch_r<D, 8>(a, s);
-  if (most <= kFewRows) return launch_r<D, 16>(a, s);
+  if (most <= kFewRows || (most <= 2 * kFewRows && (most + 15) / 16 * a.heads * a.batch <= few_units(D)))
+    return launch_r<D, 16>(a, s);
   a.few = a.q_starts ? kFewRows : 0;
   const hipError_t e = launch_prompt<D>(a, s);
   if (e != hipSuccess || !a.q_starts) return e;
