@@ -401,8 +401,8 @@ size_t qlinear_kv_nvfp4_bytes(int64_t pages, int32_t page_size, int32_t heads, i
  * strides in elements, multiples of 8 -- the k and v parts of a fused projection are taken
  * where they are -- into slots[t] (int64, device, distinct).  A token with an Inf or NaN in its
  * key or value row of a head becomes a NaN token of that head (key scales 0xFF, the rest of
- * both rows zero with e = 0): loads give NaN for both rows, and attention gives NaN to the query rows that see it; QLINEAR_STATUS_NONFINITE is
- * set in *status_word (if not NULL).  A slot outside the cache is skipped and sets
+ * both rows zero with e = 0): loads give NaN for both rows, attention gives NaN to the query
+ * rows that see it, and QLINEAR_STATUS_NONFINITE is set in *status_word (if not NULL).  A slot outside the cache is skipped and sets
  * QLINEAR_STATUS_BAD_ITEM.
  * Load: slots[t] -> k_out, v_out bf16 (same strides rule); either may be NULL.  A slot outside
  * the cache gives zeros and sets QLINEAR_STATUS_BAD_ITEM.  Values are exact, Inf where a held
@@ -447,8 +447,11 @@ typedef struct {
  * token gets zeros and lse -inf.  Query tokens of no sequence keep their out and lse.
  * Products are f16 x f16 with float32 sums: q is scaled by a power of two a row (exact but for
  * magnitudes below about 2^-29 of the row's largest), the cache's values are exact, and the
- * softmax weights are rounded to f16 (2^-11) before they meet the values.
- * Results are bitwise reproducible for the same arguments.
+ * softmax weights are rounded to f16 (2^-11) before they meet the values.  Sequences with more
+ * than 64 query rows a KV head (query tokens * q_heads / heads; up to 128 where the call is
+ * small) take a kernel that holds the keys and the values of 16 tokens relative to the largest
+ * of their row exponents: rows more than 2^18 below it are off by 2^-40 of it at most.
+ * Results are bitwise reproducible for the same arguments, also as a graph's replays.
  * Workspace: qlinear_attention_nvfp4_workspace(...) bytes with qlinear_forward's layout and
  * reuse rules (zero-filled before its first use; calls that share it must not overlap, which
  * includes replays of graphs captured on it).

@@ -161,6 +161,12 @@ __device__ __forceinline__ f16x2 both(_Float16 s) { return f16x2{s, s}; }
 // (sequence, row tile, head) make one line of chunks, of which each workgroup takes the same
 // length.  One round of workgroups fills the chip and all end together, whatever the lengths;
 // a unit that lies in more than one workgroup's part is joined from partial results.
+//
+// Decoding is bound by the cache's bytes: 256 sequences of up to 4096 tokens, 64/8 heads of 128, take
+// 131 us for 620 MB (4.7 TB/s; a large copy moves 5.2), where the same kernel with its loads alone
+// takes 129; 64 of them 54 us, 53 with the loads alone.  Pages in the order of memory in place of
+// scattered ones would give 116 and 45.  One sequence of 613 tokens, 8.7 us, is the latency of the
+// chain: cut, page, codes, joins in the workgroup and between workgroups.
 constexpr int kAttnStep = 32;                        // tokens of one wave's step
 constexpr int kAttnChunk = kAttnWaves * kAttnStep;   // of the workgroup's
 // Workgroups that fit the chip: 256 CUs and the waves a SIMD holds by the kernel's registers.
@@ -214,8 +220,9 @@ __device__ __forceinline__ int attn_lo(const Attn4& a, int nq, int n) {
 
 // How the line is cut.  A unit's start in a workgroup (its query rows, the first loads, the joins at
 // its end) takes as long as two or three chunks.  So, where that makes the shares hardly longer,
-// each unit gets whole workgroups: its stretch is filled up to a multiple of the share.  Else, where
-// the shares are long, a unit's stretch begins with `cost` places without a chunk.
+// each unit gets whole workgroups: its stretch is filled up to a multiple of the share (16 sequences of
+// 4096 tokens, 28/4 heads: 18.6 us, 22.7 without).  Else, where the shares are long, a unit's stretch
+// begins with `cost` places without a chunk (256 of up to 4096, 64/8 heads: 137 us, 148 without).
 struct AttnCut {
   uint64_t each;   // chunks a workgroup
   uint32_t cost;
@@ -236,8 +243,9 @@ struct AttnPlace {
   int done, turn;       // chunks behind it; when the waves' priority is lowered next
 };
 
-// Of the workgroups that share a CU the oldest is served first at every turn: they ended at 100, 114
-// and 146 us of a call whose work was cut equally.  So a wave that is ahead in its share gives way.
+// Of the workgroups that share a CU the oldest is served first at every turn: equal shares ended
+// after 90 to 146 us.  So a wave that is ahead gives way: its priority falls at a half, three
+// quarters and seven eighths of its share (256 sequences of up to 4096 tokens: 149 us, 158 without).
 __device__ __forceinline__ void attn_give_way(AttnPlace& pl, int each) {
   if (pl.turn < each / 2 + each / 4) {
     __builtin_amdgcn_s_setprio(2);
@@ -251,7 +259,7 @@ __device__ __forceinline__ void attn_give_way(AttnPlace& pl, int each) {
   }
 }
 
-// A sequence's chunks, and its stretch of the line (all tiles and heads).
+// A sequence's chunks, and its units (all tiles and heads).
 __device__ __forceinline__ uint32_t attn_chunks(const Attn4& a, const AttnRange& r) {
   return max((max(r.n - attn_lo(a, r.nq, r.n), 0) + kAttnChunk - 1) / kAttnChunk, 1);
 }
@@ -852,6 +860,12 @@ __global__ __launch_bounds__(256) void attn4_join_kernel(Attn4 a, int tiles) {
 // fused multiply-add with factors of its group, w = (acc kc 2^(E - 4)) + F, where a factor a
 // token would cost two more of some nine vector instructions a logit, and the vector
 // instructions (the exponential takes four of them) weigh as much as the matrix products.
+//
+// At D = 128 a prompt of 8192 tokens, 28/4 heads, takes 501 us (960 TFLOP/s of the products that are seen;
+// a library product reaches 1390), with the matrix units busy for 45% of the cycles and the vector
+// units for 50%.  More overlap lowers the clock instead (from 2.4 to 2.1 GHz and less, as the chip
+// nears its power): the products and exponentials of two tiles interleaved in a wave gave 903, waves
+// in two halves half a tile apart 920, tiles of 128 tokens 976, 64 rows a wave 703 TFLOP/s.
 constexpr int kPrTok = 64, kPrGroups = kPrTok / 16;
 // Waves of a workgroup, and workgroups of a CU: at D = 128 eight waves, two a SIMD; at D = 64 three
 // workgroups of four (40 sequences of up to 333 tokens in a window of 1024: 71 us against 88 with
@@ -944,7 +958,7 @@ __device__ __forceinline__ void prompt_values(PromptShared<D>& sh, int buf, int 
 }
 
 // Unit `id`: (sequence, row tile, head), those that see the most tokens first, so that the last
-// to start are the shortest (4 x 1024 causal, 32/8 heads: 55 us, 77 in the order of the sequences).  A
+// to start are the shortest (4 x 1024 causal, 32/8 heads: 64 us, 78 in the order of the sequences).  A
 // tile's key is its sequence's context in row tiles less the tiles behind it: each wave finds the
 // key T with fewer than `id` units above it by bisection, 64 sequences at a time.
 template <int D>

@@ -168,6 +168,13 @@ def test_bounds_that_pass_32_bits():
         s.check(*s.run())
 
 
+@pytest.mark.parametrize("nq,hq,h,d", [(12, 16, 2, 64), (16, 8, 1, 128), (9, 64, 8, 128), (65, 1, 1, 256)])
+def test_around_a_hundred_rows_a_head(nq, hq, h, d):
+    s = Seqs([(nq, n) for n in (nq, 40, 333, 1200)], hq, h, d, 32, nq)
+    s.check(*s.run())
+    s.check(*s.run(window=50), window=50)
+
+
 @pytest.mark.parametrize("hq,h,d", [(1, 1, 64), (2, 2, 128)])
 def test_prompts_of_many_sequences(hq, h, d):
     """Over 64 sequences, of all lengths: the units' order and the cuts along the tokens."""
