@@ -265,7 +265,7 @@ class KVCacheNVFP4:
 # Checks of the cache's calls.  A decode step makes several of them a layer, so they are few
 # attribute reads each; the messages are put together only when one fails.
 _BF16, _I32 = torch.bfloat16, torch.int32
-_device_now = torch.cuda.current_device
+_device_now = torch._C._cuda_getDevice   # (called where a tensor is on the GPU: it is initialised)
 
 
 def _refuse(device, dtype, name, t, what):
@@ -356,7 +356,8 @@ def attention_nvfp4(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None
         raise ValueError(f"q must be [tokens, heads, {cache.head_dim}]")
     shape = q.shape
     tq, hq, d = shape
-    _check_rows(dev, "q", q, shape)
+    if q.dtype is not _BF16 or q.device != dev or not q.is_contiguous():
+        _check_rows(dev, "q", q, shape)
     batch = kv_lens.shape[0]
     _check_dense(dev, _I32, "kv_lens", kv_lens, (batch,))
     if page_table.dtype is not _I32 or page_table.dim() != 2 or page_table.shape[0] != batch or \

@@ -174,7 +174,7 @@ def _stream_here():
     global _raw_stream
     if _raw_stream is None:
         import torch
-        _raw_stream = (torch._C._cuda_getCurrentRawStream, torch.cuda.current_device)
+        _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
     return _raw_stream[0](_raw_stream[1]())
 
 
