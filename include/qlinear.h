@@ -457,7 +457,8 @@ typedef struct {
  * includes replays of graphs captured on it).
  * From the device, in the workspace's status word as QLINEAR_STATUS_BAD_ITEM: a page number
  * outside the cache (its tokens are left out), kv_lens beyond the table or negative (cut), and
- * q_starts that do not fit total_q or max_q_len (the sequence is left out).
+ * q_starts that fall or do not fit total_q or max_q_len (the sequence is left out; where q_starts
+ * fall, sequences overlap and their tokens get the result of any of them, or none).
  * Errors: QL_ERR_NULL, QL_ERR_SHAPE (cache sizes; batch <= 0 or > QLINEAR_MAX_ATTN_BATCH;
  * max_q_len, total_q <= 0 or beyond QLINEAR_MAX_M; q_heads not a multiple of heads; total_q
  * other than batch * max_q_len without q_starts; table_pages <= 0 or 2^30 tokens and more a

@@ -1050,7 +1050,7 @@ __device__ __forceinline__ PromptCut prompt_cut(const Attn4& a) {
   sum = of_lane(wave_scan(sum), 63) / 2;
   most = of_lane(wave_max(most), 63);
   PromptCut c;
-  c.units = max(of_lane(wave_scan(units), 63), 1u);
+  c.units = min(max(of_lane(wave_scan(units), 63), 1u), (uint32_t)a.most_units);   // (q_starts may not rise)
   c.each = max(most, 1u);
   uint32_t best = c.each;   // the time in tiles beyond one start
 #pragma unroll
@@ -1452,6 +1452,7 @@ static hipError_t launch_prompt(const Attn4& call, hipStream_t s) {
   const int64_t units = prompt_units(a.total_q, a.batch, a.group, a.heads, D);
   // (no more than the longest sequence that the table holds can have)
   const int64_t room = a.table_pages << a.page_shift;
+  a.most_units = (int)units;
   a.parts_each = room < kPrCutFrom ? 1 : (int)min((int64_t)prompt_parts(units, D), room / (kPrTok * kPrPartTiles));
   const size_t lds = sizeof(PromptShared<D>);
   const hipError_t e = hipFuncSetAttribute((const void*)attn4_prompt_kernel<D>,

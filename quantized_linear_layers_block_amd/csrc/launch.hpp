@@ -98,6 +98,7 @@ struct Attn4 {
   int few;                  // most query rows of a sequence for the few-row kernel
   int join;                 // a second kernel joins the parts of its units
   int wide;                 // positions in the call's work may pass 32 bits
+  int most_units;           // of the prompt kernel
   int parts_each;           // most parts of a unit of the prompt kernel
 };
 bool attn4_launchable(int64_t batch, int64_t total_q, int64_t group, int64_t heads, int head_dim, int64_t max_q);

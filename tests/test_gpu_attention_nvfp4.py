@@ -333,6 +333,24 @@ def test_bad_tables_are_cut_and_reported():
     assert torch.equal(out[:2], ok[:2]) and bool((out[2:] == 7).all())
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_q_starts_that_fall(d):
+    """Sequences that overlap take more units than the call's sizes promise: reported, and nothing is
+    touched outside out, lse and the workspace, whose last bytes a guard follows."""
+    t, heads = 1000, 2
+    s = Seqs([(t, t)] * 9, heads, heads, d, 64, d)
+    q = s.q[:t].contiguous()
+    starts = torch.tensor([0, t, 0, t, 0, t, 0, t, 0, t], dtype=torch.int32, device=DEV)
+    need = B.qlinear_attention_nvfp4_workspace(9, t, heads, heads, d, t)
+    ws = torch.zeros(need + 4096, dtype=torch.uint8, device=DEV)
+    ws[need:] = 0x5A
+    out = torch.full((t + 8, heads, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    B.qlinear_attention_nvfp4(s.cache.handle, q, s.pt, s.kv_lens, out[:t], ws[:need], starts, t, d ** -0.5)
+    torch.cuda.synchronize()
+    assert ql.workspace_status(ws) == B.QLINEAR_STATUS_BAD_ITEM
+    assert (ws[need:] == 0x5A).all() and (out[t:] == 7.0).all()
+
+
 @pytest.mark.parametrize("lens", [[(1, n) for n in (700, 3, 2500, 90)], [(100, 400), (1, 900)]])
 def test_strides_workspace_reuse_and_reproducibility(lens):
     hq, h, d = 12, 4, 128
