@@ -233,6 +233,9 @@ struct AttnCut {
     return (T)((chunks + (uint32_t)each - 1) / (uint32_t)each) * (T)each;
   }
 };
+// kWholeMore: chunks that a share may grow by for whole workgroups.  kUnitCost is taken in full from
+// kUnitCost * kCostShare chunks a workgroup on; charged to shorter shares it costs more than it evens
+// out (32 sequences of 2000 tokens at D = 64: 19.3 us, 16.6 without).
 constexpr uint32_t kUnitCost = 2, kCostShare = 3, kWholeMore = 2;
 
 // A workgroup's place on the line.

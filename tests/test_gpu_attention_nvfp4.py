@@ -432,6 +432,58 @@ def test_other_stream():
     assert torch.equal(got, want)
 
 
+def test_captured_mixed_batch_follows_starts_and_lengths():
+    """Prompts and decode rows in one captured call: replays take the lengths and the query ranges
+    that are on the device then, and give what an eager call gives, bit by bit."""
+    lens = [(1, 900), (200, 1500), (70, 70), (1, 3), (40, 2000)]
+    s = Seqs(lens, 8, 2, 128, 16, 23)
+    starts = torch.from_numpy(s.starts).to(DEV)
+    out, lse = torch.empty_like(s.q), torch.empty((s.tq, 8), dtype=torch.float32, device=DEV)
+    ws = torch.zeros(B.qlinear_attention_nvfp4_workspace(5, s.tq, 8, 2, 128, 300), dtype=torch.uint8, device=DEV)
+
+    def call(out, lse, ws=None):
+        ql.attention_nvfp4(s.q, s.cache, s.pt, s.kv_lens, q_starts=starts, max_q_len=300, out=out, lse=lse, ws=ws)
+
+    call(out, lse, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out, lse, ws)
+    for cut in ([1, 200, 70, 1, 40], [1, 1, 1, 1, 1], [60, 250, 1, 0, 1], [1, 200, 70, 1, 40]):
+        q_lens = np.array(cut)
+        starts.copy_(torch.from_numpy(np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)))
+        s.lens = [(int(q), n) for q, (_, n) in zip(q_lens, lens)]
+        s.starts = starts.cpu().numpy()
+        out.fill_(float("nan"))
+        lse.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager, eager_lse = torch.full_like(out, float("nan")), torch.full_like(lse, float("nan"))
+        call(eager, eager_lse)
+        torch.cuda.synchronize()
+        used = int(s.starts[-1])
+        assert torch.equal(out[:used], eager[:used]) and torch.equal(lse[:used], eager_lse[:used])
+        assert torch.isnan(out[used:]).all() and torch.isnan(lse[used:]).all()
+        s.check(out, lse, rows=8)
+
+
+def test_two_calls_at_once():
+    """On two streams, each with a workspace of its own."""
+    a, b = Seqs([(1, 3000)] * 8, 16, 4, 128, 16, 31), Seqs([(150, 2500), (90, 800)], 8, 2, 64, 32, 32)
+    want = [x.run()[0].clone() for x in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, x in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                starts = None if x.uniform else torch.from_numpy(x.starts).to(DEV)
+                got[i].append(ql.attention_nvfp4(x.q, x.cache, x.pt, x.kv_lens, q_starts=starts, max_q_len=x.max_q))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 4 GiB, with the sequence's pages at its end."""
     h, d, page = 8, 256, 1024
