@@ -225,6 +225,7 @@ __device__ __forceinline__ int attn_lo(const Attn4& a, int nq, int n) {
 // begins with `cost` places without a chunk (256 of up to 4096, 64/8 heads: 137 us, 148 without).
 struct AttnCut {
   uint64_t each;   // chunks a workgroup
+  uint64_t end;    // of the line
   uint32_t cost;
   bool whole;
   template <typename T>
@@ -271,23 +272,26 @@ __device__ __forceinline__ uint32_t attn_units(const Attn4& a, const AttnRange& 
   return (r.nq * a.group > a.few ? 0u : (uint32_t)(r.nq * a.group + R - 1) / R) * (uint32_t)a.heads;
 }
 
-// units, chunks: a lane's sequence (of all, if there are no more than 64); sum, sum_u: the chunks
-// and units of all
-template <int WGS, typename T>
+// units, chunks: a lane's sequence of the first 64; sum, sum_u: the chunks and units of all
+template <int R, int WGS, typename T>
 __device__ __forceinline__ AttnCut attn_cut(const Attn4& a, uint32_t units, uint32_t chunks, T sum, T sum_u) {
-  AttnCut c{(uint64_t)((sum + WGS - 1) / WGS), 0, sum <= WGS};
+  AttnCut c{(uint64_t)((sum + WGS - 1) / WGS), (uint64_t)sum, 0, sum <= WGS};
   if (c.whole) return c;
-  if (a.batch <= 64 && sum_u <= WGS) {
+  if (sum_u <= WGS) {
     const uint32_t each = (uint32_t)c.each;   // < 2^24: a unit's chunks are
-    for (uint32_t e = each; e <= each + kWholeMore; ++e)
-      if (of_lane(wave_scan(units * ((chunks + e - 1) / e)), 63) <= WGS) {
-        c.each = e;
-        c.whole = true;
-        return c;
+    for (uint32_t e = each; e <= each + kWholeMore; ++e) {
+      uint32_t n = units * ((chunks + e - 1) / e);
+      for (int b = 64 + (threadIdx.x & 63); b < a.batch; b += 64) {
+        const AttnRange r = attn_range(a, b);
+        n += attn_units<R>(a, r) * ((attn_chunks(a, r) + e - 1) / e);
       }
+      n = of_lane(wave_scan(n), 63);
+      if (n <= WGS) return AttnCut{e, (uint64_t)n * e, 0, true};
+    }
   }
   c.cost = (uint32_t)min((T)kUnitCost, sum / (WGS * kCostShare));
-  c.each = (uint64_t)((sum + sum_u * c.cost + WGS - 1) / WGS);
+  c.end = (uint64_t)(sum + sum_u * c.cost);
+  c.each = (c.end + WGS - 1) / WGS;
   return c;
 }
 
@@ -310,9 +314,9 @@ __device__ __forceinline__ bool attn_place(const Attn4& a, AttnPlace& pl, AttnRa
   if (blockIdx.x == 0 && threadIdx.x < 64 && __any(bad) && lane == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
   sum_u = of_lane(wave_scan(sum_u), 63);
   sum = of_lane(wave_scan(sum), 63);
-  const AttnCut cut = attn_cut<WGS, T>(a, units, chunks, sum, sum_u);
+  const AttnCut cut = attn_cut<R, WGS, T>(a, units, chunks, sum, sum_u);
   T mine = (T)units * cut.stretch<T>(chunks), upto = wave_scan(mine);
-  const T each = (T)cut.each, pos = (T)blockIdx.x * each, end = cut.whole && each > 1 ? of_lane(upto, 63) : sum + sum_u * cut.cost;
+  const T each = (T)cut.each, pos = (T)blockIdx.x * each, end = (T)cut.end;
   if (pos >= end) return false;
   pl.cut = cut;
   pl.stop = min(pos + each, end);
@@ -783,10 +787,10 @@ __global__ __launch_bounds__(256) void attn4_join_kernel(Attn4 a, int tiles) {
   const int head = unit % a.heads, tile = unit / a.heads % tiles, b = unit / a.heads / tiles;
   const AttnRange rg = attn_range_uniform(a, b);
   if (tile * R + row >= rg.nq * a.group || rg.nq * a.group > a.few) return;
-  // (no more than 64 sequences: launch_r)
+  // (of no more than 64 sequences: launch_r)
   const AttnRange at = lane < a.batch ? attn_range(a, lane) : AttnRange{0, 0, 0, false};
   const uint32_t chunks = attn_chunks(a, rg), units = attn_units<R>(a, at), of_lanes = attn_chunks(a, at);
-  const AttnCut cut = attn_cut<WGS, uint64_t>(a, units, of_lanes, of_lane(wave_scan((uint64_t)units * of_lanes), 63),
+  const AttnCut cut = attn_cut<R, WGS, uint64_t>(a, units, of_lanes, of_lane(wave_scan((uint64_t)units * of_lanes), 63),
                                               of_lane(wave_scan((uint64_t)units), 63));
   const uint64_t before = lane < b ? units * cut.stretch<uint64_t>(of_lanes) : 0;
   const uint64_t u0 = of_lane(wave_scan(before), 63) +

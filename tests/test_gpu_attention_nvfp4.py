@@ -142,6 +142,7 @@ def test_prompt_pieces_far_into_long_contexts(lens, hq, h, d, page, causal, wind
     (20, 2000, 16, 8, 128),    # fewer units than workgroups: whole workgroups a unit
     (70, 1000, 16, 16, 64),    # more, over 64 sequences: shares that begin and end within units
     (70, 200, 16, 16, 64),     # the same with short shares
+    (90, 900, 4, 2, 128),      # over 64 sequences in whole workgroups
     (33, 700, 4, 4, 256)])
 def test_cuts_of_the_work(batch, n, hq, h, d):
     g = np.random.default_rng(batch + n)
