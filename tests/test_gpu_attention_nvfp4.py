@@ -71,14 +71,15 @@ class Seqs:
         torch.cuda.synchronize()
         return out, lse
 
-    def check(self, out, lse, causal=True, window=0, scale=None, rows=24, seed=0, held=None, only=None):
-        """Against the oracle, on at most `rows` query tokens a sequence (or on those of `only`)."""
+    def check(self, out, lse, causal=True, window=0, scale=None, rows=24, seed=0, held=None, only=None, every=1):
+        """Against the oracle, on at most `rows` query tokens of every `every`-th sequence (or on those
+        of `only`)."""
         g = np.random.default_rng(seed)
         qf = bf16_bits_to_f32(self.q_bits).astype(np.float64)
         o, z = bf16_bits_to_f32(bf16_bits_of(out)).astype(np.float64), lse.cpu().numpy().astype(np.float64)
         scale = self.d ** -0.5 if scale is None else scale
         for b, (nq, n) in enumerate(self.lens):
-            if nq == 0:
+            if nq == 0 or b % every:
                 continue
             pick = np.arange(nq) if nq <= rows else np.unique(np.concatenate(
                 [[0, 1, nq - 2, nq - 1], g.choice(nq, rows, replace=False)]))
@@ -147,8 +148,9 @@ def test_prompt_pieces_far_into_long_contexts(lens, hq, h, d, page, causal, wind
 def test_cuts_of_the_work(batch, n, hq, h, d):
     g = np.random.default_rng(batch + n)
     s = Seqs([(1, int(x)) for x in g.integers(n // 2, n + 1, batch)], hq, h, d, 64, n)
-    s.check(*s.run())
-    s.check(*s.run(window=n // 3), window=n // 3)
+    every = 3 if batch > 64 else 1
+    s.check(*s.run(), every=every)
+    s.check(*s.run(window=n // 3), window=n // 3, every=every)
 
 
 @pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 1])
