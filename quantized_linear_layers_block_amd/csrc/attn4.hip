@@ -14,6 +14,12 @@
 // relative) and the sum of p vhat need no second scale.  m is only moved when some w passes
 // it by 6, i.e. when p would pass 2^15; below, f16 holds p down to 2^-34 of the largest.
 //
+// l is rebuilt from p, and p is 0 below 2^-126: with ev far below the ev that set m, a token's whole
+// weight would be lost.  What is lost is at most 2^(spread of ev - 135) of l a token.  So this
+// holds while every ev lies in a window of 64 (values whose rows' largest are between 2^-35 and 2^28); from the
+// first step that has another one (a zero row is one), l is summed by itself, relative to the
+// largest logit (`apart`).
+//
 // The products are taken transposed: S^T = K Q^T and O^T = V^T P^T with the 16x16x32 MFMA, so
 // that a lane holds one query row's logits for four consecutive tokens -- the four a lane
 // takes of V^T -- and P goes from one product to the next in registers.
@@ -26,6 +32,25 @@ namespace ql {
 
 constexpr int kAttnWaves = 4;
 constexpr float kNoMax = -3.0e38f;  // m before any token was seen; exp2(-inf - kNoMax) = 0
+
+// The window of ev that l and the sums of values share one maximum in (exponent bytes).
+constexpr uint32_t kEvLow = 81, kEvSpan = 64;
+
+// x 2^d for d <= 0, also where 2^d alone would be 0.
+__device__ __forceinline__ float shrink_by(float x, float d) {
+  const float half = __builtin_exp2f(0.5f * d);
+  return x * half * half;
+}
+
+// Brings a row's maxima m (of logits with ev) and ml (of logits, which l is relative to) to one, so that l is
+// between 2^-80 and 2^110 (2^30 tokens); the factor for the sums of values.
+__device__ __forceinline__ float one_maximum(float& m, float ml, float& l) {
+  const float to = __builtin_fminf(__builtin_fmaxf(m, ml - 80.0f), ml + 80.0f);
+  const float by = __builtin_exp2f(m - to);
+  l *= __builtin_exp2f(ml - to);
+  m = to;
+  return by;
+}
 
 struct AttnRange {
   int nq, n;        // query rows (tokens) and cached tokens of the sequence
@@ -422,6 +447,8 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
 #pragma unroll
     for (int j = 0; j < KW; ++j) o[y][j] = f32x4{0, 0, 0, 0};
   float m = kNoMax, l = 0.0f;
+  bool apart = false;   // l is relative to ml, the largest logit
+  float ml = kNoMax;
   const int32_t* table = a.table + (int64_t)pl.b * a.table_stride;
   const int per = 1 << (a.page_shift - 4);
   bool bad_page = false;
@@ -450,6 +477,7 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
 
   const Lane4<D> lane_at(lane);
   const uint32_t sel_k = g == 0 ? ~0u : 0u, sel_v = g == 1 ? ~0u : 0u;
+  uint32_t sel_l = g >= 2 ? ~0u : 0u;
   Keys4<D> f[2];
   Values4<D> fv[2];
   const uint8_t* grp[2];
@@ -506,14 +534,33 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
   int done = pl.done;
   for (int t0 = lo + wave * 32; t0 < hi; t0 += kAttnWaves * 32) {
     if (++done > pl.turn) attn_give_way(pl, each);
-    // what depends on the token alone is worked out by one lane a token and shared: 2^ek, ev + 127
-    // and 2^(-9 - ev) at 0, 16 and 32 of x
+    const bool edge = !ok[0] || !ok[1] || t0 < all_from || t0 + 32 > all_to;
+    uint32_t eb[2], off[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint32_t eb = (f[u].e >> (8 * (lane & 3))) & 0xFFu, b23 = eb << 23;
+      eb[u] = (f[u].e >> (8 * (lane & 3))) & 0xFFu;
+      off[u] = eb[u] - kEvLow;
+    }
+    if (edge) {   // tokens that no row sees do not count
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = t0 + 16 * u + n16;
+        if (!(ok[u] && t >= begin && t < hi)) off[u] = 0;
+      }
+    }
+    if ((__ballot(umax(off[0], off[1]) >= kEvSpan) >> 16) != 0 && !apart) {   // (lanes past 15 hold value rows' exponents)
+      apart = true;
+      ml = m;
+      sel_l = 0;
+    }
+    // what depends on the token alone is worked out by one lane a token and shared: 2^ek, ev + 127
+    // and 2^(-9 - ev) (0 where l is apart) at 0, 16 and 32 of x
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t b23 = eb[u] << 23;
       // (selected by masks: written as a choice, the compiler branches)
-      const uint32_t ve = __float_as_uint((float)eb), lf = (245u - min(eb, 244u)) << 23;
-      sh.x[wave][u][lane] = __uint_as_float((b23 & sel_k) | (ve & sel_v) | (lf & ~(sel_k | sel_v)));
+      const uint32_t ve = __float_as_uint((float)eb[u]), lf = (245u - min(eb[u], 244u)) << 23;
+      sh.x[wave][u][lane] = __uint_as_float((b23 & sel_k) | (ve & sel_v) | (lf & sel_l));
     }
     __builtin_amdgcn_wave_barrier();
     f32x4 c[2];
@@ -545,7 +592,6 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
         for (int j = 0; j < KW; ++j) fv[u].vs[j] &= mask;
       }
     }
-    const bool edge = !ok[0] || !ok[1] || t0 < all_from || t0 + 32 > all_to;
     // The next step's keys are on their way from here, its values from when this step's are
     // used.  After the last step the same groups are fetched again: with a branch around the
     // loads the compiler would wait for all that are in flight.
@@ -585,6 +631,27 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
         for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, p[u][i]);
       return top;
     };
+    if (__builtin_expect(apart, 0)) {
+      float w[2][4], top = -__builtin_inff();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const f32x4 kf = *(const f32x4*)&sh.x[wave][u][4 * g] * kc;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[u][i] = seen >> (4 * u + i) & 1 ? c[u][i] * kf[i] : -__builtin_inff();
+          top = __builtin_fmaxf(top, w[u][i]);
+        }
+      }
+      top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+      top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+      top = __builtin_fmaxf(top, ml);
+      l *= __builtin_exp2f(ml - top);
+      ml = top;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l += __builtin_amdgcn_exp2f(w[u][i] - top);
+    }
     if (__any(weigh(9.0f - 127.0f - m) > 15.0f)) {   // x holds ev + 127
       // the maximum moves: w again in full, the sums to the new one
       float w = weigh(-127.0f);
@@ -592,7 +659,7 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
       w = __builtin_fmaxf(w, __shfl_xor(w, 32));
       const float mn = __builtin_fmaxf(m, w), shrink = __builtin_exp2f(m - mn);
       m = mn;
-      l *= shrink;
+      l *= apart ? 1.0f : shrink;
 #pragma unroll
       for (int y = 0; y < P; ++y)
 #pragma unroll
@@ -631,6 +698,13 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
 
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
+  if (apart) {
+    const float by = one_maximum(m, ml, l);
+#pragma unroll
+    for (int y = 0; y < P; ++y)
+#pragma unroll
+      for (int j = 0; j < KW; ++j) o[y][j] *= by;
+  }
 #pragma unroll
   for (int y = 0; y < P; ++y)
 #pragma unroll
@@ -658,7 +732,7 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
 #pragma unroll
   for (int w = 0; w < kAttnWaves; ++w) {
     const float s = __builtin_exp2f(sh.m[w][src] - top);
-    lsum += s * sh.l[w][src];
+    lsum += shrink_by(sh.l[w][src], sh.m[w][src] - top);
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] += s * sh.o[w][src][part * E + e];
   }
@@ -719,14 +793,14 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
 #pragma unroll
       for (int i = 0; i < kJoin; ++i) mn = __builtin_fmaxf(mn, mx[i]);
       const float shrink = __builtin_exp2f(top - mn);
+      lsum = shrink_by(lsum, top - mn);
       top = mn;
-      lsum *= shrink;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] *= shrink;
 #pragma unroll
       for (int i = 0; i < kJoin; ++i) {
         const float w = s0 + i < splits ? __builtin_exp2f(mx[i] - top) : 0.0f;
-        lsum = __builtin_fmaf(w, lx[i], lsum);
+        lsum += s0 + i < splits ? shrink_by(lx[i], mx[i] - top) : 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(w, v[i][e / 4][e & 3], acc[e]);
       }
@@ -828,8 +902,8 @@ __global__ __launch_bounds__(256) void attn4_join_kernel(Attn4 a, int tiles) {
 #pragma unroll
     for (int i = 0; i < kFly; ++i) {
       const int s = s0 + i * kSide + side;
-      const float w = s < splits ? __builtin_exp2f(sm[min(s, splits - 1)] - top) : 0.0f;
-      l = __builtin_fmaf(w, sl[min(s, splits - 1)], l);
+      const float d = sm[min(s, splits - 1)] - top, w = s < splits ? __builtin_exp2f(d) : 0.0f;
+      l += s < splits ? shrink_by(sl[min(s, splits - 1)], d) : 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(w, v[i][e], acc[e]);
     }
@@ -894,12 +968,16 @@ int prompt_parts(int64_t units, int d) {
 }
 __host__ __device__ constexpr size_t prompt_part_bytes(int d) { return (size_t)prompt_rows(d) * (d + 2) * 4; }
 
+// What keeps a tile from the short way: a group that is left out; an ev outside the window that l may share.
+constexpr uint32_t kOddOut = 1, kOddFar = 2;
+
 template <int D>
 struct PromptShared {
   uint4 k[2][kPrTok / 32][D / 16][64];   // [tile][32 tokens][16 elements][lane]
   uint4 v[2][kPrGroups][D / 32][64];     // [tile][16 tokens][32 elements][lane]
   float ke[2][kPrGroups];                // 2^(E - 4), 0 for a group that is left out
   float2 vf[2][kPrGroups];               // F and 2^(-9 - F)
+  __attribute__((aligned(8))) uint8_t odd[2][2][kPrGroups];   // kOdd.. of the groups' keys and values
   __attribute__((aligned(8))) _Float16 by[8][16];   // a wave's 2^(ev - F + 4) of 16 tokens
 };
 
@@ -926,6 +1004,7 @@ __device__ __forceinline__ void prompt_keys(PromptShared<D>& sh, int buf, int gr
     sh.k[buf][grp >> 1][w >> 1][(w & 1) * 32 + (grp & 1) * 16 + n16] =
         __builtin_bit_cast(uint4, scaled8(f.k[i], sp, sp, sp, sp));
   }
+  if (lane == 0) sh.odd[buf][0][grp] = valid ? 0 : kOddOut;
   if (lane == 0) sh.ke[buf][grp] = valid ? __uint_as_float((uint32_t)max((int)top - 4, 0) << 23) : 0.0f;
 }
 
@@ -961,7 +1040,11 @@ __device__ __forceinline__ void prompt_values(PromptShared<D>& sh, int buf, int 
     at[0] = make_uint2(__builtin_bit_cast(uint32_t, e0), __builtin_bit_cast(uint32_t, e1));
     at[32] = make_uint2(__builtin_bit_cast(uint32_t, o0), __builtin_bit_cast(uint32_t, o1));
   }
-  if (lane == 0) sh.vf[buf][grp] = make_float2((float)(int)top - 127.0f, __uint_as_float((245u - top) << 23));
+  const bool far = __any((valid >> m & 1) && e - kEvLow >= kEvSpan);
+  if (lane == 0) {
+    sh.vf[buf][grp] = make_float2((float)(int)top - 127.0f, __uint_as_float((245u - top) << 23));
+    sh.odd[buf][1][grp] = far ? kOddFar : 0;
+  }
 }
 
 // Unit `id`: (sequence, row tile, head), those that see the most tokens first, so that the last
@@ -1206,6 +1289,8 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
     for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
   float m = 0.0f, l = 0.0f;
   float limit = kNoMax;   // m moves when w - m + 9 passes it: 15 once the row has seen a token
+  bool apart = false;     // l is relative to ml, the largest logit
+  float ml = kNoMax;
 
   if (tiles > 0) {
     look_up(0);
@@ -1245,17 +1330,18 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
       __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
       __builtin_amdgcn_sched_barrier(0);
       float kf[kPrGroups], vf[kPrGroups], lf[kPrGroups];
-      bool whole = true;
 #pragma unroll
       for (int gr = 0; gr < kPrGroups; ++gr) {
         const float ke = sh.ke[buf][gr];
-        whole &= ke != 0.0f;
         kf[gr] = __builtin_fmaxf(ke * kc, 1e-37f);   // (below it a logit is 0)
         const float2 vv = sh.vf[buf][gr];
         vf[gr] = vv.x + (9.0f - m);
         lf[gr] = vv.y;
       }
-      if (!whole || t0 < all_from || t0 + kPrTok > all_to) {   // a logit that the row does not see becomes -inf
+      const uint2 odd2 = *(const uint2*)sh.odd[buf];
+      const uint32_t odd = (uint32_t)__builtin_amdgcn_readfirstlane((int)(odd2.x | odd2.y));
+      if (__builtin_expect(odd != 0 || apart || t0 < all_from || t0 + kPrTok > all_to, 0)) {
+        // a logit that the row does not see becomes -inf
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
@@ -1263,6 +1349,29 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
             const int t = t0 + 32 * tt + 8 * (i >> 2) + 4 * half + (i & 3);
             if (!(t >= from && t < to && sh.ke[buf][2 * tt + (i >> 3)] != 0.0f)) c[tt][i] = -__builtin_inff();
           }
+        if (!apart && (odd & 0x01010101u * kOddFar)) {
+          apart = true;
+          ml = limit == 15.0f ? m : kNoMax;
+        }
+        if (apart) {
+          float top = ml;
+#pragma unroll
+          for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, c[tt][i] * kf[2 * tt + (i >> 3)]);
+          top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+          l *= __builtin_exp2f(ml - top);
+          ml = top;
+#pragma unroll
+          for (int gr = 0; gr < kPrGroups; ++gr) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              sum += __builtin_amdgcn_exp2f(__builtin_fmaf(c[gr >> 1][8 * (gr & 1) + i], kf[gr], -top));
+            l += sum;
+            lf[gr] = 0.0f;
+          }
+        }
       }
       float top = -__builtin_inff();
 #pragma unroll
@@ -1280,7 +1389,7 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
         const float shrink = fresh ? 0.0f : __builtin_exp2f(-up);
         m += up;
         limit = any ? 15.0f : limit;
-        l *= shrink;
+        l *= apart ? 1.0f : shrink;
 #pragma unroll
         for (int j = 0; j < DT; ++j) o[j] *= shrink;
 #pragma unroll
@@ -1323,6 +1432,11 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
   if (__any(bad_page) && lane == 0) atomicOr(a.status, (int32_t)kStatusBadItem);
 
   l += __shfl_xor(l, 32);
+  if (apart && limit == 15.0f) {
+    const float by = one_maximum(m, ml, l);
+#pragma unroll
+    for (int j = 0; j < DT; ++j) o[j] *= by;
+  }
   if (wr + n32 >= tile_live) return;
   if (parts > 1) {   // this part's sums and their maximum, for the joining kernel
     float* to_part = (float*)(a.parts + ((size_t)unit * a.parts_each + part) * prompt_part_bytes(D));
@@ -1390,8 +1504,8 @@ __global__ __launch_bounds__(256) void attn4_prompt_join_kernel(Attn4 a) {
   for (int s = 0; s < parts; ++s)
 #pragma unroll
     for (int i = 0; i < kPrJoinRows; ++i) {
-      const float w = __builtin_exp2f(from[s * kStep + ROWS * D + r[i]] - top[i]);
-      l[i] = __builtin_fmaf(w, from[s * kStep + ROWS * D + ROWS + r[i]], l[i]);
+      const float d = from[s * kStep + ROWS * D + r[i]] - top[i], w = __builtin_exp2f(d);
+      l[i] += shrink_by(from[s * kStep + ROWS * D + ROWS + r[i]], d);
       const f32x4 v = *(const f32x4*)(from + s * kStep + r[i] * D + part * 4);
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(w, v[e], acc[i][e]);
