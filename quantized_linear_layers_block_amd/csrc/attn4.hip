@@ -36,18 +36,15 @@ constexpr float kNoMax = -3.0e38f;  // m before any token was seen; exp2(-inf - 
 // The window of ev that l and the sums of values share one maximum in (exponent bytes).
 constexpr uint32_t kEvLow = 81, kEvSpan = 64;
 
-// x 2^d for d <= 0, also where 2^d alone would be 0.
-__device__ __forceinline__ float shrink_by(float x, float d) {
-  const float half = __builtin_exp2f(0.5f * d);
-  return x * half * half;
-}
+// 2^(d / 2) for d <= 0: l is multiplied by it twice, since 2^d alone may be 0 where l 2^d counts.
+__device__ __forceinline__ float half_power(float d) { return __builtin_amdgcn_exp2f(0.5f * d); }
 
 // Brings a row's maxima m (of logits with ev) and ml (of logits, which l is relative to) to one, so that l is
 // between 2^-80 and 2^110 (2^30 tokens); the factor for the sums of values.
 __device__ __forceinline__ float one_maximum(float& m, float ml, float& l) {
   const float to = __builtin_fminf(__builtin_fmaxf(m, ml - 80.0f), ml + 80.0f);
-  const float by = __builtin_exp2f(m - to);
-  l *= __builtin_exp2f(ml - to);
+  const float by = __builtin_amdgcn_exp2f(m - to);
+  l *= __builtin_amdgcn_exp2f(ml - to);
   m = to;
   return by;
 }
@@ -447,7 +444,7 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
 #pragma unroll
     for (int j = 0; j < KW; ++j) o[y][j] = f32x4{0, 0, 0, 0};
   float m = kNoMax, l = 0.0f;
-  bool apart = false;   // l is relative to ml, the largest logit
+  uint32_t apart = 0;   // 1: l is relative to ml, the largest logit
   float ml = kNoMax;
   const int32_t* table = a.table + (int64_t)pl.b * a.table_stride;
   const int per = 1 << (a.page_shift - 4);
@@ -477,7 +474,6 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
 
   const Lane4<D> lane_at(lane);
   const uint32_t sel_k = g == 0 ? ~0u : 0u, sel_v = g == 1 ? ~0u : 0u;
-  uint32_t sel_l = g >= 2 ? ~0u : 0u;
   Keys4<D> f[2];
   Values4<D> fv[2];
   const uint8_t* grp[2];
@@ -534,33 +530,14 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
   int done = pl.done;
   for (int t0 = lo + wave * 32; t0 < hi; t0 += kAttnWaves * 32) {
     if (++done > pl.turn) attn_give_way(pl, each);
-    const bool edge = !ok[0] || !ok[1] || t0 < all_from || t0 + 32 > all_to;
-    uint32_t eb[2], off[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      eb[u] = (f[u].e >> (8 * (lane & 3))) & 0xFFu;
-      off[u] = eb[u] - kEvLow;
-    }
-    if (edge) {   // tokens that no row sees do not count
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int t = t0 + 16 * u + n16;
-        if (!(ok[u] && t >= begin && t < hi)) off[u] = 0;
-      }
-    }
-    if ((__ballot(umax(off[0], off[1]) >= kEvSpan) >> 16) != 0 && !apart) {   // (lanes past 15 hold value rows' exponents)
-      apart = true;
-      ml = m;
-      sel_l = 0;
-    }
     // what depends on the token alone is worked out by one lane a token and shared: 2^ek, ev + 127
-    // and 2^(-9 - ev) (0 where l is apart) at 0, 16 and 32 of x
+    // and 2^(-9 - ev) at 0, 16 and 32 of x
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint32_t b23 = eb[u] << 23;
+      const uint32_t eb = (f[u].e >> (8 * (lane & 3))) & 0xFFu, b23 = eb << 23;
       // (selected by masks: written as a choice, the compiler branches)
-      const uint32_t ve = __float_as_uint((float)eb[u]), lf = (245u - min(eb[u], 244u)) << 23;
-      sh.x[wave][u][lane] = __uint_as_float((b23 & sel_k) | (ve & sel_v) | (lf & sel_l));
+      const uint32_t ve = __float_as_uint((float)eb), lf = (245u - min(eb, 244u)) << 23;
+      sh.x[wave][u][lane] = __uint_as_float((b23 & sel_k) | (ve & sel_v) | (lf & ~(sel_k | sel_v)));
     }
     __builtin_amdgcn_wave_barrier();
     f32x4 c[2];
@@ -576,10 +553,11 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
       }
     }
     // which of its 8 tokens this lane's row sees
-    uint32_t seen = 0xFFu;
+    uint32_t seen = 0xFFu, off[2];   // off: of ev from the window, in the lanes past 15, which hold value rows' exponents
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int t = t0 + 16 * u;
+      off[u] = ((f[u].e >> (8 * (lane & 3))) & 0xFFu) - kEvLow;
       if (!ok[u] || t < all_from || t + 16 > all_to) {
         const int t4 = t + 4 * g;
 #pragma unroll
@@ -590,8 +568,14 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
         const uint32_t mask = (uint32_t)(((uint64_t)1 << (8 * keep)) - 1) & ~(uint32_t)(((uint64_t)1 << (8 * skip)) - 1);
 #pragma unroll
         for (int j = 0; j < KW; ++j) fv[u].vs[j] &= mask;
+        if (!(ok[u] && t + n16 >= begin && t + n16 < end)) off[u] = 0;   // a token that no row sees
       }
     }
+    if ((__ballot(umax(off[0], off[1]) >= kEvSpan) >> 16) != 0 && !apart) {
+      apart = 1;
+      ml = m;
+    }
+    const bool edge = !ok[0] || !ok[1] || t0 < all_from || t0 + 32 > all_to;
     // The next step's keys are on their way from here, its values from when this step's are
     // used.  After the last step the same groups are fetched again: with a branch around the
     // loads the compiler would wait for all that are in flight.
@@ -645,7 +629,7 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
       top = __builtin_fmaxf(top, __shfl_xor(top, 16));
       top = __builtin_fmaxf(top, __shfl_xor(top, 32));
       top = __builtin_fmaxf(top, ml);
-      l *= __builtin_exp2f(ml - top);
+      l *= __builtin_amdgcn_exp2f(ml - top);
       ml = top;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -657,7 +641,7 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
       float w = weigh(-127.0f);
       w = __builtin_fmaxf(w, __shfl_xor(w, 16));
       w = __builtin_fmaxf(w, __shfl_xor(w, 32));
-      const float mn = __builtin_fmaxf(m, w), shrink = __builtin_exp2f(m - mn);
+      const float mn = __builtin_fmaxf(m, w), shrink = __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       l *= apart ? 1.0f : shrink;
 #pragma unroll
@@ -669,6 +653,7 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[u][i] = p[u][i] - m + 9.0f;
     }
+    const float l_apart = l;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -691,6 +676,7 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
           o[P - 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, __builtin_bit_cast(f16x8, po), o[P - 1][j], 0, 0, 0);
       }
     }
+    if (apart) l = l_apart;
 #pragma unroll
     for (int u = 0; u < 2; ++u) load_values<D>(fv[u], grp[u], lane_at);
   }
@@ -731,8 +717,8 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
 #pragma unroll
   for (int w = 0; w < kAttnWaves; ++w) {
-    const float s = __builtin_exp2f(sh.m[w][src] - top);
-    lsum += shrink_by(sh.l[w][src], sh.m[w][src] - top);
+    const float r = half_power(sh.m[w][src] - top), s = r * r;
+    lsum += sh.l[w][src] * r * r;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] += s * sh.o[w][src][part * E + e];
   }
@@ -792,15 +778,15 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
       float mn = top;
 #pragma unroll
       for (int i = 0; i < kJoin; ++i) mn = __builtin_fmaxf(mn, mx[i]);
-      const float shrink = __builtin_exp2f(top - mn);
-      lsum = shrink_by(lsum, top - mn);
+      const float back = half_power(top - mn), shrink = back * back;
+      lsum = lsum * back * back;
       top = mn;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] *= shrink;
 #pragma unroll
       for (int i = 0; i < kJoin; ++i) {
-        const float w = s0 + i < splits ? __builtin_exp2f(mx[i] - top) : 0.0f;
-        lsum += s0 + i < splits ? shrink_by(lx[i], mx[i] - top) : 0.0f;
+        const float r = s0 + i < splits ? half_power(mx[i] - top) : 0.0f, w = r * r;
+        lsum = __builtin_fmaf(lx[i] * r, r, lsum);
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(w, v[i][e / 4][e & 3], acc[e]);
       }
@@ -902,8 +888,8 @@ __global__ __launch_bounds__(256) void attn4_join_kernel(Attn4 a, int tiles) {
 #pragma unroll
     for (int i = 0; i < kFly; ++i) {
       const int s = s0 + i * kSide + side;
-      const float d = sm[min(s, splits - 1)] - top, w = s < splits ? __builtin_exp2f(d) : 0.0f;
-      l += s < splits ? shrink_by(sl[min(s, splits - 1)], d) : 0.0f;
+      const float r = s < splits ? half_power(sm[min(s, splits - 1)] - top) : 0.0f, w = r * r;
+      l = __builtin_fmaf(sl[min(s, splits - 1)] * r, r, l);
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(w, v[i][e], acc[e]);
     }
@@ -1289,7 +1275,7 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
     for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
   float m = 0.0f, l = 0.0f;
   float limit = kNoMax;   // m moves when w - m + 9 passes it: 15 once the row has seen a token
-  bool apart = false;     // l is relative to ml, the largest logit
+  uint32_t apart = 0;     // l is relative to ml, the largest logit
   float ml = kNoMax;
 
   if (tiles > 0) {
@@ -1350,7 +1336,7 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
             if (!(t >= from && t < to && sh.ke[buf][2 * tt + (i >> 3)] != 0.0f)) c[tt][i] = -__builtin_inff();
           }
         if (!apart && (odd & 0x01010101u * kOddFar)) {
-          apart = true;
+          apart = 1;
           ml = limit == 15.0f ? m : kNoMax;
         }
         if (apart) {
@@ -1360,7 +1346,7 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, c[tt][i] * kf[2 * tt + (i >> 3)]);
           top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-          l *= __builtin_exp2f(ml - top);
+          l *= __builtin_amdgcn_exp2f(ml - top);
           ml = top;
 #pragma unroll
           for (int gr = 0; gr < kPrGroups; ++gr) {
@@ -1386,7 +1372,7 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
         top = __builtin_fmaxf(top, __shfl_xor(top, 32));
         const bool fresh = limit != 15.0f, any = top > kNoMax;
         const float up = any ? fresh ? top - 9.0f : __builtin_fmaxf(top - 9.0f, 0.0f) : 0.0f;
-        const float shrink = fresh ? 0.0f : __builtin_exp2f(-up);
+        const float shrink = fresh ? 0.0f : __builtin_amdgcn_exp2f(-up);
         m += up;
         limit = any ? 15.0f : limit;
         l *= apart ? 1.0f : shrink;
@@ -1504,8 +1490,8 @@ __global__ __launch_bounds__(256) void attn4_prompt_join_kernel(Attn4 a) {
   for (int s = 0; s < parts; ++s)
 #pragma unroll
     for (int i = 0; i < kPrJoinRows; ++i) {
-      const float d = from[s * kStep + ROWS * D + r[i]] - top[i], w = __builtin_exp2f(d);
-      l[i] += shrink_by(from[s * kStep + ROWS * D + ROWS + r[i]], d);
+      const float f = half_power(from[s * kStep + ROWS * D + r[i]] - top[i]), w = f * f;
+      l[i] = __builtin_fmaf(from[s * kStep + ROWS * D + ROWS + r[i]] * f, f, l[i]);
       const f32x4 v = *(const f32x4*)(from + s * kStep + r[i] * D + part * 4);
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(w, v[e], acc[i][e]);
