@@ -447,10 +447,7 @@ typedef struct {
  * token gets zeros and lse -inf.  Query tokens of no sequence keep their out and lse.
  * Products are f16 x f16 with float32 sums: q is scaled by a power of two a row (exact but for
  * magnitudes below about 2^-29 of the row's largest), the cache's values are exact, and the
- * softmax weights are rounded to f16 (2^-11) before they meet the values.  Sequences with more
- * than 64 query rows a KV head (query tokens * q_heads / heads; up to 128 where the call is
- * small) take a kernel that holds the keys and the values of 16 tokens relative to the largest
- * of their row exponents: rows more than 2^18 below it are off by 2^-40 of it at most.
+ * softmax weights are rounded to f16 (2^-11) before they meet the values.
  * Results are bitwise reproducible for the same arguments, also as a graph's replays.
  * Workspace: qlinear_attention_nvfp4_workspace(...) bytes with qlinear_forward's layout and
  * reuse rules (zero-filled before its first use; calls that share it must not overlap, which

@@ -922,11 +922,14 @@ __global__ __launch_bounds__(256) void attn4_join_kernel(Attn4 a, int tiles) {
 // codes of the tile after are on their way in registers meanwhile.
 //
 // The rows' exponents go into the f16 values here, relative to the largest of each 16 tokens,
-// E for keys and F for values: khat 2^(ek - E + 4), vhat 2^(ev - F + 4), at most 43008.  They are exact
-// for rows down to 2^-18 of the largest and off by 2^-40 of it below.  A logit then takes one
+// E for keys and F for values: khat 2^(ek - E + 4), vhat 2^(ev - F + 4), at most 43008 and exact for rows down
+// to 2^-18 of the largest.  A logit then takes one
 // fused multiply-add with factors of its group, w = (acc kc 2^(E - 4)) + F, where a factor a
 // token would cost two more of some nine vector instructions a logit, and the vector
 // instructions (the exponential takes four of them) weigh as much as the matrix products.
+// Sixteen tokens with rows further apart are held relative to their own exponents (E = ek, F = ev
+// for each), and the tiles that have some take the longer way with factors a token: tokens that a
+// query does not see are among the 16, and must not cost it the ones that it sees.
 //
 // At D = 128 a prompt of 8192 tokens, 28/4 heads, takes 501 us (960 TFLOP/s of the products that are seen;
 // a library product reaches 1390), with the matrix units busy for 45% of the cycles and the vector
@@ -954,8 +957,10 @@ int prompt_parts(int64_t units, int d) {
 }
 __host__ __device__ constexpr size_t prompt_part_bytes(int d) { return (size_t)prompt_rows(d) * (d + 2) * 4; }
 
-// What keeps a tile from the short way: a group that is left out; an ev outside the window that l may share.
-constexpr uint32_t kOddOut = 1, kOddFar = 2;
+// What keeps a tile from the short way: a group that is left out; an ev outside the window that l may
+// share; rows further apart than kPrGap.
+constexpr uint32_t kOddOut = 1, kOddFar = 2, kOddWide = 4;
+constexpr uint32_t kPrKeyGap = 18, kPrValueGap = 18;
 
 template <int D>
 struct PromptShared {
@@ -964,6 +969,7 @@ struct PromptShared {
   float ke[2][kPrGroups];                // 2^(E - 4), 0 for a group that is left out
   float2 vf[2][kPrGroups];               // F and 2^(-9 - F)
   __attribute__((aligned(8))) uint8_t odd[2][2][kPrGroups];   // kOdd.. of the groups' keys and values
+  __attribute__((aligned(16))) float tke[2][kPrTok], tf[2][kPrTok];   // ke and F of each token (kOddWide)
   __attribute__((aligned(8))) _Float16 by[8][16];   // a wave's 2^(ev - F + 4) of 16 tokens
 };
 
@@ -980,7 +986,13 @@ __device__ __forceinline__ void prompt_keys(PromptShared<D>& sh, int buf, int gr
   const int n16 = lane & 15, g = lane >> 4;
   const uint32_t e = (f.e >> (8 * (n16 & 3))) & 0xFFu;
   const uint32_t top = max_row16((valid >> n16 & 1) ? min(e, 244u) : 0u);
-  const f16x2 by = both(pow2_f16((int)e - (int)top + 4));
+  const bool wide = (__ballot(e + kPrKeyGap < top) & valid) != 0;
+  int off = (int)e - (int)top;
+  if (__builtin_expect(wide, 0)) {
+    off = 0;
+    if (g == 0) sh.tke[buf][grp * 16 + n16] = __uint_as_float((uint32_t)max((int)e - 4, 0) << 23);
+  }
+  const f16x2 by = both(pow2_f16(off + 4));
   const uint32_t ks = f.ks >> ((8 * (D / 64) * g) & 31);
   const f16x2 s01 = scales2<false>(ks) * by, s23 = scales2<true>(ks) * by;
 #pragma unroll
@@ -990,8 +1002,10 @@ __device__ __forceinline__ void prompt_keys(PromptShared<D>& sh, int buf, int gr
     sh.k[buf][grp >> 1][w >> 1][(w & 1) * 32 + (grp & 1) * 16 + n16] =
         __builtin_bit_cast(uint4, scaled8(f.k[i], sp, sp, sp, sp));
   }
-  if (lane == 0) sh.odd[buf][0][grp] = valid ? 0 : kOddOut;
-  if (lane == 0) sh.ke[buf][grp] = valid ? __uint_as_float((uint32_t)max((int)top - 4, 0) << 23) : 0.0f;
+  if (lane == 0) {
+    sh.ke[buf][grp] = valid ? __uint_as_float((uint32_t)max((int)top - 4, 0) << 23) : 0.0f;
+    sh.odd[buf][0][grp] = valid ? wide ? kOddWide : 0 : kOddOut;
+  }
 }
 
 template <int D>
@@ -1002,7 +1016,13 @@ __device__ __forceinline__ void prompt_values(PromptShared<D>& sh, int buf, int 
   // lane % 16 works out its token's factor; a lane takes those of its four tokens
   const uint32_t e = (valid >> m & 1) ? min((e4 >> (8 * (m & 3))) & 0xFFu, 244u) : 0u;
   const uint32_t top = max_row16(e);
-  sh.by[wave][m] = pow2_f16((int)e - (int)top + 4);
+  const bool wide = (__ballot(e + kPrValueGap < top) & valid) != 0, far = (__ballot(e - kEvLow >= kEvSpan) & valid) != 0;
+  int off = (int)e - (int)top;
+  if (__builtin_expect(wide, 0)) {
+    off = 0;
+    if (g == 0) sh.tf[buf][grp * 16 + m] = (float)(int)e - 127.0f;
+  }
+  sh.by[wave][m] = pow2_f16(off + 4);
   __builtin_amdgcn_wave_barrier();
   if (valid != 0xFFFFu) {   // memory that was never written: no NaN from its scales
     const uint32_t mine = valid >> (4 * g) & 15u;
@@ -1026,10 +1046,9 @@ __device__ __forceinline__ void prompt_values(PromptShared<D>& sh, int buf, int 
     at[0] = make_uint2(__builtin_bit_cast(uint32_t, e0), __builtin_bit_cast(uint32_t, e1));
     at[32] = make_uint2(__builtin_bit_cast(uint32_t, o0), __builtin_bit_cast(uint32_t, o1));
   }
-  const bool far = __any((valid >> m & 1) && e - kEvLow >= kEvSpan);
   if (lane == 0) {
     sh.vf[buf][grp] = make_float2((float)(int)top - 127.0f, __uint_as_float((245u - top) << 23));
-    sh.odd[buf][1][grp] = far ? kOddFar : 0;
+    sh.odd[buf][1][grp] = (far ? kOddFar : 0) | (wide ? kOddWide : 0);
   }
 }
 
@@ -1315,6 +1334,11 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
       }
       __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
       __builtin_amdgcn_sched_barrier(0);
+      float w[2][16];   // (numbers of their own: as vectors they would be copied around the branches)
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[tt][i] = c[tt][i];
       float kf[kPrGroups], vf[kPrGroups], lf[kPrGroups];
 #pragma unroll
       for (int gr = 0; gr < kPrGroups; ++gr) {
@@ -1325,38 +1349,61 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
         lf[gr] = vv.y;
       }
       const uint2 odd2 = *(const uint2*)sh.odd[buf];
-      const uint32_t odd = (uint32_t)__builtin_amdgcn_readfirstlane((int)(odd2.x | odd2.y));
-      if (__builtin_expect(odd != 0 || apart || t0 < all_from || t0 + kPrTok > all_to, 0)) {
+      const uint32_t odd_k = (uint32_t)__builtin_amdgcn_readfirstlane((int)odd2.x);
+      const uint32_t odd_v = (uint32_t)__builtin_amdgcn_readfirstlane((int)odd2.y);
+      uint32_t back = 0;   // l is relative to ml in this tile alone
+      if (__builtin_expect((odd_k | odd_v) != 0 || apart || t0 < all_from || t0 + kPrTok > all_to, 0)) {
         // a logit that the row does not see becomes -inf
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int t = t0 + 32 * tt + 8 * (i >> 2) + 4 * half + (i & 3);
-            if (!(t >= from && t < to && sh.ke[buf][2 * tt + (i >> 3)] != 0.0f)) c[tt][i] = -__builtin_inff();
+            if (!(t >= from && t < to && sh.ke[buf][2 * tt + (i >> 3)] != 0.0f)) w[tt][i] = -__builtin_inff();
           }
-        if (!apart && (odd & 0x01010101u * kOddFar)) {
-          apart = 1;
-          ml = limit == 15.0f ? m : kNoMax;
+        const bool wide = ((odd_k | odd_v) & 0x01010101u * kOddWide) != 0;
+        if (wide) {
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const f32x4 ke = *(const f32x4*)&sh.tke[buf][8 * y + 4 * half];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[y >> 2][4 * (y & 3) + i] *=
+                  odd_k >> (8 * (y >> 1)) & kOddWide ? __builtin_fmaxf(ke[i] * kc, 1e-37f) : kf[y >> 1];
+          }
+#pragma unroll
+          for (int gr = 0; gr < kPrGroups; ++gr) kf[gr] = 1.0f;
         }
-        if (apart) {
+        if (apart || (odd_v & 0x01010101u * (kOddFar | kOddWide))) {
+          if (!apart) ml = limit == 15.0f ? m : kNoMax;
+          apart |= odd_v & 0x01010101u * kOddFar;
+          back = apart == 0;
           float top = ml;
 #pragma unroll
           for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, c[tt][i] * kf[2 * tt + (i >> 3)]);
+            for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, w[tt][i] * kf[2 * tt + (i >> 3)]);
           top = __builtin_fmaxf(top, __shfl_xor(top, 32));
           l *= __builtin_amdgcn_exp2f(ml - top);
           ml = top;
 #pragma unroll
-          for (int gr = 0; gr < kPrGroups; ++gr) {
-            float sum = 0.0f;
+          for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              sum += __builtin_amdgcn_exp2f(__builtin_fmaf(c[gr >> 1][8 * (gr & 1) + i], kf[gr], -top));
-            l += sum;
-            lf[gr] = 0.0f;
+            for (int i = 0; i < 16; ++i)
+              l += __builtin_amdgcn_exp2f(__builtin_fmaf(w[tt][i], kf[2 * tt + (i >> 3)], -top));
+#pragma unroll
+          for (int gr = 0; gr < kPrGroups; ++gr) lf[gr] = 0.0f;
+        }
+        if (wide) {
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const f32x4 f = *(const f32x4*)&sh.tf[buf][8 * y + 4 * half];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[y >> 2][4 * (y & 3) + i] += odd_v >> (8 * (y >> 1)) & kOddWide ? f[i] + (9.0f - m) : vf[y >> 1];
           }
+#pragma unroll
+          for (int gr = 0; gr < kPrGroups; ++gr) vf[gr] = 0.0f;
         }
       }
       float top = -__builtin_inff();
@@ -1365,23 +1412,23 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int gr = 2 * tt + (i >> 3);
-          c[tt][i] = __builtin_fmaf(c[tt][i], kf[gr], vf[gr]);
-          top = __builtin_fmaxf(top, c[tt][i]);
+          w[tt][i] = __builtin_fmaf(w[tt][i], kf[gr], vf[gr]);
+          top = __builtin_fmaxf(top, w[tt][i]);
         }
-      if (__any(top > limit)) {   // the maximum moves
+      if (__any(top > limit) || __builtin_expect(back != 0, 0)) {   // the maximum moves
         top = __builtin_fmaxf(top, __shfl_xor(top, 32));
         const bool fresh = limit != 15.0f, any = top > kNoMax;
         const float up = any ? fresh ? top - 9.0f : __builtin_fmaxf(top - 9.0f, 0.0f) : 0.0f;
         const float shrink = fresh ? 0.0f : __builtin_amdgcn_exp2f(-up);
         m += up;
         limit = any ? 15.0f : limit;
-        l *= apart ? 1.0f : shrink;
+        if (!apart) l *= back ? __builtin_amdgcn_exp2f(ml - (limit == 15.0f ? m : kNoMax)) : shrink;
 #pragma unroll
         for (int j = 0; j < DT; ++j) o[j] *= shrink;
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) c[tt][i] -= up;
+          for (int i = 0; i < 16; ++i) w[tt][i] -= up;
       }
 #pragma unroll
       for (int gr = 0; gr < kPrGroups; ++gr) {
@@ -1389,7 +1436,7 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float e = __builtin_amdgcn_exp2f(c[gr >> 1][8 * (gr & 1) + i]);
+          const float e = __builtin_amdgcn_exp2f(w[gr >> 1][8 * (gr & 1) + i]);
           sum += e;
           p[i] = (_Float16)e;
         }

@@ -42,6 +42,7 @@ SPREADS = {
     "large rows, then zero ones": lambda t, n: 50 if t < n // 2 else None,
     "from the smallest to the largest": lambda t, n: -120 + 240 * t // n,
     "from the largest to the smallest": lambda t, n: 120 - 240 * t // n,
+    "the ends of the range": lambda t, n: 125 if t % 16 == 3 else -95,
     "zero rows only": lambda t, n: None,
     "large rows only": lambda t, n: 120,
 }
@@ -76,3 +77,56 @@ def test_the_sum_of_weights_over_many_workgroups(spread):
     for b, (_, n) in enumerate(s.lens):
         _rewrite(s, b, g.standard_normal((n, 4, 128)) * 0.4, _sized(g, n, 4, 128, SPREADS[spread]))
     s.check(*s.run(), rows=2, every=2)
+
+
+@pytest.mark.parametrize("gap", [14, 19, 24, 28, 29, 33, 40, 70, 130])
+@pytest.mark.parametrize("nq,n,hq,h,d", [(150, 160, 1, 1, 64), (140, 300, 2, 1, 128), (200, 200, 1, 1, 256),
+                                         (130, 2500, 2, 1, 128), (3, 50, 2, 1, 128)])
+def test_value_rows_far_apart_in_sixteen_tokens(gap, nq, n, hq, h, d):
+    """A row 2^gap larger than the others of its 16 tokens; the queries before it see the others
+    alone, and so do some behind it, which give it next to no weight."""
+    s = Seqs([(nq, n)], hq, h, d, 16, gap)
+    g = np.random.default_rng(gap)
+    k, v = g.standard_normal((n, h, d)) * 0.3, g.standard_normal((n, h, d))
+    q = g.standard_normal((max(s.tq, 1), hq, d))
+    big = np.arange(5, n, 32)
+    v[big] *= 2.0 ** min(gap, 120)
+    v[big + 1 if big[-1] + 1 < n else big[:-1] + 1] *= 2.0 ** (min(gap, 120) - gap)
+    k[..., 0], q[..., 0] = 0.0, 0.0
+    k[big, :, 0] = -80.0                     # logits far below the others for the queries with a large element 0
+    q[::2, :, 0] = 4.0 * d ** 0.5
+    _rewrite(s, 0, k, v)
+    _queries(s, q)
+    s.check(*s.run(), rows=20)
+
+
+@pytest.mark.parametrize("gap", [14, 18, 19, 24, 28, 29, 33, 40, 70])
+@pytest.mark.parametrize("nq,n,hq,h,d", [(150, 160, 1, 1, 64), (140, 300, 2, 1, 128), (200, 200, 1, 1, 256),
+                                         (130, 2500, 2, 1, 128), (3, 50, 2, 1, 128)])
+def test_key_rows_far_apart_in_sixteen_tokens(gap, nq, n, hq, h, d):
+    """Key rows 2^gap smaller than one of their 16, which lies across all queries (logit 0)."""
+    s = Seqs([(nq, n)], hq, h, d, 16, gap)
+    g = np.random.default_rng(gap)
+    k, q = g.standard_normal((n, h, d)) * 2.0 ** -gap, g.standard_normal((max(s.tq, 1), hq, d)) * 2.0 ** gap
+    q[..., :16] = 0.0
+    k[5::16] = 0.0
+    k[5::16, :, 3] = 4.0
+    _rewrite(s, 0, k, g.standard_normal((n, h, d)))
+    _queries(s, q)
+    s.check(*s.run(), rows=20)
+
+
+def test_prompt_rows_beside_a_nan_token():
+    """Small values in the 16 tokens of a NaN token, which the checked queries do not see."""
+    s = Seqs([(100, 160)], 2, 1, 128, 16, 8)
+    g = np.random.default_rng(8)
+    k, v = g.standard_normal((160, 1, 128)), g.standard_normal((160, 1, 128)) * 2.0 ** -40
+    _rewrite(s, 0, k, v)
+    bad = _bits(k[:1])
+    bad[0, 0, 9] = 0x7FC0
+    slot = torch.from_numpy(okv.sequence_slots(s.table[0], 160, 16)[140:141]).to(DEV)
+    ql.kv_store_nvfp4(to_dev(bad), to_dev(_bits(v[:1])), slot, s.cache)
+    out, lse = s.run()
+    s.data = s.cache.data.cpu().numpy()
+    assert torch.isnan(out[80:]).all() and torch.isnan(lse[80:]).all()
+    s.check(out, lse, only=[0, 3, 60, 70, 75, 78, 79])
