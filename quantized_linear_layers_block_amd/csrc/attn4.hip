@@ -922,14 +922,14 @@ __global__ __launch_bounds__(256) void attn4_join_kernel(Attn4 a, int tiles) {
 // codes of the tile after are on their way in registers meanwhile.
 //
 // The rows' exponents go into the f16 values here, relative to the largest of each 16 tokens,
-// E for keys and F for values: khat 2^(ek - E + 4), vhat 2^(ev - F + 4), at most 43008 and exact for rows down
-// to 2^-18 of the largest.  A logit then takes one
-// fused multiply-add with factors of its group, w = (acc kc 2^(E - 4)) + F, where a factor a
-// token would cost two more of some nine vector instructions a logit, and the vector
-// instructions (the exponential takes four of them) weigh as much as the matrix products.
-// Sixteen tokens with rows further apart are held relative to their own exponents (E = ek, F = ev
-// for each), and the tiles that have some take the longer way with factors a token: tokens that a
-// query does not see are among the 16, and must not cost it the ones that it sees.
+// E for keys and F for values: khat 2^(ek - E + 4), vhat 2^(ev - F + 4), at most 43008 and exact for
+// rows down to 2^-18 of the largest.  A logit then takes one fused multiply-add with factors of its
+// group, w = (acc kc 2^(E - 4)) + F, where a factor a token would cost two more of some nine vector
+// instructions a logit, and the vector instructions (the exponential takes four of them) weigh as
+// much as the matrix products.  Sixteen tokens with rows further apart (2^18 for keys, 2^5 for
+// values) are held relative to their own exponents (E = ek, F = ev for each), and the tiles that have
+// some take the longer way with factors a token: tokens that a query does not see are among the 16,
+// and must not cost it the ones that it sees.
 //
 // At D = 128 a prompt of 8192 tokens, 28/4 heads, takes 501 us (960 TFLOP/s of the products that are seen;
 // a library product reaches 1390), with the matrix units busy for 45% of the cycles and the vector
@@ -958,9 +958,12 @@ int prompt_parts(int64_t units, int d) {
 __host__ __device__ constexpr size_t prompt_part_bytes(int d) { return (size_t)prompt_rows(d) * (d + 2) * 4; }
 
 // What keeps a tile from the short way: a group that is left out; an ev outside the window that l may
-// share; rows further apart than kPrGap.
+// share; rows further apart than the gaps.  Keys are exact to 2^18.  F joins the logits, so m
+// follows it: where the row that sets F is one that a query does not see, or that has no weight, all its other
+// weights would lose F - ev of the bits below f16's smallest normal.  With 2^5 that is 2^-28 of the largest
+// weighted value a token at most.
 constexpr uint32_t kOddOut = 1, kOddFar = 2, kOddWide = 4;
-constexpr uint32_t kPrKeyGap = 18, kPrValueGap = 18;
+constexpr uint32_t kPrKeyGap = 18, kPrValueGap = 5;
 
 template <int D>
 struct PromptShared {

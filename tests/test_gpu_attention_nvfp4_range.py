@@ -9,8 +9,8 @@ import pytest
 import torch
 
 from oracle import kvcache_nvfp4 as okv
-from oracle.codecs import f32_to_bf16_bits_rne
-from tests.helpers import DEV, to_dev
+from oracle.codecs import bf16_bits_to_f32, f32_to_bf16_bits_rne
+from tests.helpers import DEV, bf16_bits_of, to_dev
 from tests.test_gpu_attention_nvfp4 import Seqs
 
 pytestmark = pytest.mark.gpu
@@ -130,3 +130,78 @@ def test_prompt_rows_beside_a_nan_token():
     s.data = s.cache.data.cpu().numpy()
     assert torch.isnan(out[80:]).all() and torch.isnan(lse[80:]).all()
     s.check(out, lse, only=[0, 3, 60, 70, 75, 78, 79])
+
+
+def _check_seen(s, out, lse, window, picks):
+    """Query rows `picks` of the one sequence, with a bound that takes only what a row sees.  A weight's
+    rounding below f16's smallest normal is at most 2^-25 against p = 2^(logit + F - m + 9) of the
+    token that set m.  A token's share of out is p vhat 2^(ev - F + 4) 2^-13 2^m / sum 2^logit, with
+    vhat 2^(ev - F + 4) <= 43008: so it is off by at most 2^-22.6 2^m / sum 2^logit.  m = logit + F of a token a
+    that the row sees, F is at most 2^5 above the exponent of a's own row, and that row's largest value is 1260 2^ev
+    or more: 2^(-22.6 + 5 - 10.3) = 2^-27.9 of the weight of a times its largest value, a token seen."""
+    (nq, n), = s.lens
+    qf = bf16_bits_to_f32(s.q_bits).astype(np.float64)
+    o, z = bf16_bits_to_f32(bf16_bits_of(out)).astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    k, v = okv.load(s.data, okv.sequence_slots(s.table[0], n, s.page), s.d)
+    for i in picks:
+        hi = n - nq + i + 1
+        lo = max(hi - window, 0) if window else 0
+        ro, rz, am = okv.attention(qf[i][None], k[lo:hi], v[lo:hi], s.d ** -0.5)
+        for j in range(s.hq):
+            g = j // (s.hq // s.h)
+            w = np.exp(s.d ** -0.5 * (k[lo:hi, g] @ qf[i, j]) - rz[0, j])
+            share = (w * np.abs(v[lo:hi, g]).max(axis=1)).max()
+            tol = 2.0 ** -8 * np.abs(ro[0, j]) + (2.0 ** -11 + 2.0 ** -12) * am[0, j] + (hi - lo) * 2.0 ** -27 * share + 1e-30
+            err = np.abs(o[i, j] - ro[0, j])
+            assert (err <= tol).all(), (i, j, err.max(), tol[err > tol].min())
+            assert abs(z[i, j] - rz[0, j]) <= 2.0 ** -16 + 2.0 ** -20 * abs(rz[0, j])
+
+
+@pytest.mark.parametrize("gap", [3, 5, 6, 10, 17, 18, 19, 27, 34, 60, 115])
+@pytest.mark.parametrize("nq,n,hq,h,d", [(150, 160, 1, 1, 64), (140, 300, 2, 1, 128), (200, 200, 1, 1, 256),
+                                         (130, 2500, 2, 1, 128), (3, 50, 2, 1, 128)])
+@pytest.mark.parametrize("window", [0, 40])
+def test_large_values_that_a_query_does_not_see(gap, nq, n, hq, h, d, window):
+    """Value rows 2^gap larger than all others in the same 16 tokens as the last (or, with a window,
+    the first) ones that a query sees; and seen ones that get no weight.  They must not take bits
+    from the weights of the tokens in other groups."""
+    s = Seqs([(nq, n)], hq, h, d, 16, gap)
+    g = np.random.default_rng(gap)
+    k, v, q = g.standard_normal((n, h, d)), g.standard_normal((n, h, d)), g.standard_normal((s.tq, hq, d))
+    k[..., 0], q[..., 0] = 0.0, 12.0 * d ** 0.5
+    first = n - nq + 20     # from here on seen by later queries only
+    big = np.arange(first // 16 * 16 + 13, n, 48)
+    v[big] *= 2.0 ** gap
+    k[big, :, 0] = -20.0    # a logit of -240: no weight where they are seen
+    _rewrite(s, 0, k, v)
+    _queries(s, q)
+    out, lse = s.run(window=window)
+    near = [b - (n - nq) + x for b in big[:4] for x in (-13, -5, -1, 0, 1, window + 1, window + 3)]
+    picks = sorted({i for i in near if 0 <= i < nq} | {0, nq // 2, nq - 1})
+    _check_seen(s, out, lse, window, picks)
+
+
+@pytest.mark.parametrize("gap", [3, 5, 6, 8, 12, 14, 16, 17, 22])
+@pytest.mark.parametrize("nq,n,d", [(150, 1000, 64), (140, 1400, 128), (200, 1500, 256), (130, 4000, 128)])
+@pytest.mark.parametrize("window", [0, 700])
+def test_many_small_weights_behind_a_large_value_row_that_does_not_count(gap, nq, n, d, window):
+    """One token with a weight of 2^10 in the 16 of the large row, and a thousand of weight 1 behind it
+    that carry half of the output: all rounded alike, so that lost bits add up.  The large row is before the
+    window, or has no weight."""
+    s = Seqs([(nq, n)], 1, 1, d, 16, gap)
+    g = np.random.default_rng(gap)
+    first = n - nq + 45 - (window or n - nq)   # of the tokens that query 44 sees through the window
+    big = (first + 15) // 16 * 16 + 3
+    i0 = 44 + big - first + 1                  # the first query that does not see it
+    k, q = np.zeros((n, 1, d)), np.zeros((s.tq, 1, d))
+    q[:, 0, 1] = d ** 0.5 * (1 + g.integers(0, 8, s.tq) / 64)
+    q[:, 0, 2] = d ** 0.5
+    k[big + 8, 0, 1] = 7.0
+    k[big, 0, 2] = 0.0 if window else -200.0
+    v = 1 + 0.1 * g.standard_normal((n, 1, d))
+    v[big + 8] *= -1
+    v[big] = 1.6 * 2.0 ** gap
+    _rewrite(s, 0, k, v)
+    _queries(s, q)
+    out, lse = s.run(window=window)
+    _check_seen(s, out, lse, window, range(i0, i0 + 8))
