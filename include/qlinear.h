@@ -447,7 +447,9 @@ typedef struct {
  * token gets zeros and lse -inf.  Query tokens of no sequence keep their out and lse.
  * Products are f16 x f16 with float32 sums: q is scaled by a power of two a row (exact but for
  * magnitudes below about 2^-29 of the row's largest), the cache's values are exact, and the
- * softmax weights are rounded to f16 (2^-11) before they meet the values.
+ * softmax weights are rounded to f16 (2^-11) before they meet the values; a weight that f16 holds
+ * less of is off by at most 2^-27 of the largest (weight times value) that the row sees.  Logits are float32:
+ * one above its range gives the row NaN, one below it a weight of 0.
  * Results are bitwise reproducible for the same arguments, also as a graph's replays.
  * Workspace: qlinear_attention_nvfp4_workspace(...) bytes with qlinear_forward's layout and
  * reuse rules (zero-filled before its first use; calls that share it must not overlap, which

@@ -36,6 +36,19 @@ constexpr float kNoMax = -3.0e38f;  // m before any token was seen; exp2(-inf - 
 // The window of ev that l and the sums of values share one maximum in (exponent bytes).
 constexpr uint32_t kEvLow = 81, kEvSpan = 64;
 
+// A logit is acc * (scale 2^e) * 2^ek, e the query row's exponent.  The factors meet in float32 where
+// |scale 2^e| is in [kRowLow, kRowHigh]; the waves with a row outside of it form scale 2^(e + ek) in
+// one step, no larger than float32 holds: acc is 0 for a key at right angles to the row, whatever their sizes.
+constexpr float kRowLow = 0x1p-110f, kRowHigh = 0x1p9f;
+__device__ __forceinline__ bool row_at_ends(float factor) {
+  const float f = __builtin_fabsf(factor);
+  return f < kRowLow || f > kRowHigh;
+}
+__device__ __forceinline__ float far_factor(float scale, int e, float key_power) {
+  const int ek = (int)(__float_as_uint(key_power) >> 23) - 127;
+  return __builtin_amdgcn_fmed3f(__builtin_ldexpf(scale, e + ek), -3.4e38f, 3.4e38f);
+}
+
 // 2^(d / 2) for d <= 0: l is multiplied by it twice, since 2^d alone may be 0 where l 2^d counts.
 __device__ __forceinline__ float half_power(float d) { return __builtin_amdgcn_exp2f(0.5f * d); }
 
@@ -502,6 +515,7 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
   // the query row as f16 with its largest magnitude in [2^14, 2^15)
   f16x8 q[KW];
   float kc;
+  uint32_t at_ends;
   {
     uint32_t amax = 0;
 #pragma unroll
@@ -514,6 +528,11 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
     amax = umax(amax, (uint32_t)__shfl_xor((int)amax, 32));
     const int e = amax ? (int)(amax >> 7) - 127 - 14 : 0;   // subnormal rows: -141, still exact
     kc = __builtin_ldexpf(a.scale_log2e, e);
+    at_ends = __any(row_at_ends(kc) && a.scale_log2e != 0.0f && amax < kBf16InfBits);
+    if (__builtin_expect(at_ends, 0)) {
+      sh.l[wave][rn] = __int_as_float(e);   // (not in use before the waves' sums are joined)
+      kc = 1.0f;
+    }
     if (amax >= kBf16InfBits) kc = __builtin_nanf("");
 #pragma unroll
     for (int s = 0; s < KW; ++s) {
@@ -551,6 +570,16 @@ __device__ __forceinline__ void attn4_unit(const Attn4& a, AttnPlace& pl, const 
         const f16x2 sp = both((s >> 1) < 2 ? s01[(s >> 1) & 1] : s23[(s >> 1) & 1]);
         c[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(scaled8(f[u].k[s], sp, sp, sp, sp), q[s], c[u], 0, 0, 0);
       }
+    }
+    if (__builtin_expect(at_ends, 0)) {   // the sums become logits here
+      const int e = __float_as_int(sh.l[wave][rn]);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[u][i] *= far_factor(a.scale_log2e, e, sh.x[wave][u][4 * g + i]);
+      __builtin_amdgcn_wave_barrier();
+      if (g == 0) sh.x[wave][0][n16] = sh.x[wave][1][n16] = 1.0f;
+      __builtin_amdgcn_wave_barrier();
     }
     // which of its 8 tokens this lane's row sees
     uint32_t seen = 0xFFu, off[2];   // off: of ev from the window, in the lanes past 15, which hold value rows' exponents
@@ -1264,7 +1293,7 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
   // the query rows as f16 with their largest magnitude in [2^14, 2^15) and the scale's sign, so that
   // kc > 0 and a logit of -inf stays -inf; a row with Inf or NaN is NaN throughout
   f16x8 q[KS];
-  float kc;
+  float kc, ke2;
   {
     const uint16_t* qp = a.q + (rg.q0 + qrow) * a.q_stride + (int64_t)head * D + half * 8;
     uint32_t amax = 0;
@@ -1277,7 +1306,11 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
     }
     amax = umax(amax, (uint32_t)__shfl_xor((int)amax, 32));
     const int e = amax ? (int)(amax >> 7) - 127 - 14 : 0;
-    kc = a.scale_log2e == 0.0f ? 1.0f : __builtin_ldexpf(__builtin_fabsf(a.scale_log2e), e);
+    // scale 2^e in two factors, each with half the exponent: neither product with 2^(E - 4) leaves
+    // float32 on the way to a number inside it
+    const int x2 = e + __builtin_amdgcn_frexp_expf(a.scale_log2e);
+    kc = a.scale_log2e == 0.0f ? 1.0f : __builtin_ldexpf(__builtin_fabsf(__builtin_amdgcn_frexp_mantf(a.scale_log2e)), x2 - (x2 >> 1));
+    ke2 = __builtin_ldexpf(1.0f, x2 >> 1);
     const float sign = amax >= kBf16InfBits ? __builtin_nanf("") : a.scale_log2e > 0.0f ? 1.0f : a.scale_log2e < 0.0f ? -1.0f : 0.0f;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
@@ -1342,11 +1375,13 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
       for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[tt][i] = c[tt][i];
+      // below 1e-37 a logit is 0; at most what float32 holds, for a key at right angles to the row (acc 0)
+      const auto factor = [&](float ke) { return __builtin_amdgcn_fmed3f(ke * ke2 * kc, 1e-37f, 3.4e38f); };
       float kf[kPrGroups], vf[kPrGroups], lf[kPrGroups];
 #pragma unroll
       for (int gr = 0; gr < kPrGroups; ++gr) {
         const float ke = sh.ke[buf][gr];
-        kf[gr] = __builtin_fmaxf(ke * kc, 1e-37f);   // (below it a logit is 0)
+        kf[gr] = factor(ke);
         const float2 vv = sh.vf[buf][gr];
         vf[gr] = vv.x + (9.0f - m);
         lf[gr] = vv.y;
@@ -1372,7 +1407,7 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               w[y >> 2][4 * (y & 3) + i] *=
-                  odd_k >> (8 * (y >> 1)) & kOddWide ? __builtin_fmaxf(ke[i] * kc, 1e-37f) : kf[y >> 1];
+                  odd_k >> (8 * (y >> 1)) & kOddWide ? factor(ke[i]) : kf[y >> 1];
           }
 #pragma unroll
           for (int gr = 0; gr < kPrGroups; ++gr) kf[gr] = 1.0f;

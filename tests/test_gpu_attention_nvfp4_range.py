@@ -205,3 +205,33 @@ def test_many_small_weights_behind_a_large_value_row_that_does_not_count(gap, nq
     _queries(s, q)
     out, lse = s.run(window=window)
     _check_seen(s, out, lse, window, range(i0, i0 + 8))
+
+
+# (log2 of the queries, of the keys that meet them, of the ones that lie across them, softmax scale)
+ENDS = {"large queries, small keys": (100, -98, 120, 0.125), "small queries, large keys": (-131, 124, -120, 3.0),
+        "large both, across": (120, -119, 126, 0.3), "a large scale": (-60, -50, 0, 2.0 ** 108),
+        "a small scale": (70, 50, 40, 2.0 ** -119), "a small negative scale": (70, 50, 40, -2.0 ** -119),
+        "the smallest queries": (-133, 127, 100, 16.0)}
+
+
+@pytest.mark.parametrize("ends", ENDS)
+@pytest.mark.parametrize("nq,n,hq,h,d", [(1, 60, 4, 2, 128), (3, 200, 8, 1, 64), (5, 333, 16, 8, 256), (1, 9000, 2, 1, 64),
+                                         (150, 170, 2, 2, 128), (140, 300, 2, 1, 64), (200, 200, 1, 1, 256),
+                                         (130, 2500, 2, 1, 128)])
+def test_queries_and_keys_at_the_ends_of_their_range(ends, nq, n, hq, h, d):
+    """Products of ordinary size of factors that float32 cannot hold the scales of, beside keys
+    that a query is at right angles to (logit 0)."""
+    eq, ek, across, scale = ENDS[ends]
+    s = Seqs([(nq, n)], hq, h, d, 16, nq + d)
+    g = np.random.default_rng(n)
+    # (queries of one binade and few bits: the smallest bf16 hold them exactly)
+    q = (1 + g.integers(0, 2, (s.tq, hq, d)) / 2) * g.choice([-1.0, 1.0], (s.tq, hq, d))
+    k = g.standard_normal((n, h, d)) * 0.3
+    k[..., :16], q[..., :16] = 0.0, 0.0
+    q[..., 16:24] = 1.0
+    k[3::7] = 0.0
+    q, k = np.ldexp(q, eq), np.ldexp(k, ek)
+    k[3::7, :, 5] = 2.0 ** across
+    _rewrite(s, 0, k, g.standard_normal((n, h, d)))
+    _queries(s, q)
+    s.check(*s.run(softmax_scale=scale), scale=scale, rows=8)
