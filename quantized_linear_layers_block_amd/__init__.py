@@ -265,7 +265,7 @@ class KVCacheNVFP4:
 # Checks of the cache's calls.  A decode step makes several of them a layer, so they are few
 # attribute reads each; the messages are put together only when one fails.
 _BF16, _I32 = torch.bfloat16, torch.int32
-_device_now = torch._C._cuda_getDevice   # (called where a tensor is on the GPU: it is initialised)
+_device_now = None   # (looked up by the first call on the GPU; a PyTorch for hosts alone has none)
 
 
 def _refuse(device, dtype, name, t, what):
@@ -300,6 +300,9 @@ def _check_dense(device, dtype, name, t, shape):
 
 def _call_on(device, fn, *args):
     """fn(*args) with `device` current, on its current stream."""
+    global _device_now
+    if _device_now is None:
+        _device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     if _device_now() == device.index:
         return fn(*args)
     with torch.cuda.device(device):

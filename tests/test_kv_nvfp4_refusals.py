@@ -98,3 +98,17 @@ def test_helpers_refuse_host_tensors_and_wrong_sizes():
         ql.kv_load_nvfp4(c, slots)
     with pytest.raises(ValueError):
         ql.attention_nvfp4(x, c, torch.zeros((3, 1), dtype=torch.int32), torch.ones(3, dtype=torch.int32))
+
+
+def test_package_imports_with_a_pytorch_for_hosts_alone():
+    """The size queries and refusals need no GPU, nor the PyTorch internals of a GPU build."""
+    import os
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "if hasattr(torch._C, '_cuda_getDevice'): del torch._C._cuda_getDevice\n"
+            "import quantized_linear_layers_block_amd as ql\n"
+            "assert ql.KVCacheNVFP4.empty(2, 2, 64, 16, device='cpu').data.numel() == 2 * 2 * (18 * 64 + 32)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
