@@ -353,7 +353,10 @@ def attention_nvfp4(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None
     (int32 [B + 1]) sequence b has tokens [q_starts[b], q_starts[b + 1]), at most max_q_len.
     softmax_scale defaults to 1 / sqrt(D).  causal aligns the last query with the last cached
     token; window > 0 keeps the last `window` tokens.  lse (float32 [Tq, Hq]) is filled if
-    given.  ws: a zero-filled workspace kept from call to call, as forward's."""
+    given.  ws: a zero-filled workspace kept from call to call, as forward's; without one the
+    call makes its own, and with it goes the status word that tells of pages, lengths and
+    q_starts outside their bounds (the call leaves them out).  No query tokens: an empty
+    result, nothing is launched."""
     dev = _cache_device(cache)
     if q.dim() != 3 or q.shape[2] != cache.head_dim:
         raise ValueError(f"q must be [tokens, heads, {cache.head_dim}]")
@@ -380,6 +383,10 @@ def attention_nvfp4(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None
         _check_rows(dev, "out", out, shape)
     if lse is not None:
         _check_dense(dev, torch.float32, "lse", lse, (tq, hq))
+    if tq == 0:
+        if hq == 0 or hq % cache.heads:
+            raise ValueError(f"q must have a multiple of {cache.heads} heads")
+        return out
     if ws is None:
         ws = _ws(binding.qlinear_attention_nvfp4_workspace(batch, tq, hq, cache.heads, d, max_q_len), dev)
     elif ws.device != dev or not ws.is_contiguous():

@@ -1,0 +1,37 @@
+"""Calls of the NVFP4 attention helper at the edge of what its arguments allow."""
+import pytest
+import torch
+
+from tests.helpers import DEV
+
+pytestmark = pytest.mark.gpu
+
+ql = pytest.importorskip("quantized_linear_layers_block_amd")
+
+
+@pytest.mark.parametrize("batch,starts", [(0, False), (0, True), (3, True), (3, False)])
+def test_no_query_tokens(batch, starts):
+    """As store and load of no tokens: nothing is launched, an empty result."""
+    cache = ql.KVCacheNVFP4.empty(2, 2, 64, 16, device=DEV)
+    q = torch.empty((0, 4, 64), dtype=torch.bfloat16, device=DEV)
+    table = torch.zeros((batch, 1), dtype=torch.int32, device=DEV)
+    lens = torch.ones(batch, dtype=torch.int32, device=DEV)
+    kw = dict(q_starts=torch.zeros(batch + 1, dtype=torch.int32, device=DEV), max_q_len=4) if starts else {}
+    lse = torch.empty((0, 4), dtype=torch.float32, device=DEV)
+    out = ql.attention_nvfp4(q, cache, table, lens, lse=lse, **kw)
+    assert out.shape == (0, 4, 64) and out.dtype == torch.bfloat16
+    given = torch.empty_like(q)
+    assert ql.attention_nvfp4(q, cache, table, lens, out=given, **kw) is given
+    # the arguments are still looked at
+    with pytest.raises(TypeError):
+        ql.attention_nvfp4(q, cache, table, lens.to(torch.int64), **kw)
+    with pytest.raises(ValueError):
+        ql.attention_nvfp4(torch.empty((0, 3, 64), dtype=torch.bfloat16, device=DEV), cache, table, lens, **kw)
+
+
+def test_queries_of_no_sequence_are_refused():
+    cache = ql.KVCacheNVFP4.empty(2, 2, 64, 16, device=DEV)
+    q = torch.zeros((2, 4, 64), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ql.QlinearError):
+        ql.attention_nvfp4(q, cache, torch.zeros((0, 1), dtype=torch.int32, device=DEV),
+                           torch.zeros(0, dtype=torch.int32, device=DEV))
