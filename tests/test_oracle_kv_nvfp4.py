@@ -83,3 +83,30 @@ def test_attention_closed_forms():
     # more queries than keys: the first rows see nothing
     out, lse, _ = okv.attention(np.zeros((3, 1, d)), np.zeros((1, 1, d)), v[:1], 1.0)
     assert not out[:2].any() and np.isneginf(lse[:2]).all() and np.allclose(out[2, 0], v[0, 0])
+
+
+@pytest.mark.parametrize("nq,n,hq,h", [(1, 7, 4, 2), (5, 40, 8, 2), (9, 9, 6, 6), (12, 30, 7, 1), (30, 12, 4, 4)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 4)])
+def test_attention_against_a_library_softmax(nq, n, hq, h, causal, window):
+    """Scale, logits, grouping of heads, masks and lse, by whole matrices in PyTorch's float64."""
+    torch = pytest.importorskip("torch")
+    d = 64
+    g = np.random.default_rng(nq * n)
+    q, k, v = g.standard_normal((nq, hq, d)), g.standard_normal((n, h, d)), g.standard_normal((n, h, d))
+    held = g.random(n) < 0.8
+    out, lse, mean = okv.attention(q, k, v, 0.3, causal, window, held)
+    pos, tok = torch.arange(n - nq, n)[:, None], torch.arange(n)[None]
+    mask = torch.from_numpy(held)[None].expand(nq, n).clone()
+    if causal:
+        mask &= tok <= pos
+    if window:
+        mask &= pos - tok < window
+    tq, tk, tv = (torch.from_numpy(x).transpose(0, 1) for x in (q, k, v))
+    tk, tv = (x.repeat_interleave(hq // h, dim=0) for x in (tk, tv))
+    s = (tq @ tk.transpose(1, 2)).mul(0.3).masked_fill(~mask, float("-inf"))
+    p = torch.softmax(s, dim=-1).nan_to_num(0.0)            # rows that see nothing: zeros
+    assert np.allclose(out, (p @ tv).transpose(0, 1).numpy(), rtol=1e-12, atol=1e-13)
+    assert np.allclose(mean, (p @ tv.abs()).transpose(0, 1).numpy(), rtol=1e-12, atol=1e-13)
+    assert np.allclose(lse, torch.logsumexp(s, dim=-1).transpose(0, 1).numpy(), rtol=1e-12, atol=1e-12)
+    seen = mask.any(dim=-1).numpy()
+    assert np.isneginf(lse[~seen]).all() and not out[~seen].any() and np.isfinite(lse[seen]).all()
