@@ -1350,6 +1350,8 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
       }
     }
     if (busy && t0 < end_w && t0 + kPrTok > begin_w) {
+      const uint2 odd2 = *(const uint2*)sh.odd[buf];   // (under way during the products)
+      __builtin_amdgcn_sched_barrier(0);
       f32x16 c[2];
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
@@ -1386,7 +1388,6 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
         vf[gr] = vv.x + (9.0f - m);
         lf[gr] = vv.y;
       }
-      const uint2 odd2 = *(const uint2*)sh.odd[buf];
       const uint32_t odd_k = (uint32_t)__builtin_amdgcn_readfirstlane((int)odd2.x);
       const uint32_t odd_v = (uint32_t)__builtin_amdgcn_readfirstlane((int)odd2.y);
       uint32_t back = 0;   // l is relative to ml in this tile alone
