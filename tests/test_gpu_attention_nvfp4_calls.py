@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from tests.helpers import DEV
+from tests.test_gpu_attention_nvfp4 import Seqs
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +36,10 @@ def test_queries_of_no_sequence_are_refused():
     with pytest.raises(ql.QlinearError):
         ql.attention_nvfp4(q, cache, torch.zeros((0, 1), dtype=torch.int32, device=DEV),
                            torch.zeros(0, dtype=torch.int32, device=DEV))
+
+
+def test_numbers_that_pass_32_bits_are_refused():
+    s = Seqs([(1, 20)], 2, 1, 64, 16, 7)
+    for kw in (dict(window=1 << 31), dict(window=4 - (1 << 32)), dict(max_q_len=(1 << 32) + 1), dict(max_q_len=1 - (1 << 32))):
+        with pytest.raises((ValueError, ql.QlinearError)):
+            ql.attention_nvfp4(s.q, s.cache, s.pt, s.kv_lens, **kw)
