@@ -451,6 +451,8 @@ typedef struct {
  * less of is off by at most 2^-27 of the largest (weight times value) that the row sees.  Logits are float32:
  * one above its range gives the row NaN, one below it a weight of 0.
  * Results are bitwise reproducible for the same arguments, also as a graph's replays.
+ * out may be q itself, with the same stride (each row is read before it is written); else they must not
+ * overlap.  Sequences may share pages.
  * Workspace: qlinear_attention_nvfp4_workspace(...) bytes with qlinear_forward's layout and
  * reuse rules (zero-filled before its first use; calls that share it must not overlap, which
  * includes replays of graphs captured on it).

@@ -356,7 +356,7 @@ def attention_nvfp4(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None
     given.  ws: a zero-filled workspace kept from call to call, as forward's; without one the
     call makes its own, and with it goes the status word that tells of pages, lengths and
     q_starts outside their bounds (the call leaves them out).  No query tokens: an empty
-    result, nothing is launched."""
+    result, nothing is launched.  out may be q itself."""
     dev = _cache_device(cache)
     if q.dim() != 3 or q.shape[2] != cache.head_dim:
         raise ValueError(f"q must be [tokens, heads, {cache.head_dim}]")
