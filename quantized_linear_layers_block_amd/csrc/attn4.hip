@@ -198,9 +198,9 @@ __device__ __forceinline__ f16x2 both(_Float16 s) { return f16x2{s, s}; }
 // a unit that lies in more than one workgroup's part is joined from partial results.
 //
 // Decoding is bound by the cache's bytes: 256 sequences of up to 4096 tokens, 64/8 heads of 128, take
-// 131 us for 620 MB (4.7 TB/s; a large copy moves 5.2), where the same kernel with its loads alone
+// 132 us for 620 MB (4.7 TB/s; a large copy moves 5.2), where the same kernel with its loads alone
 // takes 129; 64 of them 54 us, 53 with the loads alone.  Pages in the order of memory in place of
-// scattered ones would give 116 and 45.  One sequence of 613 tokens, 8.7 us, is the latency of the
+// scattered ones would give 116 and 45.  One sequence of 613 tokens, 8.9 us, is the latency of the
 // chain: cut, page, codes, joins in the workgroup and between workgroups.
 constexpr int kAttnStep = 32;                        // tokens of one wave's step
 constexpr int kAttnChunk = kAttnWaves * kAttnStep;   // of the workgroup's
@@ -960,11 +960,15 @@ __global__ __launch_bounds__(256) void attn4_join_kernel(Attn4 a, int tiles) {
 // some take the longer way with factors a token: tokens that a query does not see are among the 16,
 // and must not cost it the ones that it sees.
 //
-// At D = 128 a prompt of 8192 tokens, 28/4 heads, takes 501 us (960 TFLOP/s of the products that are seen;
-// a library product reaches 1390), with the matrix units busy for 45% of the cycles and the vector
-// units for 50%.  More overlap lowers the clock instead (from 2.4 to 2.1 GHz and less, as the chip
-// nears its power): the products and exponentials of two tiles interleaved in a wave gave 903, waves
-// in two halves half a tile apart 920, tiles of 128 tokens 976, 64 rows a wave 703 TFLOP/s.
+// At D = 128 a prompt of 8192 tokens, 28/4 heads, takes 505 us (952 TFLOP/s of the products that are
+// seen; a library product reaches 1390), with the matrix units busy for 39% of the cycles and the
+// vector units for 45%: little of the two overlaps.  Three ways to overlap more took more cycles than they
+// saved (4 x 512 tokens behind 16384, against 1005 TFLOP/s in the same runs; matrix and vector units busy
+// and clock on the prompt of 8192, against 41%, 45% and 1.94 GHz): products and exponentials of two tiles
+// interleaved in a wave 907 (34%, 41%, 2.07), waves in two halves half a tile apart 912 (34%, 40%, 2.05),
+// 64 rows a wave 699 (25%, 39%, 2.25).  Tiles of 128 tokens gave 976 against 990.
+// The longer way costs nothing where few tiles take it (518 us with four small value rows at the start
+// of the 8192) and twice the time where all do (values spread over 2^10 in every 16 tokens: 1056).
 constexpr int kPrTok = 64, kPrGroups = kPrTok / 16;
 // Waves of a workgroup, and workgroups of a CU: at D = 128 eight waves, two a SIMD; at D = 64 three
 // workgroups of four (40 sequences of up to 333 tokens in a window of 1024: 71 us against 88 with
