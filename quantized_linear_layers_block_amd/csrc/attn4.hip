@@ -967,8 +967,8 @@ __global__ __launch_bounds__(256) void attn4_join_kernel(Attn4 a, int tiles) {
 // and clock on the prompt of 8192, against 41%, 45% and 1.94 GHz): products and exponentials of two tiles
 // interleaved in a wave 907 (34%, 41%, 2.07), waves in two halves half a tile apart 912 (34%, 40%, 2.05),
 // 64 rows a wave 699 (25%, 39%, 2.25).  Tiles of 128 tokens gave 976 against 990.
-// The longer way costs nothing where few tiles take it (518 us with four small value rows at the start
-// of the 8192) and twice the time where all do (values spread over 2^10 in every 16 tokens: 1056).
+// The longer way costs nothing where few tiles take it (508 us with four small value rows at the start
+// of the 8192) and 1.6 times the time where all do (values spread over 2^10 in every 16 tokens: 836).
 constexpr int kPrTok = 64, kPrGroups = kPrTok / 16;
 // Waves of a workgroup, and workgroups of a CU: at D = 128 eight waves, two a SIMD; at D = 64 three
 // workgroups of four (40 sequences of up to 333 tokens in a window of 1024: 71 us against 88 with
@@ -1396,14 +1396,16 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
       const uint32_t odd_v = (uint32_t)__builtin_amdgcn_readfirstlane((int)odd2.y);
       uint32_t back = 0;   // l is relative to ml in this tile alone
       if (__builtin_expect((odd_k | odd_v) != 0 || apart || t0 < all_from || t0 + kPrTok > all_to, 0)) {
-        // a logit that the row does not see becomes -inf
+        if ((odd_k & 0x01010101u * kOddOut) || t0 < all_from || t0 + kPrTok > all_to) {
+          // a logit that the row does not see becomes -inf
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
+          for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int t = t0 + 32 * tt + 8 * (i >> 2) + 4 * half + (i & 3);
-            if (!(t >= from && t < to && sh.ke[buf][2 * tt + (i >> 3)] != 0.0f)) w[tt][i] = -__builtin_inff();
-          }
+            for (int i = 0; i < 16; ++i) {
+              const int t = t0 + 32 * tt + 8 * (i >> 2) + 4 * half + (i & 3);
+              if (!(t >= from && t < to && sh.ke[buf][2 * tt + (i >> 3)] != 0.0f)) w[tt][i] = -__builtin_inff();
+            }
+        }
         const bool wide = ((odd_k | odd_v) & 0x01010101u * kOddWide) != 0;
         if (wide) {
 #pragma unroll
@@ -1458,14 +1460,14 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
           w[tt][i] = __builtin_fmaf(w[tt][i], kf[gr], vf[gr]);
           top = __builtin_fmaxf(top, w[tt][i]);
         }
-      if (__any(top > limit) || __builtin_expect(back != 0, 0)) {   // the maximum moves
+      if (__any(top > limit)) {   // the maximum moves
         top = __builtin_fmaxf(top, __shfl_xor(top, 32));
         const bool fresh = limit != 15.0f, any = top > kNoMax;
         const float up = any ? fresh ? top - 9.0f : __builtin_fmaxf(top - 9.0f, 0.0f) : 0.0f;
         const float shrink = fresh ? 0.0f : __builtin_amdgcn_exp2f(-up);
         m += up;
         limit = any ? 15.0f : limit;
-        if (!apart) l *= back ? __builtin_amdgcn_exp2f(ml - (limit == 15.0f ? m : kNoMax)) : shrink;
+        if (!apart && !back) l *= shrink;
 #pragma unroll
         for (int j = 0; j < DT; ++j) o[j] *= shrink;
 #pragma unroll
@@ -1473,6 +1475,7 @@ __global__ __launch_bounds__(prompt_waves(D) * 64, prompt_waves(D) * prompt_wgs_
 #pragma unroll
           for (int i = 0; i < 16; ++i) w[tt][i] -= up;
       }
+      if (__builtin_expect(back != 0, 0)) l *= __builtin_amdgcn_exp2f(ml - (limit == 15.0f ? m : kNoMax));
 #pragma unroll
       for (int gr = 0; gr < kPrGroups; ++gr) {
         f16x8 p;
