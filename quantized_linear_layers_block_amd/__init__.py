@@ -375,7 +375,7 @@ def attention_nvfp4(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None
             raise ValueError("q_starts needs max_q_len")
     elif max_q_len is None:
         max_q_len = tq // max(batch, 1)
-    if max(max_q_len, window) > 0x7FFFFFFF or min(max_q_len, window) < -0x80000000:
+    if not (-0x80000000 <= max_q_len <= 0x7FFFFFFF and -0x80000000 <= window <= 0x7FFFFFFF):
         raise ValueError("max_q_len and window are 32-bit numbers")
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=_BF16, device=dev)
