@@ -448,8 +448,8 @@ typedef struct {
  * Products are f16 x f16 with float32 sums: q is scaled by a power of two a row (exact but for
  * magnitudes below about 2^-29 of the row's largest), the cache's values are exact, and the
  * softmax weights are rounded to f16 (2^-11) before they meet the values; a weight that f16 holds
- * less of is off by at most 2^-27 of the largest (weight times value) that the row sees.  Logits are float32:
- * one above its range gives the row NaN, one below it a weight of 0.
+ * less of is off by at most 2^-27 of the largest (weight times value) that the row sees.  Logits are
+ * float32: one above its range gives the row NaN, one below it has no weight.
  * Results are bitwise reproducible for the same arguments, also as a graph's replays.
  * out may be q itself, with the same stride (each row is read before it is written); else they must not
  * overlap.  Sequences may share pages.

@@ -235,3 +235,30 @@ def test_queries_and_keys_at_the_ends_of_their_range(ends, nq, n, hq, h, d):
     _rewrite(s, 0, k, g.standard_normal((n, h, d)))
     _queries(s, q)
     s.check(*s.run(softmax_scale=scale), scale=scale, rows=8)
+
+
+@pytest.mark.parametrize("nq,n,d", [(1, 60, 128), (3, 200, 64), (2, 9000, 64), (150, 170, 128), (130, 2500, 64), (200, 200, 256)])
+@pytest.mark.parametrize("eq,ek", [(100, 60), (20, 118)])
+def test_logits_beyond_float32(nq, n, d, eq, ek):
+    """A key whose logit is below float32 has no weight and changes nothing else; one whose logit is above it
+    gives the queries that see it NaN, and no others."""
+    s = Seqs([(nq, n)], 1, 1, d, 16, nq + d)
+    g = np.random.default_rng(n)
+    q, k = np.zeros((s.tq, 1, d)), np.zeros((n, 1, d))
+    q[..., :4], q[..., 16:] = 2.0 ** eq, 2.0 ** eq * g.choice([-1.0, 1.0], (s.tq, 1, d - 16))
+    k[..., 16:] = g.standard_normal((n, 1, d - 16)) * 2.0 ** -eq
+    low, high = 5, n - 3
+    k[low] = 0.0
+    k[low, 0, 2] = -2.0 ** ek
+    v = g.standard_normal((n, 1, d))
+    _rewrite(s, 0, k, v)
+    _queries(s, q)
+    s.check(*s.run(softmax_scale=1.0), scale=1.0, rows=12)
+    k[high] = 0.0
+    k[high, 0, 1] = 2.0 ** ek
+    _rewrite(s, 0, k, v)
+    out, lse = s.run(softmax_scale=1.0)
+    first = max(high - (n - nq), 0)
+    assert torch.isnan(out[first:]).all() and torch.isnan(lse[first:]).all()
+    if first:
+        s.check(out, lse, scale=1.0, only=sorted({0, first // 2, first - 1}))
