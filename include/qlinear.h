@@ -476,6 +476,47 @@ qlinear_status qlinear_attention_nvfp4(const qlinear_kv_nvfp4* cache, const qlin
 size_t qlinear_attention_nvfp4_workspace(int32_t batch, int64_t total_q, int32_t q_heads, int32_t heads,
                                          int32_t head_dim, int32_t max_q_len);
 
+/* ------------------------------------------- norm with the residual's addition */
+
+/* Root-mean-square norm of a residual stream, with the output in the form that the next layer
+ * takes (mexc.co NeMo RL FP8 page, "De technische doorbraak": norms stay in higher precision, the
+ * linear layers behind them take E4M3 activations with a scale for 1x128):
+ *   h = bf16_RNE(x + residual)   (h = x without a residual)
+ *   y[i][j] = h[i][j] * s_i * weight[j],   s_i = 1 / sqrt(mean_j h[i][j]^2 + eps)
+ * x, residual bf16 [m][k], row i at x + i * x_stride (elements, multiples of 8); weight bf16 [k].
+ * h bf16 (NULL without a residual if not wanted) may be x or residual itself, with that one's
+ * stride; else the buffers must not overlap.  Outputs, one at least:
+ *   y  bf16 [m][k], dense;
+ *   yq u8 [m][k] E4M3 with sy [m][k/128], for qlinear_forward_fp8_prequant and
+ *      qlinear_gated_forward: format QL_FP8_BLOCK128 (sy float32, amax/448) or QL_FP8_POW2 (sy E8M0
+ *      bytes), quantized from the float32 values of y: code = sign | E4M3 of |y| / sy (formed as a
+ *      product with sy's reciprocal, within 2^-23).  A segment that holds an Inf or NaN has the
+ *      scale NaN (0xFF), so every product with it is NaN.
+ * Sums are float32; squares beyond its range are summed scaled down.  k is a multiple of 8 (of 128
+ * with yq) up to 65536.  No workspace.
+ * Errors: QL_ERR_NULL (x, weight, both outputs, yq without sy, a residual without h), QL_ERR_SHAPE
+ * (m <= 0, m > QLINEAR_MAX_M, k, a stride < k or not a multiple of 8, sizes beyond
+ * QLINEAR_MAX_ELEMS), QL_ERR_ARG (eps not positive and finite), QL_ERR_FORMAT (with yq),
+ * QL_ERR_ALIGN. */
+qlinear_status qlinear_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual, int64_t residual_stride,
+                                const uint16_t* weight, float eps, int64_t m, int64_t k, uint16_t* h, int64_t h_stride,
+                                uint16_t* y, int32_t format, uint8_t* yq, void* sy, void* stream);
+
+/* Backward pass of qlinear_rms_norm (the quantization to 8 bits passes gradients unchanged), from
+ * dy = dL/dy, the forward's h, and dh = the gradient that reaches h beside the norm (NULL: none):
+ *   dx[i][j] = dh[i][j] + s_i (a_j - h[i][j] s_i^2 mean_j(a_j h[i][j])),   a_j = dy[i][j] weight[j]
+ *   dweight[j] = sum_i dy[i][j] h[i][j] s_i                   (float32 [k]; NULL: not wanted)
+ * dx bf16 is the gradient of x and of the residual alike; it may be dy or dh itself, with that
+ * one's stride.  All bf16 [m][k] with strides as above; sums are float32, in a fixed order.
+ * Workspace (with dweight): qlinear_rms_norm_backward_workspace(m, k) bytes of scratch, which need
+ * no zeroing and may be reused by any call once this one has finished on its stream.
+ * Errors as qlinear_rms_norm, and QL_ERR_WORKSPACE. */
+qlinear_status qlinear_rms_norm_backward(const uint16_t* dy, int64_t dy_stride, const uint16_t* h, int64_t h_stride,
+                                         const uint16_t* weight, float eps, const uint16_t* dh, int64_t dh_stride,
+                                         int64_t m, int64_t k, uint16_t* dx, int64_t dx_stride, float* dweight,
+                                         void* ws, size_t ws_bytes, void* stream);
+size_t qlinear_rms_norm_backward_workspace(int64_t m, int64_t k);
+
 #ifdef __cplusplus
 }
 #endif

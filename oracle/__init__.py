@@ -25,10 +25,12 @@ What it computes (each module cites the passage it follows):
   (token, head) vector, scattered to and gathered from cache slots.
 * ``backward`` -- the layer's backward pass with the NVFP4 base frozen: dX through the
   dequantized weight and the adapter, and the adapter's gradients dA, dB, in float64.
+* ``block``   -- what stands around the layers in a decoder block: the norm with the residual's
+  addition, the gated feed-forward block, and their backward passes, in float64.
 
 Quantizer arithmetic is IEEE float32 with round-to-nearest-even, because that is
 where the codes are decided and the GPU decides them in float32 too; every
 GEMM and every dequantized value is float64.
 """
 
-from . import codecs, nvfp4, fp8, gemm, requant, update, kvcache, backward  # noqa: F401
+from . import codecs, nvfp4, fp8, gemm, requant, update, kvcache, backward, block  # noqa: F401

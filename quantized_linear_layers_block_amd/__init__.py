@@ -20,7 +20,7 @@ from .binding import (QL_FP8_BLOCK128, QL_FP8_POW2, QL_NVFP4, QL_OUT_BF16, QL_OU
 __all__ = ["NVFP4Weight", "FP8Weight", "quantize_nvfp4", "quantize_fp8_block", "quantize_act_fp8",
            "forward", "forward_fp8_prequant", "RequantTable", "QlinearError", "binding", "workspace_status",
            "quantize_fp8_pow2", "kv_store_fp8", "kv_load_fp8", "KVCacheNVFP4", "kv_store_nvfp4", "kv_load_nvfp4",
-           "attention_nvfp4"]
+           "attention_nvfp4", "rms_norm", "rms_norm_fp8", "rms_norm_backward"]
 
 
 def _dev(t):
@@ -394,3 +394,91 @@ def attention_nvfp4(q, cache, page_table, kv_lens, q_starts=None, max_q_len=None
     _call_on(dev, binding.qlinear_attention_nvfp4, cache.handle, q, page_table, kv_lens, out, ws, q_starts, max_q_len,
              d ** -0.5 if softmax_scale is None else softmax_scale, causal, window, lse)
     return out
+
+
+# ------------------------------------------------------------------------ norm
+
+_U8, _F32 = torch.uint8, torch.float32
+
+
+def _check_matrix(device, name, t, shape):
+    # dense rows; rows may be apart
+    if t.shape != shape or t.dtype is not _BF16 or t.device != device:
+        _refuse(device, _BF16, name, t, f"of the shape {tuple(shape)}")
+    if not t.is_contiguous() and shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have dense rows")
+
+
+def _norm_inputs(x, weight, residual, h):
+    # checks what both forms of the norm share: (device, h to write or None)
+    dev = _dev(x).device
+    if x.dim() != 2:
+        raise ValueError("x must be [tokens, k]")
+    shape = x.shape
+    _check_matrix(dev, "x", x, shape)
+    _check_dense(dev, _BF16, "weight", weight, shape[1:])
+    if residual is not None:
+        _check_matrix(dev, "residual", residual, shape)
+        if h is None:
+            h = torch.empty(shape, dtype=_BF16, device=dev)
+    if h is not None:
+        _check_matrix(dev, "h", h, shape)
+    return dev, h
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None, h=None, out=None):
+    """y = h / sqrt(mean(h^2) + eps) * weight of bf16 rows [T, k], h = bf16(x + residual): y, or
+    (y, h) with a residual.  h (given, it is written also without one) may be x or residual itself;
+    y is written into out if given."""
+    dev, hs = _norm_inputs(x, weight, residual, h)
+    if out is None:
+        out = torch.empty(x.shape, dtype=_BF16, device=dev)
+    else:
+        _check_dense(dev, _BF16, "out", out, x.shape)
+    _call_on(dev, binding.qlinear_rms_norm, x, weight, eps, residual, hs, out)
+    return out if residual is None else (out, hs)
+
+
+def rms_norm_fp8(x, weight, eps=1e-6, residual=None, pow2=False, h=None, y=None):
+    """rms_norm with an output in 8 bits for the FP8 layers: (yq, sy), or (yq, sy, h) with a
+    residual; yq uint8 [T, k] E4M3 codes, sy float32 [T, k / 128] (pow2: uint8 E8M0 bytes).  y
+    (bf16 [T, k]), if given, is written too, for an adapter or a weight gradient."""
+    dev, hs = _norm_inputs(x, weight, residual, h)
+    m, k = x.shape
+    if y is not None:
+        _check_dense(dev, _BF16, "y", y, x.shape)
+    yq = torch.empty((m, k), dtype=_U8, device=dev)
+    sy = torch.empty((m, k // 128), dtype=_U8 if pow2 else _F32, device=dev)
+    _call_on(dev, binding.qlinear_rms_norm, x, weight, eps, residual, hs, y, QL_FP8_POW2 if pow2 else QL_FP8_BLOCK128,
+             yq, sy)
+    return (yq, sy) if residual is None else (yq, sy, hs)
+
+
+def rms_norm_backward(dy, h, weight, eps=1e-6, dh=None, dx=None, need_dweight=True, ws=None):
+    """Gradients of rms_norm: (dx, dweight).  dy is the gradient of y, h what the forward
+    normalised, dh the gradient that reaches h beside the norm (added to dx).  dx (bf16; dy or dh
+    itself if wanted) is the gradient of x and of the residual; dweight is float32 [k], None
+    without need_dweight.  ws: scratch kept from step to step."""
+    dev = _dev(dy).device
+    if dy.dim() != 2:
+        raise ValueError("dy must be [tokens, k]")
+    shape = dy.shape
+    m, k = shape
+    _check_matrix(dev, "dy", dy, shape)
+    _check_matrix(dev, "h", h, shape)
+    _check_dense(dev, _BF16, "weight", weight, shape[1:])
+    if dh is not None:
+        _check_matrix(dev, "dh", dh, shape)
+    if dx is None:
+        dx = torch.empty(shape, dtype=_BF16, device=dev)
+    else:
+        _check_matrix(dev, "dx", dx, shape)
+    dweight = None
+    if need_dweight:
+        dweight = torch.empty((k,), dtype=_F32, device=dev)
+        if ws is None:
+            ws = torch.empty((max(1, binding.qlinear_rms_norm_backward_workspace(m, k)),), dtype=_U8, device=dev)
+        elif ws.device != dev or not ws.is_contiguous():
+            _refuse(dev, ws.dtype, "ws", ws, "contiguous")
+    _call_on(dev, binding.qlinear_rms_norm_backward, dy, h, weight, eps, dx, dh, dweight, ws if need_dweight else None)
+    return dx, dweight

@@ -48,6 +48,9 @@ EXPORTS = [
     "qlinear_kv_load_nvfp4",
     "qlinear_attention_nvfp4",
     "qlinear_attention_nvfp4_workspace",
+    "qlinear_rms_norm",
+    "qlinear_rms_norm_backward",
+    "qlinear_rms_norm_backward_workspace",
 ]
 
 QLINEAR_STATUS_NONFINITE, QLINEAR_STATUS_TIMEOUT, QLINEAR_STATUS_BAD_ITEM = 1, 2, 4
@@ -135,6 +138,9 @@ def _load():
         "qlinear_attention_nvfp4": ([ctypes.POINTER(KvNvfp4), ctypes.POINTER(AttnBatch), vp, i64, i32, f32, i32, i32,
                                      vp, i64, vp, vp, sz, vp], i32),
         "qlinear_attention_nvfp4_workspace": ([i32, i64, i32, i32, i32, i32], sz),
+        "qlinear_rms_norm": ([vp, i64, vp, i64, vp, f32, i64, i64, vp, i64, vp, i32, vp, vp, vp], i32),
+        "qlinear_rms_norm_backward": ([vp, i64, vp, i64, vp, f32, vp, i64, i64, i64, vp, i64, vp, vp, sz, vp], i32),
+        "qlinear_rms_norm_backward_workspace": ([i64, i64], sz),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -391,6 +397,36 @@ def qlinear_attention_nvfp4(cache, q, page_table, kv_lens, out, ws, q_starts=Non
                                      _stream_here() if stream is None else stream)
     if st:
         raise QlinearError(st, "qlinear_attention_nvfp4")
+
+
+# ------------------------------------------------------------------------ norm
+
+def _rows(t):
+    # data pointer and row stride; the stride of a single row is left open by PyTorch
+    return (None, 0) if t is None else (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def qlinear_rms_norm(x, weight, eps, residual=None, h=None, y=None, fmt=0, yq=None, sy=None, stream=None):
+    """x, residual, h bf16 [m, k] (dense rows, any row stride); y bf16 [m, k] and/or yq u8 [m, k] with sy."""
+    m, k = x.shape
+    st = LIB.qlinear_rms_norm(*_rows(x), *_rows(residual), weight.data_ptr(), eps, m, k, *_rows(h), _ptr(y), fmt,
+                              _ptr(yq), _ptr(sy), _stream_here() if stream is None else stream)
+    if st:
+        raise QlinearError(st, "qlinear_rms_norm")
+
+
+def qlinear_rms_norm_backward_workspace(m, k):
+    return LIB.qlinear_rms_norm_backward_workspace(m, k)
+
+
+def qlinear_rms_norm_backward(dy, h, weight, eps, dx, dh=None, dweight=None, ws=None, stream=None):
+    """dy, h, dh, dx bf16 [m, k] (dense rows, any row stride); dweight f32 [k] or None."""
+    m, k = dy.shape
+    st = LIB.qlinear_rms_norm_backward(*_rows(dy), *_rows(h), weight.data_ptr(), eps, *_rows(dh), m, k, *_rows(dx),
+                                       _ptr(dweight), _ptr(ws), 0 if ws is None else ws.nbytes,
+                                       _stream_here() if stream is None else stream)
+    if st:
+        raise QlinearError(st, "qlinear_rms_norm_backward")
 
 
 def qlinear_status_word(ws):

@@ -609,4 +609,86 @@ qlinear_status qlinear_attention_nvfp4(const qlinear_kv_nvfp4* cache, const qlin
   return hip_status(ql::launch_attn4(a, c.head_dim, (hipStream_t)stream));
 }
 
+// ------------------------------------------------------- root-mean-square norm
+
+// Sizes and eps that both directions share.
+static qlinear_status check_norm(int64_t m, int64_t k, float eps) {
+  if (m <= 0 || m > QLINEAR_MAX_M || k <= 0 || k % 8 || k > ql::kNormMaxK) return QL_ERR_SHAPE;
+  if (!(eps > 0.0f) || !__builtin_isfinite(eps)) return QL_ERR_ARG;
+  return QL_OK;
+}
+
+qlinear_status qlinear_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual, int64_t residual_stride,
+                                const uint16_t* weight, float eps, int64_t m, int64_t k, uint16_t* h, int64_t h_stride,
+                                uint16_t* y, int32_t format, uint8_t* yq, void* sy, void* stream) {
+  if (!x || !weight || (!y && !yq) || (residual && !h)) return QL_ERR_NULL;
+  const qlinear_status st = check_norm(m, k, eps);
+  if (st != QL_OK) return st;
+  if (yq) {
+    if (!is_fp8(format)) return QL_ERR_FORMAT;
+    if (!sy) return QL_ERR_NULL;
+    if (k % 128) return QL_ERR_SHAPE;
+  }
+  if (!rows_ok(m, x_stride, k) || (residual && !rows_ok(m, residual_stride, k)) || (h && !rows_ok(m, h_stride, k)))
+    return QL_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(h) || !aligned16(y) || !aligned16(yq) ||
+      (yq && !aligned16(sy)))
+    return QL_ERR_ALIGN;
+  ql::Norm a;
+  a.x = x;
+  a.x_stride = x_stride;
+  a.r = residual;
+  a.r_stride = residual_stride;
+  a.w = weight;
+  a.eps = eps;
+  a.m = m;
+  a.k = k;
+  a.h = h;
+  a.h_stride = h_stride;
+  a.y = y;
+  a.yq = yq;
+  a.sy = sy;
+  ql::clear_hip_error();
+  return hip_status(ql::launch_rms_norm(a, !yq ? 0 : format == QL_FP8_POW2 ? 2 : 1, (hipStream_t)stream));
+}
+
+size_t qlinear_rms_norm_backward_workspace(int64_t m, int64_t k) {
+  return check_norm(m, k, 1.0f) == QL_OK ? ql::rms_norm_backward_bytes(m, k) : 0;
+}
+
+qlinear_status qlinear_rms_norm_backward(const uint16_t* dy, int64_t dy_stride, const uint16_t* h, int64_t h_stride,
+                                         const uint16_t* weight, float eps, const uint16_t* dh, int64_t dh_stride,
+                                         int64_t m, int64_t k, uint16_t* dx, int64_t dx_stride, float* dweight,
+                                         void* ws, size_t ws_bytes, void* stream) {
+  if (!dy || !h || !weight || !dx) return QL_ERR_NULL;
+  const qlinear_status st = check_norm(m, k, eps);
+  if (st != QL_OK) return st;
+  if (!rows_ok(m, dy_stride, k) || !rows_ok(m, h_stride, k) || (dh && !rows_ok(m, dh_stride, k)) ||
+      !rows_ok(m, dx_stride, k))
+    return QL_ERR_SHAPE;
+  if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(dh) || !aligned16(dx) || !aligned16(dweight))
+    return QL_ERR_ALIGN;
+  if (dweight) {
+    if (!ws || ws_bytes < ql::rms_norm_backward_bytes(m, k)) return QL_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QL_ERR_ALIGN;
+  }
+  ql::NormBackward a;
+  a.dy = dy;
+  a.dy_stride = dy_stride;
+  a.h = h;
+  a.h_stride = h_stride;
+  a.w = weight;
+  a.eps = eps;
+  a.dh = dh;
+  a.dh_stride = dh_stride;
+  a.m = m;
+  a.k = k;
+  a.dx = dx;
+  a.dx_stride = dx_stride;
+  a.dw = dweight;
+  a.part = dweight ? (float*)ws : nullptr;
+  ql::clear_hip_error();
+  return hip_status(ql::launch_rms_norm_backward(a, (hipStream_t)stream));
+}
+
 }  // extern "C"

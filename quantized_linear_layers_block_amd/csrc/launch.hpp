@@ -214,4 +214,40 @@ hipError_t launch_gemm_fp8(const uint8_t* xq, const void* sx, int64_t m, int64_t
                            const uint16_t* lora_b, int32_t rank, void* y, int out_f32,
                            hipStream_t s);
 
+// ---- root-mean-square norm with the residual's addition, and its backward pass (norm.hip);
+// k % 8 == 0, strides in elements (multiples of 8), 16-byte aligned rows
+constexpr int64_t kNormMaxK = 65536;
+struct Norm {
+  const uint16_t* x;
+  int64_t x_stride;
+  const uint16_t* r;        // residual, or null
+  int64_t r_stride;
+  const uint16_t* w;
+  float eps;
+  int64_t m, k;
+  uint16_t* h;              // x + r, or null
+  int64_t h_stride;
+  uint16_t* y;              // bf16 [m][k], or null
+  uint8_t* yq;              // with fmt 1 (float32 scales) or 2 (powers of two): E4M3 [m][k]
+  void* sy;                 // [m][k / 128]
+};
+hipError_t launch_rms_norm(const Norm& a, int fmt, hipStream_t s);
+struct NormBackward {
+  const uint16_t* dy;
+  int64_t dy_stride;
+  const uint16_t* h;
+  int64_t h_stride;
+  const uint16_t* w;
+  float eps;
+  const uint16_t* dh;       // or null
+  int64_t dh_stride;
+  int64_t m, k;
+  uint16_t* dx;
+  int64_t dx_stride;
+  float* dw;                // float32 [k], or null
+  float* part;              // rms_norm_backward_bytes with dw, else null
+};
+size_t rms_norm_backward_bytes(int64_t m, int64_t k);
+hipError_t launch_rms_norm_backward(const NormBackward& a, hipStream_t s);
+
 }  // namespace ql
