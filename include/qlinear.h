@@ -517,6 +517,32 @@ qlinear_status qlinear_rms_norm_backward(const uint16_t* dy, int64_t dy_stride, 
                                          void* ws, size_t ws_bytes, void* stream);
 size_t qlinear_rms_norm_backward_workspace(int64_t m, int64_t k);
 
+/* ---------------------------------------------------- gated feed-forward block */
+
+/* The first half of a decoder layer's feed-forward block on FP8 weights, as one kernel (mexc.co
+ * NeMo RL FP8 page, "De technische doorbraak": FP8 linear layers with a scale for 128x128 weights
+ * and 1x128 activations, the nonlinearity between them in higher precision):
+ *   g = x Wg^T,  u = x Wu^T,  h = g / (1 + exp(-g)) * u        (float32 sums and values)
+ * gate, up (host structs): FP8 weights [n][k] of the same format and sizes.  xq u8 [m][k] with sx
+ * [m][k/128]: activations already quantized in that format (qlinear_rms_norm, or
+ * qlinear_quantize_act_fp8[_pow2]).  Outputs, all dense; h or hq at least:
+ *   h  bf16 [m][n];
+ *   hq u8 [m][n] E4M3 with sh [m][n/128] (float32, or E8M0 bytes for QL_FP8_POW2), quantized from
+ *      the float32 values of h as qlinear_rms_norm's yq: the down projection's
+ *      qlinear_forward_fp8_prequant takes them;
+ *   gu bf16 [m][2n] (NULL: not wanted): g, then u, in every row, for qlinear_gated_backward.
+ * No adapter; NVFP4 layers take qlinear_forward_group.  Workspace:
+ * qlinear_gated_forward_workspace(m, n, k) bytes with qlinear_forward's layout and reuse rules
+ * (zero-filled before its first use; calls that share it must not overlap, which includes replays
+ * of graphs captured on it).
+ * Errors: QL_ERR_NULL, QL_ERR_FORMAT (not FP8, or two formats), QL_ERR_SHAPE (m <= 0, m >
+ * QLINEAR_MAX_M, weights of different sizes, n or k not multiples of 128, k >= 2^24, sizes beyond
+ * QLINEAR_MAX_ELEMS or a launch), QL_ERR_ALIGN, QL_ERR_WORKSPACE. */
+qlinear_status qlinear_gated_forward(const qlinear_qweight* gate, const qlinear_qweight* up, const uint8_t* xq,
+                                     const void* sx, int64_t m, uint16_t* h, uint8_t* hq, void* sh, uint16_t* gu,
+                                     void* ws, size_t ws_bytes, void* stream);
+size_t qlinear_gated_forward_workspace(int64_t m, int64_t n, int64_t k);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,7 +20,8 @@ from .binding import (QL_FP8_BLOCK128, QL_FP8_POW2, QL_NVFP4, QL_OUT_BF16, QL_OU
 __all__ = ["NVFP4Weight", "FP8Weight", "quantize_nvfp4", "quantize_fp8_block", "quantize_act_fp8",
            "forward", "forward_fp8_prequant", "RequantTable", "QlinearError", "binding", "workspace_status",
            "quantize_fp8_pow2", "kv_store_fp8", "kv_load_fp8", "KVCacheNVFP4", "kv_store_nvfp4", "kv_load_nvfp4",
-           "attention_nvfp4", "rms_norm", "rms_norm_fp8", "rms_norm_backward"]
+           "attention_nvfp4", "rms_norm", "rms_norm_fp8", "rms_norm_backward",
+           "gated_forward", "gated_forward_fp8"]
 
 
 def _dev(t):
@@ -482,3 +483,56 @@ def rms_norm_backward(dy, h, weight, eps=1e-6, dh=None, dx=None, need_dweight=Tr
             _refuse(dev, ws.dtype, "ws", ws, "contiguous")
     _call_on(dev, binding.qlinear_rms_norm_backward, dy, h, weight, eps, dx, dh, dweight, ws if need_dweight else None)
     return dx, dweight
+
+
+# --------------------------------------------------- gated feed-forward block
+
+def _gated_weights(gate, up):
+    # the device of a block's weights
+    if not isinstance(gate, FP8Weight) or not isinstance(up, FP8Weight):
+        raise TypeError("the gated block takes FP8 weights")
+    if gate.n != up.n or gate.k != up.k or gate.pow2 != up.pow2:
+        raise ValueError("gate and up must be alike in sizes and scales")
+    dev = _dev(gate.codes).device
+    for w in (gate, up):
+        _check_dense(dev, _U8, "codes", w.codes, (w.n, w.k))
+        _check_dense(dev, _U8 if w.pow2 else _F32, "scales", w.scales, (w.n // 128, w.k // 128))
+    return dev
+
+
+def _gated_call(gate, up, xq, sx, h, hq, sh, gu, ws):
+    dev = _gated_weights(gate, up)
+    if xq.dim() != 2:
+        raise ValueError("xq must be [tokens, k]")
+    m = xq.shape[0]
+    _check_dense(dev, _U8, "xq", xq, (m, gate.k))
+    _check_dense(dev, gate.scales.dtype, "sx", sx, (m, gate.k // 128))
+    if h is not None:
+        _check_dense(dev, _BF16, "h", h, (m, gate.n))
+    if gu is not None:
+        _check_dense(dev, _BF16, "gu", gu, (m, 2 * gate.n))
+    if ws is None:
+        ws = _ws(binding.qlinear_gated_forward_workspace(m, gate.n, gate.k), dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        _refuse(dev, ws.dtype, "ws", ws, "contiguous")
+    _call_on(dev, binding.qlinear_gated_forward, gate.qweight(), up.qweight(), xq, sx, ws, h, hq, sh, gu)
+
+
+def gated_forward(gate, up, xq, sx, h=None, gu=None, ws=None):
+    """h = silu(x Wg^T) * (x Wu^T), bf16 [T, n], from FP8 weights and activations quantized like them
+    (rms_norm_fp8, quantize_act_fp8).  gu (bf16 [T, 2n]), if given, gets both products, for
+    gated_backward.  ws: a zero-filled workspace kept from call to call, as forward's."""
+    if h is None:
+        h = torch.empty((xq.shape[0], gate.n), dtype=_BF16, device=xq.device)
+    _gated_call(gate, up, xq, sx, h, None, None, gu, ws)
+    return h
+
+
+def gated_forward_fp8(gate, up, xq, sx, h=None, gu=None, ws=None):
+    """gated_forward with an output in 8 bits for the down projection's forward_fp8_prequant:
+    (hq uint8 [T, n], sh [T, n / 128]); h (bf16 [T, n]), if given, is written too."""
+    m = xq.shape[0]
+    hq = torch.empty((m, gate.n), dtype=_U8, device=xq.device)
+    sh = torch.empty((m, gate.n // 128), dtype=_U8 if gate.pow2 else _F32, device=xq.device)
+    _gated_call(gate, up, xq, sx, h, hq, sh, gu, ws)
+    return hq, sh

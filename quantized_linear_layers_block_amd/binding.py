@@ -51,6 +51,8 @@ EXPORTS = [
     "qlinear_rms_norm",
     "qlinear_rms_norm_backward",
     "qlinear_rms_norm_backward_workspace",
+    "qlinear_gated_forward",
+    "qlinear_gated_forward_workspace",
 ]
 
 QLINEAR_STATUS_NONFINITE, QLINEAR_STATUS_TIMEOUT, QLINEAR_STATUS_BAD_ITEM = 1, 2, 4
@@ -141,6 +143,9 @@ def _load():
         "qlinear_rms_norm": ([vp, i64, vp, i64, vp, f32, i64, i64, vp, i64, vp, i32, vp, vp, vp], i32),
         "qlinear_rms_norm_backward": ([vp, i64, vp, i64, vp, f32, vp, i64, i64, i64, vp, i64, vp, vp, sz, vp], i32),
         "qlinear_rms_norm_backward_workspace": ([i64, i64], sz),
+        "qlinear_gated_forward": ([ctypes.POINTER(QWeight), ctypes.POINTER(QWeight), vp, vp, i64, vp, vp, vp, vp, vp,
+                                   sz, vp], i32),
+        "qlinear_gated_forward_workspace": ([i64, i64, i64], sz),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -427,6 +432,21 @@ def qlinear_rms_norm_backward(dy, h, weight, eps, dx, dh=None, dweight=None, ws=
                                        _stream_here() if stream is None else stream)
     if st:
         raise QlinearError(st, "qlinear_rms_norm_backward")
+
+
+# --------------------------------------------------- gated feed-forward block
+
+def qlinear_gated_forward_workspace(m, n, k):
+    return LIB.qlinear_gated_forward_workspace(m, n, k)
+
+
+def qlinear_gated_forward(gate, up, xq, sx, ws, h=None, hq=None, sh=None, gu=None, stream=None):
+    """gate, up QWeight; xq u8 [m, k], sx -> h bf16 [m, n] and/or hq u8 [m, n] with sh, gu bf16 [m, 2n]."""
+    st = LIB.qlinear_gated_forward(ctypes.byref(gate), ctypes.byref(up), xq.data_ptr(), sx.data_ptr(), xq.shape[0],
+                                   _ptr(h), _ptr(hq), _ptr(sh), _ptr(gu), ws.data_ptr(), ws.nbytes,
+                                   _stream_here() if stream is None else stream)
+    if st:
+        raise QlinearError(st, "qlinear_gated_forward")
 
 
 def qlinear_status_word(ws):

@@ -691,4 +691,57 @@ qlinear_status qlinear_rms_norm_backward(const uint16_t* dy, int64_t dy_stride, 
   return hip_status(ql::launch_rms_norm_backward(a, (hipStream_t)stream));
 }
 
+// ---------------------------------------------------- gated feed-forward block
+
+// The two weights of a block: FP8 of one kind and of the same sizes.
+static qlinear_status check_gated_weights(const qlinear_qweight* gate, const qlinear_qweight* up) {
+  qlinear_status st = check_qweight(gate);
+  if (st != QL_OK) return st;
+  st = check_qweight(up);
+  if (st != QL_OK) return st;
+  if (!is_fp8(gate->format) || up->format != gate->format) return QL_ERR_FORMAT;
+  return up->n == gate->n && up->k == gate->k ? QL_OK : QL_ERR_SHAPE;
+}
+
+static bool gated_sizes_ok(int64_t m, int64_t n, int64_t k) {
+  return m > 0 && m <= QLINEAR_MAX_M && elems_ok(n, k) && elems_ok(m, k) && n <= QLINEAR_MAX_ELEMS / 2 / m;
+}
+
+size_t qlinear_gated_forward_workspace(int64_t m, int64_t n, int64_t k) {
+  if (!gated_sizes_ok(m, n, k) || !ql::gated_launchable(m, n, k)) return 0;
+  return ql::kWsReserved + ql::gated_scratch_bytes(m, n);
+}
+
+qlinear_status qlinear_gated_forward(const qlinear_qweight* gate, const qlinear_qweight* up, const uint8_t* xq,
+                                     const void* sx, int64_t m, uint16_t* h, uint8_t* hq, void* sh, uint16_t* gu,
+                                     void* ws, size_t ws_bytes, void* stream) {
+  const qlinear_status st = check_gated_weights(gate, up);
+  if (st != QL_OK) return st;
+  if (!xq || !sx || (!h && !hq) || (hq && !sh)) return QL_ERR_NULL;
+  if (!gated_sizes_ok(m, gate->n, gate->k) || !ql::gated_launchable(m, gate->n, gate->k)) return QL_ERR_SHAPE;
+  if (!aligned16(xq) || !aligned16(sx) || !aligned16(h) || !aligned16(hq) || (hq && !aligned16(sh)) || !aligned16(gu))
+    return QL_ERR_ALIGN;
+  if (!ws || ws_bytes < ql::kWsReserved + ql::gated_scratch_bytes(m, gate->n)) return QL_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QL_ERR_ALIGN;
+  ql::Gated a;
+  a.xq = xq;
+  a.sx = sx;
+  a.wg = (const uint8_t*)gate->codes;
+  a.sg = gate->scales;
+  a.wu = (const uint8_t*)up->codes;
+  a.su = up->scales;
+  a.pow2 = gate->format == QL_FP8_POW2;
+  a.m = m;
+  a.n = gate->n;
+  a.k = gate->k;
+  a.h = h;
+  a.hq = hq;
+  a.sh = sh;
+  a.gu = gu;
+  a.counters = ql::ws_counters(ws);
+  a.scratch = (float*)ql::ws_scratch(ws);
+  ql::clear_hip_error();
+  return hip_status(ql::launch_gated(a, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -1,0 +1,693 @@
+// Gated feed-forward block on blockwise-FP8 weights for gfx950: both projections, the activation
+// and the product in one kernel.
+//
+//   g = x Wg^T,  u = x Wu^T    (E4M3 x E4M3, scales of 1x128 and 128x128 blocks, float32 sums)
+//   h = g / (1 + exp(-g)) * u  in float32, then bf16, or E4M3 with a scale for 128 columns
+//
+// A workgroup computes the same columns of g and of u, so h needs no second pass over either:
+// the weight rows of its tile are 64 of the gate and 64 of the up projection for each wave, and a
+// lane's accumulators of the two halves belong to the same elements of h.
+//
+//   more than 64 tokens  tiles of 128 columns (256 weight rows) by 256 or 128 tokens: the FP8
+//                        GEMMs' tiling (gemm_fp8.hip) with its two ways of applying scales, whose
+//                        128 columns are one segment of the 8-bit output
+//   up to 64 tokens      bound by the weights: 16 or 32 columns a workgroup, K split over its waves
+#include "common.hpp"
+#include "fp8_out.hpp"
+#include "gemm_common.hpp"
+#include "gemv_common.hpp"
+#include "launch.hpp"
+
+namespace ql {
+
+namespace {
+
+constexpr int kGCols = 128;      // columns of h per tile: one segment of an 8-bit output
+constexpr int kGRows = 256;      // weight rows per tile
+constexpr int kGRowBytes = 128;  // one K block of fp8 per LDS row
+constexpr int kGPitch = 272;     // output staging: bytes per row of 128 bf16 columns (conflict-free 8-byte writes)
+constexpr int kGPitch8 = 144;    // the same for 128 codes (conflict-free 4-byte writes)
+
+// g / (1 + exp(-g)) * u.  exp(-g) = 2^t with t = -g log2(e): what the product's rounding lost goes
+// back in as a factor 1 + d ln 2, so the result is within a few units of 2^-24 for every g.  Beyond
+// +-128 the exponential is 0 or infinite in float32 anyhow (and 1 / (1 + it) exactly 1 or 0).
+__device__ __forceinline__ float gate_product(float g, float u) {
+  const float c = __builtin_amdgcn_fmed3f(g, -128.0f, 128.0f);
+  const float t = c * -1.44269504f;
+  const float d = __builtin_fmaf(c, -1.44269504f, -t) + c * -1.92596299e-8f;   // log2(e) = 1.44269502 + 1.926e-8
+  const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(d, 0.693147181f, 1.0f);
+  return (g * __builtin_amdgcn_rcpf(1.0f + e)) * u;
+}
+
+__device__ __forceinline__ i32x8 gated_frag(const uint8_t* tile, int row, int g) {
+  const uint8_t* p = tile + row * kGRowBytes;
+  const i32x4 lo = *(const i32x4*)(p + swz(row, 2 * g) * 16);
+  const i32x4 hi = *(const i32x4*)(p + swz(row, 2 * g + 1) * 16);
+  return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+}
+
+// A tile's results to memory.  acc[0..3] is g and acc[4..7] u of the wave's 64 columns (16 i + 4 lg + e)
+// by 16 MJ tokens (16 j + r); the wave stands at column 64 wn and token mw of the tile.  Everything
+// leaves through LDS as whole rows.  `amax`: LDS for [2][TM] words.
+template <int THREADS, int TM, int MJ>
+__device__ __forceinline__ void gated_store(const Gated& a, f32x4 (&acc)[8][MJ], int64_t m0, int64_t n0, int wn, int mw,
+                                            int r, int lg, uint8_t* stage, uint32_t* amax) {
+  const int tid = threadIdx.x;
+  auto rows_out = [&](uint16_t* dst, int64_t stride, int from) {   // bf16(acc[from..from + 3]) -> dst [m][stride]
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) {
+        const f32x4 v = acc[from + i][j];
+        *(uint2*)(stage + (mw + 16 * j + r) * kGPitch + (64 * wn + 16 * i + 4 * lg) * 2) =
+            make_uint2(pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3]));
+      }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < TM * 16 / THREADS; ++q) {
+      const int row = (tid >> 4) + q * (THREADS / 16);
+      if (m0 + row < a.m)
+        *(i32x4*)(dst + (m0 + row) * stride + n0 + (tid & 15) * 8) = *(const i32x4*)(stage + row * kGPitch + (tid & 15) * 16);
+    }
+  };
+  if (a.gu) {
+    rows_out(a.gu, 2 * a.n, 0);
+    rows_out(a.gu + a.n, 2 * a.n, 4);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < MJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = gate_product(acc[i][j][e], acc[4 + i][j][e]);
+  if (a.h) rows_out(a.h, a.n, 0);
+  if (!a.hq) return;
+  // a token's 128 values are in the four lane groups of the two waves along n
+  uint32_t top[MJ];
+#pragma unroll
+  for (int j = 0; j < MJ; ++j) {
+    top[j] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top[j] = umax(top[j], abs_bits(acc[i][j][e]));
+    top[j] = umax(top[j], (uint32_t)__shfl_xor((int)top[j], 16));
+    top[j] = umax(top[j], (uint32_t)__shfl_xor((int)top[j], 32));
+  }
+  __syncthreads();
+  if (lg == 0)
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) amax[wn * TM + mw + 16 * j + r] = top[j];
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < MJ; ++j) {
+    const int row = mw + 16 * j + r;
+    const uint32_t t = umax(top[j], amax[(wn ^ 1) * TM + row]);
+    const Fp8Seg sc = a.pow2 ? fp8_seg_scale<true>(t) : fp8_seg_scale<false>(t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      *(uint32_t*)(stage + row * kGPitch8 + 64 * wn + 16 * i + 4 * lg) = fp8_encode4(f, sc);
+    }
+    if (lg == 0 && wn == 0 && m0 + row < a.m) {
+      const int64_t seg = (m0 + row) * (a.n / 128) + n0 / 128;
+      if (a.pow2)
+        ((uint8_t*)a.sh)[seg] = (uint8_t)sc.stored;
+      else
+        ((uint32_t*)a.sh)[seg] = sc.stored;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < TM * 8 / THREADS; ++q) {
+    const int row = (tid >> 3) + q * (THREADS / 8);
+    if (m0 + row < a.m)
+      *(i32x4*)(a.hq + (m0 + row) * a.n + n0 + (tid & 7) * 16) = *(const i32x4*)(stage + row * kGPitch8 + (tid & 7) * 16);
+  }
+}
+
+// The workgroup's tile, in scalar registers (the copies' base addresses have to be there).
+__device__ __forceinline__ void gated_tile(const Gated& a, int64_t& tm, int64_t& tn) {
+  gemm_tile_coords(a.tiles_m, a.tiles_n, tm, tn);
+  tm = __builtin_amdgcn_readfirstlane((int)tm);
+  tn = __builtin_amdgcn_readfirstlane((int)tn);
+}
+
+// Eight E4M3 codes -> eight f16, exactly (the converter's scale is 1).
+__device__ __forceinline__ f16x2 e4m3_f16(int w, bool high) {
+  return high ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w, 1.0f, true)
+              : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w, 1.0f, false);
+}
+__device__ __forceinline__ f16x8 e4m3_f16x8(int lo, int hi) {
+  const f16x2 a = e4m3_f16(lo, false), b = e4m3_f16(lo, true), c = e4m3_f16(hi, false), d = e4m3_f16(hi, true);
+  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// ------------------------------------------------------------------ float32 scales, many tokens
+// An output scale is amax / 448 in float32, so the sums behind it have to be right to float32's
+// order.  The FP8 matrix instructions align eight products at a time and keep 13 bits below the
+// largest (measured: 1.4e-5 of the result on normal data, 5e-5 on codes of every size), f16 ones keep
+// float32's 24; and every E4M3 value is an f16.  So the operands stay E4M3 in memory and LDS, the lanes
+// turn their fragments into f16 (a lane's 32 bytes are four steps of 8), and each K block's products
+// start from zero and are folded into the sums with one FMA by the block's scale.
+// Eight waves, 2 along n by 4 along m; a wave's 128 weight rows are 64 of the gate then 64 of the up
+// projection, its tokens 16 MJ: with MJ = 3 sums, fragments and two sets of products fit 256 registers.
+constexpr int kGfThreads = 512;
+template <int MJ>
+constexpr int gf_ring() { return 64 * MJ * 16 + 1024; }   // a slot of the scale ring: 16 bytes a token, then the weights'
+template <int MJ>
+constexpr size_t gf_lds() {
+  constexpr size_t loop = 2 * (kGRows + 64 * MJ) * kGRowBytes + 2 * gf_ring<MJ>(), out = 64 * MJ * kGPitch + 2 * 64 * MJ * 4;
+  return loop > out ? loop : out;
+}
+
+template <int MJ, bool SW4>
+__global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
+  extern __shared__ __align__(16) uint8_t smem[];  // [2][W 256 x 128 | x TM x 128], scale ring
+  constexpr int TM = 64 * MJ;
+  constexpr int kStage = (kGRows + TM) * kGRowBytes;
+  int64_t tm, tn;
+  gated_tile(a, tm, tn);
+  const int64_t n0 = tn * kGCols, m0 = tm * TM;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int wn = wave & 1, wm = wave >> 1;
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t kblocks = a.k / 128;
+
+  // Copies of a K block: q < 4 the LDS weight rows 64 q + 8 wave + lane / 8, which are rows
+  // 64 (q / 2) + 8 wave + lane / 8 of the gate (q even) or of the up projection; q >= 4 the tokens
+  // 64 (q - 4) + 8 wave + lane / 8 (past the last one, the last again).
+  uint32_t ow[2], ox[MJ];
+  const int64_t m_last = a.m - 1 - m0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = 64 * i + 8 * wave + (lane >> 3);   // (its swizzle is that of LDS rows 64 further, too)
+    ow[i] = (uint32_t)row * (uint32_t)a.k + (uint32_t)swz(row, lane & 7) * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < MJ; ++i) {
+    const int row = 64 * i + 8 * wave + (lane >> 3);
+    ox[i] = (uint32_t)(row < m_last ? row : m_last) * (uint32_t)a.k + (uint32_t)swz(row, lane & 7) * 16;
+  }
+  const uint8_t* gbase = a.wg + n0 * a.k;
+  const uint8_t* ubase = a.wu + n0 * a.k;
+  const uint8_t* xbase = a.xq + m0 * a.k;
+  auto dma = [&](int64_t kb, int buf, int q) {
+    const uint32_t lb = lds_addr(smem + buf * kStage) + 8 * wave * kGRowBytes;
+    if (q < 4)
+      lds_copy16((q & 1 ? ubase : gbase) + kb * 128, ow[q >> 1], lb + 64 * q * kGRowBytes);
+    else
+      lds_copy16(xbase + kb * 128, ox[q - 4], lb + (kGRows + 64 * (q - 4)) * kGRowBytes);
+  };
+  // Scales.  SW4 (K a multiple of 512, 16-byte aligned arrays): the four float scales of four blocks of a
+  // row are one 16-byte unit, copied to the ring once per four blocks (waves 0 .. MJ - 1 a token a
+  // lane, wave 4 the gate's unit in lane 0 and the up projection's in the others).
+  const float* sxb = (const float*)a.sx + m0 * kblocks;
+  const float* sgb = (const float*)a.sg + tn * kblocks;
+  const float* sub = (const float*)a.su + tn * kblocks;
+  uint32_t osx[MJ];
+#pragma unroll
+  for (int j = 0; j < MJ; ++j) {
+    const int64_t row = 16 * MJ * wm + 16 * j + r;
+    osx[j] = (uint32_t)((row < m_last ? row : m_last) * kblocks);
+  }
+  constexpr int kRing = 2 * kStage;
+  const int arow = 64 * (wave & 3) + lane;
+  const uint32_t oxu = (uint32_t)((arow < m_last ? arow : m_last) * kblocks * 4);
+  auto dma_sc = [&](int64_t grp) {
+    const uint32_t lb = lds_addr(smem + kRing) + (uint32_t)(grp & 1) * gf_ring<MJ>();
+    if (wave < MJ)
+      lds_copy16((const uint8_t*)sxb + 16 * grp, oxu, lb + wave * 1024);
+    else if (wave == 4)
+      lds_copy16_va((lane == 0 ? sgb : sub) + 4 * grp, lb + TM * 16);
+  };
+  float sxn[MJ], sgn, sun;
+  auto next_sc = [&](int64_t kb) {
+    if (SW4) {
+      const uint8_t* sl = smem + kRing + (int)((kb >> 2) & 1) * gf_ring<MJ>() + 4 * (int)(kb & 3);
+      sgn = *(const float*)(sl + TM * 16);
+      sun = *(const float*)(sl + TM * 16 + 16);
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) sxn[j] = *(const float*)(sl + 16 * (16 * MJ * wm + 16 * j + r));
+    } else {
+      sgn = sgb[kb];
+      sun = sub[kb];
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) sxn[j] = sxb[osx[j] + kb];
+    }
+  };
+
+  f32x4 acc[8][MJ];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int q = 0; q < 4 + MJ; ++q) dma(0, 0, q);
+  if (SW4) dma_sc(0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  next_sc(0);
+
+  // Software pipeline, fragment by fragment (8 fragments of 16 weight rows against MJ of 16 tokens).
+  // Each MFMA stands with one of the FMAs that fold the fragment before and with conversions of the
+  // fragment's next step, so that matrix and vector units have work side by side.  The next fragment
+  // comes from LDS during a fragment's first step; the next block's copies go out during fragments
+  // 0 .. 6, and the barrier sits before fragment 7, which also takes the next block's tokens.
+  const f32x4 zero = {0, 0, 0, 0};
+  f32x4 p[2][MJ];
+  float scg[MJ], scu[MJ], scl[MJ];
+  f16x8 xf[MJ][4], wf[2];
+  i32x8 wr, wrn;
+#pragma unroll
+  for (int j = 0; j < MJ; ++j) {
+    p[1][j] = zero;
+    scu[j] = 0.0f;
+    const i32x8 x = gated_frag(smem + kGRows * kGRowBytes, 16 * MJ * wm + 16 * j + r, g);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) xf[j][kk] = e4m3_f16x8(x[2 * kk], x[2 * kk + 1]);
+  }
+  wr = gated_frag(smem, 128 * wn + r, g);
+  wf[0] = e4m3_f16x8(wr[0], wr[1]);
+  for (int64_t kb = 0; kb < kblocks; ++kb) {
+    const int buf = (int)(kb & 1);
+    const int64_t kn = kb + 1 < kblocks ? kb + 1 : kb;  // the last block copies itself into the idle buffer again
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) {
+      scl[j] = scu[j];
+      scg[j] = sxn[j] * sgn;
+      scu[j] = sxn[j] * sun;
+    }
+    // kn's group landed at least a block's barrier ago: a group's copy goes out two blocks before its first
+    if (SW4 && ((kb + 2) & 3) == 0 && kb + 2 < kblocks) dma_sc((kb + 2) >> 2);
+    next_sc(kn);
+    const uint8_t* As = smem + buf * kStage;
+    const uint8_t* An = smem + (buf ^ 1) * kStage;
+    i32x8 xr[MJ];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i == 7) {
+        // this block's LDS reads are done and the next block's copies have landed
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < MJ; ++j) xr[j] = gated_frag(An + kGRows * kGRowBytes, 16 * MJ * wm + 16 * j + r, g);
+      }
+      f32x4(&pn)[MJ] = p[i & 1];
+      const f32x4(&po)[MJ] = p[(i & 1) ^ 1];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+        for (int j = 0; j < MJ; ++j) {
+          const int s = kk * MJ + j;
+          pn[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[kk & 1], xf[j][kk], kk ? pn[j] : zero, 0, 0, 0);
+          {  // 4 MJ products of the fragment before, one a step
+            const int t = s >> 2, e = s & 3;
+            const float sc = i == 0 ? scl[t] : i <= 4 ? scg[t] : scu[t];
+            acc[(i + 7) & 7][t][e] += sc * po[t][e];
+          }
+          if (s == 0) wrn = i < 7 ? gated_frag(As, 128 * wn + 16 * (i + 1) + r, g) : gated_frag(An, 128 * wn + r, g);
+          if (j == MJ - 1) wf[(kk & 1) ^ 1] = kk < 3 ? e4m3_f16x8(wr[2 * kk + 2], wr[2 * kk + 3]) : e4m3_f16x8(wrn[0], wrn[1]);
+          if (i < 4 + MJ && s == 1) dma(kn, buf ^ 1, i);
+          if (i == 7) xf[j][kk] = e4m3_f16x8(xr[j][2 * kk], xr[j][2 * kk + 1]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      wr = wrn;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < MJ; ++j) acc[7][j] += scu[j] * p[1][j];
+  gated_store<kGfThreads, TM, MJ>(a, acc, m0, n0, wn, 16 * MJ * wm, r, g, smem, (uint32_t*)(smem + TM * kGPitch));
+}
+
+// ------------------------------------------------------------------ powers of two, many tokens
+// The MFMA applies E8M0 scales itself and accumulates in place: four waves, 2 along n by 2 along m, as
+// in gemm_fp8_pow2_kernel.
+constexpr int kGpThreads = 256;
+template <int TM>
+constexpr int gp_ring() { return TM * 4 + 256; }
+template <int TM>
+constexpr size_t gp_lds() {
+  constexpr size_t loop = 2 * (kGRows + TM) * kGRowBytes + 2 * gp_ring<TM>(), out = TM * kGPitch + 2 * TM * 4;
+  return loop > out ? loop : out;
+}
+
+template <int TM, bool SW4>
+__global__ __launch_bounds__(kGpThreads) void gated_pow2_kernel(Gated a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int MJ = TM / 32;
+  constexpr int kStage = (kGRows + TM) * kGRowBytes;
+  int64_t tm, tn;
+  gated_tile(a, tm, tn);
+  const int64_t n0 = tn * kGCols, m0 = tm * TM;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int wn = wave & 1, wm = wave >> 1;
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t kblocks = a.k / 128;
+
+  // Copies of a K block: q < 8 the LDS weight rows 32 q + 8 wave + lane / 8, which are rows 64 (q / 4) +
+  // 32 (q % 2) + 8 wave + lane / 8 of the gate (q % 4 < 2) or of the up projection; q >= 8 the tokens
+  // 32 (q - 8) + 8 wave + lane / 8.
+  uint32_t ow[4], ox[MJ];
+  const int64_t m_last = a.m - 1 - m0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 32 * i + 8 * wave + (lane >> 3);   // (its swizzle is that of any row 32 further, too)
+    ow[i] = (uint32_t)row * (uint32_t)a.k + (uint32_t)swz(row, lane & 7) * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < MJ; ++i) {
+    const int row = 32 * i + 8 * wave + (lane >> 3);
+    ox[i] = (uint32_t)(row < m_last ? row : m_last) * (uint32_t)a.k + (uint32_t)swz(row, lane & 7) * 16;
+  }
+  const uint8_t* gbase = a.wg + n0 * a.k;
+  const uint8_t* ubase = a.wu + n0 * a.k;
+  const uint8_t* xbase = a.xq + m0 * a.k;
+  auto dma = [&](int64_t kb, int buf, int q) {
+    const uint32_t lb = lds_addr(smem + buf * kStage) + 8 * wave * kGRowBytes;
+    if (q < 8)
+      lds_copy16((q & 2 ? ubase : gbase) + kb * 128, ow[2 * (q >> 2) + (q & 1)], lb + 32 * q * kGRowBytes);
+    else
+      lds_copy16(xbase + kb * 128, ox[q - 8], lb + (kGRows + 32 * (q - 8)) * kGRowBytes);
+  };
+  const uint8_t* sxb = (const uint8_t*)a.sx + m0 * kblocks;
+  const uint8_t* sgb = (const uint8_t*)a.sg + tn * kblocks;
+  const uint8_t* sub = (const uint8_t*)a.su + tn * kblocks;
+  uint32_t osx[MJ];
+#pragma unroll
+  for (int j = 0; j < MJ; ++j) {
+    const int64_t row = 16 * MJ * wm + 16 * j + r;
+    osx[j] = (uint32_t)((row < m_last ? row : m_last) * kblocks);
+  }
+  // SW4 (K a multiple of 512, 4-byte aligned arrays): the bytes of four blocks are one word, in a ring of two
+  constexpr int kRing = 2 * kStage;
+  const int arow = 64 * wave + lane;
+  const uint32_t oxw = (uint32_t)((arow < m_last ? arow : m_last) * kblocks);
+  auto dma_sc = [&](int64_t grp) {
+    const uint32_t lb = lds_addr(smem + kRing) + (uint32_t)(grp & 1) * gp_ring<TM>();
+    if (wave < TM / 64) lds_copy4(sxb + 4 * grp, oxw, lb + wave * 256);
+    if (wave == 3) lds_copy4_va((lane == 0 ? sgb : sub) + 4 * grp, lb + TM * 4);
+  };
+  int sgn, sun, sbn[MJ];
+  auto next_sc = [&](int64_t kb) {
+    if (SW4) {
+      const uint8_t* sl = smem + kRing + (int)((kb >> 2) & 1) * gp_ring<TM>() + (int)(kb & 3);
+      sgn = sl[TM * 4];
+      sun = sl[TM * 4 + 4];
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) sbn[j] = sl[4 * (16 * MJ * wm + 16 * j + r)];
+    } else {
+      sgn = sgb[kb];
+      sun = sub[kb];
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) sbn[j] = sxb[osx[j] + kb];
+    }
+  };
+
+  f32x4 acc[8][MJ];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int q = 0; q < 8 + MJ; ++q) dma(0, 0, q);
+  if (SW4) dma_sc(0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  next_sc(0);
+  int sg = sgn, su = sun, sb[MJ];
+#pragma unroll
+  for (int j = 0; j < MJ; ++j) sb[j] = sbn[j];
+  i32x8 bf[MJ], af, afn;
+#pragma unroll
+  for (int j = 0; j < MJ; ++j) bf[j] = gated_frag(smem + kGRows * kGRowBytes, 16 * MJ * wm + 16 * j + r, g);
+  af = gated_frag(smem, 128 * wn + r, g);
+  for (int64_t kb = 0; kb < kblocks; ++kb) {
+    const int buf = (int)(kb & 1);
+    const int64_t kn = kb + 1 < kblocks ? kb + 1 : kb;
+    if (SW4 && ((kb + 2) & 3) == 0 && kb + 2 < kblocks) dma_sc((kb + 2) >> 2);
+    next_sc(kn);
+    const uint8_t* As = smem + buf * kStage;
+    const uint8_t* An = smem + (buf ^ 1) * kStage;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i == 7) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+      }
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af, bf[j], acc[i][j], 0, 0, 0, i < 4 ? sg : su, 0, sb[j]);
+        if (j == 0) afn = i < 7 ? gated_frag(As, 128 * wn + 16 * (i + 1) + r, g) : gated_frag(An, 128 * wn + r, g);
+        if (MJ == 8) {
+          if (i < 4 && (j & 1)) dma(kn, buf ^ 1, 4 * i + (j >> 1));
+        } else if (i < 6 && (j & 1)) {
+          dma(kn, buf ^ 1, 2 * i + (j >> 1));
+        }
+        if (i == 7) bf[j] = gated_frag(An + kGRows * kGRowBytes, 16 * MJ * wm + 16 * j + r, g);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      af = afn;
+    }
+    sg = sgn;
+    su = sun;
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) sb[j] = sbn[j];
+  }
+  gated_store<kGpThreads, TM, MJ>(a, acc, m0, n0, wn, 16 * MJ * wm, r, g, smem, (uint32_t*)(smem + TM * kGPitch));
+}
+
+// ------------------------------------------------------------------ up to 64 tokens
+// Bound by the weights, which are read once, straight into the MFMA's fragments: a lane's 32 bytes
+// of a K block (row lane % 16, bytes 32 (lane / 16) ..), four lanes to a whole 128-byte line.  A
+// workgroup has RT x 16 rows of each projection and MT x 16 tokens, and its eight waves take the K
+// blocks in turn; their sums are added in wave order through LDS.  An 8-bit output needs 128 columns:
+// the workgroups of a segment leave float32 values in the workspace, and the last to arrive (an
+// integer counter, returned to zero) quantizes them.
+constexpr int kFewWaves = 8, kFewThreads = kFewWaves * kWave;
+
+template <int MT, int RT, bool POW2>
+__global__ __launch_bounds__(kFewThreads) void gated_few_kernel(Gated a) {
+  __shared__ __align__(16) f32x4 part[4 * 2 * MT * RT * kWave];
+  __shared__ int last;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+  const int64_t kblocks = a.k / 128;
+  const int64_t nb = n0 / 128;
+  const uint8_t* gp = a.wg + (n0 + r) * a.k + 32 * g;
+  const uint8_t* up = a.wu + (n0 + r) * a.k + 32 * g;
+  int64_t xrow[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int64_t row = 16 * j + r;
+    xrow[j] = row < a.m ? row : a.m - 1;
+  }
+  f32x4 acc[2][RT][MT];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[h][i][j] = f32x4{0, 0, 0, 0};
+
+  auto load32 = [](const uint8_t* p) {
+    const i32x4 lo = *(const i32x4*)p, hi = *(const i32x4*)(p + 16);
+    return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+  for (int64_t kb = wave; kb < kblocks; kb += kFewWaves) {
+    i32x8 wf[2][RT], xf[MT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      wf[0][i] = load32(gp + (int64_t)16 * i * a.k + kb * 128);
+      wf[1][i] = load32(up + (int64_t)16 * i * a.k + kb * 128);
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j) xf[j] = load32(a.xq + xrow[j] * a.k + kb * 128 + 32 * g);
+    if (POW2) {
+      const int sw[2] = {((const uint8_t*)a.sg)[nb * kblocks + kb], ((const uint8_t*)a.su)[nb * kblocks + kb]};
+      int sx[MT];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) sx[j] = ((const uint8_t*)a.sx)[xrow[j] * kblocks + kb];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+            acc[h][i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[h][i], xf[j], acc[h][i][j], 0, 0, 0, sw[h], 0, sx[j]);
+    } else {
+      const float sw[2] = {((const float*)a.sg)[nb * kblocks + kb], ((const float*)a.su)[nb * kblocks + kb]};
+      float sx[MT];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) sx[j] = ((const float*)a.sx)[xrow[j] * kblocks + kb];
+      f32x4 p[2][RT][MT];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        f16x8 x16[MT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) x16[j] = e4m3_f16x8(xf[j][2 * kk], xf[j][2 * kk + 1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const f16x8 w16 = e4m3_f16x8(wf[h][i][2 * kk], wf[h][i][2 * kk + 1]);
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+              p[h][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w16, x16[j], kk ? p[h][i][j] : f32x4{0, 0, 0, 0}, 0, 0, 0);
+          }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            acc[h][i][j] += p[h][i][j] * (sw[h] * sx[j]);
+          }
+    }
+  }
+
+  // waves 4..7 hand their sums to waves 0..3, then all four to everybody
+  constexpr int kTiles = 2 * RT * MT;
+  auto put = [&](int w) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) part[(w * kTiles + (h * RT + i) * MT + j) * kWave + lane] = acc[h][i][j];
+  };
+  if (wave >= 4) put(wave - 4);
+  __syncthreads();
+  if (wave < 4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[h][i][j] += part[(wave * kTiles + (h * RT + i) * MT + j) * kWave + lane];
+  }
+  __syncthreads();
+  if (wave < 4) put(wave);
+  __syncthreads();
+  __amdgpu_buffer_rsrc_t hs = dev_rsrc(a.scratch);
+  for (int t = wave; t < RT * MT; t += kFewWaves) {   // one 16 x 16 piece of h a wave
+    const int i = t / MT, j = t % MT;
+    f32x4 gv = {0, 0, 0, 0}, uv = gv, hv;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      gv += part[(w * kTiles + i * MT + j) * kWave + lane];
+      uv += part[(w * kTiles + (RT + i) * MT + j) * kWave + lane];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) hv[e] = gate_product(gv[e], uv[e]);
+    const int64_t row = 16 * j + r, col = n0 + 16 * i + 4 * g;
+    if (row >= a.m) continue;
+    auto out = [&](uint16_t* p, f32x4 v) {
+      *(uint2*)p = make_uint2(pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3]));
+    };
+    if (a.gu) {
+      out(a.gu + row * 2 * a.n + col, gv);
+      out(a.gu + row * 2 * a.n + a.n + col, uv);
+    }
+    if (a.h) out(a.h + row * a.n + col, hv);
+    // the segment's block of the workspace: [n / 128][m][128] float32
+    if (a.hq) st_dev4v(hs, (uint32_t)(((nb * a.m + row) * 128 + col % 128) * 4), hv);
+  }
+  if (!a.hq) return;
+  wait_stores();
+  __syncthreads();
+  constexpr uint32_t kArrive = 128 / (16 * RT);
+  if (threadIdx.x == 0) {
+    uint32_t* cnt = a.counters + nb;
+    const uint32_t old = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = old == kArrive - 1;
+    if (last) st_dev_u32(cnt, 0u);
+  }
+  __syncthreads();
+  if (!last) return;
+  // 32 lanes a token, 4 columns each
+  const int c4 = threadIdx.x & 31;
+  for (int64_t row = threadIdx.x >> 5; row < a.m; row += kFewThreads / 32) {
+    const f32x4 v = ld_dev4v(hs, (uint32_t)(((nb * a.m + row) * 128 + 4 * c4) * 4));
+    uint32_t top = umax(umax(abs_bits(v[0]), abs_bits(v[1])), umax(abs_bits(v[2]), abs_bits(v[3])));
+    top = max_row16(top);
+    top = umax(top, (uint32_t)__shfl_xor((int)top, 16));
+    const Fp8Seg sc = fp8_seg_scale<POW2>(top);
+    const float f[4] = {v[0], v[1], v[2], v[3]};
+    *(uint32_t*)(a.hq + row * a.n + nb * 128 + 4 * c4) = fp8_encode4(f, sc);
+    if (c4 == 0) {
+      const int64_t seg = row * (a.n / 128) + nb;
+      if (POW2)
+        ((uint8_t*)a.sh)[seg] = (uint8_t)sc.stored;
+      else
+        ((uint32_t*)a.sh)[seg] = sc.stored;
+    }
+  }
+}
+
+constexpr int64_t kFewM = 64;
+
+template <int MT, int RT>
+hipError_t launch_few(const Gated& a, hipStream_t s) {
+  const unsigned grid = (unsigned)(a.n / (16 * RT));
+  if (a.pow2)
+    gated_few_kernel<MT, RT, true><<<grid, kFewThreads, 0, s>>>(a);
+  else
+    gated_few_kernel<MT, RT, false><<<grid, kFewThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// TM tokens a tile; `four`: the scales of four K blocks lie in one aligned unit.
+template <int TM>
+hipError_t launch_tiles(Gated a, hipStream_t s) {
+  a.tiles_m = (a.m + TM - 1) / TM;
+  a.tiles_n = a.n / kGCols;
+  const unsigned grid = (unsigned)(a.tiles_m * a.tiles_n);
+  const uintptr_t all = (uintptr_t)a.sx | (uintptr_t)a.sg | (uintptr_t)a.su;
+  const bool four = (a.k / 128) % 4 == 0 && (all & (a.pow2 ? 3 : 15)) == 0;
+  auto go = [&](auto kernel, int threads, size_t lds) {
+    hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    kernel<<<grid, threads, lds, s>>>(a);
+    return hipGetLastError();
+  };
+  if constexpr (TM % 64 == 0 && TM <= 192) {
+    if (!a.pow2)
+      return four ? go(gated_f32s_kernel<TM / 64, true>, kGfThreads, gf_lds<TM / 64>())
+                  : go(gated_f32s_kernel<TM / 64, false>, kGfThreads, gf_lds<TM / 64>());
+  }
+  if constexpr (TM % 128 == 0)
+    return four ? go(gated_pow2_kernel<TM, true>, kGpThreads, gp_lds<TM>())
+                : go(gated_pow2_kernel<TM, false>, kGpThreads, gp_lds<TM>());
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+bool gated_launchable(int64_t m, int64_t n, int64_t k) {
+  if (m <= 0 || n <= 0 || k <= 0 || n % 128 || k % 128 || k >= kFp8MaxK) return false;
+  // counters of the few-token kernel, and its 32-bit scratch offsets
+  if (m <= kFewM) return n / 128 <= (int64_t)((kWsReserved - kWsCounterOff) / 4) && m * n < (int64_t(1) << 29);
+  return (m + 127) / 128 * (n / 128) < (int64_t(1) << 31);
+}
+
+size_t gated_scratch_bytes(int64_t m, int64_t n) { return m <= kFewM ? (size_t)(m * n) * 4 : 0; }
+
+hipError_t launch_gated(const Gated& a, hipStream_t s) {
+  if (!gated_launchable(a.m, a.n, a.k)) return hipErrorInvalidValue;
+  if (a.m <= 16) return launch_few<1, 1>(a, s);
+  if (a.m <= 32) return launch_few<2, 1>(a, s);
+  if (a.m <= 48) return launch_few<3, 2>(a, s);
+  if (a.m <= kFewM) return launch_few<4, 2>(a, s);
+  if (a.m <= 128) return launch_tiles<128>(a, s);
+  return a.pow2 ? launch_tiles<256>(a, s) : launch_tiles<192>(a, s);
+}
+
+}  // namespace ql

@@ -250,4 +250,27 @@ struct NormBackward {
 size_t rms_norm_backward_bytes(int64_t m, int64_t k);
 hipError_t launch_rms_norm_backward(const NormBackward& a, hipStream_t s);
 
+// ---- gated feed-forward block on FP8 weights (gated.hip); n % 128 == 0, k % 128 == 0
+struct Gated {
+  const uint8_t* xq;        // E4M3 [m][k]
+  const void* sx;           // [m][k / 128]: float32, or E8M0 bytes with pow2, as all scales here
+  const uint8_t* wg;        // E4M3 [n][k]
+  const void* sg;           // [n / 128][k / 128]
+  const uint8_t* wu;
+  const void* su;
+  bool pow2;
+  int64_t m, n, k;
+  uint16_t* h;              // bf16 [m][n], or null
+  uint8_t* hq;              // E4M3 [m][n], or null
+  void* sh;                 // [m][n / 128]
+  uint16_t* gu;             // bf16 [m][2 n], or null
+  uint32_t* counters;       // zero before and after a call
+  float* scratch;           // gated_scratch_bytes
+  // set by the launcher
+  int64_t tiles_m, tiles_n;
+};
+bool gated_launchable(int64_t m, int64_t n, int64_t k);
+size_t gated_scratch_bytes(int64_t m, int64_t n);
+hipError_t launch_gated(const Gated& a, hipStream_t s);
+
 }  // namespace ql
