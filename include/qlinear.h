@@ -543,6 +543,25 @@ qlinear_status qlinear_gated_forward(const qlinear_qweight* gate, const qlinear_
                                      void* ws, size_t ws_bytes, void* stream);
 size_t qlinear_gated_forward_workspace(int64_t m, int64_t n, int64_t k);
 
+/* Backward pass of qlinear_gated_forward (rapidrecap.app Jet-RL summary, "Key Points": FP8 forward,
+ * BF16 backward), from dh = dL/dh (bf16 [m][n]), the forward's gu, and x (bf16 [m][k]), the
+ * activations before their quantization, which passes gradients unchanged.  With
+ * s = 1 / (1 + exp(-g)):
+ *   dg = dh u s (1 + g (1 - s)),  du = dh g s
+ *   dx [m][k] = dg Wg + du Wu            dgate [n][k] = dg^T x            dup [n][k] = du^T x
+ * all bf16 (a weight gradient is an update that qlinear_update_requantize_all takes, once scaled),
+ * with float32 sums.  dg and du, formed in float32, enter dx as f16 with a power of two a row
+ * (values below about 2^-29 of the row's largest lose bits), the weights as f16 with one for 128
+ * columns; they enter the weights' gradients rounded to bf16.
+ * dx, or dgate and dup, may be NULL (not wanted); x is read for dgate and dup only.
+ * Workspace: qlinear_gated_backward_workspace(m, n, k) bytes of scratch (about 8 m n), which need no
+ * zeroing and may be reused by any call once this one has finished on its stream.
+ * Errors as qlinear_gated_forward, with n, k < 2^22, and QL_ERR_NULL for dgate without dup. */
+qlinear_status qlinear_gated_backward(const qlinear_qweight* gate, const qlinear_qweight* up, const uint16_t* dh,
+                                      const uint16_t* gu, const uint16_t* x, int64_t m, uint16_t* dx, uint16_t* dgate,
+                                      uint16_t* dup, void* ws, size_t ws_bytes, void* stream);
+size_t qlinear_gated_backward_workspace(int64_t m, int64_t n, int64_t k);
+
 #ifdef __cplusplus
 }
 #endif

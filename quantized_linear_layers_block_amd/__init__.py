@@ -21,7 +21,7 @@ __all__ = ["NVFP4Weight", "FP8Weight", "quantize_nvfp4", "quantize_fp8_block", "
            "forward", "forward_fp8_prequant", "RequantTable", "QlinearError", "binding", "workspace_status",
            "quantize_fp8_pow2", "kv_store_fp8", "kv_load_fp8", "KVCacheNVFP4", "kv_store_nvfp4", "kv_load_nvfp4",
            "attention_nvfp4", "rms_norm", "rms_norm_fp8", "rms_norm_backward",
-           "gated_forward", "gated_forward_fp8"]
+           "gated_forward", "gated_forward_fp8", "gated_backward"]
 
 
 def _dev(t):
@@ -536,3 +536,32 @@ def gated_forward_fp8(gate, up, xq, sx, h=None, gu=None, ws=None):
     sh = torch.empty((m, gate.n // 128), dtype=_U8 if gate.pow2 else _F32, device=xq.device)
     _gated_call(gate, up, xq, sx, h, hq, sh, gu, ws)
     return hq, sh
+
+
+def gated_backward(gate, up, dh, gu, x=None, need_dx=True, need_dweight=True, ws=None):
+    """Gradients of gated_forward: (dx, dgate, dup), bf16 [T, k] and [n, k] twice (None where not
+    wanted).  dh (bf16 [T, n]) is the gradient of h, gu what the forward filled, x (bf16 [T, k]) the
+    activations before their quantization, needed for the weights' gradients.  ws: scratch kept
+    from step to step."""
+    dev = _gated_weights(gate, up)
+    n, k = gate.n, gate.k
+    if dh.dim() != 2:
+        raise ValueError("dh must be [tokens, n]")
+    m = dh.shape[0]
+    _check_dense(dev, _BF16, "dh", dh, (m, n))
+    _check_dense(dev, _BF16, "gu", gu, (m, 2 * n))
+    dx = dgate = dup = None
+    if need_dweight:
+        if x is None:
+            raise ValueError("the weights' gradients need x")
+        _check_dense(dev, _BF16, "x", x, (m, k))
+        dgate = torch.empty((n, k), dtype=_BF16, device=dev)
+        dup = torch.empty((n, k), dtype=_BF16, device=dev)
+    if need_dx:
+        dx = torch.empty((m, k), dtype=_BF16, device=dev)
+    if ws is None:
+        ws = torch.empty((max(1, binding.qlinear_gated_backward_workspace(m, n, k)),), dtype=_U8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        _refuse(dev, ws.dtype, "ws", ws, "contiguous")
+    _call_on(dev, binding.qlinear_gated_backward, gate.qweight(), up.qweight(), dh, gu, ws, x, dx, dgate, dup)
+    return dx, dgate, dup

@@ -53,6 +53,8 @@ EXPORTS = [
     "qlinear_rms_norm_backward_workspace",
     "qlinear_gated_forward",
     "qlinear_gated_forward_workspace",
+    "qlinear_gated_backward",
+    "qlinear_gated_backward_workspace",
 ]
 
 QLINEAR_STATUS_NONFINITE, QLINEAR_STATUS_TIMEOUT, QLINEAR_STATUS_BAD_ITEM = 1, 2, 4
@@ -146,6 +148,9 @@ def _load():
         "qlinear_gated_forward": ([ctypes.POINTER(QWeight), ctypes.POINTER(QWeight), vp, vp, i64, vp, vp, vp, vp, vp,
                                    sz, vp], i32),
         "qlinear_gated_forward_workspace": ([i64, i64, i64], sz),
+        "qlinear_gated_backward": ([ctypes.POINTER(QWeight), ctypes.POINTER(QWeight), vp, vp, vp, i64, vp, vp, vp, vp,
+                                    sz, vp], i32),
+        "qlinear_gated_backward_workspace": ([i64, i64, i64], sz),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -447,6 +452,19 @@ def qlinear_gated_forward(gate, up, xq, sx, ws, h=None, hq=None, sh=None, gu=Non
                                    _stream_here() if stream is None else stream)
     if st:
         raise QlinearError(st, "qlinear_gated_forward")
+
+
+def qlinear_gated_backward_workspace(m, n, k):
+    return LIB.qlinear_gated_backward_workspace(m, n, k)
+
+
+def qlinear_gated_backward(gate, up, dh, gu, ws, x=None, dx=None, dgate=None, dup=None, stream=None):
+    """gate, up QWeight; dh bf16 [m, n], gu bf16 [m, 2n], x bf16 [m, k] -> dx bf16 [m, k], dgate, dup bf16 [n, k]."""
+    st = LIB.qlinear_gated_backward(ctypes.byref(gate), ctypes.byref(up), dh.data_ptr(), gu.data_ptr(), _ptr(x),
+                                    dh.shape[0], _ptr(dx), _ptr(dgate), _ptr(dup), ws.data_ptr(), ws.nbytes,
+                                    _stream_here() if stream is None else stream)
+    if st:
+        raise QlinearError(st, "qlinear_gated_backward")
 
 
 def qlinear_status_word(ws):

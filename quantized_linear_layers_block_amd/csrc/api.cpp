@@ -744,4 +744,40 @@ qlinear_status qlinear_gated_forward(const qlinear_qweight* gate, const qlinear_
   return hip_status(ql::launch_gated(a, (hipStream_t)stream));
 }
 
+size_t qlinear_gated_backward_workspace(int64_t m, int64_t n, int64_t k) {
+  if (!gated_sizes_ok(m, n, k) || !ql::gated_backward_launchable(m, n, k)) return 0;
+  return ql::gated_backward_bytes(m, n, k);
+}
+
+qlinear_status qlinear_gated_backward(const qlinear_qweight* gate, const qlinear_qweight* up, const uint16_t* dh,
+                                      const uint16_t* gu, const uint16_t* x, int64_t m, uint16_t* dx, uint16_t* dgate,
+                                      uint16_t* dup, void* ws, size_t ws_bytes, void* stream) {
+  const qlinear_status st = check_gated_weights(gate, up);
+  if (st != QL_OK) return st;
+  if (!dh || !gu || (!dx && !dgate) || !dgate != !dup || (dgate && !x)) return QL_ERR_NULL;
+  if (!gated_sizes_ok(m, gate->n, gate->k) || !ql::gated_backward_launchable(m, gate->n, gate->k)) return QL_ERR_SHAPE;
+  if (!aligned16(dh) || !aligned16(gu) || !aligned16(x) || !aligned16(dx) || !aligned16(dgate) || !aligned16(dup))
+    return QL_ERR_ALIGN;
+  if (!ws || ws_bytes < ql::gated_backward_bytes(m, gate->n, gate->k)) return QL_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QL_ERR_ALIGN;
+  ql::GatedBackward a;
+  a.dh = dh;
+  a.gu = gu;
+  a.x = x;
+  a.wg = (const uint8_t*)gate->codes;
+  a.sg = gate->scales;
+  a.wu = (const uint8_t*)up->codes;
+  a.su = up->scales;
+  a.pow2 = gate->format == QL_FP8_POW2;
+  a.m = m;
+  a.n = gate->n;
+  a.k = gate->k;
+  a.dx = dx;
+  a.dgate = dgate;
+  a.dup = dup;
+  a.scratch = ws;
+  ql::clear_hip_error();
+  return hip_status(ql::launch_gated_backward(a, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -1,0 +1,590 @@
+// Backward pass of the gated feed-forward block on FP8 weights, gfx950 (FP8 forward, BF16 backward:
+// rapidrecap.app Jet-RL summary, "Key Points").  With s = 1 / (1 + exp(-g)):
+//
+//   dg = dh u s (1 + g (1 - s)),  du = dh g s
+//   dx = dg Wg + du Wu,   dWg = dg^T x,   dWu = du^T x
+//
+// Four kernels: the weights' scales made ready, dg and du side by side (D, [m][2 n]), and two matrix
+// products.  D is formed once in float32 and held twice: as f16 rows scaled by powers of two for dx
+// (its rounding, 2^-11, is far below that of a bf16 result; the weights meet it as f16 too, E4M3 values
+// times their scales rounded once more), and as bf16 for the weights' gradients, whose sums run over
+// tokens of any size, so that a row's factor could not be taken out.
+#include "common.hpp"
+#include "gemm_common.hpp"
+#include "launch.hpp"
+
+namespace ql {
+
+namespace {
+
+constexpr int kBTile = 256;                 // columns (k) and rows (tokens, or weight rows) of an output tile
+constexpr int kBStep = 32;                  // depth of a step: one MFMA deep
+constexpr int kBThreads = 256;
+constexpr int kBRing = 4;                   // steps in flight
+constexpr int kBPitch = 272;                // output staging: bytes per row of 128 bf16 columns
+constexpr int kBStagePerWave = 128 * kBPitch;
+constexpr int kBRowsBytes = kBTile * kBStep * 2;   // one operand of one step, 16 bits an element
+constexpr int kBCodeBytes = kBTile * kBStep;
+constexpr int kBScaleBytes = 1024;          // one word a thread
+constexpr size_t kBLds = 4 * kBStagePerWave;
+// dx: ring of D rows, ring of codes, two steps of weights in f16, ring of scale words
+constexpr int kBCodeOff = kBRing * kBRowsBytes, kBWOff = kBCodeOff + kBRing * kBCodeBytes,
+              kBScaleOff = kBWOff + 2 * kBRowsBytes;
+static_assert(kBScaleOff + kBRing * kBScaleBytes <= (int)kBLds && 2 * kBRing * kBRowsBytes <= (int)kBLds,
+              "the operands fit in the output's staging area");
+
+__device__ __forceinline__ float pow2_float(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ uint32_t f16_pair(float a, float b) {
+  return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+}
+
+// ---------------------------------------------------------------------- scales of the weights
+// For each 128 columns of k the power of two 2^E that puts the largest of the 2 n / 128 scales in
+// [32, 64): then every weight is an f16 (448 * 64 < 2^15), normal down to 2^-20 of the largest scale.  tab
+// [2 n / 128][k / 128] holds f16(scale * 2^-E) twice in a word, cols [k / 128] 2^E.
+__global__ __launch_bounds__(256) void gated_scales_kernel(const void* __restrict__ sg, const void* __restrict__ su,
+                                                           int pow2, int64_t nb, int64_t kb, uint32_t* __restrict__ tab,
+                                                           float* __restrict__ cols, uint32_t* __restrict__ zeros) {
+  __shared__ uint32_t red[4];
+  const int64_t c = blockIdx.x;
+  auto scale = [&](int64_t i) {
+    const void* s = i < nb ? sg : su;
+    const int64_t at = (i < nb ? i : i - nb) * kb + c;
+    if (!pow2) return ((const float*)s)[at];
+    const uint32_t b = ((const uint8_t*)s)[at];
+    return b == 255 ? __uint_as_float(0x7FC00000u) : b == 0 ? 0x1p-127f : __uint_as_float(b << 23);
+  };
+  uint32_t top = 0;
+  for (int64_t i = threadIdx.x; i < 2 * nb; i += 256) top = umax(top, __float_as_uint(scale(i)) & 0x7FFFFFFFu);
+  top = max_block<256>(top, red);
+  int e = top >= 0x7F800000u ? 0 : (int)(top >> 23) - 127 - 5;
+  e = e < -120 ? -120 : e > 120 ? 120 : e;
+  for (int64_t i = threadIdx.x; i < 2 * nb; i += 256) {
+    const float s = scale(i) * pow2_float(-e);
+    tab[i * kb + c] = f16_pair(s, s);
+  }
+  if (threadIdx.x == 0) cols[c] = pow2_float(e);
+  if (c == 0 && threadIdx.x < 128) zeros[threadIdx.x] = 0;   // what rows past the last token read
+}
+
+// --------------------------------------------------------------------------------- D
+__device__ __forceinline__ void gate_grad(float g, float u, float dh, float& dg, float& du) {
+  // (g beyond +-128 leaves s at 0 or 1 in float32; products are ordered so that no finite value meets an
+  // infinite one)
+  const float c = __builtin_amdgcn_fmed3f(g, -128.0f, 128.0f);
+  const float t = c * -1.44269504f;
+  const float d = __builtin_fmaf(c, -1.44269504f, -t) + c * -1.92596299e-8f;
+  const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(d, 0.693147181f, 1.0f);
+  const float s = __builtin_amdgcn_rcpf(1.0f + e);
+  const float q = e < 3e38f ? e * s : 1.0f;   // 1 - s without cancellation
+  const float gs = g * s;
+  du = dh * gs;
+  dg = (dh * u) * (s + gs * q);
+}
+
+struct GateGrad {
+  const uint16_t* dh;   // [m][n]
+  const uint16_t* gu;   // [m][2 n]
+  int64_t m, n, m_pad;
+  uint16_t* d16;        // f16 [m][2 n], or null
+  float* rs;            // [m]
+  uint16_t* db;         // bf16 [m_pad][2 n], rows past m zero, or null
+};
+
+// T threads a row, NV units of 8 columns each in registers (NV 0: any n, read twice).  Bound by memory:
+// 6 bytes read, 4 or 8 written a column of h.
+template <int T, int NV>
+__global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
+  __shared__ uint32_t red[T / kWave];
+  const int64_t row = blockIdx.x;
+  const int64_t units = a.n / 8;
+  const int t = threadIdx.x;
+  if (row >= a.m) {   // padding of db
+    for (int64_t u = t; u < 2 * units; u += T) *(uint4*)(a.db + row * 2 * a.n + u * 8) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const uint16_t* ph = a.dh + row * a.n;
+  const uint16_t* pg = a.gu + row * 2 * a.n;
+  auto at = [](const uint4& v, int e) {
+    const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
+    return e & 1 ? bf16_hi(w) : bf16_lo(w);
+  };
+  auto grads = [&](const uint4& g, const uint4& u, const uint4& h, float (&dg)[8], float (&du)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) gate_grad(at(g, e), at(u, e), at(h, e), dg[e], du[e]);
+  };
+  auto highest = [](const float (&dg)[8], const float (&du)[8]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      top = umax(top, umax(__float_as_uint(dg[e]) & 0x7FFFFFFFu, __float_as_uint(du[e]) & 0x7FFFFFFFu));
+    return top;
+  };
+  auto store = [&](int64_t u, const float (&dg)[8], const float (&du)[8], float f) {
+    if (a.db) {
+      uint16_t* p = a.db + row * 2 * a.n + u * 8;
+      *(uint4*)p = make_uint4(pack_bf16x2_rne(dg[0], dg[1]), pack_bf16x2_rne(dg[2], dg[3]),
+                              pack_bf16x2_rne(dg[4], dg[5]), pack_bf16x2_rne(dg[6], dg[7]));
+      *(uint4*)(p + a.n) = make_uint4(pack_bf16x2_rne(du[0], du[1]), pack_bf16x2_rne(du[2], du[3]),
+                                      pack_bf16x2_rne(du[4], du[5]), pack_bf16x2_rne(du[6], du[7]));
+    }
+    if (a.d16) {
+      uint16_t* p = a.d16 + row * 2 * a.n + u * 8;
+      *(uint4*)p = make_uint4(f16_pair(dg[0] * f, dg[1] * f), f16_pair(dg[2] * f, dg[3] * f),
+                              f16_pair(dg[4] * f, dg[5] * f), f16_pair(dg[6] * f, dg[7] * f));
+      *(uint4*)(p + a.n) = make_uint4(f16_pair(du[0] * f, du[1] * f), f16_pair(du[2] * f, du[3] * f),
+                                      f16_pair(du[4] * f, du[5] * f), f16_pair(du[6] * f, du[7] * f));
+    }
+  };
+  // the power of two that puts the row's largest value in [2^14, 2^15)
+  auto factor = [&](uint32_t top) {
+    top = max_block<T>(top, red);
+    int e = top == 0 || top >= 0x7F800000u ? 0 : 14 - ((int)(top >> 23) - 127);
+    e = e < -120 ? -120 : e > 120 ? 120 : e;
+    if (t == 0 && a.rs) a.rs[row] = pow2_float(-e);
+    return pow2_float(e);
+  };
+  if constexpr (NV > 0) {
+    float dg[NV][8], du[NV][8];
+    uint4 g[NV], u[NV], h[NV];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)i * T + t;
+      const bool in = c < units;
+      g[i] = in ? *(const uint4*)(pg + c * 8) : make_uint4(0, 0, 0, 0);
+      u[i] = in ? *(const uint4*)(pg + a.n + c * 8) : make_uint4(0, 0, 0, 0);
+      h[i] = in ? *(const uint4*)(ph + c * 8) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      grads(g[i], u[i], h[i], dg[i], du[i]);
+      top = umax(top, highest(dg[i], du[i]));
+    }
+    const float f = factor(top);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)i * T + t;
+      if (c < units) store(c, dg[i], du[i], f);
+    }
+  } else {
+    uint32_t top = 0;
+    float dg[8], du[8];
+    for (int64_t c = t; c < units; c += T) {
+      grads(*(const uint4*)(pg + c * 8), *(const uint4*)(pg + a.n + c * 8), *(const uint4*)(ph + c * 8), dg, du);
+      top = umax(top, highest(dg, du));
+    }
+    const float f = factor(top);
+    for (int64_t c = t; c < units; c += T) {
+      grads(*(const uint4*)(pg + c * 8), *(const uint4*)(pg + a.n + c * 8), *(const uint4*)(ph + c * 8), dg, du);
+      store(c, dg, du, f);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ products
+// out[row][k] = factors * sum over z of P[z][k] Q[z][row]
+//   DX:   rows are tokens, z the 2 n weight rows: P the weights (E4M3 in memory, f16 from there), Q = D16 [row][z]
+//   else: rows are the 2 n weight rows, z tokens: P = x [z][k], Q = Db [z][row], bf16
+// Tiles of 256 k x 256 rows by four waves (2 x 2) of 128 x 128 each: 64 MFMAs of 16x16x32 for 16 fragments
+// a step, which leaves half of LDS's read rate free.  P is the MFMA's A operand, so a lane's four results
+// lie side by side along k.  Operands whose z is not contiguous in memory are kept in LDS as they come
+// ([z][256], 512-byte rows) and read with the transposing read (four z of a lane's column each).
+// Ring of four steps: at the barrier that opens step s everything of step s + 1 has landed, s + 2 and s + 3 are
+// under way, and the copies of s + 4 go out during the step.  Fragments of step s + 1 replace those of s one by
+// one behind their last use.
+struct GatedProduct {
+  const uint8_t* codes[2];   // DX: gate and up, E4M3 [n][k]
+  const uint32_t* tab;       // DX: [2 n / 128][k / 128] f16 scale twice
+  const uint16_t* p;         // x [z][k] (not DX)
+  const uint16_t* q;         // D16 [rows][z], or Db [z padded][rows]
+  const uint8_t* zeros;      // 512 bytes
+  const float* rs;           // DX: [rows]
+  const float* cols;         // DX: [k / 128]
+  int64_t rows, z, n, k;     // z: 2 n, or tokens; n: rows of one weight
+  uint16_t* out[2];          // DX: dx twice; else the gate's and the up projection's gradient
+  int64_t tiles_r, tiles_c, full;
+  int32_t split;
+  float* part;               // [split workgroup][256 rows][256 k]
+};
+
+// 16-byte slot of logical slot s in LDS row z (32 slots of 512 bytes).  A transposing read of 32 lanes
+// covers eight rows (z & 3 and bit 3 vary) by 32 bytes, which slot bits 1..3 spread over the banks; a write
+// of 16 lanes to even slots of one row takes odd ones in the row's second half.
+__device__ __forceinline__ int zslot(int z, int s) { return s ^ ((s >> 4) & 1) ^ (2 * ((z & 3) | ((z >> 1) & 4))); }
+
+template <bool DX>
+__global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const GemmWork work = gemm_schedule(a.tiles_r, a.tiles_c, a.full, a.split);
+  const int64_t c0 = (int64_t)__builtin_amdgcn_readfirstlane((int)work.tn) * kBTile;
+  const int64_t r0 = (int64_t)__builtin_amdgcn_readfirstlane((int)work.tm) * kBTile;
+  const int part_no = __builtin_amdgcn_readfirstlane(work.split);
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int wk = wave & 1, wr = wave >> 1;
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t steps = (a.z + kBStep - 1) / kBStep;
+  const int nsplit = __builtin_amdgcn_readfirstlane(work.nsplit);
+  const int64_t per = (steps + nsplit - 1) / nsplit;
+  const int64_t st0 = part_no * per;
+  const int64_t st1 = st0 + per < steps ? st0 + per : steps;
+  const int64_t c_room = a.k - c0;         // at least 128
+  const int64_t r_last = a.rows - 1 - r0;
+  auto clamp_st = [&](int64_t st) { return st < st1 ? st : st1 - 1; };
+  const uint32_t lds0 = lds_addr(smem);
+
+  // ---- copies of a step, the same number by every wave
+  constexpr int kCopies = DX ? 7 : 8;      // DX: two of codes, one of scales, four of D
+  uint32_t oq[4];                          // DX: D rows 64 wave + 16 c + lane / 4, 16-byte slot lane % 4
+  uint32_t oc[2];                          // DX: weight rows 8 wave + 4 c + lane / 16, 16 codes a lane
+  uint32_t oz;                             // not DX: D rows (z) 8 wave + 2 c + lane / 32, slot lane % 32
+  int64_t kcol = 0;
+  if (DX) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int row = 64 * wave + 16 * c + (lane >> 2);
+      oq[c] = (uint32_t)((row < r_last ? row : r_last) * a.z * 2 + ((lane & 3) ^ ((lane >> 4) & 3)) * 16);
+    }
+    kcol = 16 * (lane & 15) < c_room ? 16 * (lane & 15) : 16 * (lane & 15) - 128;   // past k: the 128 columns before
+#pragma unroll
+    for (int c = 0; c < 2; ++c) oc[c] = (uint32_t)((8 * wave + 4 * c + (lane >> 4)) * a.k + kcol);
+  } else {
+    // (8 wave + 2 c + lane / 32: z & 3 is 2 (c & 1) + lane / 32 and bit 3 of z is wave & 1)
+    oz = (uint32_t)((lane >> 5) * a.rows * 2);
+  }
+  auto copy = [&](int64_t st, int slot, int c) {
+    if (DX) {
+      const int64_t z0 = st * kBStep;
+      const int up = z0 >= a.n;
+      const int64_t zr = up ? z0 - a.n : z0;
+      if (c < 2)
+        lds_copy16((up ? a.codes[1] : a.codes[0]) + zr * a.k + c0, oc[c],
+                   lds0 + kBCodeOff + slot * kBCodeBytes + (8 * wave + 4 * c) * 256);
+      else if (c == 2)
+        lds_copy4_va(a.tab + (z0 / 128) * (a.k / 128) + (c0 + kcol) / 128, lds0 + kBScaleOff + slot * kBScaleBytes + wave * 256);
+      else
+        lds_copy16((const uint8_t*)(a.q + r0 * a.z + z0), oq[c - 3], lds0 + slot * kBRowsBytes + (64 * wave + 16 * (c - 3)) * 64);
+    } else {
+      const int cc = c & 3;
+      const int zl = 8 * wave + 2 * cc;          // this copy's first row
+      const int mask = (2 * (cc & 1) + (lane >> 5)) | ((wave & 1) << 2);
+      const int p = lane & 31;
+      const int s = p ^ ((p >> 4) & 1) ^ (2 * mask);
+      const uint32_t dst = lds0 + slot * (2 * kBRowsBytes) + (c < 4 ? 0 : kBRowsBytes) + zl * 512;
+      if (c < 4) {
+        const int64_t z = st * kBStep + zl + (lane >> 5);
+        const int col = 8 * s < c_room ? 8 * s : 8 * s - 128;
+        const uint8_t* src = z < a.z ? (const uint8_t*)(a.p + z * a.k + c0 + col) : a.zeros + 16 * p;
+        lds_copy16_va(src, dst);
+      } else {
+        lds_copy16((const uint8_t*)(a.q + (st * kBStep + zl) * a.rows + r0), oz + 16 * s, dst);
+      }
+    }
+  };
+
+  // ---- DX: the step's weights from codes to f16, 32 a thread, those that the thread itself copied
+  auto read_codes = [&](int slot, int c) {
+    return *(const i32x4*)(smem + kBCodeOff + slot * kBCodeBytes + (8 * wave + 4 * c + (lane >> 4)) * 256 + 16 * (lane & 15));
+  };
+  auto read_scale = [&](int slot) {
+    return __builtin_bit_cast(f16x2, *(const uint32_t*)(smem + kBScaleOff + slot * kBScaleBytes + wave * 256 + 4 * lane));
+  };
+  auto dequant = [&](const i32x4& w, const f16x2& sc, int buf, int c) {
+    const int z = 8 * wave + 4 * c + (lane >> 4), u = lane & 15;
+    uint8_t* row = smem + kBWOff + buf * kBRowsBytes + z * 512;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const f16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w[2 * q], 1.0f, false) * sc;
+      const f16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w[2 * q], 1.0f, true) * sc;
+      const f16x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w[2 * q + 1], 1.0f, false) * sc;
+      const f16x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w[2 * q + 1], 1.0f, true) * sc;
+      *(f16x8*)(row + zslot(z, 2 * u + q) * 16) = f16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+    }
+  };
+
+  // ---- fragments: lane (r, g) has z 8 g .. 8 g + 7 of column (or row) r.  Transposing reads: lanes 4 e + b name row
+  // 8 g + 4 q + e, columns 4 b .. 4 b + 3, and receive rows 8 g + 4 q + (0 .. 3) of column r.
+  const int te = r >> 2, tb = r & 3;
+  const int tmask = te | ((g & 1) << 2);
+  auto tr_base = [&](int half) {   // of fragment 0 of columns 128 half ..; fragment i flips bits 5 .. 7
+    return (8 * g + te) * 512 + half * 256 + tmask * 32 + (((tb >> 1) ^ half) << 4) + (tb & 1) * 8;
+  };
+  const int ta = tr_base(wk), tbq = tr_base(wr);
+  auto read_tr = [&](const uint8_t* tile, int base, int i) {
+    const uint8_t* p = tile + (base ^ (i << 5));
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
+    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 2048));
+    return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto read_a = [&](int64_t s, int i) {
+    return DX ? read_tr(smem + kBWOff + (int)(s & 1) * kBRowsBytes, ta, i)
+              : read_tr(smem + (int)(s & 3) * (2 * kBRowsBytes), ta, i);
+  };
+  auto read_b = [&](int64_t s, int j) {
+    if (DX) {
+      const int row = 128 * wr + 16 * j + r;
+      return *(const i32x4*)(smem + (int)(s & 3) * kBRowsBytes + row * 64 + (g ^ ((r >> 2) & 3)) * 16);
+    }
+    return read_tr(smem + (int)(s & 3) * (2 * kBRowsBytes) + kBRowsBytes, tbq, j);
+  };
+  auto mfma = [](const i32x4& x, const i32x4& y, const f32x4& c) {
+    if (DX) return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
+  };
+
+  f32x4 acc[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  i32x4 af[8], bf[8];
+  if (st1 > st0) {
+#pragma unroll
+    for (int s = 0; s < kBRing; ++s)
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) copy(clamp_st(st0 + s), s, c);
+    if (DX) {
+      asm volatile("s_waitcnt vmcnt(14)" ::: "memory");   // steps 0 and 1
+#pragma unroll
+      for (int q = 0; q < 4; ++q) dequant(read_codes(q >> 1, q & 1), read_scale(q >> 1), q >> 1, q & 1);
+    } else {
+      asm volatile("s_waitcnt vmcnt(24)" ::: "memory");   // step 0
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) af[i] = read_a(0, i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bf[j] = read_b(0, j);
+  }
+  for (int64_t st = st0; st < st1; ++st) {
+    const int64_t s = st - st0;
+    // landed: step s + 1, and of step s + 2 the codes and scales (DX), which each lane reads for itself
+    if (DX)
+      asm volatile("s_waitcnt vmcnt(11)" ::: "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+    __syncthreads();
+    const int64_t next = clamp_st(st + kBRing);
+    const int slot = (int)(s & 3);
+    i32x4 cw = {0, 0, 0, 0};
+    f16x2 sc = {0, 0};
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        acc[i][j] = mfma(af[i], bf[j], acc[i][j]);
+        if (i == 7) {
+          __builtin_amdgcn_sched_barrier(0);
+          bf[j] = read_b(s + 1, j);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      af[i] = read_a(s + 1, i);
+      if (i < kCopies) copy(next, slot, i);
+      if (!DX && i == 7) copy(next, slot, 7);
+      if (DX) {   // codes of step s + 2, read two fragments before their conversion
+        if (i == 3 || i == 6) dequant(cw, sc, slot & 1, i == 6);
+        if (i == 0) sc = read_scale((int)((s + 2) & 3));
+        if (i == 1 || i == 4) cw = read_codes((int)((s + 2) & 3), i == 4);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+  // lane: k = c0 + 128 wk + 16 i + 4 g + (0 .. 3), row r0 + 128 wr + 16 j + r
+  if (DX) {
+    const float cf = a.cols[(128 * wk < c_room ? c0 + 128 * wk : c0) / 128];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t row = r0 + 128 * wr + 16 * j + r;
+      const float rf = a.rs[row < a.rows ? row : a.rows - 1];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i][j] = acc[i][j] * rf * cf;
+    }
+  }
+  if (work.slot >= 0) {   // a part of a tile's depth, added by gated_join_kernel
+    float* pt = a.part + work.slot * (kBTile * kBTile);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *(f32x4*)(pt + (128 * wr + 16 * j + r) * kBTile + 128 * wk + 16 * i + 4 * g) = acc[i][j];
+    return;
+  }
+  __syncthreads();   // every wave is done with the operands
+  uint8_t* stage = smem + wave * kBStagePerWave;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const f32x4 v = acc[i][j];
+      *(uint2*)(stage + (16 * j + r) * kBPitch + (16 * i + 4 * g) * 2) =
+          make_uint2(pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3]));
+    }
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's LDS writes are done
+  if (128 * wk >= c_room) return;
+  // the wave's 128 rows lie in one of the two outputs (n is a multiple of 128)
+  const int64_t row0 = r0 + 128 * wr;
+  const int second = !DX && row0 >= a.n;
+  uint16_t* base = (second ? a.out[1] : a.out[0]) + (second ? row0 - a.n : row0) * a.k + c0 + 128 * wk + (lane & 15) * 8;
+#pragma unroll
+  for (int q = 0; q < 32; ++q) {
+    const int row = 4 * q + (lane >> 4);
+    if (row0 + row < a.rows) *(i32x4*)(base + row * a.k) = *(const i32x4*)(stage + row * kBPitch + (lane & 15) * 16);
+  }
+}
+
+// The parts of split tiles added in their order: 4 rows of a tile a workgroup, 4 columns a thread.
+__global__ __launch_bounds__(256) void gated_join_kernel(GatedProduct a) {
+  const int64_t tail = blockIdx.x / 64;
+  const int row = (int)(blockIdx.x % 64) * 4 + (int)(threadIdx.x >> 6);
+  const int col = (int)(threadIdx.x & 63) * 4;
+  int64_t tr, tc;
+  gemm_group_tile(a.full + tail, a.tiles_r, a.tiles_c, tr, tc);
+  const int64_t rr = tr * kBTile + row, c = tc * kBTile + col;
+  if (rr >= a.rows || c >= a.k) return;
+  const float* p = a.part + tail * a.split * (kBTile * kBTile) + row * kBTile + col;
+  f32x4 v = *(const f32x4*)p;
+  for (int sp = 1; sp < a.split; ++sp) v += *(const f32x4*)(p + (int64_t)sp * (kBTile * kBTile));
+  const int second = rr >= a.n && a.out[1] != a.out[0];
+  store4((second ? a.out[1] : a.out[0]) - (second ? a.n * a.k : 0), 0, a.k, rr, c, v, a.k);
+}
+
+// Tiles and how the ones behind the last full round of the chip are split along z.
+struct ProductPlan {
+  int64_t tiles_r, tiles_c, full;
+  int32_t split;
+  size_t part_bytes() const {
+    return split > 1 ? (size_t)(tiles_r * tiles_c - full) * (size_t)split * kBTile * kBTile * 4 : 0;
+  }
+};
+constexpr int64_t kBCUs = 256;
+ProductPlan plan_product(int64_t rows, int64_t z, int64_t k) {
+  ProductPlan p;
+  p.tiles_r = (rows + kBTile - 1) / kBTile;
+  p.tiles_c = (k + kBTile - 1) / kBTile;
+  const int64_t tiles = p.tiles_r * p.tiles_c, rem = tiles % kBCUs;
+  const int64_t steps = (z + kBStep - 1) / kBStep;
+  int64_t sp = rem > 0 && rem <= kBCUs / 2 ? kBCUs / rem : 1;
+  if (sp > 32) sp = 32;
+  if (sp > steps / 8) sp = steps / 8;
+  p.split = (int32_t)(sp > 1 ? sp : 1);
+  p.full = p.split > 1 ? tiles - rem : tiles;
+  return p;
+}
+
+template <bool DX>
+hipError_t launch_product(GatedProduct a, const ProductPlan& p, hipStream_t s) {
+  a.tiles_r = p.tiles_r;
+  a.tiles_c = p.tiles_c;
+  a.full = p.full;
+  a.split = p.split;
+  const int64_t tail = p.tiles_r * p.tiles_c - p.full;
+  hipError_t e = hipFuncSetAttribute((const void*)gated_product_kernel<DX>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kBLds);
+  if (e != hipSuccess) return e;
+  gated_product_kernel<DX><<<(unsigned)(p.full + tail * p.split), kBThreads, kBLds, s>>>(a);
+  if (p.split > 1) gated_join_kernel<<<(unsigned)(tail * 64), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+constexpr size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// zeros | cols | scale table | row factors | D16 | Db | parts (both products', one after the other)
+struct BwdWs {
+  uint32_t* zeros;
+  float* cols;
+  uint32_t* tab;
+  float* rs;
+  uint16_t* d16;
+  uint16_t* db;
+  float* part;
+  size_t bytes;
+};
+int64_t pad_tokens(int64_t m) { return (m + kBStep - 1) / kBStep * kBStep; }
+BwdWs bwd_ws(void* ws, int64_t m, int64_t n, int64_t k) {
+  BwdWs w;
+  char* p = (char*)ws;
+  size_t at = 0;
+  auto take = [&](size_t b) {
+    char* q = p + at;
+    at += up256(b);
+    return q;
+  };
+  w.zeros = (uint32_t*)take(512);
+  w.cols = (float*)take((size_t)(k / 128) * 4);
+  w.tab = (uint32_t*)take((size_t)(2 * n / 128) * (size_t)(k / 128) * 4);
+  w.rs = (float*)take((size_t)m * 4);
+  w.d16 = (uint16_t*)take((size_t)m * 2 * n * 2);
+  w.db = (uint16_t*)take((size_t)pad_tokens(m) * 2 * n * 2);
+  const size_t a = plan_product(m, 2 * n, k).part_bytes(), b = plan_product(2 * n, m, k).part_bytes();
+  w.part = (float*)take(a > b ? a : b);
+  w.bytes = at;
+  return w;
+}
+
+}  // namespace
+
+// 32-bit offsets of a tile's rows, and grids
+bool gated_backward_launchable(int64_t m, int64_t n, int64_t k) {
+  if (m <= 0 || n <= 0 || k <= 0 || n % 128 || k % 128 || n >= (int64_t(1) << 22) || k >= (int64_t(1) << 22)) return false;
+  const int64_t rt = (m + 255) / 256, jt = (2 * n + 255) / 256, ct = (k + 255) / 256;
+  return rt * ct < (int64_t(1) << 24) && jt * ct < (int64_t(1) << 24);
+}
+
+size_t gated_backward_bytes(int64_t m, int64_t n, int64_t k) { return bwd_ws(nullptr, m, n, k).bytes; }
+
+hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
+  if (!gated_backward_launchable(a.m, a.n, a.k)) return hipErrorInvalidValue;
+  const BwdWs w = bwd_ws(a.scratch, a.m, a.n, a.k);
+  gated_scales_kernel<<<(unsigned)(a.k / 128), 256, 0, s>>>(a.sg, a.su, a.pow2, a.n / 128, a.k / 128, w.tab, w.cols, w.zeros);
+  GateGrad d;
+  d.dh = a.dh;
+  d.gu = a.gu;
+  d.m = a.m;
+  d.n = a.n;
+  d.m_pad = pad_tokens(a.m);
+  d.d16 = a.dx ? w.d16 : nullptr;
+  d.rs = w.rs;
+  d.db = a.dgate ? w.db : nullptr;
+  const unsigned grid = (unsigned)(a.dgate ? d.m_pad : a.m);
+  if (a.n <= 2048) gate_grad_kernel<256, 1><<<grid, 256, 0, s>>>(d);
+  else if (a.n <= 4096) gate_grad_kernel<256, 2><<<grid, 256, 0, s>>>(d);
+  else if (a.n <= 8192) gate_grad_kernel<512, 2><<<grid, 512, 0, s>>>(d);
+  else if (a.n <= 16384) gate_grad_kernel<1024, 2><<<grid, 1024, 0, s>>>(d);
+  else gate_grad_kernel<1024, 0><<<grid, 1024, 0, s>>>(d);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  GatedProduct p = {};
+  p.n = a.n;
+  p.k = a.k;
+  p.zeros = (const uint8_t*)w.zeros;
+  p.part = w.part;
+  if (a.dx) {
+    p.codes[0] = a.wg;
+    p.codes[1] = a.wu;
+    p.tab = w.tab;
+    p.q = w.d16;
+    p.rs = w.rs;
+    p.cols = w.cols;
+    p.rows = a.m;
+    p.z = 2 * a.n;
+    p.out[0] = p.out[1] = a.dx;
+    e = launch_product<true>(p, plan_product(a.m, 2 * a.n, a.k), s);
+    if (e != hipSuccess) return e;
+  }
+  if (a.dgate) {
+    p.p = a.x;
+    p.q = w.db;
+    p.rows = 2 * a.n;
+    p.z = a.m;
+    p.out[0] = a.dgate;
+    p.out[1] = a.dup;
+    e = launch_product<false>(p, plan_product(2 * a.n, a.m, a.k), s);
+  }
+  return e;
+}
+
+}  // namespace ql

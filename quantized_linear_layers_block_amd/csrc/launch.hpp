@@ -273,4 +273,24 @@ bool gated_launchable(int64_t m, int64_t n, int64_t k);
 size_t gated_scratch_bytes(int64_t m, int64_t n);
 hipError_t launch_gated(const Gated& a, hipStream_t s);
 
+// ---- its backward pass (gated_bwd.hip)
+struct GatedBackward {
+  const uint16_t* dh;       // bf16 [m][n]
+  const uint16_t* gu;       // bf16 [m][2 n]
+  const uint16_t* x;        // bf16 [m][k], read for dgate and dup
+  const uint8_t* wg;
+  const void* sg;
+  const uint8_t* wu;
+  const void* su;
+  bool pow2;
+  int64_t m, n, k;
+  uint16_t* dx;             // bf16 [m][k], or null
+  uint16_t* dgate;          // bf16 [n][k], both or neither
+  uint16_t* dup;
+  void* scratch;            // gated_backward_bytes
+};
+bool gated_backward_launchable(int64_t m, int64_t n, int64_t k);
+size_t gated_backward_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s);
+
 }  // namespace ql

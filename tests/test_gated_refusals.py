@@ -44,6 +44,27 @@ def test_gated_forward_errors():
     assert f(ws=None) == b.QL_ERR_WORKSPACE and f(wsb=need - 1) == b.QL_ERR_WORKSPACE
 
 
+def test_gated_backward_errors():
+    need = b.qlinear_gated_backward_workspace(5, 256, 512)
+    assert need >= 2 * 5 * 512 * 2
+    for bad in [(0, 256, 512), (5, 100, 512), (5, 256, 64), (5, 1 << 22, 128), (5, 128, 1 << 22)]:
+        assert b.qlinear_gated_backward_workspace(*bad) == 0, bad
+
+    def f(gate=_w(), up=_w(), dh=FAKE, gu=FAKE, x=FAKE, m=5, dx=FAKE, dg=FAKE, du=FAKE, ws=FAKE, wsb=1 << 40):
+        return L.qlinear_gated_backward(ctypes.byref(gate), ctypes.byref(up), dh, gu, x, m, dx, dg, du, ws, wsb, None)
+
+    assert f(dh=None) == b.QL_ERR_NULL and f(gu=None) == b.QL_ERR_NULL and f(x=None) == b.QL_ERR_NULL
+    assert f(dx=None, dg=None, du=None) == b.QL_ERR_NULL and f(dg=None) == b.QL_ERR_NULL and f(du=None) == b.QL_ERR_NULL
+    assert f(_w(codes=None)) == b.QL_ERR_NULL
+    nv = b.QWeight(b.QL_NVFP4, 0, 256, 512, FAKE, FAKE, FAKE)
+    assert f(nv, nv) == b.QL_ERR_FORMAT and f(up=_w(b.QL_FP8_POW2)) == b.QL_ERR_FORMAT
+    assert f(up=_w(n=128)) == b.QL_ERR_SHAPE and f(m=0) == b.QL_ERR_SHAPE and f(m=(1 << 24) + 1) == b.QL_ERR_SHAPE
+    assert f(_w(n=128, k=1 << 22), _w(n=128, k=1 << 22)) == b.QL_ERR_SHAPE
+    for name in ("dh", "gu", "x", "dx", "dg", "du", "ws"):
+        assert f(**{name: FAKE + 8}) == b.QL_ERR_ALIGN, name
+    assert f(ws=None) == b.QL_ERR_WORKSPACE and f(wsb=need - 1) == b.QL_ERR_WORKSPACE
+
+
 def test_helpers_refuse():
     torch = pytest.importorskip("torch")
     import quantized_linear_layers_block_amd as ql
@@ -57,3 +78,6 @@ def test_helpers_refuse():
         ql.gated_forward_fp8(w, ql.FP8Weight.empty(256, 256, device="cpu"), xq, sx)
     with pytest.raises(ValueError):
         ql.gated_forward(w, ql.FP8Weight.empty(128, 256, device="cpu", pow2=True), xq, sx)
+    dh = torch.zeros((3, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        ql.gated_backward(w, w, dh, dh)
