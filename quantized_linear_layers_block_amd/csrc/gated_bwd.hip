@@ -44,7 +44,7 @@ __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
 // [2 n / 128][k / 128] holds f16(scale * 2^-E) twice in a word, cols [k / 128] 2^E.
 __global__ __launch_bounds__(256) void gated_scales_kernel(const void* __restrict__ sg, const void* __restrict__ su,
                                                            int pow2, int64_t nb, int64_t kb, uint32_t* __restrict__ tab,
-                                                           float* __restrict__ cols, uint32_t* __restrict__ zeros) {
+                                                           float* __restrict__ cols) {
   __shared__ uint32_t red[4];
   const int64_t c = blockIdx.x;
   auto scale = [&](int64_t i) {
@@ -64,7 +64,6 @@ __global__ __launch_bounds__(256) void gated_scales_kernel(const void* __restric
     tab[i * kb + c] = f16_pair(s, s);
   }
   if (threadIdx.x == 0) cols[c] = pow2_float(e);
-  if (c == 0 && threadIdx.x < 128) zeros[threadIdx.x] = 0;   // what rows past the last token read
 }
 
 // --------------------------------------------------------------------------------- D
@@ -89,6 +88,9 @@ struct GateGrad {
   uint16_t* d16;        // f16 [m][2 n], or null
   float* rs;            // [m]
   uint16_t* db;         // bf16 [m_pad][2 n], rows past m zero, or null
+  const uint16_t* x;    // with db: [m][k], whose last m % 32 rows go to xt [32][k], the others there zero
+  uint16_t* xt;
+  int64_t k;
 };
 
 // T threads a row, NV units of 8 columns each in registers (NV 0: any n, read twice).  Bound by memory:
@@ -99,9 +101,14 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
   const int64_t row = blockIdx.x;
   const int64_t units = a.n / 8;
   const int t = threadIdx.x;
-  if (row >= a.m) {   // padding of db
-    for (int64_t u = t; u < 2 * units; u += T) *(uint4*)(a.db + row * 2 * a.n + u * 8) = make_uint4(0, 0, 0, 0);
-    return;
+  if (a.db && a.m_pad != a.m && row >= a.m_pad - kBStep) {   // the last step of the weights' gradients is not full
+    uint16_t* p = a.xt + (row - (a.m_pad - kBStep)) * a.k;
+    for (int64_t u = t; u < a.k / 8; u += T)
+      *(uint4*)(p + u * 8) = row < a.m ? *(const uint4*)(a.x + row * a.k + u * 8) : make_uint4(0, 0, 0, 0);
+    if (row >= a.m) {
+      for (int64_t u = t; u < 2 * units; u += T) *(uint4*)(a.db + row * 2 * a.n + u * 8) = make_uint4(0, 0, 0, 0);
+      return;
+    }
   }
   const uint16_t* ph = a.dh + row * a.n;
   const uint16_t* pg = a.gu + row * 2 * a.n;
@@ -190,15 +197,19 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
 // a step, which leaves half of LDS's read rate free.  P is the MFMA's A operand, so a lane's four results
 // lie side by side along k.  Operands whose z is not contiguous in memory are kept in LDS as they come
 // ([z][256], 512-byte rows) and read with the transposing read (four z of a lane's column each).
-// Ring of four steps: at the barrier that opens step s everything of step s + 1 has landed, s + 2 and s + 3 are
-// under way, and the copies of s + 4 go out during the step.  Fragments of step s + 1 replace those of s one by
-// one behind their last use.
+// A step is eight rows of eight MFMAs: a P fragment against the eight Q fragments, which stay.  The next row's
+// P fragment is read during a row; the last row also takes the next step's Q fragments, each behind its
+// last use, so the barrier stands before it.  Ring of four steps: copies of step s + 3 go out during step s, and
+// at its barrier s + 1 has landed (DX: and s + 2's codes, which each lane reads for itself: a step's weights are
+// turned into f16 during the step before).  With one wave a SIMD nothing else fills the matrix unit's time, so
+// every other instruction has its place behind an MFMA, a few behind each: reads, copies and conversions
+// in a row's end cost the unit half its time (4.1 of 8.3 million cycles at 8192 x 14336 x 4096).
 struct GatedProduct {
   const uint8_t* codes[2];   // DX: gate and up, E4M3 [n][k]
   const uint32_t* tab;       // DX: [2 n / 128][k / 128] f16 scale twice
   const uint16_t* p;         // x [z][k] (not DX)
+  const uint16_t* xt;        // its last step, rows past the last token zero, where z is no multiple of 32
   const uint16_t* q;         // D16 [rows][z], or Db [z padded][rows]
-  const uint8_t* zeros;      // 512 bytes
   const float* rs;           // DX: [rows]
   const float* cols;         // DX: [k / 128]
   int64_t rows, z, n, k;     // z: 2 n, or tokens; n: rows of one weight
@@ -234,25 +245,35 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
   auto clamp_st = [&](int64_t st) { return st < st1 ? st : st1 - 1; };
   const uint32_t lds0 = lds_addr(smem);
 
-  // ---- copies of a step, the same number by every wave
-  constexpr int kCopies = DX ? 7 : 8;      // DX: two of codes, one of scales, four of D
+  // ---- copies of a step, the same number by every wave, from uniform addresses with a lane's 32-bit offset
+  constexpr int kCopies = DX ? 7 : 8;      // DX: two of codes, one of scales, four of D; else four of x, four of D
   uint32_t oq[4];                          // DX: D rows 64 wave + 16 c + lane / 4, 16-byte slot lane % 4
   uint32_t oc[2];                          // DX: weight rows 8 wave + 4 c + lane / 16, 16 codes a lane
-  uint32_t oz;                             // not DX: D rows (z) 8 wave + 2 c + lane / 32, slot lane % 32
-  int64_t kcol = 0;
+  uint32_t osc = 0;                        // DX: the scale word of the lane's codes
+  uint32_t op[2], od[2];                   // not DX: rows (z) 8 wave + 2 c + lane / 32, slot lane % 32; by c's parity
   if (DX) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int row = 64 * wave + 16 * c + (lane >> 2);
       oq[c] = (uint32_t)((row < r_last ? row : r_last) * a.z * 2 + ((lane & 3) ^ ((lane >> 4) & 3)) * 16);
     }
-    kcol = 16 * (lane & 15) < c_room ? 16 * (lane & 15) : 16 * (lane & 15) - 128;   // past k: the 128 columns before
+    // columns past k: the 128 before
+    const int col = 16 * (lane & 15) < c_room ? 16 * (lane & 15) : 16 * (lane & 15) - 128;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) oc[c] = (uint32_t)((8 * wave + 4 * c + (lane >> 4)) * a.k + kcol);
+    for (int c = 0; c < 2; ++c) oc[c] = (uint32_t)((8 * wave + 4 * c + (lane >> 4)) * a.k + col);
+    osc = (uint32_t)(col / 128 * 4);
   } else {
-    // (8 wave + 2 c + lane / 32: z & 3 is 2 (c & 1) + lane / 32 and bit 3 of z is wave & 1)
-    oz = (uint32_t)((lane >> 5) * a.rows * 2);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      // z & 3 is 2 (c & 1) + lane / 32, and bit 3 of z is wave & 1
+      const int mask = (2 * c + (lane >> 5)) | ((wave & 1) << 2);
+      const int s = (lane & 31) ^ ((lane >> 4) & 1) ^ (2 * mask);
+      const int col = 8 * s < c_room ? 8 * s : 8 * s - 128;
+      op[c] = (uint32_t)((lane >> 5) * a.k * 2 + col * 2);
+      od[c] = (uint32_t)((lane >> 5) * a.rows * 2 + s * 16);
+    }
   }
+  const int64_t whole = DX ? steps : a.z / kBStep;   // steps of whole rows of x
   auto copy = [&](int64_t st, int slot, int c) {
     if (DX) {
       const int64_t z0 = st * kBStep;
@@ -262,24 +283,17 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
         lds_copy16((up ? a.codes[1] : a.codes[0]) + zr * a.k + c0, oc[c],
                    lds0 + kBCodeOff + slot * kBCodeBytes + (8 * wave + 4 * c) * 256);
       else if (c == 2)
-        lds_copy4_va(a.tab + (z0 / 128) * (a.k / 128) + (c0 + kcol) / 128, lds0 + kBScaleOff + slot * kBScaleBytes + wave * 256);
+        lds_copy4((const uint8_t*)(a.tab + (z0 / 128) * (a.k / 128) + c0 / 128), osc,
+                  lds0 + kBScaleOff + slot * kBScaleBytes + wave * 256);
       else
         lds_copy16((const uint8_t*)(a.q + r0 * a.z + z0), oq[c - 3], lds0 + slot * kBRowsBytes + (64 * wave + 16 * (c - 3)) * 64);
     } else {
-      const int cc = c & 3;
-      const int zl = 8 * wave + 2 * cc;          // this copy's first row
-      const int mask = (2 * (cc & 1) + (lane >> 5)) | ((wave & 1) << 2);
-      const int p = lane & 31;
-      const int s = p ^ ((p >> 4) & 1) ^ (2 * mask);
+      const int zl = 8 * wave + 2 * (c & 3);     // this copy's first row
       const uint32_t dst = lds0 + slot * (2 * kBRowsBytes) + (c < 4 ? 0 : kBRowsBytes) + zl * 512;
-      if (c < 4) {
-        const int64_t z = st * kBStep + zl + (lane >> 5);
-        const int col = 8 * s < c_room ? 8 * s : 8 * s - 128;
-        const uint8_t* src = z < a.z ? (const uint8_t*)(a.p + z * a.k + c0 + col) : a.zeros + 16 * p;
-        lds_copy16_va(src, dst);
-      } else {
-        lds_copy16((const uint8_t*)(a.q + (st * kBStep + zl) * a.rows + r0), oz + 16 * s, dst);
-      }
+      if (c < 4)
+        lds_copy16((const uint8_t*)((st < whole ? a.p + st * kBStep * a.k : a.xt) + zl * a.k + c0), op[c & 1], dst);
+      else
+        lds_copy16((const uint8_t*)(a.q + (st * kBStep + zl) * a.rows + r0), od[c & 1], dst);
     }
   };
 
@@ -290,17 +304,17 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
   auto read_scale = [&](int slot) {
     return __builtin_bit_cast(f16x2, *(const uint32_t*)(smem + kBScaleOff + slot * kBScaleBytes + wave * 256 + 4 * lane));
   };
-  auto dequant = [&](const i32x4& w, const f16x2& sc, int buf, int c) {
-    const int z = 8 * wave + 4 * c + (lane >> 4), u = lane & 15;
-    uint8_t* row = smem + kBWOff + buf * kBRowsBytes + z * 512;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const f16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w[2 * q], 1.0f, false) * sc;
-      const f16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w[2 * q], 1.0f, true) * sc;
-      const f16x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w[2 * q + 1], 1.0f, false) * sc;
-      const f16x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w[2 * q + 1], 1.0f, true) * sc;
-      *(f16x8*)(row + zslot(z, 2 * u + q) * 16) = f16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+  f16x2 wv[4];
+  auto dequant = [&](const i32x4& w, const f16x2& sc, int buf, int c, int q) {   // piece q of ten of one 16-code unit
+    const int h = q / 5, e = q % 5;
+    if (e < 4) {
+      wv[e] = (e & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w[2 * h + (e >> 1)], 1.0f, true)
+                     : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w[2 * h + (e >> 1)], 1.0f, false)) * sc;
+      return;
     }
+    const int z = 8 * wave + 4 * c + (lane >> 4), u = lane & 15;
+    *(f16x8*)(smem + kBWOff + buf * kBRowsBytes + z * 512 + zslot(z, 2 * u + h) * 16) =
+        f16x8{wv[0][0], wv[0][1], wv[1][0], wv[1][1], wv[2][0], wv[2][1], wv[3][0], wv[3][1]};
   };
 
   // ---- fragments: lane (r, g) has z 8 g .. 8 g + 7 of column (or row) r.  Transposing reads: lanes 4 e + b name row
@@ -310,23 +324,23 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
   auto tr_base = [&](int half) {   // of fragment 0 of columns 128 half ..; fragment i flips bits 5 .. 7
     return (8 * g + te) * 512 + half * 256 + tmask * 32 + (((tb >> 1) ^ half) << 4) + (tb & 1) * 8;
   };
-  const int ta = tr_base(wk), tbq = tr_base(wr);
-  auto read_tr = [&](const uint8_t* tile, int base, int i) {
-    const uint8_t* p = tile + (base ^ (i << 5));
+  int ta[8], tq[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    ta[i] = tr_base(wk) ^ (i << 5);
+    tq[i] = DX ? (128 * wr + 16 * i + r) * 64 + (g ^ ((r >> 2) & 3)) * 16 : kBRowsBytes + (tr_base(wr) ^ (i << 5));
+  }
+  auto read_tr = [&](const uint8_t* p) {
     const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
     const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 2048));
     return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  auto read_a = [&](int64_t s, int i) {
-    return DX ? read_tr(smem + kBWOff + (int)(s & 1) * kBRowsBytes, ta, i)
-              : read_tr(smem + (int)(s & 3) * (2 * kBRowsBytes), ta, i);
+  auto read_p = [&](int64_t s, int i) {
+    return read_tr(smem + ta[i] + (DX ? kBWOff + (int)(s & 1) * kBRowsBytes : (int)(s & 3) * (2 * kBRowsBytes)));
   };
-  auto read_b = [&](int64_t s, int j) {
-    if (DX) {
-      const int row = 128 * wr + 16 * j + r;
-      return *(const i32x4*)(smem + (int)(s & 3) * kBRowsBytes + row * 64 + (g ^ ((r >> 2) & 3)) * 16);
-    }
-    return read_tr(smem + (int)(s & 3) * (2 * kBRowsBytes) + kBRowsBytes, tbq, j);
+  auto read_q = [&](int64_t s, int j) {
+    if (DX) return *(const i32x4*)(smem + tq[j] + (int)(s & 3) * kBRowsBytes);
+    return read_tr(smem + tq[j] + (int)(s & 3) * (2 * kBRowsBytes));
   };
   auto mfma = [](const i32x4& x, const i32x4& y, const f32x4& c) {
     if (DX) return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
@@ -338,58 +352,64 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  i32x4 af[8], bf[8];
+  i32x4 pf[2], qf[8];
   if (st1 > st0) {
 #pragma unroll
-    for (int s = 0; s < kBRing; ++s)
+    for (int s = 0; s < 3; ++s)
 #pragma unroll
       for (int c = 0; c < kCopies; ++c) copy(clamp_st(st0 + s), s, c);
     if (DX) {
-      asm volatile("s_waitcnt vmcnt(14)" ::: "memory");   // steps 0 and 1
+      asm volatile("s_waitcnt vmcnt(11)" ::: "memory");   // step 0, and step 1's codes and scales
+      const f16x2 sc = read_scale(0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) dequant(read_codes(q >> 1, q & 1), read_scale(q >> 1), q >> 1, q & 1);
+      for (int c = 0; c < 2; ++c) {
+        const i32x4 w = read_codes(0, c);
+#pragma unroll
+        for (int q = 0; q < 10; ++q) dequant(w, sc, 0, c, q);
+      }
     } else {
-      asm volatile("s_waitcnt vmcnt(24)" ::: "memory");   // step 0
+      asm volatile("s_waitcnt vmcnt(16)" ::: "memory");   // step 0
     }
     __syncthreads();
+    pf[0] = read_p(0, 0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) af[i] = read_a(0, i);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) bf[j] = read_b(0, j);
+    for (int j = 0; j < 8; ++j) qf[j] = read_q(0, j);
   }
   for (int64_t st = st0; st < st1; ++st) {
     const int64_t s = st - st0;
-    // landed: step s + 1, and of step s + 2 the codes and scales (DX), which each lane reads for itself
-    if (DX)
-      asm volatile("s_waitcnt vmcnt(11)" ::: "memory");
-    else
-      asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
-    __syncthreads();
-    const int64_t next = clamp_st(st + kBRing);
-    const int slot = (int)(s & 3);
+    const int64_t ahead = clamp_st(st + 3);
+    const int slot = (int)((s + 3) & 3), cslot = (int)((s + 1) & 3), wbuf = (int)((s + 1) & 1);
     i32x4 cw = {0, 0, 0, 0};
     f16x2 sc = {0, 0};
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      if (i == 7) {
+        // this step's fragments are read; the next step has landed and (DX) its weights are written, and so have
+        // the codes of the one behind.  Under way may be (DX) four copies of that and the seven of step s + 3, else
+        // the eight of step s + 2 and seven of s + 3.
+        if (DX)
+          asm volatile("s_waitcnt vmcnt(11)" ::: "memory");
+        else
+          asm volatile("s_waitcnt vmcnt(15)" ::: "memory");
+        __syncthreads();
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        acc[i][j] = mfma(af[i], bf[j], acc[i][j]);
+        acc[i][j] = mfma(pf[i & 1], qf[j], acc[i][j]);
+        if (j == 0) pf[(i & 1) ^ 1] = i < 7 ? read_p(s, i + 1) : read_p(s + 1, 0);
         if (i == 7) {
           __builtin_amdgcn_sched_barrier(0);
-          bf[j] = read_b(s + 1, j);
+          qf[j] = read_q(s + 1, j);
         }
+        if (j == 2 && i < kCopies) copy(ahead, slot, i);
+        if (DX) {   // the next step's weights: 2 units of ten pieces, their codes read a row before
+          if (j == 1 && i == 0) sc = read_scale(cslot);
+          if (j == 1 && (i == 0 || i == 3)) cw = read_codes(cslot, i == 3);
+          if (j >= 3 && (i == 1 || i == 2)) dequant(cw, sc, wbuf, 0, 5 * (i - 1) + j - 3);
+          if (j >= 3 && (i == 4 || i == 5)) dequant(cw, sc, wbuf, 1, 5 * (i - 4) + j - 3);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
-      af[i] = read_a(s + 1, i);
-      if (i < kCopies) copy(next, slot, i);
-      if (!DX && i == 7) copy(next, slot, 7);
-      if (DX) {   // codes of step s + 2, read two fragments before their conversion
-        if (i == 3 || i == 6) dequant(cw, sc, slot & 1, i == 6);
-        if (i == 0) sc = read_scale((int)((s + 2) & 3));
-        if (i == 1 || i == 4) cw = read_codes((int)((s + 2) & 3), i == 4);
-      }
-      __builtin_amdgcn_sched_barrier(0);
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -492,9 +512,9 @@ hipError_t launch_product(GatedProduct a, const ProductPlan& p, hipStream_t s) {
 
 constexpr size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// zeros | cols | scale table | row factors | D16 | Db | parts (both products', one after the other)
+// last rows of x | cols | scale table | row factors | D16 | Db | parts (both products', one after the other)
 struct BwdWs {
-  uint32_t* zeros;
+  uint16_t* xt;
   float* cols;
   uint32_t* tab;
   float* rs;
@@ -513,7 +533,7 @@ BwdWs bwd_ws(void* ws, int64_t m, int64_t n, int64_t k) {
     at += up256(b);
     return q;
   };
-  w.zeros = (uint32_t*)take(512);
+  w.xt = (uint16_t*)take((size_t)kBStep * (size_t)k * 2);
   w.cols = (float*)take((size_t)(k / 128) * 4);
   w.tab = (uint32_t*)take((size_t)(2 * n / 128) * (size_t)(k / 128) * 4);
   w.rs = (float*)take((size_t)m * 4);
@@ -539,7 +559,7 @@ size_t gated_backward_bytes(int64_t m, int64_t n, int64_t k) { return bwd_ws(nul
 hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
   if (!gated_backward_launchable(a.m, a.n, a.k)) return hipErrorInvalidValue;
   const BwdWs w = bwd_ws(a.scratch, a.m, a.n, a.k);
-  gated_scales_kernel<<<(unsigned)(a.k / 128), 256, 0, s>>>(a.sg, a.su, a.pow2, a.n / 128, a.k / 128, w.tab, w.cols, w.zeros);
+  gated_scales_kernel<<<(unsigned)(a.k / 128), 256, 0, s>>>(a.sg, a.su, a.pow2, a.n / 128, a.k / 128, w.tab, w.cols);
   GateGrad d;
   d.dh = a.dh;
   d.gu = a.gu;
@@ -549,6 +569,9 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
   d.d16 = a.dx ? w.d16 : nullptr;
   d.rs = w.rs;
   d.db = a.dgate ? w.db : nullptr;
+  d.x = a.x;
+  d.xt = w.xt;
+  d.k = a.k;
   const unsigned grid = (unsigned)(a.dgate ? d.m_pad : a.m);
   if (a.n <= 2048) gate_grad_kernel<256, 1><<<grid, 256, 0, s>>>(d);
   else if (a.n <= 4096) gate_grad_kernel<256, 2><<<grid, 256, 0, s>>>(d);
@@ -560,7 +583,6 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
   GatedProduct p = {};
   p.n = a.n;
   p.k = a.k;
-  p.zeros = (const uint8_t*)w.zeros;
   p.part = w.part;
   if (a.dx) {
     p.codes[0] = a.wg;
@@ -577,6 +599,7 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
   }
   if (a.dgate) {
     p.p = a.x;
+    p.xt = w.xt;
     p.q = w.db;
     p.rows = 2 * a.n;
     p.z = a.m;
