@@ -9,6 +9,8 @@
 // (its rounding, 2^-11, is far below that of a bf16 result; the weights meet it as f16 too, E4M3 values
 // times their scales rounded once more), and as bf16 for the weights' gradients, whose sums run over
 // tokens of any size, so that a row's factor could not be taken out.
+#include <type_traits>
+
 #include "common.hpp"
 #include "gemm_common.hpp"
 #include "launch.hpp"
@@ -197,13 +199,15 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
 // a step, which leaves half of LDS's read rate free.  P is the MFMA's A operand, so a lane's four results
 // lie side by side along k.  Operands whose z is not contiguous in memory are kept in LDS as they come
 // ([z][256], 512-byte rows) and read with the transposing read (four z of a lane's column each).
-// A step is eight rows of eight MFMAs: a P fragment against the eight Q fragments, which stay.  The next row's
-// P fragment is read during a row; the last row also takes the next step's Q fragments, each behind its
-// last use, so the barrier stands before it.  Ring of four steps: copies of step s + 3 go out during step s, and
-// at its barrier s + 1 has landed (DX: and s + 2's codes, which each lane reads for itself: a step's weights are
-// turned into f16 during the step before).  With one wave a SIMD nothing else fills the matrix unit's time, so
-// every other instruction has its place behind an MFMA, a few behind each: reads, copies and conversions
-// in a row's end cost the unit half its time (4.1 of 8.3 million cycles at 8192 x 14336 x 4096).
+// A step is four quarters of 16 MFMAs (4 fragments of each operand): P low Q low, P high Q low, P high Q high,
+// P low Q high.  Each quarter reads the four fragments that are new in a later one, over those that no
+// MFMA needs any more, so LDS, which the four waves' fragments keep busy for half of a step's time and the
+// copies for a quarter, is read evenly (all of Q read in an eighth of the step made the MFMAs wait for it).
+// The barrier stands in the middle: there every fragment of step s is read and step s + 1 has landed, so
+// that from there to the next middle the copies of s + 4 go into the place of s, in a ring of four.  DX: the codes of
+// s + 2 have landed too, and each lane turns those that it copied itself into f16 from this middle to the next.
+// With one wave a SIMD nothing else fills the matrix unit's time, so every other instruction has its place
+// behind an MFMA, a few behind each.
 struct GatedProduct {
   const uint8_t* codes[2];   // DX: gate and up, E4M3 [n][k]
   const uint32_t* tab;       // DX: [2 n / 128][k / 128] f16 scale twice
@@ -223,6 +227,10 @@ struct GatedProduct {
 // covers eight rows (z & 3 and bit 3 vary) by 32 bytes, which slot bits 1..3 spread over the banks; a write
 // of 16 lanes to even slots of one row takes odd ones in the row's second half.
 __device__ __forceinline__ int zslot(int z, int s) { return s ^ ((s >> 4) & 1) ^ (2 * ((z & 3) | ((z >> 1) & 4))); }
+
+// The 16-byte slot of a 64-byte row of D that holds slot 0, by bits 2 and 3 of the row: 16-byte reads of one slot of
+// 16 rows go over LDS as rows 0..3 and 12..15 of one slot with 4..11 of the next, which these four keep apart.
+__device__ __forceinline__ int dslot(int q) { return ((q << 1) ^ (q & 2 ? 3 : 0)) & 3; }
 
 template <bool DX>
 __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a) {
@@ -245,56 +253,50 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
   auto clamp_st = [&](int64_t st) { return st < st1 ? st : st1 - 1; };
   const uint32_t lds0 = lds_addr(smem);
 
-  // ---- copies of a step, the same number by every wave, from uniform addresses with a lane's 32-bit offset
-  constexpr int kCopies = DX ? 7 : 8;      // DX: two of codes, one of scales, four of D; else four of x, four of D
-  uint32_t oq[4];                          // DX: D rows 64 wave + 16 c + lane / 4, 16-byte slot lane % 4
-  uint32_t oc[2];                          // DX: weight rows 8 wave + 4 c + lane / 16, 16 codes a lane
-  uint32_t osc = 0;                        // DX: the scale word of the lane's codes
-  uint32_t op[2], od[2];                   // not DX: rows (z) 8 wave + 2 c + lane / 32, slot lane % 32; by c's parity
+  // ---- copies of a step, the same by every wave, from uniform addresses with a lane's 32-bit offsets
+  //   DX: seven: weight rows 8 wave + 4 c + lane / 16 (two, 16 codes a lane), a scale word for a lane's codes, D rows
+  //   64 wave + 16 c + lane / 4, 16-byte slot lane % 4 (four)
+  //   else eight: rows (z) 8 wave + 2 c + lane / 32, slot lane % 32, of x and of D (four each)
+  constexpr uint32_t kUp = 3072;     // see lds_copy16x4
+  uint32_t op[4], od[4], osc = 0;
   if (DX) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int row = 64 * wave + 16 * c + (lane >> 2);
-      oq[c] = (uint32_t)((row < r_last ? row : r_last) * a.z * 2 + ((lane & 3) ^ ((lane >> 4) & 3)) * 16);
-    }
     // columns past k: the 128 before
     const int col = 16 * (lane & 15) < c_room ? 16 * (lane & 15) : 16 * (lane & 15) - 128;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) oc[c] = (uint32_t)((8 * wave + 4 * c + (lane >> 4)) * a.k + col);
+    for (int c = 0; c < 4; ++c) {
+      const int row = 64 * wave + 16 * c + (lane >> 2);
+      od[c] = (uint32_t)((row < r_last ? row : r_last) * a.z * 2 + ((lane & 3) ^ dslot(lane >> 4)) * 16) + kUp - 1024 * c;
+      op[c] = (uint32_t)((8 * wave + 4 * (c & 1) + (lane >> 4)) * a.k + col) + kUp - 1024 * (c & 1);
+    }
     osc = (uint32_t)(col / 128 * 4);
   } else {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      // z & 3 is 2 (c & 1) + lane / 32, and bit 3 of z is wave & 1
-      const int mask = (2 * c + (lane >> 5)) | ((wave & 1) << 2);
-      const int s = (lane & 31) ^ ((lane >> 4) & 1) ^ (2 * mask);
+    for (int c = 0; c < 4; ++c) {
+      const int z = 8 * wave + 2 * c + (lane >> 5);
+      const int s = zslot(z, lane & 31);     // (its own inverse)
       const int col = 8 * s < c_room ? 8 * s : 8 * s - 128;
-      op[c] = (uint32_t)((lane >> 5) * a.k * 2 + col * 2);
-      od[c] = (uint32_t)((lane >> 5) * a.rows * 2 + s * 16);
+      op[c] = (uint32_t)(z * a.k * 2 + col * 2) + kUp - 1024 * c;
+      od[c] = (uint32_t)(z * a.rows * 2 + s * 16) + kUp - 1024 * c;
     }
   }
   const int64_t whole = DX ? steps : a.z / kBStep;   // steps of whole rows of x
-  auto copy = [&](int64_t st, int slot, int c) {
+  auto copy_p = [&](int64_t st, int slot) {
     if (DX) {
       const int64_t z0 = st * kBStep;
       const int up = z0 >= a.n;
-      const int64_t zr = up ? z0 - a.n : z0;
-      if (c < 2)
-        lds_copy16((up ? a.codes[1] : a.codes[0]) + zr * a.k + c0, oc[c],
-                   lds0 + kBCodeOff + slot * kBCodeBytes + (8 * wave + 4 * c) * 256);
-      else if (c == 2)
-        lds_copy4((const uint8_t*)(a.tab + (z0 / 128) * (a.k / 128) + c0 / 128), osc,
-                  lds0 + kBScaleOff + slot * kBScaleBytes + wave * 256);
-      else
-        lds_copy16((const uint8_t*)(a.q + r0 * a.z + z0), oq[c - 3], lds0 + slot * kBRowsBytes + (64 * wave + 16 * (c - 3)) * 64);
+      lds_copy16x2((up ? a.codes[1] : a.codes[0]) + (up ? z0 - a.n : z0) * a.k + c0 - kUp, op[0], op[1],
+                   lds0 + kBCodeOff + slot * kBCodeBytes + wave * 2048);
+      lds_copy4((const uint8_t*)(a.tab + (z0 / 128) * (a.k / 128) + c0 / 128), osc,
+                lds0 + kBScaleOff + slot * kBScaleBytes + wave * 256);
     } else {
-      const int zl = 8 * wave + 2 * (c & 3);     // this copy's first row
-      const uint32_t dst = lds0 + slot * (2 * kBRowsBytes) + (c < 4 ? 0 : kBRowsBytes) + zl * 512;
-      if (c < 4)
-        lds_copy16((const uint8_t*)((st < whole ? a.p + st * kBStep * a.k : a.xt) + zl * a.k + c0), op[c & 1], dst);
-      else
-        lds_copy16((const uint8_t*)(a.q + (st * kBStep + zl) * a.rows + r0), od[c & 1], dst);
+      lds_copy16x4((const uint8_t*)((st < whole ? a.p + st * kBStep * a.k : a.xt) + c0) - kUp, op[0], op[1], op[2], op[3],
+                   lds0 + slot * (2 * kBRowsBytes) + wave * 4096);
     }
+  };
+  auto copy_d = [&](int64_t st, int slot) {
+    const uint16_t* d = a.q + (DX ? r0 * a.z + st * kBStep : st * kBStep * a.rows + r0);
+    lds_copy16x4((const uint8_t*)d - kUp, od[0], od[1], od[2], od[3],
+                 lds0 + (DX ? slot * kBRowsBytes : slot * (2 * kBRowsBytes) + kBRowsBytes) + wave * 4096);
   };
 
   // ---- DX: the step's weights from codes to f16, 32 a thread, those that the thread itself copied
@@ -305,6 +307,14 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
     return __builtin_bit_cast(f16x2, *(const uint32_t*)(smem + kBScaleOff + slot * kBScaleBytes + wave * 256 + 4 * lane));
   };
   f16x2 wv[4];
+  int wo[2][2];   // where a thread's pieces of 8 go
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int z = 8 * wave + 4 * c + (lane >> 4);
+      wo[c][h] = z * 512 + zslot(z, 2 * (lane & 15) + h) * 16;
+    }
   auto dequant = [&](const i32x4& w, const f16x2& sc, int buf, int c, int q) {   // piece q of ten of one 16-code unit
     const int h = q / 5, e = q % 5;
     if (e < 4) {
@@ -312,8 +322,7 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
                      : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w[2 * h + (e >> 1)], 1.0f, false)) * sc;
       return;
     }
-    const int z = 8 * wave + 4 * c + (lane >> 4), u = lane & 15;
-    *(f16x8*)(smem + kBWOff + buf * kBRowsBytes + z * 512 + zslot(z, 2 * u + h) * 16) =
+    *(f16x8*)(smem + wo[c][h] + kBWOff + buf * kBRowsBytes) =
         f16x8{wv[0][0], wv[0][1], wv[1][0], wv[1][1], wv[2][0], wv[2][1], wv[3][0], wv[3][1]};
   };
 
@@ -328,19 +337,19 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     ta[i] = tr_base(wk) ^ (i << 5);
-    tq[i] = DX ? (128 * wr + 16 * i + r) * 64 + (g ^ ((r >> 2) & 3)) * 16 : kBRowsBytes + (tr_base(wr) ^ (i << 5));
+    tq[i] = DX ? (128 * wr + 16 * i + r) * 64 + (g ^ dslot(r >> 2)) * 16 : kBRowsBytes + (tr_base(wr) ^ (i << 5));
   }
   auto read_tr = [&](const uint8_t* p) {
     const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
     const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 2048));
     return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  auto read_p = [&](int64_t s, int i) {
-    return read_tr(smem + ta[i] + (DX ? kBWOff + (int)(s & 1) * kBRowsBytes : (int)(s & 3) * (2 * kBRowsBytes)));
+  auto read_p = [&](int s, int i) {
+    return read_tr(smem + ta[i] + (DX ? kBWOff + (s & 1) * kBRowsBytes : (s & 3) * (2 * kBRowsBytes)));
   };
-  auto read_q = [&](int64_t s, int j) {
-    if (DX) return *(const i32x4*)(smem + tq[j] + (int)(s & 3) * kBRowsBytes);
-    return read_tr(smem + tq[j] + (int)(s & 3) * (2 * kBRowsBytes));
+  auto read_q = [&](int s, int j) {
+    if (DX) return *(const i32x4*)(smem + tq[j] + (s & 3) * kBRowsBytes);
+    return read_tr(smem + tq[j] + (s & 3) * (2 * kBRowsBytes));
   };
   auto mfma = [](const i32x4& x, const i32x4& y, const f32x4& c) {
     if (DX) return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
@@ -352,65 +361,79 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  i32x4 pf[2], qf[8];
+  i32x4 pf[8], qf[8], cw = {0, 0, 0, 0};
+  f16x2 sc = {0, 0};
   if (st1 > st0) {
 #pragma unroll
-    for (int s = 0; s < 3; ++s)
-#pragma unroll
-      for (int c = 0; c < kCopies; ++c) copy(clamp_st(st0 + s), s, c);
+    for (int s = 0; s < kBRing; ++s) {
+      copy_p(clamp_st(st0 + s), s);
+      copy_d(clamp_st(st0 + s), s);
+    }
     if (DX) {
-      asm volatile("s_waitcnt vmcnt(11)" ::: "memory");   // step 0, and step 1's codes and scales
-      const f16x2 sc = read_scale(0);
+      asm volatile("s_waitcnt vmcnt(18)" ::: "memory");   // step 0, and step 1's codes and scales
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const i32x4 w = read_codes(0, c);
+      for (int u = 0; u < 3; ++u) {   // all of step 0, half of step 1
+        sc = read_scale(u >> 1);
+        cw = read_codes(u >> 1, u & 1);
 #pragma unroll
-        for (int q = 0; q < 10; ++q) dequant(w, sc, 0, c, q);
+        for (int q = 0; q < 10; ++q) dequant(cw, sc, u >> 1, u & 1, q);
       }
     } else {
-      asm volatile("s_waitcnt vmcnt(16)" ::: "memory");   // step 0
+      asm volatile("s_waitcnt vmcnt(24)" ::: "memory");   // step 0
     }
     __syncthreads();
-    pf[0] = read_p(0, 0);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) qf[j] = read_q(0, j);
+    for (int i = 0; i < 4; ++i) {
+      if (i < 3) pf[i] = read_p(0, i);
+      qf[i] = read_q(0, i);
+    }
   }
-  for (int64_t st = st0; st < st1; ++st) {
-    const int64_t s = st - st0;
-    const int64_t ahead = clamp_st(st + 3);
-    const int slot = (int)((s + 3) & 3), cslot = (int)((s + 1) & 3), wbuf = (int)((s + 1) & 1);
-    i32x4 cw = {0, 0, 0, 0};
-    f16x2 sc = {0, 0};
+  // one step, the U-th of each four (the ring's places are then constants); true if it was the last
+  auto step = [&](auto U, int64_t st) {
+    constexpr int s = decltype(U)::value;
+    const int64_t ahead = clamp_st(st + kBRing);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i == 7) {
-        // this step's fragments are read; the next step has landed and (DX) its weights are written, and so have
-        // the codes of the one behind.  Under way may be (DX) four copies of that and the seven of step s + 3, else
-        // the eight of step s + 2 and seven of s + 3.
+    for (int h = 0; h < 4; ++h) {
+      if (h == 2) {
+        // under way may be the copies of steps s + 2 (DX: four of them) and s + 3
         if (DX)
           asm volatile("s_waitcnt vmcnt(11)" ::: "memory");
         else
-          asm volatile("s_waitcnt vmcnt(15)" ::: "memory");
+          asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
         __syncthreads();
       }
+      const int i0 = h == 1 || h == 2 ? 4 : 0, j0 = h >= 2 ? 4 : 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        acc[i][j] = mfma(pf[i & 1], qf[j], acc[i][j]);
-        if (j == 0) pf[(i & 1) ^ 1] = i < 7 ? read_p(s, i + 1) : read_p(s + 1, 0);
-        if (i == 7) {
-          __builtin_amdgcn_sched_barrier(0);
-          qf[j] = read_q(s + 1, j);
+      for (int x = 0; x < 16; ++x) {
+        const int i = i0 + x / 4, j = j0 + x % 4;
+        acc[i][j] = mfma(pf[i], qf[j], acc[i][j]);
+        if (h == 0) {
+          if (x == 0) pf[3] = read_p(s, 3);
+          if (x == 2 || x == 5 || x == 8 || x == 11) pf[4 + x / 3] = read_p(s, 4 + x / 3);
         }
-        if (j == 2 && i < kCopies) copy(ahead, slot, i);
-        if (DX) {   // the next step's weights: 2 units of ten pieces, their codes read a row before
-          if (j == 1 && i == 0) sc = read_scale(cslot);
-          if (j == 1 && (i == 0 || i == 3)) cw = read_codes(cslot, i == 3);
-          if (j >= 3 && (i == 1 || i == 2)) dequant(cw, sc, wbuf, 0, 5 * (i - 1) + j - 3);
-          if (j >= 3 && (i == 4 || i == 5)) dequant(cw, sc, wbuf, 1, 5 * (i - 4) + j - 3);
+        if (h == 1 && x % 3 == 0 && x < 12) qf[4 + x / 3] = read_q(s, 4 + x / 3);
+        if (h == 2 && x % 3 == 0 && x < 12) qf[x / 3] = read_q(s + 1, x / 3);
+        if (h == 3 && x % 4 == 0 && x > 0) pf[x / 4 - 1] = read_p(s + 1, x / 4 - 1);
+        if (h == 2 && x == 8) copy_p(ahead, s & 3);
+        if (h == 3 && x == 7) copy_d(ahead, s & 3);
+        if (DX) {   // a unit of ten pieces in two quarters
+          const int d = h >= 2 ? s + 2 : s + 1;
+          if ((h == 0 || h == 2) && x == 1) {
+            sc = read_scale(d & 3);
+            cw = read_codes(d & 3, h == 0);
+          }
+          const int q = x == 9 ? 0 : x == 10 ? 1 : x == 12 ? 2 : x == 13 ? 3 : x == 15 ? 4 : -1;
+          if (q >= 0) dequant(cw, sc, d & 1, h < 2, q + 5 * (h & 1));
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+    return st + 1 >= st1;
+  };
+  for (int64_t st = st0; st < st1; st += 4) {
+    if (step(std::integral_constant<int, 0>(), st) || step(std::integral_constant<int, 1>(), st + 1) ||
+        step(std::integral_constant<int, 2>(), st + 2) || step(std::integral_constant<int, 3>(), st + 3))
+      break;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 

@@ -185,6 +185,28 @@ __device__ __forceinline__ void lds_copy16_va(const void* src, uint32_t lds_base
                : "memory");
 }
 
+// Four such copies, to LDS pieces 1 KB apart from lds_base on (two: the first two).  An instruction's offset counts
+// for the global and for the LDS address alike, so the c-th lane offset is 1024 c less than what it names
+// (the caller lowers `base` and raises the offsets, which are unsigned, by the same).
+__device__ __forceinline__ void lds_copy16x4(const uint8_t* base, uint32_t o0, uint32_t o1, uint32_t o2, uint32_t o3,
+                                             uint32_t lds_base) {
+  uint32_t saved;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %6\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
+               "global_load_lds_dwordx4 %2, %5 offset:1024\n\tglobal_load_lds_dwordx4 %3, %5 offset:2048\n\t"
+               "global_load_lds_dwordx4 %4, %5 offset:3072\n\ts_mov_b32 m0, %0"
+               : "=&s"(saved)
+               : "v"(o0), "v"(o1), "v"(o2), "v"(o3), "s"(base), "s"(lds_base)
+               : "memory");
+}
+__device__ __forceinline__ void lds_copy16x2(const uint8_t* base, uint32_t o0, uint32_t o1, uint32_t lds_base) {
+  uint32_t saved;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %4\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
+               "global_load_lds_dwordx4 %2, %3 offset:1024\n\ts_mov_b32 m0, %0"
+               : "=&s"(saved)
+               : "v"(o0), "v"(o1), "s"(base), "s"(lds_base)
+               : "memory");
+}
+
 // 4 bytes per lane from a per-lane 64-bit global address into LDS at m0 + 4 * lane.
 __device__ __forceinline__ void lds_copy4_va(const void* src, uint32_t lds_base) {
   uint32_t saved;
