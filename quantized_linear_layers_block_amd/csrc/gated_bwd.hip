@@ -191,10 +191,42 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
   }
 }
 
+// ------------------------------------------------------------------------------ weights, turned
+// For many tokens: both weights as f16 [k][2 n], times their scales from tab.  A workgroup takes 128 x 128 codes; a
+// thread 8 rows by 4 columns, whose bytes v_perm_b32 turns into 4 columns of 8.  Bound by memory (1 byte read, 2
+// written a weight): 70 us for 2 x 14336 x 4096, which the product gains back from about 1500 tokens on.
+__global__ __launch_bounds__(256) void gated_weights_kernel(const uint8_t* __restrict__ wg, const uint8_t* __restrict__ wu,
+                                                            const uint32_t* __restrict__ tab, int64_t n, int64_t k,
+                                                            uint16_t* __restrict__ w16) {
+  const int64_t z0 = (int64_t)blockIdx.y * 128, k0 = (int64_t)blockIdx.x * 128;
+  const uint8_t* w = z0 < n ? wg + z0 * k : wu + (z0 - n) * k;
+  const f16x2 sc = __builtin_bit_cast(f16x2, tab[(z0 / 128) * (k / 128) + k0 / 128]);
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int z = 64 * (wave & 1) + 8 * (lane & 7), c = 32 * (2 * q + (wave >> 1)) + 4 * (lane >> 3);
+    uint32_t v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = *(const uint32_t*)(w + (int64_t)(z + e) * k + k0 + c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {   // column c + e: byte e of the eight rows
+      const uint32_t pick = 0x0C0C0400u + (uint32_t)e * 0x0101u;   // (byte e of the second operand, then of the first)
+      uint32_t out[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const uint32_t two = __builtin_amdgcn_perm(v[2 * h + 1], v[2 * h], pick);
+        out[h] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(two, 1.0f, false) * sc);
+      }
+      *(uint4*)(w16 + (k0 + c + e) * 2 * n + z0 + z) = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+  }
+}
+
 // ------------------------------------------------------------------------------ products
 // out[row][k] = factors * sum over z of P[z][k] Q[z][row]
-//   DX:   rows are tokens, z the 2 n weight rows: P the weights (E4M3 in memory, f16 from there), Q = D16 [row][z]
-//   else: rows are the 2 n weight rows, z tokens: P = x [z][k], Q = Db [z][row], bf16
+//   kDx:  rows are tokens, z the 2 n weight rows: P the weights (E4M3 in memory, f16 from there), Q = D16 [row][z]
+//   kDxT: the same with P = the weights as f16 [k][z], turned by gated_weights_kernel beforehand
+//   kDw:  rows are the 2 n weight rows, z tokens: P = x [z][k], Q = Db [z][row], bf16
 // Tiles of 256 k x 256 rows by four waves (2 x 2) of 128 x 128 each: 64 MFMAs of 16x16x32 for 16 fragments
 // a step, which leaves half of LDS's read rate free.  P is the MFMA's A operand, so a lane's four results
 // lie side by side along k.  Operands whose z is not contiguous in memory are kept in LDS as they come
@@ -204,20 +236,21 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
 // MFMA needs any more, so LDS, which the four waves' fragments keep busy for half of a step's time and the
 // copies for a quarter, is read evenly (all of Q read in an eighth of the step made the MFMAs wait for it).
 // The barrier stands in the middle: there every fragment of step s is read and step s + 1 has landed, so
-// that from there to the next middle the copies of s + 4 go into the place of s, in a ring of four.  DX: the codes of
+// that from there to the next middle the copies of s + 4 go into the place of s, in a ring of four.  kDx: the codes of
 // s + 2 have landed too, and each lane turns those that it copied itself into f16 from this middle to the next.
 // With one wave a SIMD nothing else fills the matrix unit's time, so every other instruction has its place
 // behind an MFMA, a few behind each.
+enum Kind { kDw, kDx, kDxT };
 struct GatedProduct {
-  const uint8_t* codes[2];   // DX: gate and up, E4M3 [n][k]
-  const uint32_t* tab;       // DX: [2 n / 128][k / 128] f16 scale twice
-  const uint16_t* p;         // x [z][k] (not DX)
+  const uint8_t* codes[2];   // kDx: gate and up, E4M3 [n][k]
+  const uint32_t* tab;       // kDx: [2 n / 128][k / 128] f16 scale twice
+  const uint16_t* p;         // kDw: x [z][k]; kDxT: the weights, f16 [k][z]
   const uint16_t* xt;        // its last step, rows past the last token zero, where z is no multiple of 32
   const uint16_t* q;         // D16 [rows][z], or Db [z padded][rows]
-  const float* rs;           // DX: [rows]
-  const float* cols;         // DX: [k / 128]
+  const float* rs;           // kDx, kDxT: [rows]
+  const float* cols;         // the same: [k / 128]
   int64_t rows, z, n, k;     // z: 2 n, or tokens; n: rows of one weight
-  uint16_t* out[2];          // DX: dx twice; else the gate's and the up projection's gradient
+  uint16_t* out[2];          // kDx, kDxT: dx twice; else the gate's and the up projection's gradient
   int64_t tiles_r, tiles_c, full;
   int32_t split;
   float* part;               // [split workgroup][256 rows][256 k]
@@ -232,9 +265,10 @@ __device__ __forceinline__ int zslot(int z, int s) { return s ^ ((s >> 4) & 1) ^
 // 16 rows go over LDS as rows 0..3 and 12..15 of one slot with 4..11 of the next, which these four keep apart.
 __device__ __forceinline__ int dslot(int q) { return ((q << 1) ^ (q & 2 ? 3 : 0)) & 3; }
 
-template <bool DX>
+template <Kind KIND>
 __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a) {
   extern __shared__ __align__(16) uint8_t smem[];
+  constexpr bool FUSED = KIND == kDx, TURNED = KIND == kDxT, DW = KIND == kDw;
   const GemmWork work = gemm_schedule(a.tiles_r, a.tiles_c, a.full, a.split);
   const int64_t c0 = (int64_t)__builtin_amdgcn_readfirstlane((int)work.tn) * kBTile;
   const int64_t r0 = (int64_t)__builtin_amdgcn_readfirstlane((int)work.tm) * kBTile;
@@ -254,19 +288,23 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
   const uint32_t lds0 = lds_addr(smem);
 
   // ---- copies of a step, the same by every wave, from uniform addresses with a lane's 32-bit offsets
-  //   DX: seven: weight rows 8 wave + 4 c + lane / 16 (two, 16 codes a lane), a scale word for a lane's codes, D rows
+  //   kDx: seven: weight rows 8 wave + 4 c + lane / 16 (two, 16 codes a lane), a scale word for a lane's codes, D rows
   //   64 wave + 16 c + lane / 4, 16-byte slot lane % 4 (four)
-  //   else eight: rows (z) 8 wave + 2 c + lane / 32, slot lane % 32, of x and of D (four each)
+  //   kDxT: eight: rows 64 wave + 16 c + lane / 4 of the weights (columns of k) and of D
+  //   kDw: eight: rows (z) 8 wave + 2 c + lane / 32, slot lane % 32, of x and of D
   constexpr uint32_t kUp = 3072;     // see lds_copy16x4
   uint32_t op[4], od[4], osc = 0;
-  if (DX) {
+  if (!DW) {
     // columns past k: the 128 before
     const int col = 16 * (lane & 15) < c_room ? 16 * (lane & 15) : 16 * (lane & 15) - 128;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int row = 64 * wave + 16 * c + (lane >> 2);
-      od[c] = (uint32_t)((row < r_last ? row : r_last) * a.z * 2 + ((lane & 3) ^ dslot(lane >> 4)) * 16) + kUp - 1024 * c;
-      op[c] = (uint32_t)((8 * wave + 4 * (c & 1) + (lane >> 4)) * a.k + col) + kUp - 1024 * (c & 1);
+      const int row = 64 * wave + 16 * c + (lane >> 2), in = ((lane & 3) ^ dslot(lane >> 4)) * 16;
+      od[c] = (uint32_t)((row < r_last ? row : r_last) * a.z * 2 + in) + kUp - 1024 * c;
+      if (TURNED)
+        op[c] = (uint32_t)((row < c_room ? row : row - 128) * a.z * 2 + in) + kUp - 1024 * c;
+      else
+        op[c] = (uint32_t)((8 * wave + 4 * (c & 1) + (lane >> 4)) * a.k + col) + kUp - 1024 * (c & 1);
     }
     osc = (uint32_t)(col / 128 * 4);
   } else {
@@ -279,27 +317,30 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
       od[c] = (uint32_t)(z * a.rows * 2 + s * 16) + kUp - 1024 * c;
     }
   }
-  const int64_t whole = DX ? steps : a.z / kBStep;   // steps of whole rows of x
+  const int64_t whole = DW ? a.z / kBStep : steps;   // steps of whole rows of x
   auto copy_p = [&](int64_t st, int slot) {
-    if (DX) {
+    if (FUSED) {
       const int64_t z0 = st * kBStep;
       const int up = z0 >= a.n;
       lds_copy16x2((up ? a.codes[1] : a.codes[0]) + (up ? z0 - a.n : z0) * a.k + c0 - kUp, op[0], op[1],
                    lds0 + kBCodeOff + slot * kBCodeBytes + wave * 2048);
       lds_copy4((const uint8_t*)(a.tab + (z0 / 128) * (a.k / 128) + c0 / 128), osc,
                 lds0 + kBScaleOff + slot * kBScaleBytes + wave * 256);
+    } else if (TURNED) {
+      lds_copy16x4((const uint8_t*)(a.p + c0 * a.z + st * kBStep) - kUp, op[0], op[1], op[2], op[3],
+                   lds0 + slot * (2 * kBRowsBytes) + wave * 4096);
     } else {
       lds_copy16x4((const uint8_t*)((st < whole ? a.p + st * kBStep * a.k : a.xt) + c0) - kUp, op[0], op[1], op[2], op[3],
                    lds0 + slot * (2 * kBRowsBytes) + wave * 4096);
     }
   };
   auto copy_d = [&](int64_t st, int slot) {
-    const uint16_t* d = a.q + (DX ? r0 * a.z + st * kBStep : st * kBStep * a.rows + r0);
+    const uint16_t* d = a.q + (DW ? st * kBStep * a.rows + r0 : r0 * a.z + st * kBStep);
     lds_copy16x4((const uint8_t*)d - kUp, od[0], od[1], od[2], od[3],
-                 lds0 + (DX ? slot * kBRowsBytes : slot * (2 * kBRowsBytes) + kBRowsBytes) + wave * 4096);
+                 lds0 + (FUSED ? slot * kBRowsBytes : slot * (2 * kBRowsBytes) + kBRowsBytes) + wave * 4096);
   };
 
-  // ---- DX: the step's weights from codes to f16, 32 a thread, those that the thread itself copied
+  // ---- kDx: the step's weights from codes to f16, 32 a thread, those that the thread itself copied
   auto read_codes = [&](int slot, int c) {
     return *(const i32x4*)(smem + kBCodeOff + slot * kBCodeBytes + (8 * wave + 4 * c + (lane >> 4)) * 256 + 16 * (lane & 15));
   };
@@ -336,8 +377,9 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
   int ta[8], tq[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    ta[i] = tr_base(wk) ^ (i << 5);
-    tq[i] = DX ? (128 * wr + 16 * i + r) * 64 + (g ^ dslot(r >> 2)) * 16 : kBRowsBytes + (tr_base(wr) ^ (i << 5));
+    const int in = 16 * i * 64 + r * 64 + (g ^ dslot(r >> 2)) * 16;
+    ta[i] = TURNED ? 128 * wk * 64 + in : tr_base(wk) ^ (i << 5);
+    tq[i] = DW ? kBRowsBytes + (tr_base(wr) ^ (i << 5)) : (TURNED ? kBRowsBytes : 0) + 128 * wr * 64 + in;
   }
   auto read_tr = [&](const uint8_t* p) {
     const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
@@ -345,14 +387,15 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
     return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
   auto read_p = [&](int s, int i) {
-    return read_tr(smem + ta[i] + (DX ? kBWOff + (s & 1) * kBRowsBytes : (s & 3) * (2 * kBRowsBytes)));
+    if (TURNED) return *(const i32x4*)(smem + ta[i] + (s & 3) * (2 * kBRowsBytes));
+    return read_tr(smem + ta[i] + (FUSED ? kBWOff + (s & 1) * kBRowsBytes : (s & 3) * (2 * kBRowsBytes)));
   };
   auto read_q = [&](int s, int j) {
-    if (DX) return *(const i32x4*)(smem + tq[j] + (s & 3) * kBRowsBytes);
+    if (!DW) return *(const i32x4*)(smem + tq[j] + (s & 3) * (FUSED ? kBRowsBytes : 2 * kBRowsBytes));
     return read_tr(smem + tq[j] + (s & 3) * (2 * kBRowsBytes));
   };
   auto mfma = [](const i32x4& x, const i32x4& y, const f32x4& c) {
-    if (DX) return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
+    if (!DW) return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
   };
 
@@ -369,7 +412,7 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
       copy_p(clamp_st(st0 + s), s);
       copy_d(clamp_st(st0 + s), s);
     }
-    if (DX) {
+    if (FUSED) {
       asm volatile("s_waitcnt vmcnt(18)" ::: "memory");   // step 0, and step 1's codes and scales
 #pragma unroll
       for (int u = 0; u < 3; ++u) {   // all of step 0, half of step 1
@@ -395,8 +438,8 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       if (h == 2) {
-        // under way may be the copies of steps s + 2 (DX: four of them) and s + 3
-        if (DX)
+        // under way may be the copies of steps s + 2 (kDx: four of them) and s + 3
+        if (FUSED)
           asm volatile("s_waitcnt vmcnt(11)" ::: "memory");
         else
           asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
@@ -416,7 +459,7 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
         if (h == 3 && x % 4 == 0 && x > 0) pf[x / 4 - 1] = read_p(s + 1, x / 4 - 1);
         if (h == 2 && x == 8) copy_p(ahead, s & 3);
         if (h == 3 && x == 7) copy_d(ahead, s & 3);
-        if (DX) {   // a unit of ten pieces in two quarters
+        if (FUSED) {   // a unit of ten pieces in two quarters
           const int d = h >= 2 ? s + 2 : s + 1;
           if ((h == 0 || h == 2) && x == 1) {
             sc = read_scale(d & 3);
@@ -438,7 +481,7 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   // lane: k = c0 + 128 wk + 16 i + 4 g + (0 .. 3), row r0 + 128 wr + 16 j + r
-  if (DX) {
+  if (!DW) {
     const float cf = a.cols[(128 * wk < c_room ? c0 + 128 * wk : c0) / 128];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -471,7 +514,7 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
   if (128 * wk >= c_room) return;
   // the wave's 128 rows lie in one of the two outputs (n is a multiple of 128)
   const int64_t row0 = r0 + 128 * wr;
-  const int second = !DX && row0 >= a.n;
+  const int second = DW && row0 >= a.n;
   uint16_t* base = (second ? a.out[1] : a.out[0]) + (second ? row0 - a.n : row0) * a.k + c0 + 128 * wk + (lane & 15) * 8;
 #pragma unroll
   for (int q = 0; q < 32; ++q) {
@@ -519,23 +562,26 @@ ProductPlan plan_product(int64_t rows, int64_t z, int64_t k) {
   return p;
 }
 
-template <bool DX>
+template <Kind KIND>
 hipError_t launch_product(GatedProduct a, const ProductPlan& p, hipStream_t s) {
   a.tiles_r = p.tiles_r;
   a.tiles_c = p.tiles_c;
   a.full = p.full;
   a.split = p.split;
   const int64_t tail = p.tiles_r * p.tiles_c - p.full;
-  hipError_t e = hipFuncSetAttribute((const void*)gated_product_kernel<DX>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kBLds);
+  hipError_t e = hipFuncSetAttribute((const void*)gated_product_kernel<KIND>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kBLds);
   if (e != hipSuccess) return e;
-  gated_product_kernel<DX><<<(unsigned)(p.full + tail * p.split), kBThreads, kBLds, s>>>(a);
+  gated_product_kernel<KIND><<<(unsigned)(p.full + tail * p.split), kBThreads, kBLds, s>>>(a);
   if (p.split > 1) gated_join_kernel<<<(unsigned)(tail * 64), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
 constexpr size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// last rows of x | cols | scale table | row factors | D16 | Db | parts (both products', one after the other)
+// From so many tokens on dx reads the weights turned to f16 beforehand.
+bool turned(int64_t m) { return m >= 2048; }
+
+// last rows of x | cols | scale table | row factors | D16 | Db | turned weights | parts (both products', one after the other)
 struct BwdWs {
   uint16_t* xt;
   float* cols;
@@ -543,6 +589,7 @@ struct BwdWs {
   float* rs;
   uint16_t* d16;
   uint16_t* db;
+  uint16_t* w16;
   float* part;
   size_t bytes;
 };
@@ -562,6 +609,7 @@ BwdWs bwd_ws(void* ws, int64_t m, int64_t n, int64_t k) {
   w.rs = (float*)take((size_t)m * 4);
   w.d16 = (uint16_t*)take((size_t)m * 2 * n * 2);
   w.db = (uint16_t*)take((size_t)pad_tokens(m) * 2 * n * 2);
+  w.w16 = (uint16_t*)take(turned(m) ? (size_t)k * 2 * n * 2 : 0);
   const size_t a = plan_product(m, 2 * n, k).part_bytes(), b = plan_product(2 * n, m, k).part_bytes();
   w.part = (float*)take(a > b ? a : b);
   w.bytes = at;
@@ -617,7 +665,14 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
     p.rows = a.m;
     p.z = 2 * a.n;
     p.out[0] = p.out[1] = a.dx;
-    e = launch_product<true>(p, plan_product(a.m, 2 * a.n, a.k), s);
+    const ProductPlan plan = plan_product(a.m, 2 * a.n, a.k);
+    if (turned(a.m)) {
+      gated_weights_kernel<<<dim3((unsigned)(a.k / 128), (unsigned)(2 * a.n / 128)), 256, 0, s>>>(a.wg, a.wu, w.tab, a.n, a.k, w.w16);
+      p.p = w.w16;
+      e = launch_product<kDxT>(p, plan, s);
+    } else {
+      e = launch_product<kDx>(p, plan, s);
+    }
     if (e != hipSuccess) return e;
   }
   if (a.dgate) {
@@ -628,7 +683,7 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
     p.z = a.m;
     p.out[0] = a.dgate;
     p.out[1] = a.dup;
-    e = launch_product<false>(p, plan_product(2 * a.n, a.m, a.k), s);
+    e = launch_product<kDw>(p, plan_product(2 * a.n, a.m, a.k), s);
   }
   return e;
 }
