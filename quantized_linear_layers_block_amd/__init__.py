@@ -403,56 +403,68 @@ _U8, _F32 = torch.uint8, torch.float32
 
 
 def _check_matrix(device, name, t, shape):
-    # dense rows; rows may be apart
+    # the row stride of a matrix of dense rows, which may be apart
     if t.shape != shape or t.dtype is not _BF16 or t.device != device:
         _refuse(device, _BF16, name, t, f"of the shape {tuple(shape)}")
-    if not t.is_contiguous() and shape[1] > 1 and t.stride(1) != 1:
+    if t.is_contiguous():
+        return shape[1]
+    if shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have dense rows")
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
-def _norm_inputs(x, weight, residual, h):
-    # checks what both forms of the norm share: (device, h to write or None)
-    dev = _dev(x).device
-    if x.dim() != 2:
-        raise ValueError("x must be [tokens, k]")
+def _norm_device(name, t):
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [tokens, k]")
+    return dev
+
+
+def _norm(x, weight, eps, residual, h, y, fmt, pow2):
+    # both forms of the norm: (y or None, yq, sy, h)
+    dev = _norm_device("x", x)
     shape = x.shape
-    _check_matrix(dev, "x", x, shape)
-    _check_dense(dev, _BF16, "weight", weight, shape[1:])
+    k = shape[1]
+    xs = _check_matrix(dev, "x", x, shape)
+    if weight.shape != (k,) or weight.dtype is not _BF16 or weight.device != dev or not weight.is_contiguous():
+        _check_dense(dev, _BF16, "weight", weight, (k,))
+    rs = hs = 0
     if residual is not None:
-        _check_matrix(dev, "residual", residual, shape)
+        rs = _check_matrix(dev, "residual", residual, shape)
         if h is None:
-            h = torch.empty(shape, dtype=_BF16, device=dev)
-    if h is not None:
-        _check_matrix(dev, "h", h, shape)
-    return dev, h
+            h, hs = torch.empty_like(x) if xs == k else torch.empty(shape, dtype=_BF16, device=dev), k
+    if h is not None and not hs:
+        hs = _check_matrix(dev, "h", h, shape)
+    yq = sy = None
+    if fmt:
+        if y is not None:
+            _check_dense(dev, _BF16, "y", y, shape)
+        yq = torch.empty(shape, dtype=_U8, device=dev)
+        sy = torch.empty((shape[0], k // 128), dtype=_U8 if pow2 else _F32, device=dev)
+    elif y is not None:
+        _check_dense(dev, _BF16, "out", y, shape)
+    else:
+        y = torch.empty_like(x) if xs == k else torch.empty(shape, dtype=_BF16, device=dev)
+    _call_on(dev, binding.qlinear_rms_norm, x, xs, weight, eps, residual, rs, h, hs, y, fmt, yq, sy)
+    return y, yq, sy, h
 
 
 def rms_norm(x, weight, eps=1e-6, residual=None, h=None, out=None):
     """y = h / sqrt(mean(h^2) + eps) * weight of bf16 rows [T, k], h = bf16(x + residual): y, or
     (y, h) with a residual.  h (given, it is written also without one) may be x or residual itself;
     y is written into out if given."""
-    dev, hs = _norm_inputs(x, weight, residual, h)
-    if out is None:
-        out = torch.empty(x.shape, dtype=_BF16, device=dev)
-    else:
-        _check_dense(dev, _BF16, "out", out, x.shape)
-    _call_on(dev, binding.qlinear_rms_norm, x, weight, eps, residual, hs, out)
-    return out if residual is None else (out, hs)
+    y, _, _, h = _norm(x, weight, eps, residual, h, out, 0, False)
+    return y if residual is None else (y, h)
 
 
 def rms_norm_fp8(x, weight, eps=1e-6, residual=None, pow2=False, h=None, y=None):
     """rms_norm with an output in 8 bits for the FP8 layers: (yq, sy), or (yq, sy, h) with a
     residual; yq uint8 [T, k] E4M3 codes, sy float32 [T, k / 128] (pow2: uint8 E8M0 bytes).  y
     (bf16 [T, k]), if given, is written too, for an adapter or a weight gradient."""
-    dev, hs = _norm_inputs(x, weight, residual, h)
-    m, k = x.shape
-    if y is not None:
-        _check_dense(dev, _BF16, "y", y, x.shape)
-    yq = torch.empty((m, k), dtype=_U8, device=dev)
-    sy = torch.empty((m, k // 128), dtype=_U8 if pow2 else _F32, device=dev)
-    _call_on(dev, binding.qlinear_rms_norm, x, weight, eps, residual, hs, y, QL_FP8_POW2 if pow2 else QL_FP8_BLOCK128,
-             yq, sy)
-    return (yq, sy) if residual is None else (yq, sy, hs)
+    _, yq, sy, h = _norm(x, weight, eps, residual, h, y, QL_FP8_POW2 if pow2 else QL_FP8_BLOCK128, pow2)
+    return (yq, sy) if residual is None else (yq, sy, h)
 
 
 def rms_norm_backward(dy, h, weight, eps=1e-6, dh=None, dx=None, need_dweight=True, ws=None):
@@ -460,20 +472,17 @@ def rms_norm_backward(dy, h, weight, eps=1e-6, dh=None, dx=None, need_dweight=Tr
     normalised, dh the gradient that reaches h beside the norm (added to dx).  dx (bf16; dy or dh
     itself if wanted) is the gradient of x and of the residual; dweight is float32 [k], None
     without need_dweight.  ws: scratch kept from step to step."""
-    dev = _dev(dy).device
-    if dy.dim() != 2:
-        raise ValueError("dy must be [tokens, k]")
+    dev = _norm_device("dy", dy)
     shape = dy.shape
     m, k = shape
-    _check_matrix(dev, "dy", dy, shape)
-    _check_matrix(dev, "h", h, shape)
-    _check_dense(dev, _BF16, "weight", weight, shape[1:])
-    if dh is not None:
-        _check_matrix(dev, "dh", dh, shape)
+    ds = _check_matrix(dev, "dy", dy, shape)
+    hs = _check_matrix(dev, "h", h, shape)
+    _check_dense(dev, _BF16, "weight", weight, (k,))
+    dhs = 0 if dh is None else _check_matrix(dev, "dh", dh, shape)
     if dx is None:
-        dx = torch.empty(shape, dtype=_BF16, device=dev)
+        dx, dxs = torch.empty_like(dy) if ds == k else torch.empty(shape, dtype=_BF16, device=dev), k
     else:
-        _check_matrix(dev, "dx", dx, shape)
+        dxs = _check_matrix(dev, "dx", dx, shape)
     dweight = None
     if need_dweight:
         dweight = torch.empty((k,), dtype=_F32, device=dev)
@@ -481,7 +490,8 @@ def rms_norm_backward(dy, h, weight, eps=1e-6, dh=None, dx=None, need_dweight=Tr
             ws = torch.empty((max(1, binding.qlinear_rms_norm_backward_workspace(m, k)),), dtype=_U8, device=dev)
         elif ws.device != dev or not ws.is_contiguous():
             _refuse(dev, ws.dtype, "ws", ws, "contiguous")
-    _call_on(dev, binding.qlinear_rms_norm_backward, dy, h, weight, eps, dx, dh, dweight, ws if need_dweight else None)
+    _call_on(dev, binding.qlinear_rms_norm_backward, dy, ds, h, hs, weight, eps, dx, dxs, dh, dhs, dweight,
+             ws if need_dweight else None)
     return dx, dweight
 
 
@@ -491,51 +501,55 @@ def _gated_weights(gate, up):
     # the device of a block's weights
     if not isinstance(gate, FP8Weight) or not isinstance(up, FP8Weight):
         raise TypeError("the gated block takes FP8 weights")
-    if gate.n != up.n or gate.k != up.k or gate.pow2 != up.pow2:
+    n, k, pow2 = gate.n, gate.k, gate.pow2
+    if n != up.n or k != up.k or pow2 != up.pow2:
         raise ValueError("gate and up must be alike in sizes and scales")
-    dev = _dev(gate.codes).device
+    dev = gate.codes.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
+    codes, scales, kind = (n, k), (n // 128, k // 128), _U8 if pow2 else _F32
     for w in (gate, up):
-        _check_dense(dev, _U8, "codes", w.codes, (w.n, w.k))
-        _check_dense(dev, _U8 if w.pow2 else _F32, "scales", w.scales, (w.n // 128, w.k // 128))
+        _check_dense(dev, _U8, "codes", w.codes, codes)
+        _check_dense(dev, kind, "scales", w.scales, scales)
     return dev
 
 
-def _gated_call(gate, up, xq, sx, h, hq, sh, gu, ws):
+def _gated_call(gate, up, xq, sx, h, gu, ws, quant):
+    # both forms of the forward: (h, hq, sh)
     dev = _gated_weights(gate, up)
     if xq.dim() != 2:
         raise ValueError("xq must be [tokens, k]")
-    m = xq.shape[0]
-    _check_dense(dev, _U8, "xq", xq, (m, gate.k))
-    _check_dense(dev, gate.scales.dtype, "sx", sx, (m, gate.k // 128))
+    m, n, k = xq.shape[0], gate.n, gate.k
+    _check_dense(dev, _U8, "xq", xq, (m, k))
+    _check_dense(dev, gate.scales.dtype, "sx", sx, (m, k // 128))
     if h is not None:
-        _check_dense(dev, _BF16, "h", h, (m, gate.n))
+        _check_dense(dev, _BF16, "h", h, (m, n))
     if gu is not None:
-        _check_dense(dev, _BF16, "gu", gu, (m, 2 * gate.n))
+        _check_dense(dev, _BF16, "gu", gu, (m, 2 * n))
     if ws is None:
-        ws = _ws(binding.qlinear_gated_forward_workspace(m, gate.n, gate.k), dev)
+        ws = _ws(binding.qlinear_gated_forward_workspace(m, n, k), dev)
     elif ws.device != dev or not ws.is_contiguous():
         _refuse(dev, ws.dtype, "ws", ws, "contiguous")
+    hq = sh = None
+    if quant:
+        hq, sh = xq.new_empty((m, n)), sx.new_empty((m, n // 128))
+    elif h is None:
+        h = torch.empty((m, n), dtype=_BF16, device=dev)
     _call_on(dev, binding.qlinear_gated_forward, gate.qweight(), up.qweight(), xq, sx, ws, h, hq, sh, gu)
+    return h, hq, sh
 
 
 def gated_forward(gate, up, xq, sx, h=None, gu=None, ws=None):
     """h = silu(x Wg^T) * (x Wu^T), bf16 [T, n], from FP8 weights and activations quantized like them
     (rms_norm_fp8, quantize_act_fp8).  gu (bf16 [T, 2n]), if given, gets both products, for
     gated_backward.  ws: a zero-filled workspace kept from call to call, as forward's."""
-    if h is None:
-        h = torch.empty((xq.shape[0], gate.n), dtype=_BF16, device=xq.device)
-    _gated_call(gate, up, xq, sx, h, None, None, gu, ws)
-    return h
+    return _gated_call(gate, up, xq, sx, h, gu, ws, False)[0]
 
 
 def gated_forward_fp8(gate, up, xq, sx, h=None, gu=None, ws=None):
     """gated_forward with an output in 8 bits for the down projection's forward_fp8_prequant:
     (hq uint8 [T, n], sh [T, n / 128]); h (bf16 [T, n]), if given, is written too."""
-    m = xq.shape[0]
-    hq = torch.empty((m, gate.n), dtype=_U8, device=xq.device)
-    sh = torch.empty((m, gate.n // 128), dtype=_U8 if gate.pow2 else _F32, device=xq.device)
-    _gated_call(gate, up, xq, sx, h, hq, sh, gu, ws)
-    return hq, sh
+    return _gated_call(gate, up, xq, sx, h, gu, ws, True)[1:]
 
 
 def gated_backward(gate, up, dh, gu, x=None, need_dx=True, need_dweight=True, ws=None):

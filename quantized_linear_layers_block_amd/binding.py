@@ -410,17 +410,17 @@ def qlinear_attention_nvfp4(cache, q, page_table, kv_lens, out, ws, q_starts=Non
 
 
 # ------------------------------------------------------------------------ norm
+# Steps of every layer, too: the row strides come from the caller, which has them from its checks.
 
-def _rows(t):
-    # data pointer and row stride; the stride of a single row is left open by PyTorch
-    return (None, 0) if t is None else (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1])
-
-
-def qlinear_rms_norm(x, weight, eps, residual=None, h=None, y=None, fmt=0, yq=None, sy=None, stream=None):
-    """x, residual, h bf16 [m, k] (dense rows, any row stride); y bf16 [m, k] and/or yq u8 [m, k] with sy."""
+def qlinear_rms_norm(x, x_stride, weight, eps, residual=None, residual_stride=0, h=None, h_stride=0, y=None, fmt=0,
+                     yq=None, sy=None, stream=None):
+    """x, residual, h bf16 [m, k] (dense rows, strides in elements); y bf16 [m, k] and/or yq u8 [m, k] with sy."""
     m, k = x.shape
-    st = LIB.qlinear_rms_norm(*_rows(x), *_rows(residual), weight.data_ptr(), eps, m, k, *_rows(h), _ptr(y), fmt,
-                              _ptr(yq), _ptr(sy), _stream_here() if stream is None else stream)
+    st = LIB.qlinear_rms_norm(x.data_ptr(), x_stride, None if residual is None else residual.data_ptr(),
+                              residual_stride, weight.data_ptr(), eps, m, k, None if h is None else h.data_ptr(),
+                              h_stride, None if y is None else y.data_ptr(), fmt,
+                              None if yq is None else yq.data_ptr(), None if sy is None else sy.data_ptr(),
+                              _stream_here() if stream is None else stream)
     if st:
         raise QlinearError(st, "qlinear_rms_norm")
 
@@ -429,11 +429,14 @@ def qlinear_rms_norm_backward_workspace(m, k):
     return LIB.qlinear_rms_norm_backward_workspace(m, k)
 
 
-def qlinear_rms_norm_backward(dy, h, weight, eps, dx, dh=None, dweight=None, ws=None, stream=None):
-    """dy, h, dh, dx bf16 [m, k] (dense rows, any row stride); dweight f32 [k] or None."""
+def qlinear_rms_norm_backward(dy, dy_stride, h, h_stride, weight, eps, dx, dx_stride, dh=None, dh_stride=0,
+                              dweight=None, ws=None, stream=None):
+    """dy, h, dh, dx bf16 [m, k] (dense rows, strides in elements); dweight f32 [k] or None."""
     m, k = dy.shape
-    st = LIB.qlinear_rms_norm_backward(*_rows(dy), *_rows(h), weight.data_ptr(), eps, *_rows(dh), m, k, *_rows(dx),
-                                       _ptr(dweight), _ptr(ws), 0 if ws is None else ws.nbytes,
+    st = LIB.qlinear_rms_norm_backward(dy.data_ptr(), dy_stride, h.data_ptr(), h_stride, weight.data_ptr(), eps,
+                                       None if dh is None else dh.data_ptr(), dh_stride, m, k, dx.data_ptr(),
+                                       dx_stride, None if dweight is None else dweight.data_ptr(),
+                                       None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
                                        _stream_here() if stream is None else stream)
     if st:
         raise QlinearError(st, "qlinear_rms_norm_backward")

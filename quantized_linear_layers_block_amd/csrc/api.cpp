@@ -709,7 +709,7 @@ static bool gated_sizes_ok(int64_t m, int64_t n, int64_t k) {
 
 size_t qlinear_gated_forward_workspace(int64_t m, int64_t n, int64_t k) {
   if (!gated_sizes_ok(m, n, k) || !ql::gated_launchable(m, n, k)) return 0;
-  return ql::kWsReserved + ql::gated_scratch_bytes(m, n);
+  return ql::kWsReserved + ql::gated_scratch_bytes(m, n, k);
 }
 
 qlinear_status qlinear_gated_forward(const qlinear_qweight* gate, const qlinear_qweight* up, const uint8_t* xq,
@@ -721,7 +721,7 @@ qlinear_status qlinear_gated_forward(const qlinear_qweight* gate, const qlinear_
   if (!gated_sizes_ok(m, gate->n, gate->k) || !ql::gated_launchable(m, gate->n, gate->k)) return QL_ERR_SHAPE;
   if (!aligned16(xq) || !aligned16(sx) || !aligned16(h) || !aligned16(hq) || (hq && !aligned16(sh)) || !aligned16(gu))
     return QL_ERR_ALIGN;
-  if (!ws || ws_bytes < ql::kWsReserved + ql::gated_scratch_bytes(m, gate->n)) return QL_ERR_WORKSPACE;
+  if (!ws || ws_bytes < ql::kWsReserved + ql::gated_scratch_bytes(m, gate->n, gate->k)) return QL_ERR_WORKSPACE;
   if (!aligned16(ws)) return QL_ERR_ALIGN;
   ql::Gated a;
   a.xq = xq;

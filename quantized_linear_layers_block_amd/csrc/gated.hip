@@ -50,9 +50,20 @@ __device__ __forceinline__ i32x8 gated_frag(const uint8_t* tile, int row, int g)
 // by 16 MJ tokens (16 j + r); the wave stands at column 64 wn and token mw of the tile.  Everything
 // leaves through LDS as whole rows.  `amax`: LDS for [2][TM] words.
 template <int THREADS, int TM, int MJ>
-__device__ __forceinline__ void gated_store(const Gated& a, f32x4 (&acc)[8][MJ], int64_t m0, int64_t n0, int wn, int mw,
-                                            int r, int lg, uint8_t* stage, uint32_t* amax) {
+__device__ __forceinline__ void gated_store(const Gated& a, f32x4 (&acc)[8][MJ], int split, int64_t m0, int64_t n0, int wn,
+                                            int mw, int r, int lg, uint8_t* stage, uint32_t* amax) {
   const int tid = threadIdx.x;
+  if (a.split > 1) {   // a part of K: float32 [split][m][2 n], for gated_join_kernel
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) {
+      const int64_t row = m0 + mw + 16 * j + r;
+      if (row >= a.m) continue;
+      float* p = a.scratch + ((int64_t)split * a.m + row) * 2 * a.n + n0 + 64 * wn + 4 * lg;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) *(f32x4*)(p + (i < 4 ? 16 * i : a.n + 16 * (i - 4))) = acc[i][j];
+    }
+    return;
+  }
   auto rows_out = [&](uint16_t* dst, int64_t stride, int from) {   // bf16(acc[from..from + 3]) -> dst [m][stride]
     __syncthreads();
 #pragma unroll
@@ -127,11 +138,23 @@ __device__ __forceinline__ void gated_store(const Gated& a, f32x4 (&acc)[8][MJ],
   }
 }
 
-// The workgroup's tile, in scalar registers (the copies' base addresses have to be there).
-__device__ __forceinline__ void gated_tile(const Gated& a, int64_t& tm, int64_t& tn) {
-  gemm_tile_coords(a.tiles_m, a.tiles_n, tm, tn);
-  tm = __builtin_amdgcn_readfirstlane((int)tm);
-  tn = __builtin_amdgcn_readfirstlane((int)tn);
+// The workgroup's tile and K blocks, in scalar registers (the copies' base addresses have to be there).
+struct GatedWork {
+  int64_t tm, tn, kb0, kb1;
+  int split;
+};
+__device__ __forceinline__ GatedWork gated_work(const Gated& a) {
+  GatedWork w;
+  int64_t tm, tn;
+  const int64_t b = a.split > 1 ? blockIdx.x / a.split : gemm_xcd_remap(blockIdx.x, gridDim.x);
+  gemm_group_tile(b, a.tiles_m, a.tiles_n, tm, tn);
+  w.tm = __builtin_amdgcn_readfirstlane((int)tm);
+  w.tn = __builtin_amdgcn_readfirstlane((int)tn);
+  w.split = __builtin_amdgcn_readfirstlane(a.split > 1 ? (int)(blockIdx.x % a.split) : 0);
+  const int64_t kblocks = a.k / 128;
+  w.kb0 = w.split * a.blocks_each;
+  w.kb1 = w.kb0 + a.blocks_each < kblocks ? w.kb0 + a.blocks_each : kblocks;
+  return w;
 }
 
 // Eight E4M3 codes -> eight f16, exactly (the converter's scale is 1).
@@ -167,9 +190,8 @@ __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
   extern __shared__ __align__(16) uint8_t smem[];  // [2][W 256 x 128 | x TM x 128], scale ring
   constexpr int TM = 64 * MJ;
   constexpr int kStage = (kGRows + TM) * kGRowBytes;
-  int64_t tm, tn;
-  gated_tile(a, tm, tn);
-  const int64_t n0 = tn * kGCols, m0 = tm * TM;
+  const GatedWork work = gated_work(a);
+  const int64_t tn = work.tn, n0 = tn * kGCols, m0 = work.tm * TM;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
   const int wn = wave & 1, wm = wave >> 1;
@@ -245,11 +267,11 @@ __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
 #pragma unroll
     for (int j = 0; j < MJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-  for (int q = 0; q < 4 + MJ; ++q) dma(0, 0, q);
-  if (SW4) dma_sc(0);
+  for (int q = 0; q < 4 + MJ; ++q) dma(work.kb0, 0, q);
+  if (SW4) dma_sc(work.kb0 >> 2);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  next_sc(0);
+  next_sc(work.kb0);
 
   // Software pipeline, fragment by fragment (8 fragments of 16 weight rows against MJ of 16 tokens).
   // Each MFMA stands with one of the FMAs that fold the fragment before and with conversions of the
@@ -271,9 +293,9 @@ __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
   }
   wr = gated_frag(smem, 128 * wn + r, g);
   wf[0] = e4m3_f16x8(wr[0], wr[1]);
-  for (int64_t kb = 0; kb < kblocks; ++kb) {
-    const int buf = (int)(kb & 1);
-    const int64_t kn = kb + 1 < kblocks ? kb + 1 : kb;  // the last block copies itself into the idle buffer again
+  for (int64_t kb = work.kb0; kb < work.kb1; ++kb) {
+    const int buf = (int)((kb - work.kb0) & 1);
+    const int64_t kn = kb + 1 < work.kb1 ? kb + 1 : kb;  // the last block copies itself into the idle buffer again
 #pragma unroll
     for (int j = 0; j < MJ; ++j) {
       scl[j] = scu[j];
@@ -281,7 +303,7 @@ __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
       scu[j] = sxn[j] * sun;
     }
     // kn's group landed at least a block's barrier ago: a group's copy goes out two blocks before its first
-    if (SW4 && ((kb + 2) & 3) == 0 && kb + 2 < kblocks) dma_sc((kb + 2) >> 2);
+    if (SW4 && ((kb + 2) & 3) == 0 && kb + 2 < work.kb1) dma_sc((kb + 2) >> 2);
     next_sc(kn);
     const uint8_t* As = smem + buf * kStage;
     const uint8_t* An = smem + (buf ^ 1) * kStage;
@@ -320,7 +342,7 @@ __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
   }
 #pragma unroll
   for (int j = 0; j < MJ; ++j) acc[7][j] += scu[j] * p[1][j];
-  gated_store<kGfThreads, TM, MJ>(a, acc, m0, n0, wn, 16 * MJ * wm, r, g, smem, (uint32_t*)(smem + TM * kGPitch));
+  gated_store<kGfThreads, TM, MJ>(a, acc, work.split, m0, n0, wn, 16 * MJ * wm, r, g, smem, (uint32_t*)(smem + TM * kGPitch));
 }
 
 // ------------------------------------------------------------------ powers of two, many tokens
@@ -340,9 +362,8 @@ __global__ __launch_bounds__(kGpThreads) void gated_pow2_kernel(Gated a) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int MJ = TM / 32;
   constexpr int kStage = (kGRows + TM) * kGRowBytes;
-  int64_t tm, tn;
-  gated_tile(a, tm, tn);
-  const int64_t n0 = tn * kGCols, m0 = tm * TM;
+  const GatedWork work = gated_work(a);
+  const int64_t tn = work.tn, n0 = tn * kGCols, m0 = work.tm * TM;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
   const int wn = wave & 1, wm = wave >> 1;
@@ -414,11 +435,11 @@ __global__ __launch_bounds__(kGpThreads) void gated_pow2_kernel(Gated a) {
 #pragma unroll
     for (int j = 0; j < MJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-  for (int q = 0; q < 8 + MJ; ++q) dma(0, 0, q);
-  if (SW4) dma_sc(0);
+  for (int q = 0; q < 8 + MJ; ++q) dma(work.kb0, 0, q);
+  if (SW4) dma_sc(work.kb0 >> 2);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  next_sc(0);
+  next_sc(work.kb0);
   int sg = sgn, su = sun, sb[MJ];
 #pragma unroll
   for (int j = 0; j < MJ; ++j) sb[j] = sbn[j];
@@ -426,10 +447,10 @@ __global__ __launch_bounds__(kGpThreads) void gated_pow2_kernel(Gated a) {
 #pragma unroll
   for (int j = 0; j < MJ; ++j) bf[j] = gated_frag(smem + kGRows * kGRowBytes, 16 * MJ * wm + 16 * j + r, g);
   af = gated_frag(smem, 128 * wn + r, g);
-  for (int64_t kb = 0; kb < kblocks; ++kb) {
-    const int buf = (int)(kb & 1);
-    const int64_t kn = kb + 1 < kblocks ? kb + 1 : kb;
-    if (SW4 && ((kb + 2) & 3) == 0 && kb + 2 < kblocks) dma_sc((kb + 2) >> 2);
+  for (int64_t kb = work.kb0; kb < work.kb1; ++kb) {
+    const int buf = (int)((kb - work.kb0) & 1);
+    const int64_t kn = kb + 1 < work.kb1 ? kb + 1 : kb;
+    if (SW4 && ((kb + 2) & 3) == 0 && kb + 2 < work.kb1) dma_sc((kb + 2) >> 2);
     next_sc(kn);
     const uint8_t* As = smem + buf * kStage;
     const uint8_t* An = smem + (buf ^ 1) * kStage;
@@ -445,8 +466,9 @@ __global__ __launch_bounds__(kGpThreads) void gated_pow2_kernel(Gated a) {
         if (j == 0) afn = i < 7 ? gated_frag(As, 128 * wn + 16 * (i + 1) + r, g) : gated_frag(An, 128 * wn + r, g);
         if (MJ == 8) {
           if (i < 4 && (j & 1)) dma(kn, buf ^ 1, 4 * i + (j >> 1));
-        } else if (i < 6 && (j & 1)) {
-          dma(kn, buf ^ 1, 2 * i + (j >> 1));
+        } else if (j == MJ - 1 && 2 * i < 8 + MJ) {
+          dma(kn, buf ^ 1, 2 * i);
+          dma(kn, buf ^ 1, 2 * i + 1);
         }
         if (i == 7) bf[j] = gated_frag(An + kGRows * kGRowBytes, 16 * MJ * wm + 16 * j + r, g);
         __builtin_amdgcn_sched_barrier(0);
@@ -458,7 +480,7 @@ __global__ __launch_bounds__(kGpThreads) void gated_pow2_kernel(Gated a) {
 #pragma unroll
     for (int j = 0; j < MJ; ++j) sb[j] = sbn[j];
   }
-  gated_store<kGpThreads, TM, MJ>(a, acc, m0, n0, wn, 16 * MJ * wm, r, g, smem, (uint32_t*)(smem + TM * kGPitch));
+  gated_store<kGpThreads, TM, MJ>(a, acc, work.split, m0, n0, wn, 16 * MJ * wm, r, g, smem, (uint32_t*)(smem + TM * kGPitch));
 }
 
 // ------------------------------------------------------------------ up to 64 tokens
@@ -632,6 +654,47 @@ __global__ __launch_bounds__(kFewThreads) void gated_few_kernel(Gated a) {
   }
 }
 
+// The parts of K added in their order, and what the tiles' epilogue does: 32 lanes a segment of 128 columns.
+__global__ __launch_bounds__(256) void gated_join_kernel(Gated a) {
+  const int64_t nb = a.n / 128;
+  const int64_t seg = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (seg >= a.m * nb) return;
+  const int64_t row = seg / nb, col = (seg % nb) * 128 + 4 * (threadIdx.x & 31);
+  const float* p = a.scratch + row * 2 * a.n + col;
+  const int64_t each = a.m * 2 * a.n;
+  f32x4 g = *(const f32x4*)p, u = *(const f32x4*)(p + a.n);
+  for (int s = 1; s < a.split; ++s) {
+    g += *(const f32x4*)(p + s * each);
+    u += *(const f32x4*)(p + s * each + a.n);
+  }
+  float h[4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    h[e] = gate_product(g[e], u[e]);
+    top = umax(top, abs_bits(h[e]));
+  }
+  auto out = [](uint16_t* q, float a0, float a1, float a2, float a3) {
+    *(uint2*)q = make_uint2(pack_bf16x2_rne(a0, a1), pack_bf16x2_rne(a2, a3));
+  };
+  if (a.gu) {
+    out(a.gu + row * 2 * a.n + col, g[0], g[1], g[2], g[3]);
+    out(a.gu + row * 2 * a.n + a.n + col, u[0], u[1], u[2], u[3]);
+  }
+  if (a.h) out(a.h + row * a.n + col, h[0], h[1], h[2], h[3]);
+  if (!a.hq) return;
+  top = max_row16(top);
+  top = umax(top, (uint32_t)__shfl_xor((int)top, 16));
+  const Fp8Seg sc = a.pow2 ? fp8_seg_scale<true>(top) : fp8_seg_scale<false>(top);
+  *(uint32_t*)(a.hq + row * a.n + col) = fp8_encode4(h, sc);
+  if ((threadIdx.x & 31) == 0) {
+    if (a.pow2)
+      ((uint8_t*)a.sh)[seg] = (uint8_t)sc.stored;
+    else
+      ((uint32_t*)a.sh)[seg] = sc.stored;
+  }
+}
+
 constexpr int64_t kFewM = 64;
 
 template <int MT, int RT>
@@ -644,26 +707,60 @@ hipError_t launch_few(const Gated& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// How more than 64 tokens are cut.  Tiles that cannot fill the chip are taken small, and if K is long, cut along
+// it: a tile's time then is that of its copies' latency, block by block.  Otherwise the height with the least
+// time for all rounds of the chip, a tile's time being its tokens and a share for the weights, which every
+// height reads and converts alike.
+constexpr int64_t kGCUs = 256;
+constexpr int64_t kGWeightShare = 64;
+struct GatedPlan {
+  int tm;
+  int split;
+  int64_t blocks_each;
+};
+GatedPlan plan_gated(int64_t m, int64_t n, int64_t k, bool pow2) {
+  const int64_t nb = n / 128, kb = k / 128;
+  const int64_t small = (m + 63) / 64 * nb;
+  int64_t sp = small <= kGCUs / 2 ? kGCUs / small : 1;
+  if (sp > kb / 4) sp = kb / 4;
+  if (sp > 1) {
+    const int64_t each = ((kb + sp - 1) / sp + 3) / 4 * 4;   // whole units of four blocks' scales
+    return {64, (int)((kb + each - 1) / each), each};
+  }
+  const int high = pow2 ? 256 : 192;
+  int best = 64;
+  int64_t least = INT64_MAX;
+  for (int tm : {64, 128, high}) {
+    const int64_t t = (((m + tm - 1) / tm * nb + kGCUs - 1) / kGCUs) * (tm + kGWeightShare);
+    if (t < least) {
+      least = t;
+      best = tm;
+    }
+  }
+  return {best, 1, kb};
+}
+
 // TM tokens a tile; `four`: the scales of four K blocks lie in one aligned unit.
 template <int TM>
 hipError_t launch_tiles(Gated a, hipStream_t s) {
   a.tiles_m = (a.m + TM - 1) / TM;
   a.tiles_n = a.n / kGCols;
-  const unsigned grid = (unsigned)(a.tiles_m * a.tiles_n);
+  const unsigned grid = (unsigned)(a.tiles_m * a.tiles_n * a.split);
   const uintptr_t all = (uintptr_t)a.sx | (uintptr_t)a.sg | (uintptr_t)a.su;
   const bool four = (a.k / 128) % 4 == 0 && (all & (a.pow2 ? 3 : 15)) == 0;
   auto go = [&](auto kernel, int threads, size_t lds) {
     hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
     kernel<<<grid, threads, lds, s>>>(a);
+    if (a.split > 1) gated_join_kernel<<<(unsigned)((a.m * (a.n / 128) + 7) / 8), 256, 0, s>>>(a);
     return hipGetLastError();
   };
-  if constexpr (TM % 64 == 0 && TM <= 192) {
+  if constexpr (TM <= 192) {
     if (!a.pow2)
       return four ? go(gated_f32s_kernel<TM / 64, true>, kGfThreads, gf_lds<TM / 64>())
                   : go(gated_f32s_kernel<TM / 64, false>, kGfThreads, gf_lds<TM / 64>());
   }
-  if constexpr (TM % 128 == 0)
+  if constexpr (TM != 192)
     return four ? go(gated_pow2_kernel<TM, true>, kGpThreads, gp_lds<TM>())
                 : go(gated_pow2_kernel<TM, false>, kGpThreads, gp_lds<TM>());
   return hipErrorInvalidValue;
@@ -675,18 +772,27 @@ bool gated_launchable(int64_t m, int64_t n, int64_t k) {
   if (m <= 0 || n <= 0 || k <= 0 || n % 128 || k % 128 || k >= kFp8MaxK) return false;
   // counters of the few-token kernel, and its 32-bit scratch offsets
   if (m <= kFewM) return n / 128 <= (int64_t)((kWsReserved - kWsCounterOff) / 4) && m * n < (int64_t(1) << 29);
-  return (m + 127) / 128 * (n / 128) < (int64_t(1) << 31);
+  return (m + 63) / 64 * (n / 128) < (int64_t(1) << 31);
 }
 
-size_t gated_scratch_bytes(int64_t m, int64_t n) { return m <= kFewM ? (size_t)(m * n) * 4 : 0; }
+size_t gated_scratch_bytes(int64_t m, int64_t n, int64_t k) {
+  if (m <= kFewM) return (size_t)(m * n) * 4;
+  const int split = plan_gated(m, n, k, false).split;   // (the same for both kinds of scales)
+  return split > 1 ? (size_t)split * (size_t)m * 2 * n * 4 : 0;
+}
 
-hipError_t launch_gated(const Gated& a, hipStream_t s) {
+hipError_t launch_gated(Gated a, hipStream_t s) {
   if (!gated_launchable(a.m, a.n, a.k)) return hipErrorInvalidValue;
+  a.split = 1;
   if (a.m <= 16) return launch_few<1, 1>(a, s);
   if (a.m <= 32) return launch_few<2, 1>(a, s);
   if (a.m <= 48) return launch_few<3, 2>(a, s);
   if (a.m <= kFewM) return launch_few<4, 2>(a, s);
-  if (a.m <= 128) return launch_tiles<128>(a, s);
+  const GatedPlan p = plan_gated(a.m, a.n, a.k, a.pow2);
+  a.split = p.split;
+  a.blocks_each = p.blocks_each;
+  if (p.tm == 64) return launch_tiles<64>(a, s);
+  if (p.tm == 128) return launch_tiles<128>(a, s);
   return a.pow2 ? launch_tiles<256>(a, s) : launch_tiles<192>(a, s);
 }
 

@@ -268,10 +268,12 @@ struct Gated {
   float* scratch;           // gated_scratch_bytes
   // set by the launcher
   int64_t tiles_m, tiles_n;
+  int split;                // parts of K, each of blocks_each blocks of 128
+  int64_t blocks_each;
 };
 bool gated_launchable(int64_t m, int64_t n, int64_t k);
-size_t gated_scratch_bytes(int64_t m, int64_t n);
-hipError_t launch_gated(const Gated& a, hipStream_t s);
+size_t gated_scratch_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_gated(Gated a, hipStream_t s);
 
 // ---- its backward pass (gated_bwd.hip)
 struct GatedBackward {

@@ -105,7 +105,8 @@ def _check(m, n, k, pow2, seed, ws_buf=None):
 @pytest.mark.parametrize("m,n,k", [(1, 128, 128), (1, 256, 4096), (16, 384, 640), (17, 128, 1152), (32, 256, 512),
                                    (33, 128, 896), (48, 256, 1024), (49, 384, 256), (64, 128, 2048), (65, 128, 128),
                                    (100, 256, 512), (128, 384, 640), (129, 256, 384), (256, 128, 1024),
-                                   (300, 640, 1536), (513, 128, 128), (3, 1152, 7168)])
+                                   (300, 640, 1536), (513, 128, 128), (3, 1152, 7168), (65, 128, 1024), (100, 256, 1152),
+                                   (700, 128, 7168), (1500, 4096, 640), (1500, 4224, 256)])
 @pytest.mark.parametrize("pow2", [False, True])
 def test_gated_forward(m, n, k, pow2):
     print(f"gated m={m} n={n} k={k} pow2={pow2}", flush=True)
@@ -115,7 +116,7 @@ def test_gated_forward(m, n, k, pow2):
 @pytest.mark.parametrize("pow2", [False, True])
 def test_one_workspace_for_every_size(pow2):
     print(f"gated workspace pow2={pow2}", flush=True)
-    sizes = [(1, 512, 256), (40, 256, 384), (70, 256, 256), (2, 128, 512), (300, 128, 256), (64, 512, 128)]
+    sizes = [(1, 512, 256), (40, 256, 384), (70, 256, 256), (80, 256, 1024), (2, 128, 512), (300, 128, 256), (64, 512, 128)]
     need = max(ql.binding.qlinear_gated_forward_workspace(*s) for s in sizes)
     ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
     for i, s in enumerate(sizes):
