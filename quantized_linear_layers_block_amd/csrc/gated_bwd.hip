@@ -4,8 +4,8 @@
 //   dg = dh u s (1 + g (1 - s)),  du = dh g s
 //   dx = dg Wg + du Wu,   dWg = dg^T x,   dWu = du^T x
 //
-// Four kernels: the weights' scales made ready, dg and du side by side (D, [m][2 n]), and two matrix
-// products.  D is formed once in float32 and held twice: as f16 rows scaled by powers of two for dx
+// First a kernel forms dg and du side by side (D, [m][2 n]) and makes the weights' scales ready, then two
+// matrix products follow.  D is formed once in float32 and held twice: as f16 rows scaled by powers of two for dx
 // (its rounding, 2^-11, is far below that of a bf16 result; the weights meet it as f16 too, E4M3 values
 // times their scales rounded once more), and as bf16 for the weights' gradients, whose sums run over
 // tokens of any size, so that a row's factor could not be taken out.
@@ -44,28 +44,33 @@ __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
 // For each 128 columns of k the power of two 2^E that puts the largest of the 2 n / 128 scales in
 // [32, 64): then every weight is an f16 (448 * 64 < 2^15), normal down to 2^-20 of the largest scale.  tab
 // [2 n / 128][k / 128] holds f16(scale * 2^-E) twice in a word, cols [k / 128] 2^E.
-__global__ __launch_bounds__(256) void gated_scales_kernel(const void* __restrict__ sg, const void* __restrict__ su,
-                                                           int pow2, int64_t nb, int64_t kb, uint32_t* __restrict__ tab,
-                                                           float* __restrict__ cols) {
-  __shared__ uint32_t red[4];
-  const int64_t c = blockIdx.x;
+struct WeightScales {
+  const void* sg;
+  const void* su;
+  int pow2;
+  int64_t nb, kb;       // n / 128, k / 128
+  uint32_t* tab;
+  float* cols;
+};
+template <int T>
+__device__ __forceinline__ void weight_scales(const WeightScales& a, int64_t c, uint32_t* red) {
   auto scale = [&](int64_t i) {
-    const void* s = i < nb ? sg : su;
-    const int64_t at = (i < nb ? i : i - nb) * kb + c;
-    if (!pow2) return ((const float*)s)[at];
+    const void* s = i < a.nb ? a.sg : a.su;
+    const int64_t at = (i < a.nb ? i : i - a.nb) * a.kb + c;
+    if (!a.pow2) return ((const float*)s)[at];
     const uint32_t b = ((const uint8_t*)s)[at];
     return b == 255 ? __uint_as_float(0x7FC00000u) : b == 0 ? 0x1p-127f : __uint_as_float(b << 23);
   };
   uint32_t top = 0;
-  for (int64_t i = threadIdx.x; i < 2 * nb; i += 256) top = umax(top, __float_as_uint(scale(i)) & 0x7FFFFFFFu);
-  top = max_block<256>(top, red);
+  for (int64_t i = threadIdx.x; i < 2 * a.nb; i += T) top = umax(top, __float_as_uint(scale(i)) & 0x7FFFFFFFu);
+  top = max_block<T>(top, red);
   int e = top >= 0x7F800000u ? 0 : (int)(top >> 23) - 127 - 5;
   e = e < -120 ? -120 : e > 120 ? 120 : e;
-  for (int64_t i = threadIdx.x; i < 2 * nb; i += 256) {
+  for (int64_t i = threadIdx.x; i < 2 * a.nb; i += T) {
     const float s = scale(i) * pow2_float(-e);
-    tab[i * kb + c] = f16_pair(s, s);
+    a.tab[i * a.kb + c] = f16_pair(s, s);
   }
-  if (threadIdx.x == 0) cols[c] = pow2_float(e);
+  if (threadIdx.x == 0) a.cols[c] = pow2_float(e);
 }
 
 // --------------------------------------------------------------------------------- D
@@ -93,6 +98,7 @@ struct GateGrad {
   const uint16_t* x;    // with db: [m][k], whose last m % 32 rows go to xt [32][k], the others there zero
   uint16_t* xt;
   int64_t k;
+  WeightScales ws;      // with d16: its kb workgroups come first
 };
 
 // T threads a row, NV units of 8 columns each in registers (NV 0: any n, read twice).  Bound by memory:
@@ -100,7 +106,12 @@ struct GateGrad {
 template <int T, int NV>
 __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
   __shared__ uint32_t red[T / kWave];
-  const int64_t row = blockIdx.x;
+  const int64_t scales = a.d16 ? a.ws.kb : 0;
+  if (blockIdx.x < scales) {
+    weight_scales<T>(a.ws, blockIdx.x, red);
+    return;
+  }
+  const int64_t row = blockIdx.x - scales;
   const int64_t units = a.n / 8;
   const int t = threadIdx.x;
   if (a.db && a.m_pad != a.m && row >= a.m_pad - kBStep) {   // the last step of the weights' gradients is not full
@@ -265,11 +276,29 @@ __device__ __forceinline__ int zslot(int z, int s) { return s ^ ((s >> 4) & 1) ^
 // 16 rows go over LDS as rows 0..3 and 12..15 of one slot with 4..11 of the next, which these four keep apart.
 __device__ __forceinline__ int dslot(int q) { return ((q << 1) ^ (q & 2 ? 3 : 0)) & 3; }
 
+// Workgroup b of a product's: whole tiles first, then the parts of the split ones.
+__device__ __forceinline__ GemmWork product_work(const GatedProduct& a, int64_t b) {
+  GemmWork w;
+  int64_t t;
+  if (b < a.full) {
+    t = gemm_xcd_remap(b, a.full);
+    w.slot = -1;
+    w.split = 0;
+    w.nsplit = 1;
+  } else {
+    w.slot = b - a.full;
+    t = a.full + w.slot / a.split;
+    w.split = (int)(w.slot % a.split);
+    w.nsplit = a.split;
+  }
+  gemm_group_tile(t, a.tiles_r, a.tiles_c, w.tm, w.tn);
+  return w;
+}
+
 template <Kind KIND>
-__global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a) {
-  extern __shared__ __align__(16) uint8_t smem[];
+__device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, uint8_t* smem) {
   constexpr bool FUSED = KIND == kDx, TURNED = KIND == kDxT, DW = KIND == kDw;
-  const GemmWork work = gemm_schedule(a.tiles_r, a.tiles_c, a.full, a.split);
+  const GemmWork work = product_work(a, b);
   const int64_t c0 = (int64_t)__builtin_amdgcn_readfirstlane((int)work.tn) * kBTile;
   const int64_t r0 = (int64_t)__builtin_amdgcn_readfirstlane((int)work.tm) * kBTile;
   const int part_no = __builtin_amdgcn_readfirstlane(work.split);
@@ -523,10 +552,25 @@ __global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a
   }
 }
 
+template <Kind KIND>
+__global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  gated_product<KIND>(a, blockIdx.x, smem);
+}
+// dx and the weights' gradients side by side: few tokens leave neither enough tiles to fill the chip, and
+// a workgroup of a few steps takes some 12 us, most of it its start and end.
+__global__ __launch_bounds__(kBThreads) void gated_both_kernel(GatedProduct dx, GatedProduct dw, unsigned first) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  if (blockIdx.x < first)
+    gated_product<kDx>(dx, blockIdx.x, smem);
+  else
+    gated_product<kDw>(dw, blockIdx.x - first, smem);
+}
+
 // The parts of split tiles added in their order: 4 rows of a tile a workgroup, 4 columns a thread.
-__global__ __launch_bounds__(256) void gated_join_kernel(GatedProduct a) {
-  const int64_t tail = blockIdx.x / 64;
-  const int row = (int)(blockIdx.x % 64) * 4 + (int)(threadIdx.x >> 6);
+__device__ __forceinline__ void gated_join(const GatedProduct& a, int64_t b) {
+  const int64_t tail = b / 64;
+  const int row = (int)(b % 64) * 4 + (int)(threadIdx.x >> 6);
   const int col = (int)(threadIdx.x & 63) * 4;
   int64_t tr, tc;
   gemm_group_tile(a.full + tail, a.tiles_r, a.tiles_c, tr, tc);
@@ -538,14 +582,20 @@ __global__ __launch_bounds__(256) void gated_join_kernel(GatedProduct a) {
   const int second = rr >= a.n && a.out[1] != a.out[0];
   store4((second ? a.out[1] : a.out[0]) - (second ? a.n * a.k : 0), 0, a.k, rr, c, v, a.k);
 }
+__global__ __launch_bounds__(256) void gated_join_kernel(GatedProduct dx, GatedProduct dw, unsigned first) {
+  if (blockIdx.x < first)
+    gated_join(dx, blockIdx.x);
+  else
+    gated_join(dw, blockIdx.x - first);
+}
 
 // Tiles and how the ones behind the last full round of the chip are split along z.
 struct ProductPlan {
-  int64_t tiles_r, tiles_c, full;
-  int32_t split;
-  size_t part_bytes() const {
-    return split > 1 ? (size_t)(tiles_r * tiles_c - full) * (size_t)split * kBTile * kBTile * 4 : 0;
-  }
+  int64_t tiles_r = 0, tiles_c = 0, full = 0;
+  int32_t split = 1;
+  int64_t tail() const { return split > 1 ? tiles_r * tiles_c - full : 0; }
+  unsigned grid() const { return (unsigned)(full + tail() * split); }
+  size_t part_bytes() const { return (size_t)tail() * (size_t)split * kBTile * kBTile * 4; }
 };
 constexpr int64_t kBCUs = 256;
 ProductPlan plan_product(int64_t rows, int64_t z, int64_t k) {
@@ -562,26 +612,12 @@ ProductPlan plan_product(int64_t rows, int64_t z, int64_t k) {
   return p;
 }
 
-template <Kind KIND>
-hipError_t launch_product(GatedProduct a, const ProductPlan& p, hipStream_t s) {
-  a.tiles_r = p.tiles_r;
-  a.tiles_c = p.tiles_c;
-  a.full = p.full;
-  a.split = p.split;
-  const int64_t tail = p.tiles_r * p.tiles_c - p.full;
-  hipError_t e = hipFuncSetAttribute((const void*)gated_product_kernel<KIND>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kBLds);
-  if (e != hipSuccess) return e;
-  gated_product_kernel<KIND><<<(unsigned)(p.full + tail * p.split), kBThreads, kBLds, s>>>(a);
-  if (p.split > 1) gated_join_kernel<<<(unsigned)(tail * 64), 256, 0, s>>>(a);
-  return hipGetLastError();
-}
-
 constexpr size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // From so many tokens on dx reads the weights turned to f16 beforehand.
 bool turned(int64_t m) { return m >= 2048; }
 
-// last rows of x | cols | scale table | row factors | D16 | Db | turned weights | parts (both products', one after the other)
+// last rows of x | cols | scale table | row factors | D16 | Db | turned weights | parts of dx | of the weights' gradients
 struct BwdWs {
   uint16_t* xt;
   float* cols;
@@ -590,7 +626,7 @@ struct BwdWs {
   uint16_t* d16;
   uint16_t* db;
   uint16_t* w16;
-  float* part;
+  float* part[2];
   size_t bytes;
 };
 int64_t pad_tokens(int64_t m) { return (m + kBStep - 1) / kBStep * kBStep; }
@@ -610,8 +646,8 @@ BwdWs bwd_ws(void* ws, int64_t m, int64_t n, int64_t k) {
   w.d16 = (uint16_t*)take((size_t)m * 2 * n * 2);
   w.db = (uint16_t*)take((size_t)pad_tokens(m) * 2 * n * 2);
   w.w16 = (uint16_t*)take(turned(m) ? (size_t)k * 2 * n * 2 : 0);
-  const size_t a = plan_product(m, 2 * n, k).part_bytes(), b = plan_product(2 * n, m, k).part_bytes();
-  w.part = (float*)take(a > b ? a : b);
+  w.part[0] = (float*)take(plan_product(m, 2 * n, k).part_bytes());
+  w.part[1] = (float*)take(plan_product(2 * n, m, k).part_bytes());
   w.bytes = at;
   return w;
 }
@@ -630,7 +666,6 @@ size_t gated_backward_bytes(int64_t m, int64_t n, int64_t k) { return bwd_ws(nul
 hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
   if (!gated_backward_launchable(a.m, a.n, a.k)) return hipErrorInvalidValue;
   const BwdWs w = bwd_ws(a.scratch, a.m, a.n, a.k);
-  gated_scales_kernel<<<(unsigned)(a.k / 128), 256, 0, s>>>(a.sg, a.su, a.pow2, a.n / 128, a.k / 128, w.tab, w.cols);
   GateGrad d;
   d.dh = a.dh;
   d.gu = a.gu;
@@ -643,7 +678,14 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
   d.x = a.x;
   d.xt = w.xt;
   d.k = a.k;
-  const unsigned grid = (unsigned)(a.dgate ? d.m_pad : a.m);
+  d.ws.sg = a.sg;
+  d.ws.su = a.su;
+  d.ws.pow2 = a.pow2;
+  d.ws.nb = a.n / 128;
+  d.ws.kb = a.k / 128;
+  d.ws.tab = w.tab;
+  d.ws.cols = w.cols;
+  const unsigned grid = (unsigned)((a.dgate ? d.m_pad : a.m) + (a.dx ? d.ws.kb : 0));
   if (a.n <= 2048) gate_grad_kernel<256, 1><<<grid, 256, 0, s>>>(d);
   else if (a.n <= 4096) gate_grad_kernel<256, 2><<<grid, 256, 0, s>>>(d);
   else if (a.n <= 8192) gate_grad_kernel<512, 2><<<grid, 512, 0, s>>>(d);
@@ -651,41 +693,66 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
   else gate_grad_kernel<1024, 0><<<grid, 1024, 0, s>>>(d);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  GatedProduct p = {};
-  p.n = a.n;
-  p.k = a.k;
-  p.part = w.part;
+
+  GatedProduct dx = {}, dw = {};
+  ProductPlan px = {}, pw = {};
+  auto planned = [&](GatedProduct& p, const ProductPlan& plan, float* part) {
+    p.n = a.n;
+    p.k = a.k;
+    p.tiles_r = plan.tiles_r;
+    p.tiles_c = plan.tiles_c;
+    p.full = plan.full;
+    p.split = plan.split;
+    p.part = part;
+  };
   if (a.dx) {
-    p.codes[0] = a.wg;
-    p.codes[1] = a.wu;
-    p.tab = w.tab;
-    p.q = w.d16;
-    p.rs = w.rs;
-    p.cols = w.cols;
-    p.rows = a.m;
-    p.z = 2 * a.n;
-    p.out[0] = p.out[1] = a.dx;
-    const ProductPlan plan = plan_product(a.m, 2 * a.n, a.k);
-    if (turned(a.m)) {
-      gated_weights_kernel<<<dim3((unsigned)(a.k / 128), (unsigned)(2 * a.n / 128)), 256, 0, s>>>(a.wg, a.wu, w.tab, a.n, a.k, w.w16);
-      p.p = w.w16;
-      e = launch_product<kDxT>(p, plan, s);
-    } else {
-      e = launch_product<kDx>(p, plan, s);
-    }
-    if (e != hipSuccess) return e;
+    px = plan_product(a.m, 2 * a.n, a.k);
+    planned(dx, px, w.part[0]);
+    dx.codes[0] = a.wg;
+    dx.codes[1] = a.wu;
+    dx.tab = w.tab;
+    dx.p = w.w16;
+    dx.q = w.d16;
+    dx.rs = w.rs;
+    dx.cols = w.cols;
+    dx.rows = a.m;
+    dx.z = 2 * a.n;
+    dx.out[0] = dx.out[1] = a.dx;
   }
   if (a.dgate) {
-    p.p = a.x;
-    p.xt = w.xt;
-    p.q = w.db;
-    p.rows = 2 * a.n;
-    p.z = a.m;
-    p.out[0] = a.dgate;
-    p.out[1] = a.dup;
-    e = launch_product<kDw>(p, plan_product(2 * a.n, a.m, a.k), s);
+    pw = plan_product(2 * a.n, a.m, a.k);
+    planned(dw, pw, w.part[1]);
+    dw.p = a.x;
+    dw.xt = w.xt;
+    dw.q = w.db;
+    dw.rows = 2 * a.n;
+    dw.z = a.m;
+    dw.out[0] = a.dgate;
+    dw.out[1] = a.dup;
   }
-  return e;
+  auto room = [](auto kernel) {
+    return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kBLds);
+  };
+  if (!turned(a.m) && a.dx && a.dgate) {
+    if ((e = room(gated_both_kernel)) != hipSuccess) return e;
+    gated_both_kernel<<<px.grid() + pw.grid(), kBThreads, kBLds, s>>>(dx, dw, px.grid());
+  } else {
+    if (a.dx && turned(a.m)) {
+      if ((e = room(gated_product_kernel<kDxT>)) != hipSuccess) return e;
+      gated_weights_kernel<<<dim3((unsigned)(a.k / 128), (unsigned)(2 * a.n / 128)), 256, 0, s>>>(a.wg, a.wu, w.tab, a.n, a.k, w.w16);
+      gated_product_kernel<kDxT><<<px.grid(), kBThreads, kBLds, s>>>(dx);
+    } else if (a.dx) {
+      if ((e = room(gated_product_kernel<kDx>)) != hipSuccess) return e;
+      gated_product_kernel<kDx><<<px.grid(), kBThreads, kBLds, s>>>(dx);
+    }
+    if (a.dgate) {
+      if ((e = room(gated_product_kernel<kDw>)) != hipSuccess) return e;
+      gated_product_kernel<kDw><<<pw.grid(), kBThreads, kBLds, s>>>(dw);
+    }
+  }
+  const unsigned join = (unsigned)((px.tail() + pw.tail()) * 64);
+  if (join) gated_join_kernel<<<join, 256, 0, s>>>(dx, dw, (unsigned)(px.tail() * 64));
+  return hipGetLastError();
 }
 
 }  // namespace ql
