@@ -92,7 +92,7 @@ struct GateGrad {
   const uint16_t* dh;   // [m][n]
   const uint16_t* gu;   // [m][2 n]
   int64_t m, n, m_pad;
-  uint16_t* d16;        // f16 [m][2 n], or null
+  uint16_t* d16;        // f16 [2 n / 32][m][32], or null
   float* rs;            // [m]
   uint16_t* db;         // bf16 [m_pad][2 n], rows past m zero, or null
   const uint16_t* x;    // with db: [m][k], whose last m % 32 rows go to xt [32][k], the others there zero
@@ -111,7 +111,10 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
     weight_scales<T>(a.ws, blockIdx.x, red);
     return;
   }
-  const int64_t row = blockIdx.x - scales;
+  // Neighbouring rows share lines of d16: they go to one XCD, whose cache puts the lines together (287 us for 8192 x
+  // 14336; 386 with the rows dealt out one by one).
+  const int64_t b = blockIdx.x - scales, rows = gridDim.x - scales, whole = rows / 8 * 8;
+  const int64_t row = b < whole ? gemm_xcd_remap(b, whole) : b;
   const int64_t units = a.n / 8;
   const int t = threadIdx.x;
   if (a.db && a.m_pad != a.m && row >= a.m_pad - kBStep) {   // the last step of the weights' gradients is not full
@@ -149,10 +152,10 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
                                       pack_bf16x2_rne(du[4], du[5]), pack_bf16x2_rne(du[6], du[7]));
     }
     if (a.d16) {
-      uint16_t* p = a.d16 + row * 2 * a.n + u * 8;
+      uint16_t* p = a.d16 + ((u >> 2) * a.m + row) * 32 + (u & 3) * 8;
       *(uint4*)p = make_uint4(f16_pair(dg[0] * f, dg[1] * f), f16_pair(dg[2] * f, dg[3] * f),
                               f16_pair(dg[4] * f, dg[5] * f), f16_pair(dg[6] * f, dg[7] * f));
-      *(uint4*)(p + a.n) = make_uint4(f16_pair(du[0] * f, du[1] * f), f16_pair(du[2] * f, du[3] * f),
+      *(uint4*)(p + a.n * a.m) = make_uint4(f16_pair(du[0] * f, du[1] * f), f16_pair(du[2] * f, du[3] * f),
                                       f16_pair(du[4] * f, du[5] * f), f16_pair(du[6] * f, du[7] * f));
     }
   };
@@ -203,7 +206,7 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
 }
 
 // ------------------------------------------------------------------------------ weights, turned
-// For many tokens: both weights as f16 [k][2 n], times their scales from tab.  A workgroup takes 128 x 128 codes; a
+// For many tokens: both weights as f16 [2 n / 32][k][32], times their scales from tab.  A workgroup takes 128 x 128 codes; a
 // thread 8 rows by 4 columns, whose bytes v_perm_b32 turns into 4 columns of 8.  Bound by memory (1 byte read, 2
 // written a weight): 70 us for 2 x 14336 x 4096, which the product gains back from about 1500 tokens on.
 __global__ __launch_bounds__(256) void gated_weights_kernel(const uint8_t* __restrict__ wg, const uint8_t* __restrict__ wu,
@@ -228,15 +231,16 @@ __global__ __launch_bounds__(256) void gated_weights_kernel(const uint8_t* __res
         const uint32_t two = __builtin_amdgcn_perm(v[2 * h + 1], v[2 * h], pick);
         out[h] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(two, 1.0f, false) * sc);
       }
-      *(uint4*)(w16 + (k0 + c + e) * 2 * n + z0 + z) = make_uint4(out[0], out[1], out[2], out[3]);
+      *(uint4*)(w16 + ((z0 + z) / 32 * k + k0 + c + e) * 32 + z % 32) = make_uint4(out[0], out[1], out[2], out[3]);
     }
   }
 }
 
 // ------------------------------------------------------------------------------ products
 // out[row][k] = factors * sum over z of P[z][k] Q[z][row]
-//   kDx:  rows are tokens, z the 2 n weight rows: P the weights (E4M3 in memory, f16 from there), Q = D16 [row][z]
-//   kDxT: the same with P = the weights as f16 [k][z], turned by gated_weights_kernel beforehand
+//   kDx:  rows are tokens, z the 2 n weight rows: P the weights (E4M3 in memory, f16 from there), Q = D16 in steps,
+//         [z / 32][row][32], so that what a step reads of 256 rows is one piece of whole lines
+//   kDxT: the same with P = the weights as f16 [z / 32][k][32], turned by gated_weights_kernel beforehand
 //   kDw:  rows are the 2 n weight rows, z tokens: P = x [z][k], Q = Db [z][row], bf16
 // Tiles of 256 k x 256 rows by four waves (2 x 2) of 128 x 128 each: 64 MFMAs of 16x16x32 for 16 fragments
 // a step, which leaves half of LDS's read rate free.  P is the MFMA's A operand, so a lane's four results
@@ -255,9 +259,9 @@ enum Kind { kDw, kDx, kDxT };
 struct GatedProduct {
   const uint8_t* codes[2];   // kDx: gate and up, E4M3 [n][k]
   const uint32_t* tab;       // kDx: [2 n / 128][k / 128] f16 scale twice
-  const uint16_t* p;         // kDw: x [z][k]; kDxT: the weights, f16 [k][z]
+  const uint16_t* p;         // kDw: x [z][k]; kDxT: the weights, f16 [z / 32][k][32]
   const uint16_t* xt;        // its last step, rows past the last token zero, where z is no multiple of 32
-  const uint16_t* q;         // D16 [rows][z], or Db [z padded][rows]
+  const uint16_t* q;         // D16 [z / 32][rows][32], or Db [z padded][rows]
   const float* rs;           // kDx, kDxT: [rows]
   const float* cols;         // the same: [k / 128]
   int64_t rows, z, n, k;     // z: 2 n, or tokens; n: rows of one weight
@@ -329,9 +333,9 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int row = 64 * wave + 16 * c + (lane >> 2), in = ((lane & 3) ^ dslot(lane >> 4)) * 16;
-      od[c] = (uint32_t)((row < r_last ? row : r_last) * a.z * 2 + in) + kUp - 1024 * c;
+      od[c] = (uint32_t)((row < r_last ? row : r_last) * 64 + in) + kUp - 1024 * c;
       if (TURNED)
-        op[c] = (uint32_t)((row < c_room ? row : row - 128) * a.z * 2 + in) + kUp - 1024 * c;
+        op[c] = (uint32_t)((row < c_room ? row : row - 128) * 64 + in) + kUp - 1024 * c;
       else
         op[c] = (uint32_t)((8 * wave + 4 * (c & 1) + (lane >> 4)) * a.k + col) + kUp - 1024 * (c & 1);
     }
@@ -356,7 +360,7 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
       lds_copy4((const uint8_t*)(a.tab + (z0 / 128) * (a.k / 128) + c0 / 128), osc,
                 lds0 + kBScaleOff + slot * kBScaleBytes + wave * 256);
     } else if (TURNED) {
-      lds_copy16x4((const uint8_t*)(a.p + c0 * a.z + st * kBStep) - kUp, op[0], op[1], op[2], op[3],
+      lds_copy16x4((const uint8_t*)(a.p + (st * a.k + c0) * kBStep) - kUp, op[0], op[1], op[2], op[3],
                    lds0 + slot * (2 * kBRowsBytes) + wave * 4096);
     } else {
       lds_copy16x4((const uint8_t*)((st < whole ? a.p + st * kBStep * a.k : a.xt) + c0) - kUp, op[0], op[1], op[2], op[3],
@@ -364,7 +368,7 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
     }
   };
   auto copy_d = [&](int64_t st, int slot) {
-    const uint16_t* d = a.q + (DW ? st * kBStep * a.rows + r0 : r0 * a.z + st * kBStep);
+    const uint16_t* d = a.q + (DW ? st * kBStep * a.rows + r0 : (st * a.rows + r0) * kBStep);
     lds_copy16x4((const uint8_t*)d - kUp, od[0], od[1], od[2], od[3],
                  lds0 + (FUSED ? slot * kBRowsBytes : slot * (2 * kBRowsBytes) + kBRowsBytes) + wave * 4096);
   };
