@@ -19,21 +19,13 @@ namespace ql {
 
 namespace {
 
-constexpr int kBTile = 256;                 // columns (k) and rows (tokens, or weight rows) of an output tile
+constexpr int kBCols = 256;                 // columns (k) of an output tile
 constexpr int kBStep = 32;                  // depth of a step: one MFMA deep
 constexpr int kBThreads = 256;
-constexpr int kBRing = 4;                   // steps in flight
 constexpr int kBPitch = 272;                // output staging: bytes per row of 128 bf16 columns
-constexpr int kBStagePerWave = 128 * kBPitch;
-constexpr int kBRowsBytes = kBTile * kBStep * 2;   // one operand of one step, 16 bits an element
-constexpr int kBCodeBytes = kBTile * kBStep;
+constexpr int kBPBytes = kBCols * kBStep * 2;      // P of one step, 16 bits an element
+constexpr int kBCodeBytes = kBCols * kBStep;
 constexpr int kBScaleBytes = 1024;          // one word a thread
-constexpr size_t kBLds = 4 * kBStagePerWave;
-// dx: ring of D rows, ring of codes, two steps of weights in f16, ring of scale words
-constexpr int kBCodeOff = kBRing * kBRowsBytes, kBWOff = kBCodeOff + kBRing * kBCodeBytes,
-              kBScaleOff = kBWOff + 2 * kBRowsBytes;
-static_assert(kBScaleOff + kBRing * kBScaleBytes <= (int)kBLds && 2 * kBRing * kBRowsBytes <= (int)kBLds,
-              "the operands fit in the output's staging area");
 
 __device__ __forceinline__ float pow2_float(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
@@ -249,18 +241,25 @@ __global__ __launch_bounds__(256) void gated_weights_kernel(const uint8_t* __res
 // A step is four quarters of 16 MFMAs (4 fragments of each operand): P low Q low, P high Q low, P high Q high,
 // P low Q high.  Each quarter reads the four fragments that are new in a later one, over those that no
 // MFMA needs any more, so LDS, which the four waves' fragments keep busy for half of a step's time and the
-// copies for a quarter, is read evenly (all of Q read in an eighth of the step made the MFMAs wait for it).
-// The barrier stands in the middle: there every fragment of step s is read and step s + 1 has landed, so
-// that from there to the next middle the copies of s + 4 go into the place of s, in a ring of four.  kDx: the codes of
-// s + 2 have landed too, and each lane turns those that it copied itself into f16 from this middle to the next.
-// With one wave a SIMD nothing else fills the matrix unit's time, so every other instruction has its place
-// behind an MFMA, a few behind each.
+// copies for a quarter, is read evenly.  The barrier stands in the middle: there every fragment of step s is read
+// and step s + 1 has landed, so that from there to the next middle the copies of s + RING go into the place of s.
+// kDx: the codes of s + 2 have landed too, and each lane turns those that it copied itself into f16 from this
+// middle to the next.
+// A wave alone on its SIMD issues an instruction in about five cycles (measured: MFMAs of 16x16x32, 16
+// cycles, keep their rate beside one other instruction each and lose a quarter beside two): so every
+// other instruction has a place behind an MFMA, and there are few of them -- copies by four with one base, the
+// ring's places constants of an unrolled loop.  (32x32x16 MFMAs leave more room and took a fifth fewer cycles, but
+// move their sums twice as often for the same work: the card's power lowered the clock from 1.9 to 1.5 GHz and the
+// time rose by a tenth.)
+// NJ: Q fragments of a wave.  8 (tiles of 256 rows, one wave a SIMD) for depth; 4 (128 rows) has half the sums
+// -- two halves of 16 MFMAs a step, P low and P high -- for few tokens (kDx), or so that two workgroups share a CU
+// and one's start and end, most of the time of a few steps, run beside the other's products (kDw).
 enum Kind { kDw, kDx, kDxT };
 struct GatedProduct {
   const uint8_t* codes[2];   // kDx: gate and up, E4M3 [n][k]
   const uint32_t* tab;       // kDx: [2 n / 128][k / 128] f16 scale twice
   const uint16_t* p;         // kDw: x [z][k]; kDxT: the weights, f16 [z / 32][k][32]
-  const uint16_t* xt;        // its last step, rows past the last token zero, where z is no multiple of 32
+  const uint16_t* xt;        // kDw: x's last step, rows past the last token zero, where z is no multiple of 32
   const uint16_t* q;         // D16 [z / 32][rows][32], or Db [z padded][rows]
   const float* rs;           // kDx, kDxT: [rows]
   const float* cols;         // the same: [k / 128]
@@ -268,7 +267,8 @@ struct GatedProduct {
   uint16_t* out[2];          // kDx, kDxT: dx twice; else the gate's and the up projection's gradient
   int64_t tiles_r, tiles_c, full;
   int32_t split;
-  float* part;               // [split workgroup][256 rows][256 k]
+  int32_t tile_rows;         // 32 NJ
+  float* part;               // [split workgroup][tile_rows][256 k]
 };
 
 // 16-byte slot of logical slot s in LDS row z (32 slots of 512 bytes).  A transposing read of 32 lanes
@@ -276,9 +276,17 @@ struct GatedProduct {
 // of 16 lanes to even slots of one row takes odd ones in the row's second half.
 __device__ __forceinline__ int zslot(int z, int s) { return s ^ ((s >> 4) & 1) ^ (2 * ((z & 3) | ((z >> 1) & 4))); }
 
+// The same for rows of 256 bytes (16 slots).
+__device__ __forceinline__ int qslot(int z, int s) { return s ^ (2 * ((z & 3) | ((z >> 1) & 4))); }
 // The 16-byte slot of a 64-byte row of D that holds slot 0, by bits 2 and 3 of the row: 16-byte reads of one slot of
 // 16 rows go over LDS as rows 0..3 and 12..15 of one slot with 4..11 of the next, which these four keep apart.
 __device__ __forceinline__ int dslot(int q) { return ((q << 1) ^ (q & 2 ? 3 : 0)) & 3; }
+
+// At most N of the copies under way are left.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
 // Workgroup b of a product's: whole tiles first, then the parts of the split ones.
 __device__ __forceinline__ GemmWork product_work(const GatedProduct& a, int64_t b) {
@@ -290,21 +298,44 @@ __device__ __forceinline__ GemmWork product_work(const GatedProduct& a, int64_t 
     w.split = 0;
     w.nsplit = 1;
   } else {
-    w.slot = b - a.full;
-    t = a.full + w.slot / a.split;
-    w.split = (int)(w.slot % a.split);
+    const int64_t tail = a.tiles_r * a.tiles_c - a.full, at = b - a.full;
+    if (a.split % 8 == 0) {   // workgroups go to the eight XCDs in turn: an XCD takes a part of z of every tile
+      w.split = (int)(at % 8 + 8 * (at / 8 / tail));
+      t = at / 8 % tail;
+    } else {
+      w.split = (int)(at % a.split);
+      t = at / a.split;
+    }
+    w.slot = t * a.split + w.split;
+    t += a.full;
     w.nsplit = a.split;
   }
   gemm_group_tile(t, a.tiles_r, a.tiles_c, w.tm, w.tn);
   return w;
 }
 
-template <Kind KIND>
+// LDS of a kind: slots of P and Q together; kDx: ring of Q, ring of codes, two steps of weights in f16, ring of scale
+// words.  The output's staging takes the same place.
+template <Kind KIND, int NJ>
+struct Lds {
+  static constexpr int kRing = KIND == kDw && NJ == 4 ? 3 : 4;
+  static constexpr int kQBytes = 32 * NJ * kBStep * 2;
+  static constexpr int kQOff = KIND == kDx ? 0 : kBPBytes;
+  static constexpr int kSlot = KIND == kDx ? kQBytes : kBPBytes + kQBytes;
+  static constexpr int kCodeOff = kRing * kSlot, kWOff = kCodeOff + kRing * kBCodeBytes, kScaleOff = kWOff + 2 * kBPBytes;
+  static constexpr int kStage = 16 * NJ * kBPitch;   // of a wave's output
+  static constexpr int kLoop = KIND == kDx ? kScaleOff + kRing * kBScaleBytes : kRing * kSlot;
+  static constexpr int kBytes = kLoop > 4 * kStage ? kLoop : 4 * kStage;
+};
+
+template <Kind KIND, int NJ>
 __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, uint8_t* smem) {
+  using L = Lds<KIND, NJ>;
   constexpr bool FUSED = KIND == kDx, TURNED = KIND == kDxT, DW = KIND == kDw;
+  constexpr int kRows = 32 * NJ, kWRows = 16 * NJ;      // rows of a tile, of a wave
   const GemmWork work = product_work(a, b);
-  const int64_t c0 = (int64_t)__builtin_amdgcn_readfirstlane((int)work.tn) * kBTile;
-  const int64_t r0 = (int64_t)__builtin_amdgcn_readfirstlane((int)work.tm) * kBTile;
+  const int64_t c0 = (int64_t)__builtin_amdgcn_readfirstlane((int)work.tn) * kBCols;
+  const int64_t r0 = (int64_t)__builtin_amdgcn_readfirstlane((int)work.tm) * kRows;
   const int part_no = __builtin_amdgcn_readfirstlane(work.split);
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
@@ -321,34 +352,33 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
   const uint32_t lds0 = lds_addr(smem);
 
   // ---- copies of a step, the same by every wave, from uniform addresses with a lane's 32-bit offsets
-  //   kDx: seven: weight rows 8 wave + 4 c + lane / 16 (two, 16 codes a lane), a scale word for a lane's codes, D rows
-  //   64 wave + 16 c + lane / 4, 16-byte slot lane % 4 (four)
-  //   kDxT: eight: rows 64 wave + 16 c + lane / 4 of the weights (columns of k) and of D
-  //   kDw: eight: rows (z) 8 wave + 2 c + lane / 32, slot lane % 32, of x and of D
+  //   P  kDx: weight rows 8 wave + 4 c + lane / 16 (two copies, 16 codes a lane), and a scale word for a lane's codes
+  //      kDxT: columns of k 64 wave + 16 c + lane / 4, 16-byte slot lane % 4
+  //      kDw: x rows (z) 8 wave + 2 c + lane / 32, slot lane % 32
+  //   Q  kDx, kDxT: D rows 8 NJ wave + 16 c + lane / 4, slot lane % 4; kDw: D rows (z) of 2 kRows bytes
+  constexpr int kQCopies = NJ / 2;
+  constexpr int kCopies = (FUSED ? 3 : 4) + kQCopies;
   constexpr uint32_t kUp = 3072;     // see lds_copy16x4
   uint32_t op[4], od[4], osc = 0;
-  if (!DW) {
+  {
     // columns past k: the 128 before
     const int col = 16 * (lane & 15) < c_room ? 16 * (lane & 15) : 16 * (lane & 15) - 128;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int row = 64 * wave + 16 * c + (lane >> 2), in = ((lane & 3) ^ dslot(lane >> 4)) * 16;
-      od[c] = (uint32_t)((row < r_last ? row : r_last) * 64 + in) + kUp - 1024 * c;
-      if (TURNED)
-        op[c] = (uint32_t)((row < c_room ? row : row - 128) * 64 + in) + kUp - 1024 * c;
-      else
-        op[c] = (uint32_t)((8 * wave + 4 * (c & 1) + (lane >> 4)) * a.k + col) + kUp - 1024 * (c & 1);
+      if (DW) {
+        const int z = 8 * wave + 2 * c + (lane >> 5), s = zslot(z, lane & 31);     // (its own inverse)
+        op[c] = (uint32_t)(z * a.k * 2 + (8 * s < c_room ? 8 * s : 8 * s - 128) * 2) + kUp - 1024 * c;
+        const int zq = NJ == 8 ? z : 8 * wave + 4 * (c & 1) + (lane >> 4);
+        od[c] = (uint32_t)(zq * a.rows * 2 + (NJ == 8 ? s : qslot(zq, lane & 15)) * 16) + kUp - 1024 * (NJ == 8 ? c : c & 1);
+      } else {
+        const int in = ((lane & 3) ^ dslot(lane >> 4)) * 16;
+        const int prow = 64 * wave + 16 * c + (lane >> 2), qrow = 8 * NJ * wave + 16 * c + (lane >> 2);
+        op[c] = TURNED ? (uint32_t)((prow < c_room ? prow : prow - 128) * 64 + in) + kUp - 1024 * c
+                       : (uint32_t)((8 * wave + 4 * (c & 1) + (lane >> 4)) * a.k + col) + kUp - 1024 * (c & 1);
+        od[c] = (uint32_t)((qrow < r_last ? qrow : r_last) * 64 + in) + kUp - 1024 * c;
+      }
     }
     osc = (uint32_t)(col / 128 * 4);
-  } else {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int z = 8 * wave + 2 * c + (lane >> 5);
-      const int s = zslot(z, lane & 31);     // (its own inverse)
-      const int col = 8 * s < c_room ? 8 * s : 8 * s - 128;
-      op[c] = (uint32_t)(z * a.k * 2 + col * 2) + kUp - 1024 * c;
-      od[c] = (uint32_t)(z * a.rows * 2 + s * 16) + kUp - 1024 * c;
-    }
   }
   const int64_t whole = DW ? a.z / kBStep : steps;   // steps of whole rows of x
   auto copy_p = [&](int64_t st, int slot) {
@@ -356,29 +386,29 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
       const int64_t z0 = st * kBStep;
       const int up = z0 >= a.n;
       lds_copy16x2((up ? a.codes[1] : a.codes[0]) + (up ? z0 - a.n : z0) * a.k + c0 - kUp, op[0], op[1],
-                   lds0 + kBCodeOff + slot * kBCodeBytes + wave * 2048);
+                   lds0 + L::kCodeOff + slot * kBCodeBytes + wave * 2048);
       lds_copy4((const uint8_t*)(a.tab + (z0 / 128) * (a.k / 128) + c0 / 128), osc,
-                lds0 + kBScaleOff + slot * kBScaleBytes + wave * 256);
-    } else if (TURNED) {
-      lds_copy16x4((const uint8_t*)(a.p + (st * a.k + c0) * kBStep) - kUp, op[0], op[1], op[2], op[3],
-                   lds0 + slot * (2 * kBRowsBytes) + wave * 4096);
+                lds0 + L::kScaleOff + slot * kBScaleBytes + wave * 256);
     } else {
-      lds_copy16x4((const uint8_t*)((st < whole ? a.p + st * kBStep * a.k : a.xt) + c0) - kUp, op[0], op[1], op[2], op[3],
-                   lds0 + slot * (2 * kBRowsBytes) + wave * 4096);
+      const uint16_t* src = TURNED ? a.p + (st * a.k + c0) * kBStep : (st < whole ? a.p + st * kBStep * a.k : a.xt) + c0;
+      lds_copy16x4((const uint8_t*)src - kUp, op[0], op[1], op[2], op[3], lds0 + slot * L::kSlot + wave * 4096);
     }
   };
   auto copy_d = [&](int64_t st, int slot) {
-    const uint16_t* d = a.q + (DW ? st * kBStep * a.rows + r0 : (st * a.rows + r0) * kBStep);
-    lds_copy16x4((const uint8_t*)d - kUp, od[0], od[1], od[2], od[3],
-                 lds0 + (FUSED ? slot * kBRowsBytes : slot * (2 * kBRowsBytes) + kBRowsBytes) + wave * 4096);
+    const uint8_t* d = (const uint8_t*)(a.q + (DW ? st * kBStep * a.rows + r0 : (st * a.rows + r0) * kBStep)) - kUp;
+    const uint32_t dst = lds0 + L::kQOff + slot * L::kSlot + wave * 512 * NJ;
+    if (NJ == 8)
+      lds_copy16x4(d, od[0], od[1], od[2], od[3], dst);
+    else
+      lds_copy16x2(d, od[0], od[1], dst);
   };
 
   // ---- kDx: the step's weights from codes to f16, 32 a thread, those that the thread itself copied
   auto read_codes = [&](int slot, int c) {
-    return *(const i32x4*)(smem + kBCodeOff + slot * kBCodeBytes + (8 * wave + 4 * c + (lane >> 4)) * 256 + 16 * (lane & 15));
+    return *(const i32x4*)(smem + L::kCodeOff + slot * kBCodeBytes + (8 * wave + 4 * c + (lane >> 4)) * 256 + 16 * (lane & 15));
   };
   auto read_scale = [&](int slot) {
-    return __builtin_bit_cast(f16x2, *(const uint32_t*)(smem + kBScaleOff + slot * kBScaleBytes + wave * 256 + 4 * lane));
+    return __builtin_bit_cast(f16x2, *(const uint32_t*)(smem + L::kScaleOff + slot * kBScaleBytes + wave * 256 + 4 * lane));
   };
   f16x2 wv[4];
   int wo[2][2];   // where a thread's pieces of 8 go
@@ -396,57 +426,61 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
                      : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)w[2 * h + (e >> 1)], 1.0f, false)) * sc;
       return;
     }
-    *(f16x8*)(smem + wo[c][h] + kBWOff + buf * kBRowsBytes) =
+    *(f16x8*)(smem + wo[c][h] + L::kWOff + buf * kBPBytes) =
         f16x8{wv[0][0], wv[0][1], wv[1][0], wv[1][1], wv[2][0], wv[2][1], wv[3][0], wv[3][1]};
   };
 
   // ---- fragments: lane (r, g) has z 8 g .. 8 g + 7 of column (or row) r.  Transposing reads: lanes 4 e + b name row
   // 8 g + 4 q + e, columns 4 b .. 4 b + 3, and receive rows 8 g + 4 q + (0 .. 3) of column r.
-  const int te = r >> 2, tb = r & 3;
-  const int tmask = te | ((g & 1) << 2);
-  auto tr_base = [&](int half) {   // of fragment 0 of columns 128 half ..; fragment i flips bits 5 .. 7
-    return (8 * g + te) * 512 + half * 256 + tmask * 32 + (((tb >> 1) ^ half) << 4) + (tb & 1) * 8;
-  };
-  int ta[8], tq[8];
+  const int te = r >> 2, tb = r & 3, tz = 8 * g + te;
+  int ta[8], tq[NJ];   // fragment i flips bits 5 .. 7 of fragment 0's place
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int in = 16 * i * 64 + r * 64 + (g ^ dslot(r >> 2)) * 16;
-    ta[i] = TURNED ? 128 * wk * 64 + in : tr_base(wk) ^ (i << 5);
-    tq[i] = DW ? kBRowsBytes + (tr_base(wr) ^ (i << 5)) : (TURNED ? kBRowsBytes : 0) + 128 * wr * 64 + in;
+    ta[i] = TURNED ? 128 * wk * 64 + in : (tz * 512 + zslot(tz, 16 * wk + (tb >> 1)) * 16 + (tb & 1) * 8) ^ (i << 5);
+    if (i < NJ) {
+      const int z0 = NJ == 8 ? tz * 512 + zslot(tz, 16 * wr + (tb >> 1)) * 16 : tz * 256 + qslot(tz, 8 * wr + (tb >> 1)) * 16;
+      tq[i < NJ ? i : 0] = L::kQOff + (DW ? (z0 + (tb & 1) * 8) ^ (i << 5) : kWRows * wr * 64 + in);
+    }
   }
-  auto read_tr = [&](const uint8_t* p) {
+  auto read_tr = [&](const uint8_t* p, int four) {   // four: bytes of four rows
     const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p);
-    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 2048));
+    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + four));
     return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
   auto read_p = [&](int s, int i) {
-    if (TURNED) return *(const i32x4*)(smem + ta[i] + (s & 3) * (2 * kBRowsBytes));
-    return read_tr(smem + ta[i] + (FUSED ? kBWOff + (s & 1) * kBRowsBytes : (s & 3) * (2 * kBRowsBytes)));
+    if (TURNED) return *(const i32x4*)(smem + ta[i] + s % L::kRing * L::kSlot);
+    return read_tr(smem + ta[i] + (FUSED ? L::kWOff + (s & 1) * kBPBytes : s % L::kRing * L::kSlot), 2048);
   };
   auto read_q = [&](int s, int j) {
-    if (!DW) return *(const i32x4*)(smem + tq[j] + (s & 3) * (FUSED ? kBRowsBytes : 2 * kBRowsBytes));
-    return read_tr(smem + tq[j] + (s & 3) * (2 * kBRowsBytes));
+    if (!DW) return *(const i32x4*)(smem + tq[j] + s % L::kRing * L::kSlot);
+    return read_tr(smem + tq[j] + s % L::kRing * L::kSlot, 8 * kRows);
   };
   auto mfma = [](const i32x4& x, const i32x4& y, const f32x4& c) {
     if (!DW) return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
   };
 
-  f32x4 acc[8][8];
+  f32x4 acc[8][NJ];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  i32x4 pf[8], qf[8], cw = {0, 0, 0, 0};
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  i32x4 pf[8], qf[NJ], cw = {0, 0, 0, 0};
   f16x2 sc = {0, 0};
+  // Copies that may be under way at a step's middle: those of the steps behind the next (kDx: but for the codes and scale
+  // of the first of them, three copies).
+  constexpr int kAhead = (L::kRing - 2) * kCopies - (FUSED ? 3 : 0);
   if (st1 > st0) {
 #pragma unroll
-    for (int s = 0; s < kBRing; ++s) {
+    for (int s = 0; s < L::kRing; ++s) {
       copy_p(clamp_st(st0 + s), s);
       copy_d(clamp_st(st0 + s), s);
     }
+    // step 0 (kDx: and step 1's codes and scales)
+    __builtin_amdgcn_sched_barrier(0);
+    wait_copies<kAhead + kCopies>();
     if (FUSED) {
-      asm volatile("s_waitcnt vmcnt(18)" ::: "memory");   // step 0, and step 1's codes and scales
 #pragma unroll
       for (int u = 0; u < 3; ++u) {   // all of step 0, half of step 1
         sc = read_scale(u >> 1);
@@ -454,135 +488,148 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
 #pragma unroll
         for (int q = 0; q < 10; ++q) dequant(cw, sc, u >> 1, u & 1, q);
       }
-    } else {
-      asm volatile("s_waitcnt vmcnt(24)" ::: "memory");   // step 0
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (i < 3) pf[i] = read_p(0, i);
-      qf[i] = read_q(0, i);
+      if (i < 3 || NJ == 4) pf[i] = read_p(0, i);
+      if (i < 3 || NJ == 8) qf[i] = read_q(0, i);
     }
   }
-  // one step, the U-th of each four (the ring's places are then constants); true if it was the last
+  // One step, the U-th of each turn of the ring (its places are then constants); true if it was the last.  For kDx the
+  // turn is even, so that the two places of the weights are constants as well.
   auto step = [&](auto U, int64_t st) {
     constexpr int s = decltype(U)::value;
-    const int64_t ahead = clamp_st(st + kBRing);
+    const int64_t ahead = clamp_st(st + L::kRing);
+    constexpr int kParts = NJ / 2;     // quarters or halves
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      if (h == 2) {
-        // under way may be the copies of steps s + 2 (kDx: four of them) and s + 3
-        if (FUSED)
-          asm volatile("s_waitcnt vmcnt(11)" ::: "memory");
-        else
-          asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+    for (int h = 0; h < kParts; ++h) {
+      const bool late = h >= kParts / 2;
+      if (h == kParts / 2) {
+        wait_copies<kAhead>();
         __syncthreads();
       }
-      const int i0 = h == 1 || h == 2 ? 4 : 0, j0 = h >= 2 ? 4 : 0;
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
-        const int i = i0 + x / 4, j = j0 + x % 4;
-        acc[i][j] = mfma(pf[i], qf[j], acc[i][j]);
-        if (h == 0) {
-          if (x == 0) pf[3] = read_p(s, 3);
-          if (x == 2 || x == 5 || x == 8 || x == 11) pf[4 + x / 3] = read_p(s, 4 + x / 3);
-        }
-        if (h == 1 && x % 3 == 0 && x < 12) qf[4 + x / 3] = read_q(s, 4 + x / 3);
-        if (h == 2 && x % 3 == 0 && x < 12) qf[x / 3] = read_q(s + 1, x / 3);
-        if (h == 3 && x % 4 == 0 && x > 0) pf[x / 4 - 1] = read_p(s + 1, x / 4 - 1);
-        if (h == 2 && x == 8) copy_p(ahead, s & 3);
-        if (h == 3 && x == 7) copy_d(ahead, s & 3);
-        if (FUSED) {   // a unit of ten pieces in two quarters
-          const int d = h >= 2 ? s + 2 : s + 1;
-          if ((h == 0 || h == 2) && x == 1) {
-            sc = read_scale(d & 3);
-            cw = read_codes(d & 3, h == 0);
+        if (NJ == 8) {
+          const int i = (h == 1 || h == 2 ? 4 : 0) + x / 4, j = (h >= 2 ? 4 : 0) + x % 4;
+          acc[i][j] = mfma(pf[i], qf[j], acc[i][j]);
+          if (h == 0) {
+            if (x == 0) pf[3] = read_p(s, 3);
+            if (x == 2 || x == 5 || x == 8 || x == 11) pf[4 + x / 3] = read_p(s, 4 + x / 3);
           }
-          const int q = x == 9 ? 0 : x == 10 ? 1 : x == 12 ? 2 : x == 13 ? 3 : x == 15 ? 4 : -1;
-          if (q >= 0) dequant(cw, sc, d & 1, h < 2, q + 5 * (h & 1));
+          if (h == 1 && x % 3 == 0 && x < 12) qf[4 + x / 3] = read_q(s, 4 + x / 3);
+          if (h == 2 && x % 3 == 0 && x < 12) qf[x / 3] = read_q(s + 1, x / 3);
+          if (h == 3 && x % 4 == 0 && x > 0) pf[x / 4 - 1] = read_p(s + 1, x / 4 - 1);
+        } else {
+          const int i = 4 * h + x % 4, j = x / 4;
+          acc[i][j] = mfma(pf[i], qf[j], acc[i][j]);
+          if (h == 0) {
+            if (x == 0) qf[3] = read_q(s, 3);
+            if (x == 2 || x == 5 || x == 8 || x == 11) pf[4 + x / 3] = read_p(s, 4 + x / 3);
+          } else {
+            if (x == 1 || x == 3 || x == 5 || x == 7) pf[x / 2] = read_p(s + 1, x / 2);
+            if (x == 4 || x == 8 || x == 12) qf[x / 4 - 1] = read_q(s + 1, x / 4 - 1);
+          }
+        }
+        if (NJ == 8 ? h == 2 && x == 8 : late && x == 2) copy_p(ahead, s % L::kRing);
+        if (NJ == 8 ? h == 3 && x == 7 : late && x == 10) copy_d(ahead, s % L::kRing);
+        if (FUSED) {   // a unit of ten pieces in two quarters, or in a half
+          const int d = late ? s + 2 : s + 1;
+          if (h % (kParts / 2) == 0 && x == 1) {
+            sc = read_scale(d % L::kRing);
+            cw = read_codes(d % L::kRing, !late);
+          }
+          const int q = NJ == 4 ? (x >= 6 ? x - 6 : -1) : x == 9 ? 0 : x == 10 ? 1 : x == 12 ? 2 : x == 13 ? 3 : x == 15 ? 4 : -1;
+          if (q >= 0) dequant(cw, sc, d & 1, !late, NJ == 4 ? q : q + 5 * (h & 1));
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
     return st + 1 >= st1;
   };
-  for (int64_t st = st0; st < st1; st += 4) {
+  for (int64_t st = st0; st < st1; st += L::kRing) {
     if (step(std::integral_constant<int, 0>(), st) || step(std::integral_constant<int, 1>(), st + 1) ||
-        step(std::integral_constant<int, 2>(), st + 2) || step(std::integral_constant<int, 3>(), st + 3))
+        step(std::integral_constant<int, 2>(), st + 2))
       break;
+    if (L::kRing == 4 && step(std::integral_constant<int, 3>(), st + 3)) break;
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  wait_copies<0>();
 
-  // lane: k = c0 + 128 wk + 16 i + 4 g + (0 .. 3), row r0 + 128 wr + 16 j + r
+  // lane: k = c0 + 128 wk + 16 i + 4 g + (0 .. 3), row r0 + kWRows wr + 16 j + r
   if (!DW) {
     const float cf = a.cols[(128 * wk < c_room ? c0 + 128 * wk : c0) / 128];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t row = r0 + 128 * wr + 16 * j + r;
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t row = r0 + kWRows * wr + 16 * j + r;
       const float rf = a.rs[row < a.rows ? row : a.rows - 1];
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i][j] = acc[i][j] * rf * cf;
     }
   }
   if (work.slot >= 0) {   // a part of a tile's depth, added by gated_join_kernel
-    float* pt = a.part + work.slot * (kBTile * kBTile);
+    float* pt = a.part + work.slot * (kRows * kBCols);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int j = 0; j < NJ; ++j) {
+      const int row = kWRows * wr + 16 * j + r;
+      if (r0 + row >= a.rows) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        *(f32x4*)(pt + (128 * wr + 16 * j + r) * kBTile + 128 * wk + 16 * i + 4 * g) = acc[i][j];
+      for (int i = 0; i < 8; ++i) *(f32x4*)(pt + row * kBCols + 128 * wk + 16 * i + 4 * g) = acc[i][j];
+    }
     return;
   }
   __syncthreads();   // every wave is done with the operands
-  uint8_t* stage = smem + wave * kBStagePerWave;
+  uint8_t* stage = smem + wave * L::kStage;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < NJ; ++j) {
       const f32x4 v = acc[i][j];
       *(uint2*)(stage + (16 * j + r) * kBPitch + (16 * i + 4 * g) * 2) =
           make_uint2(pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3]));
     }
   __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's LDS writes are done
   if (128 * wk >= c_room) return;
-  // the wave's 128 rows lie in one of the two outputs (n is a multiple of 128)
-  const int64_t row0 = r0 + 128 * wr;
+  // the wave's rows lie in one of the two outputs (n is a multiple of 128)
+  const int64_t row0 = r0 + kWRows * wr;
   const int second = DW && row0 >= a.n;
   uint16_t* base = (second ? a.out[1] : a.out[0]) + (second ? row0 - a.n : row0) * a.k + c0 + 128 * wk + (lane & 15) * 8;
 #pragma unroll
-  for (int q = 0; q < 32; ++q) {
+  for (int q = 0; q < 4 * NJ; ++q) {
     const int row = 4 * q + (lane >> 4);
     if (row0 + row < a.rows) *(i32x4*)(base + row * a.k) = *(const i32x4*)(stage + row * kBPitch + (lane & 15) * 16);
   }
 }
 
-template <Kind KIND>
-__global__ __launch_bounds__(kBThreads) void gated_product_kernel(GatedProduct a) {
+template <Kind KIND, int NJ>
+__global__ __launch_bounds__(kBThreads, KIND == kDw && NJ == 4 ? 2 : 1) void gated_product_kernel(GatedProduct a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  gated_product<KIND>(a, blockIdx.x, smem);
+  gated_product<KIND, NJ>(a, blockIdx.x, smem);
 }
-// dx and the weights' gradients side by side: few tokens leave neither enough tiles to fill the chip, and
-// a workgroup of a few steps takes some 12 us, most of it its start and end.
+// dx and the weights' gradients side by side, where neither has enough tiles to fill the chip: a workgroup of a
+// few steps takes some 12 us, most of it its start and end.
+template <int NJ>
 __global__ __launch_bounds__(kBThreads) void gated_both_kernel(GatedProduct dx, GatedProduct dw, unsigned first) {
   extern __shared__ __align__(16) uint8_t smem[];
   if (blockIdx.x < first)
-    gated_product<kDx>(dx, blockIdx.x, smem);
+    gated_product<kDx, NJ>(dx, blockIdx.x, smem);
   else
-    gated_product<kDw>(dw, blockIdx.x - first, smem);
+    gated_product<kDw, 8>(dw, blockIdx.x - first, smem);
 }
 
 // The parts of split tiles added in their order: 4 rows of a tile a workgroup, 4 columns a thread.
 __device__ __forceinline__ void gated_join(const GatedProduct& a, int64_t b) {
-  const int64_t tail = b / 64;
-  const int row = (int)(b % 64) * 4 + (int)(threadIdx.x >> 6);
+  const int64_t per = a.tile_rows / 4, tail = b / per;
+  const int row = (int)(b % per) * 4 + (int)(threadIdx.x >> 6);
   const int col = (int)(threadIdx.x & 63) * 4;
   int64_t tr, tc;
   gemm_group_tile(a.full + tail, a.tiles_r, a.tiles_c, tr, tc);
-  const int64_t rr = tr * kBTile + row, c = tc * kBTile + col;
+  const int64_t rr = tr * a.tile_rows + row, c = tc * kBCols + col;
   if (rr >= a.rows || c >= a.k) return;
-  const float* p = a.part + tail * a.split * (kBTile * kBTile) + row * kBTile + col;
+  const int64_t each = (int64_t)a.tile_rows * kBCols;
+  const float* p = a.part + tail * a.split * each + row * kBCols + col;
   f32x4 v = *(const f32x4*)p;
-  for (int sp = 1; sp < a.split; ++sp) v += *(const f32x4*)(p + (int64_t)sp * (kBTile * kBTile));
+  for (int sp = 1; sp < a.split; ++sp) v += *(const f32x4*)(p + sp * each);
   const int second = rr >= a.n && a.out[1] != a.out[0];
   store4((second ? a.out[1] : a.out[0]) - (second ? a.n * a.k : 0), 0, a.k, rr, c, v, a.k);
 }
@@ -593,27 +640,44 @@ __global__ __launch_bounds__(256) void gated_join_kernel(GatedProduct dx, GatedP
     gated_join(dw, blockIdx.x - first);
 }
 
-// Tiles and how the ones behind the last full round of the chip are split along z.
+// Tiles and how the ones behind the last full round of the chip are split along z.  More than eight parts come in
+// eights, a part of every tile on one XCD.
 struct ProductPlan {
   int64_t tiles_r = 0, tiles_c = 0, full = 0;
-  int32_t split = 1;
+  int32_t split = 1, tile_rows = 256;
   int64_t tail() const { return split > 1 ? tiles_r * tiles_c - full : 0; }
   unsigned grid() const { return (unsigned)(full + tail() * split); }
-  size_t part_bytes() const { return (size_t)tail() * (size_t)split * kBTile * kBTile * 4; }
+  unsigned joins() const { return (unsigned)(tail() * (tile_rows / 4)); }
+  size_t part_bytes() const { return (size_t)tail() * (size_t)split * (size_t)tile_rows * kBCols * 4; }
 };
 constexpr int64_t kBCUs = 256;
-ProductPlan plan_product(int64_t rows, int64_t z, int64_t k) {
+ProductPlan plan_product(int64_t rows, int64_t z, int64_t k, int tile_rows) {
   ProductPlan p;
-  p.tiles_r = (rows + kBTile - 1) / kBTile;
-  p.tiles_c = (k + kBTile - 1) / kBTile;
+  p.tile_rows = tile_rows;
+  p.tiles_r = (rows + tile_rows - 1) / tile_rows;
+  p.tiles_c = (k + kBCols - 1) / kBCols;
   const int64_t tiles = p.tiles_r * p.tiles_c, rem = tiles % kBCUs;
   const int64_t steps = (z + kBStep - 1) / kBStep;
   int64_t sp = rem > 0 && rem <= kBCUs / 2 ? kBCUs / rem : 1;
   if (sp > 32) sp = 32;
   if (sp > steps / 8) sp = steps / 8;
+  if (sp > 8) sp = sp / 8 * 8;
   p.split = (int32_t)(sp > 1 ? sp : 1);
   p.full = p.split > 1 ? tiles - rem : tiles;
   return p;
+}
+ProductPlan plan_dx(int64_t m, int64_t n, int64_t k) { return plan_product(m, 2 * n, k, m <= 128 ? 128 : 256); }
+// The weights' gradients: few steps a tile and more than a round of tiles go two workgroups a CU.
+constexpr int64_t kShallow = 512;
+ProductPlan plan_dw(int64_t m, int64_t n, int64_t k) {
+  const ProductPlan p = plan_product(2 * n, m, k, 256);
+  if (m > kShallow || p.tiles_r * p.tiles_c <= kBCUs) return p;
+  ProductPlan q = p;
+  q.tile_rows = 128;
+  q.tiles_r = 2 * n / 128;
+  q.full = q.tiles_r * q.tiles_c;
+  q.split = 1;
+  return q;
 }
 
 constexpr size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -650,8 +714,8 @@ BwdWs bwd_ws(void* ws, int64_t m, int64_t n, int64_t k) {
   w.d16 = (uint16_t*)take((size_t)m * 2 * n * 2);
   w.db = (uint16_t*)take((size_t)pad_tokens(m) * 2 * n * 2);
   w.w16 = (uint16_t*)take(turned(m) ? (size_t)k * 2 * n * 2 : 0);
-  w.part[0] = (float*)take(plan_product(m, 2 * n, k).part_bytes());
-  w.part[1] = (float*)take(plan_product(2 * n, m, k).part_bytes());
+  w.part[0] = (float*)take(plan_dx(m, n, k).part_bytes());
+  w.part[1] = (float*)take(plan_dw(m, n, k).part_bytes());
   w.bytes = at;
   return w;
 }
@@ -707,10 +771,11 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
     p.tiles_c = plan.tiles_c;
     p.full = plan.full;
     p.split = plan.split;
+    p.tile_rows = plan.tile_rows;
     p.part = part;
   };
   if (a.dx) {
-    px = plan_product(a.m, 2 * a.n, a.k);
+    px = plan_dx(a.m, a.n, a.k);
     planned(dx, px, w.part[0]);
     dx.codes[0] = a.wg;
     dx.codes[1] = a.wu;
@@ -724,7 +789,7 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
     dx.out[0] = dx.out[1] = a.dx;
   }
   if (a.dgate) {
-    pw = plan_product(2 * a.n, a.m, a.k);
+    pw = plan_dw(a.m, a.n, a.k);
     planned(dw, pw, w.part[1]);
     dw.p = a.x;
     dw.xt = w.xt;
@@ -734,28 +799,37 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
     dw.out[0] = a.dgate;
     dw.out[1] = a.dup;
   }
-  auto room = [](auto kernel) {
-    return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kBLds);
+  auto go = [&](auto kernel, int lds, unsigned grid, auto... args) {
+    e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return false;
+    kernel<<<grid, kBThreads, lds, s>>>(args...);
+    return true;
   };
-  if (!turned(a.m) && a.dx && a.dgate) {
-    if ((e = room(gated_both_kernel)) != hipSuccess) return e;
-    gated_both_kernel<<<px.grid() + pw.grid(), kBThreads, kBLds, s>>>(dx, dw, px.grid());
+  constexpr auto most = [](int x, int y) { return x > y ? x : y; };
+  const bool small_dx = px.tile_rows == 128;
+  bool ok = true;
+  if (!turned(a.m) && a.dx && a.dgate && pw.tile_rows == 256) {
+    constexpr int dw8 = Lds<kDw, 8>::kBytes;
+    if (small_dx)
+      ok = go(gated_both_kernel<4>, most(Lds<kDx, 4>::kBytes, dw8), px.grid() + pw.grid(), dx, dw, px.grid());
+    else
+      ok = go(gated_both_kernel<8>, most(Lds<kDx, 8>::kBytes, dw8), px.grid() + pw.grid(), dx, dw, px.grid());
   } else {
     if (a.dx && turned(a.m)) {
-      if ((e = room(gated_product_kernel<kDxT>)) != hipSuccess) return e;
       gated_weights_kernel<<<dim3((unsigned)(a.k / 128), (unsigned)(2 * a.n / 128)), 256, 0, s>>>(a.wg, a.wu, w.tab, a.n, a.k, w.w16);
-      gated_product_kernel<kDxT><<<px.grid(), kBThreads, kBLds, s>>>(dx);
+      ok = go(gated_product_kernel<kDxT, 8>, Lds<kDxT, 8>::kBytes, px.grid(), dx);
+    } else if (a.dx && small_dx) {
+      ok = go(gated_product_kernel<kDx, 4>, Lds<kDx, 4>::kBytes, px.grid(), dx);
     } else if (a.dx) {
-      if ((e = room(gated_product_kernel<kDx>)) != hipSuccess) return e;
-      gated_product_kernel<kDx><<<px.grid(), kBThreads, kBLds, s>>>(dx);
+      ok = go(gated_product_kernel<kDx, 8>, Lds<kDx, 8>::kBytes, px.grid(), dx);
     }
-    if (a.dgate) {
-      if ((e = room(gated_product_kernel<kDw>)) != hipSuccess) return e;
-      gated_product_kernel<kDw><<<pw.grid(), kBThreads, kBLds, s>>>(dw);
-    }
+    if (ok && a.dgate)
+      ok = pw.tile_rows == 128 ? go(gated_product_kernel<kDw, 4>, Lds<kDw, 4>::kBytes, pw.grid(), dw)
+                               : go(gated_product_kernel<kDw, 8>, Lds<kDw, 8>::kBytes, pw.grid(), dw);
   }
-  const unsigned join = (unsigned)((px.tail() + pw.tail()) * 64);
-  if (join) gated_join_kernel<<<join, 256, 0, s>>>(dx, dw, (unsigned)(px.tail() * 64));
+  if (!ok) return e;
+  const unsigned join = px.joins() + pw.joins();
+  if (join) gated_join_kernel<<<join, 256, 0, s>>>(dx, dw, px.joins());
   return hipGetLastError();
 }
 

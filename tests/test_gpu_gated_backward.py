@@ -75,7 +75,7 @@ def _check(ws, dh, gu, x, got):
 @pytest.mark.parametrize("m,n,k", [(1, 128, 128), (5, 256, 384), (31, 128, 256), (32, 384, 128), (33, 128, 640), (100, 256, 256),
                                    (255, 128, 128), (256, 640, 512), (257, 128, 384), (600, 384, 256), (2000, 128, 128),
                                    (7, 4224, 128), (3, 8320, 256), (2, 16512, 128), (64, 2176, 512), (2048, 128, 384),
-                                   (2111, 256, 128)])
+                                   (2111, 256, 128), (40, 2176, 4224), (129, 4224, 2304)])
 @pytest.mark.parametrize("pow2", [False, True])
 def test_gated_backward(m, n, k, pow2):
     print(f"gated backward m={m} n={n} k={k} pow2={pow2}", flush=True)
