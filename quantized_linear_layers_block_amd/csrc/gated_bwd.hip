@@ -273,8 +273,8 @@ struct GatedProduct {
 
 // 16-byte slot of logical slot s in LDS row z (32 slots of 512 bytes).  A transposing read of 32 lanes
 // covers eight rows (z & 3 and bit 3 vary) by 32 bytes, which slot bits 1..3 spread over the banks; a write
-// of 16 lanes to even slots of one row takes odd ones in the row's second half.
-__device__ __forceinline__ int zslot(int z, int s) { return s ^ ((s >> 4) & 1) ^ (2 * ((z & 3) | ((z >> 1) & 4))); }
+// of even slots of one row and the row two below takes odd ones in the second half and in the lower row.
+__device__ __forceinline__ int zslot(int z, int s) { return s ^ (((s >> 4) ^ (z >> 1)) & 1) ^ (2 * ((z & 3) | ((z >> 1) & 4))); }
 
 // The same for rows of 256 bytes (16 slots).
 __device__ __forceinline__ int qslot(int z, int s) { return s ^ (2 * ((z & 3) | ((z >> 1) & 4))); }
@@ -341,14 +341,14 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
   const int wk = wave & 1, wr = wave >> 1;
   const int r = lane & 15, g = lane >> 4;
-  const int64_t steps = (a.z + kBStep - 1) / kBStep;
+  const int steps = (int)((a.z + kBStep - 1) / kBStep);
   const int nsplit = __builtin_amdgcn_readfirstlane(work.nsplit);
-  const int64_t per = (steps + nsplit - 1) / nsplit;
-  const int64_t st0 = part_no * per;
-  const int64_t st1 = st0 + per < steps ? st0 + per : steps;
+  const int per = (steps + nsplit - 1) / nsplit;
+  const int st0 = part_no * per;
+  const int st1 = st0 + per < steps ? st0 + per : steps;
   const int64_t c_room = a.k - c0;         // at least 128
   const int64_t r_last = a.rows - 1 - r0;
-  auto clamp_st = [&](int64_t st) { return st < st1 ? st : st1 - 1; };
+  auto clamp_st = [&](int st) { return st < st1 ? st : st1 - 1; };
   const uint32_t lds0 = lds_addr(smem);
 
   // ---- copies of a step, the same by every wave, from uniform addresses with a lane's 32-bit offsets
@@ -380,27 +380,37 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
     }
     osc = (uint32_t)(col / 128 * 4);
   }
-  const int64_t whole = DW ? a.z / kBStep : steps;   // steps of whole rows of x
-  auto copy_p = [&](int64_t st, int slot) {
+  const int whole = DW ? (int)(a.z / kBStep) : steps;   // steps of whole rows of x
+  // (sizes in 32 bits: a 64-bit product is two scalar instructions then, not seven)
+  const uint32_t k32 = (uint32_t)a.k, rows32 = (uint32_t)a.rows, n32 = (uint32_t)a.n;
+  auto from_p = [&](int st) {
+    const uint32_t z0 = (uint32_t)st * kBStep;
     if (FUSED) {
-      const int64_t z0 = st * kBStep;
-      const int up = z0 >= a.n;
-      lds_copy16x2((up ? a.codes[1] : a.codes[0]) + (up ? z0 - a.n : z0) * a.k + c0 - kUp, op[0], op[1],
-                   lds0 + L::kCodeOff + slot * kBCodeBytes + wave * 2048);
-      lds_copy4((const uint8_t*)(a.tab + (z0 / 128) * (a.k / 128) + c0 / 128), osc,
-                lds0 + L::kScaleOff + slot * kBScaleBytes + wave * 256);
-    } else {
-      const uint16_t* src = TURNED ? a.p + (st * a.k + c0) * kBStep : (st < whole ? a.p + st * kBStep * a.k : a.xt) + c0;
-      lds_copy16x4((const uint8_t*)src - kUp, op[0], op[1], op[2], op[3], lds0 + slot * L::kSlot + wave * 4096);
+      const bool up = z0 >= n32;
+      return (up ? a.codes[1] : a.codes[0]) + (uint64_t)(up ? z0 - n32 : z0) * k32 + c0 - kUp;
     }
+    if (TURNED) return (const uint8_t*)(a.p + ((uint64_t)(uint32_t)st * k32 + c0) * kBStep) - kUp;
+    return (const uint8_t*)((st < whole ? a.p + (uint64_t)z0 * k32 : a.xt) + c0) - kUp;
   };
-  auto copy_d = [&](int64_t st, int slot) {
-    const uint8_t* d = (const uint8_t*)(a.q + (DW ? st * kBStep * a.rows + r0 : (st * a.rows + r0) * kBStep)) - kUp;
+  auto from_d = [&](int st) {
+    return (const uint8_t*)(a.q + (DW ? (uint64_t)((uint32_t)st * kBStep) * rows32 + r0 : ((uint64_t)(uint32_t)st * rows32 + r0) * kBStep)) - kUp;
+  };
+  auto copy_p = [&](const uint8_t* src, int slot) {
+    if (FUSED)
+      lds_copy16x2(src, op[0], op[1], lds0 + L::kCodeOff + slot * kBCodeBytes + wave * 2048);
+    else
+      lds_copy16x4(src, op[0], op[1], op[2], op[3], lds0 + slot * L::kSlot + wave * 4096);
+  };
+  auto copy_sc = [&](int st, int slot) {
+    lds_copy4((const uint8_t*)(a.tab + ((uint32_t)st / (128 / kBStep)) * (k32 / 128) + c0 / 128), osc,
+              lds0 + L::kScaleOff + slot * kBScaleBytes + wave * 256);
+  };
+  auto copy_d = [&](const uint8_t* src, int slot) {
     const uint32_t dst = lds0 + L::kQOff + slot * L::kSlot + wave * 512 * NJ;
     if (NJ == 8)
-      lds_copy16x4(d, od[0], od[1], od[2], od[3], dst);
+      lds_copy16x4(src, od[0], od[1], od[2], od[3], dst);
     else
-      lds_copy16x2(d, od[0], od[1], dst);
+      lds_copy16x2(src, od[0], od[1], dst);
   };
 
   // ---- kDx: the step's weights from codes to f16, 32 a thread, those that the thread itself copied
@@ -474,8 +484,9 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
   if (st1 > st0) {
 #pragma unroll
     for (int s = 0; s < L::kRing; ++s) {
-      copy_p(clamp_st(st0 + s), s);
-      copy_d(clamp_st(st0 + s), s);
+      copy_p(from_p(clamp_st(st0 + s)), s);
+      if (FUSED) copy_sc(clamp_st(st0 + s), s);
+      copy_d(from_d(clamp_st(st0 + s)), s);
     }
     // step 0 (kDx: and step 1's codes and scales)
     __builtin_amdgcn_sched_barrier(0);
@@ -498,10 +509,11 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
   }
   // One step, the U-th of each turn of the ring (its places are then constants); true if it was the last.  For kDx the
   // turn is even, so that the two places of the weights are constants as well.
-  auto step = [&](auto U, int64_t st) {
+  auto step = [&](auto U, int st) {
     constexpr int s = decltype(U)::value;
-    const int64_t ahead = clamp_st(st + L::kRing);
+    const int ahead = clamp_st(st + L::kRing);
     constexpr int kParts = NJ / 2;     // quarters or halves
+    const uint8_t* src = nullptr;
 #pragma unroll
     for (int h = 0; h < kParts; ++h) {
       const bool late = h >= kParts / 2;
@@ -532,8 +544,12 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
             if (x == 4 || x == 8 || x == 12) qf[x / 4 - 1] = read_q(s + 1, x / 4 - 1);
           }
         }
-        if (NJ == 8 ? h == 2 && x == 8 : late && x == 2) copy_p(ahead, s % L::kRing);
-        if (NJ == 8 ? h == 3 && x == 7 : late && x == 10) copy_d(ahead, s % L::kRing);
+        // the copies of step s + kRing, their addresses a few places before
+        if (NJ == 8 ? h == 2 && x == 1 : late && x == 0) src = from_p(ahead);
+        if (NJ == 8 ? h == 2 && x == 5 : late && x == 2) copy_p(src, s % L::kRing);
+        if (FUSED && (NJ == 8 ? h == 2 && x == 14 : late && x == 5)) copy_sc(ahead, s % L::kRing);
+        if (NJ == 8 ? h == 3 && x == 2 : late && x == 9) src = from_d(ahead);
+        if (NJ == 8 ? h == 3 && x == 7 : late && x == 11) copy_d(src, s % L::kRing);
         if (FUSED) {   // a unit of ten pieces in two quarters, or in a half
           const int d = late ? s + 2 : s + 1;
           if (h % (kParts / 2) == 0 && x == 1) {
@@ -548,7 +564,7 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
     }
     return st + 1 >= st1;
   };
-  for (int64_t st = st0; st < st1; st += L::kRing) {
+  for (int st = st0; st < st1; st += L::kRing) {
     if (step(std::integral_constant<int, 0>(), st) || step(std::integral_constant<int, 1>(), st + 1) ||
         step(std::integral_constant<int, 2>(), st + 2))
       break;
