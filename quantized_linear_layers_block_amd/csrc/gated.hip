@@ -11,7 +11,8 @@
 //   more than 64 tokens  tiles of 128 columns (256 weight rows) by 256 or 128 tokens: the FP8
 //                        GEMMs' tiling (gemm_fp8.hip) with its two ways of applying scales, whose
 //                        128 columns are one segment of the 8-bit output
-//   up to 64 tokens      bound by the weights: 16 or 32 columns a workgroup, K split over its waves
+//   up to 64 tokens      bound by the weights: 16 to 64 columns a workgroup
+#include <type_traits>
 #include "common.hpp"
 #include "fp8_out.hpp"
 #include "gemm_common.hpp"
@@ -484,126 +485,32 @@ __global__ __launch_bounds__(kGpThreads) void gated_pow2_kernel(Gated a) {
 }
 
 // ------------------------------------------------------------------ up to 64 tokens
-// Bound by the weights, which are read once, straight into the MFMA's fragments: a lane's 32 bytes
-// of a K block (row lane % 16, bytes 32 (lane / 16) ..), four lanes to a whole 128-byte line.  A
-// workgroup has RT x 16 rows of each projection and MT x 16 tokens, and its eight waves take the K
-// blocks in turn; their sums are added in wave order through LDS.  An 8-bit output needs 128 columns:
-// the workgroups of a segment leave float32 values in the workspace, and the last to arrive (an
-// integer counter, returned to zero) quantizes them.
-constexpr int kFewWaves = 8, kFewThreads = kFewWaves * kWave;
+// Bound by the weights, which are read once.  A workgroup has 16, 32 or 64 columns of h, so an 8-bit output's
+// segment of 128 columns comes from several: they leave float32 values in the workspace, and the last to arrive
+// (an integer counter, returned to zero) quantizes them.
+//   gated_few_kernel   16 columns; eight waves take the K blocks in turn and read weights and tokens straight
+//                      into the MFMA's fragments.  For narrow projections, where K has to be split to have waves
+//                      enough: 4096 x 4096, one token 11.2 us, 64 tokens 24 (float32 scales; wide: 17.3, 31).
+//   gated_wide_kernel  32 or 64 columns, each wave 16 weight rows and all of K, tokens shared through LDS.  Read
+//                      into each wave's fragments, 64 tokens cost more than the weights: 14336 x 4096 28.8 us
+//                      against 65 (powers of two), 35 against 83 (float32); one token 24 against 28.
+constexpr int kFewWaves = 8;
 
-template <int MT, int RT, bool POW2>
-__global__ __launch_bounds__(kFewThreads) void gated_few_kernel(Gated a) {
-  __shared__ __align__(16) f32x4 part[4 * 2 * MT * RT * kWave];
-  __shared__ int last;
+// What follows a workgroup's sums: the outputs of 16 RT columns from n0 on.  part: [copies][2 RT MT pieces][lane],
+// the copies' sums to be added, the pieces those of g and then of u; `last` is one word of LDS.
+template <int MT, int RT, int COPIES, int WAVES, bool POW2>
+__device__ __forceinline__ void few_finish(const Gated& a, int64_t n0, const f32x4* part, int* last) {
+  constexpr int kTiles = 2 * RT * MT, kFewThreads = WAVES * kWave;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
   const int r = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
-  const int64_t kblocks = a.k / 128;
   const int64_t nb = n0 / 128;
-  const uint8_t* gp = a.wg + (n0 + r) * a.k + 32 * g;
-  const uint8_t* up = a.wu + (n0 + r) * a.k + 32 * g;
-  int64_t xrow[MT];
-#pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int64_t row = 16 * j + r;
-    xrow[j] = row < a.m ? row : a.m - 1;
-  }
-  f32x4 acc[2][RT][MT];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < MT; ++j) acc[h][i][j] = f32x4{0, 0, 0, 0};
-
-  auto load32 = [](const uint8_t* p) {
-    const i32x4 lo = *(const i32x4*)p, hi = *(const i32x4*)(p + 16);
-    return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-  };
-  for (int64_t kb = wave; kb < kblocks; kb += kFewWaves) {
-    i32x8 wf[2][RT], xf[MT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      wf[0][i] = load32(gp + (int64_t)16 * i * a.k + kb * 128);
-      wf[1][i] = load32(up + (int64_t)16 * i * a.k + kb * 128);
-    }
-#pragma unroll
-    for (int j = 0; j < MT; ++j) xf[j] = load32(a.xq + xrow[j] * a.k + kb * 128 + 32 * g);
-    if (POW2) {
-      const int sw[2] = {((const uint8_t*)a.sg)[nb * kblocks + kb], ((const uint8_t*)a.su)[nb * kblocks + kb]};
-      int sx[MT];
-#pragma unroll
-      for (int j = 0; j < MT; ++j) sx[j] = ((const uint8_t*)a.sx)[xrow[j] * kblocks + kb];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int j = 0; j < MT; ++j)
-            acc[h][i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[h][i], xf[j], acc[h][i][j], 0, 0, 0, sw[h], 0, sx[j]);
-    } else {
-      const float sw[2] = {((const float*)a.sg)[nb * kblocks + kb], ((const float*)a.su)[nb * kblocks + kb]};
-      float sx[MT];
-#pragma unroll
-      for (int j = 0; j < MT; ++j) sx[j] = ((const float*)a.sx)[xrow[j] * kblocks + kb];
-      f32x4 p[2][RT][MT];
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        f16x8 x16[MT];
-#pragma unroll
-        for (int j = 0; j < MT; ++j) x16[j] = e4m3_f16x8(xf[j][2 * kk], xf[j][2 * kk + 1]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            const f16x8 w16 = e4m3_f16x8(wf[h][i][2 * kk], wf[h][i][2 * kk + 1]);
-#pragma unroll
-            for (int j = 0; j < MT; ++j)
-              p[h][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w16, x16[j], kk ? p[h][i][j] : f32x4{0, 0, 0, 0}, 0, 0, 0);
-          }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int j = 0; j < MT; ++j) {
-            acc[h][i][j] += p[h][i][j] * (sw[h] * sx[j]);
-          }
-    }
-  }
-
-  // waves 4..7 hand their sums to waves 0..3, then all four to everybody
-  constexpr int kTiles = 2 * RT * MT;
-  auto put = [&](int w) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j) part[(w * kTiles + (h * RT + i) * MT + j) * kWave + lane] = acc[h][i][j];
-  };
-  if (wave >= 4) put(wave - 4);
-  __syncthreads();
-  if (wave < 4) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j) acc[h][i][j] += part[(wave * kTiles + (h * RT + i) * MT + j) * kWave + lane];
-  }
-  __syncthreads();
-  if (wave < 4) put(wave);
-  __syncthreads();
   __amdgpu_buffer_rsrc_t hs = dev_rsrc(a.scratch);
-  for (int t = wave; t < RT * MT; t += kFewWaves) {   // one 16 x 16 piece of h a wave
+  for (int t = wave; t < RT * MT; t += WAVES) {   // one 16 x 16 piece of h a wave
     const int i = t / MT, j = t % MT;
     f32x4 gv = {0, 0, 0, 0}, uv = gv, hv;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < COPIES; ++w) {
       gv += part[(w * kTiles + i * MT + j) * kWave + lane];
       uv += part[(w * kTiles + (RT + i) * MT + j) * kWave + lane];
     }
@@ -629,11 +536,11 @@ __global__ __launch_bounds__(kFewThreads) void gated_few_kernel(Gated a) {
   if (threadIdx.x == 0) {
     uint32_t* cnt = a.counters + nb;
     const uint32_t old = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = old == kArrive - 1;
-    if (last) st_dev_u32(cnt, 0u);
+    *last = old == kArrive - 1;
+    if (*last) st_dev_u32(cnt, 0u);
   }
   __syncthreads();
-  if (!last) return;
+  if (!*last) return;
   // 32 lanes a token, 4 columns each
   const int c4 = threadIdx.x & 31;
   for (int64_t row = threadIdx.x >> 5; row < a.m; row += kFewThreads / 32) {
@@ -652,6 +559,211 @@ __global__ __launch_bounds__(kFewThreads) void gated_few_kernel(Gated a) {
         ((uint32_t*)a.sh)[seg] = sc.stored;
     }
   }
+}
+
+template <int MT, bool POW2>
+__global__ __launch_bounds__(kFewWaves * kWave) void gated_few_kernel(Gated a) {
+  __shared__ __align__(16) f32x4 part[4 * 2 * MT * kWave];
+  __shared__ int last;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t kblocks = a.k / 128;
+  const int64_t nb = n0 / 128;
+  const uint8_t* gp = a.wg + (n0 + r) * a.k + 16 * g;
+  const uint8_t* up = a.wu + (n0 + r) * a.k + 16 * g;
+  int64_t xrow[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int64_t row = 16 * j + r;
+    xrow[j] = row < a.m ? row : a.m - 1;
+  }
+  f32x4 acc[2][MT];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[h][j] = f32x4{0, 0, 0, 0};
+
+  auto load32 = [](const uint8_t* p) {
+    const i32x4 lo = *(const i32x4*)p, hi = *(const i32x4*)(p + 64);
+    return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+  for (int64_t kb = wave; kb < kblocks; kb += kFewWaves) {
+    const i32x8 wf[2] = {load32(gp + kb * 128), load32(up + kb * 128)};
+    i32x8 xf[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) xf[j] = load32(a.xq + xrow[j] * a.k + kb * 128 + 16 * g);
+    if (POW2) {
+      const int sw[2] = {((const uint8_t*)a.sg)[nb * kblocks + kb], ((const uint8_t*)a.su)[nb * kblocks + kb]};
+      int sx[MT];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) sx[j] = ((const uint8_t*)a.sx)[xrow[j] * kblocks + kb];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+          acc[h][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[h], xf[j], acc[h][j], 0, 0, 0, sw[h], 0, sx[j]);
+    } else {
+      const float sw[2] = {((const float*)a.sg)[nb * kblocks + kb], ((const float*)a.su)[nb * kblocks + kb]};
+      float sx[MT];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) sx[j] = ((const float*)a.sx)[xrow[j] * kblocks + kb];
+      f32x4 p[2][MT];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        f16x8 x16[MT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) x16[j] = e4m3_f16x8(xf[j][2 * kk], xf[j][2 * kk + 1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f16x8 w16 = e4m3_f16x8(wf[h][2 * kk], wf[h][2 * kk + 1]);
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+            p[h][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w16, x16[j], kk ? p[h][j] : f32x4{0, 0, 0, 0}, 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[h][j] += p[h][j] * (sw[h] * sx[j]);
+    }
+  }
+
+  // waves 4..7 hand their sums to waves 0..3, then all four to everybody
+  auto put = [&](int w) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) part[((w * 2 + h) * MT + j) * kWave + lane] = acc[h][j];
+  };
+  if (wave >= 4) put(wave - 4);
+  __syncthreads();
+  if (wave < 4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[h][j] += part[((wave * 2 + h) * MT + j) * kWave + lane];
+  }
+  __syncthreads();
+  if (wave < 4) put(wave);
+  __syncthreads();
+  few_finish<MT, 1, 4, kFewWaves, POW2>(a, n0, part, &last);
+}
+
+// A ring of three K blocks (two under way: 4 to 6 were equal or, with fewer workgroups a CU, slower).  Every
+// workgroup begins at another K block: with all of them at one, rows of 4096 bytes lie in the same few channels
+// of the memory (14336 x 4096, one token: 28.3 -> 23.8 us; 18944 x 3584: alike).  The order of a sum is a matter
+// of n0 and k alone.  Scales come in panels of 16 blocks.
+constexpr int kWidePanel = 16, kWideRing = 3;
+template <int MT, int WAVES, bool POW2>
+constexpr size_t wide_panel() { return kWidePanel * (16 * MT + 2) * (POW2 ? 1 : 4); }
+template <int MT, int WAVES, bool POW2>
+constexpr size_t wide_lds() { return kWideRing * (16 * WAVES + 16 * MT) * kGRowBytes + wide_panel<MT, WAVES, POW2>() + 64; }
+
+template <int MT, int WAVES, bool POW2>
+__global__ __launch_bounds__(WAVES * kWave) void gated_wide_kernel(Gated a) {
+  using S = typename std::conditional<POW2, uint8_t, float>::type;
+  constexpr int RING = kWideRing, kStage = (16 * WAVES + 16 * MT) * kGRowBytes, kRT = WAVES / 2;
+  extern __shared__ __align__(16) uint8_t smem[];
+  S* const sxp = (S*)(smem + RING * kStage);
+  S* const swp = sxp + kWidePanel * 16 * MT;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int r = lane & 15, g = lane >> 4;
+  const bool up = wave >= kRT;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * kRT);
+  const int kblocks = (int)(a.k / 128);
+  const int first = (int)(blockIdx.x * 5 % kblocks);
+  auto at = [&](int t) { return t + first < kblocks ? t + first : t + first - kblocks; };
+  const S* sxs = (const S*)a.sx;
+  const S* sgs = (const S*)a.sg + n0 / 128 * kblocks;
+  const S* sus = (const S*)a.su + n0 / 128 * kblocks;
+
+  const uint8_t* wbase = up ? a.wu + (n0 + 16 * (wave - kRT)) * a.k : a.wg + (n0 + 16 * wave) * a.k;
+  constexpr int kX = 2 * MT / WAVES, kOdd = 2 * MT % WAVES;
+  uint32_t ow[2], ox[kX + 1];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int row = 8 * q + (lane >> 3);
+    ow[q] = (uint32_t)row * (uint32_t)a.k + (uint32_t)swz(row, lane & 7) * 16;
+  }
+#pragma unroll
+  for (int q = 0; q <= kX; ++q) {
+    const int row = 8 * (wave + WAVES * q) + (lane >> 3);
+    ox[q] = (uint32_t)(row < a.m ? row : a.m - 1) * (uint32_t)a.k + (uint32_t)swz(row, lane & 7) * 16;
+  }
+  auto copy = [&](int t, int slot) {
+    const int64_t kb = at(t);
+    const uint32_t lb = lds_addr(smem + slot * kStage);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) lds_copy16(wbase + kb * 128, ow[q], lb + (16 * wave + 8 * q) * kGRowBytes);
+#pragma unroll
+    for (int q = 0; q <= kX; ++q)
+      if (q < kX || wave < kOdd) lds_copy16(a.xq + kb * 128, ox[q], lb + (16 * WAVES + 8 * (wave + WAVES * q)) * kGRowBytes);
+  };
+  f32x4 acc[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) acc[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int t = 0; t < RING - 1; ++t)
+    if (t < kblocks) copy(t, t);
+  int slot = 0;
+  for (int t = 0; t < kblocks; ++t) {
+    if (t % kWidePanel == 0) {
+      if (t) __syncthreads();
+      for (int e = threadIdx.x; e < kWidePanel * (16 * MT + 2); e += WAVES * kWave) {
+        const int row = e / kWidePanel, b = e % kWidePanel;
+        if (t + b >= kblocks) continue;
+        const int kb = at(t + b);
+        if (row < 16 * MT)
+          sxp[b * 16 * MT + row] = sxs[(row < a.m ? row : a.m - 1) * (int64_t)kblocks + kb];
+        else
+          swp[2 * b + row - 16 * MT] = row == 16 * MT ? sgs[kb] : sus[kb];
+      }
+    }
+    if (t + RING - 2 < kblocks) {
+      if (wave < kOdd)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((RING - 2) * (3 + kX)) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((RING - 2) * (2 + kX)) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    __syncthreads();
+    if (t + RING - 1 < kblocks) copy(t + RING - 1, slot == 0 ? RING - 1 : slot - 1);
+    const uint8_t* As = smem + slot * kStage;
+    slot = slot == RING - 1 ? 0 : slot + 1;
+    const i32x8 wf = gated_frag(As, 16 * wave + r, g);
+    const S* sp = sxp + (t % kWidePanel) * 16 * MT + r;
+    const S sw = swp[2 * (t % kWidePanel) + up];
+    if constexpr (POW2) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        const i32x8 xf = gated_frag(As + 16 * WAVES * kGRowBytes, 16 * j + r, g);
+        acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, acc[j], 0, 0, 0, (int)sw, 0, (int)sp[16 * j]);
+      }
+    } else {
+      f16x8 w16[4];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) w16[kk] = e4m3_f16x8(wf[2 * kk], wf[2 * kk + 1]);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        const i32x8 xf = gated_frag(As + 16 * WAVES * kGRowBytes, 16 * j + r, g);
+        f32x4 p = {0, 0, 0, 0};
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w16[kk], e4m3_f16x8(xf[2 * kk], xf[2 * kk + 1]), p, 0, 0, 0);
+        acc[j] += p * (sw * sp[16 * j]);
+      }
+    }
+  }
+  __syncthreads();
+  f32x4* part = (f32x4*)smem;   // the ring is free
+#pragma unroll
+  for (int j = 0; j < MT; ++j) part[(wave * MT + j) * kWave + lane] = acc[j];
+  __syncthreads();
+  few_finish<MT, kRT, 1, WAVES, POW2>(a, n0, part, (int*)(smem + wide_lds<MT, WAVES, POW2>() - 64));
 }
 
 // The parts of K added in their order, and what the tiles' epilogue does: 32 lanes a segment of 128 columns.
@@ -696,22 +808,40 @@ __global__ __launch_bounds__(256) void gated_join_kernel(Gated a) {
 }
 
 constexpr int64_t kFewM = 64;
+constexpr int64_t kGCUs = 256;
 
-template <int MT, int RT>
+// Up to 64 tokens: the wide kernel from 8192 columns on, where each CU has a workgroup, and above 16 tokens from
+// 5120 on (5120 x 2048: 16 tokens 11.0 us against the other's 10.9, 64 tokens 15.3 against 19.8; 8192 x 4096:
+// one token 18.2 against 17.7, 64 tokens 24 against 36).  Of its two widths the one that leaves the fullest CU
+// less; if they do alike, the greater, which reads the tokens half as often (powers of two, 64 tokens: 14336 x 4096
+// 28.8 us against 33.4, 28672 x 4096 50 against 64; 48 tokens, 18944 x 3584 38.0 against 36.9).
+template <int MT>
 hipError_t launch_few(const Gated& a, hipStream_t s) {
-  const unsigned grid = (unsigned)(a.n / (16 * RT));
-  if (a.pow2)
-    gated_few_kernel<MT, RT, true><<<grid, kFewThreads, 0, s>>>(a);
-  else
-    gated_few_kernel<MT, RT, false><<<grid, kFewThreads, 0, s>>>(a);
-  return hipGetLastError();
+  if (a.n < (a.m > 16 ? 20 : 32) * kGCUs) {
+    const unsigned grid = (unsigned)(a.n / 16);
+    if (a.pow2)
+      gated_few_kernel<MT, true><<<grid, kFewWaves * kWave, 0, s>>>(a);
+    else
+      gated_few_kernel<MT, false><<<grid, kFewWaves * kWave, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  auto go = [&](auto kernel, int waves, size_t lds) {
+    hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    kernel<<<(unsigned)(a.n / (8 * waves)), waves * kWave, lds, s>>>(a);
+    return hipGetLastError();
+  };
+  if ((a.n / 32 + kGCUs - 1) / kGCUs < 2 * ((a.n / 64 + kGCUs - 1) / kGCUs))
+    return a.pow2 ? go(gated_wide_kernel<MT, 4, true>, 4, wide_lds<MT, 4, true>())
+                  : go(gated_wide_kernel<MT, 4, false>, 4, wide_lds<MT, 4, false>());
+  return a.pow2 ? go(gated_wide_kernel<MT, 8, true>, 8, wide_lds<MT, 8, true>())
+                : go(gated_wide_kernel<MT, 8, false>, 8, wide_lds<MT, 8, false>());
 }
 
 // How more than 64 tokens are cut.  Tiles that cannot fill the chip are taken small, and if K is long, cut along
 // it: a tile's time then is that of its copies' latency, block by block.  Otherwise the height with the least
 // time for all rounds of the chip, a tile's time being its tokens and a share for the weights, which every
 // height reads and converts alike.
-constexpr int64_t kGCUs = 256;
 constexpr int64_t kGWeightShare = 64;
 struct GatedPlan {
   int tm;
@@ -784,10 +914,10 @@ size_t gated_scratch_bytes(int64_t m, int64_t n, int64_t k) {
 hipError_t launch_gated(Gated a, hipStream_t s) {
   if (!gated_launchable(a.m, a.n, a.k)) return hipErrorInvalidValue;
   a.split = 1;
-  if (a.m <= 16) return launch_few<1, 1>(a, s);
-  if (a.m <= 32) return launch_few<2, 1>(a, s);
-  if (a.m <= 48) return launch_few<3, 2>(a, s);
-  if (a.m <= kFewM) return launch_few<4, 2>(a, s);
+  if (a.m <= 16) return launch_few<1>(a, s);
+  if (a.m <= 32) return launch_few<2>(a, s);
+  if (a.m <= 48) return launch_few<3>(a, s);
+  if (a.m <= kFewM) return launch_few<4>(a, s);
   const GatedPlan p = plan_gated(a.m, a.n, a.k, a.pow2);
   a.split = p.split;
   a.blocks_each = p.blocks_each;

@@ -113,6 +113,38 @@ def test_gated_forward(m, n, k, pow2):
     _check(m, n, k, pow2, m * 3 + n + k)
 
 
+# up to 64 tokens on wide projections: both widths of a workgroup, from 8192 columns and (above 16 tokens) from
+# 5120 on; K of one block, fewer than the ring's, and around the panels of 16 blocks' scales
+@pytest.mark.parametrize("m,n,k", [(1, 8192, 128), (16, 8192, 256), (5, 8320, 384), (17, 5120, 2048), (33, 5248, 2176),
+                                   (64, 8192, 640), (48, 8320, 4224), (64, 14336, 512), (2, 8192, 2176), (32, 8320, 128),
+                                   (16, 5120, 256), (17, 4992, 256)])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_gated_forward_wide(m, n, k, pow2):
+    print(f"gated wide m={m} n={n} k={k} pow2={pow2}", flush=True)
+    _check(m, n, k, pow2, m * 3 + n + k)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+def test_special_values_wide(pow2):
+    """A NaN token and a NaN weight row stay in their row and their column; zeros stay zeros."""
+    print(f"gated special wide pow2={pow2}", flush=True)
+    m, n, k = 40, 8192, 384
+    w, x = _case(m, n, k, pow2, 78)
+    w[1][0][7000] = 0
+    w[0][0][130, 3] = 0x7F               # NaN in one gate row
+    x[0][39] = 0
+    x[0][3, 200] = 0xFF                  # NaN in one token
+    gate, up = _weights(w, n, k, pow2)
+    h = ql.gated_forward(gate, up, _dev(x[0]), _dev(x[1]))
+    nan = torch.isnan(h)
+    assert nan[3].all() and nan[:, 130].all()
+    nan[3] = False
+    nan[:, 130] = False
+    assert not nan.any()
+    rest = torch.arange(m, device=DEV) != 3
+    assert not h[rest, 7000].any() and not h[39, torch.arange(n, device=DEV) != 130].any()
+
+
 @pytest.mark.parametrize("pow2", [False, True])
 def test_one_workspace_for_every_size(pow2):
     print(f"gated workspace pow2={pow2}", flush=True)
