@@ -347,21 +347,26 @@ __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
 }
 
 // ------------------------------------------------------------------ powers of two, many tokens
-// The MFMA applies E8M0 scales itself and accumulates in place: four waves, 2 along n by 2 along m, as
-// in gemm_fp8_pow2_kernel.
-constexpr int kGpThreads = 256;
+// The MFMA applies E8M0 scales itself and accumulates in place: eight waves, 2 along n by 4 along m, so that one
+// wave's epilogue runs beside the other's of its SIMD (four waves of twice the sums spilled 97 registers there:
+// 8192 x 14336 x 512 546 us against 180, x 4096 1073 against 760).  K blocks are copied one ahead, two ahead where
+// LDS has the room: a tile of 64 or 128 tokens has less work in a block than a copy takes (n = 16384, K 5120, 128
+// tokens a tile: 258 -> 180 us; 64: 226 -> 148).
+constexpr int kGpThreads = 512;
+template <int TM>
+constexpr int gp_stages() { return TM == 256 ? 2 : 3; }
 template <int TM>
 constexpr int gp_ring() { return TM * 4 + 256; }
 template <int TM>
 constexpr size_t gp_lds() {
-  constexpr size_t loop = 2 * (kGRows + TM) * kGRowBytes + 2 * gp_ring<TM>(), out = TM * kGPitch + 2 * TM * 4;
+  constexpr size_t loop = gp_stages<TM>() * (kGRows + TM) * kGRowBytes + 2 * gp_ring<TM>(), out = TM * kGPitch + 2 * TM * 4;
   return loop > out ? loop : out;
 }
 
 template <int TM, bool SW4>
 __global__ __launch_bounds__(kGpThreads) void gated_pow2_kernel(Gated a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int MJ = TM / 32;
+  constexpr int MJ = TM / 64, NX = TM / 64, AHEAD = gp_stages<TM>() - 1;
   constexpr int kStage = (kGRows + TM) * kGRowBytes;
   const GatedWork work = gated_work(a);
   const int64_t tn = work.tn, n0 = tn * kGCols, m0 = work.tm * TM;
@@ -371,30 +376,27 @@ __global__ __launch_bounds__(kGpThreads) void gated_pow2_kernel(Gated a) {
   const int r = lane & 15, g = lane >> 4;
   const int64_t kblocks = a.k / 128;
 
-  // Copies of a K block: q < 8 the LDS weight rows 32 q + 8 wave + lane / 8, which are rows 64 (q / 4) +
-  // 32 (q % 2) + 8 wave + lane / 8 of the gate (q % 4 < 2) or of the up projection; q >= 8 the tokens
-  // 32 (q - 8) + 8 wave + lane / 8.
-  uint32_t ow[4], ox[MJ];
+  // Copies of a K block, each 64 LDS rows: gate, up, gate and up rows, then tokens.
+  uint32_t ow[2], ox[NX];
   const int64_t m_last = a.m - 1 - m0;
+  const int crow = 8 * wave + (lane >> 3);
+  const uint32_t chunk = (uint32_t)swz(crow, lane & 7) * 16;   // (that of any row 64 further, too)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 32 * i + 8 * wave + (lane >> 3);   // (its swizzle is that of any row 32 further, too)
-    ow[i] = (uint32_t)row * (uint32_t)a.k + (uint32_t)swz(row, lane & 7) * 16;
-  }
+  for (int i = 0; i < 2; ++i) ow[i] = (uint32_t)(64 * i + crow) * (uint32_t)a.k + chunk;
 #pragma unroll
-  for (int i = 0; i < MJ; ++i) {
-    const int row = 32 * i + 8 * wave + (lane >> 3);
-    ox[i] = (uint32_t)(row < m_last ? row : m_last) * (uint32_t)a.k + (uint32_t)swz(row, lane & 7) * 16;
+  for (int i = 0; i < NX; ++i) {
+    const int row = 64 * i + crow;
+    ox[i] = (uint32_t)(row < m_last ? row : m_last) * (uint32_t)a.k + chunk;
   }
   const uint8_t* gbase = a.wg + n0 * a.k;
   const uint8_t* ubase = a.wu + n0 * a.k;
   const uint8_t* xbase = a.xq + m0 * a.k;
   auto dma = [&](int64_t kb, int buf, int q) {
-    const uint32_t lb = lds_addr(smem + buf * kStage) + 8 * wave * kGRowBytes;
-    if (q < 8)
-      lds_copy16((q & 2 ? ubase : gbase) + kb * 128, ow[2 * (q >> 2) + (q & 1)], lb + 32 * q * kGRowBytes);
+    const uint32_t lb = lds_addr(smem + buf * kStage) + (64 * q + 8 * wave) * kGRowBytes;
+    if (q < 4)
+      lds_copy16((q & 1 ? ubase : gbase) + kb * 128, ow[q >> 1], lb);
     else
-      lds_copy16(xbase + kb * 128, ox[q - 8], lb + (kGRows + 32 * (q - 8)) * kGRowBytes);
+      lds_copy16(xbase + kb * 128, ox[q - 4], lb);
   };
   const uint8_t* sxb = (const uint8_t*)a.sx + m0 * kblocks;
   const uint8_t* sgb = (const uint8_t*)a.sg + tn * kblocks;
@@ -406,7 +408,7 @@ __global__ __launch_bounds__(kGpThreads) void gated_pow2_kernel(Gated a) {
     osx[j] = (uint32_t)((row < m_last ? row : m_last) * kblocks);
   }
   // SW4 (K a multiple of 512, 4-byte aligned arrays): the bytes of four blocks are one word, in a ring of two
-  constexpr int kRing = 2 * kStage;
+  constexpr int kRing = gp_stages<TM>() * kStage;
   const int arow = 64 * wave + lane;
   const uint32_t oxw = (uint32_t)((arow < m_last ? arow : m_last) * kblocks);
   auto dma_sc = [&](int64_t grp) {
@@ -436,7 +438,9 @@ __global__ __launch_bounds__(kGpThreads) void gated_pow2_kernel(Gated a) {
 #pragma unroll
     for (int j = 0; j < MJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-  for (int q = 0; q < 8 + MJ; ++q) dma(work.kb0, 0, q);
+  for (int t = 0; t < AHEAD; ++t)
+#pragma unroll
+    for (int q = 0; q < 4 + NX; ++q) dma(work.kb0 + t < work.kb1 ? work.kb0 + t : work.kb1 - 1, t, q);
   if (SW4) dma_sc(work.kb0 >> 2);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
@@ -448,39 +452,43 @@ __global__ __launch_bounds__(kGpThreads) void gated_pow2_kernel(Gated a) {
 #pragma unroll
   for (int j = 0; j < MJ; ++j) bf[j] = gated_frag(smem + kGRows * kGRowBytes, 16 * MJ * wm + 16 * j + r, g);
   af = gated_frag(smem, 128 * wn + r, g);
+  int buf = 0;
   for (int64_t kb = work.kb0; kb < work.kb1; ++kb) {
-    const int buf = (int)((kb - work.kb0) & 1);
     const int64_t kn = kb + 1 < work.kb1 ? kb + 1 : kb;
+    const int64_t kc = kb + AHEAD < work.kb1 ? kb + AHEAD : work.kb1 - 1;   // (past the last: into a slot not read again)
+    const int bufn = buf == AHEAD ? 0 : buf + 1, bufc = buf == 0 ? AHEAD : buf - 1;
     if (SW4 && ((kb + 2) & 3) == 0 && kb + 2 < work.kb1) dma_sc((kb + 2) >> 2);
     next_sc(kn);
     const uint8_t* As = smem + buf * kStage;
-    const uint8_t* An = smem + (buf ^ 1) * kStage;
+    const uint8_t* An = smem + bufn * kStage;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i == 7) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        // all but this block's own copies, if those are for the block after the next
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(AHEAD == 2 ? 4 + NX : 0) : "memory");
         __syncthreads();
       }
 #pragma unroll
       for (int j = 0; j < MJ; ++j) {
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af, bf[j], acc[i][j], 0, 0, 0, i < 4 ? sg : su, 0, sb[j]);
         if (j == 0) afn = i < 7 ? gated_frag(As, 128 * wn + 16 * (i + 1) + r, g) : gated_frag(An, 128 * wn + r, g);
-        if (MJ == 8) {
-          if (i < 4 && (j & 1)) dma(kn, buf ^ 1, 4 * i + (j >> 1));
-        } else if (j == MJ - 1 && 2 * i < 8 + MJ) {
-          dma(kn, buf ^ 1, 2 * i);
-          dma(kn, buf ^ 1, 2 * i + 1);
+        if (MJ == 4) {
+          if (i < 4 && (j == 1 || j == 2)) dma(kc, bufc, 2 * i + j - 1);
+        } else if (j == MJ - 1 && i < 4 + NX) {
+          dma(kc, bufc, i);
         }
         if (i == 7) bf[j] = gated_frag(An + kGRows * kGRowBytes, 16 * MJ * wm + 16 * j + r, g);
         __builtin_amdgcn_sched_barrier(0);
       }
       af = afn;
     }
+    buf = bufn;
     sg = sgn;
     su = sun;
 #pragma unroll
     for (int j = 0; j < MJ; ++j) sb[j] = sbn[j];
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // copies still under way into what gated_store writes
   gated_store<kGpThreads, TM, MJ>(a, acc, work.split, m0, n0, wn, 16 * MJ * wm, r, g, smem, (uint32_t*)(smem + TM * kGPitch));
 }
 
@@ -841,8 +849,8 @@ hipError_t launch_few(const Gated& a, hipStream_t s) {
 // How more than 64 tokens are cut.  Tiles that cannot fill the chip are taken small, and if K is long, cut along
 // it: a tile's time then is that of its copies' latency, block by block.  Otherwise the height with the least
 // time for all rounds of the chip, a tile's time being its tokens and a share for the weights, which every
-// height reads and converts alike.
-constexpr int64_t kGWeightShare = 64;
+// height reads (and, with float32 scales, converts) alike: K 5120, powers of two 64 / 128 / 256 tokens 31 / 41 /
+// 68 us a round, share 80; float32 64 / 128 / 192 tokens 60 / 79 / 100 us, share 96.
 struct GatedPlan {
   int tm;
   int split;
@@ -857,11 +865,11 @@ GatedPlan plan_gated(int64_t m, int64_t n, int64_t k, bool pow2) {
     const int64_t each = ((kb + sp - 1) / sp + 3) / 4 * 4;   // whole units of four blocks' scales
     return {64, (int)((kb + each - 1) / each), each};
   }
-  const int high = pow2 ? 256 : 192;
+  const int high = pow2 ? 256 : 192, share = pow2 ? 80 : 96;
   int best = 64;
   int64_t least = INT64_MAX;
   for (int tm : {64, 128, high}) {
-    const int64_t t = (((m + tm - 1) / tm * nb + kGCUs - 1) / kGCUs) * (tm + kGWeightShare);
+    const int64_t t = (((m + tm - 1) / tm * nb + kGCUs - 1) / kGCUs) * (tm + share);
     if (t < least) {
       least = t;
       best = tm;
