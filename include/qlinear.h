@@ -531,7 +531,7 @@ size_t qlinear_rms_norm_backward_workspace(int64_t m, int64_t k);
  *      the float32 values of h as qlinear_rms_norm's yq: the down projection's
  *      qlinear_forward_fp8_prequant takes them;
  *   gu bf16 [m][2n] (NULL: not wanted): g, then u, in every row, for qlinear_gated_backward.
- * No adapter; NVFP4 layers take qlinear_forward_group.  Workspace:
+ * No buffer may overlap another.  No adapter; NVFP4 layers take qlinear_forward_group.  Workspace:
  * qlinear_gated_forward_workspace(m, n, k) bytes with qlinear_forward's layout and reuse rules
  * (zero-filled before its first use; calls that share it must not overlap, which includes replays
  * of graphs captured on it).
@@ -552,10 +552,13 @@ size_t qlinear_gated_forward_workspace(int64_t m, int64_t n, int64_t k);
  * all bf16 (a weight gradient is an update that qlinear_update_requantize_all takes, once scaled),
  * with float32 sums.  dg and du, formed in float32, enter dx as f16 with a power of two a row
  * (values below about 2^-29 of the row's largest lose bits), the weights as f16 with one for 128
- * columns; they enter the weights' gradients rounded to bf16.
- * dx, or dgate and dup, may be NULL (not wanted); x is read for dgate and dup only.
- * Workspace: qlinear_gated_backward_workspace(m, n, k) bytes of scratch (about 8 m n), which need no
- * zeroing and may be reused by any call once this one has finished on its stream.
+ * columns (a block of weights whose scale is below 2^-20 of the largest in its columns loses bits);
+ * dg and du enter the weights' gradients rounded to bf16.
+ * dx, or dgate and dup, may be NULL (not wanted); x is read for dgate and dup only.  No buffer may
+ * overlap another.
+ * Workspace: qlinear_gated_backward_workspace(m, n, k) bytes of scratch (about 8 m n, for thousands of
+ * tokens 4 n k besides, for few tokens parts of dx in float32), which need no zeroing and may be
+ * reused by any call once this one has finished on its stream.
  * Errors as qlinear_gated_forward, with n, k < 2^22, and QL_ERR_NULL for dgate without dup. */
 qlinear_status qlinear_gated_backward(const qlinear_qweight* gate, const qlinear_qweight* up, const uint16_t* dh,
                                       const uint16_t* gu, const uint16_t* x, int64_t m, uint16_t* dx, uint16_t* dgate,

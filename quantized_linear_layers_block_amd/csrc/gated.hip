@@ -910,7 +910,11 @@ bool gated_launchable(int64_t m, int64_t n, int64_t k) {
   if (m <= 0 || n <= 0 || k <= 0 || n % 128 || k % 128 || k >= kFp8MaxK) return false;
   // counters of the few-token kernel, and its 32-bit scratch offsets
   if (m <= kFewM) return n / 128 <= (int64_t)((kWsReserved - kWsCounterOff) / 4) && m * n < (int64_t(1) << 29);
-  return (m + 63) / 64 * (n / 128) < (int64_t(1) << 31);
+  for (const bool pow2 : {false, true}) {   // fewer than 2^32 threads
+    const GatedPlan p = plan_gated(m, n, k, pow2);
+    if ((m + p.tm - 1) / p.tm * (n / 128) * p.split >= (int64_t(1) << 32) / 512) return false;
+  }
+  return true;
 }
 
 size_t gated_scratch_bytes(int64_t m, int64_t n, int64_t k) {

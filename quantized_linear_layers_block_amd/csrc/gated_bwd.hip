@@ -103,8 +103,8 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
     weight_scales<T>(a.ws, blockIdx.x, red);
     return;
   }
-  // Neighbouring rows share lines of d16: they go to one XCD, whose cache puts the lines together (287 us for 8192 x
-  // 14336; 386 with the rows dealt out one by one).
+  // Neighbouring rows share lines of d16: they go to one XCD, whose cache puts the lines together (8192 x 14336: 351
+  // us, 1.73 GB at 4.9 TB/s; 386 with the rows dealt out one by one).
   const int64_t b = blockIdx.x - scales, rows = gridDim.x - scales, whole = rows / 8 * 8;
   const int64_t row = b < whole ? gemm_xcd_remap(b, whole) : b;
   const int64_t units = a.n / 8;
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
 // ------------------------------------------------------------------------------ weights, turned
 // For many tokens: both weights as f16 [2 n / 32][k][32], times their scales from tab.  A workgroup takes 128 x 128 codes; a
 // thread 8 rows by 4 columns, whose bytes v_perm_b32 turns into 4 columns of 8.  Bound by memory (1 byte read, 2
-// written a weight): 70 us for 2 x 14336 x 4096, which the product gains back from about 1500 tokens on.
+// written a weight): 103 us for 2 x 14336 x 4096, which the product gains back from about 2800 tokens on.
 __global__ __launch_bounds__(256) void gated_weights_kernel(const uint8_t* __restrict__ wg, const uint8_t* __restrict__ wu,
                                                             const uint32_t* __restrict__ tab, int64_t n, int64_t k,
                                                             uint16_t* __restrict__ w16) {
@@ -682,8 +682,12 @@ ProductPlan plan_product(int64_t rows, int64_t z, int64_t k, int tile_rows) {
   p.full = p.split > 1 ? tiles - rem : tiles;
   return p;
 }
+// dx: tiles of 128 rows for up to 128 tokens (14336 x 4096, 64 tokens 52 us against 70 with half-empty ones of 256; 256
+// tokens 88 against 82).
 ProductPlan plan_dx(int64_t m, int64_t n, int64_t k) { return plan_product(m, 2 * n, k, m <= 128 ? 128 : 256); }
-// The weights' gradients: few steps a tile and more than a round of tiles go two workgroups a CU.
+// The weights' gradients: few steps a tile and more than a round of tiles go two workgroups a CU, whose starts and
+// ends then run beside one another (14336 x 4096, the whole call: 64 tokens 119 -> 109 us, 512 283 -> 266, 768 374 ->
+// 372, 1024 455 -> 462).
 constexpr int64_t kShallow = 512;
 ProductPlan plan_dw(int64_t m, int64_t n, int64_t k) {
   const ProductPlan p = plan_product(2 * n, m, k, 256);
@@ -698,8 +702,13 @@ ProductPlan plan_dw(int64_t m, int64_t n, int64_t k) {
 
 constexpr size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// From so many tokens on dx reads the weights turned to f16 beforehand.
-bool turned(int64_t m) { return m >= 2048; }
+// From so many tokens on dx reads the weights turned to f16 beforehand (14336 x 4096, the whole call: 1024 tokens 458 us
+// without, 535 with; 2048 842 and 888; 4096 1614 and 1543).
+bool turned(int64_t m) { return m >= 2816; }
+
+int grad_threads(int64_t n) { return n <= 4096 ? 256 : n <= 8192 ? 512 : 1024; }   // a row of D
+int64_t pad_tokens(int64_t m) { return (m + kBStep - 1) / kBStep * kBStep; }
+constexpr int64_t kGridThreads = int64_t(1) << 32;   // a launch's threads stay below
 
 // last rows of x | cols | scale table | row factors | D16 | Db | turned weights | parts of dx | of the weights' gradients
 struct BwdWs {
@@ -713,7 +722,6 @@ struct BwdWs {
   float* part[2];
   size_t bytes;
 };
-int64_t pad_tokens(int64_t m) { return (m + kBStep - 1) / kBStep * kBStep; }
 BwdWs bwd_ws(void* ws, int64_t m, int64_t n, int64_t k) {
   BwdWs w;
   char* p = (char*)ws;
@@ -741,8 +749,9 @@ BwdWs bwd_ws(void* ws, int64_t m, int64_t n, int64_t k) {
 // 32-bit offsets of a tile's rows, and grids
 bool gated_backward_launchable(int64_t m, int64_t n, int64_t k) {
   if (m <= 0 || n <= 0 || k <= 0 || n % 128 || k % 128 || n >= (int64_t(1) << 22) || k >= (int64_t(1) << 22)) return false;
-  const int64_t rt = (m + 255) / 256, jt = (2 * n + 255) / 256, ct = (k + 255) / 256;
-  return rt * ct < (int64_t(1) << 24) && jt * ct < (int64_t(1) << 24);
+  const int64_t rt = (m + 255) / 256, jt = 2 * n / 128, ct = (k + 255) / 256;
+  return rt * ct < kGridThreads / kBThreads && jt * ct < kGridThreads / kBThreads &&
+         pad_tokens(m) + k / 128 < kGridThreads / grad_threads(n);
 }
 
 size_t gated_backward_bytes(int64_t m, int64_t n, int64_t k) { return bwd_ws(nullptr, m, n, k).bytes; }

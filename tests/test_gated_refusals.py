@@ -81,3 +81,15 @@ def test_helpers_refuse():
     dh = torch.zeros((3, 128), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         ql.gated_backward(w, w, dh, dh)
+
+
+def test_launch_limits():
+    """More than 2^32 - 1 threads cannot be launched: refused, not left to the launch to fail."""
+    assert b.qlinear_gated_forward_workspace(1 << 24, 4096, 128) > 0
+    assert b.qlinear_gated_forward_workspace(1 << 24, 1 << 15, 128) == 0
+    assert b.qlinear_gated_backward_workspace((1 << 24) - 64, 128, 4096) > 0
+    assert b.qlinear_gated_backward_workspace((1 << 24) - 32, 128, 4096) == 0
+    assert b.qlinear_gated_backward_workspace(1 << 24, 128, 128) == 0
+    w = _w(n=128, k=128)
+    assert L.qlinear_gated_backward(ctypes.byref(w), ctypes.byref(w), FAKE, FAKE, FAKE, 1 << 24, FAKE, FAKE, FAKE, FAKE,
+                                    1 << 60, None) == b.QL_ERR_SHAPE

@@ -93,6 +93,34 @@ def test_gated_backward(m, n, k, pow2):
     assert two[0] is None and torch.equal(two[1], got[1]) and torch.equal(two[2], got[2])
 
 
+# thousands of tokens, where dx reads the weights turned beforehand: around the border, ragged rows, half tiles of n and k
+@pytest.mark.parametrize("m,n,k", [(2815, 128, 256), (2816, 256, 128), (2911, 128, 384), (4100, 384, 256)])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_gated_backward_many(m, n, k, pow2):
+    test_gated_backward(m, n, k, pow2)
+
+
+def test_special_values_many():
+    """A NaN code of the weights reaches its column of dx, a NaN of dh its row, and nothing else."""
+    print("gated backward special many", flush=True)
+    m, n, k = 2820, 256, 256
+    ws, dh, gu, x = _case(m, n, k, True, 5)
+    gate, up = [ql.FP8Weight(_dev(c), _dev(s), n, k, True) for c, s in ws]
+    want = ql.gated_backward(gate, up, to_dev(dh), to_dev(gu), to_dev(x))
+    _check(ws, dh, gu, x, want)
+    bad = dh.copy()
+    bad[2817, 40] = 0x7FC0
+    up.codes[7, 100] = 0x7F
+    got = ql.gated_backward(gate, up, to_dev(bad), to_dev(gu), to_dev(x))
+    nan = torch.isnan(got[0])
+    assert nan[2817].all() and nan[:, 100].all()
+    clean = ~nan
+    assert clean.sum() == (m - 1) * (k - 1) and torch.equal(got[0][clean], want[0][clean])
+    rows = np.delete(np.arange(n), 40)
+    for p, q in zip(got[1:], want[1:]):
+        assert torch.isnan(p[40]).all() and torch.equal(p[rows], q[rows])
+
+
 @pytest.mark.parametrize("pow2", [False, True])
 def test_special_values(pow2):
     print(f"gated backward special pow2={pow2}", flush=True)
