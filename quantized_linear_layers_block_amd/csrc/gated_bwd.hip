@@ -358,7 +358,7 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
   //   Q  kDx, kDxT: D rows 8 NJ wave + 16 c + lane / 4, slot lane % 4; kDw: D rows (z) of 2 kRows bytes
   constexpr int kQCopies = NJ / 2;
   constexpr int kCopies = (FUSED ? 3 : 4) + kQCopies;
-  constexpr uint32_t kUp = 3072;     // see lds_copy16x4
+  constexpr uint32_t kUp = 3 * 1024;     // see lds_copy16x4
   uint32_t op[4], od[4], osc = 0;
   {
     // columns past k: the 128 before

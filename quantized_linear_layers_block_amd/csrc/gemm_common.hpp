@@ -192,10 +192,10 @@ __device__ __forceinline__ void lds_copy16x4(const uint8_t* base, uint32_t o0, u
                                              uint32_t lds_base) {
   uint32_t saved;
   asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %6\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
-               "global_load_lds_dwordx4 %2, %5 offset:1024\n\tglobal_load_lds_dwordx4 %3, %5 offset:2048\n\t"
-               "global_load_lds_dwordx4 %4, %5 offset:3072\n\ts_mov_b32 m0, %0"
+               "global_load_lds_dwordx4 %2, %5 offset:%7\n\tglobal_load_lds_dwordx4 %3, %5 offset:2 * %7\n\t"
+               "global_load_lds_dwordx4 %4, %5 offset:3 * %7\n\ts_mov_b32 m0, %0"
                : "=&s"(saved)
-               : "v"(o0), "v"(o1), "v"(o2), "v"(o3), "s"(base), "s"(lds_base)
+               : "v"(o0), "v"(o1), "v"(o2), "v"(o3), "s"(base), "s"(lds_base), "n"(1024)
                : "memory");
 }
 __device__ __forceinline__ void lds_copy16x2(const uint8_t* base, uint32_t o0, uint32_t o1, uint32_t lds_base) {

@@ -7,7 +7,10 @@
 // Bound by memory: a row is read once, kept in registers, and everything is written from there.
 // T threads take a row, NV units of 8 elements (16 bytes) each, unit i T + t: 16 neighbouring lanes
 // hold a segment of 128, so its maximum is four DPP steps.  A workgroup goes through rows with the
-// weight's elements in registers.
+// weight's elements in registers.  Measured: 8192 x 4096 with the residual and all outputs 57 us (302 MB at 5.3
+// TB/s), 1777 x 3584 to 8 bits 6.6 us, one row of 4096 3.2 us; backward 16384 x 5120 127 us (671 MB at 5.3 TB/s).
+#include <type_traits>
+
 #include "common.hpp"
 #include "fp8_out.hpp"
 #include "launch.hpp"
@@ -266,32 +269,50 @@ __global__ __launch_bounds__(norm_block<T>()) void rms_norm_backward_kernel(Norm
   }
 }
 
-// dw[c] = sum over p of part[p][c]: 32 columns a workgroup, 8 lanes of 4 columns by 32 rows at a time.
+// dw[c] = sum over p of part[p][c]: 32 columns a workgroup, 8 lanes of 4 columns by 32 rows, four of them under way.
 __global__ __launch_bounds__(256) void rms_norm_dw_kernel(const float* __restrict__ part, int parts, int64_t k,
                                                           float* __restrict__ dw) {
-  __shared__ f32x4 red[256];
-  const int lane = threadIdx.x & 7, slot = threadIdx.x >> 3;
+  __shared__ f32x4 red[4][8];
+  const int lane = threadIdx.x & 7, slot = threadIdx.x >> 3, wave = threadIdx.x / kWave;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane * 4;
-  f32x4 s = {0, 0, 0, 0};
+  const f32x4 zero = {0, 0, 0, 0};
+  f32x4 s[4] = {zero, zero, zero, zero};
   if (c < k)
-    for (int p = slot; p < parts; p += 32) s += *(const f32x4*)(part + p * k + c);
-  red[threadIdx.x] = s;
-  __syncthreads();
-  if (slot == 0 && c < k) {
-    for (int q = 1; q < 32; ++q) s += red[q * 8 + lane];
-    *(f32x4*)(dw + c) = s;
+    for (int p = slot; p < parts; p += 128) {
+      f32x4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = p + 32 * i < parts ? *(const f32x4*)(part + (p + 32 * i) * k + c) : zero;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += v[i];
+    }
+  f32x4 t = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {   // the wave's eight rows
+    t[e] += __shfl_xor(t[e], 8);
+    t[e] += __shfl_xor(t[e], 16);
+    t[e] += __shfl_xor(t[e], 32);
   }
+  if ((threadIdx.x & (kWave - 1)) < 8) red[wave][lane] = t;
+  __syncthreads();
+  if (slot == 0 && c < k) *(f32x4*)(dw + c) = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
 }
 
-// Threads of a row: a wave for many rows (no barrier), else as many as keep a row's units few.
-// (T, NV) covers rows of up to 8 T NV elements.
+// Threads of a row, (T, NV) for up to 8 T NV elements: as many as keep a row's units few, or a wave alone, which has no
+// barrier.  Alone: the forward up to 1024 elements if there are more than 1024 rows (8192 x 1024 12.1 us against 15.0
+// with a workgroup a row, 256 x 1024 3.7 against 3.3, 8192 x 2048 23.0 against 20.0); the backward, whose workgroup
+// then joins four rows' shares of dw, up to 2048 (256 x 1024 6.2 against 8.0, 32768 x 1024 39 against 71, 32768 x 2048
+// 83 against 101).
 template <typename F>
 hipError_t norm_dispatch(int64_t m, int64_t k, F&& f) {
   const int64_t units = k / 8;
   if (units <= 64) return f.template run<64, 1>();
-  if (m > 1024 && units <= 128) return f.template run<64, 2>();
-  if (m > 1024 && units <= 256) return f.template run<64, 4>();
-  if (units <= 256) return f.template run<256, 1>();
+  if constexpr (std::remove_reference_t<F>::kBackward) {
+    if (units <= 128) return f.template run<64, 2>();
+    if (units <= 256) return f.template run<64, 4>();
+  } else {
+    if (m > 1024 && units <= 128) return f.template run<64, 2>();
+    if (units <= 256) return f.template run<256, 1>();
+  }
   if (units <= 512) return f.template run<256, 2>();
   if (units <= 768) return f.template run<256, 3>();
   if (units <= 1024) return f.template run<256, 4>();
@@ -309,6 +330,7 @@ unsigned norm_grid(int64_t m, int64_t most) {
 }
 
 struct RunNorm {
+  static constexpr bool kBackward = false;
   const Norm& a;
   int fmt;
   hipStream_t s;
@@ -323,15 +345,18 @@ struct RunNorm {
   }
 };
 
-// Rows of dw's partial sums: few enough that adding them is short beside the pass over the rows.
-constexpr int64_t kNormParts = 512;
+// Rows of dw's partial sums: few enough that adding them is short beside the pass over the rows, which one workgroup
+// a CU makes alone up to 1024 rows (700 x 4096: 256 parts 10.6 us, 512 12.3; 2048 x 4096: 17.9, 16.4; 16384 x 5120: 124,
+// 97.5, 1024 parts 113).
+int64_t norm_parts(int64_t m) { return m <= 1024 ? 256 : 512; }
 
 struct RunNormBackward {
+  static constexpr bool kBackward = true;
   const NormBackward& a;
   hipStream_t s;
   template <int T, int NV>
   hipError_t run() {
-    const unsigned grid = norm_grid<T>(a.m, kNormParts);
+    const unsigned grid = norm_grid<T>(a.m, norm_parts(a.m));
     rms_norm_backward_kernel<T, NV><<<grid, norm_block<T>(), 0, s>>>(a);
     if (a.dw)
       rms_norm_dw_kernel<<<(unsigned)((a.k + 31) / 32), 256, 0, s>>>(a.part, (int)grid, a.k, a.dw);
@@ -347,7 +372,7 @@ hipError_t launch_rms_norm(const Norm& a, int fmt, hipStream_t s) {
 }
 
 size_t rms_norm_backward_bytes(int64_t m, int64_t k) {
-  return (size_t)(m < kNormParts ? m : kNormParts) * (size_t)k * 4;
+  return (size_t)(m < norm_parts(m) ? m : norm_parts(m)) * (size_t)k * 4;
 }
 
 hipError_t launch_rms_norm_backward(const NormBackward& a, hipStream_t s) {
