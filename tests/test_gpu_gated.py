@@ -236,3 +236,77 @@ def test_graph_replays(m):
         torch.cuda.synchronize()
         assert torch.equal(hq, want[0]) and torch.equal(sh, want[1]), i
         assert not ws[:ql.binding.QLINEAR_WS_RESERVED_BYTES].any()
+
+
+@pytest.mark.parametrize("m,n", [(3, 256), (40, 8192), (40, 8320), (100, 256), (300, 384)])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_scales_that_are_nan(m, n, pow2):
+    """A segment whose scale is NaN (what the norm stores for one with an Inf) makes its token NaN, a weight block's
+    its 128 columns; nothing else changes."""
+    print(f"gated NaN scales m={m} n={n} pow2={pow2}", flush=True)
+    k = 384
+    w, x = _case(m, n, k, pow2, 21)
+    gate, up = _weights(w, n, k, pow2)
+    xq, sx = _dev(x[0]), _dev(x[1])
+    want = ql.gated_forward(gate, up, xq, sx)
+    nan = 255 if pow2 else float("nan")
+    sx[m - 1, 2] = nan
+    up.scales[1, 0] = nan
+    h = torch.empty_like(want)
+    hq, sh = ql.gated_forward_fp8(gate, up, xq, sx, h=h)
+    got = torch.isnan(h)
+    assert got[m - 1].all() and got[:, 128:256].all()
+    assert got.sum() == n + 128 * (m - 1) and torch.equal(h[~got], want[~got])
+    bad = sh == 0xFF if pow2 else torch.isnan(sh)
+    assert bad[m - 1].all() and bad[:, 1].all() and bad.sum() == n // 128 + m - 1
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 8192, 512), (48, 8320, 640), (20, 512, 1024), (100, 384, 1024), (300, 1024, 256)])
+def test_two_streams_and_one_weight(m, n, k):
+    """Calls side by side on two streams with a workspace each; the same weight as gate and as up projection."""
+    print(f"gated streams m={m} n={n} k={k}", flush=True)
+    w, x = _case(m, n, k, True, 9)
+    gate, _ = _weights(w, n, k, True)
+    xq, sx = _dev(x[0]), _dev(x[1])
+    x2 = _dev(_codes(np.random.default_rng(1), (m, k)))
+    size = ql.binding.qlinear_gated_forward_workspace(m, n, k)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.zeros(size, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    want = [[t.clone() for t in ql.gated_forward_fp8(gate, gate, i, sx)] for i in (xq, x2)]
+    rh, _, _, eh, _, _ = _reference([w[0], w[0]], x)
+    assert _near(ql.gated_forward(gate, gate, xq, sx), rh, eh)
+    torch.cuda.synchronize()
+    out = [[], []]
+    for _ in range(8):
+        for s in range(2):
+            with torch.cuda.stream(streams[s]):
+                out[s].append(ql.gated_forward_fp8(gate, gate, (xq, x2)[s], sx, ws=spaces[s]))
+    torch.cuda.synchronize()
+    for s in range(2):
+        assert all(torch.equal(p, q) for got in out[s] for p, q in zip(got, want[s]))
+        assert not spaces[s][:ql.binding.QLINEAR_WS_RESERVED_BYTES].any()
+
+
+def test_graphs_of_wide_calls_on_one_workspace():
+    """Two captured calls of different sizes that share a workspace, replayed in turn."""
+    print("gated wide graphs", flush=True)
+    n, k = 8192, 640
+    cases, ws = [], torch.zeros(ql.binding.qlinear_gated_forward_workspace(64, n, k), dtype=torch.uint8, device=DEV)
+    for m in (64, 2):
+        w, x = _case(m, n, k, False, m)
+        gate, up = _weights(w, n, k, False)
+        xq, sx = _dev(x[0]), _dev(x[1])
+        ql.gated_forward_fp8(gate, up, xq, sx, ws=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = ql.gated_forward_fp8(gate, up, xq, sx, ws=ws)
+        cases.append((graph, out, gate, up, xq, sx))
+    for i in range(3):
+        for graph, out, gate, up, xq, sx in cases:
+            xq.copy_(_dev(_codes(np.random.default_rng(i), tuple(xq.shape))))
+            want = ql.gated_forward_fp8(gate, up, xq, sx)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]), i
+    assert not ws[:ql.binding.QLINEAR_WS_RESERVED_BYTES].any()

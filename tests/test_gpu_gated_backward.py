@@ -229,3 +229,34 @@ def test_training_step_of_a_block():
     rdx, rdg, rdu = ob.gated_backward(f(dh), f(got[5][:, :n]), f(got[5][:, n:]), f(got[6]), *vals)
     for p, q in ((got[7], rdx), (got[1], rdg), (got[2], rdu)):
         assert np.linalg.norm(f(p) - q) <= BF16 * np.linalg.norm(q)
+
+
+@pytest.mark.parametrize("m,n,k", [(2, 256, 384), (130, 2176, 256), (300, 384, 512), (2900, 256, 128)])
+def test_two_streams_and_a_graph(m, n, k):
+    """Calls side by side on two streams with a workspace each, and a captured one between eager ones."""
+    print(f"gated backward streams m={m} n={n} k={k}", flush=True)
+    ws, dh, gu, x = _case(m, n, k, True, 31)
+    gate, up = [ql.FP8Weight(_dev(c), _dev(s), n, k, True) for c, s in ws]
+    dev = to_dev(dh), to_dev(gu), to_dev(x)
+    want = ql.gated_backward(gate, up, *dev)
+    size = ql.binding.qlinear_gated_backward_workspace(m, n, k)
+    spaces = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(4):
+        for s in range(2):
+            with torch.cuda.stream(streams[s]):
+                out.append(ql.gated_backward(gate, up, *dev, ws=spaces[s]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for got in out for p, q in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = ql.gated_backward(gate, up, *dev, ws=spaces[0])
+    for i in range(3):
+        dev[0].copy_(to_dev(_bits(np.random.default_rng(i), (m, n), 0.1)))
+        want = ql.gated_backward(gate, up, *dev, ws=spaces[1])
+        spaces[0].fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), i
