@@ -8,9 +8,8 @@
 // the weight rows of its tile are 64 of the gate and 64 of the up projection for each wave, and a
 // lane's accumulators of the two halves belong to the same elements of h.
 //
-//   more than 64 tokens  tiles of 128 columns (256 weight rows) by 256 or 128 tokens: the FP8
-//                        GEMMs' tiling (gemm_fp8.hip) with its two ways of applying scales, whose
-//                        128 columns are one segment of the 8-bit output
+//   more than 64 tokens  tiles of 128 columns (256 weight rows), one segment of the 8-bit output, by 64
+//                        to 256 tokens, a kernel for each way of applying scales
 //   up to 64 tokens      bound by the weights: 16 to 64 columns a workgroup
 #include <type_traits>
 #include "common.hpp"
@@ -176,20 +175,24 @@ __device__ __forceinline__ f16x8 e4m3_f16x8(int lo, int hi) {
 // turn their fragments into f16 (a lane's 32 bytes are four steps of 8), and each K block's products
 // start from zero and are folded into the sums with one FMA by the block's scale.
 // Eight waves, 2 along n by 4 along m; a wave's 128 weight rows are 64 of the gate then 64 of the up
-// projection, its tokens 16 MJ: with MJ = 3 sums, fragments and two sets of products fit 256 registers.
+// projection, its tokens 16 MJ: with MJ = 3 sums, fragments and two sets of products fit 256 registers.  K blocks are
+// copied one ahead, two where LDS has the room (300 x 5120 x 2048 27.5 -> 25.9 us; longer ones 2% or less).  8192 x 14336
+// x 4096 1590 us: matrix units 52%, vector units 59% (folding, and each wave's conversions) of the cycles at 1.9 GHz.
 constexpr int kGfThreads = 512;
+template <int MJ>
+constexpr int gf_stages() { return MJ == 3 ? 2 : 3; }
 template <int MJ>
 constexpr int gf_ring() { return 64 * MJ * 16 + 1024; }   // a slot of the scale ring: 16 bytes a token, then the weights'
 template <int MJ>
 constexpr size_t gf_lds() {
-  constexpr size_t loop = 2 * (kGRows + 64 * MJ) * kGRowBytes + 2 * gf_ring<MJ>(), out = 64 * MJ * kGPitch + 2 * 64 * MJ * 4;
+  constexpr size_t loop = gf_stages<MJ>() * (kGRows + 64 * MJ) * kGRowBytes + 2 * gf_ring<MJ>(), out = 64 * MJ * kGPitch + 2 * 64 * MJ * 4;
   return loop > out ? loop : out;
 }
 
 template <int MJ, bool SW4>
 __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
   extern __shared__ __align__(16) uint8_t smem[];  // [2][W 256 x 128 | x TM x 128], scale ring
-  constexpr int TM = 64 * MJ;
+  constexpr int TM = 64 * MJ, AHEAD = gf_stages<MJ>() - 1;
   constexpr int kStage = (kGRows + TM) * kGRowBytes;
   const GatedWork work = gated_work(a);
   const int64_t tn = work.tn, n0 = tn * kGCols, m0 = work.tm * TM;
@@ -236,7 +239,7 @@ __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
     const int64_t row = 16 * MJ * wm + 16 * j + r;
     osx[j] = (uint32_t)((row < m_last ? row : m_last) * kblocks);
   }
-  constexpr int kRing = 2 * kStage;
+  constexpr int kRing = gf_stages<MJ>() * kStage;
   const int arow = 64 * (wave & 3) + lane;
   const uint32_t oxu = (uint32_t)((arow < m_last ? arow : m_last) * kblocks * 4);
   auto dma_sc = [&](int64_t grp) {
@@ -268,7 +271,9 @@ __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
 #pragma unroll
     for (int j = 0; j < MJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-  for (int q = 0; q < 4 + MJ; ++q) dma(work.kb0, 0, q);
+  for (int t = 0; t < AHEAD; ++t)
+#pragma unroll
+    for (int q = 0; q < 4 + MJ; ++q) dma(work.kb0 + t < work.kb1 ? work.kb0 + t : work.kb1 - 1, t, q);
   if (SW4) dma_sc(work.kb0 >> 2);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
@@ -294,9 +299,11 @@ __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
   }
   wr = gated_frag(smem, 128 * wn + r, g);
   wf[0] = e4m3_f16x8(wr[0], wr[1]);
+  int buf = 0;
   for (int64_t kb = work.kb0; kb < work.kb1; ++kb) {
-    const int buf = (int)((kb - work.kb0) & 1);
-    const int64_t kn = kb + 1 < work.kb1 ? kb + 1 : kb;  // the last block copies itself into the idle buffer again
+    const int64_t kn = kb + 1 < work.kb1 ? kb + 1 : kb;
+    const int64_t kc = kb + AHEAD < work.kb1 ? kb + AHEAD : work.kb1 - 1;   // (past the last: into a slot not read again)
+    const int bufn = buf == AHEAD ? 0 : buf + 1, bufc = buf == 0 ? AHEAD : buf - 1;
 #pragma unroll
     for (int j = 0; j < MJ; ++j) {
       scl[j] = scu[j];
@@ -307,13 +314,13 @@ __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
     if (SW4 && ((kb + 2) & 3) == 0 && kb + 2 < work.kb1) dma_sc((kb + 2) >> 2);
     next_sc(kn);
     const uint8_t* As = smem + buf * kStage;
-    const uint8_t* An = smem + (buf ^ 1) * kStage;
+    const uint8_t* An = smem + bufn * kStage;
     i32x8 xr[MJ];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i == 7) {
         // this block's LDS reads are done and the next block's copies have landed
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(AHEAD == 2 ? 4 + MJ : 0) : "memory");
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < MJ; ++j) xr[j] = gated_frag(An + kGRows * kGRowBytes, 16 * MJ * wm + 16 * j + r, g);
@@ -333,14 +340,16 @@ __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
           }
           if (s == 0) wrn = i < 7 ? gated_frag(As, 128 * wn + 16 * (i + 1) + r, g) : gated_frag(An, 128 * wn + r, g);
           if (j == MJ - 1) wf[(kk & 1) ^ 1] = kk < 3 ? e4m3_f16x8(wr[2 * kk + 2], wr[2 * kk + 3]) : e4m3_f16x8(wrn[0], wrn[1]);
-          if (i < 4 + MJ && s == 1) dma(kn, buf ^ 1, i);
+          if (i < 4 + MJ && s == 1) dma(kc, bufc, i);
           if (i == 7) xf[j][kk] = e4m3_f16x8(xr[j][2 * kk], xr[j][2 * kk + 1]);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
       wr = wrn;
     }
+    buf = bufn;
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // copies still under way into what gated_store writes
 #pragma unroll
   for (int j = 0; j < MJ; ++j) acc[7][j] += scu[j] * p[1][j];
   gated_store<kGfThreads, TM, MJ>(a, acc, work.split, m0, n0, wn, 16 * MJ * wm, r, g, smem, (uint32_t*)(smem + TM * kGPitch));
