@@ -602,6 +602,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void gated_few_kernel(Gated a) {
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[h][j] = f32x4{0, 0, 0, 0};
 
+  // 16 bytes of each half of a block's 128: four lanes have 64 bytes side by side (K's order is alike in both operands)
   auto load32 = [](const uint8_t* p) {
     const i32x4 lo = *(const i32x4*)p, hi = *(const i32x4*)(p + 64);
     return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
