@@ -709,9 +709,51 @@ ProductPlan plan_dw(int64_t m, int64_t n, int64_t k) {
 
 constexpr size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// From so many tokens on dx reads the weights turned to f16 beforehand (14336 x 4096, the whole call: 1024 tokens 458 us
-// without, 535 with; 2048 842 and 888; 4096 1614 and 1543).
-bool turned(int64_t m) { return m >= 2816; }
+// Both products.  If all their tiles fit one round of the chip they may run side by side, each cut along its depth so
+// that together they fill the round: the slower is cut further (by more than eight in eights) while there is room and
+// a part has eight steps or more.  Against each filling the chip by itself, one behind the other, that halves the
+// parts to be added (8192 x 1024 x 512 108 -> 74 us, 8192 x 2048 x 1024 195 -> 171) but may leave the longer one alone in
+// the end (6614 x 2816 x 640 190 -> 198), so the two are compared: a step of the weights' gradients is 0.6 us, one of dx
+// 0.9, a part written and read 0.1.  The plan is that of both gradients whatever is asked for, so that the bits do not
+// depend on it.
+// Otherwise, from many tokens on, dx reads the weights turned to f16 beforehand (14336 x 4096, the whole call: 1024 tokens
+// 458 us without, 535 with; 2048 842 and 888; 4096 1614 and 1543).
+struct BackwardPlan {
+  ProductPlan dx, dw;
+  bool turned, side;   // side: one launch for both
+};
+constexpr int64_t kTurned = 2816;
+BackwardPlan plan_backward(int64_t m, int64_t n, int64_t k) {
+  BackwardPlan b;
+  b.dx = plan_dx(m, n, k);
+  b.dw = plan_dw(m, n, k);
+  const int64_t tiles[2] = {b.dx.tiles_r * b.dx.tiles_c, b.dw.tiles_r * b.dw.tiles_c};
+  bool round = tiles[0] + tiles[1] <= kBCUs;
+  if (round) {
+    const int64_t steps[2] = {2 * n / kBStep, (m + kBStep - 1) / kBStep};
+    int64_t sp[2] = {1, 1};
+    auto time = [&](int i, int64_t split) { return (steps[i] + split - 1) / split * (i == 0 ? 9 : 6); };   // tenths of a us
+    auto parts = [&](int i, int64_t split) { return split > 1 ? tiles[i] * split : 0; };
+    for (;;) {
+      const int i = time(0, sp[0]) >= time(1, sp[1]) ? 0 : 1;
+      const int64_t next = sp[i] < 8 ? sp[i] + 1 : sp[i] + 8;
+      if (next > 32 || next > steps[i] / 8 || tiles[i] * next + tiles[1 - i] * sp[1 - i] > kBCUs) break;
+      sp[i] = next;
+    }
+    const int64_t t0 = time(0, sp[0]), t1 = time(1, sp[1]);
+    const int64_t together = (t0 > t1 ? t0 : t1) + parts(0, sp[0]) + parts(1, sp[1]);
+    const int64_t apart = time(0, b.dx.split) + time(1, b.dw.split) + parts(0, b.dx.split) + parts(1, b.dw.split);
+    round = together < apart;
+    ProductPlan* p[2] = {&b.dx, &b.dw};
+    for (int i = 0; round && i < 2; ++i) {
+      p[i]->split = (int32_t)sp[i];
+      p[i]->full = sp[i] > 1 ? 0 : tiles[i];
+    }
+  }
+  b.turned = m >= kTurned && !round;
+  b.side = !b.turned && b.dw.tile_rows == 256;
+  return b;
+}
 
 int grad_threads(int64_t n) { return n <= 4096 ? 256 : n <= 8192 ? 512 : 1024; }   // a row of D
 int64_t pad_tokens(int64_t m) { return (m + kBStep - 1) / kBStep * kBStep; }
@@ -744,9 +786,10 @@ BwdWs bwd_ws(void* ws, int64_t m, int64_t n, int64_t k) {
   w.rs = (float*)take((size_t)m * 4);
   w.d16 = (uint16_t*)take((size_t)m * 2 * n * 2);
   w.db = (uint16_t*)take((size_t)pad_tokens(m) * 2 * n * 2);
-  w.w16 = (uint16_t*)take(turned(m) ? (size_t)k * 2 * n * 2 : 0);
-  w.part[0] = (float*)take(plan_dx(m, n, k).part_bytes());
-  w.part[1] = (float*)take(plan_dw(m, n, k).part_bytes());
+  const BackwardPlan plan = plan_backward(m, n, k);
+  w.w16 = (uint16_t*)take(plan.turned ? (size_t)k * 2 * n * 2 : 0);
+  w.part[0] = (float*)take(plan.dx.part_bytes());
+  w.part[1] = (float*)take(plan.dw.part_bytes());
   w.bytes = at;
   return w;
 }
@@ -795,6 +838,7 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
   if (e != hipSuccess) return e;
 
   GatedProduct dx = {}, dw = {};
+  const BackwardPlan plan = plan_backward(a.m, a.n, a.k);
   ProductPlan px = {}, pw = {};
   auto planned = [&](GatedProduct& p, const ProductPlan& plan, float* part) {
     p.n = a.n;
@@ -807,7 +851,7 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
     p.part = part;
   };
   if (a.dx) {
-    px = plan_dx(a.m, a.n, a.k);
+    px = plan.dx;
     planned(dx, px, w.part[0]);
     dx.codes[0] = a.wg;
     dx.codes[1] = a.wu;
@@ -821,7 +865,7 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
     dx.out[0] = dx.out[1] = a.dx;
   }
   if (a.dgate) {
-    pw = plan_dw(a.m, a.n, a.k);
+    pw = plan.dw;
     planned(dw, pw, w.part[1]);
     dw.p = a.x;
     dw.xt = w.xt;
@@ -840,14 +884,14 @@ hipError_t launch_gated_backward(const GatedBackward& a, hipStream_t s) {
   constexpr auto most = [](int x, int y) { return x > y ? x : y; };
   const bool small_dx = px.tile_rows == 128;
   bool ok = true;
-  if (!turned(a.m) && a.dx && a.dgate && pw.tile_rows == 256) {
+  if (plan.side && a.dx && a.dgate) {
     constexpr int dw8 = Lds<kDw, 8>::kBytes;
     if (small_dx)
       ok = go(gated_both_kernel<4>, most(Lds<kDx, 4>::kBytes, dw8), px.grid() + pw.grid(), dx, dw, px.grid());
     else
       ok = go(gated_both_kernel<8>, most(Lds<kDx, 8>::kBytes, dw8), px.grid() + pw.grid(), dx, dw, px.grid());
   } else {
-    if (a.dx && turned(a.m)) {
+    if (a.dx && plan.turned) {
       gated_weights_kernel<<<dim3((unsigned)(a.k / 128), (unsigned)(2 * a.n / 128)), 256, 0, s>>>(a.wg, a.wu, w.tab, a.n, a.k, w.w16);
       ok = go(gated_product_kernel<kDxT, 8>, Lds<kDxT, 8>::kBytes, px.grid(), dx);
     } else if (a.dx && small_dx) {

@@ -100,6 +100,30 @@ def test_gated_backward_many(m, n, k, pow2):
     test_gated_backward(m, n, k, pow2)
 
 
+# thousands of tokens: more tiles than a round of the chip (weights turned beforehand), and both products in one round
+@pytest.mark.parametrize("m,n,k", [(2816, 256, 6272), (2911, 128, 5760), (4100, 128, 4096), (5000, 512, 512), (1347, 1664, 1920)])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_gated_backward_plans(m, n, k, pow2):
+    test_gated_backward(m, n, k, pow2)
+
+
+def test_special_values_turned():
+    """As test_special_values_many where the weights are turned beforehand."""
+    print("gated backward special turned", flush=True)
+    m, n, k = 2820, 128, 5888
+    ws, dh, gu, x = _case(m, n, k, True, 6)
+    gate, up = [ql.FP8Weight(_dev(c), _dev(s), n, k, True) for c, s in ws]
+    want = ql.gated_backward(gate, up, to_dev(dh), to_dev(gu), to_dev(x))
+    bad = dh.copy()
+    bad[2817, 40] = 0x7FC0
+    up.codes[7, 5800] = 0x7F
+    got = ql.gated_backward(gate, up, to_dev(bad), to_dev(gu), to_dev(x))
+    nan = torch.isnan(got[0])
+    assert nan[2817].all() and nan[:, 5800].all()
+    clean = ~nan
+    assert clean.sum() == (m - 1) * (k - 1) and torch.equal(got[0][clean], want[0][clean])
+
+
 def test_special_values_many():
     """A NaN code of the weights reaches its column of dx, a NaN of dh its row, and nothing else."""
     print("gated backward special many", flush=True)
