@@ -46,15 +46,17 @@ __device__ __forceinline__ float sum_wave(float v) {
   return v;
 }
 
-// Sum over the T threads of a row.  Two sets of LDS words in turn: a set is written again only after
-// the barrier of the sum between, which every wave reaches after reading it.
-template <int T, int N>
+// Sums over the T threads of a row.  Two sets of LDS words in turn: a set is written again only after
+// the barrier of the sum between, which every wave reaches after reading it.  MOST is the largest N of a
+// kernel's sums: sets of sums of any N then lie in the same two places, which the turns rely on.
+template <int T, int MOST, int N>
 __device__ __forceinline__ void sum_row(float (&v)[N], float* red, int& turn) {
+  static_assert(N <= MOST, "a set holds MOST sums");
 #pragma unroll
   for (int n = 0; n < N; ++n) v[n] = sum_wave(v[n]);
   if (T > kWave) {
     constexpr int W = T / kWave;
-    float* p = red + turn * (N * W);
+    float* p = red + turn * (MOST * W);
     turn ^= 1;
     if ((threadIdx.x & (kWave - 1)) == 0)
 #pragma unroll
@@ -72,7 +74,7 @@ __device__ __forceinline__ void sum_row(float (&v)[N], float* red, int& turn) {
 
 // s of a row from its elements.  The squares pass float32 where an element passes 2^63: then the
 // sum is taken again of elements scaled down (eps is lost beside it).
-template <int T, int NV>
+template <int T, int MOST, int NV>
 __device__ __forceinline__ float row_rstd_scaled(const uint4 (&h)[NV], float k, float* red, int& turn) {
   float s[1] = {0.0f};
 #pragma unroll
@@ -82,7 +84,7 @@ __device__ __forceinline__ float row_rstd_scaled(const uint4 (&h)[NV], float k, 
       const float f = bf16_at(h[i], e) * 0x1p-80f;
       s[0] += f * f;
     }
-  sum_row<T>(s, red, turn);
+  sum_row<T, MOST>(s, red, turn);
   return (1.0f / sqrtf(s[0] / k)) * 0x1p-80f;
 }
 
@@ -137,9 +139,9 @@ __global__ __launch_bounds__(norm_block<T>()) void rms_norm_kernel(Norm a) {
         if (u < units) *(uint4*)(a.h + row * a.h_stride + u * 8) = h[i];
       }
     }
-    sum_row<T>(ss, red, turn);
+    sum_row<T, 1>(ss, red, turn);
     float s = 1.0f / sqrtf(ss[0] / k + a.eps);
-    if (__builtin_expect(ss[0] == INFINITY, 0)) s = row_rstd_scaled<T, NV>(h, k, red, turn);
+    if (__builtin_expect(ss[0] == INFINITY, 0)) s = row_rstd_scaled<T, 1>(h, k, red, turn);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t u = (int64_t)i * T + t;
@@ -217,9 +219,9 @@ __global__ __launch_bounds__(norm_block<T>()) void rms_norm_backward_kernel(Norm
         sum[0] += f * f;
         sum[1] += (bf16_at(dy[i], e) * bf16_at(w[i], e)) * f;
       }
-    sum_row<T>(sum, red, turn);
+    sum_row<T, 2>(sum, red, turn);
     float s = 1.0f / sqrtf(sum[0] / k + a.eps);
-    if (__builtin_expect(sum[0] == INFINITY, 0)) s = row_rstd_scaled<T, NV>(h, k, red, turn);
+    if (__builtin_expect(sum[0] == INFINITY, 0)) s = row_rstd_scaled<T, 2>(h, k, red, turn);
     float sc = (s * (sum[1] / k)) * s;   // s^2 c without a square of its own, which may leave the range
     if (__builtin_expect(sum[0] == INFINITY, 0)) {
       float c[1] = {0.0f};
@@ -228,7 +230,7 @@ __global__ __launch_bounds__(norm_block<T>()) void rms_norm_backward_kernel(Norm
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           c[0] += (bf16_at(dy[i], e) * bf16_at(w[i], e)) * (bf16_at(h[i], e) * 0x1p-80f);
-      sum_row<T>(c, red, turn);
+      sum_row<T, 2>(c, red, turn);
       sc = ((s * 0x1p80f) * (c[0] / k)) * s;
     }
 #pragma unroll

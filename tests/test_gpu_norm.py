@@ -218,3 +218,24 @@ def test_norm_streams_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(got, want)), i
+
+
+# rows over several waves (256 and 1024 threads), several rows a workgroup: up to 2048 (or 512) workgroups forward, 256 or
+# 512 backward
+@pytest.mark.parametrize("m,k", [(1100, 2560), (2100, 4096), (700, 8192), (2600, 2304), (1600, 8320), (1200, 16512)])
+def test_norm_rows_beyond_float32_among_others(m, k):
+    """Rows whose squares pass float32 take more sums than the others: both kinds in turn in one workgroup."""
+    print(f"norm mixed rows m={m} k={k}", flush=True)
+    g = np.random.default_rng(m + k)
+    x, w, dy, dh = _bits(g, (m, k), 2.0), _bits(g, (k,)), _bits(g, (m, k)), _bits(g, (m, k))
+    far = g.random(m) < 0.4
+    x[far] = _bits(g, (int(far.sum()), k), 1e30)
+    xd, wd = to_dev(x), to_dev(w)
+    y = torch.empty((m, k), dtype=torch.bfloat16, device=DEV)
+    yq, sy = ql.rms_norm_fp8(xd, wd, EPS, y=y)
+    ref = ob.rms_norm(ob._f64(x), ob._f64(w), EPS)
+    assert (np.abs(_f64(y) - ref) <= np.abs(ref) * (BF16 + F32)).all()
+    assert ob.output_errors(yq.cpu().numpy(), sy.cpu().numpy(), ref, F32)[0] <= 1.0
+    for d in (None, dh):
+        dx, dw = ql.rms_norm_backward(to_dev(dy), xd, wd, EPS, dh=None if d is None else to_dev(d))
+        _check_backward(dx, dw, dy, x, w, d)
