@@ -77,25 +77,34 @@ def weight_values(codes, scales):
 
 
 def output_errors(codes, scales, y, tol):
-    """How E4M3 codes and their segment scales miss the float64 values y [m, k], given that the
-    quantized values may be off by `tol` relative to each segment's largest value: (worst scale,
-    worst element), each in units of what is allowed, so both are at most 1 where all is right.
+    """How E4M3 codes and their segment scales miss the finite float64 values y [m, k], given that
+    the quantized values may be off by `tol` relative to each segment's largest value: (worst
+    scale, worst element), each in units of what is allowed, so both are at most 1 where all is
+    right.  A code or a scale that is not a number is off by infinity.
 
     A float32 scale is amax / 448 within tol.  A power of two is the smallest 2^e with
     amax <= 448 2^e, where a rounding may go either way within tol of that border.  An element
     is off by at most half a step of E4M3 of its scale: 2^-4 of its value, or 2^-10 of the scale
-    below the normal range, plus tol of the segment's largest value."""
+    below the normal range, plus tol of the segment's largest value.  A segment of zeros has the
+    scale 0 (1 as a power of two) and codes of zero, whatever its tol, which is relative to nothing."""
     m, k = y.shape
     seg = np.asarray(y, np.float64).reshape(m, k // 128, 128)
     amax = np.abs(seg).max(2)
-    s = _fp8.e8m0_decode(scales) if scales.dtype == np.uint8 else np.asarray(scales, np.float64)
-    if scales.dtype == np.uint8:
+    tol = np.where(amax > 0, tol, 0.0)
+    e8m0 = scales.dtype == np.uint8
+    s = _fp8.e8m0_decode(scales) if e8m0 else np.asarray(scales, np.float64)
+    if e8m0:
         low = np.where((s > 2.0 ** -127) & (amax > 0), amax <= 448.0 * (s / 2) * (1 - tol), False)
         bad = np.where(amax > 0, (amax > 448.0 * s * (1 + tol)) | low, s != 1.0)
-        worst_scale = np.where(bad, np.inf, 0.0).max()
+        off = np.where(bad, np.inf, 0.0)
+        lost = np.asarray(scales) == 0xFF
     else:
         off = np.abs(s - amax / 448.0)
-        worst_scale = np.where(amax > 0, off / (np.maximum(amax / 448.0 * tol, 2.0 ** -150)), np.where(s == 0, 0, np.inf)).max()
-    v = act_values(codes, scales).reshape(seg.shape)
-    allowed = np.maximum(np.abs(seg) * 2.0 ** -4, s[..., None] * 2.0 ** -10) + (2 * tol * amax)[..., None] + 2.0 ** -140
-    return float(worst_scale), float((np.abs(v - seg) / allowed).max())
+        off = np.where(amax > 0, off / (np.maximum(amax / 448.0 * tol, 2.0 ** -150)), np.where(s == 0, 0, np.inf))
+        lost = ~np.isfinite(s)
+    worst_scale = np.where(lost | np.isnan(off), np.inf, off).max()
+    with np.errstate(invalid="ignore"):
+        v = act_values(codes, scales).reshape(seg.shape)
+        allowed = np.maximum(np.abs(seg) * 2.0 ** -4, s[..., None] * 2.0 ** -10) + (2 * tol * amax)[..., None] + 2.0 ** -140
+        off = np.abs(v - seg) / allowed
+    return float(worst_scale), float(np.where(np.isnan(off) | lost[..., None], np.inf, off).max())

@@ -61,3 +61,30 @@ def test_output_errors_accept_the_quantizer_and_see_a_wrong_code(pow2):
     off = s.copy()
     off[1, 1] = off[1, 1] + 1 if pow2 else off[1, 1] * np.float32(1.001)
     assert ob.output_errors(codes, off, y, 2.0 ** -22)[0] > 1.0
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+def test_output_errors_see_what_is_not_a_number(pow2):
+    g = np.random.default_rng(10)
+    bits = (g.normal(size=(5, 384)).astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    bits[3, 128:256] = 0
+    y = ob._f64(bits)
+    codes, s = (ofp8.quantize_act_pow2 if pow2 else ofp8.quantize_act)(bits)
+    # a tolerance relative to the largest value of a segment of zeros is not a number: the segment is held to zeros
+    tol = np.full((5, 3), 2.0 ** -22)
+    tol[3, 1] = np.nan
+    assert max(ob.output_errors(codes, s, y, tol)) <= 1.0
+    for where in ((2, 200), (3, 140), slice(None)):
+        for code in (0x7F, 0xFF):
+            wrong = codes.copy()
+            wrong[where] = code
+            assert max(ob.output_errors(wrong, s, y, tol)) == np.inf, (where, code)
+    for where in ((2, 1), (3, 1), slice(None)):
+        for scale in ((255,) if pow2 else (np.nan, np.inf)):
+            wrong = s.copy()
+            wrong[where] = scale
+            assert max(ob.output_errors(codes, wrong, y, tol)) == np.inf, (where, scale)
+    # values where there are none
+    wrong, off = codes.copy(), s.copy()
+    wrong[3, 130], off[3, 1] = 1, 127 if pow2 else 1.0
+    assert max(ob.output_errors(wrong, off, y, tol)) > 1.0
