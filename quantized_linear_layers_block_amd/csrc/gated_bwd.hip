@@ -27,7 +27,6 @@ constexpr int kBPBytes = kBCols * kBStep * 2;      // P of one step, 16 bits an 
 constexpr int kBCodeBytes = kBCols * kBStep;
 constexpr int kBScaleBytes = 1024;          // one word a thread
 
-__device__ __forceinline__ float pow2_float(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
 }
@@ -35,14 +34,14 @@ __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
 // ---------------------------------------------------------------------- scales of the weights
 // For each 128 columns of k the power of two 2^E that puts the largest of the 2 n / 128 scales in
 // [32, 64): then every weight is an f16 (448 * 64 < 2^15), normal down to 2^-20 of the largest scale.  tab
-// [2 n / 128][k / 128] holds f16(scale * 2^-E) twice in a word, cols [k / 128] 2^E.
+// [2 n / 128][k / 128] holds f16(scale * 2^-E) twice in a word, cols [k / 128] E.
 struct WeightScales {
   const void* sg;
   const void* su;
   int pow2;
   int64_t nb, kb;       // n / 128, k / 128
   uint32_t* tab;
-  float* cols;
+  int32_t* cols;
 };
 template <int T>
 __device__ __forceinline__ void weight_scales(const WeightScales& a, int64_t c, uint32_t* red) {
@@ -56,13 +55,12 @@ __device__ __forceinline__ void weight_scales(const WeightScales& a, int64_t c, 
   uint32_t top = 0;
   for (int64_t i = threadIdx.x; i < 2 * a.nb; i += T) top = umax(top, __float_as_uint(scale(i)) & 0x7FFFFFFFu);
   top = max_block<T>(top, red);
-  int e = top >= 0x7F800000u ? 0 : (int)(top >> 23) - 127 - 5;
-  e = e < -120 ? -120 : e > 120 ? 120 : e;
+  const int e = top >= 0x7F800000u ? 0 : (int)(top >> 23) - 127 - 5;
   for (int64_t i = threadIdx.x; i < 2 * a.nb; i += T) {
-    const float s = scale(i) * pow2_float(-e);
+    const float s = __builtin_amdgcn_ldexpf(scale(i), -e);
     a.tab[i * a.kb + c] = f16_pair(s, s);
   }
-  if (threadIdx.x == 0) a.cols[c] = pow2_float(e);
+  if (threadIdx.x == 0) a.cols[c] = e;
 }
 
 // --------------------------------------------------------------------------------- D
@@ -85,7 +83,7 @@ struct GateGrad {
   const uint16_t* gu;   // [m][2 n]
   int64_t m, n, m_pad;
   uint16_t* d16;        // f16 [2 n / 32][m][32], or null
-  float* rs;            // [m]
+  int32_t* rs;          // [m]: exponents of the rows' factors, which dx takes off again
   uint16_t* db;         // bf16 [m_pad][2 n], rows past m zero, or null
   const uint16_t* x;    // with db: [m][k], whose last m % 32 rows go to xt [32][k], the others there zero
   uint16_t* xt;
@@ -135,7 +133,7 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
       top = umax(top, umax(__float_as_uint(dg[e]) & 0x7FFFFFFFu, __float_as_uint(du[e]) & 0x7FFFFFFFu));
     return top;
   };
-  auto store = [&](int64_t u, const float (&dg)[8], const float (&du)[8], float f) {
+  auto store = [&](int64_t u, const float (&dg)[8], const float (&du)[8], int e) {
     if (a.db) {
       uint16_t* p = a.db + row * 2 * a.n + u * 8;
       *(uint4*)p = make_uint4(pack_bf16x2_rne(dg[0], dg[1]), pack_bf16x2_rne(dg[2], dg[3]),
@@ -145,19 +143,19 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
     }
     if (a.d16) {
       uint16_t* p = a.d16 + ((u >> 2) * a.m + row) * 32 + (u & 3) * 8;
-      *(uint4*)p = make_uint4(f16_pair(dg[0] * f, dg[1] * f), f16_pair(dg[2] * f, dg[3] * f),
-                              f16_pair(dg[4] * f, dg[5] * f), f16_pair(dg[6] * f, dg[7] * f));
-      *(uint4*)(p + a.n * a.m) = make_uint4(f16_pair(du[0] * f, du[1] * f), f16_pair(du[2] * f, du[3] * f),
-                                      f16_pair(du[4] * f, du[5] * f), f16_pair(du[6] * f, du[7] * f));
+      auto pair = [&](const float (&d)[8], int i) {
+        return f16_pair(__builtin_amdgcn_ldexpf(d[i], e), __builtin_amdgcn_ldexpf(d[i + 1], e));
+      };
+      *(uint4*)p = make_uint4(pair(dg, 0), pair(dg, 2), pair(dg, 4), pair(dg, 6));
+      *(uint4*)(p + a.n * a.m) = make_uint4(pair(du, 0), pair(du, 2), pair(du, 4), pair(du, 6));
     }
   };
-  // the power of two that puts the row's largest value in [2^14, 2^15)
+  // the exponent of the power of two that puts the row's largest value in [2^14, 2^15)
   auto factor = [&](uint32_t top) {
     top = max_block<T>(top, red);
-    int e = top == 0 || top >= 0x7F800000u ? 0 : 14 - ((int)(top >> 23) - 127);
-    e = e < -120 ? -120 : e > 120 ? 120 : e;
-    if (t == 0 && a.rs) a.rs[row] = pow2_float(-e);
-    return pow2_float(e);
+    const int e = top == 0 || top >= 0x7F800000u ? 0 : 14 - ((int)(top >> 23) - 127);
+    if (t == 0 && a.rs) a.rs[row] = -e;
+    return e;
   };
   if constexpr (NV > 0) {
     float dg[NV][8], du[NV][8];
@@ -176,11 +174,11 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
       grads(g[i], u[i], h[i], dg[i], du[i]);
       top = umax(top, highest(dg[i], du[i]));
     }
-    const float f = factor(top);
+    const int e = factor(top);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t c = (int64_t)i * T + t;
-      if (c < units) store(c, dg[i], du[i], f);
+      if (c < units) store(c, dg[i], du[i], e);
     }
   } else {
     uint32_t top = 0;
@@ -189,10 +187,10 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
       grads(*(const uint4*)(pg + c * 8), *(const uint4*)(pg + a.n + c * 8), *(const uint4*)(ph + c * 8), dg, du);
       top = umax(top, highest(dg, du));
     }
-    const float f = factor(top);
+    const int e = factor(top);
     for (int64_t c = t; c < units; c += T) {
       grads(*(const uint4*)(pg + c * 8), *(const uint4*)(pg + a.n + c * 8), *(const uint4*)(ph + c * 8), dg, du);
-      store(c, dg, du, f);
+      store(c, dg, du, e);
     }
   }
 }
@@ -229,7 +227,7 @@ __global__ __launch_bounds__(256) void gated_weights_kernel(const uint8_t* __res
 }
 
 // ------------------------------------------------------------------------------ products
-// out[row][k] = factors * sum over z of P[z][k] Q[z][row]
+// out[row][k] = 2^(rs[row] + cols[k / 128]) * sum over z of P[z][k] Q[z][row]   (kDw: without the factor)
 //   kDx:  rows are tokens, z the 2 n weight rows: P the weights (E4M3 in memory, f16 from there), Q = D16 in steps,
 //         [z / 32][row][32], so that what a step reads of 256 rows is one piece of whole lines
 //   kDxT: the same with P = the weights as f16 [z / 32][k][32], turned by gated_weights_kernel beforehand
@@ -261,8 +259,8 @@ struct GatedProduct {
   const uint16_t* p;         // kDw: x [z][k]; kDxT: the weights, f16 [z / 32][k][32]
   const uint16_t* xt;        // kDw: x's last step, rows past the last token zero, where z is no multiple of 32
   const uint16_t* q;         // D16 [z / 32][rows][32], or Db [z padded][rows]
-  const float* rs;           // kDx, kDxT: [rows]
-  const float* cols;         // the same: [k / 128]
+  const int32_t* rs;         // kDx, kDxT: [rows]
+  const int32_t* cols;       // the same: [k / 128]
   int64_t rows, z, n, k;     // z: 2 n, or tokens; n: rows of one weight
   uint16_t* out[2];          // kDx, kDxT: dx twice; else the gate's and the up projection's gradient
   int64_t tiles_r, tiles_c, full;
@@ -574,13 +572,16 @@ __device__ __forceinline__ void gated_product(const GatedProduct& a, int64_t b, 
 
   // lane: k = c0 + 128 wk + 16 i + 4 g + (0 .. 3), row r0 + kWRows wr + 16 j + r
   if (!DW) {
-    const float cf = a.cols[(128 * wk < c_room ? c0 + 128 * wk : c0) / 128];
+    // both exponents at once: the row's factor alone may leave float32's range where the result does not
+    const int ce = a.cols[(128 * wk < c_room ? c0 + 128 * wk : c0) / 128];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int64_t row = r0 + kWRows * wr + 16 * j + r;
-      const float rf = a.rs[row < a.rows ? row : a.rows - 1];
+      const int e = a.rs[row < a.rows ? row : a.rows - 1] + ce;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i][j] = acc[i][j] * rf * cf;
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_amdgcn_ldexpf(acc[i][j][q], e);
     }
   }
   if (work.slot >= 0) {   // a part of a tile's depth, added by gated_join_kernel
@@ -762,9 +763,9 @@ constexpr int64_t kGridThreads = int64_t(1) << 32;   // a launch's threads stay 
 // last rows of x | cols | scale table | row factors | D16 | Db | turned weights | parts of dx | of the weights' gradients
 struct BwdWs {
   uint16_t* xt;
-  float* cols;
+  int32_t* cols;
   uint32_t* tab;
-  float* rs;
+  int32_t* rs;
   uint16_t* d16;
   uint16_t* db;
   uint16_t* w16;
@@ -781,9 +782,9 @@ BwdWs bwd_ws(void* ws, int64_t m, int64_t n, int64_t k) {
     return q;
   };
   w.xt = (uint16_t*)take((size_t)kBStep * (size_t)k * 2);
-  w.cols = (float*)take((size_t)(k / 128) * 4);
+  w.cols = (int32_t*)take((size_t)(k / 128) * 4);
   w.tab = (uint32_t*)take((size_t)(2 * n / 128) * (size_t)(k / 128) * 4);
-  w.rs = (float*)take((size_t)m * 4);
+  w.rs = (int32_t*)take((size_t)m * 4);
   w.d16 = (uint16_t*)take((size_t)m * 2 * n * 2);
   w.db = (uint16_t*)take((size_t)pad_tokens(m) * 2 * n * 2);
   const BackwardPlan plan = plan_backward(m, n, k);

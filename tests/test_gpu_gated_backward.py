@@ -284,3 +284,20 @@ def test_two_streams_and_a_graph(m, n, k):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, want)), i
+
+
+# dx's kernels: tiles of 128 and of 256 rows, alone and beside the weights' gradients, weights turned beforehand
+@pytest.mark.parametrize("m,n,k", [(70, 256, 256), (300, 384, 512), (200, 8320, 640), (2900, 256, 6272)])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_rows_of_any_size(m, n, k, pow2):
+    """Gradients from 2^-100 to 2^112 a row: a row's factor alone passes float32 where dx does not."""
+    print(f"gated backward rows of any size m={m} n={n} k={k} pow2={pow2}", flush=True)
+    ws, _, gu, x = _case(m, n, k, pow2, m + n)
+    g = np.random.default_rng(m)
+    dh = np.ldexp(g.normal(size=(m, n)), g.integers(-100, 113, size=(m, 1))).astype(np.float32)
+    dh = (np.ascontiguousarray(dh).view(np.uint32) >> 16).astype(np.uint16)
+    gate, up = [ql.FP8Weight(_dev(c), _dev(s), n, k, pow2) for c, s in ws]
+    got = ql.gated_backward(gate, up, to_dev(dh), to_dev(gu), to_dev(x))
+    _check(ws, dh, gu, x, got)
+    one = ql.gated_backward(gate, up, to_dev(dh), to_dev(gu), need_dweight=False)[0]
+    assert torch.equal(one, got[0])
