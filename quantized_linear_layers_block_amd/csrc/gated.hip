@@ -14,6 +14,7 @@
 #include <type_traits>
 #include "common.hpp"
 #include "fp8_out.hpp"
+#include "gate.hpp"
 #include "gemm_common.hpp"
 #include "gemv_common.hpp"
 #include "launch.hpp"
@@ -27,17 +28,6 @@ constexpr int kGRows = 256;      // weight rows per tile
 constexpr int kGRowBytes = 128;  // one K block of fp8 per LDS row
 constexpr int kGPitch = 272;     // output staging: bytes per row of 128 bf16 columns (conflict-free 8-byte writes)
 constexpr int kGPitch8 = 144;    // the same for 128 codes (conflict-free 4-byte writes)
-
-// g / (1 + exp(-g)) * u.  exp(-g) = 2^t with t = -g log2(e): what the product's rounding lost goes
-// back in as a factor 1 + d ln 2, so the result is within a few units of 2^-24 for every g.  Beyond
-// +-128 the exponential is 0 or infinite in float32 anyhow (and 1 / (1 + it) exactly 1 or 0).
-__device__ __forceinline__ float gate_product(float g, float u) {
-  const float c = __builtin_amdgcn_fmed3f(g, -128.0f, 128.0f);
-  const float t = c * -1.44269504f;
-  const float d = __builtin_fmaf(c, -1.44269504f, -t) + c * -1.92596299e-8f;   // log2(e) = 1.44269502 + 1.926e-8
-  const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(d, 0.693147181f, 1.0f);
-  return (g * __builtin_amdgcn_rcpf(1.0f + e)) * u;
-}
 
 __device__ __forceinline__ i32x8 gated_frag(const uint8_t* tile, int row, int g) {
   const uint8_t* p = tile + row * kGRowBytes;
@@ -86,12 +76,7 @@ __device__ __forceinline__ void gated_store(const Gated& a, f32x4 (&acc)[8][MJ],
     rows_out(a.gu, 2 * a.n, 0);
     rows_out(a.gu + a.n, 2 * a.n, 4);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < MJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = gate_product(acc[i][j][e], acc[4 + i][j][e]);
+  gate_products(*(f32x4(*)[4][MJ])acc, *(const f32x4(*)[4][MJ])(acc + 4));
   if (a.h) rows_out(a.h, a.n, 0);
   if (!a.hq) return;
   // a token's 128 values are in the four lane groups of the two waves along n
@@ -525,14 +510,13 @@ __device__ __forceinline__ void few_finish(const Gated& a, int64_t n0, const f32
   __amdgpu_buffer_rsrc_t hs = dev_rsrc(a.scratch);
   for (int t = wave; t < RT * MT; t += WAVES) {   // one 16 x 16 piece of h a wave
     const int i = t / MT, j = t % MT;
-    f32x4 gv = {0, 0, 0, 0}, uv = gv, hv;
+    f32x4 gv = {0, 0, 0, 0}, uv = gv;
 #pragma unroll
     for (int w = 0; w < COPIES; ++w) {
       gv += part[(w * kTiles + i * MT + j) * kWave + lane];
       uv += part[(w * kTiles + (RT + i) * MT + j) * kWave + lane];
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) hv[e] = gate_product(gv[e], uv[e]);
+    const f32x4 hv = gate_product4(gv, uv);
     const int64_t row = 16 * j + r, col = n0 + 16 * i + 4 * g;
     if (row >= a.m) continue;
     auto out = [&](uint16_t* p, f32x4 v) {
@@ -797,13 +781,11 @@ __global__ __launch_bounds__(256) void gated_join_kernel(Gated a) {
     g += *(const f32x4*)(p + s * each);
     u += *(const f32x4*)(p + s * each + a.n);
   }
-  float h[4];
+  const f32x4 h4 = gate_product4(g, u);
+  const float h[4] = {h4[0], h4[1], h4[2], h4[3]};
   uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    h[e] = gate_product(g[e], u[e]);
-    top = umax(top, abs_bits(h[e]));
-  }
+  for (int e = 0; e < 4; ++e) top = umax(top, abs_bits(h[e]));
   auto out = [](uint16_t* q, float a0, float a1, float a2, float a3) {
     *(uint2*)q = make_uint2(pack_bf16x2_rne(a0, a1), pack_bf16x2_rne(a2, a3));
   };

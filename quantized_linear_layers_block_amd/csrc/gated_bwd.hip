@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "gate.hpp"
 #include "gemm_common.hpp"
 #include "launch.hpp"
 
@@ -64,20 +65,6 @@ __device__ __forceinline__ void weight_scales(const WeightScales& a, int64_t c, 
 }
 
 // --------------------------------------------------------------------------------- D
-__device__ __forceinline__ void gate_grad(float g, float u, float dh, float& dg, float& du) {
-  // (g beyond +-128 leaves s at 0 or 1 in float32; products are ordered so that no finite value meets an
-  // infinite one)
-  const float c = __builtin_amdgcn_fmed3f(g, -128.0f, 128.0f);
-  const float t = c * -1.44269504f;
-  const float d = __builtin_fmaf(c, -1.44269504f, -t) + c * -1.92596299e-8f;
-  const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(d, 0.693147181f, 1.0f);
-  const float s = __builtin_amdgcn_rcpf(1.0f + e);
-  const float q = e < 3e38f ? e * s : 1.0f;   // 1 - s without cancellation
-  const float gs = g * s;
-  du = dh * gs;
-  dg = (dh * u) * (s + gs * q);
-}
-
 struct GateGrad {
   const uint16_t* dh;   // [m][n]
   const uint16_t* gu;   // [m][2 n]
@@ -92,9 +79,9 @@ struct GateGrad {
 };
 
 // T threads a row, NV units of 8 columns each in registers (NV 0: any n, read twice).  Bound by memory:
-// 6 bytes read, 4 or 8 written a column of h.
+// 6 bytes read, 4 or 8 written a column of h; eight waves a SIMD, so that two workgroups of 1024 threads share a CU.
 template <int T, int NV>
-__global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
+__global__ __launch_bounds__(T, 8) void gate_grad_kernel(GateGrad a) {
   __shared__ uint32_t red[T / kWave];
   const int64_t scales = a.d16 ? a.ws.kb : 0;
   if (blockIdx.x < scales) {
@@ -118,14 +105,6 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
   }
   const uint16_t* ph = a.dh + row * a.n;
   const uint16_t* pg = a.gu + row * 2 * a.n;
-  auto at = [](const uint4& v, int e) {
-    const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
-    return e & 1 ? bf16_hi(w) : bf16_lo(w);
-  };
-  auto grads = [&](const uint4& g, const uint4& u, const uint4& h, float (&dg)[8], float (&du)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) gate_grad(at(g, e), at(u, e), at(h, e), dg[e], du[e]);
-  };
   auto highest = [](const float (&dg)[8], const float (&du)[8]) {
     uint32_t top = 0;
 #pragma unroll
@@ -171,7 +150,7 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      grads(g[i], u[i], h[i], dg[i], du[i]);
+      gate_grad8(g[i], u[i], h[i], dg[i], du[i]);
       top = umax(top, highest(dg[i], du[i]));
     }
     const int e = factor(top);
@@ -184,12 +163,12 @@ __global__ __launch_bounds__(T) void gate_grad_kernel(GateGrad a) {
     uint32_t top = 0;
     float dg[8], du[8];
     for (int64_t c = t; c < units; c += T) {
-      grads(*(const uint4*)(pg + c * 8), *(const uint4*)(pg + a.n + c * 8), *(const uint4*)(ph + c * 8), dg, du);
+      gate_grad8(*(const uint4*)(pg + c * 8), *(const uint4*)(pg + a.n + c * 8), *(const uint4*)(ph + c * 8), dg, du);
       top = umax(top, highest(dg, du));
     }
     const int e = factor(top);
     for (int64_t c = t; c < units; c += T) {
-      grads(*(const uint4*)(pg + c * 8), *(const uint4*)(pg + a.n + c * 8), *(const uint4*)(ph + c * 8), dg, du);
+      gate_grad8(*(const uint4*)(pg + c * 8), *(const uint4*)(pg + a.n + c * 8), *(const uint4*)(ph + c * 8), dg, du);
       store(c, dg, du, e);
     }
   }

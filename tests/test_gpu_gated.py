@@ -310,3 +310,42 @@ def test_graphs_of_wide_calls_on_one_workspace():
             torch.cuda.synchronize()
             assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]), i
     assert not ws[:ql.binding.QLINEAR_WS_RESERVED_BYTES].any()
+
+
+# the kernels that finish a call: a wave's pieces (narrow and wide), tiles, and parts of K joined
+@pytest.mark.parametrize("m,n,k", [(1, 256, 128), (20, 384, 384), (3, 8192, 128), (40, 8320, 256), (100, 384, 128),
+                                   (300, 640, 256), (70, 128, 1024)])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_gates_far_below_zero(m, n, k, pow2):
+    """Gates down to -450 beside up projections near the end of float32's range: exp(g) is below float32's
+    smallest number, what it multiplies brings it back.
+
+    Tokens have one value each, so g and u are one product: exact but for the roundings of the two scales'
+    product and its own, 2^-23 together, which exp turns into |g| 2^-23 < 2^-14 of h."""
+    print(f"gated far gates m={m} n={n} k={k} pow2={pow2}", flush=True)
+    g = np.random.default_rng(m + n)
+    xc = np.zeros((m, k), np.uint8)
+    xc[np.arange(m), g.integers(0, k, size=m)] = 0x38          # 1.0
+    gc = g.integers(0x80 + 0x58, 0xFF, size=(n, k)).astype(np.uint8)      # -16 to -448
+    gc[::5] ^= 0x80                                            # and some far above zero
+    uc = g.integers(0x28, 0x7F, size=(n, k)).astype(np.uint8)  # 0.25 to 448
+    shape = n // 128, k // 128
+    size = np.where(np.arange(np.prod(shape)) % 2, g.integers(-60, 80, size=np.prod(shape)),
+                    g.integers(80, 110, size=np.prod(shape))).reshape(shape)
+    if pow2:
+        sx, sg = np.full((m, k // 128), 127, np.uint8), g.integers(125, 128, size=shape).astype(np.uint8)
+        su = (127 + size).astype(np.uint8)
+    else:
+        sx, sg = g.uniform(0.5, 1, size=(m, k // 128)).astype(np.float32), g.uniform(0.2, 1, size=shape).astype(np.float32)
+        su = (2.0 ** size * g.uniform(0.5, 1, size=shape)).astype(np.float32)
+    gate, up = _weights([(gc, sg), (uc, su)], n, k, pow2)
+    h = torch.empty((m, n), dtype=torch.bfloat16, device=DEV)
+    hq, sh = ql.gated_forward_fp8(gate, up, _dev(xc), _dev(sx), h=h)
+    rh, rg, _ = ob.gated_forward(ob.act_values(xc, sx), ob.weight_values(gc, sg), ob.weight_values(uc, su))
+    assert (rg < -100).any() and ((rg < -90) & (np.abs(rh) > 1e-30)).any()
+    d = np.abs(ob._f64(bf16_bits_of(h)) - rh)
+    assert (d <= np.abs(rh) * (BF16 + 2.0 ** -13) + 2.0 ** -133).all()
+    # (2^-137: scales below float32's normal range, 448 times 2^-146 there)
+    big = np.abs(rh).reshape(m, n // 128, 128).max(2) > 2.0 ** -110
+    tol = np.where(big, 2.0 ** -13, 1.0)
+    assert max(ob.output_errors(hq.cpu().numpy(), sh.cpu().numpy(), rh, tol)) <= 1.0

@@ -301,3 +301,25 @@ def test_rows_of_any_size(m, n, k, pow2):
     _check(ws, dh, gu, x, got)
     one = ql.gated_backward(gate, up, to_dev(dh), to_dev(gu), need_dweight=False)[0]
     assert torch.equal(one, got[0])
+
+
+@pytest.mark.parametrize("m,n,k", [(60, 256, 128), (130, 4224, 128), (40, 8320, 256), (20, 16512, 128)])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_gates_far_below_zero(m, n, k, pow2):
+    """Rows of gates down to -160 with dh and u so large that dg is of usual size: exp(g) is below float32's
+    smallest number, dh u above its largest."""
+    print(f"gated backward far gates m={m} n={n} k={k} pow2={pow2}", flush=True)
+    ws, _, _, x = _case(m, n, k, pow2, m + n)
+    g = np.random.default_rng(m)
+    level = g.uniform(-160, 0, size=(m, 1))
+    gates = level + g.normal(size=(m, n))
+    room = -level / np.log(2)                                  # dh u of 2^room and some
+    a = np.clip(room * g.uniform(0.4, 0.6, size=(m, 1)), room - 120, 120)
+    dh, u = g.normal(size=(m, n)) * 2 ** a, g.normal(size=(m, n)) * 2 ** (room - a)
+    dh, gu = ((np.ascontiguousarray(t.astype(np.float32)).view(np.uint32) >> 16).astype(np.uint16)
+              for t in (dh, np.concatenate((gates, u), 1)))
+    with np.errstate(over="ignore"):
+        assert np.isinf(ob._f64(dh).astype(np.float32) * ob._f64(gu[:, n:]).astype(np.float32)).any()
+    gate, up = [ql.FP8Weight(_dev(c), _dev(s), n, k, pow2) for c, s in ws]
+    got = ql.gated_backward(gate, up, to_dev(dh), to_dev(gu), to_dev(x))
+    _check(ws, dh, gu, x, got)
