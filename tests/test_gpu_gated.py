@@ -349,3 +349,14 @@ def test_gates_far_below_zero(m, n, k, pow2):
     big = np.abs(rh).reshape(m, n // 128, 128).max(2) > 2.0 ** -110
     tol = np.where(big, 2.0 ** -13, 1.0)
     assert max(ob.output_errors(hq.cpu().numpy(), sh.cpu().numpy(), rh, tol)) <= 1.0
+
+
+# Each height of the tiles (64, 128, and 192 with float32 scales or 256 with powers of two) with 12 to 16 K blocks: scales in
+# units of four blocks (K a multiple of 512), whose ring turns over several times, and one by one.  Then parts of K of
+# more than one unit of scales each.
+@pytest.mark.parametrize("m,n,k", [(150, 5504, 2048), (150, 5504, 1664), (270, 6656, 2048), (270, 6656, 1664),
+                                   (540, 7296, 2048), (540, 7296, 1664), (130, 1024, 8192), (300, 1024, 4096)])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_gated_forward_tiles(m, n, k, pow2):
+    print(f"gated tiles m={m} n={n} k={k} pow2={pow2}", flush=True)
+    _check(m, n, k, pow2, m * 3 + n + k)
