@@ -323,3 +323,18 @@ def test_gates_far_below_zero(m, n, k, pow2):
     gate, up = [ql.FP8Weight(_dev(c), _dev(s), n, k, pow2) for c, s in ws]
     got = ql.gated_backward(gate, up, to_dev(dh), to_dev(gu), to_dev(x))
     _check(ws, dh, gu, x, got)
+
+
+# more tiles than a round of the chip: the last count of tokens whose weights dx turns as it reads them, the first whose
+# weights are turned beforehand, and one of the latter with parts of dx; K with half tiles
+@pytest.mark.parametrize("m,n,k", [(2815, 128, 5888), (2816, 128, 5888), (2977, 384, 5504)])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_gated_backward_turned_border(m, n, k, pow2):
+    test_gated_backward(m, n, k, pow2)
+
+
+# the plans with a launch for each product: weights turned beforehand (the turned copy lies in the workspace), and weights'
+# gradients of few tokens two workgroups a CU
+@pytest.mark.parametrize("m,n,k", [(2820, 128, 5888), (40, 2176, 4224)])
+def test_two_streams_and_a_graph_apart(m, n, k):
+    test_two_streams_and_a_graph(m, n, k)
