@@ -523,6 +523,9 @@ size_t qlinear_rms_norm_backward_workspace(int64_t m, int64_t k);
  * NeMo RL FP8 page, "De technische doorbraak": FP8 linear layers with a scale for 128x128 weights
  * and 1x128 activations, the nonlinearity between them in higher precision):
  *   g = x Wg^T,  u = x Wu^T,  h = g / (1 + exp(-g)) * u        (float32 sums and values)
+ * The products of a block of 128 are exact and enter float32 sums with float32 scales.  With
+ * QL_FP8_POW2 the FP8 matrix instruction sums them: of eight neighbours along k it keeps 13 bits below
+ * the largest (by the exponents of its factors), 1.4e-5 of g on normal data, 2^-10 sum |x| |w| at worst.
  * gate, up (host structs): FP8 weights [n][k] of the same format and sizes.  xq u8 [m][k] with sx
  * [m][k/128]: activations already quantized in that format (qlinear_rms_norm, or
  * qlinear_quantize_act_fp8[_pow2]).  Outputs, all dense; h or hq at least:

@@ -542,7 +542,9 @@ def _gated_call(gate, up, xq, sx, h, gu, ws, quant):
 def gated_forward(gate, up, xq, sx, h=None, gu=None, ws=None):
     """h = silu(x Wg^T) * (x Wu^T), bf16 [T, n], from FP8 weights and activations quantized like them
     (rms_norm_fp8, quantize_act_fp8).  gu (bf16 [T, 2n]), if given, gets both products, for
-    gated_backward.  ws: a zero-filled workspace kept from call to call, as forward's."""
+    gated_backward.  With pow2 weights the sums drop what is 13 bits below the largest of eight
+    products (1.4e-5 of g on normal data).  ws: a zero-filled workspace kept from call to call, as
+    forward's."""
     return _gated_call(gate, up, xq, sx, h, gu, ws, False)[0]
 
 

@@ -341,7 +341,9 @@ __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
 }
 
 // ------------------------------------------------------------------ powers of two, many tokens
-// The MFMA applies E8M0 scales itself and accumulates in place: eight waves, 2 along n by 4 along m, so that one
+// The MFMA applies E8M0 scales itself and accumulates in place, with the 13 bits named above: a scale, being a power of
+// two, is right unless its segment's largest value lies within the sums' error of a border, and f16 products took 1550
+// us in place of 885 (8192 x 14336 x 4096, in one tiling).  Eight waves, 2 along n by 4 along m, so that one
 // wave's epilogue runs beside the other's of its SIMD (four waves of twice the sums spilled 97 registers there:
 // 8192 x 14336 x 512 546 us against 180, x 4096 1073 against 760).  K blocks are copied one ahead, two ahead where
 // LDS has the room: a tile of 64 or 128 tokens has less work in a block than a copy takes (n = 16384, K 5120, 128

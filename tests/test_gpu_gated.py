@@ -360,3 +360,28 @@ def test_gates_far_below_zero(m, n, k, pow2):
 def test_gated_forward_tiles(m, n, k, pow2):
     print(f"gated tiles m={m} n={n} k={k} pow2={pow2}", flush=True)
     _check(m, n, k, pow2, m * 3 + n + k)
+
+
+@pytest.mark.parametrize("m,n", [(1, 128), (20, 256), (1, 8192), (40, 8320), (100, 128), (300, 256)])
+def test_bits_that_products_keep(m, n):
+    """What the bounds above rest on.  Beside 448 * 448 and -448 * 448 (2^16 by their factors' exponents) stands one
+    small product, at every place of a block of 128.  With powers of two it counts down to 2^3, 13 bits below,
+    in the same eight as those, and at any size in other eights; with float32 scales at any size anywhere (2^-6:
+    the 24th bit of 448 * 448)."""
+    print(f"gated products m={m} n={n}", flush=True)
+    k = 128
+    xc = np.full((m, k), 0x38, np.uint8)                      # 1.0
+    xc[:, 0], xc[:, 1] = 0x7E, 0xFE                           # 448, -448
+    for size in (4, 3, 2, 0, -3, -6):
+        w = np.zeros((n, k), np.uint8)
+        w[:, :2] = 0x7E
+        place = 2 + np.arange(n) % 126
+        w[np.arange(n), place] = (size + 7) << 3              # 2^size
+        for pow2 in (False, True):
+            one = (lambda s: np.full(s, 127, np.uint8)) if pow2 else (lambda s: np.ones(s, np.float32))   # noqa: E731
+            wq = _weights([(w, one((n // 128, 1)))], n, k, pow2)[0]
+            gu = torch.empty((m, 2 * n), dtype=torch.bfloat16, device=DEV)
+            ql.gated_forward(wq, wq, _dev(xc), _dev(one((m, 1))), gu=gu)
+            got = ob._f64(bf16_bits_of(gu)).reshape(m, 2, n)
+            lost = pow2 and size < 3
+            assert (got == np.where(lost & (place < 8), 0.0, 2.0 ** size)).all(), (size, pow2)
