@@ -493,7 +493,8 @@ size_t qlinear_attention_nvfp4_workspace(int32_t batch, int64_t total_q, int32_t
  *      product with sy's reciprocal, within 2^-23).  A segment that holds an Inf or NaN has the
  *      scale NaN (0xFF), so every product with it is NaN.
  * Sums are float32; squares beyond its range are summed scaled down.  k is a multiple of 8 (of 128
- * with yq) up to 65536.  No workspace.
+ * with yq) up to 65536; up to 16384 (32768 forward) it runs at the memory's rate, wider rows at a
+ * fraction of it.  No workspace.
  * Errors: QL_ERR_NULL (x, weight, both outputs, yq without sy, a residual without h), QL_ERR_SHAPE
  * (m <= 0, m > QLINEAR_MAX_M, k, a stride < k or not a multiple of 8, sizes beyond
  * QLINEAR_MAX_ELEMS), QL_ERR_ARG (eps not positive and finite), QL_ERR_FORMAT (with yq),

@@ -176,7 +176,7 @@ constexpr size_t gf_lds() {
 
 template <int MJ, bool SW4>
 __global__ __launch_bounds__(kGfThreads) void gated_f32s_kernel(Gated a) {
-  extern __shared__ __align__(16) uint8_t smem[];  // [2][W 256 x 128 | x TM x 128], scale ring
+  extern __shared__ __align__(16) uint8_t smem[];  // [AHEAD + 1][W 256 x 128 | x TM x 128], scale ring
   constexpr int TM = 64 * MJ, AHEAD = gf_stages<MJ>() - 1;
   constexpr int kStage = (kGRows + TM) * kGRowBytes;
   const GatedWork work = gated_work(a);
@@ -658,7 +658,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void gated_few_kernel(Gated a) {
 // A ring of three K blocks (two under way: 4 to 6 were equal or, with fewer workgroups a CU, slower).  Every
 // workgroup begins at another K block: with all of them at one, rows of 4096 bytes lie in the same few channels
 // of the memory (14336 x 4096, one token: 28.3 -> 23.8 us; 18944 x 3584: alike).  The order of a sum is a matter
-// of n0 and k alone.  Scales come in panels of 16 blocks.
+// of n, n0 and k (n chooses a workgroup's width, and n0 its place among them).  Scales come in panels of 16 blocks.
 constexpr int kWidePanel = 16, kWideRing = 3;
 template <int MT, int WAVES, bool POW2>
 constexpr size_t wide_panel() { return kWidePanel * (16 * MT + 2) * (POW2 ? 1 : 4); }

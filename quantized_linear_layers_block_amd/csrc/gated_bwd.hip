@@ -78,7 +78,8 @@ struct GateGrad {
   WeightScales ws;      // with d16: its kb workgroups come first
 };
 
-// T threads a row, NV units of 8 columns each in registers (NV 0: any n, read twice).  Bound by memory:
+// T threads a row, NV units of 8 columns each in registers (NV 0: any n, read twice, the second
+// time from the caches: 8192 x 18944 461 us, 2.2 GB at 4.7 TB/s).  Bound by memory:
 // 6 bytes read, 4 or 8 written a column of h; eight waves a SIMD, so that two workgroups of 1024 threads share a CU.
 template <int T, int NV>
 __global__ __launch_bounds__(T, 8) void gate_grad_kernel(GateGrad a) {

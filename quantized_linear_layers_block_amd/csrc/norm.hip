@@ -9,6 +9,10 @@
 // hold a segment of 128, so its maximum is four DPP steps.  A workgroup goes through rows with the
 // weight's elements in registers.  Measured: 8192 x 4096 with the residual and all outputs 57 us (302 MB at 5.3
 // TB/s), 1777 x 3584 to 8 bits 6.6 us, one row of 4096 3.2 us; backward 16384 x 5120 127 us (671 MB at 5.3 TB/s).
+// That holds up to 16384 columns (16384: forward 5.3, backward 5.0 TB/s).  Behind, 1024 threads with 128 registers each
+// do not hold a row's share of everything, and the rest goes through scratch memory: the backward, which has h, dy, dh, w
+// and dw, spills 109 registers up to 32768 columns (20480: 1.3 TB/s, 32768: 1.7) and 413 up to 65536 (0.5 to 0.7 TB/s), the
+// forward 25 to 48 beyond 32768 (40960: 4.4 TB/s to bf16, 2.9 to 8 bits; 65536: 4.6 and 3.4).
 #include <type_traits>
 
 #include "common.hpp"
