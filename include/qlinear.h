@@ -492,7 +492,7 @@ size_t qlinear_attention_nvfp4_workspace(int32_t batch, int64_t total_q, int32_t
  *      bytes), quantized from the float32 values of y: code = sign | E4M3 of |y| / sy (formed as a
  *      product with sy's reciprocal, within 2^-23).  A segment that holds an Inf or NaN has the
  *      scale NaN (0xFF), so every product with it is NaN.
- * Sums are float32; squares beyond its range are summed scaled down.  k is a multiple of 8 (of 128
+ * Sums are float32; where one leaves its range, of scaled values.  k is a multiple of 8 (of 128
  * with yq) up to 65536; up to 16384 (32768 forward) it runs at the memory's rate, wider rows at a
  * fraction of it.  No workspace.
  * Errors: QL_ERR_NULL (x, weight, both outputs, yq without sy, a residual without h), QL_ERR_SHAPE

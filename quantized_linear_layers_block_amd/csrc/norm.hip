@@ -11,7 +11,7 @@
 // TB/s), 1777 x 3584 to 8 bits 6.6 us, one row of 4096 3.2 us; backward 16384 x 5120 127 us (671 MB at 5.3 TB/s).
 // That holds up to 16384 columns (16384: forward 5.3, backward 5.0 TB/s).  Behind, 1024 threads with 128 registers each
 // do not hold a row's share of everything, and the rest goes through scratch memory: the backward, which has h, dy, dh, w
-// and dw, spills 109 registers up to 32768 columns (20480: 1.3 TB/s, 32768: 1.7) and 413 up to 65536 (0.5 to 0.7 TB/s), the
+// and dw, spills 91 registers up to 32768 columns (20480: 1.5 TB/s, 32768: 1.8) and 394 up to 65536 (0.6 to 0.8 TB/s), the
 // forward 25 to 48 beyond 32768 (40960: 4.4 TB/s to bf16, 2.9 to 8 bits; 65536: 4.6 and 3.4).
 #include <type_traits>
 
@@ -76,20 +76,22 @@ __device__ __forceinline__ void sum_row(float (&v)[N], float* red, int& turn) {
   }
 }
 
-// s of a row from its elements.  The squares pass float32 where an element passes 2^63: then the
-// sum is taken again of elements scaled down (eps is lost beside it).
+// The factor that brings a row's squares into float32's range, by v = mean(h^2) + eps as it came out: squares pass the
+// range where an element passes 2^63, and lose bits below it where v is (an eps below 2^-90, and elements like it).
+__device__ __forceinline__ float row_scale(float v) { return v == INFINITY ? 0x1p-80f : v < 0x1p-90f ? 0x1p70f : 1.0f; }
+// s / scale of a row from its elements times scale (eps is lost beside large ones).
 template <int T, int MOST, int NV>
-__device__ __forceinline__ float row_rstd_scaled(const uint4 (&h)[NV], float k, float* red, int& turn) {
+__device__ __forceinline__ float row_rstd_scaled(const uint4 (&h)[NV], float k, float eps, float scale, float* red, int& turn) {
   float s[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float f = bf16_at(h[i], e) * 0x1p-80f;
+      const float f = bf16_at(h[i], e) * scale;
       s[0] += f * f;
     }
   sum_row<T, MOST>(s, red, turn);
-  return (1.0f / sqrtf(s[0] / k)) * 0x1p-80f;
+  return 1.0f / sqrtf(s[0] / k + (eps * scale) * scale);
 }
 
 template <int T, int NV, int FMT>
@@ -144,8 +146,9 @@ __global__ __launch_bounds__(norm_block<T>()) void rms_norm_kernel(Norm a) {
       }
     }
     sum_row<T, 1>(ss, red, turn);
-    float s = 1.0f / sqrtf(ss[0] / k + a.eps);
-    if (__builtin_expect(ss[0] == INFINITY, 0)) s = row_rstd_scaled<T, 1>(h, k, red, turn);
+    const float v = ss[0] / k + a.eps, scale = row_scale(v);
+    float s = 1.0f / sqrtf(v);
+    if (__builtin_expect(scale != 1.0f, 0)) s = row_rstd_scaled<T, 1>(h, k, a.eps, scale, red, turn) * scale;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t u = (int64_t)i * T + t;
@@ -224,18 +227,22 @@ __global__ __launch_bounds__(norm_block<T>()) void rms_norm_backward_kernel(Norm
         sum[1] += (bf16_at(dy[i], e) * bf16_at(w[i], e)) * f;
       }
     sum_row<T, 2>(sum, red, turn);
-    float s = 1.0f / sqrtf(sum[0] / k + a.eps);
-    if (__builtin_expect(sum[0] == INFINITY, 0)) s = row_rstd_scaled<T, 2>(h, k, red, turn);
+    const float v = sum[0] / k + a.eps, scale = row_scale(v);
+    float s = 1.0f / sqrtf(v);
     float sc = (s * (sum[1] / k)) * s;   // s^2 c without a square of its own, which may leave the range
-    if (__builtin_expect(sum[0] == INFINITY, 0)) {
+    const bool finite = __builtin_fabsf(sum[1]) < INFINITY;
+    if (__builtin_expect(scale != 1.0f || !finite, 0)) {   // a sum left the range: both again of scaled factors
+      const float rs = row_rstd_scaled<T, 2>(h, k, a.eps, scale, red, turn);
+      const float down = finite ? 1.0f : 0x1p-100f, up = finite ? 1.0f : 0x1p100f;
       float c[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          c[0] += (bf16_at(dy[i], e) * bf16_at(w[i], e)) * (bf16_at(h[i], e) * 0x1p-80f);
+          c[0] += ((bf16_at(dy[i], e) * down) * bf16_at(w[i], e)) * (bf16_at(h[i], e) * scale);
       sum_row<T, 2>(c, red, turn);
-      sc = ((s * 0x1p80f) * (c[0] / k)) * s;
+      s = rs * scale;
+      sc = ((rs * (c[0] / k)) * up) * s;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {

@@ -239,3 +239,22 @@ def test_norm_rows_beyond_float32_among_others(m, k):
     for d in (None, dh):
         dx, dw = ql.rms_norm_backward(to_dev(dy), xd, wd, EPS, dh=None if d is None else to_dev(d))
         _check_backward(dx, dw, dy, x, w, d)
+
+
+@pytest.mark.parametrize("m,k", [(300, 256), (2100, 1024), (1100, 2560), (600, 8320), (5, 16640)])
+@pytest.mark.parametrize("eps", [2.0 ** -149, 2.0 ** -140, 2.0 ** -100, 1e-6])
+def test_norm_sums_out_of_range(m, k, eps):
+    """An eps below float32's usual numbers with rows as small, whose squares are subnormal or 0; gradients
+    whose products with h pass float32, beside usual rows."""
+    print(f"norm sums out of range m={m} k={k} eps={eps}", flush=True)
+    g = np.random.default_rng(m + k)
+    size = g.integers(-85, 40, size=(m, 1))
+    x, w = g.normal(size=(m, k)) * 2.0 ** size, _bits(g, (k,))
+    dy = g.normal(size=(m, k)) * 2.0 ** np.where(size > 10, g.integers(70, 105, size=(m, 1)), 0)
+    x, dy = ((np.ascontiguousarray(t.astype(np.float32)).view(np.uint32) >> 16).astype(np.uint16) for t in (x, dy))
+    y = ql.rms_norm(to_dev(x), to_dev(w), eps)
+    ref = ob.rms_norm(ob._f64(x), ob._f64(w), eps)
+    assert (np.abs(_f64(y) - ref) <= np.abs(ref) * (BF16 + F32) + 2.0 ** -134).all()
+    for d in (None, _bits(g, (m, k))):
+        dx, dw = ql.rms_norm_backward(to_dev(dy), to_dev(x), to_dev(w), eps, dh=None if d is None else to_dev(d))
+        _check_backward(dx, dw, dy, x, w, d, eps)
