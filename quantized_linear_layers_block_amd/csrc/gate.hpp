@@ -22,15 +22,15 @@ __device__ __forceinline__ uint32_t gate_bits(float g) { return __float_as_uint(
 constexpr uint32_t kGateFarBits = 0xC2AC0000u;
 __device__ __forceinline__ bool gate_far(float g) { return g < kGateFar && g >= -3.4028235e38f; }
 
-// There exp(g) = 1 / (1 + exp(-g)) to 2^-124: as f 2^e, f in [0.7, 1.5).  c is g, or -208 from there on, where any
-// product of exp(g) with two numbers of float32 less than c vanishes or stays 0.
+// There exp(g) = 1 / (1 + exp(-g)) to 2^-124: as f 2^e, f in [0.7, 1.5).  c is g, or -300 from there on: exp(c) is
+// 2^-433, and c exp(c) times two numbers of float32 (2^256) still rounds to 0.
 struct GateFar {
   float c, f;
   int e;
 };
 __device__ __forceinline__ GateFar gate_exp_far(float g) {
   GateFar o;
-  o.c = g < -208.0f ? -208.0f : g;
+  o.c = g < -300.0f ? -300.0f : g;
   const float t = o.c * 1.44269504f;
   const float d = __builtin_fmaf(o.c, 1.44269504f, -t) + o.c * 1.92596299e-8f;
   const float n = __builtin_rintf(t);

@@ -338,3 +338,33 @@ def test_gated_backward_turned_border(m, n, k, pow2):
 @pytest.mark.parametrize("m,n,k", [(2820, 128, 5888), (40, 2176, 4224)])
 def test_two_streams_and_a_graph_apart(m, n, k):
     test_two_streams_and_a_graph(m, n, k)
+
+
+@pytest.mark.parametrize("m,n,k", [(40, 256, 128), (20, 16512, 128)])
+def test_gates_beyond_every_product(m, n, k):
+    """Gates from -200 to -400 beside dh and u of 2^124: dg goes from 2^-30 to nothing, and so does what follows.
+
+    du is below 2^125 400 exp(-195) = 2^-147, so a weight gradient of up is below 2^-147 m max|x| < 2^-139:
+    nothing but 0 is as near in bf16, whose least number is 2^-133, and so it is no part of _check, which holds
+    2-norms to each other.  dx and the gate's gradient are held to the bounds above."""
+    print(f"gated backward gates beyond m={m} n={n} k={k}", flush=True)
+    ws, _, _, x = _case(m, n, k, False, m + n)
+    g = np.random.default_rng(m)
+    gates = np.linspace(-200, -400, m)[:, None] + g.normal(size=(m, n))
+    dh, u = (g.choice([-1.0, 1.0], size=(m, n)) * 2.0 ** 124 * g.uniform(1, 2, size=(m, n)) for _ in range(2))
+    dh, gu = ((np.ascontiguousarray(t.astype(np.float32)).view(np.uint32) >> 16).astype(np.uint16)
+              for t in (dh, np.concatenate((gates, u), 1)))
+    gate, up = [ql.FP8Weight(_dev(c), _dev(s), n, k, False) for c, s in ws]
+    dx, dgate, dup = ql.gated_backward(gate, up, to_dev(dh), to_dev(gu), to_dev(x))
+    dhv, gv, uv, xv = ob._f64(dh), ob._f64(gu[:, :n]), ob._f64(gu[:, n:]), ob._f64(x)
+    wv = [ob.weight_values(*w) for w in ws]
+    rdx, rdg, _ = ob.gated_backward(dhv, gv, uv, xv, *wv)
+    assert np.abs(xv).max() * m < 2.0 ** 8 and not dup.any()
+    sg, su = np.abs(dhv * uv * np.exp(gv) * (1 + gv)), np.abs(dhv * gv * np.exp(gv))
+    aw = [np.abs(w) for w in wv]
+    top = np.maximum(sg.max(1), su.max(1))[:, None]
+    e = (sg @ aw[0] + su @ aw[1]) * (3 * 2.0 ** -11 + 2.0 ** -17 + (2 * n / 8 + 40) * 2.0 ** -23)
+    e += 2.0 ** -39 * top * (aw[0].sum(0) + aw[1].sum(0))
+    e += 2.0 ** -30 * (sg + su).sum(1, keepdims=True) * np.maximum(aw[0].max(0), aw[1].max(0))
+    assert _off(dx, rdx, e)[0] <= 1
+    assert _off(dgate, rdg, (sg.T @ np.abs(xv)) * (BF16 + 2.0 ** -17 + (m / 8 + 40) * 2.0 ** -23))[0] <= 1
