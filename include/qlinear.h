@@ -524,7 +524,8 @@ size_t qlinear_rms_norm_backward_workspace(int64_t m, int64_t k);
  * NeMo RL FP8 page, "De technische doorbraak": FP8 linear layers with a scale for 128x128 weights
  * and 1x128 activations, the nonlinearity between them in higher precision):
  *   g = x Wg^T,  u = x Wu^T,  h = g / (1 + exp(-g)) * u        (float32 sums and values)
- * The products of a block of 128 are exact and enter float32 sums with float32 scales.  With
+ * The products of a block of 128 are exact and enter float32 sums with float32 scales; a token's scale
+ * times a weight block's is formed first, in float32, and has to be in its normal range.  With
  * QL_FP8_POW2 the FP8 matrix instruction sums them: of eight neighbours along k it keeps 13 bits below
  * the largest (by the exponents of its factors), 1.4e-5 of g on normal data, 2^-10 sum |x| |w| at worst.
  * gate, up (host structs): FP8 weights [n][k] of the same format and sizes.  xq u8 [m][k] with sx
